@@ -30,12 +30,17 @@ __all__ = [
     "attn_decode_step_window", "attn_decode_multi", "attn_test_skip_tile",
     "attn_debug_build", "attn_read_prefill_skips", "debug_collect_range_bits",
     "attn_test_force_schedule",
+    "attn_qk_norm_rope", "attn_qk_norm_rope_append", "attn_kv8_append", "attn_kv8_workspace_size",
+    "kv8_workspace", "attn_decode_step_kv8", "attn_block_scores", "attn_block_select",
+    "attn_decode_step_kv8_blocks", "attn_decode_step_kv8_sparse",
+    "attn_kv8_sparse_workspace_size", "kv8_sparse_workspace",
 ]
 
 ATTN_OK = 0
 ATTN_DEV_BAD_POSITION = 0x1
 ATTN_DEV_TIMEOUT = 0x2
 ATTN_DEV_RANGE = 0x4
+ATTN_DEV_BAD_BLOCK = 0x8
 
 _LIB: Optional[ctypes.CDLL] = None
 # Range-checked builds only: every workspace handed out by decode_workspace()
@@ -117,6 +122,33 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.attn_debug_build.restype = i32
     lib.attn_read_prefill_skips.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
     lib.attn_read_prefill_skips.restype = i32
+    i64 = ctypes.c_int64
+    lib.attn_qk_norm_rope.argtypes = [vp, vp, i64, i64, vp, vp, f32, vp, vp, vp, i32, i32, i32,
+                                      i32, i32, vp, vp, vp]
+    lib.attn_qk_norm_rope.restype = i32
+    lib.attn_qk_norm_rope_append.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, f32, vp, vp, vp,
+                                             vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.attn_qk_norm_rope_append.restype = i32
+    lib.attn_kv8_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                                    vp]
+    lib.attn_kv8_append.restype = i32
+    lib.attn_kv8_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.attn_kv8_workspace_size.restype = sz
+    lib.attn_kv8_sparse_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.attn_kv8_sparse_workspace_size.restype = sz
+    lib.attn_decode_step_kv8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                                         f32, vp, vp, sz, vp]
+    lib.attn_decode_step_kv8.restype = i32
+    lib.attn_decode_step_kv8_blocks.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                                i32, i32, i32, f32, vp, vp, sz, vp]
+    lib.attn_decode_step_kv8_blocks.restype = i32
+    lib.attn_decode_step_kv8_sparse.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                                i32, i32, i32, i32, i32, f32, vp, vp, sz, vp]
+    lib.attn_decode_step_kv8_sparse.restype = i32
+    lib.attn_block_scores.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.attn_block_scores.restype = i32
+    lib.attn_block_select.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.attn_block_select.restype = i32
     _LIB = lib
     return lib
 
@@ -481,3 +513,10 @@ def attn_read_device_status(workspace, stream=None) -> int:
         raise AttnError(code, "attn_read_device_status")
     _DEBUG_RANGE_SEEN |= int(bits.value) & ATTN_DEV_RANGE
     return int(bits.value)
+
+
+from .kv8 import (  # noqa: E402
+    attn_block_scores, attn_block_select, attn_decode_step_kv8, attn_decode_step_kv8_blocks,
+    attn_decode_step_kv8_sparse, attn_kv8_append, attn_kv8_sparse_workspace_size,
+    attn_kv8_workspace_size, attn_qk_norm_rope, attn_qk_norm_rope_append, kv8_sparse_workspace,
+    kv8_workspace)

@@ -180,6 +180,207 @@ int attn_decode_step_noalloc(const void* q, const int32_t* positions, const void
                                                 D, scale, out, stream));
 }
 
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int qk_norm_rope(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                 int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
+                 const int32_t* positions, const float* cos_table, const float* sin_table, int B,
+                 int S, int Hq, int Hkv, int D, int L, void* q_out, void* k_out, void* k_cache,
+                 void* v_cache, cudaStream_t stream) {
+  if (B < 0 || S < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || L <= 0) return ATTN_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || eps > 3e38f) return ATTN_ERR_INVALID_ARG;
+  if ((long long)B * S >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  if (D % 16 != 0 || D > 256) return ATTN_ERR_UNSUPPORTED;
+  if (Hq > 65536 || Hkv > 65536) return ATTN_ERR_UNSUPPORTED;
+  if ((cos_table == nullptr) != (sin_table == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || S == 0) return ATTN_OK;
+  if (!q || !k || !positions || !q_out) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_weight) ||
+      !aligned16(k_weight) || !aligned16(cos_table) || !aligned16(sin_table) ||
+      !aligned16(q_out) || !aligned16(k_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned4(positions))
+    return ATTN_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)Hq * D || k_stride < (int64_t)Hkv * D || q_stride % 8 || k_stride % 8 ||
+      (v && (v_stride < (int64_t)Hkv * D || v_stride % 8)))
+    return ATTN_ERR_INVALID_ARG;
+  return cuda_status(gqa::launch_qk_norm_rope(q, k, v, q_stride, k_stride, v_stride, q_weight,
+                                              k_weight, eps, cos_table, sin_table, positions, B, S,
+                                              Hq, Hkv, D, L, q_out, k_out, k_cache, v_cache,
+                                              stream));
+}
+
+bool block_supported(int block) {
+  return block == 16 || block == 32 || block == 64 || block == 128;
+}
+
+// Sizes common to the 8-bit cache's calls: ATTN_OK, or the error.
+int kv8_sizes(int B, int Hq, int Hkv, int L, int D, int block) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || L <= 0 || D <= 0 || block <= 0 || Hq % Hkv != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (D != gqa::kDecodeD || !block_supported(block) || Hq / Hkv > 16 || Hkv > 1024 ||
+      B > gqa::kDecodeMaxB || L > (1 << 24))
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+int kv8_decode(const void* q, const int32_t* positions, const void* k_cache, const void* v_cache,
+               const float* k_scale, const float* v_scale, const int32_t* block_index, int count,
+               int B, int Hq, int Hkv, int L, int D, int block, float scale, void* out,
+               void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!q || !positions || !k_cache || !v_cache || !k_scale || !v_scale || !out)
+    return ATTN_ERR_INVALID_ARG;
+  if (const int st = kv8_sizes(B, Hq, Hkv, L, D, block)) return st;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned4(positions) || !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(block_index))
+    return ATTN_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < gqa::kv8_workspace_layout(B, Hq, Hkv).total)
+    return ATTN_ERR_WORKSPACE;
+  return cuda_status(gqa::launch_kv8_decode(q, positions, k_cache, v_cache, k_scale, v_scale,
+                                            block_index, count, B, Hq, Hkv, L, block, scale, out,
+                                            workspace, stream));
+}
+
+bool list_ok(int count, int block) {
+  return count >= 1 && (long long)count * block < (1ll << 30);
+}
+
+// Workspace of the sparse step: the decode's, then the scores, then the list.
+struct SparseWorkspace {
+  size_t scores_off, index_off, total;
+};
+SparseWorkspace sparse_layout(int B, int Hq, int Hkv, int L, int block, int count) {
+  auto align256 = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  SparseWorkspace w;
+  w.scores_off = gqa::kv8_workspace_layout(B, Hq, Hkv).total;
+  w.index_off = align256(w.scores_off + (size_t)B * Hkv * ((L + block - 1) / block) * 4);
+  w.total = align256(w.index_off + (size_t)B * Hkv * count * 4);
+  return w;
+}
+
+}  // namespace
+
+int attn_qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
+                      const void* q_weight, const void* k_weight, float eps,
+                      const int32_t* positions, const float* cos_table, const float* sin_table,
+                      int N, int Hq, int Hkv, int D, int L, void* q_out, void* k_out,
+                      cudaStream_t stream) {
+  if (N > 0 && !k_out) return ATTN_ERR_INVALID_ARG;
+  return qk_norm_rope(q, k, nullptr, q_stride, k_stride, 0, q_weight, k_weight, eps, positions,
+                      cos_table, sin_table, N, 1, Hq, Hkv, D, L, q_out, k_out, nullptr, nullptr,
+                      stream);
+}
+
+int attn_qk_norm_rope_append(const void* q, const void* k_new, const void* v_new,
+                             int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                             const void* q_weight, const void* k_weight, float eps,
+                             const int32_t* positions, const float* cos_table,
+                             const float* sin_table, void* k_cache, void* v_cache, int B, int S,
+                             int Hq, int Hkv, int D, int L, void* q_out, cudaStream_t stream) {
+  if (B > 0 && S > 0 && (!v_new || !k_cache || !v_cache)) return ATTN_ERR_INVALID_ARG;
+  return qk_norm_rope(q, k_new, v_new, q_stride, k_stride, v_stride, q_weight, k_weight, eps,
+                      positions, cos_table, sin_table, B, S, Hq, Hkv, D, L, q_out, nullptr,
+                      k_cache, v_cache, stream);
+}
+
+int attn_kv8_append(const void* k_new, const void* v_new, const int32_t* positions,
+                    void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* k_bounds,
+                    int B, int S, int Hkv, int L, int D, int block, cudaStream_t stream) {
+  if (S < 0) return ATTN_ERR_INVALID_ARG;
+  if (const int st = kv8_sizes(B, Hkv, Hkv, L, D, block)) return st;
+  if (S == 0) return ATTN_OK;
+  if (!k_new || !v_new || !positions || !k_cache || !v_cache || !k_scale || !v_scale)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(k_bounds) || !aligned4(positions) || !aligned4(k_scale) || !aligned4(v_scale))
+    return ATTN_ERR_INVALID_ARG;
+  if (S > L) return ATTN_OK;  // no sequence's rows fit: all are skipped
+  return cuda_status(gqa::launch_kv8_append(k_new, v_new, positions, k_cache, v_cache, k_scale,
+                                            v_scale, k_bounds, B, S, Hkv, L, block, stream));
+}
+
+size_t attn_kv8_workspace_size(int B, int Hq, int Hkv, int L, int D) {
+  if (kv8_sizes(B, Hq, Hkv, L, D, 16) != ATTN_OK) return 0;
+  return gqa::kv8_workspace_layout(B, Hq, Hkv).total;
+}
+
+size_t attn_kv8_sparse_workspace_size(int B, int Hq, int Hkv, int L, int D, int block,
+                                      int count) {
+  if (kv8_sizes(B, Hq, Hkv, L, D, block) != ATTN_OK || !list_ok(count, block)) return 0;
+  return sparse_layout(B, Hq, Hkv, L, block, count).total;
+}
+
+int attn_decode_step_kv8(const void* q, const int32_t* positions, const void* k_cache,
+                         const void* v_cache, const float* k_scale, const float* v_scale, int B,
+                         int Hq, int Hkv, int L, int D, int block, float scale, void* out,
+                         void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return kv8_decode(q, positions, k_cache, v_cache, k_scale, v_scale, nullptr, 0, B, Hq, Hkv, L,
+                    D, block, scale, out, workspace, workspace_bytes, stream);
+}
+
+int attn_decode_step_kv8_blocks(const void* q, const int32_t* positions, const void* k_cache,
+                                const void* v_cache, const float* k_scale, const float* v_scale,
+                                const int32_t* block_index, int count, int B, int Hq, int Hkv,
+                                int L, int D, int block, float scale, void* out, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream) {
+  if (!block_index || !list_ok(count, block)) return ATTN_ERR_INVALID_ARG;
+  return kv8_decode(q, positions, k_cache, v_cache, k_scale, v_scale, block_index, count, B, Hq,
+                    Hkv, L, D, block, scale, out, workspace, workspace_bytes, stream);
+}
+
+int attn_block_scores(const void* q, const int32_t* positions, const void* k_bounds, int B,
+                      int Hq, int Hkv, int L, int D, int block, float* scores,
+                      cudaStream_t stream) {
+  if (!q || !positions || !k_bounds || !scores) return ATTN_ERR_INVALID_ARG;
+  if (const int st = kv8_sizes(B, Hq, Hkv, L, D, block)) return st;
+  if (!aligned16(q) || !aligned16(k_bounds) || !aligned4(positions) || !aligned4(scores))
+    return ATTN_ERR_INVALID_ARG;
+  return cuda_status(gqa::launch_block_scores(q, positions, k_bounds, B, Hq, Hkv, L, block,
+                                              scores, stream));
+}
+
+int attn_block_select(const float* scores, const int32_t* positions, int B, int Hkv, int L,
+                      int block, int count, int first, int recent, int32_t* block_index,
+                      cudaStream_t stream) {
+  if (!scores || !positions || !block_index) return ATTN_ERR_INVALID_ARG;
+  if (count < 1 || first < 0 || recent < 0 || first > count - recent)
+    return ATTN_ERR_INVALID_ARG;
+  if (const int st = kv8_sizes(B, Hkv, Hkv, L, gqa::kDecodeD, block)) return st;
+  if (!aligned4(scores) || !aligned4(positions) || !aligned4(block_index))
+    return ATTN_ERR_INVALID_ARG;
+  return cuda_status(gqa::launch_block_select(scores, positions, B, Hkv, L, block, count, first,
+                                              recent, block_index, stream));
+}
+
+int attn_decode_step_kv8_sparse(const void* q, const int32_t* positions, const void* k_cache,
+                                const void* v_cache, const float* k_scale, const float* v_scale,
+                                const void* k_bounds, int count, int first, int recent, int B,
+                                int Hq, int Hkv, int L, int D, int block, float scale, void* out,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !out || !list_ok(count, block) ||
+      first < 0 || recent < 0 || first > count - recent)
+    return ATTN_ERR_INVALID_ARG;
+  if (const int st = kv8_sizes(B, Hq, Hkv, L, D, block)) return st;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned4(k_scale) ||
+      !aligned4(v_scale))
+    return ATTN_ERR_INVALID_ARG;
+  const SparseWorkspace ws = sparse_layout(B, Hq, Hkv, L, block, count);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < ws.total)
+    return ATTN_ERR_WORKSPACE;
+  float* scores = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.scores_off);
+  int32_t* index = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + ws.index_off);
+  int st = attn_block_scores(q, positions, k_bounds, B, Hq, Hkv, L, D, block, scores, stream);
+  if (st == ATTN_OK)
+    st = attn_block_select(scores, positions, B, Hkv, L, block, count, first, recent, index,
+                           stream);
+  if (st == ATTN_OK)
+    st = kv8_decode(q, positions, k_cache, v_cache, k_scale, v_scale, index, count, B, Hq, Hkv, L,
+                    D, block, scale, out, workspace, ws.scores_off, stream);
+  return st;
+}
+
 int attn_prefill_causal(const void* q, const void* k, const void* v, int S, int start_pos,
                         int Hq, int Hkv, int d, float scale, void* out, cudaStream_t stream) {
   if (S < 0 || start_pos < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0)

@@ -66,6 +66,7 @@
 #include "internal.h"
 #include "decode_params.h"
 #include "tcgen05.cuh"
+#include "warp_ops.cuh"
 
 namespace gqa {
 namespace {
@@ -131,28 +132,6 @@ template <int G> struct Cfg {
   static constexpr int kMaxRegs = (kRegsFit > 255 ? 255 : kRegsFit) & ~7;
 };
 
-// Barrier among the NW consumer warps.  It sits on an
-// mbarrier (count NW, one arrival per warp from lane 0 once the warp's lanes
-// have synced) so that its wait is bounded like every other: a named barrier
-// has no time limit, and a warp that gave up on a tile after a timeout would
-// leave the others waiting at one for ever.
-struct ConsumerSync {
-  uint32_t bar;
-  volatile int* abort_flag;
-  uint32_t* status;
-  uint32_t n;  // completed phases
-  __device__ __forceinline__ void operator()(int lane) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-    if (!mbar_wait(bar, n & 1u, abort_flag) && lane == 0) {
-      *abort_flag = 1;
-      set_status(status, ATTN_DEV_TIMEOUT);
-    }
-    ++n;
-    __syncwarp();
-  }
-};
-
 // Position of flat tile t within (sequence, KV head, tile) order.
 // Rows a step at position pos attends: n rows from lo (lo = 0 without a
 // local window; with window W the last W rows, the current one included).
@@ -194,11 +173,6 @@ __device__ __forceinline__ void walk_next(Walk& w, const int* prefix, const int3
   }
 }
 
-// CTA whose tile range [c*T/G, (c+1)*T/G) contains flat tile t.
-__device__ __forceinline__ int cta_of(long long t, long long T, int G) {
-  return (int)(((unsigned long long)(t + 1) * G + T - 1) / T) - 1;
-}
-
 template <int G> struct Log2;
 template <> struct Log2<1> { static constexpr int v = 0; };
 template <> struct Log2<2> { static constexpr int v = 1; };
@@ -231,34 +205,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Transpose of an 8x8 matrix of 16-bit values held as one row pair per lane
-// (lane 4r + c holds row r, columns 2c and 2c+1).
-__device__ __forceinline__ uint32_t movm_trans(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-// Bytes of a and b picked by `sel` (prmt): 0x5410 gives {a.lo, b.lo},
-// 0x7632 gives {a.hi, b.hi}.
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-}
-
-__device__ __forceinline__ uint4 lds128(const uint8_t* p) {
-  return *reinterpret_cast<const uint4*>(p);
-}
-__device__ __forceinline__ uint32_t word(const uint4& u, int i) {
-  return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
-}
-// Byte offset of row r, dims 8c..8c+7 within one 64-dim box of a tile, as the
-// 128-byte swizzle of the tiled copy lays it out (16-byte chunk c of row r
-// sits at chunk c ^ (r mod 8); the stage buffers are 1024-byte aligned).
-__device__ __forceinline__ int sw128(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 // Byte offset of dims 8q..8q+7 (q = 0..15) of row r of a K or V tile.
 __device__ __forceinline__ int tile_chunk(int r, int q) { return (q >> 3) * kHalf + sw128(r, q & 7); }
 
@@ -592,20 +538,6 @@ __device__ __forceinline__ void stage_fresh_rope(float* rope_cs, const float* rc
     dst[2] = *reinterpret_cast<const float4*>(rs + 8 * lane);
     dst[3] = *reinterpret_cast<const float4*>(rs + 8 * lane + 4);
   }
-}
-
-// A consumer warp's wait for a tile, with the outcome made warp-uniform (the
-// tile math uses full-warp shuffles, so either every lane goes on or every
-// lane leaves the loop).
-__device__ __forceinline__ bool consumer_wait(uint32_t bar, uint32_t parity,
-                                              volatile int* abort_flag, uint32_t* status,
-                                              int lane) {
-  if (__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag))) return true;
-  if (lane == 0) {
-    *abort_flag = 1;
-    set_status(status, ATTN_DEV_TIMEOUT);
-  }
-  return false;
 }
 
 // The fused append.  Lane l of the one consumer warp whose keys include the

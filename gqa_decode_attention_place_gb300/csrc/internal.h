@@ -44,6 +44,34 @@ cudaError_t launch_decode_noalloc(const void* q, const int32_t* positions, const
                                   const void* v_cache, int B, int Hq, int Hkv, int L, int D,
                                   float scale, void* out, cudaStream_t stream);
 
+// Norm of q and k heads, rotation, and (k_out null) the bf16 cache write.
+cudaError_t launch_qk_norm_rope(const void* q, const void* k, const void* v, long long q_stride,
+                                long long k_stride, long long v_stride, const void* q_weight,
+                                const void* k_weight, float eps, const float* cos,
+                                const float* sin, const int32_t* positions, int B, int S, int Hq,
+                                int Hkv, int D, int L, void* q_out, void* k_out, void* k_cache,
+                                void* v_cache, cudaStream_t stream);
+
+// 8-bit cache: append, block scores and selection, decode (block_index null:
+// all rows; else count listed blocks per (sequence, KV head)).
+constexpr int kKv8MaxGrid = 512;  // CTAs of the 8-bit decode (workspace partial slots)
+cudaError_t launch_kv8_append(const void* k_new, const void* v_new, const int32_t* positions,
+                              void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                              void* k_bounds, int B, int S, int Hkv, int L, int block,
+                              cudaStream_t stream);
+cudaError_t launch_block_scores(const void* q, const int32_t* positions, const void* k_bounds,
+                                int B, int Hq, int Hkv, int L, int block, float* scores,
+                                cudaStream_t stream);
+cudaError_t launch_block_select(const float* scores, const int32_t* positions, int B, int Hkv,
+                                int L, int block, int count, int first, int recent, int32_t* out,
+                                cudaStream_t stream);
+DecodeWorkspace kv8_workspace_layout(int B, int Hq, int Hkv);
+cudaError_t launch_kv8_decode(const void* q, const int32_t* positions, const void* k_cache,
+                              const void* v_cache, const float* k_scale, const float* v_scale,
+                              const int32_t* block_index, int count, int B, int Hq, int Hkv,
+                              int L, int block, float scale, void* out, void* workspace,
+                              cudaStream_t stream);
+
 cudaError_t launch_prefill(const void* q, const void* k, const void* v, int S, int start_pos,
                            int Hq, int Hkv, int d, float scale, void* out,
                            cudaStream_t stream);

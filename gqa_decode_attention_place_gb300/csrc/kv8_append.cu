@@ -1,0 +1,174 @@
+// kv8_append.cu -- new key and value rows into the 8-bit cache: e4m3 codes
+// with one power-of-two scale per block of `block` tokens, KV head and
+// operand, and (optionally) the channel bounds of each block's keys.
+//
+// For every block the append touches, over its new rows x (bf16):
+//   s_new = 2^e, e the least integer with max|x| <= 448 * 2^e  (block_scale)
+//   s     = max(s_old, s_new) if the block already held rows, else s_new
+//   old rows (if s > s_old): code <- e4m3(code * s_old / s)
+//   new rows:                code <- e4m3(x / s)
+//   bounds: per channel, max and min of the new rows and, if the block
+//           already held rows, of what was there.
+//
+// One CTA per (block, KV head, operand): 16 rows of 16 lanes x 16 bytes per
+// pass, all passes in registers, so the rows are read once; the maximum goes
+// through one block reduction.  Bound by memory for prompts (2 bytes read
+// and 1 written per value) and by latency for single tokens.
+#include "fp8.cuh"
+#include "internal.h"
+
+namespace gqa {
+namespace {
+
+constexpr int kD8 = 128;
+
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_min(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Largest finite magnitude of two bf16, as bf16 bits.
+__device__ __forceinline__ uint32_t finite_abs_max(uint32_t w) {
+  const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+  return max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u);
+}
+
+template <int P>  // passes of 16 rows: block = 16 * P
+__global__ void __launch_bounds__(256) kv8_append_kernel(
+    const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
+    const int32_t* __restrict__ positions, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
+    float* v_scale, uint32_t* k_bounds, int B, int S, int Hkv, int L, int nb) {
+  constexpr int T = 16 * P;
+  __shared__ uint32_t s_max[8];
+  __shared__ uint32_t s_hi[8][64], s_lo[8][64];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int h = blockIdx.y >> 1, op = blockIdx.y & 1, b = blockIdx.z;
+  const int pos = positions[b];
+  if (!rows_in_cache(pos, S - 1, L)) return;  // reported by the decode call
+  const int j = pos / T + blockIdx.x;
+  if (j > (pos + S - 1) / T) return;
+  const int tid = threadIdx.x, c = tid & 15, warp = tid >> 5, lane = tid & 31;
+  const uint4* src = op ? v_new : k_new;
+  uint8_t* cache = (op ? v_cache : k_cache) + ((size_t)b * Hkv + h) * L * kD8;
+  float* scale = (op ? v_scale : k_scale) + ((size_t)b * Hkv + h) * nb + j;
+  const int row0 = j * T;
+  const bool had = row0 < pos;
+  const float s_old = had ? *scale : 0.f;
+
+  uint4 x[P];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int t = row0 + i * 16 + (tid >> 4) - pos;  // new token
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (t >= 0 && t < S) x[i] = src[(((size_t)b * S + t) * Hkv + h) * 16 + c];
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    amax = max(max(max(amax, finite_abs_max(x[i].x)), max(finite_abs_max(x[i].y),
+               finite_abs_max(x[i].z))), finite_abs_max(x[i].w));
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if (lane == 0) s_max[warp] = amax;
+
+  const bool bounds = op == 0 && k_bounds != nullptr;
+  if (bounds) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      hi[w] = 0xff80ff80u;  // -inf, -inf
+      lo[w] = 0x7f807f80u;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int t = row0 + i * 16 + (tid >> 4) - pos;
+      if (t >= 0 && t < S) {
+        const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          hi[w] = bf16x2_max(hi[w], w4[w]);
+          lo[w] = bf16x2_min(lo[w], w4[w]);
+        }
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      hi[w] = bf16x2_max(hi[w], __shfl_xor_sync(0xffffffffu, hi[w], 16));
+      lo[w] = bf16x2_min(lo[w], __shfl_xor_sync(0xffffffffu, lo[w], 16));
+      if (lane < 16) {
+        s_hi[warp][c * 4 + w] = hi[w];
+        s_lo[warp][c * 4 + w] = lo[w];
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) amax = max(amax, s_max[w]);
+  const float s_new = block_scale(__uint_as_float(amax << 16));
+  const float s = had ? fmaxf(s_old, s_new) : s_new;
+  if (tid == 0) *scale = s;  // every thread's read of s_old came before the barrier
+  const float inv = 1.f / s;
+
+  if (had && s > s_old) {  // the block's scale grew: move the older rows
+    const float ratio = s_old * inv;
+    for (int r = row0 + (tid >> 4); r < pos; r += 16) {
+      uint2* at = reinterpret_cast<uint2*>(cache + (size_t)r * kD8 + c * 8);
+      uint2 w = *at;
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(((k & 2) ? w.y : w.x) >> ((k & 1) * 16)));
+        o[k] = f32x2_to_e4m3x2(f.x * ratio, f.y * ratio);
+      }
+      *at = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int r = row0 + i * 16 + (tid >> 4), t = r - pos;
+    if (t >= 0 && t < S) {
+      const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        o[k] = f32x2_to_e4m3x2(bf16lo(w4[k]) * inv, bf16hi(w4[k]) * inv);
+      *reinterpret_cast<uint2*>(cache + (size_t)r * kD8 + c * 8) =
+          make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+    }
+  }
+  if (bounds && tid < 128) {  // words 0..63: the maxima, 64..127: the minima
+    const int w = tid & 63;
+    uint32_t* dst = k_bounds + (((size_t)b * Hkv + h) * nb + j) * 128 + tid;
+    uint32_t m = tid < 64 ? s_hi[0][w] : s_lo[0][w];
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      m = tid < 64 ? bf16x2_max(m, s_hi[i][w]) : bf16x2_min(m, s_lo[i][w]);
+    if (had) m = tid < 64 ? bf16x2_max(m, *dst) : bf16x2_min(m, *dst);
+    *dst = m;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_append(const void* k_new, const void* v_new, const int32_t* positions,
+                              void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                              void* k_bounds, int B, int S, int Hkv, int L, int block,
+                              cudaStream_t stream) {
+  const int nb = (L + block - 1) / block;
+  const int touched = min(nb, (S + block - 2) / block + 1);
+  auto kernel = block == 16   ? kv8_append_kernel<1>
+                : block == 32 ? kv8_append_kernel<2>
+                : block == 64 ? kv8_append_kernel<4>
+                              : kv8_append_kernel<8>;
+  return launch_pdl(kernel, dim3(touched, 2 * Hkv, B), dim3(256), 0, stream,
+                    static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), positions,
+                    static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale,
+                    v_scale, static_cast<uint32_t*>(k_bounds), B, S, Hkv, L, nb);
+}
+
+}  // namespace gqa

@@ -1,0 +1,717 @@
+// kv8_decode.cu -- split-KV decode attention over the 8-bit cache (e4m3 codes
+// with a power-of-two scale per block of rows, KV head and operand), over all
+// rows up to each position or over the rows of listed blocks only.
+//
+// For sequence b, query head h and KV head h/g, over the attended rows j:
+//   s_j   = scale * ks_j * (q . k8_j)          ks_j, vs_j: the scales of j's block
+//   out   = sum_j 2^(x_j - M) v8_j / sum_j 2^(x_j - M) / vs_j,
+//   x_j   = log2(e) s_j + log2(vs_j),  M = max x_j
+// which is softmax(s) (vs v8) with the value scale moved into the exponent:
+// every probability then enters its product on the scale of what it
+// contributes, so one fp16 rounding of 2^(x_j - M) is enough whatever the
+// blocks' scales are.
+//
+// Bound by memory: a row costs 256 bytes for K and V, half of the bf16
+// cache's.  How:
+//  * 128-row tiles (32 KB for K and V) stream through a shared-memory ring by
+//    tiled TMA copies (128-byte swizzle: a row of codes is exactly one
+//    swizzle span) issued by a producer warp that also fetches each 16-row
+//    slice's scales one tile ahead and leaves them beside the tile.
+//  * 8 consumer warps take 16 rows each.  e4m3 -> fp16 is exact and one
+//    conversion instruction per two values; both products run on warp-level
+//    MMAs (m16n8k16, fp16 in, fp32 out) with rows or dims as M and the heads
+//    as N, so a KV head's g heads share one conversion of its codes.  q is
+//    scaled per head by a power of two into fp16 (its 8 bits fit).
+//  * The order of the dims in q.k and of the dims in the output blocks is
+//    free, so every lane reads 16-byte pieces without bank conflicts and no
+//    code is moved between lanes: K pieces feed the A operand as they are, V
+//    pieces of two rows are interleaved byte-wise (prmt) before conversion.
+//  * A flat list of all tiles is split evenly over the grid (one CTA per SM);
+//    a segment split over CTAs is merged by the CTA that arrives last, in
+//    CTA order, so results do not depend on timing.
+#include <atomic>
+
+#include "fp8.cuh"
+#include "internal.h"
+#include "decode_params.h"
+#include "tcgen05.cuh"
+#include "warp_ops.cuh"
+
+namespace gqa {
+
+namespace {
+
+constexpr int kD = kDecodeD;
+constexpr int kTile = 128;
+constexpr int kSlices = kTile / 16;         // one per consumer warp
+constexpr int kOpBytes = kTile * kD;        // 16 KB per operand
+constexpr int kStageBytes = 2 * kOpBytes;
+constexpr int kWarps = kSlices;
+constexpr int kConsumers = kWarps * 32;
+constexpr int kThreads = kConsumers + 32;
+constexpr int kMaxStages = 6;
+constexpr int kMiscInts = 32;
+constexpr int kNoRow = 0x40000000;          // row of a slice that holds nothing
+constexpr float kMInit = -1e30f;            // running maximum before any row
+constexpr float kTau = 8.f;                 // the running maximum may lag by 2^kTau
+constexpr float kShift = 6.f;               // probabilities sit at 2^kShift .. 2^(kShift+kTau)
+constexpr int kMaxSmem = 227 * 1024;
+constexpr int kWholeTiles = 4;              // segments this short are not split
+
+struct SliceMeta {
+  int row0;       // first row, or kNoRow
+  float ks;       // K scale
+  float lv;       // log2 of the V scale
+  float inv_vs;   // 1 / V scale
+};
+
+struct Kv8Params {
+  const uint16_t* q;
+  const int32_t* positions;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* index;  // [B, Hkv, count], or null
+  uint16_t* out;
+  uint32_t* status;
+  uint32_t* counters;
+  float* part_ml;        // [slots][g][2]
+  float* part_o;         // [slots][g][kD]
+  int B, Hq, Hkv, L, g;
+  int lb;                // log2 of the block's rows
+  int nb;                // blocks of a cache
+  int count;
+  int stages;
+  int test_skip;
+  float qscale;          // scale * log2(e)
+};
+
+template <int NT> struct Lay {
+  static constexpr int kHeads = 8 * NT;
+  static constexpr int kMergeFloats = kWarps * kHeads * (kD + 2);
+  static size_t bytes(int stages, int B) {
+    return (size_t)stages * kStageBytes + kMergeFloats * 4 + stages * kSlices * sizeof(SliceMeta) +
+           (2 * stages + 2) * 8 + kMiscInts * 4 + ((size_t)B + 1) * 4;
+  }
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// A place in the flat (sequence, KV head, tile) order.
+struct Walk8 {
+  int b, kvh, k, nt, pos;
+};
+__device__ __forceinline__ void walk8_init(Walk8& w, long long t, const int* prefix,
+                                           const int32_t* positions, int B, int Hkv) {
+  int lo = 0, hi = B - 1;  // largest b with Hkv*prefix[b] <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((long long)Hkv * prefix[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  w.b = lo;
+  w.nt = prefix[lo + 1] - prefix[lo];
+  const long long off = t - (long long)Hkv * prefix[lo];
+  w.kvh = (int)(off / w.nt);
+  w.k = (int)(off % w.nt);
+  w.pos = positions[lo];
+}
+// To the first tile of the next segment.
+__device__ __forceinline__ void walk8_segment(Walk8& w, const int* prefix,
+                                              const int32_t* positions, int B, int Hkv) {
+  w.k = 0;
+  if (++w.kvh < Hkv) return;
+  w.kvh = 0;
+  do { ++w.b; } while (w.b < B && prefix[w.b + 1] == prefix[w.b]);
+  if (w.b < B) {
+    w.nt = prefix[w.b + 1] - prefix[w.b];
+    w.pos = positions[w.b];
+  }
+}
+
+// One consumer warp: 16 rows of each tile for one KV head's g <= 8*NT heads.
+// Lane 4c + t.
+//  * S = K q^T: MMA row c is slice row c (c+8 the upper half), columns the
+//    heads.  MMA step w takes dims 32t + 4w .. +3 of every lane t, so a
+//    lane's 32 bytes of a row are its operand and q is held to match.
+//  * P^T by 8x8 transposes; O^T += V^T P^T: MMA m-block i holds dims 16c+2i
+//    (row c) and 16c+2i+1 (row c+8); keys 2t, 2t+1, 2t+8, 2t+9 per lane.
+template <int NT>
+struct Consumer8 {
+  uint32_t qb[NT][8][2];
+  float o[NT][8][4];
+  float m[NT][2], l[NT][2], qk[NT][2];
+  int c, t;
+
+  __device__ __forceinline__ void load_q(const Kv8Params& p, int b, int kvh) {
+    const uint16_t* base = p.q + ((size_t)b * p.Hq + (size_t)kvh * p.g) * kD;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = 8 * n + c;
+      uint4 u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        u[i] = h < p.g ? *reinterpret_cast<const uint4*>(base + (size_t)h * kD + 32 * t + 8 * i)
+                       : make_uint4(0u, 0u, 0u, 0u);
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          amax = fmax3(amax, fabsf(bf16lo(word(u[i], w))), fabsf(bf16hi(word(u[i], w))));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // q * 2^(7-ex) lies below 2^8: exact in fp16 down to 2^-22 of the
+      // head's largest element, and off by 2^-33 of it below
+      const int ex = max((int)(__float_as_uint(amax) >> 23) - 127, -119);
+      const float f = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+      const float un = __uint_as_float((uint32_t)(127 - 7 + ex) << 23) * p.qscale;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t x = word(u[i], w);
+          qb[n][2 * i + (w >> 1)][w & 1] = pack_f16x2(bf16lo(x) * f, bf16hi(x) * f);
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qk[n][e] = __shfl_sync(0xffffffffu, un, 4 * (2 * t + e));
+    }
+  }
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[n][e] = kMInit;
+        l[n][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[n][i][k] = 0.f;
+    }
+  }
+  // 16 rows at Ks, Vs (the slice's first row in the tile), of which the
+  // first `rows` count (rows >= 1); the others may hold anything.
+  __device__ __forceinline__ void slice(const uint8_t* Ks, const uint8_t* Vs, int rows,
+                                        const SliceMeta& meta) {
+    uint4 ka[2], kb[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ka[i] = lds128(Ks + sw128(c, 2 * t + i));
+      kb[i] = lds128(Ks + sw128(c + 8, 2 * t + i));
+    }
+    float s[NT][2][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[n][0][k] = s[n][1][k] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const uint32_t wa = word(ka[w >> 2], w & 3), wb = word(kb[w >> 2], w & 3);
+      const uint32_t a0 = e4m3x2_to_f16x2(wa), a2 = e4m3x2_to_f16x2(wa >> 16);
+      const uint32_t a1 = e4m3x2_to_f16x2(wb), a3 = e4m3x2_to_f16x2(wb >> 16);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        mma_f16(s[n][w & 1], a0, a1, a2, a3, qb[n][w][0], qb[n][w][1]);
+    }
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 2 * t + (k & 1) + 8 * (k >> 1);
+      v[k] = lds128(Vs + sw128(r, c));
+      if (r >= rows) v[k] = make_uint4(0u, 0u, 0u, 0u);  // may be NaN: 0 * NaN would spread
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float sc = s[n][0][k] + s[n][1][k];
+        x[k] = (c + 8 * (k >> 1)) < rows ? fmaf(sc, qk[n][k & 1] * meta.ks, meta.lv) : -INFINITY;
+      }
+      const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+      if (__any_sync(0xffffffffu, mx0 > m[n][0] + kTau || mx1 > m[n][1] + kTau)) {
+        float mx[2] = {mx0, mx1};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1)
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], off));
+          const float to = mx[e] > m[n][e] + kTau ? mx[e] : m[n][e];
+          const float alpha = ex2(m[n][e] - to);
+          m[n][e] = to;
+          l[n][e] *= alpha;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[n][i][e] *= alpha;
+            o[n][i][2 + e] *= alpha;
+          }
+        }
+      }
+      float pr[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pr[k] = ex2(x[k] - (m[n][k & 1] - kShift));
+      l[n][0] = fmaf(pr[0] + pr[2], meta.inv_vs, l[n][0]);
+      l[n][1] = fmaf(pr[1] + pr[3], meta.inv_vs, l[n][1]);
+      // one rounding to fp16 (2^-12 relative), far below the bf16 output's 2^-9
+      pb[n][0] = movm_trans(pack_f16x2(pr[0], pr[1]));
+      pb[n][1] = movm_trans(pack_f16x2(pr[2], pr[3]));
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint32_t sel = hf ? 0x7362u : 0x5140u;
+        const uint32_t e0 = prmt(word(v[0], w), word(v[1], w), sel);
+        const uint32_t e1 = prmt(word(v[2], w), word(v[3], w), sel);
+        const uint32_t a0 = e4m3x2_to_f16x2(e0), a1 = e4m3x2_to_f16x2(e0 >> 16);
+        const uint32_t a2 = e4m3x2_to_f16x2(e1), a3 = e4m3x2_to_f16x2(e1 >> 16);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * w + hf], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+      }
+    }
+  }
+  // This warp's (m, l, o) -> ml [warp][heads][2], mo [warp][heads][kD].
+  __device__ __forceinline__ void stash(float* mo, float* ml, int warp, int g) {
+    constexpr int H = Lay<NT>::kHeads;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[n][e];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const int h = 8 * n + 2 * t + e;
+        if (h < g) {
+          float4* dst = reinterpret_cast<float4*>(mo + (warp * H + h) * kD + 16 * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_float4(o[n][2 * i][e], o[n][2 * i][2 + e], o[n][2 * i + 1][e],
+                                 o[n][2 * i + 1][2 + e]);
+          if (c == 0) {
+            ml[(warp * H + h) * 2] = m[n][e];
+            ml[(warp * H + h) * 2 + 1] = sum;
+          }
+        }
+      }
+  }
+};
+
+__device__ __forceinline__ void store_bf16(uint16_t* out, size_t i, float x) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(x);
+  out[i] = *reinterpret_cast<const uint16_t*>(&h);
+}
+
+template <int NT, bool LIST>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const Kv8Params p) {
+  constexpr int H = Lay<NT>::kHeads;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int NS = p.stages;
+  uint8_t* stages = smem;
+  float* merge_o = reinterpret_cast<float*>(smem + (size_t)NS * kStageBytes);  // [warps][H][kD]
+  float* merge_ml = merge_o + kWarps * H * kD;                                 // [warps][H][2]
+  SliceMeta* meta = reinterpret_cast<SliceMeta*>(merge_ml + kWarps * H * 2);   // [NS][kSlices]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(meta + NS * kSlices);           // full, empty, sync
+  int* misc = reinterpret_cast<int*>(bars + 2 * NS + 2);  // [0] abort, [1] last, [8..16) scan
+  int* prefix = misc + kMiscInts;                         // [B+1]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int B = p.B, Hkv = p.Hkv, L = p.L, g = p.g;
+  volatile int* abort_flag = misc;
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_u32(&bars[s]), 1);
+      mbar_init(smem_u32(&bars[NS + s]), kWarps);
+    }
+    mbar_init(smem_u32(&bars[2 * NS]), kWarps);
+    misc[0] = 0;
+    fence_mbar_init();
+  }
+  grid_dependency_wait();
+  grid_dependents_launch();
+
+  // ---- tiles per sequence and their exclusive prefix sum (every CTA) ------
+  const int list_tiles = LIST ? (int)((((long long)p.count << p.lb) + kTile - 1) / kTile) : 0;
+  int carry = 0;
+  for (int base = 0; base < B; base += kConsumers) {
+    const int b = base + tid;
+    int v = 0;
+    if (tid < kConsumers && b < B) {
+      const int pos = p.positions[b];
+      if (rows_in_cache(pos, 0, L)) {
+        v = LIST ? list_tiles : pos / kTile + 1;
+      } else if (b % (int)gridDim.x == (int)blockIdx.x) {
+        // out-of-range position: flag it and make the sequence's output NaN
+        set_status(p.status, ATTN_DEV_BAD_POSITION);
+        uint4* row = reinterpret_cast<uint4*>(p.out + (size_t)b * p.Hq * kD);
+        for (int i = 0; i < p.Hq * kD / 8; ++i)
+          row[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+      }
+    }
+    int x = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    if (lane == 31 && warp < kWarps) misc[8 + warp] = x;
+    __syncthreads();
+    int before = 0, chunk = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int s = misc[8 + w];
+      before += w < warp ? s : 0;
+      chunk += s;
+    }
+    if (tid < kConsumers && b < B) prefix[b] = carry + before + x - v;
+    carry += chunk;
+    __syncthreads();
+  }
+  if (tid == 0) prefix[B] = carry;
+  __syncthreads();
+
+  const long long T = (long long)Hkv * carry;  // all tiles
+  // As many CTAs as there are tiles at most; one per segment where segments
+  // are short (a split costs a round trip through L2).
+  const long long nseg = (long long)B * Hkv;
+  long long gw = min((long long)gridDim.x, T);
+  if (T <= (long long)kWholeTiles * nseg) gw = min(gw, nseg);
+  const int G = (int)gw;
+  if ((int)blockIdx.x >= G) return;
+  const long long t0 = T * blockIdx.x / G, t1 = T * (blockIdx.x + 1) / G;
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer --
+    // lanes 0-7: slice `lane` and its K scale; lanes 8-15: the V scales
+    const int slice = lane & 7, op = (lane >> 3) & 1;
+    const float* scales = op ? p.v_scale : p.k_scale;
+    const int entry_rows = 1 << p.lb;
+    const int in_block = (slice * 16) & (entry_rows - 1);
+    const int entry = (slice * 16) >> p.lb;            // of this slice, within a tile
+    const int per_tile = kTile >> p.lb;
+    // the block a listed tile's slice lies in (-1: none)
+    auto fetch = [&](const Walk8& w) -> int {
+      const int e = w.k * per_tile + entry;
+      return e < p.count ? p.index[((size_t)w.b * Hkv + w.kvh) * p.count + e] : -1;
+    };
+    auto row_of = [&](const Walk8& w, int blk) -> int {
+      int row;
+      if (LIST) {
+        row = blk >= 0 && blk < p.nb ? (blk << p.lb) + in_block : kNoRow;
+        if ((blk < -1 || blk >= p.nb) && op == 0) set_status(p.status, ATTN_DEV_BAD_BLOCK);
+      } else {
+        row = w.k * kTile + slice * 16;
+      }
+      return row <= w.pos ? row : kNoRow;
+    };
+    auto scale_of = [&](const Walk8& w, int row) -> float {
+      return row != kNoRow ? scales[((size_t)w.b * Hkv + w.kvh) * p.nb + (row >> p.lb)] : 1.f;
+    };
+    auto next = [&](Walk8& w) {
+      if (++w.k == w.nt) walk8_segment(w, prefix, p.positions, B, Hkv);
+    };
+    // two walks: `w` is the tile to issue, `a` the one after it, whose list
+    // entries and scales are on their way
+    Walk8 w, a;
+    walk8_init(w, t0, prefix, p.positions, B, Hkv);
+    a = w;
+    int row = row_of(w, LIST ? fetch(w) : 0);
+    float sc = scale_of(w, row);
+    int blk_next = 0;
+    if (t0 + 1 < t1) {
+      next(a);
+      if (LIST) blk_next = fetch(a);
+    }
+    for (long long i = 0; t0 + i < t1; ++i) {
+      const int s = (int)(i % NS);
+      const uint32_t u = (uint32_t)(i / NS);
+      int row_next = kNoRow;
+      float sc_next = 1.f;
+      Walk8 a2 = a;
+      int blk_next2 = 0;
+      if (t0 + i + 1 < t1) {
+        row_next = row_of(a, blk_next);
+        sc_next = scale_of(a, row_next);
+        if (t0 + i + 2 < t1) {
+          next(a2);
+          if (LIST) blk_next2 = fetch(a2);
+        }
+      }
+      if (i >= NS && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[NS + s]), (u & 1u) ^ 1u,
+                                                        abort_flag))) {
+        if (lane == 0) {
+          *abort_flag = 1;
+          set_status(p.status, ATTN_DEV_TIMEOUT);
+        }
+        break;
+      }
+      const float v = __shfl_down_sync(0xffffffffu, sc, 8);  // the slice's V scale
+      if (lane < kSlices) {
+        SliceMeta mt;
+        mt.row0 = row;
+        mt.ks = sc;
+        // log2 of a power of two comes out exact
+        const uint32_t bits = __float_as_uint(v);
+        mt.lv = (float)((int)(bits >> 23) - 127) +
+                log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
+        mt.inv_vs = 1.f / v;
+        meta[s * kSlices + lane] = mt;
+      }
+      const uint32_t full = smem_u32(&bars[s]);
+      const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes), sV = sK + kOpBytes;
+      const int z = w.b * Hkv + w.kvh;
+      const bool skip = p.test_skip >= 0 && z == 0 && w.k == p.test_skip;  // failure-path tests
+      if (LIST) {
+        const bool issue = lane < kSlices && in_block == 0 && row != kNoRow &&
+                           range_ok(row >= 0 && row < L && z < B * Hkv, p.status);
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
+        __syncwarp();
+        if (!skip) {
+          if (lane == 0) mbar_arrive_expect_tx(full, boxes * (uint32_t)entry_rows * 2u * kD);
+          __syncwarp();
+          if (issue) {
+            tma_load_3d(sK + slice * 16 * kD, &tm_k, 0, row, z, full);
+            tma_load_3d(sV + slice * 16 * kD, &tm_v, 0, row, z, full);
+          }
+        }
+      } else {
+        __syncwarp();
+        if (lane == 0 && !skip && range_ok(row >= 0 && row < L && z < B * Hkv, p.status)) {
+          mbar_arrive_expect_tx(full, kStageBytes);
+          tma_load_3d(sK, &tm_k, 0, row, z, full);
+          tma_load_3d(sV, &tm_v, 0, row, z, full);
+        }
+      }
+      w = a;
+      a = a2;
+      row = row_next;
+      sc = sc_next;
+      blk_next = blk_next2;
+      __syncwarp();
+    }
+  } else {
+    // ----------------------------------------------------------- consumers --
+    ConsumerSync csync{smem_u32(&bars[2 * NS]), abort_flag, p.status, 0u};
+    Consumer8<NT> cs;
+    cs.c = lane >> 2;
+    cs.t = lane & 3;
+    Walk8 w;
+    walk8_init(w, t0, prefix, p.positions, B, Hkv);
+    bool first_piece = true;
+    int s = 0;
+    uint32_t ph = 0;
+    for (long long t = t0; t < t1;) {
+      const int len = (int)min((long long)(w.nt - w.k), t1 - t);
+      cs.load_q(p, w.b, w.kvh);
+      cs.reset();
+      bool ok = true;
+      for (int i = 0; i < len; ++i) {
+        if (!consumer_wait(smem_u32(&bars[s]), ph, abort_flag, p.status, lane)) {
+          ok = false;
+          break;
+        }
+        const SliceMeta mt = meta[s * kSlices + warp];
+        const int rows = min(16, w.pos + 1 - mt.row0);
+        const uint8_t* Ks = stages + (size_t)s * kStageBytes + warp * 16 * kD;
+        if (rows > 0) cs.slice(Ks, Ks + kOpBytes, rows, mt);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars[NS + s]));
+        if (++s == NS) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      cs.stash(merge_o, merge_ml, warp, g);
+      csync(lane);
+      // ---- this CTA's part: the 8 warps' partials, in warp order -----------
+      const bool whole = w.k == 0 && len == w.nt;
+      const int seg = w.b * Hkv + w.kvh;
+      const int slot = 2 * blockIdx.x + (first_piece ? 0 : 1);
+      uint16_t* out = p.out + ((size_t)w.b * p.Hq + (size_t)w.kvh * g) * kD;
+      if (!*abort_flag) {
+        for (int i = tid; i < g * kD; i += kConsumers) {
+          const int h = i / kD, d = i % kD;
+          float M = kMInit;
+#pragma unroll
+          for (int ww = 0; ww < kWarps; ++ww) M = fmaxf(M, merge_ml[(ww * H + h) * 2]);
+          float ls = 0.f, os = 0.f;
+#pragma unroll
+          for (int ww = 0; ww < kWarps; ++ww) {
+            const float e = ex2(merge_ml[(ww * H + h) * 2] - M);
+            ls = fmaf(merge_ml[(ww * H + h) * 2 + 1], e, ls);
+            os = fmaf(merge_o[(ww * H + h) * kD + d], e, os);
+          }
+          if (whole) {
+            store_bf16(out, i, ls == 0.f ? 0.f : os / ls);
+          } else {
+            p.part_o[((size_t)slot * g) * kD + i] = os;
+            if (d == 0) {
+              p.part_ml[((size_t)slot * g + h) * 2] = M;
+              p.part_ml[((size_t)slot * g + h) * 2 + 1] = ls;
+            }
+          }
+        }
+        if (!whole) {
+          // ---- the segment's last CTA to arrive merges its parts ------------
+          const long long f0 = t - w.k, f1 = f0 + w.nt;  // the segment in the flat list
+          const int c0 = cta_of(f0, T, G), c1 = cta_of(f1 - 1, T, G);
+          __threadfence();
+          csync(lane);
+          if (tid == 0) {
+            const uint32_t before = atomicAdd(&p.counters[seg], 1u);
+            misc[1] = before + 1 == (uint32_t)(c1 - c0 + 1);
+            if (misc[1]) p.counters[seg] = 0;
+            __threadfence();
+          }
+          csync(lane);
+          if (misc[1] && !*abort_flag) {
+            __threadfence();
+            // CTA c0's part is its second unless the segment opens its range
+            const int slot0 = 2 * c0 + (T * c0 / G == f0 ? 0 : 1);
+            for (int i = tid; i < g * kD; i += kConsumers) {
+              const int h = i / kD;
+              float M = kMInit;
+              for (int cc = c0; cc <= c1; ++cc) {
+                const int sl = cc == c0 ? slot0 : 2 * cc;
+                M = fmaxf(M, __ldcg(&p.part_ml[((size_t)sl * g + h) * 2]));
+              }
+              float ls = 0.f, os = 0.f;
+              for (int cc = c0; cc <= c1; ++cc) {
+                const int sl = cc == c0 ? slot0 : 2 * cc;
+                const float e = ex2(__ldcg(&p.part_ml[((size_t)sl * g + h) * 2]) - M);
+                ls = fmaf(__ldcg(&p.part_ml[((size_t)sl * g + h) * 2 + 1]), e, ls);
+                os = fmaf(__ldcg(&p.part_o[((size_t)sl * g) * kD + i]), e, os);
+              }
+              store_bf16(out, i, ls == 0.f ? 0.f : os / ls);
+            }
+          }
+        }
+      }
+      csync(lane);  // the merge buffers may be written again
+      if (*abort_flag) break;
+      t += len;
+      first_piece = false;
+      if (t < t1) walk8_segment(w, prefix, p.positions, B, Hkv);
+    }
+  }
+  if (*abort_flag) {  // copies in flight land before the shared memory goes
+    const uint64_t t_start = globaltimer_ns();
+    while (globaltimer_ns() - t_start < 2000000ull) {
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host --
+
+int num_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  int n = known[dev].load();
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+      n = 148;
+    known[dev].store(n);
+  }
+  return n;
+}
+
+// A cache [segs, L, 128] of codes as a 3-D tensor map, box 128 codes x rows x
+// 1, 128-byte swizzle.  Rows past L read as zeros.
+bool codes_map(CUtensorMap* m, const void* ptr, int L, long long segs, int rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)L, (cuuint64_t)segs};
+  cuuint64_t strides[2] = {(cuuint64_t)kD, (cuuint64_t)kD * (cuuint64_t)L};
+  cuuint32_t box[3] = {(cuuint32_t)kD, (cuuint32_t)rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+template <int NT, bool LIST>
+cudaError_t launch8(Kv8Params& p, const CUtensorMap& mk, const CUtensorMap& mv,
+                    cudaStream_t stream) {
+  p.stages = kMaxStages;
+  while (p.stages > 2 && Lay<NT>::bytes(p.stages, p.B) > (size_t)kMaxSmem) --p.stages;
+  const size_t smem = Lay<NT>::bytes(p.stages, p.B);
+  const cudaError_t e = cudaFuncSetAttribute(
+      kv8_decode_kernel<NT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv8_decode_kernel<NT, LIST>, dim3(min(kKv8MaxGrid, num_sms())),
+                    dim3(kThreads), smem, stream, mk, mv, p);
+}
+
+}  // namespace
+
+DecodeWorkspace kv8_workspace_layout(int B, int Hq, int Hkv) {
+  auto align256 = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  DecodeWorkspace w{};
+  const int g = Hq / Hkv;
+  w.slots = 2 * kKv8MaxGrid;
+  w.status_off = 0;
+  w.ticket_off = 128;
+  w.counters_off = 256;
+  w.ml_off = align256(w.counters_off + (size_t)B * Hkv * sizeof(uint32_t));
+  w.o_off = align256(w.ml_off + (size_t)w.slots * g * 2 * sizeof(float));
+  w.total = align256(w.o_off + (size_t)w.slots * g * kD * sizeof(float));
+  return w;
+}
+
+cudaError_t launch_kv8_decode(const void* q, const int32_t* positions, const void* k_cache,
+                              const void* v_cache, const float* k_scale, const float* v_scale,
+                              const int32_t* block_index, int count, int B, int Hq, int Hkv,
+                              int L, int block, float scale, void* out, void* workspace,
+                              cudaStream_t stream) {
+  const DecodeWorkspace ws = kv8_workspace_layout(B, Hq, Hkv);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  Kv8Params p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.positions = positions;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.index = block_index;
+  p.out = static_cast<uint16_t*>(out);
+  p.status = reinterpret_cast<uint32_t*>(base + ws.status_off);
+  p.counters = reinterpret_cast<uint32_t*>(base + ws.counters_off);
+  p.part_ml = reinterpret_cast<float*>(base + ws.ml_off);
+  p.part_o = reinterpret_cast<float*>(base + ws.o_off);
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.L = L;
+  p.g = Hq / Hkv;
+  p.lb = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+  p.nb = (L + block - 1) / block;
+  p.count = count;
+  p.stages = 0;
+  p.test_skip = g_decode_test_skip;
+  p.qscale = scale * 1.4426950408889634f;
+  CUtensorMap mk, mv;
+  const int rows = block_index ? block : kTile;
+  if (!codes_map(&mk, k_cache, L, (long long)B * Hkv, rows) ||
+      !codes_map(&mv, v_cache, L, (long long)B * Hkv, rows))
+    return cudaErrorInvalidValue;
+  if (block_index)
+    return p.g <= 8 ? launch8<1, true>(p, mk, mv, stream) : launch8<2, true>(p, mk, mv, stream);
+  return p.g <= 8 ? launch8<1, false>(p, mk, mv, stream) : launch8<2, false>(p, mk, mv, stream);
+}
+
+}  // namespace gqa

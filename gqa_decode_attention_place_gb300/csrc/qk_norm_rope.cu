@@ -1,0 +1,192 @@
+// qk_norm_rope.cu -- RMS norm of every query and key head followed by the
+// rotary embedding, in one pass, with the key and value rows written to the
+// bf16 cache in the same launch when there is one.
+//
+// For a row x of D dims (one head of one token), weight w, and the rotation
+// row (cos, sin) of the token's position:
+//   y      = x * rsqrt(mean(x^2) + eps) * w
+//   out[d] = y[d]*cos[d] - y[d+D/2]*sin[d]      for d <  D/2
+//   out[d] = y[d]*cos[d] + y[d-D/2]*sin[d]      for d >= D/2
+// all in fp32, rounded to bf16 once at the end.
+//
+// A lane holds dims 8c..8c+7 and their partners D/2 further on, so the
+// rotation needs no exchange between lanes; the row's D/16 lanes (padded to
+// a power of two) share only the sum of squares.  A warp stays with one
+// token, so the rotation row (32 values per lane) is read once and serves
+// every head the warp takes.  Bound by memory for prompts, by latency for
+// single tokens.
+#include "common.cuh"
+#include "internal.h"
+
+namespace gqa {
+namespace {
+
+struct NormRopeParams {
+  const uint16_t *q, *k, *v;
+  long long q_stride, k_stride, v_stride;  // elements from token to token
+  const uint16_t *q_weight, *k_weight;     // [D] or null (ones)
+  const float *cos, *sin;                  // [L, D] or null (no rotation)
+  const int32_t* positions;                // [B]; token t of sequence b sits at positions[b] + t
+  uint16_t *q_out, *k_out;                 // k_out null: keys and values go to the caches
+  uint8_t *k_cache, *v_cache;
+  float eps;
+  int N, S, Hq, Hkv, D, L;                 // N = B * S tokens
+};
+
+constexpr int kNormWarps = 4;
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  f[0] = bf16lo(u.x); f[1] = bf16hi(u.x); f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
+  f[4] = bf16lo(u.z); f[5] = bf16hi(u.z); f[6] = bf16lo(u.w); f[7] = bf16hi(u.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ void load8f(const float* p, float (&f)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  const float4 b = *reinterpret_cast<const float4*>(p + 4);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+// LPR lanes per row (a power of two >= D/16).  A warp handles 32/LPR heads at
+// a time, `steps` times, of one token; blockIdx.y and the warp pick the heads.
+template <int LPR>
+__global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const NormRopeParams p,
+                                                                       int warps_per_token,
+                                                                       int steps) {
+  constexpr int RPW = 32 / LPR;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int lane = threadIdx.x & 31;
+  const long long gw = (long long)blockIdx.x * kNormWarps + (threadIdx.x >> 5);
+  const long long n = gw / warps_per_token;
+  if (n >= p.N) return;
+  const int part = (int)(gw % warps_per_token);
+  const int c = lane % LPR, D = p.D, half = D >> 1;
+  const bool on = c * 16 < D;  // lanes past D/16 only take part in the shuffles
+  const int d0 = c * 8;
+  const int b = (int)(n / p.S), t = (int)(n % p.S);
+  const int pos0 = p.positions[b];
+  const bool ok = rows_in_cache(pos0, p.S - 1, p.L);
+  const int pos = pos0 + t;
+  float ca[8], cb[8], sa[8], sb[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    ca[i] = cb[i] = 1.f;
+    sa[i] = sb[i] = 0.f;
+  }
+  if (p.cos && ok && on) {
+    const size_t row = (size_t)pos * D + d0;
+    load8f(p.cos + row, ca);
+    load8f(p.cos + row + half, cb);
+    load8f(p.sin + row, sa);
+    load8f(p.sin + row + half, sb);
+  }
+  const int heads = p.Hq + p.Hkv * (p.k_out ? 1 : 2);
+  for (int st = 0; st < steps; ++st) {
+    const int head = (part * steps + st) * RPW + lane / LPR;
+    const bool row_on = on && head < heads;
+    const bool is_q = head < p.Hq, is_v = head >= p.Hq + p.Hkv;
+    const int h = is_q ? head : is_v ? head - p.Hq - p.Hkv : head - p.Hq;
+    const uint16_t* src = is_q   ? p.q + n * p.q_stride
+                          : is_v ? p.v + n * p.v_stride
+                                 : p.k + n * p.k_stride;
+    uint4 ua = make_uint4(0u, 0u, 0u, 0u), ub = ua;
+    if (row_on) {
+      ua = *reinterpret_cast<const uint4*>(src + (size_t)h * D + d0);
+      ub = *reinterpret_cast<const uint4*>(src + (size_t)h * D + d0 + half);
+    }
+    float xa[8], xb[8];
+    unpack8(ua, xa);
+    unpack8(ub, xb);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
+#pragma unroll
+    for (int off = 1; off < LPR; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    if (!row_on) continue;
+    if (!is_v) {
+      const float r = rsqrtf(ss / (float)D + p.eps);
+      float wa[8], wb[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.f;
+      const uint16_t* w = is_q ? p.q_weight : p.k_weight;
+      if (w) {
+        unpack8(*reinterpret_cast<const uint4*>(w + d0), wa);
+        unpack8(*reinterpret_cast<const uint4*>(w + d0 + half), wb);
+      }
+      float oa[8], ob[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float ya = xa[i] * r * wa[i], yb = xb[i] * r * wb[i];
+        oa[i] = ya * ca[i] - yb * sa[i];
+        ob[i] = yb * cb[i] + ya * sb[i];
+        if (!ok) oa[i] = ob[i] = __uint_as_float(0x7fffffffu);
+      }
+      ua = pack8(oa);
+      ub = pack8(ob);
+    }
+    uint16_t* dst;
+    if (is_q) {
+      dst = p.q_out + ((size_t)n * p.Hq + h) * D;
+    } else if (p.k_out) {
+      dst = p.k_out + ((size_t)n * p.Hkv + h) * D;
+    } else {
+      if (!ok) continue;  // nothing of this sequence is written to the cache
+      dst = reinterpret_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) +
+            (((size_t)b * p.Hkv + h) * p.L + pos) * D;
+    }
+    *reinterpret_cast<uint4*>(dst + d0) = ua;
+    *reinterpret_cast<uint4*>(dst + d0 + half) = ub;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_rope(const void* q, const void* k, const void* v, long long q_stride,
+                                long long k_stride, long long v_stride, const void* q_weight,
+                                const void* k_weight, float eps, const float* cos,
+                                const float* sin, const int32_t* positions, int B, int S, int Hq,
+                                int Hkv, int D, int L, void* q_out, void* k_out, void* k_cache,
+                                void* v_cache, cudaStream_t stream) {
+  NormRopeParams p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_weight = static_cast<const uint16_t*>(q_weight);
+  p.k_weight = static_cast<const uint16_t*>(k_weight);
+  p.cos = cos;
+  p.sin = sin;
+  p.positions = positions;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.eps = eps;
+  p.N = B * S;
+  p.S = S;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.L = L;
+  int lpr = 1;
+  while (lpr * 16 < D) lpr *= 2;
+  const int rpw = 32 / lpr;
+  const int all = (Hq + Hkv * (k_out ? 1 : 2) + rpw - 1) / rpw;  // steps of one warp for a token
+  const int steps = 1, wpt = (all + steps - 1) / steps;
+  const long long blocks = ((long long)p.N * wpt + kNormWarps - 1) / kNormWarps;
+  auto kernel = lpr == 1   ? qk_norm_rope_kernel<1>
+                : lpr == 2 ? qk_norm_rope_kernel<2>
+                : lpr == 4 ? qk_norm_rope_kernel<4>
+                : lpr == 8 ? qk_norm_rope_kernel<8>
+                           : qk_norm_rope_kernel<16>;
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kNormWarps * 32), 0, stream, p, wpt,
+                    steps);
+}
+
+}  // namespace gqa

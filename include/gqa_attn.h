@@ -63,6 +63,8 @@ extern "C" {
                                         a cluster landing slot, a partial-result slot, an
                                         output or new-row address) failed its range check
                                         and was skipped; the launch's outputs are undefined */
+#define ATTN_DEV_BAD_BLOCK     0x8u  /* a listed block below -1 or past the cache's last one
+                                        (attn_decode_step_kv8_blocks); it was skipped */
 
 /*
  * attn_kv_append -- the in-place cache write of the decode page, section 4.1
@@ -307,6 +309,186 @@ int attn_decode_step_noalloc(const void* q, const int32_t* positions,
                              const void* k_cache, const void* v_cache,
                              int B, int Hq, int Hkv, int L, int D, float scale,
                              void* out, cudaStream_t stream);
+
+/*
+ * attn_qk_norm_rope -- RMS norm of every query and key head and the rotary
+ * embedding, in one pass.  For each row x (one head of one token, D dims) with
+ * the head's weight w (one vector of D for all query heads, one for all key
+ * heads):
+ *     y[d]  = x[d] * w[d] / sqrt(mean(x^2) + eps)
+ *     x'[d] = y[d]*cos[d] - y[d+D/2]*sin[d]          for d <  D/2
+ *     x'[d] = y[d]*cos[d] + y[d-D/2]*sin[d]          for d >= D/2
+ * in fp32 (the rotate-half form of attn_decode_step_rope_append), rounded to
+ * bf16 once at the end.
+ *
+ *   q            : [N, Hq, D] bf16, token n at q + n * q_stride elements; the
+ *                  heads of a token are dense.  k: [N, Hkv, D] with k_stride.
+ *                  Strides let both be views of one fused projection buffer.
+ *   q_weight,
+ *   k_weight     : [D] bf16, or null for ones.
+ *   cos_table,
+ *   sin_table    : [L, D] fp32, row p the rotation at position p; both null for
+ *                  no rotation.
+ *   positions    : [N] int32, device memory, token n's position.
+ *   q_out, k_out : [N, Hq, D] and [N, Hkv, D] bf16, dense.  They may be q and k
+ *                  themselves where those are dense; no other overlap.
+ *   Supported: D a multiple of 16, 16 <= D <= 256; N >= 0 (0 does nothing);
+ *   strides multiples of 8 and at least a token's heads.
+ *
+ * A position outside [0, L) gives NaN in that token's rows.
+ * Errors: ATTN_ERR_INVALID_ARG also for exactly one of cos_table and sin_table
+ * null, a bad stride, or eps negative or not finite.
+ */
+int attn_qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
+                      const void* q_weight, const void* k_weight, float eps,
+                      const int32_t* positions, const float* cos_table, const float* sin_table,
+                      int N, int Hq, int Hkv, int D, int L, void* q_out, void* k_out,
+                      cudaStream_t stream);
+
+/*
+ * attn_qk_norm_rope_append -- attn_qk_norm_rope for S new tokens per sequence
+ * with the cache write of attn_kv_append in the same launch: the normed and
+ * rotated keys and the values as they are become rows positions[b] + t of the
+ * bf16 cache.  S = 1 is a decode step's, a long S a prompt's.
+ *
+ *   q            : [B, S, Hq, D] bf16, token b*S + t at q + (b*S + t) * q_stride;
+ *                  k_new, v_new: [B, S, Hkv, D] with k_stride and v_stride.
+ *   positions    : [B] int32, device memory: the first new token's position.
+ *   k_cache,
+ *   v_cache      : [B, Hkv, L, D] bf16, written in place.
+ *   q_out        : [B, S, Hq, D] bf16, dense.
+ *   the rest, sizes and errors: as attn_qk_norm_rope (S = 0 does nothing).
+ *
+ * A sequence whose rows positions[b] .. positions[b] + S - 1 are not all in
+ * [0, L) gets no cache write and NaN in its rows of q_out.
+ */
+int attn_qk_norm_rope_append(const void* q, const void* k_new, const void* v_new,
+                             int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                             const void* q_weight, const void* k_weight, float eps,
+                             const int32_t* positions, const float* cos_table,
+                             const float* sin_table, void* k_cache, void* v_cache, int B, int S,
+                             int Hq, int Hkv, int D, int L, void* q_out, cudaStream_t stream);
+
+/*
+ * The 8-bit cache.  k_cache and v_cache are [B, Hkv, L, D] e4m3 codes (one
+ * byte each); every block of `block` consecutive rows of a KV head has one
+ * fp32 scale per operand, k_scale and v_scale [B, Hkv, NB] with
+ * NB = ceil(L / block), and row j stands for scale[j / block] * code.  A row
+ * costs half of what it does in the bf16 cache.
+ *   block : 16, 32, 64 or 128.   D == 128.
+ * The append writes scales 2^e with e in [-60, 60]; the decode takes any
+ * positive scale in [2^-60, 2^60].
+ * k_bounds [B, Hkv, NB, 2, D] bf16 (optional, for block selection): per block
+ * and channel the largest (index 0) and the smallest (1) key value appended,
+ * before rounding to 8 bits.
+ *
+ * attn_kv8_append -- S new rows per sequence, k_new and v_new [B, S, Hkv, D]
+ * bf16, to rows positions[b] .. positions[b] + S - 1.  For every block of a
+ * KV head that gets new rows, and for K and V apart:
+ *     s_new = 2^e, e the least integer with max |x| <= 448 * 2^e over the
+ *             block's new rows x (finite values only)
+ *     s     = s_new if the block held no row before (positions[b] <= its
+ *             first row), else max(s_old, s_new)
+ *     its earlier rows, if s > s_old: code <- e4m3(code * s_old / s)
+ *     its new rows:                   code <- e4m3(x / s)
+ * rounded to nearest even, beyond +-448 saturating, NaN kept.  Only codes of
+ * rows up to the last new one are written.  The bounds of a block become those
+ * of its new rows and, if it held rows before, what they were (NaN ignored).
+ *   k_bounds : or null.
+ *   S        : >= 0 (0 does nothing).
+ * A sequence whose rows are not all in [0, L) is skipped (the decode call
+ * reports it).  Supported: B <= 8192, Hkv <= 1024, L <= 2^24.
+ */
+int attn_kv8_append(const void* k_new, const void* v_new, const int32_t* positions,
+                    void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* k_bounds,
+                    int B, int S, int Hkv, int L, int D, int block, cudaStream_t stream);
+
+/*
+ * attn_kv8_workspace_size -- bytes of device workspace the 8-bit decode calls
+ * need; 0 if the sizes are invalid or unsupported.  The rules of
+ * attn_decode_workspace_size hold: zero-filled before first use and before use
+ * with other sizes, no overlapping calls on one workspace (two captured graphs
+ * that may run at once need one each).  Its first word is the device status
+ * word of attn_read_device_status.
+ */
+size_t attn_kv8_workspace_size(int B, int Hq, int Hkv, int L, int D);
+
+/*
+ * attn_decode_step_kv8 -- attn_decode_step over the 8-bit cache: for every
+ * sequence b and query head h, over rows j = 0..positions[b],
+ *     out[b,h,:] = softmax_j(scale * q[b,h,:] . ks_j k_j) (vs_j v_j)
+ * with the codes k_j, v_j and scales ks_j, vs_j of row j and KV head h / g.
+ * Codes enter both products exactly (as fp16), q exactly to 2^-22 of its
+ * head's largest element, the probabilities rounded once to fp16; sums in
+ * fp32.  Codes and scales of rows above positions[b] are not used and may hold
+ * anything.
+ *
+ *   Supported: D == 128; any g = Hq / Hkv from 1 to 16; B <= 8192;
+ *   B * Hkv < 2^31 / 16; L <= 2^24.
+ * A position outside [0, L) gives NaN output rows and ATTN_DEV_BAD_POSITION.
+ * Errors: as attn_decode_step; ATTN_ERR_UNSUPPORTED also for another block.
+ */
+int attn_decode_step_kv8(const void* q, const int32_t* positions, const void* k_cache,
+                         const void* v_cache, const float* k_scale, const float* v_scale, int B,
+                         int Hq, int Hkv, int L, int D, int block, float scale, void* out,
+                         void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * attn_block_scores -- an upper bound of what a query can score in each block,
+ * summed over the g query heads of a KV head:
+ *     scores[b,hk,j] = sum_h sum_d max(q[b,h,d] * max_jd, q[b,h,d] * min_jd)
+ * over the heads h of KV head hk, from k_bounds; -inf for blocks past
+ * positions[b] / block (and for all blocks of a position outside [0, L)).
+ * Their bounds are not read.  fp32 sums.
+ *
+ *   scores : [B, Hkv, NB] fp32.
+ *   Sizes as attn_decode_step_kv8.  The bounds are taken as finite.
+ */
+int attn_block_scores(const void* q, const int32_t* positions, const void* k_bounds, int B,
+                      int Hq, int Hkv, int L, int D, int block, float* scores,
+                      cudaStream_t stream);
+
+/*
+ * attn_block_select -- per sequence and KV head, `count` of the blocks
+ * 0 .. positions[b] / block: all of them if there are no more, else the first
+ * `first`, the last `recent`, and of the others those with the largest scores,
+ * ties to the lowest index (NaN counts as -inf).  block_index [B, Hkv, count]
+ * int32, ascending, -1 behind the last (all -1 for a position outside [0, L)).
+ *
+ *   Errors: ATTN_ERR_INVALID_ARG also for count < 1, first or recent < 0, or
+ *   first + recent > count.
+ */
+int attn_block_select(const float* scores, const int32_t* positions, int B, int Hkv, int L,
+                      int block, int count, int first, int recent, int32_t* block_index,
+                      cudaStream_t stream);
+
+/*
+ * attn_decode_step_kv8_blocks -- attn_decode_step_kv8 over the rows of listed
+ * blocks only, up to each position: block_index [B, Hkv, count] int32, any
+ * order, -1 for none.  A block listed twice counts twice; one past the
+ * position adds nothing; a list without any row gives zeros.  An index below
+ * -1 or not below NB is skipped and sets ATTN_DEV_BAD_BLOCK.
+ *   count : >= 1, count * block < 2^30.  The rest as attn_decode_step_kv8.
+ */
+int attn_decode_step_kv8_blocks(const void* q, const int32_t* positions, const void* k_cache,
+                                const void* v_cache, const float* k_scale, const float* v_scale,
+                                const int32_t* block_index, int count, int B, int Hq, int Hkv,
+                                int L, int D, int block, float scale, void* out, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * attn_decode_step_kv8_sparse -- attn_block_scores, attn_block_select and
+ * attn_decode_step_kv8_blocks in turn on `stream`: one decode step that attends
+ * `count` blocks per KV head.  The block of the position itself is attended if
+ * recent >= 1.  Scores and indices lie in the workspace, which needs
+ * attn_kv8_sparse_workspace_size(...) bytes (0: invalid or unsupported).
+ */
+size_t attn_kv8_sparse_workspace_size(int B, int Hq, int Hkv, int L, int D, int block, int count);
+int attn_decode_step_kv8_sparse(const void* q, const int32_t* positions, const void* k_cache,
+                                const void* v_cache, const float* k_scale, const float* v_scale,
+                                const void* k_bounds, int count, int first, int recent, int B,
+                                int Hq, int Hkv, int L, int D, int block, float scale, void* out,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * attn_prefill_causal -- causal prefill over a cached prefix (prefill page,

@@ -1,0 +1,93 @@
+"""attn_block_scores and attn_block_select against oracle/kv8.py."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import gqa_decode_attention_place_gb300 as ga
+from oracle import kv8
+from _kv8 import D, F32_HALF, f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("block", [16, 32, 64, 128])
+@pytest.mark.parametrize("B,Hkv,g,L,positions", [
+    (1, 1, 1, 1, [0]),
+    (1, 8, 2, 9000, [8999]),
+    (4, 3, 5, 1000, [0, 15, 16, 999]),
+    (2, 2, 16, 5001, [5000, 2047]),
+    (3, 2, 8, 300, [-1, 300, 128]),
+])
+def test_scores(B, Hkv, g, L, positions, block):
+    gen = torch.Generator(device="cuda").manual_seed(60)
+    nb = -(-L // block)
+    q = torch.randn((B, Hkv * g, D), generator=gen, device="cuda").bfloat16()
+    mid = torch.randn((B, Hkv, nb, D), generator=gen, device="cuda")
+    rad = torch.randn((B, Hkv, nb, D), generator=gen, device="cuda").abs()
+    bounds = torch.stack([mid + rad, mid - rad], dim=3).bfloat16()
+    for b, p in enumerate(positions):  # bounds past the position are not read
+        bounds[b, :, (p // block + 1 if 0 <= p < L else 0):] = float("nan")
+    pos = torch.tensor(positions, dtype=torch.int32, device="cuda")
+    got = f64(ga.attn_block_scores(q, pos, bounds, L, block))
+    for b, p in enumerate(positions):
+        if not 0 <= p < L:
+            assert np.isneginf(got[b]).all()
+            continue
+        want, mag = kv8.block_scores(f64(q[b]), f64(bounds[b]), p, block, g)
+        n = p // block + 1
+        assert np.isneginf(got[b, :, n:]).all()
+        # g sums and 256 fused products and sums, half a step each, of the terms' size
+        tol = (256 + g) * F32_HALF * mag[:, :n] + 1e-30
+        assert (np.abs(got[b, :, :n] - want[:, :n]) <= tol).all()
+
+
+def _select(scores, positions, L, block, count, first, recent):
+    pos = torch.tensor(positions, dtype=torch.int32, device="cuda")
+    got = ga.attn_block_select(scores, pos, L, block, count, first, recent).cpu().numpy()
+    s = scores.cpu().numpy()
+    for b, p in enumerate(positions):
+        for h in range(s.shape[1]):
+            want = kv8.block_select(s[b, h], p, L, block, count, first, recent)
+            assert np.array_equal(got[b, h], want), (b, h, got[b, h], want)
+
+
+@pytest.mark.parametrize("L,block,count,first,recent", [
+    (1, 16, 1, 0, 0), (100, 16, 3, 1, 1), (100, 16, 7, 1, 1), (100, 16, 20, 2, 3),
+    (16384, 16, 64, 1, 2), (16400, 16, 1, 0, 0), (16400, 16, 1, 1, 0), (16400, 16, 1, 0, 1),
+    (40000, 16, 64, 0, 64), (40000, 16, 65, 64, 1), (70000, 16, 512, 4, 16),
+    (140000, 16, 100, 1, 2), (262144, 16, 16000, 1, 1), (300000, 16, 37, 1, 1),
+])
+def test_select(L, block, count, first, recent):
+    """From one block to more than the kernel holds in registers."""
+    nb = -(-L // block)
+    gen = torch.Generator(device="cuda").manual_seed(61)
+    scores = torch.randn((3, 2, nb), generator=gen, device="cuda")
+    _select(scores, [L - 1, L // 2, L // 3], L, block, count, first, recent)
+
+
+def test_select_ties_signs_and_non_finite():
+    nb = 3000
+    gen = torch.Generator(device="cuda").manual_seed(62)
+    s = torch.randint(-2, 3, (6, 2, nb), generator=gen, device="cuda").float() * 0.5
+    s[1] = 0.0
+    s[1, 0, ::2] = -0.0
+    s[2, :, 100:2000] = math.inf
+    s[3, :, 5:] = -math.inf
+    s[4, :, ::3] = math.nan
+    s[5] = torch.finfo(torch.float32).min
+    for count, first, recent in ((1, 0, 0), (50, 1, 1), (1500, 0, 3), (2999, 1, 0)):
+        _select(s, [nb * 16 - 1] * 6, nb * 16, 16, count, first, recent)
+
+
+def test_select_bad_positions():
+    s = torch.zeros((4, 2, 10), device="cuda")
+    _select(s, [-1, 160, 2 ** 31 - 1, 5], 160, 16, 3, 1, 1)
+
+
+def test_scores_past_the_position_are_ignored():
+    s = torch.zeros((1, 1, 400), device="cuda")
+    s[..., 200:] = math.inf
+    _select(s, [200 * 16 - 1], 6400, 16, 10, 1, 1)
