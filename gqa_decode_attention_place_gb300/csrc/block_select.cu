@@ -50,24 +50,39 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(
         w[2 * i + 1] += lane < 16 ? fmaxf(hi, 0.f) : fminf(hi, 0.f);
       }
     }
+  // the bounds of the warp's 8 blocks, all in flight together
+  uint4 u[kScoreBlocksPerWarp];
+#pragma unroll
+  for (int i = 0; i < kScoreBlocksPerWarp; ++i)
+    u[i] = j0 + i < n ? bounds[((size_t)seg * nb + j0 + i) * 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
+  float s[kScoreBlocksPerWarp];
+#pragma unroll
   for (int i = 0; i < kScoreBlocksPerWarp; ++i) {
-    const int j = j0 + i;
-    if (j >= nb) return;
-    float s = 0.f;
-    if (j < n) {
-      const uint4 u = bounds[((size_t)seg * nb + j) * 32 + lane];
-      const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+    s[i] = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        s = fmaf(bf16lo(x[k]), w[2 * k], fmaf(bf16hi(x[k]), w[2 * k + 1], s));
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    }
-    if (lane == 0) scores[(size_t)seg * nb + j] = j < n ? s : -INFINITY;
+    for (int k = 0; k < 4; ++k)
+      s[i] = fmaf(bf16lo(x[k]), w[2 * k], fmaf(bf16hi(x[k]), w[2 * k + 1], s[i]));
   }
+  // 8 sums over 32 lanes: each of the first three exchanges halves the number
+  // of sums a lane still carries, so 9 shuffles do the work of 40
+#pragma unroll
+  for (int half = 4; half > 0; half >>= 1) {
+    const bool up = lane & (4 * half);
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give = up ? s[i] : s[i + half], keep = up ? s[i + half] : s[i];
+      s[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * half);
+    }
+  }
+  s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
+  s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+  const int j = j0 + (lane >> 2);  // lanes 4i .. 4i+3 hold block i's sum
+  if ((lane & 3) == 0 && j < nb) scores[(size_t)seg * nb + j] = j < n ? s[0] : -INFINITY;
 }
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
 
 // Order-preserving key of a score: larger score, larger key; -0 = +0; NaN is
 // taken as -inf.
@@ -79,16 +94,16 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 }
 
 // Sum of v over the block; every thread gets it.  `slots` holds two sets of
-// 32 counters so that one barrier per call suffices.
-__device__ __forceinline__ int block_sum(int v, int (*slots)[32], int phase) {
+// counters so that one barrier per call suffices.
+__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t (*slots)[32], int phase) {
   v = __reduce_add_sync(0xffffffffu, v);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) slots[phase][warp] = v;
   __syncthreads();
-  return __reduce_add_sync(0xffffffffu, slots[phase][lane]);
+  return __reduce_add_sync(0xffffffffu, lane < kSelectWarps ? slots[phase][lane] : 0u);
 }
 // Exclusive prefix sum of v over the block's threads.
-__device__ __forceinline__ int block_scan(int v, int (*slots)[32], int phase) {
+__device__ __forceinline__ int block_scan(int v, uint32_t (*slots)[32], int phase) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int x = v;
 #pragma unroll
@@ -98,8 +113,8 @@ __device__ __forceinline__ int block_scan(int v, int (*slots)[32], int phase) {
   }
   if (lane == 31) slots[phase][warp] = x;
   __syncthreads();
-  const int w = lane < warp ? slots[phase][lane] : 0;
-  return __reduce_add_sync(0xffffffffu, w) + x - v;
+  const uint32_t w = lane < warp ? slots[phase][lane] : 0u;
+  return (int)__reduce_add_sync(0xffffffffu, w) + x - v;
 }
 
 // I items per thread, thread t holding items t*I .. t*I + I-1 (I = 0: any
@@ -108,7 +123,7 @@ template <int I>
 __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
     const float* __restrict__ scores, const int32_t* __restrict__ positions, int32_t* out,
     int Hkv, int L, int block, int nb, int count, int first, int recent) {
-  __shared__ int slots[2][32];
+  __shared__ uint32_t slots[2][32];
   grid_dependency_wait();
   grid_dependents_launch();
   const int seg = blockIdx.x, b = seg / Hkv, tid = threadIdx.x;
@@ -137,15 +152,18 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
     return j >= first && j < n - recent ? score_key(s[j]) : 0u;
   };
   int phase = 0;
-  uint32_t th = 0;  // the need-th largest key: the largest th with count(key >= th) >= need
+  // the need-th largest key: the largest th with count(key >= th) >= need
+  uint32_t th = 0;
   if (need > 0) {
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t cand = th | (1u << bit);
       int c = 0;
 #pragma unroll
       for (int i = 0; i < items; ++i) c += get(i) >= cand;
-      if (block_sum(c, slots, phase) >= need) th = cand;
+      const int all = (int)block_sum(c, slots, phase);
       phase ^= 1;
+      if (all >= need) th = cand;
+      if (all == need) break;  // exactly the keys >= th: the lower bits do not matter
     }
   }
   int above = 0, ties = 0;
@@ -155,7 +173,7 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
     above += need > 0 && k > th;
     ties += need > 0 && k == th;
   }
-  const int all_above = block_sum(above, slots, phase);
+  const int all_above = (int)block_sum(above, slots, phase);
   phase ^= 1;
   const int ties_before = block_scan(ties, slots, phase);
   phase ^= 1;
@@ -202,6 +220,7 @@ cudaError_t launch_block_select(const float* scores, const int32_t* positions, i
                 : per <= 4  ? block_select_kernel<4>
                 : per <= 8  ? block_select_kernel<8>
                 : per <= 16 ? block_select_kernel<16>
+                : per <= 32 ? block_select_kernel<32>
                             : block_select_kernel<0>;
   return launch_pdl(kernel, dim3(B * Hkv), dim3(kSelectThreads), 0, stream, scores, positions,
                     out, Hkv, L, block, nb, count, first, recent);

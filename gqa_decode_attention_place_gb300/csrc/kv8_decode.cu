@@ -16,7 +16,7 @@
 //  * 128-row tiles (32 KB for K and V) stream through a shared-memory ring by
 //    tiled TMA copies (128-byte swizzle: a row of codes is exactly one
 //    swizzle span) issued by a producer warp that also fetches each 16-row
-//    slice's scales one tile ahead and leaves them beside the tile.
+//    slice's scales, four tiles at a time, and leaves them beside the tile.
 //  * 8 consumer warps take 16 rows each.  e4m3 -> fp16 is exact and one
 //    conversion instruction per two values; both products run on warp-level
 //    MMAs (m16n8k16, fp16 in, fp32 out) with rows or dims as M and the heads
@@ -396,13 +396,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ producer --
-    // lanes 0-7: slice `lane` and its K scale; lanes 8-15: the V scales
-    const int slice = lane & 7, op = (lane >> 3) & 1;
-    const float* scales = op ? p.v_scale : p.k_scale;
+    // Tiles go out in batches of four: lane 8*ti + slice looks after slice
+    // `slice` of the batch's tile ti.  The scales of a batch (and the list
+    // entries of the one after) are loaded while the batch before it is
+    // issued, so their latency is spread over four tiles' time.
+    const int ti = lane >> 3, slice = lane & 7;
     const int entry_rows = 1 << p.lb;
     const int in_block = (slice * 16) & (entry_rows - 1);
     const int entry = (slice * 16) >> p.lb;            // of this slice, within a tile
     const int per_tile = kTile >> p.lb;
+    const long long n_t = t1 - t0;
     // the block a listed tile's slice lies in (-1: none)
     auto fetch = [&](const Walk8& w) -> int {
       const int e = w.k * per_tile + entry;
@@ -411,97 +414,92 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto row_of = [&](const Walk8& w, int blk) -> int {
       int row;
       if (LIST) {
-        row = blk >= 0 && blk < p.nb ? (blk << p.lb) + in_block : kNoRow;
-        if ((blk < -1 || blk >= p.nb) && op == 0) set_status(p.status, ATTN_DEV_BAD_BLOCK);
+        if (blk < -1 || blk >= p.nb) {
+          set_status(p.status, ATTN_DEV_BAD_BLOCK);
+          blk = -1;
+        }
+        row = blk >= 0 ? (blk << p.lb) + in_block : kNoRow;
       } else {
         row = w.k * kTile + slice * 16;
       }
       return row <= w.pos ? row : kNoRow;
     };
-    auto scale_of = [&](const Walk8& w, int row) -> float {
-      return row != kNoRow ? scales[((size_t)w.b * Hkv + w.kvh) * p.nb + (row >> p.lb)] : 1.f;
+    struct Mine {  // this lane's slice of a batch
+      int row, z, k;
+      float ks, vs;
     };
-    auto next = [&](Walk8& w) {
-      if (++w.k == w.nt) walk8_segment(w, prefix, p.positions, B, Hkv);
+    auto look_up = [&](const Walk8& w, int blk, bool on) -> Mine {
+      Mine m;
+      m.z = w.b * Hkv + w.kvh;
+      m.k = w.k;
+      m.row = on ? row_of(w, blk) : kNoRow;
+      m.ks = m.vs = 1.f;
+      if (m.row != kNoRow) {
+        const size_t at = (size_t)m.z * p.nb + (m.row >> p.lb);
+        m.ks = p.k_scale[at];
+        m.vs = p.v_scale[at];
+      }
+      return m;
     };
-    // two walks: `w` is the tile to issue, `a` the one after it, whose list
-    // entries and scales are on their way
-    Walk8 w, a;
-    walk8_init(w, t0, prefix, p.positions, B, Hkv);
-    a = w;
-    int row = row_of(w, LIST ? fetch(w) : 0);
-    float sc = scale_of(w, row);
-    int blk_next = 0;
-    if (t0 + 1 < t1) {
-      next(a);
-      if (LIST) blk_next = fetch(a);
-    }
-    for (long long i = 0; t0 + i < t1; ++i) {
-      const int s = (int)(i % NS);
-      const uint32_t u = (uint32_t)(i / NS);
-      int row_next = kNoRow;
-      float sc_next = 1.f;
-      Walk8 a2 = a;
-      int blk_next2 = 0;
-      if (t0 + i + 1 < t1) {
-        row_next = row_of(a, blk_next);
-        sc_next = scale_of(a, row_next);
-        if (t0 + i + 2 < t1) {
-          next(a2);
-          if (LIST) blk_next2 = fetch(a2);
-        }
-      }
-      if (i >= NS && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[NS + s]), (u & 1u) ^ 1u,
-                                                        abort_flag))) {
-        if (lane == 0) {
-          *abort_flag = 1;
-          set_status(p.status, ATTN_DEV_TIMEOUT);
-        }
-        break;
-      }
-      const float v = __shfl_down_sync(0xffffffffu, sc, 8);  // the slice's V scale
-      if (lane < kSlices) {
-        SliceMeta mt;
-        mt.row0 = row;
-        mt.ks = sc;
-        // log2 of a power of two comes out exact
-        const uint32_t bits = __float_as_uint(v);
-        mt.lv = (float)((int)(bits >> 23) - 127) +
-                log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
-        mt.inv_vs = 1.f / v;
-        meta[s * kSlices + lane] = mt;
-      }
-      const uint32_t full = smem_u32(&bars[s]);
-      const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes), sV = sK + kOpBytes;
-      const int z = w.b * Hkv + w.kvh;
-      const bool skip = p.test_skip >= 0 && z == 0 && w.k == p.test_skip;  // failure-path tests
-      if (LIST) {
-        const bool issue = lane < kSlices && in_block == 0 && row != kNoRow &&
-                           range_ok(row >= 0 && row < L && z < B * Hkv, p.status);
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
-        __syncwarp();
-        if (!skip) {
-          if (lane == 0) mbar_arrive_expect_tx(full, boxes * (uint32_t)entry_rows * 2u * kD);
-          __syncwarp();
-          if (issue) {
-            tma_load_3d(sK + slice * 16 * kD, &tm_k, 0, row, z, full);
-            tma_load_3d(sV + slice * 16 * kD, &tm_v, 0, row, z, full);
+    auto step4 = [&](Walk8& w, long long i) {  // from tile i to tile i + 4, as far as there are
+      for (int k = 0; k < 4 && i + k + 1 < n_t; ++k)
+        if (++w.k == w.nt) walk8_segment(w, prefix, p.positions, B, Hkv);
+    };
+    Walk8 w;
+    walk8_init(w, t0 + min((long long)ti, n_t - 1), prefix, p.positions, B, Hkv);
+    long long i = ti;  // this lane's tile of the batch that `w` stands at
+    Mine cur = look_up(w, LIST ? fetch(w) : 0, i < n_t);
+    step4(w, i);
+    i += 4;
+    int blk = LIST && i < n_t ? fetch(w) : -1;
+    bool ok = true;
+    for (long long base = 0; ok && base < n_t; base += 4) {
+      const Mine nxt = look_up(w, blk, i < n_t);  // w stands at batch base + 4
+      step4(w, i);
+      i += 4;
+      blk = LIST && i < n_t ? fetch(w) : -1;
+      SliceMeta mt;
+      mt.row0 = cur.row;
+      mt.ks = cur.ks;
+      // log2 of a power of two comes out exact
+      const uint32_t bits = __float_as_uint(cur.vs);
+      mt.lv = (float)((int)(bits >> 23) - 127) +
+              log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
+      mt.inv_vs = 1.f / cur.vs;
+#pragma unroll 1
+      for (int q = 0; q < 4 && base + q < n_t; ++q) {
+        const int s = (int)((base + q) % NS);
+        const uint32_t u = (uint32_t)((base + q) / NS);
+        if (base + q >= NS &&
+            !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[NS + s]), (u & 1u) ^ 1u,
+                                               abort_flag))) {
+          if (lane == 0) {
+            *abort_flag = 1;
+            set_status(p.status, ATTN_DEV_TIMEOUT);
           }
+          ok = false;
+          break;
         }
-      } else {
+        if (ti == q) meta[s * kSlices + slice] = mt;
         __syncwarp();
-        if (lane == 0 && !skip && range_ok(row >= 0 && row < L && z < B * Hkv, p.status)) {
-          mbar_arrive_expect_tx(full, kStageBytes);
-          tma_load_3d(sK, &tm_k, 0, row, z, full);
-          tma_load_3d(sV, &tm_v, 0, row, z, full);
+        const uint32_t full = smem_u32(&bars[s]);
+        const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes), sV = sK + kOpBytes;
+        // failure-path tests only: a tile never issued
+        const bool skip = p.test_skip >= 0 && cur.z == 0 && cur.k == p.test_skip;
+        const bool issue = ti == q && !skip && cur.row != kNoRow &&
+                           (LIST ? in_block == 0 : slice == 0) &&
+                           range_ok(cur.row >= 0 && cur.row < L && cur.z < B * Hkv, p.status);
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
+        if (ti == q && slice == 0 && !skip)
+          mbar_arrive_expect_tx(full, boxes * (LIST ? (uint32_t)entry_rows * 2u * kD
+                                                    : (uint32_t)kStageBytes));  // 0: nothing to come
+        __syncwarp();
+        if (issue) {
+          tma_load_3d(sK + slice * 16 * kD, &tm_k, 0, cur.row, cur.z, full);
+          tma_load_3d(sV + slice * 16 * kD, &tm_v, 0, cur.row, cur.z, full);
         }
       }
-      w = a;
-      a = a2;
-      row = row_next;
-      sc = sc_next;
-      blk_next = blk_next2;
-      __syncwarp();
+      cur = nxt;
     }
   } else {
     // ----------------------------------------------------------- consumers --

@@ -85,19 +85,27 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
     load8f(p.sin + row + half, sb);
   }
   const int heads = p.Hq + p.Hkv * (p.k_out ? 1 : 2);
+  // this lane's two pieces of a head (nothing past the last head)
+  auto load = [&](int head, uint4& ua, uint4& ub) {
+    ua = ub = make_uint4(0u, 0u, 0u, 0u);
+    if (!on || head >= heads) return;
+    const bool is_q = head < p.Hq, is_v = head >= p.Hq + p.Hkv;
+    const uint16_t* src = is_q   ? p.q + n * p.q_stride + (size_t)head * D
+                          : is_v ? p.v + n * p.v_stride + (size_t)(head - p.Hq - p.Hkv) * D
+                                 : p.k + n * p.k_stride + (size_t)(head - p.Hq) * D;
+    ua = *reinterpret_cast<const uint4*>(src + d0);
+    ub = *reinterpret_cast<const uint4*>(src + d0 + half);
+  };
+  const int head0 = part * steps * RPW + lane / LPR;
+  uint4 next_a, next_b;
+  load(head0, next_a, next_b);
   for (int st = 0; st < steps; ++st) {
-    const int head = (part * steps + st) * RPW + lane / LPR;
+    const int head = head0 + st * RPW;
+    uint4 ua = next_a, ub = next_b;
+    if (st + 1 < steps) load(head + RPW, next_a, next_b);  // in flight during this step's work
     const bool row_on = on && head < heads;
     const bool is_q = head < p.Hq, is_v = head >= p.Hq + p.Hkv;
     const int h = is_q ? head : is_v ? head - p.Hq - p.Hkv : head - p.Hq;
-    const uint16_t* src = is_q   ? p.q + n * p.q_stride
-                          : is_v ? p.v + n * p.v_stride
-                                 : p.k + n * p.k_stride;
-    uint4 ua = make_uint4(0u, 0u, 0u, 0u), ub = ua;
-    if (row_on) {
-      ua = *reinterpret_cast<const uint4*>(src + (size_t)h * D + d0);
-      ub = *reinterpret_cast<const uint4*>(src + (size_t)h * D + d0 + half);
-    }
     float xa[8], xb[8];
     unpack8(ua, xa);
     unpack8(ub, xb);
@@ -178,7 +186,14 @@ cudaError_t launch_qk_norm_rope(const void* q, const void* k, const void* v, lon
   while (lpr * 16 < D) lpr *= 2;
   const int rpw = 32 / lpr;
   const int all = (Hq + Hkv * (k_out ? 1 : 2) + rpw - 1) / rpw;  // steps of one warp for a token
-  const int steps = 1, wpt = (all + steps - 1) / steps;
+  // Few tokens: a warp for every step, for latency.  Many: a warp keeps its
+  // token's rotation row over several steps, as long as the device stays full
+  // of warps.
+  const long long full = 152ll * 24;
+  int steps = 1;
+  while (steps < all && (long long)p.N * ((all + 2 * steps - 1) / (2 * steps)) >= full) steps *= 2;
+  steps = min(steps, all);
+  const int wpt = (all + steps - 1) / steps;
   const long long blocks = ((long long)p.N * wpt + kNormWarps - 1) / kNormWarps;
   auto kernel = lpr == 1   ? qk_norm_rope_kernel<1>
                 : lpr == 2 ? qk_norm_rope_kernel<2>
