@@ -85,14 +85,14 @@ struct Kv8Params {
   float qscale;          // scale * log2(e)
 };
 
-template <int NT> struct Lay {
-  static constexpr int kHeads = 8 * NT;
-  static constexpr int kMergeFloats = kWarps * kHeads * (kD + 2);
-  static size_t bytes(int stages, int B) {
-    return (size_t)stages * kStageBytes + kMergeFloats * 4 + stages * kSlices * sizeof(SliceMeta) +
-           (2 * stages + 2) * 8 + kMiscInts * 4 + ((size_t)B + 1) * 4;
-  }
-};
+// Shared memory: the ring, per stage the q rows of a piece that starts there
+// and the slices' scales, the warps' partials, barriers, and per sequence the
+// tiles before it and its position.
+__host__ __device__ constexpr int merge_floats(int g) { return kWarps * g * (kD + 2); }
+inline size_t smem_bytes(int stages, int B, int g) {
+  return (size_t)stages * (kStageBytes + g * kD * 2 + kSlices * sizeof(SliceMeta) + 16) + 16 +
+         (size_t)merge_floats(g) * 4 + kMiscInts * 4 + ((size_t)2 * B + 1) * 4;
+}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -107,12 +107,22 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
+// Untiled bulk copy of `bytes` (a multiple of 16) from global memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // A place in the flat (sequence, KV head, tile) order.
 struct Walk8 {
   int b, kvh, k, nt, pos;
 };
 __device__ __forceinline__ void walk8_init(Walk8& w, long long t, const int* prefix,
-                                           const int32_t* positions, int B, int Hkv) {
+                                           const int* spos, int B, int Hkv) {
   int lo = 0, hi = B - 1;  // largest b with Hkv*prefix[b] <= t
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -123,18 +133,18 @@ __device__ __forceinline__ void walk8_init(Walk8& w, long long t, const int* pre
   const long long off = t - (long long)Hkv * prefix[lo];
   w.kvh = (int)(off / w.nt);
   w.k = (int)(off % w.nt);
-  w.pos = positions[lo];
+  w.pos = spos[lo];
 }
 // To the first tile of the next segment.
-__device__ __forceinline__ void walk8_segment(Walk8& w, const int* prefix,
-                                              const int32_t* positions, int B, int Hkv) {
+__device__ __forceinline__ void walk8_segment(Walk8& w, const int* prefix, const int* spos,
+                                              int B, int Hkv) {
   w.k = 0;
   if (++w.kvh < Hkv) return;
   w.kvh = 0;
   do { ++w.b; } while (w.b < B && prefix[w.b + 1] == prefix[w.b]);
   if (w.b < B) {
     w.nt = prefix[w.b + 1] - prefix[w.b];
-    w.pos = positions[w.b];
+    w.pos = spos[w.b];
   }
 }
 
@@ -152,16 +162,15 @@ struct Consumer8 {
   float m[NT][2], l[NT][2], qk[NT][2];
   int c, t;
 
-  __device__ __forceinline__ void load_q(const Kv8Params& p, int b, int kvh) {
-    const uint16_t* base = p.q + ((size_t)b * p.Hq + (size_t)kvh * p.g) * kD;
+  // the g query rows of the segment, in shared memory
+  __device__ __forceinline__ void load_q(const uint8_t* qs, int g, float qscale) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int h = 8 * n + c;
       uint4 u[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        u[i] = h < p.g ? *reinterpret_cast<const uint4*>(base + (size_t)h * kD + 32 * t + 8 * i)
-                       : make_uint4(0u, 0u, 0u, 0u);
+        u[i] = h < g ? lds128(qs + h * (kD * 2) + 64 * t + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
       float amax = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -174,7 +183,7 @@ struct Consumer8 {
       // head's largest element, and off by 2^-33 of it below
       const int ex = max((int)(__float_as_uint(amax) >> 23) - 127, -119);
       const float f = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
-      const float un = __uint_as_float((uint32_t)(127 - 7 + ex) << 23) * p.qscale;
+      const float un = __uint_as_float((uint32_t)(127 - 7 + ex) << 23) * qscale;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -282,9 +291,8 @@ struct Consumer8 {
       }
     }
   }
-  // This warp's (m, l, o) -> ml [warp][heads][2], mo [warp][heads][kD].
+  // This warp's (m, l, o) -> ml [warp][g][2], mo [warp][g][kD].
   __device__ __forceinline__ void stash(float* mo, float* ml, int warp, int g) {
-    constexpr int H = Lay<NT>::kHeads;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -294,14 +302,14 @@ struct Consumer8 {
         for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         const int h = 8 * n + 2 * t + e;
         if (h < g) {
-          float4* dst = reinterpret_cast<float4*>(mo + (warp * H + h) * kD + 16 * c);
+          float4* dst = reinterpret_cast<float4*>(mo + (warp * g + h) * kD + 16 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             dst[i] = make_float4(o[n][2 * i][e], o[n][2 * i][2 + e], o[n][2 * i + 1][e],
                                  o[n][2 * i + 1][2 + e]);
           if (c == 0) {
-            ml[(warp * H + h) * 2] = m[n][e];
-            ml[(warp * H + h) * 2 + 1] = sum;
+            ml[(warp * g + h) * 2] = m[n][e];
+            ml[(warp * g + h) * 2 + 1] = sum;
           }
         }
       }
@@ -313,23 +321,111 @@ __device__ __forceinline__ void store_bf16(uint16_t* out, size_t i, float x) {
   out[i] = *reinterpret_cast<const uint16_t*>(&h);
 }
 
+// A segment of which this CTA did a part: its tiles [f0, f1) in the flat list.
+struct Part8 {
+  long long f0, f1;
+  size_t out_at;
+  int seg;
+};
+
+// Merge the parts of a split segment, in CTA order, by the consumer warps.
+// All of the parts' (max, sum) come in one round trip, then the outputs, a
+// float4 per thread and part: heads x 32 columns, and where those leave
+// threads over (g < 8) the parts are dealt out among them as well.
+__device__ __forceinline__ void merge_parts(const Kv8Params& p, const Part8& pt, long long T,
+                                            int G, float* buf, ConsumerSync& csync, int warp,
+                                            int lane) {
+  const int g = p.g, tid = warp * 32 + lane;
+  const int c0 = cta_of(pt.f0, T, G), n = cta_of(pt.f1 - 1, T, G) - c0 + 1;
+  // CTA c0's part is its second unless the segment opens its range
+  const int slot0 = 2 * c0 + (T * c0 / G == pt.f0 ? 0 : 1);
+  auto slot = [&](int r) { return r == 0 ? slot0 : 2 * (c0 + r); };
+  float* wt = buf;              // [n][g] maxima, then weights
+  float* ls = buf + n * g;      // [n][g] sums
+  for (int i = tid; i < n * g; i += kConsumers) {
+    const int r = i / g, h = i - r * g;
+    const float2 ml =
+        __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((size_t)slot(r) * g + h) * 2));
+    wt[i] = ml.x;
+    ls[i] = ml.y;
+  }
+  csync(lane);
+  for (int h = warp; h < g; h += kWarps) {
+    float M = kMInit, sum = 0.f;
+    for (int r = lane; r < n; r += 32) M = fmaxf(M, wt[r * g + h]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    for (int r = lane; r < n; r += 32) {
+      const float e = ex2(wt[r * g + h] - M);
+      wt[r * g + h] = e;
+      sum = fmaf(ls[r * g + h], e, sum);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    __syncwarp();
+    if (lane == 0) ls[h] = sum == 0.f ? 0.f : 1.f / sum;  // row 0's own sum has been read
+  }
+  csync(lane);
+  const int cols = g * (kD / 4);
+  const int deal = max(1, kConsumers / cols);  // threads that share a column
+  float4* red = reinterpret_cast<float4*>(buf + ((2 * n * g + 3) & ~3));
+  for (int base = 0; base < cols; base += kConsumers) {
+    const int who = tid / cols, col = base + (deal > 1 ? tid - who * cols : tid);
+    const bool on = deal > 1 ? who < deal : col < cols;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) {
+      const int h = col / (kD / 4);
+#pragma unroll 4
+      for (int r = deal > 1 ? who : 0; r < n; r += deal) {
+        const float4 x =
+            __ldcg(reinterpret_cast<const float4*>(p.part_o + (size_t)slot(r) * g * kD) + col);
+        const float e = wt[r * g + h];
+        o.x = fmaf(x.x, e, o.x);
+        o.y = fmaf(x.y, e, o.y);
+        o.z = fmaf(x.z, e, o.z);
+        o.w = fmaf(x.w, e, o.w);
+      }
+    }
+    if (deal > 1) {
+      if (on) red[tid] = o;
+      csync(lane);
+      if (who == 0) {
+        for (int k = 1; k < deal; ++k) {
+          const float4 x = red[k * cols + tid];
+          o.x += x.x;
+          o.y += x.y;
+          o.z += x.z;
+          o.w += x.w;
+        }
+      }
+    }
+    if (on && (deal == 1 || who == 0)) {
+      const float inv = ls[col / (kD / 4)];
+      uint2 v = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      *reinterpret_cast<uint2*>(p.out + pt.out_at + (size_t)col * 4) = v;
+    }
+  }
+  csync(lane);  // buf may be written again
+}
+
 template <int NT, bool LIST>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Kv8Params p) {
-  constexpr int H = Lay<NT>::kHeads;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int NS = p.stages;
   uint8_t* stages = smem;
-  float* merge_o = reinterpret_cast<float*>(smem + (size_t)NS * kStageBytes);  // [warps][H][kD]
-  float* merge_ml = merge_o + kWarps * H * kD;                                 // [warps][H][2]
-  SliceMeta* meta = reinterpret_cast<SliceMeta*>(merge_ml + kWarps * H * 2);   // [NS][kSlices]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(meta + NS * kSlices);           // full, empty, sync
-  int* misc = reinterpret_cast<int*>(bars + 2 * NS + 2);  // [0] abort, [1] last, [8..16) scan
+  const int B = p.B, Hkv = p.Hkv, L = p.L, g = p.g;
+  uint8_t* qbuf = smem + (size_t)NS * kStageBytes;                             // [NS][g][kD] bf16
+  SliceMeta* meta = reinterpret_cast<SliceMeta*>(qbuf + NS * g * kD * 2);      // [NS][kSlices]
+  float* merge_o = reinterpret_cast<float*>(meta + NS * kSlices);              // [warps][g][kD]
+  float* merge_ml = merge_o + kWarps * g * kD;                                 // [warps][g][2]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(merge_ml + kWarps * g * 2);     // full, empty, sync
+  int* misc = reinterpret_cast<int*>(bars + 2 * NS + 2);  // [0] abort, [2..4) last, [8..16) scan
   int* prefix = misc + kMiscInts;                         // [B+1]
+  int* spos = prefix + B + 1;                             // [B]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int B = p.B, Hkv = p.Hkv, L = p.L, g = p.g;
   volatile int* abort_flag = misc;
 
   if (tid == 0) {
@@ -352,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int v = 0;
     if (tid < kConsumers && b < B) {
       const int pos = p.positions[b];
+      spos[b] = pos;
       if (rows_in_cache(pos, 0, L)) {
         v = LIST ? list_tiles : pos / kTile + 1;
       } else if (b % (int)gridDim.x == (int)blockIdx.x) {
@@ -425,13 +522,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       return row <= w.pos ? row : kNoRow;
     };
     struct Mine {  // this lane's slice of a batch
-      int row, z, k;
+      int row, z, k, b;
       float ks, vs;
     };
     auto look_up = [&](const Walk8& w, int blk, bool on) -> Mine {
       Mine m;
       m.z = w.b * Hkv + w.kvh;
       m.k = w.k;
+      m.b = w.b;
       m.row = on ? row_of(w, blk) : kNoRow;
       m.ks = m.vs = 1.f;
       if (m.row != kNoRow) {
@@ -443,10 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto step4 = [&](Walk8& w, long long i) {  // from tile i to tile i + 4, as far as there are
       for (int k = 0; k < 4 && i + k + 1 < n_t; ++k)
-        if (++w.k == w.nt) walk8_segment(w, prefix, p.positions, B, Hkv);
+        if (++w.k == w.nt) walk8_segment(w, prefix, spos, B, Hkv);
     };
     Walk8 w;
-    walk8_init(w, t0 + min((long long)ti, n_t - 1), prefix, p.positions, B, Hkv);
+    walk8_init(w, t0 + min((long long)ti, n_t - 1), prefix, spos, B, Hkv);
     long long i = ti;  // this lane's tile of the batch that `w` stands at
     Mine cur = look_up(w, LIST ? fetch(w) : 0, i < n_t);
     step4(w, i);
@@ -490,9 +588,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                            (LIST ? in_block == 0 : slice == 0) &&
                            range_ok(cur.row >= 0 && cur.row < L && cur.z < B * Hkv, p.status);
         const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
-        if (ti == q && slice == 0 && !skip)
-          mbar_arrive_expect_tx(full, boxes * (LIST ? (uint32_t)entry_rows * 2u * kD
-                                                    : (uint32_t)kStageBytes));  // 0: nothing to come
+        if (ti == q && slice == 0 && !skip) {
+          // a piece's first tile brings the segment's query rows along
+          const uint32_t q_bytes = base + q == 0 || cur.k == 0 ? (uint32_t)g * kD * 2u : 0u;
+          mbar_arrive_expect_tx(full, q_bytes + boxes * (LIST ? (uint32_t)entry_rows * 2u * kD
+                                                              : (uint32_t)kStageBytes));
+          if (q_bytes)
+            bulk_load(smem_u32(qbuf + s * g * kD * 2),
+                      p.q + ((size_t)cur.b * p.Hq + (size_t)(cur.z - cur.b * Hkv) * g) * kD,
+                      q_bytes, full);
+        }
         __syncwarp();
         if (issue) {
           tma_load_3d(sK + slice * 16 * kD, &tm_k, 0, cur.row, cur.z, full);
@@ -508,13 +613,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     cs.c = lane >> 2;
     cs.t = lane & 3;
     Walk8 w;
-    walk8_init(w, t0, prefix, p.positions, B, Hkv);
-    bool first_piece = true;
+    walk8_init(w, t0, prefix, spos, B, Hkv);
+    // A piece that is only part of its segment leaves its partial in global
+    // memory; who merges the segment is settled at the end, so that the
+    // round trips through L2 never hold up the tiles.  A CTA has at most two
+    // such pieces, its first and its last.
+    Part8 parts[2];
+    int n_parts = 0;
     int s = 0;
     uint32_t ph = 0;
     for (long long t = t0; t < t1;) {
       const int len = (int)min((long long)(w.nt - w.k), t1 - t);
-      cs.load_q(p, w.b, w.kvh);
       cs.reset();
       bool ok = true;
       for (int i = 0; i < len; ++i) {
@@ -522,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        if (i == 0) cs.load_q(qbuf + s * g * kD * 2, g, p.qscale);
         const SliceMeta mt = meta[s * kSlices + warp];
         const int rows = min(16, w.pos + 1 - mt.row0);
         const uint8_t* Ks = stages + (size_t)s * kStageBytes + warp * 16 * kD;
@@ -536,75 +646,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       cs.stash(merge_o, merge_ml, warp, g);
       csync(lane);
+      if (*abort_flag) break;
       // ---- this CTA's part: the 8 warps' partials, in warp order -----------
       const bool whole = w.k == 0 && len == w.nt;
-      const int seg = w.b * Hkv + w.kvh;
-      const int slot = 2 * blockIdx.x + (first_piece ? 0 : 1);
-      uint16_t* out = p.out + ((size_t)w.b * p.Hq + (size_t)w.kvh * g) * kD;
-      if (!*abort_flag) {
-        for (int i = tid; i < g * kD; i += kConsumers) {
-          const int h = i / kD, d = i % kD;
-          float M = kMInit;
+      const int slot = 2 * blockIdx.x + (t == t0 ? 0 : 1);
+      const size_t out_at = ((size_t)w.b * p.Hq + (size_t)w.kvh * g) * kD;
+      for (int i = tid; i < g * kD; i += kConsumers) {
+        const int h = i / kD, d = i % kD;
+        float M = kMInit;
 #pragma unroll
-          for (int ww = 0; ww < kWarps; ++ww) M = fmaxf(M, merge_ml[(ww * H + h) * 2]);
-          float ls = 0.f, os = 0.f;
+        for (int ww = 0; ww < kWarps; ++ww) M = fmaxf(M, merge_ml[(ww * g + h) * 2]);
+        float ls = 0.f, os = 0.f;
 #pragma unroll
-          for (int ww = 0; ww < kWarps; ++ww) {
-            const float e = ex2(merge_ml[(ww * H + h) * 2] - M);
-            ls = fmaf(merge_ml[(ww * H + h) * 2 + 1], e, ls);
-            os = fmaf(merge_o[(ww * H + h) * kD + d], e, os);
-          }
-          if (whole) {
-            store_bf16(out, i, ls == 0.f ? 0.f : os / ls);
-          } else {
-            p.part_o[((size_t)slot * g) * kD + i] = os;
-            if (d == 0) {
-              p.part_ml[((size_t)slot * g + h) * 2] = M;
-              p.part_ml[((size_t)slot * g + h) * 2 + 1] = ls;
-            }
-          }
+        for (int ww = 0; ww < kWarps; ++ww) {
+          const float e = ex2(merge_ml[(ww * g + h) * 2] - M);
+          ls = fmaf(merge_ml[(ww * g + h) * 2 + 1], e, ls);
+          os = fmaf(merge_o[(ww * g + h) * kD + d], e, os);
         }
-        if (!whole) {
-          // ---- the segment's last CTA to arrive merges its parts ------------
-          const long long f0 = t - w.k, f1 = f0 + w.nt;  // the segment in the flat list
-          const int c0 = cta_of(f0, T, G), c1 = cta_of(f1 - 1, T, G);
-          __threadfence();
-          csync(lane);
-          if (tid == 0) {
-            const uint32_t before = atomicAdd(&p.counters[seg], 1u);
-            misc[1] = before + 1 == (uint32_t)(c1 - c0 + 1);
-            if (misc[1]) p.counters[seg] = 0;
-            __threadfence();
-          }
-          csync(lane);
-          if (misc[1] && !*abort_flag) {
-            __threadfence();
-            // CTA c0's part is its second unless the segment opens its range
-            const int slot0 = 2 * c0 + (T * c0 / G == f0 ? 0 : 1);
-            for (int i = tid; i < g * kD; i += kConsumers) {
-              const int h = i / kD;
-              float M = kMInit;
-              for (int cc = c0; cc <= c1; ++cc) {
-                const int sl = cc == c0 ? slot0 : 2 * cc;
-                M = fmaxf(M, __ldcg(&p.part_ml[((size_t)sl * g + h) * 2]));
-              }
-              float ls = 0.f, os = 0.f;
-              for (int cc = c0; cc <= c1; ++cc) {
-                const int sl = cc == c0 ? slot0 : 2 * cc;
-                const float e = ex2(__ldcg(&p.part_ml[((size_t)sl * g + h) * 2]) - M);
-                ls = fmaf(__ldcg(&p.part_ml[((size_t)sl * g + h) * 2 + 1]), e, ls);
-                os = fmaf(__ldcg(&p.part_o[((size_t)sl * g) * kD + i]), e, os);
-              }
-              store_bf16(out, i, ls == 0.f ? 0.f : os / ls);
-            }
-          }
+        if (whole) {
+          store_bf16(p.out, out_at + i, ls == 0.f ? 0.f : os / ls);
+        } else {
+          p.part_o[((size_t)slot * g) * kD + i] = os;
+          if (d == 0)
+            *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * g + h) * 2) =
+                make_float2(M, ls);
         }
       }
+      if (!whole) {
+        Part8& pt = parts[n_parts++];
+        pt.f0 = t - w.k;
+        pt.f1 = pt.f0 + w.nt;
+        pt.seg = w.b * Hkv + w.kvh;
+        pt.out_at = out_at;
+      }
       csync(lane);  // the merge buffers may be written again
-      if (*abort_flag) break;
       t += len;
-      first_piece = false;
-      if (t < t1) walk8_segment(w, prefix, p.positions, B, Hkv);
+      if (t < t1) walk8_segment(w, prefix, spos, B, Hkv);
+    }
+    if (n_parts > 0 && !*abort_flag) {
+      // ---- each split segment: its last CTA to arrive merges the parts ------
+      __threadfence();
+      csync(lane);
+      if (tid == 0) {
+        for (int i = 0; i < n_parts; ++i) {
+          const uint32_t n =
+              (uint32_t)(cta_of(parts[i].f1 - 1, T, G) - cta_of(parts[i].f0, T, G) + 1);
+          const bool last = atomicAdd(&p.counters[parts[i].seg], 1u) + 1 == n;
+          if (last) p.counters[parts[i].seg] = 0;
+          misc[2 + i] = last;
+        }
+        __threadfence();
+      }
+      csync(lane);
+      for (int i = 0; i < n_parts && !*abort_flag; ++i)
+        if (misc[2 + i])  // every tile has been consumed: the ring is free
+          merge_parts(p, parts[i], T, G, reinterpret_cast<float*>(stages), csync, warp, lane);
     }
   }
   if (*abort_flag) {  // copies in flight land before the shared memory goes
@@ -648,8 +744,8 @@ template <int NT, bool LIST>
 cudaError_t launch8(Kv8Params& p, const CUtensorMap& mk, const CUtensorMap& mv,
                     cudaStream_t stream) {
   p.stages = kMaxStages;
-  while (p.stages > 2 && Lay<NT>::bytes(p.stages, p.B) > (size_t)kMaxSmem) --p.stages;
-  const size_t smem = Lay<NT>::bytes(p.stages, p.B);
+  while (p.stages > 2 && smem_bytes(p.stages, p.B, p.g) > (size_t)kMaxSmem) --p.stages;
+  const size_t smem = smem_bytes(p.stages, p.B, p.g);
   const cudaError_t e = cudaFuncSetAttribute(
       kv8_decode_kernel<NT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return e;
