@@ -43,12 +43,12 @@ namespace {
 
 constexpr int kD = kDecodeD;
 constexpr int kTile = 128;
-constexpr int kSlices = kTile / 16;         // one per consumer warp
+constexpr int kSlices = kTile / 16;         // 16-row slices, one per consumer warp
 constexpr int kOpBytes = kTile * kD;        // 16 KB per operand
 constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kWarps = kSlices;
+constexpr int kWarps = kSlices;             // consumer warps
 constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 32;
+constexpr int kThreads = kConsumers + 64;   // and the two producer warps
 constexpr int kMaxStages = 6;
 constexpr int kMiscInts = 32;
 constexpr int kNoRow = 0x40000000;          // row of a slice that holds nothing
@@ -418,10 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int B = p.B, Hkv = p.Hkv, L = p.L, g = p.g;
   uint8_t* qbuf = smem + (size_t)NS * kStageBytes;                             // [NS][g][kD] bf16
   SliceMeta* meta = reinterpret_cast<SliceMeta*>(qbuf + NS * g * kD * 2);      // [NS][kSlices]
-  float* merge_o = reinterpret_cast<float*>(meta + NS * kSlices);              // [warps][g][kD]
-  float* merge_ml = merge_o + kWarps * g * kD;                                 // [warps][g][2]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(merge_ml + kWarps * g * 2);     // full, empty, sync
-  int* misc = reinterpret_cast<int*>(bars + 2 * NS + 2);  // [0] abort, [2..4) last, [8..16) scan
+  float* merge_o = reinterpret_cast<float*>(meta + NS * kSlices);              // [kWarps][g][kD]
+  float* merge_ml = merge_o + kWarps * g * kD;                                     // [kWarps][g][2]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(merge_ml + kWarps * g * 2);         // full, empty, sync
+  int* misc = reinterpret_cast<int*>(bars + 2 * NS + 2);  // [0] abort, [2..4) last, [8..24) scan
   int* prefix = misc + kMiscInts;                         // [B+1]
   int* spos = prefix + B + 1;                             // [B]
 
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_u32(&bars[s]), 1);
+      mbar_init(smem_u32(&bars[s]), 2);  // the copies issued; the scales in place
       mbar_init(smem_u32(&bars[NS + s]), kWarps);
     }
     mbar_init(smem_u32(&bars[2 * NS]), kWarps);
@@ -491,28 +491,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   if ((int)blockIdx.x >= G) return;
   const long long t0 = T * blockIdx.x / G, t1 = T * (blockIdx.x + 1) / G;
 
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ producer --
-    // Tiles go out in batches of four: lane 8*ti + slice looks after slice
-    // `slice` of the batch's tile ti.  The scales of a batch (and the list
-    // entries of the one after) are loaded while the batch before it is
-    // issued, so their latency is spread over four tiles' time.
+  const long long n_t = t1 - t0;
+  if (warp >= kWarps) {
+    // ----------------------------------------------------------- producers --
+    // Warp kWarps issues the copies, warp kWarps + 1 brings the scales; a tile is full
+    // when both have arrived and the copies have landed.
+    // Where an address hangs on a load, tiles go in batches of four: lane
+    // 8*ti + slice looks after slice `slice` of the batch's tile ti, and what
+    // a batch needs is loaded while the one before it is issued, so that the
+    // latency is spread over four tiles' time.
+    const bool copies = warp == kWarps;
     const int ti = lane >> 3, slice = lane & 7;
     const int entry_rows = 1 << p.lb;
     const int in_block = (slice * 16) & (entry_rows - 1);
     const int entry = (slice * 16) >> p.lb;            // of this slice, within a tile
     const int per_tile = kTile >> p.lb;
-    const long long n_t = t1 - t0;
     // the block a listed tile's slice lies in (-1: none)
     auto fetch = [&](const Walk8& w) -> int {
       const int e = w.k * per_tile + entry;
-      return e < p.count ? p.index[((size_t)w.b * Hkv + w.kvh) * p.count + e] : -1;
+      return e < p.count ? p.index[(size_t)(w.b * Hkv + w.kvh) * p.count + e] : -1;
     };
     auto row_of = [&](const Walk8& w, int blk) -> int {
       int row;
       if (LIST) {
         if (blk < -1 || blk >= p.nb) {
-          set_status(p.status, ATTN_DEV_BAD_BLOCK);
+          if (copies) set_status(p.status, ATTN_DEV_BAD_BLOCK);
           blk = -1;
         }
         row = blk >= 0 ? (blk << p.lb) + in_block : kNoRow;
@@ -521,90 +524,142 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return row <= w.pos ? row : kNoRow;
     };
-    struct Mine {  // this lane's slice of a batch
-      int row, z, k, b;
-      float ks, vs;
-    };
-    auto look_up = [&](const Walk8& w, int blk, bool on) -> Mine {
-      Mine m;
-      m.z = w.b * Hkv + w.kvh;
-      m.k = w.k;
-      m.b = w.b;
-      m.row = on ? row_of(w, blk) : kNoRow;
-      m.ks = m.vs = 1.f;
-      if (m.row != kNoRow) {
-        const size_t at = (size_t)m.z * p.nb + (m.row >> p.lb);
-        m.ks = p.k_scale[at];
-        m.vs = p.v_scale[at];
-      }
-      return m;
+    auto next = [&](Walk8& w) {
+      if (++w.k == w.nt) walk8_segment(w, prefix, spos, B, Hkv);
     };
     auto step4 = [&](Walk8& w, long long i) {  // from tile i to tile i + 4, as far as there are
-      for (int k = 0; k < 4 && i + k + 1 < n_t; ++k)
-        if (++w.k == w.nt) walk8_segment(w, prefix, spos, B, Hkv);
+      for (int k = 0; k < 4 && i + k + 1 < n_t; ++k) next(w);
+    };
+    int s = 0;          // the ring's stage and pass of the tile at hand
+    uint32_t pass = 0;
+    auto wait_empty = [&]() -> bool {  // by the whole warp
+      if (pass == 0) return true;
+      if (__all_sync(0xffffffffu,
+                     mbar_wait(smem_u32(&bars[NS + s]), (pass & 1u) ^ 1u, abort_flag)))
+        return true;
+      if (lane == 0) {
+        *abort_flag = 1;
+        set_status(p.status, ATTN_DEV_TIMEOUT);
+      }
+      return false;
+    };
+    auto turn = [&]() {
+      if (++s == NS) {
+        s = 0;
+        ++pass;
+      }
+    };
+    // the tile's arrival, with its bytes; a piece's first tile brings the
+    // segment's query rows along
+    auto expect = [&](uint32_t full, uint32_t bytes, bool starts, int b, int kvh) {
+      const uint32_t q_bytes = starts ? (uint32_t)g * kD * 2u : 0u;
+      mbar_arrive_expect_tx(full, q_bytes + bytes);
+      if (q_bytes)
+        bulk_load(smem_u32(qbuf + s * g * kD * 2),
+                  p.q + ((size_t)b * p.Hq + (size_t)kvh * g) * kD, q_bytes, full);
     };
     Walk8 w;
-    walk8_init(w, t0 + min((long long)ti, n_t - 1), prefix, spos, B, Hkv);
-    long long i = ti;  // this lane's tile of the batch that `w` stands at
-    Mine cur = look_up(w, LIST ? fetch(w) : 0, i < n_t);
-    step4(w, i);
-    i += 4;
-    int blk = LIST && i < n_t ? fetch(w) : -1;
-    bool ok = true;
-    for (long long base = 0; ok && base < n_t; base += 4) {
-      const Mine nxt = look_up(w, blk, i < n_t);  // w stands at batch base + 4
-      step4(w, i);
-      i += 4;
-      blk = LIST && i < n_t ? fetch(w) : -1;
-      SliceMeta mt;
-      mt.row0 = cur.row;
-      mt.ks = cur.ks;
-      // log2 of a power of two comes out exact
-      const uint32_t bits = __float_as_uint(cur.vs);
-      mt.lv = (float)((int)(bits >> 23) - 127) +
-              log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
-      mt.inv_vs = 1.f / cur.vs;
-#pragma unroll 1
-      for (int q = 0; q < 4 && base + q < n_t; ++q) {
-        const int s = (int)((base + q) % NS);
-        const uint32_t u = (uint32_t)((base + q) / NS);
-        if (base + q >= NS &&
-            !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[NS + s]), (u & 1u) ^ 1u,
-                                               abort_flag))) {
-          if (lane == 0) {
-            *abort_flag = 1;
-            set_status(p.status, ATTN_DEV_TIMEOUT);
-          }
-          ok = false;
-          break;
-        }
-        if (ti == q) meta[s * kSlices + slice] = mt;
-        __syncwarp();
-        const uint32_t full = smem_u32(&bars[s]);
-        const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes), sV = sK + kOpBytes;
+    if (copies && !LIST) {
+      walk8_init(w, t0, prefix, spos, B, Hkv);
+      for (long long i = 0; i < n_t; ++i) {
+        if (!wait_empty()) break;
+        const int z = w.b * Hkv + w.kvh, row = w.k * kTile;
         // failure-path tests only: a tile never issued
-        const bool skip = p.test_skip >= 0 && cur.z == 0 && cur.k == p.test_skip;
-        const bool issue = ti == q && !skip && cur.row != kNoRow &&
-                           (LIST ? in_block == 0 : slice == 0) &&
-                           range_ok(cur.row >= 0 && cur.row < L && cur.z < B * Hkv, p.status);
-        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
-        if (ti == q && slice == 0 && !skip) {
-          // a piece's first tile brings the segment's query rows along
-          const uint32_t q_bytes = base + q == 0 || cur.k == 0 ? (uint32_t)g * kD * 2u : 0u;
-          mbar_arrive_expect_tx(full, q_bytes + boxes * (LIST ? (uint32_t)entry_rows * 2u * kD
-                                                              : (uint32_t)kStageBytes));
-          if (q_bytes)
-            bulk_load(smem_u32(qbuf + s * g * kD * 2),
-                      p.q + ((size_t)cur.b * p.Hq + (size_t)(cur.z - cur.b * Hkv) * g) * kD,
-                      q_bytes, full);
+        const bool skip = p.test_skip >= 0 && z == 0 && w.k == p.test_skip;
+        if (lane == 0 && !skip && range_ok(row < L && z < B * Hkv, p.status)) {
+          const uint32_t full = smem_u32(&bars[s]);
+          const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes);
+          expect(full, kStageBytes, i == 0 || w.k == 0, w.b, w.kvh);
+          tma_load_3d(sK, &tm_k, 0, row, z, full);
+          tma_load_3d(sK + kOpBytes, &tm_v, 0, row, z, full);
         }
         __syncwarp();
-        if (issue) {
-          tma_load_3d(sK + slice * 16 * kD, &tm_k, 0, cur.row, cur.z, full);
-          tma_load_3d(sV + slice * 16 * kD, &tm_v, 0, cur.row, cur.z, full);
+        next(w);
+        turn();
+      }
+    } else if (copies) {
+      walk8_init(w, t0 + min((long long)ti, n_t - 1), prefix, spos, B, Hkv);
+      long long i = ti;  // this lane's tile of the batch that `w` stands at
+      int blk = i < n_t ? fetch(w) : -1;
+      bool ok = true;
+      for (long long base = 0; ok && base < n_t; base += 4) {
+        const int row = row_of(w, blk), b = w.b, kvh = w.kvh, k = w.k;
+        const int z = b * Hkv + kvh;
+        step4(w, i);
+        i += 4;
+        blk = i < n_t ? fetch(w) : -1;
+        const bool skip = p.test_skip >= 0 && z == 0 && k == p.test_skip;
+        const bool have = !skip && row != kNoRow && in_block == 0 &&
+                          range_ok(row >= 0 && row < L && z < B * Hkv, p.status);
+        const uint32_t boxes = __ballot_sync(0xffffffffu, have);
+        const int n_q = (int)min(4ll, n_t - base);
+        for (int q = 0; q < n_q; ++q) {
+          if (!wait_empty()) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = smem_u32(&bars[s]);
+          if (lane == 8 * q && !skip)
+            expect(full, __popc((boxes >> (8 * q)) & 0xffu) * (uint32_t)entry_rows * 2u * kD,
+                   base + q == 0 || k == 0, b, kvh);
+          __syncwarp();
+          if (ti == q && have) {
+            const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes) + slice * 16 * kD;
+            tma_load_3d(sK, &tm_k, 0, row, z, full);
+            tma_load_3d(sK + kOpBytes, &tm_v, 0, row, z, full);
+          }
+          turn();
         }
       }
-      cur = nxt;
+    } else {
+      walk8_init(w, t0 + min((long long)ti, n_t - 1), prefix, spos, B, Hkv);
+      long long i = ti;
+      auto look_up = [&](int blk, bool on, int& row, float& ks, float& vs) {
+        row = on ? row_of(w, blk) : kNoRow;
+        ks = vs = 1.f;
+        if (row != kNoRow) {
+          const size_t at = (size_t)(w.b * Hkv + w.kvh) * p.nb + (row >> p.lb);
+          ks = p.k_scale[at];
+          vs = p.v_scale[at];
+        }
+      };
+      int row;
+      float ks, vs;
+      look_up(LIST && i < n_t ? fetch(w) : -1, i < n_t, row, ks, vs);
+      step4(w, i);
+      i += 4;
+      int blk = LIST && i < n_t ? fetch(w) : -1;
+      bool ok = true;
+      for (long long base = 0; ok && base < n_t; base += 4) {
+        int row_next;
+        float ks_next, vs_next;
+        look_up(blk, i < n_t, row_next, ks_next, vs_next);
+        step4(w, i);
+        i += 4;
+        blk = LIST && i < n_t ? fetch(w) : -1;
+        SliceMeta mt;
+        mt.row0 = row;
+        mt.ks = ks;
+        // log2 of a power of two comes out exact
+        const uint32_t bits = __float_as_uint(vs);
+        mt.lv = (float)((int)(bits >> 23) - 127) +
+                log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
+        mt.inv_vs = 1.f / vs;
+        const int n_q = (int)min(4ll, n_t - base);
+        for (int q = 0; q < n_q; ++q) {
+          if (!wait_empty()) {
+            ok = false;
+            break;
+          }
+          if (ti == q) meta[s * kSlices + slice] = mt;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars[s]));
+          turn();
+        }
+        row = row_next;
+        ks = ks_next;
+        vs = vs_next;
+      }
     }
   } else {
     // ----------------------------------------------------------- consumers --
@@ -647,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cs.stash(merge_o, merge_ml, warp, g);
       csync(lane);
       if (*abort_flag) break;
-      // ---- this CTA's part: the 8 warps' partials, in warp order -----------
+      // ---- this CTA's part: the warps' partials, in warp order -----------
       const bool whole = w.k == 0 && len == w.nt;
       const int slot = 2 * blockIdx.x + (t == t0 ? 0 : 1);
       const size_t out_at = ((size_t)w.b * p.Hq + (size_t)w.kvh * g) * kD;
@@ -804,8 +859,10 @@ cudaError_t launch_kv8_decode(const void* q, const int32_t* positions, const voi
       !codes_map(&mv, v_cache, L, (long long)B * Hkv, rows))
     return cudaErrorInvalidValue;
   if (block_index)
-    return p.g <= 8 ? launch8<1, true>(p, mk, mv, stream) : launch8<2, true>(p, mk, mv, stream);
-  return p.g <= 8 ? launch8<1, false>(p, mk, mv, stream) : launch8<2, false>(p, mk, mv, stream);
+    return p.g <= 8 ? launch8<1, true>(p, mk, mv, stream)
+                    : launch8<2, true>(p, mk, mv, stream);
+  return p.g <= 8 ? launch8<1, false>(p, mk, mv, stream)
+                  : launch8<2, false>(p, mk, mv, stream);
 }
 
 }  // namespace gqa
