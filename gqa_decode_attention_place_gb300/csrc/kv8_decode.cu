@@ -88,7 +88,14 @@ struct Kv8Params {
 // Shared memory: the ring, per stage the q rows of a piece that starts there
 // and the slices' scales, the warps' partials, barriers, and per sequence the
 // tiles before it and its position.
-__host__ __device__ constexpr int merge_floats(int g) { return kWarps * g * (kD + 2); }
+constexpr int kMergeRow = kD + 4;
+__host__ __device__ constexpr int merge_heads(int g) { return (g + 1) & ~1; }
+__host__ __device__ constexpr int merge_row(int warp, int h, int g) {
+  return ((warp * 2 + (h & 1)) * (merge_heads(g) >> 1) + (h >> 1)) * kMergeRow;
+}
+__host__ __device__ constexpr int merge_floats(int g) {
+  return kWarps * (merge_heads(g) * kMergeRow + 2 * g);
+}
 inline size_t smem_bytes(int stages, int B, int g) {
   return (size_t)stages * (kStageBytes + g * kD * 2 + kSlices * sizeof(SliceMeta) + 16) + 16 +
          (size_t)merge_floats(g) * 4 + kMiscInts * 4 + ((size_t)2 * B + 1) * 4;
@@ -117,35 +124,49 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// A place in the flat (sequence, KV head, tile) order.
+// A tile's place in the flat (sequence, KV head, tile) order.  The order is
+// counted in units: a segment of nt tiles takes nt + 1, its tiles and one for
+// what its end costs (about a tile's time), so that an even split of the
+// units is an even split of the work however short the segments are.
 struct Walk8 {
+  long long u;
   int b, kvh, k, nt, pos;
 };
-__device__ __forceinline__ void walk8_init(Walk8& w, long long t, const int* prefix,
-                                           const int* spos, int B, int Hkv) {
-  int lo = 0, hi = B - 1;  // largest b with Hkv*prefix[b] <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((long long)Hkv * prefix[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  w.b = lo;
-  w.nt = prefix[lo + 1] - prefix[lo];
-  const long long off = t - (long long)Hkv * prefix[lo];
-  w.kvh = (int)(off / w.nt);
-  w.k = (int)(off % w.nt);
-  w.pos = spos[lo];
-}
-// To the first tile of the next segment.
+// To the first tile of the next segment (b = B past the last).
 __device__ __forceinline__ void walk8_segment(Walk8& w, const int* prefix, const int* spos,
                                               int B, int Hkv) {
+  w.u += w.nt - w.k + 1;
   w.k = 0;
   if (++w.kvh < Hkv) return;
   w.kvh = 0;
   do { ++w.b; } while (w.b < B && prefix[w.b + 1] == prefix[w.b]);
   if (w.b < B) {
-    w.nt = prefix[w.b + 1] - prefix[w.b];
+    w.nt = prefix[w.b + 1] - prefix[w.b] - 1;
     w.pos = spos[w.b];
   }
+}
+// The first tile at or after unit u.
+__device__ __forceinline__ void walk8_init(Walk8& w, long long u, const int* prefix,
+                                           const int* spos, int B, int Hkv) {
+  int lo = 0, hi = B - 1;  // largest b with Hkv*prefix[b] <= u
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((long long)Hkv * prefix[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  const int n = prefix[lo + 1] - prefix[lo];
+  const uint32_t off = (uint32_t)(u - (long long)Hkv * prefix[lo]);
+  w.u = u;
+  w.b = lo;
+  w.nt = n - 1;
+  w.kvh = (int)(off / (uint32_t)n);
+  w.k = (int)(off % (uint32_t)n);
+  w.pos = spos[lo];
+  if (w.k == w.nt) walk8_segment(w, prefix, spos, B, Hkv);
+}
+__device__ __forceinline__ void walk8_next(Walk8& w, const int* prefix, const int* spos, int B,
+                                           int Hkv) {
+  ++w.u;
+  if (++w.k == w.nt) walk8_segment(w, prefix, spos, B, Hkv);
 }
 
 // One consumer warp: 16 rows of each tile for one KV head's g <= 8*NT heads.
@@ -291,7 +312,9 @@ struct Consumer8 {
       }
     }
   }
-  // This warp's (m, l, o) -> ml [warp][g][2], mo [warp][g][kD].
+  // This warp's (m, l, o) -> ml [warp][g][2], mo (merge_row): rows of even and
+  // of odd heads apart and 132 floats long, so that the 8 lanes of a store
+  // phase (two c, four t) fall on 32 different banks.
   __device__ __forceinline__ void stash(float* mo, float* ml, int warp, int g) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -302,26 +325,19 @@ struct Consumer8 {
         for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         const int h = 8 * n + 2 * t + e;
         if (h < g) {
-          float4* dst = reinterpret_cast<float4*>(mo + (warp * g + h) * kD + 16 * c);
+          float4* dst = reinterpret_cast<float4*>(mo + merge_row(warp, h, g) + 16 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             dst[i] = make_float4(o[n][2 * i][e], o[n][2 * i][2 + e], o[n][2 * i + 1][e],
                                  o[n][2 * i + 1][2 + e]);
-          if (c == 0) {
-            ml[(warp * g + h) * 2] = m[n][e];
-            ml[(warp * g + h) * 2 + 1] = sum;
-          }
+          if (c == 0)
+            *reinterpret_cast<float2*>(ml + (warp * g + h) * 2) = make_float2(m[n][e], sum);
         }
       }
   }
 };
 
-__device__ __forceinline__ void store_bf16(uint16_t* out, size_t i, float x) {
-  const __nv_bfloat16 h = __float2bfloat16_rn(x);
-  out[i] = *reinterpret_cast<const uint16_t*>(&h);
-}
-
-// A segment of which this CTA did a part: its tiles [f0, f1) in the flat list.
+// A segment of which this CTA did a part: its tiles' units [f0, f1) in the flat order.
 struct Part8 {
   long long f0, f1;
   size_t out_at;
@@ -337,8 +353,9 @@ __device__ __forceinline__ void merge_parts(const Kv8Params& p, const Part8& pt,
                                             int lane) {
   const int g = p.g, tid = warp * 32 + lane;
   const int c0 = cta_of(pt.f0, T, G), n = cta_of(pt.f1 - 1, T, G) - c0 + 1;
-  // CTA c0's part is its second unless the segment opens its range
-  const int slot0 = 2 * c0 + (T * c0 / G == pt.f0 ? 0 : 1);
+  // CTA c0's part is its second unless the segment opens its range, right
+  // away or after the end unit of the one before
+  const int slot0 = 2 * c0 + (T * c0 / G >= pt.f0 - 1 ? 0 : 1);
   auto slot = [&](int r) { return r == 0 ? slot0 : 2 * (c0 + r); };
   float* wt = buf;              // [n][g] maxima, then weights
   float* ls = buf + n * g;      // [n][g] sums
@@ -418,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int B = p.B, Hkv = p.Hkv, L = p.L, g = p.g;
   uint8_t* qbuf = smem + (size_t)NS * kStageBytes;                             // [NS][g][kD] bf16
   SliceMeta* meta = reinterpret_cast<SliceMeta*>(qbuf + NS * g * kD * 2);      // [NS][kSlices]
-  float* merge_o = reinterpret_cast<float*>(meta + NS * kSlices);              // [kWarps][g][kD]
-  float* merge_ml = merge_o + kWarps * g * kD;                                     // [kWarps][g][2]
+  float* merge_o = reinterpret_cast<float*>(meta + NS * kSlices);              // merge_row
+  float* merge_ml = merge_o + kWarps * merge_heads(g) * kMergeRow;             // [warps][g][2]
   uint64_t* bars = reinterpret_cast<uint64_t*>(merge_ml + kWarps * g * 2);         // full, empty, sync
   int* misc = reinterpret_cast<int*>(bars + 2 * NS + 2);  // [0] abort, [2..4) last, [8..24) scan
   int* prefix = misc + kMiscInts;                         // [B+1]
@@ -440,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   grid_dependents_launch();
 
-  // ---- tiles per sequence and their exclusive prefix sum (every CTA) ------
+  // ---- units per sequence and KV head, their exclusive prefix sum (every CTA)
   const int list_tiles = LIST ? (int)((((long long)p.count << p.lb) + kTile - 1) / kTile) : 0;
   int carry = 0;
   for (int base = 0; base < B; base += kConsumers) {
@@ -450,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = p.positions[b];
       spos[b] = pos;
       if (rows_in_cache(pos, 0, L)) {
-        v = LIST ? list_tiles : pos / kTile + 1;
+        v = (LIST ? list_tiles : pos / kTile + 1) + 1;
       } else if (b % (int)gridDim.x == (int)blockIdx.x) {
         // out-of-range position: flag it and make the sequence's output NaN
         set_status(p.status, ATTN_DEV_BAD_POSITION);
@@ -481,17 +498,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) prefix[B] = carry;
   __syncthreads();
 
-  const long long T = (long long)Hkv * carry;  // all tiles
-  // As many CTAs as there are tiles at most; one per segment where segments
+  const long long T = (long long)Hkv * carry;  // all units
+  // As many CTAs as there are units at most; one per segment where segments
   // are short (a split costs a round trip through L2).
   const long long nseg = (long long)B * Hkv;
   long long gw = min((long long)gridDim.x, T);
-  if (T <= (long long)kWholeTiles * nseg) gw = min(gw, nseg);
+  if (T <= (long long)(kWholeTiles + 1) * nseg) gw = min(gw, nseg);
   const int G = (int)gw;
   if ((int)blockIdx.x >= G) return;
   const long long t0 = T * blockIdx.x / G, t1 = T * (blockIdx.x + 1) / G;
 
-  const long long n_t = t1 - t0;
   if (warp >= kWarps) {
     // ----------------------------------------------------------- producers --
     // Warp kWarps issues the copies, warp kWarps + 1 brings the scales; a tile is full
@@ -524,11 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return row <= w.pos ? row : kNoRow;
     };
-    auto next = [&](Walk8& w) {
-      if (++w.k == w.nt) walk8_segment(w, prefix, spos, B, Hkv);
-    };
-    auto step4 = [&](Walk8& w, long long i) {  // from tile i to tile i + 4, as far as there are
-      for (int k = 0; k < 4 && i + k + 1 < n_t; ++k) next(w);
+    auto step = [&](Walk8& w, int n) {  // n tiles on, as far as the range goes
+      for (int k = 0; k < n && w.u < t1; ++k) walk8_next(w, prefix, spos, B, Hkv);
     };
     int s = 0;          // the ring's stage and pass of the tile at hand
     uint32_t pass = 0;
@@ -559,9 +572,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   p.q + ((size_t)b * p.Hq + (size_t)kvh * g) * kD, q_bytes, full);
     };
     Walk8 w;
+    walk8_init(w, t0, prefix, spos, B, Hkv);
+    bool first = true;
     if (copies && !LIST) {
-      walk8_init(w, t0, prefix, spos, B, Hkv);
-      for (long long i = 0; i < n_t; ++i) {
+      for (; w.u < t1; walk8_next(w, prefix, spos, B, Hkv)) {
         if (!wait_empty()) break;
         const int z = w.b * Hkv + w.kvh, row = w.k * kTile;
         // failure-path tests only: a tile never issued
@@ -569,30 +583,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0 && !skip && range_ok(row < L && z < B * Hkv, p.status)) {
           const uint32_t full = smem_u32(&bars[s]);
           const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes);
-          expect(full, kStageBytes, i == 0 || w.k == 0, w.b, w.kvh);
+          expect(full, kStageBytes, first || w.k == 0, w.b, w.kvh);
           tma_load_3d(sK, &tm_k, 0, row, z, full);
           tma_load_3d(sK + kOpBytes, &tm_v, 0, row, z, full);
         }
         __syncwarp();
-        next(w);
+        first = false;
         turn();
       }
     } else if (copies) {
-      walk8_init(w, t0 + min((long long)ti, n_t - 1), prefix, spos, B, Hkv);
-      long long i = ti;  // this lane's tile of the batch that `w` stands at
-      int blk = i < n_t ? fetch(w) : -1;
+      step(w, ti);  // this lane's tile of the batch at hand
+      int blk = w.u < t1 ? fetch(w) : -1;
       bool ok = true;
-      for (long long base = 0; ok && base < n_t; base += 4) {
-        const int row = row_of(w, blk), b = w.b, kvh = w.kvh, k = w.k;
+      while (ok) {
+        const bool on = w.u < t1;
+        const int n_q = __popc(__ballot_sync(0xffffffffu, on)) >> 3;  // tiles of the batch
+        if (n_q == 0) break;
+        const int row = on ? row_of(w, blk) : kNoRow, b = w.b, kvh = w.kvh, k = w.k;
         const int z = b * Hkv + kvh;
-        step4(w, i);
-        i += 4;
-        blk = i < n_t ? fetch(w) : -1;
+        step(w, 4);
+        blk = w.u < t1 ? fetch(w) : -1;
         const bool skip = p.test_skip >= 0 && z == 0 && k == p.test_skip;
         const bool have = !skip && row != kNoRow && in_block == 0 &&
                           range_ok(row >= 0 && row < L && z < B * Hkv, p.status);
         const uint32_t boxes = __ballot_sync(0xffffffffu, have);
-        const int n_q = (int)min(4ll, n_t - base);
         for (int q = 0; q < n_q; ++q) {
           if (!wait_empty()) {
             ok = false;
@@ -601,21 +615,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t full = smem_u32(&bars[s]);
           if (lane == 8 * q && !skip)
             expect(full, __popc((boxes >> (8 * q)) & 0xffu) * (uint32_t)entry_rows * 2u * kD,
-                   base + q == 0 || k == 0, b, kvh);
+                   first || k == 0, b, kvh);
           __syncwarp();
           if (ti == q && have) {
             const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes) + slice * 16 * kD;
             tma_load_3d(sK, &tm_k, 0, row, z, full);
             tma_load_3d(sK + kOpBytes, &tm_v, 0, row, z, full);
           }
+          first = false;
           turn();
         }
       }
     } else {
-      walk8_init(w, t0 + min((long long)ti, n_t - 1), prefix, spos, B, Hkv);
-      long long i = ti;
-      auto look_up = [&](int blk, bool on, int& row, float& ks, float& vs) {
-        row = on ? row_of(w, blk) : kNoRow;
+      step(w, ti);
+      auto look_up = [&](int blk, int& row, float& ks, float& vs) {
+        row = w.u < t1 ? row_of(w, blk) : kNoRow;
         ks = vs = 1.f;
         if (row != kNoRow) {
           const size_t at = (size_t)(w.b * Hkv + w.kvh) * p.nb + (row >> p.lb);
@@ -625,18 +639,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int row;
       float ks, vs;
-      look_up(LIST && i < n_t ? fetch(w) : -1, i < n_t, row, ks, vs);
-      step4(w, i);
-      i += 4;
-      int blk = LIST && i < n_t ? fetch(w) : -1;
+      bool on = w.u < t1;
+      look_up(LIST && on ? fetch(w) : -1, row, ks, vs);
+      step(w, 4);
+      int blk = LIST && w.u < t1 ? fetch(w) : -1;
       bool ok = true;
-      for (long long base = 0; ok && base < n_t; base += 4) {
+      while (ok) {
+        const int n_q = __popc(__ballot_sync(0xffffffffu, on)) >> 3;
+        if (n_q == 0) break;
         int row_next;
         float ks_next, vs_next;
-        look_up(blk, i < n_t, row_next, ks_next, vs_next);
-        step4(w, i);
-        i += 4;
-        blk = LIST && i < n_t ? fetch(w) : -1;
+        look_up(blk, row_next, ks_next, vs_next);
+        on = w.u < t1;
+        step(w, 4);
+        blk = LIST && w.u < t1 ? fetch(w) : -1;
         SliceMeta mt;
         mt.row0 = row;
         mt.ks = ks;
@@ -645,7 +661,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mt.lv = (float)((int)(bits >> 23) - 127) +
                 log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
         mt.inv_vs = 1.f / vs;
-        const int n_q = (int)min(4ll, n_t - base);
         for (int q = 0; q < n_q; ++q) {
           if (!wait_empty()) {
             ok = false;
@@ -677,8 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n_parts = 0;
     int s = 0;
     uint32_t ph = 0;
-    for (long long t = t0; t < t1;) {
-      const int len = (int)min((long long)(w.nt - w.k), t1 - t);
+    for (bool first = true; w.u < t1; first = false) {
+      const int len = (int)min((long long)(w.nt - w.k), t1 - w.u);
       cs.reset();
       bool ok = true;
       for (int i = 0; i < len; ++i) {
@@ -704,24 +719,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*abort_flag) break;
       // ---- this CTA's part: the warps' partials, in warp order -----------
       const bool whole = w.k == 0 && len == w.nt;
-      const int slot = 2 * blockIdx.x + (t == t0 ? 0 : 1);
+      const int slot = 2 * blockIdx.x + (first ? 0 : 1);
       const size_t out_at = ((size_t)w.b * p.Hq + (size_t)w.kvh * g) * kD;
-      for (int i = tid; i < g * kD; i += kConsumers) {
-        const int h = i / kD, d = i % kD;
-        float M = kMInit;
-#pragma unroll
-        for (int ww = 0; ww < kWarps; ++ww) M = fmaxf(M, merge_ml[(ww * g + h) * 2]);
-        float ls = 0.f, os = 0.f;
+      for (int i = tid; i < g * (kD / 4); i += kConsumers) {
+        const int h = i / (kD / 4), d = (i % (kD / 4)) * 4;
+        float2 ml[kWarps];
+        float M = kMInit, ls = 0.f;
 #pragma unroll
         for (int ww = 0; ww < kWarps; ++ww) {
-          const float e = ex2(merge_ml[(ww * g + h) * 2] - M);
-          ls = fmaf(merge_ml[(ww * g + h) * 2 + 1], e, ls);
-          os = fmaf(merge_o[(ww * g + h) * kD + d], e, os);
+          ml[ww] = *reinterpret_cast<const float2*>(merge_ml + (ww * g + h) * 2);
+          M = fmaxf(M, ml[ww].x);
+        }
+        float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int ww = 0; ww < kWarps; ++ww) {
+          const float e = ex2(ml[ww].x - M);
+          const float4 x = *reinterpret_cast<const float4*>(merge_o + merge_row(ww, h, g) + d);
+          ls = fmaf(ml[ww].y, e, ls);
+          os.x = fmaf(x.x, e, os.x);
+          os.y = fmaf(x.y, e, os.y);
+          os.z = fmaf(x.z, e, os.z);
+          os.w = fmaf(x.w, e, os.w);
         }
         if (whole) {
-          store_bf16(p.out, out_at + i, ls == 0.f ? 0.f : os / ls);
+          const float inv = ls == 0.f ? 0.f : 1.f / ls;
+          *reinterpret_cast<uint2*>(p.out + out_at + (size_t)i * 4) = make_uint2(
+              pack_bf16x2(os.x * inv, os.y * inv), pack_bf16x2(os.z * inv, os.w * inv));
         } else {
-          p.part_o[((size_t)slot * g) * kD + i] = os;
+          reinterpret_cast<float4*>(p.part_o + (size_t)slot * g * kD)[i] = os;
           if (d == 0)
             *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * g + h) * 2) =
                 make_float2(M, ls);
@@ -729,14 +754,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!whole) {
         Part8& pt = parts[n_parts++];
-        pt.f0 = t - w.k;
+        pt.f0 = w.u - w.k;
         pt.f1 = pt.f0 + w.nt;
         pt.seg = w.b * Hkv + w.kvh;
         pt.out_at = out_at;
       }
       csync(lane);  // the merge buffers may be written again
-      t += len;
-      if (t < t1) walk8_segment(w, prefix, spos, B, Hkv);
+      if (len < w.nt - w.k) break;  // the range ends inside the segment
+      walk8_segment(w, prefix, spos, B, Hkv);
     }
     if (n_parts > 0 && !*abort_flag) {
       // ---- each split segment: its last CTA to arrive merges the parts ------
