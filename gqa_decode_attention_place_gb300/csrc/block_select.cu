@@ -11,78 +11,104 @@
 // Selection.  Of the blocks 0..last a position has (last = pos / block): all
 // of them if there are no more than `count`; else the first `first`, the
 // `recent` last ones, and of the others the best-scored, ties to the lowest
-// index.  The threshold is the need-th largest score: found bit by bit from
-// the top over order-preserving integer keys (32 block-wide counts, the keys
-// in registers), then one block scan places the chosen indices in ascending
-// order.
+// index.  Scores become order-preserving integer keys; the need-th largest is
+// found digit by digit from the top (12, 12 and 8 bits: a histogram in shared
+// memory and a scan over its bins each), with the keys in registers, and most
+// often the first or second digit already settles it.  Then one scan over
+// (round, warp) counts places the chosen indices in ascending order.  The
+// first digit holds sign, exponent and three bits of the mantissa, so that
+// scores of one size still spread over many bins (the histogram's atomics
+// contend only where scores are alike).
 #include "common.cuh"
+#include "decode_params.h"
 #include "internal.h"
 
 namespace gqa {
 namespace {
 
 constexpr int kScoreWarps = 8;
-constexpr int kScoreBlocksPerWarp = 8;
+constexpr int kScoreThreads = kScoreWarps * 32;
+constexpr int kScoreBlocksPerWarp = 16;
 constexpr int kScoreBlocksPerCta = kScoreWarps * kScoreBlocksPerWarp;
 
-__global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(
-    const uint4* __restrict__ q, const int32_t* __restrict__ positions,
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A warp scores 16 blocks: their bounds are the 16 rows of MMA operand A,
+// loaded from memory in the operand's own layout (lane 4c + t takes 16-byte
+// pieces 4i + t of rows c and c + 8; the order of the 256 products is free),
+// and the vector is operand B as three bf16 columns (value, remainder,
+// remainder of that: 24 bits), so every product is exact and nothing is
+// unpacked.  (With fp32 multiply-adds on unpacked values the kernel was bound
+// by its instructions: 30.5 against 24 us for 142 MB.)
+__global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(
+    const uint16_t* __restrict__ q, const int32_t* __restrict__ positions,
     const uint4* __restrict__ bounds, float* __restrict__ scores, int Hkv, int g, int L,
     int block, int nb) {
+  __shared__ __align__(16) uint16_t parts[3][2 * kDecodeD];
   grid_dependency_wait();
   grid_dependents_launch();
-  const int seg = blockIdx.x, b = seg / Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int seg = blockIdx.x, b = seg / Hkv, tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31, c = lane >> 2, t = lane & 3;
   const int pos = positions[b];
   const int n = rows_in_cache(pos, 0, L) ? pos / block + 1 : 0;
   const int j0 = blockIdx.y * kScoreBlocksPerCta + warp * kScoreBlocksPerWarp;
-  float w[8];  // lanes 0-15: sum of q+ for dims 8l.., lanes 16-31: sum of q-
+  const int cta0 = blockIdx.y * kScoreBlocksPerCta;
+  float* out = scores + (size_t)seg * nb;
+  if (cta0 >= n) {  // nothing here up to the position
+    for (int j = cta0 + tid; j < min(nb, cta0 + kScoreBlocksPerCta); j += kScoreThreads)
+      out[j] = -INFINITY;
+    return;
+  }
+  uint4 ua[8], ub[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = 0.f;
-  if (j0 < n)
+  for (int i = 0; i < 8; ++i) {
+    const uint4* row = bounds + ((size_t)seg * nb + j0) * 32 + 4 * i + t;
+    ua[i] = j0 + c < n ? row[c * 32] : make_uint4(0u, 0u, 0u, 0u);
+    ub[i] = j0 + c + 8 < n ? row[(c + 8) * 32] : make_uint4(0u, 0u, 0u, 0u);
+  }
+  {  // element tid of the vector: dims of q+ summed over the heads, then of q-
+    const uint16_t* src = q + (size_t)seg * g * kDecodeD + (tid & (kDecodeD - 1));
+    float w = 0.f;
+#pragma unroll 4
     for (int h = 0; h < g; ++h) {
-      const uint4 u = q[((size_t)seg * g + h) * 16 + (lane & 15)];
-      const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = bf16lo(x[i]), hi = bf16hi(x[i]);
-        w[2 * i] += lane < 16 ? fmaxf(lo, 0.f) : fminf(lo, 0.f);
-        w[2 * i + 1] += lane < 16 ? fmaxf(hi, 0.f) : fminf(hi, 0.f);
-      }
+      const float x = __uint_as_float((uint32_t)src[h * kDecodeD] << 16);
+      w += tid < kDecodeD ? fmaxf(x, 0.f) : fminf(x, 0.f);
     }
-  // the bounds of the warp's 8 blocks, all in flight together
-  uint4 u[kScoreBlocksPerWarp];
 #pragma unroll
-  for (int i = 0; i < kScoreBlocksPerWarp; ++i)
-    u[i] = j0 + i < n ? bounds[((size_t)seg * nb + j0 + i) * 32 + lane] : make_uint4(0u, 0u, 0u, 0u);
-  float s[kScoreBlocksPerWarp];
-#pragma unroll
-  for (int i = 0; i < kScoreBlocksPerWarp; ++i) {
-    const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-    s[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      s[i] = fmaf(bf16lo(x[k]), w[2 * k], fmaf(bf16hi(x[k]), w[2 * k + 1], s[i]));
-  }
-  // 8 sums over 32 lanes: each of the first three exchanges halves the number
-  // of sums a lane still carries, so 9 shuffles do the work of 40
-#pragma unroll
-  for (int half = 4; half > 0; half >>= 1) {
-    const bool up = lane & (4 * half);
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float give = up ? s[i] : s[i + half], keep = up ? s[i + half] : s[i];
-      s[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * half);
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t r = pack_bf16x2(w, 0.f);
+      parts[k][tid] = (uint16_t)r;
+      w -= bf16lo(r);
     }
   }
-  s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
-  s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
-  const int j = j0 + (lane >> 2);  // lanes 4i .. 4i+3 hold block i's sum
-  if ((lane & 3) == 0 && j < nb) scores[(size_t)seg * nb + j] = j < n ? s[0] : -INFINITY;
+  __syncthreads();
+  float d[2][4] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint4 v = c < 3 ? *reinterpret_cast<const uint4*>(&parts[c < 3 ? c : 0][8 * (4 * i + t)])
+                          : make_uint4(0u, 0u, 0u, 0u);
+    mma_bf16(d[0], ua[i].x, ub[i].x, ua[i].y, ub[i].y, v.x, v.y);
+    mma_bf16(d[1], ua[i].z, ub[i].z, ua[i].w, ub[i].w, v.z, v.w);
+  }
+  // columns 0 and 1 are in the lanes t = 0, column 2 in t = 1
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const float c0 = d[0][2 * r] + d[1][2 * r], c1 = d[0][2 * r + 1] + d[1][2 * r + 1];
+    const float s = c0 + (c1 + __shfl_down_sync(0xffffffffu, c0, 1));
+    const int j = j0 + c + 8 * r;
+    if (t == 0 && j < nb) out[j] = j < n ? s : -INFINITY;
+  }
 }
 
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 4096;
 
 // Order-preserving key of a score: larger score, larger key; -0 = +0; NaN is
 // taken as -inf.
@@ -93,17 +119,9 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Sum of v over the block; every thread gets it.  `slots` holds two sets of
-// counters so that one barrier per call suffices.
-__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t (*slots)[32], int phase) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) slots[phase][warp] = v;
-  __syncthreads();
-  return __reduce_add_sync(0xffffffffu, lane < kSelectWarps ? slots[phase][lane] : 0u);
-}
-// Exclusive prefix sum of v over the block's threads.
-__device__ __forceinline__ int block_scan(int v, uint32_t (*slots)[32], int phase) {
+// Exclusive prefix sum of v over the block's threads; *all = the total.  One
+// barrier; calls in a row use the two sets of `slots` in turn.
+__device__ __forceinline__ int block_scan(int v, uint32_t (*slots)[32], int& phase, int* all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int x = v;
 #pragma unroll
@@ -113,20 +131,28 @@ __device__ __forceinline__ int block_scan(int v, uint32_t (*slots)[32], int phas
   }
   if (lane == 31) slots[phase][warp] = x;
   __syncthreads();
-  const uint32_t w = lane < warp ? slots[phase][lane] : 0u;
-  return (int)__reduce_add_sync(0xffffffffu, w) + x - v;
+  const uint32_t w = lane < kSelectWarps ? slots[phase][lane] : 0u;
+  phase ^= 1;
+  *all = (int)__reduce_add_sync(0xffffffffu, w);
+  return (int)__reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + x - v;
 }
 
-// I items per thread, thread t holding items t*I .. t*I + I-1 (I = 0: any
-// number of items, read again from memory in every pass).
-template <int I>
+// Items are dealt out to the threads in rounds (item r*kSelectThreads + tid in
+// round r), I rounds to a chunk.  LOOP: more than one chunk, whose scores are
+// read again in every pass; else the keys stay in registers.
+template <int I, bool LOOP>
 __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
     const float* __restrict__ scores, const int32_t* __restrict__ positions, int32_t* out,
     int Hkv, int L, int block, int nb, int count, int first, int recent) {
+  constexpr int kChunk = I * kSelectThreads;
+  __shared__ __align__(16) int hist[kBins];
   __shared__ uint32_t slots[2][32];
+  __shared__ int rounds[2][I * kSelectWarps];
+  __shared__ int found[3];
   grid_dependency_wait();
   grid_dependents_launch();
   const int seg = blockIdx.x, b = seg / Hkv, tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31;
   const int pos = positions[b];
   const int n = rows_in_cache(pos, 0, L) ? pos / block + 1 : 0;
   int32_t* o = out + (size_t)seg * count;
@@ -134,67 +160,148 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
     for (int i = tid; i < count; i += kSelectThreads) o[i] = i < n ? i : -1;
     return;
   }
-  const float* s = scores + (size_t)seg * nb;
-  const int items = I > 0 ? I : (n + kSelectThreads - 1) / kSelectThreads;
-  const long long i0 = (long long)tid * items;
+  const float* sc = scores + (size_t)seg * nb;
   const int need = count - first - recent;  // of the blocks first .. n-recent-1
-  uint32_t key[I > 0 ? I : 1];
-  if (I > 0) {
+  uint32_t key[I];
+  auto load = [&](int at) {  // the keys of the chunk at item `at`; 0 (below every key): no candidate
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const long long j = i0 + i;
-      key[i] = j >= first && j < n - recent ? score_key(s[j]) : 0u;  // 0: below every key
+      const int j = at + i * kSelectThreads + tid;
+      key[i] = 0u;
+      if (at + i * kSelectThreads >= n) continue;  // (the whole block)
+      key[i] = j >= first && j < n - recent ? score_key(sc[j]) : 0u;
     }
-  }
-  auto get = [&](int i) -> uint32_t {
-    if (I > 0) return key[i];
-    const long long j = i0 + i;
-    return j >= first && j < n - recent ? score_key(s[j]) : 0u;
   };
   int phase = 0;
-  // the need-th largest key: the largest th with count(key >= th) >= need
-  uint32_t th = 0;
+  uint32_t th = 0;   // all keys above th are chosen,
+  int tie_room = 0;  // and the first tie_room of those equal to it
+  bool all_ties = true;  // ... which are all of them
   if (need > 0) {
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t cand = th | (1u << bit);
-      int c = 0;
+    if (!LOOP) load(0);
+    int left = need;
+    uint32_t mask = 0;  // bits of th settled so far
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 20 : pass == 1 ? 8 : 0;
+      const uint32_t digits = pass == 2 ? 0xffu : 0xfffu;
+      for (int i = tid; i < kBins / 4; i += kSelectThreads)
+        reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+      __syncthreads();
+      for (int at = 0; at < (LOOP ? n : 1); at += kChunk) {
+        if (LOOP) load(at);
 #pragma unroll
-      for (int i = 0; i < items; ++i) c += get(i) >= cand;
-      const int all = (int)block_sum(c, slots, phase);
-      phase ^= 1;
-      if (all >= need) th = cand;
-      if (all == need) break;  // exactly the keys >= th: the lower bits do not matter
+        for (int i = 0; i < I; ++i)
+          if (at + i * kSelectThreads < n && key[i] != 0u && (key[i] & mask) == th)
+            atomicAdd(&hist[(key[i] >> shift) & digits], 1);
+      }
+      __syncthreads();
+      // the digit of the left-th largest: thread t holds bins from the top
+      constexpr int kPer = kBins / kSelectThreads;
+      int c[kPer], sum = 0, all;
+      const int top = kBins - 1 - tid * kPer;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        c[i] = hist[top - i];
+        sum += c[i];
+      }
+      int before = block_scan(sum, slots, phase, &all);
+      if (before < left && before + sum >= left) {  // one thread
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (before < left && before + c[i] >= left) {
+            found[0] = top - i;
+            found[1] = left - before;
+            found[2] = c[i];
+          }
+          before += c[i];
+        }
+      }
+      __syncthreads();
+      th |= (uint32_t)found[0] << shift;
+      mask |= digits << shift;
+      left = found[1];
+      all_ties = found[2] == left;
+      if (all_ties) break;  // every key of the bin is chosen: the lower bits do not matter
+      // (found is written again only after another barrier)
     }
+    tie_room = left;
   }
-  int above = 0, ties = 0;
+  // Place the chosen indices in ascending order: per round and warp a count,
+  // one scan over them, then each lane's rank within its warp.
+  int base = 0, tie_base = 0;
+  for (int at = 0; at < n; at += kChunk) {
+    if (LOOP && need > 0) load(at);
+    uint32_t take = 0;  // bit i: item of round i
+    if (need > 0 && !all_ties) {  // ties in part: their ranks first
 #pragma unroll
-  for (int i = 0; i < items; ++i) {
-    const uint32_t k = get(i);
-    above += need > 0 && k > th;
-    ties += need > 0 && k == th;
-  }
-  const int all_above = (int)block_sum(above, slots, phase);
-  phase ^= 1;
-  const int ties_before = block_scan(ties, slots, phase);
-  phase ^= 1;
-  const int tie_room = need - all_above;  // ties taken, lowest indices first
-  const int forced = (int)(min(i0 + items, (long long)n) - min(i0, (long long)n)) -
-                     (int)max(0ll, min(i0 + items, (long long)(n - recent)) -
-                                       max(i0, (long long)first));
-  const int mine = above + min(ties, max(0, tie_room - ties_before)) + max(0, forced);
-  int at = block_scan(mine, slots, phase);
-  int tie = ties_before;
+      for (int i = 0; i < I; ++i) {
+        const uint32_t t = __ballot_sync(0xffffffffu, key[i] == th);
+        if (lane == 0) rounds[0][i * kSelectWarps + warp] = __popc(t);
+      }
+      __syncthreads();
+      int all;
+      constexpr int kCells = I * kSelectWarps, kCellPer = (kCells + kSelectThreads - 1) / kSelectThreads;
+      int v = 0;
 #pragma unroll
-  for (int i = 0; i < items; ++i) {
-    const long long j = i0 + i;
-    if (j >= n) break;
-    bool take = j < first || j >= n - recent;
-    if (!take && need > 0) {
-      const uint32_t k = get(i);
-      take = k > th || (k == th && tie < tie_room);
-      tie += k == th;
+      for (int k = 0; k < kCellPer; ++k)
+        if (tid * kCellPer + k < kCells) v += rounds[0][tid * kCellPer + k];
+      int run = block_scan(v, slots, phase, &all) + tie_base;
+#pragma unroll
+      for (int k = 0; k < kCellPer; ++k)
+        if (tid * kCellPer + k < kCells) {
+          const int x = rounds[0][tid * kCellPer + k];
+          rounds[0][tid * kCellPer + k] = run;
+          run += x;
+        }
+      __syncthreads();
+      tie_base += all;
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        const uint32_t t = __ballot_sync(0xffffffffu, key[i] == th);
+        const int rank = rounds[0][i * kSelectWarps + warp] + __popc(t & ((1u << lane) - 1u));
+        if (key[i] > th || (key[i] == th && rank < tie_room)) take |= 1u << i;
+      }
+    } else if (need > 0) {
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+        if (key[i] >= th) take |= 1u << i;
     }
-    if (take) o[at++] = (int)j;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int j = at + i * kSelectThreads + tid;
+      if (at + i * kSelectThreads >= n) {
+        if (lane == 0) rounds[1][i * kSelectWarps + warp] = 0;
+        continue;
+      }
+      if (j < first || (j >= n - recent && j < n)) take |= 1u << i;
+      const uint32_t t = __ballot_sync(0xffffffffu, (take >> i) & 1u);
+      if (lane == 0) rounds[1][i * kSelectWarps + warp] = __popc(t);
+    }
+    __syncthreads();
+    int all;
+    constexpr int kCells = I * kSelectWarps, kCellPer = (kCells + kSelectThreads - 1) / kSelectThreads;
+    int v = 0;
+#pragma unroll
+    for (int k = 0; k < kCellPer; ++k)
+      if (tid * kCellPer + k < kCells) v += rounds[1][tid * kCellPer + k];
+    int run = block_scan(v, slots, phase, &all) + base;
+#pragma unroll
+    for (int k = 0; k < kCellPer; ++k)
+      if (tid * kCellPer + k < kCells) {
+        const int x = rounds[1][tid * kCellPer + k];
+        rounds[1][tid * kCellPer + k] = run;
+        run += x;
+      }
+    __syncthreads();
+    base += all;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      if (at + i * kSelectThreads >= n) continue;
+      const uint32_t t = __ballot_sync(0xffffffffu, (take >> i) & 1u);
+      if ((take >> i) & 1u)
+        o[rounds[1][i * kSelectWarps + warp] + __popc(t & ((1u << lane) - 1u))] =
+            at + i * kSelectThreads + tid;
+    }
+    if (LOOP) __syncthreads();  // the cells may be written again
   }
 }
 
@@ -205,8 +312,8 @@ cudaError_t launch_block_scores(const void* q, const int32_t* positions, const v
                                 cudaStream_t stream) {
   const int nb = (L + block - 1) / block;
   const int ctas = (nb + kScoreBlocksPerCta - 1) / kScoreBlocksPerCta;
-  return launch_pdl(block_scores_kernel, dim3(B * Hkv, ctas), dim3(kScoreWarps * 32), 0, stream,
-                    static_cast<const uint4*>(q), positions, static_cast<const uint4*>(k_bounds),
+  return launch_pdl(block_scores_kernel, dim3(B * Hkv, ctas), dim3(kScoreThreads), 0, stream,
+                    static_cast<const uint16_t*>(q), positions, static_cast<const uint4*>(k_bounds),
                     scores, Hkv, Hq / Hkv, L, block, nb);
 }
 
@@ -215,13 +322,10 @@ cudaError_t launch_block_select(const float* scores, const int32_t* positions, i
                                 cudaStream_t stream) {
   const int nb = (L + block - 1) / block;
   const int per = (nb + kSelectThreads - 1) / kSelectThreads;
-  auto kernel = per <= 1    ? block_select_kernel<1>
-                : per <= 2  ? block_select_kernel<2>
-                : per <= 4  ? block_select_kernel<4>
-                : per <= 8  ? block_select_kernel<8>
-                : per <= 16 ? block_select_kernel<16>
-                : per <= 32 ? block_select_kernel<32>
-                            : block_select_kernel<0>;
+  auto kernel = per <= 1    ? block_select_kernel<1, false>
+                : per <= 4  ? block_select_kernel<4, false>
+                : per <= 16 ? block_select_kernel<16, false>
+                            : block_select_kernel<16, true>;
   return launch_pdl(kernel, dim3(B * Hkv), dim3(kSelectThreads), 0, stream, scores, positions,
                     out, Hkv, L, block, nb, count, first, recent);
 }

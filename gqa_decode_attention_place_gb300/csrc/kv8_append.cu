@@ -10,9 +10,9 @@
 //   bounds: per channel, max and min of the new rows and, if the block
 //           already held rows, of what was there.
 //
-// One CTA per (block, KV head, operand): 16 rows of 16 lanes x 16 bytes per
-// pass, all passes in registers, so the rows are read once; the maximum goes
-// through one block reduction.  Bound by memory for prompts (2 bytes read
+// One CTA per (block, KV head), keys and values together: 16 rows of 16 lanes
+// x 16 bytes per pass, all passes in registers, so the rows are read once and
+// all in flight together; the maxima go through one block reduction.  Bound by memory for prompts (2 bytes read
 // and 1 written per value) and by latency for single tokens.
 #include "fp8.cuh"
 #include "internal.h"
@@ -44,40 +44,50 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
     const int32_t* __restrict__ positions, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
     float* v_scale, uint32_t* k_bounds, int B, int S, int Hkv, int L, int nb) {
   constexpr int T = 16 * P;
-  __shared__ uint32_t s_max[8];
+  __shared__ uint32_t s_max[2][8];
   __shared__ uint32_t s_hi[8][64], s_lo[8][64];
   grid_dependency_wait();
   grid_dependents_launch();
-  const int h = blockIdx.y >> 1, op = blockIdx.y & 1, b = blockIdx.z;
+  const int h = blockIdx.y, b = blockIdx.z;
   const int pos = positions[b];
   if (!rows_in_cache(pos, S - 1, L)) return;  // reported by the decode call
   const int j = pos / T + blockIdx.x;
   if (j > (pos + S - 1) / T) return;
   const int tid = threadIdx.x, c = tid & 15, warp = tid >> 5, lane = tid & 31;
-  const uint4* src = op ? v_new : k_new;
-  uint8_t* cache = (op ? v_cache : k_cache) + ((size_t)b * Hkv + h) * L * kD8;
-  float* scale = (op ? v_scale : k_scale) + ((size_t)b * Hkv + h) * nb + j;
+  const size_t seg = (size_t)b * Hkv + h;
   const int row0 = j * T;
+  const int t0 = row0 + (tid >> 4) - pos;  // new token of pass 0; 16 more each pass
   const bool had = row0 < pos;
-  const float s_old = had ? *scale : 0.f;
 
-  uint4 x[P];
-  uint32_t amax = 0;
+  uint4 x[2][P];
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int t = row0 + i * 16 + (tid >> 4) - pos;  // new token
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (t >= 0 && t < S) x[i] = src[(((size_t)b * S + t) * Hkv + h) * 16 + c];
+  for (int op = 0; op < 2; ++op)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int t = t0 + i * 16;
+      x[op][i] = make_uint4(0u, 0u, 0u, 0u);
+      if (t >= 0 && t < S) x[op][i] = (op ? v_new : k_new)[(((size_t)b * S + t) * Hkv + h) * 16 + c];
+    }
+  float s_old[2] = {0.f, 0.f};
+  if (had) {
+    s_old[0] = k_scale[seg * nb + j];
+    s_old[1] = v_scale[seg * nb + j];
   }
+  // this thread's word of the block's bounds: 0..63 the maxima, 64..127 the minima
+  uint32_t* bound = k_bounds + (seg * nb + j) * 128 + tid;
+  const bool bounds = k_bounds != nullptr && tid < 128;
+  const uint32_t was = bounds && had ? *bound : 0u;
 #pragma unroll
-  for (int i = 0; i < P; ++i)
-    amax = max(max(max(amax, finite_abs_max(x[i].x)), max(finite_abs_max(x[i].y),
-               finite_abs_max(x[i].z))), finite_abs_max(x[i].w));
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  if (lane == 0) s_max[warp] = amax;
-
-  const bool bounds = op == 0 && k_bounds != nullptr;
-  if (bounds) {
+  for (int op = 0; op < 2; ++op) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      amax = max(max(max(amax, finite_abs_max(x[op][i].x)), max(finite_abs_max(x[op][i].y),
+                 finite_abs_max(x[op][i].z))), finite_abs_max(x[op][i].w));
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    if (lane == 0) s_max[op][warp] = amax;
+  }
+  if (k_bounds != nullptr) {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -86,9 +96,9 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int t = row0 + i * 16 + (tid >> 4) - pos;
+      const int t = t0 + i * 16;
       if (t >= 0 && t < S) {
-        const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        const uint32_t w4[4] = {x[0][i].x, x[0][i].y, x[0][i].z, x[0][i].w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           hi[w] = bf16x2_max(hi[w], w4[w]);
@@ -108,48 +118,54 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
   }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) amax = max(amax, s_max[w]);
-  const float s_new = block_scale(__uint_as_float(amax << 16));
-  const float s = had ? fmaxf(s_old, s_new) : s_new;
-  if (tid == 0) *scale = s;  // every thread's read of s_old came before the barrier
-  const float inv = 1.f / s;
+  for (int op = 0; op < 2; ++op) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) amax = max(amax, s_max[op][w]);
+    const float s_new = block_scale(__uint_as_float(amax << 16));
+    const float s = had ? fmaxf(s_old[op], s_new) : s_new;
+    // every thread's read of s_old came before the barrier
+    if (tid == 0) (op ? v_scale : k_scale)[seg * nb + j] = s;
+    const float inv = 1.f / s;
+    uint8_t* cache = (op ? v_cache : k_cache) + seg * L * kD8;
 
-  if (had && s > s_old) {  // the block's scale grew: move the older rows
-    const float ratio = s_old * inv;
-    for (int r = row0 + (tid >> 4); r < pos; r += 16) {
-      uint2* at = reinterpret_cast<uint2*>(cache + (size_t)r * kD8 + c * 8);
-      uint2 w = *at;
-      uint32_t o[4];
+    if (had && s > s_old[op]) {  // the block's scale grew: move the older rows
+      const float ratio = s_old[op] * inv;
+      for (int r = row0 + (tid >> 4); r < pos; r += 16) {
+        uint2* at = reinterpret_cast<uint2*>(cache + (size_t)r * kD8 + c * 8);
+        uint2 w = *at;
+        uint32_t o[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(((k & 2) ? w.y : w.x) >> ((k & 1) * 16)));
-        o[k] = f32x2_to_e4m3x2(f.x * ratio, f.y * ratio);
+        for (int k = 0; k < 4; ++k) {
+          const float2 f =
+              f16x2_to_f32x2(e4m3x2_to_f16x2(((k & 2) ? w.y : w.x) >> ((k & 1) * 16)));
+          o[k] = f32x2_to_e4m3x2(f.x * ratio, f.y * ratio);
+        }
+        *at = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
       }
-      *at = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int t = t0 + i * 16;
+      if (t >= 0 && t < S) {
+        const uint32_t w4[4] = {x[op][i].x, x[op][i].y, x[op][i].z, x[op][i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = f32x2_to_e4m3x2(bf16lo(w4[k]) * inv, bf16hi(w4[k]) * inv);
+        *reinterpret_cast<uint2*>(cache + (size_t)(t + pos) * kD8 + c * 8) =
+            make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+      }
     }
   }
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int r = row0 + i * 16 + (tid >> 4), t = r - pos;
-    if (t >= 0 && t < S) {
-      const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      uint32_t o[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        o[k] = f32x2_to_e4m3x2(bf16lo(w4[k]) * inv, bf16hi(w4[k]) * inv);
-      *reinterpret_cast<uint2*>(cache + (size_t)r * kD8 + c * 8) =
-          make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
-    }
-  }
-  if (bounds && tid < 128) {  // words 0..63: the maxima, 64..127: the minima
+  if (bounds) {
     const int w = tid & 63;
-    uint32_t* dst = k_bounds + (((size_t)b * Hkv + h) * nb + j) * 128 + tid;
     uint32_t m = tid < 64 ? s_hi[0][w] : s_lo[0][w];
 #pragma unroll
     for (int i = 1; i < 8; ++i)
       m = tid < 64 ? bf16x2_max(m, s_hi[i][w]) : bf16x2_min(m, s_lo[i][w]);
-    if (had) m = tid < 64 ? bf16x2_max(m, *dst) : bf16x2_min(m, *dst);
-    *dst = m;
+    if (had) m = tid < 64 ? bf16x2_max(m, was) : bf16x2_min(m, was);
+    *bound = m;
   }
 }
 
@@ -165,7 +181,7 @@ cudaError_t launch_kv8_append(const void* k_new, const void* v_new, const int32_
                 : block == 32 ? kv8_append_kernel<2>
                 : block == 64 ? kv8_append_kernel<4>
                               : kv8_append_kernel<8>;
-  return launch_pdl(kernel, dim3(touched, 2 * Hkv, B), dim3(256), 0, stream,
+  return launch_pdl(kernel, dim3(touched, Hkv, B), dim3(256), 0, stream,
                     static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), positions,
                     static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale,
                     v_scale, static_cast<uint32_t*>(k_bounds), B, S, Hkv, L, nb);

@@ -12,9 +12,9 @@
 // A lane holds dims 8c..8c+7 and their partners D/2 further on, so the
 // rotation needs no exchange between lanes; the row's D/16 lanes (padded to
 // a power of two) share only the sum of squares.  A warp stays with one
-// token, so the rotation row (32 values per lane) is read once and serves
-// every head the warp takes.  Bound by memory for prompts, by latency for
-// single tokens.
+// token, so weight and rotation are multiplied into one set of factors (32
+// values per lane) that serves every query head, and another every key head,
+// the warp takes.  Bound by memory for prompts, by latency for single tokens.
 #include "common.cuh"
 #include "internal.h"
 
@@ -35,23 +35,36 @@ struct NormRopeParams {
 
 constexpr int kNormWarps = 4;
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-  f[0] = bf16lo(u.x); f[1] = bf16hi(u.x); f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
-  f[4] = bf16lo(u.z); f[5] = bf16hi(u.z); f[6] = bf16lo(u.w); f[7] = bf16hi(u.w);
+// 8 bf16 as 4 packed fp32 pairs, and back.
+__device__ __forceinline__ void unpack8(const uint4& u, f2 (&f)[4]) {
+  f[0] = mk2(bf16lo(u.x), bf16hi(u.x));
+  f[1] = mk2(bf16lo(u.y), bf16hi(u.y));
+  f[2] = mk2(bf16lo(u.z), bf16hi(u.z));
+  f[3] = mk2(bf16lo(u.w), bf16hi(u.w));
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint32_t pack2(f2 x) {
+  float lo, hi;
+  brk2(x, lo, hi);
+  return pack_bf16x2(lo, hi);
 }
-__device__ __forceinline__ void load8f(const float* p, float (&f)[8]) {
+__device__ __forceinline__ void load8f(const float* p, f2 (&f)[4]) {
   const float4 a = *reinterpret_cast<const float4*>(p);
   const float4 b = *reinterpret_cast<const float4*>(p + 4);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  f[0] = mk2(a.x, a.y);
+  f[1] = mk2(a.z, a.w);
+  f[2] = mk2(b.x, b.y);
+  f[3] = mk2(b.z, b.w);
 }
 
+// What a lane multiplies its dims x (first half) and y (second half) by, with
+// weight and rotation in one factor (r: the row's 1/rms):
+//   out x = r * (x * xx - y * yx),  out y = r * (y * yy + x * xy)
+struct Coef {
+  f2 xx[4], yx[4], yy[4], xy[4];
+};
+
 // LPR lanes per row (a power of two >= D/16).  A warp handles 32/LPR heads at
-// a time, `steps` times, of one token; blockIdx.y and the warp pick the heads.
+// a time, `steps` times, of one token.
 template <int LPR>
 __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const NormRopeParams p,
                                                                        int warps_per_token,
@@ -67,23 +80,6 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
   const int c = lane % LPR, D = p.D, half = D >> 1;
   const bool on = c * 16 < D;  // lanes past D/16 only take part in the shuffles
   const int d0 = c * 8;
-  const int b = (int)(n / p.S), t = (int)(n % p.S);
-  const int pos0 = p.positions[b];
-  const bool ok = rows_in_cache(pos0, p.S - 1, p.L);
-  const int pos = pos0 + t;
-  float ca[8], cb[8], sa[8], sb[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    ca[i] = cb[i] = 1.f;
-    sa[i] = sb[i] = 0.f;
-  }
-  if (p.cos && ok && on) {
-    const size_t row = (size_t)pos * D + d0;
-    load8f(p.cos + row, ca);
-    load8f(p.cos + row + half, cb);
-    load8f(p.sin + row, sa);
-    load8f(p.sin + row + half, sb);
-  }
   const int heads = p.Hq + p.Hkv * (p.k_out ? 1 : 2);
   // this lane's two pieces of a head (nothing past the last head)
   auto load = [&](int head, uint4& ua, uint4& ub) {
@@ -96,9 +92,18 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
     ua = *reinterpret_cast<const uint4*>(src + d0);
     ub = *reinterpret_cast<const uint4*>(src + d0 + half);
   };
+  // The first loads go out before the position is read: the rotation row's
+  // address hangs on it, the heads' do not.
   const int head0 = part * steps * RPW + lane / LPR;
   uint4 next_a, next_b;
   load(head0, next_a, next_b);
+  const int b = (int)(n / p.S), t = (int)(n % p.S);
+  const int pos0 = p.positions[b];
+  const bool ok = rows_in_cache(pos0, p.S - 1, p.L);
+  const int pos = pos0 + t;
+  const float inv_d = 1.f / (float)D;
+  Coef cf;
+  int kind = -1;  // of cf: 0 queries, 1 keys
   for (int st = 0; st < steps; ++st) {
     const int head = head0 + st * RPW;
     uint4 ua = next_a, ub = next_b;
@@ -106,35 +111,60 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
     const bool row_on = on && head < heads;
     const bool is_q = head < p.Hq, is_v = head >= p.Hq + p.Hkv;
     const int h = is_q ? head : is_v ? head - p.Hq - p.Hkv : head - p.Hq;
-    float xa[8], xb[8];
+    f2 xa[4], xb[4];
     unpack8(ua, xa);
     unpack8(ub, xb);
-    float ss = 0.f;
+    f2 s2 = mul2(xa[0], xa[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
+    for (int i = 1; i < 4; ++i) s2 = fma2(xa[i], xa[i], s2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s2 = fma2(xb[i], xb[i], s2);
+    float s_lo, s_hi;
+    brk2(s2, s_lo, s_hi);
+    float ss = s_lo + s_hi;
 #pragma unroll
     for (int off = 1; off < LPR; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
     if (!row_on) continue;
     if (!is_v) {
-      const float r = rsqrtf(ss / (float)D + p.eps);
-      float wa[8], wb[8];
+      if (kind != (is_q ? 0 : 1)) {  // at the first head, and from queries to keys
+        kind = is_q ? 0 : 1;
+        const float one = ok ? 1.f : __uint_as_float(0x7fffffffu);  // bad position: NaN rows
+        f2 wa[4], wb[4], ca[4], cb[4], sa[4], sb[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.f;
-      const uint16_t* w = is_q ? p.q_weight : p.k_weight;
-      if (w) {
-        unpack8(*reinterpret_cast<const uint4*>(w + d0), wa);
-        unpack8(*reinterpret_cast<const uint4*>(w + d0 + half), wb);
-      }
-      float oa[8], ob[8];
+        for (int i = 0; i < 4; ++i) {
+          wa[i] = wb[i] = ca[i] = cb[i] = mk2(one, one);
+          sa[i] = sb[i] = mk2(0.f, 0.f);
+        }
+        const uint16_t* w = is_q ? p.q_weight : p.k_weight;
+        if (w) {
+          unpack8(*reinterpret_cast<const uint4*>(w + d0), wa);
+          unpack8(*reinterpret_cast<const uint4*>(w + d0 + half), wb);
+        }
+        if (p.cos && ok) {
+          const size_t row = (size_t)pos * D + d0;
+          load8f(p.cos + row, ca);
+          load8f(p.cos + row + half, cb);
+          load8f(p.sin + row, sa);
+          load8f(p.sin + row + half, sb);
+        }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float ya = xa[i] * r * wa[i], yb = xb[i] * r * wb[i];
-        oa[i] = ya * ca[i] - yb * sa[i];
-        ob[i] = yb * cb[i] + ya * sb[i];
-        if (!ok) oa[i] = ob[i] = __uint_as_float(0x7fffffffu);
+        for (int i = 0; i < 4; ++i) {
+          cf.xx[i] = mul2(wa[i], ca[i]);
+          cf.yx[i] = mul2(wb[i], mul2(sa[i], mk2(-1.f, -1.f)));
+          cf.yy[i] = mul2(wb[i], cb[i]);
+          cf.xy[i] = mul2(wa[i], sb[i]);
+        }
       }
-      ua = pack8(oa);
-      ub = pack8(ob);
+      const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+      const f2 r2 = mk2(r, r);
+      uint32_t oa[4], ob[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        oa[i] = pack2(mul2(r2, fma2(xb[i], cf.yx[i], mul2(xa[i], cf.xx[i]))));
+        ob[i] = pack2(mul2(r2, fma2(xa[i], cf.xy[i], mul2(xb[i], cf.yy[i]))));
+      }
+      ua = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+      ub = make_uint4(ob[0], ob[1], ob[2], ob[3]);
     }
     uint16_t* dst;
     if (is_q) {
