@@ -10,6 +10,10 @@ with ``-DGQA_DEBUG``: the kernels then check their index-derived addresses
 (bulk-copy tile coordinates, cluster landing slots, partial-result slots,
 output rows) before each access and record a failed check instead of making
 it.  Setting ``GQA_ATTN_DEBUG=1`` makes the package load that library.
+
+``build_marshal()`` makes ``lib/_gqa_marshal.so`` from ``csrc/marshal.cpp`` with
+the host compiler against the installed PyTorch's headers: the Python
+binding's argument checks.
 """
 
 from __future__ import annotations
@@ -20,6 +24,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -111,5 +116,35 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     return path
 
 
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL_PATH = os.path.join(LIBDIR, "_gqa_marshal.so")
+
+
+def build_marshal(force: bool = False) -> str:
+    """Compile the binding's native argument checks; return the module's path."""
+    deps = (MARSHAL_SRC, os.path.abspath(__file__))
+    if not force and os.path.exists(MARSHAL_PATH) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL_PATH) for p in deps):
+        return MARSHAL_PATH
+    import torch
+    base = os.path.dirname(torch.__file__)
+    os.makedirs(LIBDIR, exist_ok=True)
+    tmp = f"{MARSHAL_PATH}.{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           MARSHAL_SRC, "-o", tmp, "-L", os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(MARSHAL_SRC)} failed to compile:\n"
+                           f"{r.stdout}{r.stderr}")
+    os.replace(tmp, MARSHAL_PATH)
+    return MARSHAL_PATH
+
+
 if __name__ == "__main__":
+    build_marshal(force="--force" in sys.argv)
     build(force="--force" in sys.argv, verbose=True, debug="--debug" in sys.argv)
