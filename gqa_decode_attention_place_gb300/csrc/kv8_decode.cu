@@ -28,8 +28,12 @@
 //    pieces of two rows are interleaved byte-wise (prmt) before conversion.
 //  * A flat list of all tiles is split evenly over the grid (one CTA per SM);
 //    a segment split over CTAs is merged by the CTA that arrives last, in
-//    CTA order, so results do not depend on timing.
+//    CTA order, so results do not depend on timing.  For few segments a
+//    thread-block cluster takes each (kv8_cluster.cuh).
+#include <cooperative_groups.h>
+
 #include <atomic>
+#include <mutex>
 
 #include "fp8.cuh"
 #include "internal.h"
@@ -64,6 +68,18 @@ struct SliceMeta {
   float lv;       // log2 of the V scale
   float inv_vs;   // 1 / V scale
 };
+
+__device__ __forceinline__ SliceMeta slice_meta(int row, float ks, float vs) {
+  SliceMeta mt;
+  mt.row0 = row;
+  mt.ks = ks;
+  // log2 of a power of two comes out exact
+  const uint32_t bits = __float_as_uint(vs);
+  mt.lv = (float)((int)(bits >> 23) - 127) +
+          log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
+  mt.inv_vs = 1.f / vs;
+  return mt;
+}
 
 struct Kv8Params {
   const uint16_t* q;
@@ -336,6 +352,32 @@ struct Consumer8 {
       }
   }
 };
+
+// The warps' partials of column i (head i / 32, four dims), in warp order: the
+// maximum, and sum and unnormalised output relative to it.
+__device__ __forceinline__ void merge_warps8(const float* mo, const float* mml, int i, int g,
+                                             float& M, float& ls, float4& os) {
+  const int h = i / (kD / 4), d = (i % (kD / 4)) * 4;
+  float2 ml[kWarps];
+  M = kMInit;
+#pragma unroll
+  for (int ww = 0; ww < kWarps; ++ww) {
+    ml[ww] = *reinterpret_cast<const float2*>(mml + (ww * g + h) * 2);
+    M = fmaxf(M, ml[ww].x);
+  }
+  ls = 0.f;
+  os = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int ww = 0; ww < kWarps; ++ww) {
+    const float e = ex2(ml[ww].x - M);
+    const float4 x = *reinterpret_cast<const float4*>(mo + merge_row(ww, h, g) + d);
+    ls = fmaf(ml[ww].y, e, ls);
+    os.x = fmaf(x.x, e, os.x);
+    os.y = fmaf(x.y, e, os.y);
+    os.z = fmaf(x.z, e, os.z);
+    os.w = fmaf(x.w, e, os.w);
+  }
+}
 
 // A segment of which this CTA did a part: its tiles' units [f0, f1) in the flat order.
 struct Part8 {
@@ -653,14 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         on = w.u < t1;
         step(w, 4);
         blk = LIST && w.u < t1 ? fetch(w) : -1;
-        SliceMeta mt;
-        mt.row0 = row;
-        mt.ks = ks;
-        // log2 of a power of two comes out exact
-        const uint32_t bits = __float_as_uint(vs);
-        mt.lv = (float)((int)(bits >> 23) - 127) +
-                log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
-        mt.inv_vs = 1.f / vs;
+        const SliceMeta mt = slice_meta(row, ks, vs);
         for (int q = 0; q < n_q; ++q) {
           if (!wait_empty()) {
             ok = false;
@@ -723,24 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t out_at = ((size_t)w.b * p.Hq + (size_t)w.kvh * g) * kD;
       for (int i = tid; i < g * (kD / 4); i += kConsumers) {
         const int h = i / (kD / 4), d = (i % (kD / 4)) * 4;
-        float2 ml[kWarps];
-        float M = kMInit, ls = 0.f;
-#pragma unroll
-        for (int ww = 0; ww < kWarps; ++ww) {
-          ml[ww] = *reinterpret_cast<const float2*>(merge_ml + (ww * g + h) * 2);
-          M = fmaxf(M, ml[ww].x);
-        }
-        float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int ww = 0; ww < kWarps; ++ww) {
-          const float e = ex2(ml[ww].x - M);
-          const float4 x = *reinterpret_cast<const float4*>(merge_o + merge_row(ww, h, g) + d);
-          ls = fmaf(ml[ww].y, e, ls);
-          os.x = fmaf(x.x, e, os.x);
-          os.y = fmaf(x.y, e, os.y);
-          os.z = fmaf(x.z, e, os.z);
-          os.w = fmaf(x.w, e, os.w);
-        }
+        float M, ls;
+        float4 os;
+        merge_warps8(merge_o, merge_ml, i, g, M, ls, os);
         if (whole) {
           const float inv = ls == 0.f ? 0.f : 1.f / ls;
           *reinterpret_cast<uint2*>(p.out + out_at + (size_t)i * 4) = make_uint2(
@@ -790,19 +810,104 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+}  // namespace
+}  // namespace gqa
+
+#include "kv8_cluster.cuh"
+
+namespace gqa {
+namespace {
+
 // ------------------------------------------------------------------ host --
 
-int num_sms() {
-  static std::atomic<int> known[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-  int n = known[dev].load();
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-      n = 148;
-    known[dev].store(n);
+// Per device, found once: its SMs and how many clusters of each size can run
+// at once with one CTA to an SM (a cluster stays within one GPC).
+struct Device8 {
+  int sms;
+  int clusters[kMaxCluster + 1];
+};
+
+template <int NT, bool LIST>
+cudaError_t set_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(
+      kv8_decode_kernel<NT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kv8_cluster_kernel<NT, LIST>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kv8_cluster_kernel<NT, LIST>,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e;
+}
+
+cudaError_t find_device(Device8& d, int dev) {
+  cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = set_attributes<1, false>();
+  if (e == cudaSuccess) e = set_attributes<1, true>();
+  if (e == cudaSuccess) e = set_attributes<2, false>();
+  if (e == cudaSuccess) e = set_attributes<2, true>();
+  if (e != cudaSuccess) return e;
+  for (int c = 1; c <= kMaxCluster; ++c) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c * 64);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kMaxSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&d.clusters[c], kv8_cluster_kernel<1, false>, &cfg) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      d.clusters[c] = 0;
+    }
   }
-  return n;
+  return cudaSuccess;
+}
+
+cudaError_t device8(const Device8** out) {
+  static Device8 known[64];
+  static std::atomic<bool> ready[64];
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+  if (e != cudaSuccess) return e;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev].load(std::memory_order_relaxed)) {
+      e = find_device(known[dev], dev);
+      if (e != cudaSuccess) return e;
+      ready[dev].store(true, std::memory_order_release);
+    }
+  }
+  *out = &known[dev];
+  return cudaSuccess;
+}
+
+// CTAs per segment in cluster mode, or 0 for the split over a flat list.  A
+// cluster for every segment, all resident at once and of at least 8 CTAs
+// where there are tiles for them; with several sequences, whose lengths may
+// differ, only while the longest possible one leaves a CTA no more than
+// kClusterTiles tiles: beyond that an even split is worth more than the
+// latency saved.
+constexpr int kClusterTiles = 8;
+int cluster_size8(const Kv8Params& p, const Device8& d) {
+  if (g_decode_test_cluster >= 0)  // schedule tests only
+    return min(g_decode_test_cluster, kMaxCluster);
+  const long long nseg = (long long)p.B * p.Hkv;
+  const long long rows = p.index ? (long long)p.count << p.lb : (long long)p.L;
+  const int tiles = (int)((rows + kTile - 1) / kTile);
+  const int want = min(kMaxCluster, tiles);
+  for (int c = want; c >= min(8, want); --c)
+    if (nseg <= d.clusters[c]) {
+      if (p.B > 1 && (tiles + c - 1) / c > kClusterTiles) return 0;
+      return c;
+    }
+  return 0;
 }
 
 // A cache [segs, L, 128] of codes as a 3-D tensor map, box 128 codes x rows x
@@ -823,14 +928,34 @@ bool codes_map(CUtensorMap* m, const void* ptr, int L, long long segs, int rows)
 template <int NT, bool LIST>
 cudaError_t launch8(Kv8Params& p, const CUtensorMap& mk, const CUtensorMap& mv,
                     cudaStream_t stream) {
-  p.stages = kMaxStages;
-  while (p.stages > 2 && smem_bytes(p.stages, p.B, p.g) > (size_t)kMaxSmem) --p.stages;
-  const size_t smem = smem_bytes(p.stages, p.B, p.g);
-  const cudaError_t e = cudaFuncSetAttribute(
-      kv8_decode_kernel<NT, LIST>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  const Device8* d = nullptr;
+  cudaError_t e = device8(&d);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv8_decode_kernel<NT, LIST>, dim3(min(kKv8MaxGrid, num_sms())),
-                    dim3(kThreads), smem, stream, mk, mv, p);
+  p.stages = kMaxStages;
+  const int C = cluster_size8(p, *d);
+  if (C > 0) {
+    if (d->clusters[C] == 0) return cudaErrorNotSupported;
+    while (p.stages > 2 && cluster_smem_bytes(p.stages, p.g, C) > (size_t)kMaxSmem) --p.stages;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * C));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = cluster_smem_bytes(p.stages, p.g, C);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kv8_cluster_kernel<NT, LIST>, mk, mv, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+  while (p.stages > 2 && smem_bytes(p.stages, p.B, p.g) > (size_t)kMaxSmem) --p.stages;
+  return launch_pdl(kv8_decode_kernel<NT, LIST>, dim3(min(kKv8MaxGrid, d->sms)), dim3(kThreads),
+                    smem_bytes(p.stages, p.B, p.g), stream, mk, mv, p);
 }
 
 }  // namespace

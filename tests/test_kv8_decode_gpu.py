@@ -229,3 +229,55 @@ def test_nan_in_attended_rows_reaches_the_output():
     torch.cuda.synchronize()
     assert torch.isnan(out[0, :2, 9]).all() and torch.isfinite(out[0, :2, :9]).all()
     assert torch.isfinite(out[0, 2]).all() and torch.isnan(out[0, 3]).all()
+
+
+@pytest.mark.parametrize("cluster", [0, 1, 3, 8, 16])
+@pytest.mark.parametrize("g", [2, 5, 16])
+def test_every_way_of_splitting(cluster, g):
+    """The flat list (0) and clusters of each size, with more and with fewer CTAs than a segment
+    has tiles, and a sequence at a bad position among them."""
+    L, block = 3100, 32
+    pos = [3099, 0, -1, 700, 129]
+    st = _case(5, 2, g, L, block, pos, seed=49)
+    gen = torch.Generator().manual_seed(50)
+    index = torch.randint(-1, 97, (5, 2, 21), generator=gen).int()
+    ws = ga.kv8_workspace(5, 2 * g, 2, L, D)
+    ga.attn_test_force_schedule(cluster)
+    try:
+        for _ in range(3):
+            dense = _run(st, block, workspace=ws)
+            listed = _run_blocks(st, block, index.cuda(), workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        ga.attn_test_force_schedule(-1)
+    assert ga.attn_read_device_status(ws) == ga.ATTN_DEV_BAD_POSITION
+    assert torch.isnan(dense[2]).all() and torch.isnan(listed[2]).all()
+    good = [0, 1, 3, 4]
+    _check(dense, st, L, block, pos, seqs=good, what=f"cluster {cluster}")
+    _check(listed, st, L, block, pos, index=index.tolist(), seqs=good, what=f"cluster {cluster}")
+
+
+@pytest.mark.parametrize("cluster", [0, 8])
+@pytest.mark.parametrize("listed", [False, True])
+def test_a_wait_that_runs_out_is_reported(cluster, listed):
+    """A tile that never comes (its copy is not issued): the waits give up, the status says so,
+    and the context and a zeroed workspace go on working."""
+    pos = [2000]
+    st = _case(1, 1, 4, 2001, 64, pos, seed=51)
+    index = torch.arange(32, dtype=torch.int32, device="cuda")[None, None].contiguous()
+    run = (lambda **kw: _run_blocks(st, 64, index, **kw)) if listed else \
+        (lambda **kw: _run(st, 64, **kw))
+    ws = ga.kv8_workspace(1, 4, 1, 2001, D)
+    ga.attn_test_force_schedule(cluster)
+    ga.attn_test_skip_tile(3)
+    try:
+        run(workspace=ws)
+        bits = ga.attn_read_device_status(ws)
+    finally:
+        ga.attn_test_skip_tile(-1)
+        ga.attn_test_force_schedule(-1)
+    assert bits & ga.ATTN_DEV_TIMEOUT
+    ws.zero_()
+    _check(run(workspace=ws), st, 2001, 64, pos,
+           index=index.cpu().tolist() if listed else None)
+    assert ga.attn_read_device_status(ws) == 0
