@@ -13,9 +13,12 @@
 // `recent` last ones, and of the others the best-scored, ties to the lowest
 // index.  Scores become order-preserving integer keys; the need-th largest is
 // found digit by digit from the top (12, 12 and 8 bits: a histogram in shared
-// memory and a scan over its bins each), with the keys in registers, and most
-// often the first or second digit already settles it.  Then one scan over
-// (round, warp) counts places the chosen indices in ascending order.  The
+// memory and a scan over its bins each), with the keys in registers; most
+// often the bin of the first digit is small, and its few keys are ranked among
+// themselves.  Then one scan over (round, warp) counts places the chosen
+// indices in ascending order.  Bound by its instructions (512 rows of up to
+// 8192 scores: 36 us with one bit a round, 20 us with three digits a row,
+// SELECT_NOW us this way).  The
 // first digit holds sign, exponent and three bits of the mantissa, so that
 // scores of one size still spread over many bins (the histogram's atomics
 // contend only where scores are alike).
@@ -109,6 +112,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 4096;
+constexpr int kListed = 256;  // a bin this small is ranked directly
 
 // Order-preserving key of a score: larger score, larger key; -0 = +0; NaN is
 // taken as -inf.
@@ -145,14 +149,17 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
     const float* __restrict__ scores, const int32_t* __restrict__ positions, int32_t* out,
     int Hkv, int L, int block, int nb, int count, int first, int recent) {
   constexpr int kChunk = I * kSelectThreads;
+  constexpr int kCells = I * kSelectWarps;
   __shared__ __align__(16) int hist[kBins];
   __shared__ uint32_t slots[2][32];
-  __shared__ int rounds[2][I * kSelectWarps];
-  __shared__ int found[3];
+  __shared__ int cells[kCells];
+  __shared__ int found[4];
   grid_dependency_wait();
   grid_dependents_launch();
   const int seg = blockIdx.x, b = seg / Hkv, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < kBins / 4; i += kSelectThreads)
+    reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
   const int pos = positions[b];
   const int n = rows_in_cache(pos, 0, L) ? pos / block + 1 : 0;
   int32_t* o = out + (size_t)seg * count;
@@ -162,29 +169,29 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
   }
   const float* sc = scores + (size_t)seg * nb;
   const int need = count - first - recent;  // of the blocks first .. n-recent-1
+  const int lo = first, hi = n - recent;
   uint32_t key[I];
   auto load = [&](int at) {  // the keys of the chunk at item `at`; 0 (below every key): no candidate
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int j = at + i * kSelectThreads + tid;
       key[i] = 0u;
-      if (at + i * kSelectThreads >= n) continue;  // (the whole block)
-      key[i] = j >= first && j < n - recent ? score_key(sc[j]) : 0u;
+      if (at + i * kSelectThreads < n && j >= lo && j < hi) key[i] = score_key(sc[j]);
     }
   };
   int phase = 0;
-  uint32_t th = 0;   // all keys above th are chosen,
-  int tie_room = 0;  // and the first tie_room of those equal to it
-  bool all_ties = true;  // ... which are all of them
+  uint32_t th = 0, mask = 0;  // keys above every key with (key & mask) == th are chosen,
+  int left = need;            // and `left` of those in that bin: the largest, the lowest indices
+  bool whole = true;          // ... which are all of them
+  bool listed = false;        // ... which are ranked in a list
   if (need > 0) {
     if (!LOOP) load(0);
-    int left = need;
-    uint32_t mask = 0;  // bits of th settled so far
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 20 : pass == 1 ? 8 : 0;
       const uint32_t digits = pass == 2 ? 0xffu : 0xfffu;
-      for (int i = tid; i < kBins / 4; i += kSelectThreads)
-        reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+      if (pass > 0)
+        for (int i = tid; i < kBins / 4; i += kSelectThreads)
+          reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
       __syncthreads();
       for (int at = 0; at < (LOOP ? n : 1); at += kChunk) {
         if (LOOP) load(at);
@@ -194,23 +201,24 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
             atomicAdd(&hist[(key[i] >> shift) & digits], 1);
       }
       __syncthreads();
-      // the digit of the left-th largest: thread t holds bins from the top
+      // the digit of the left-th largest: thread t holds 8 bins from the top
       constexpr int kPer = kBins / kSelectThreads;
+      static_assert(kPer == 8, "two int4 per thread");
       int c[kPer], sum = 0, all;
       const int top = kBins - 1 - tid * kPer;
+      *reinterpret_cast<int4*>(c) = *reinterpret_cast<const int4*>(&hist[top - 7]);
+      *reinterpret_cast<int4*>(c + 4) = *reinterpret_cast<const int4*>(&hist[top - 3]);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        c[i] = hist[top - i];
-        sum += c[i];
-      }
+      for (int i = 0; i < kPer; ++i) sum += c[i];
       int before = block_scan(sum, slots, phase, &all);
       if (before < left && before + sum >= left) {  // one thread
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = kPer - 1; i >= 0; --i) {
           if (before < left && before + c[i] >= left) {
-            found[0] = top - i;
+            found[0] = top - 7 + i;
             found[1] = left - before;
             found[2] = c[i];
+            found[3] = 0;  // the list's length
           }
           before += c[i];
         }
@@ -219,86 +227,113 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
       th |= (uint32_t)found[0] << shift;
       mask |= digits << shift;
       left = found[1];
-      all_ties = found[2] == left;
-      if (all_ties) break;  // every key of the bin is chosen: the lower bits do not matter
-      // (found is written again only after another barrier)
+      const int in_bin = found[2];
+      whole = in_bin == left;
+      if (whole) break;
+      if (!LOOP && in_bin <= kListed) {  // few: rank them among themselves
+        listed = true;
+        break;
+      }
     }
-    tie_room = left;
+  }
+  // The bin's keys and indices, in any order, then each one's rank among them
+  // (a larger key first, then a lower index): chosen if below `left`.  The
+  // list takes the histogram's place; a thread keeps its item's place in it
+  // where the key was.
+  uint2* list = reinterpret_cast<uint2*>(hist);  // [kListed]
+  int* chosen = hist + 2 * kListed;              // [kListed]
+  uint32_t in_list = 0;                          // bit i: the key of round i is a place
+  if (listed) {
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+      if (i * kSelectThreads < n && key[i] != 0u && (key[i] & mask) == th) {
+        const int k = atomicAdd(&found[3], 1);
+        list[k] = make_uint2(key[i], (uint32_t)(i * kSelectThreads + tid));
+        key[i] = (uint32_t)k;
+        in_list |= 1u << i;
+      }
+    __syncthreads();
+    const int m = found[3];
+    if (tid < m) {
+      const uint2 me = list[tid];
+      int rank = 0;
+#pragma unroll 4
+      for (int x = 0; x < m; ++x) {
+        const uint2 other = list[x];
+        rank += other.x > me.x || (other.x == me.x && other.y < me.y);
+      }
+      chosen[tid] = rank < left;
+    }
+    __syncthreads();
   }
   // Place the chosen indices in ascending order: per round and warp a count,
   // one scan over them, then each lane's rank within its warp.
   int base = 0, tie_base = 0;
+  const uint32_t all_of_bin = th | ~mask;  // the bin's largest possible key
   for (int at = 0; at < n; at += kChunk) {
     if (LOOP && need > 0) load(at);
     uint32_t take = 0;  // bit i: item of round i
-    if (need > 0 && !all_ties) {  // ties in part: their ranks first
+    // a partly chosen bin that went into no list holds one key alone (all three
+    // digits): its lowest indices, by a scan of their own
+    const bool ties = need > 0 && !whole && !listed;
+    auto scan_cells = [&](int from) -> int {  // exclusive, in place; the total
+      int v[(kCells + kSelectThreads - 1) / kSelectThreads], sum = 0, all;
+      constexpr int kPer = (kCells + kSelectThreads - 1) / kSelectThreads;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        v[k] = tid * kPer + k < kCells ? cells[tid * kPer + k] : 0;
+        sum += v[k];
+      }
+      int run = block_scan(sum, slots, phase, &all) + from;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (tid * kPer + k < kCells) cells[tid * kPer + k] = run;
+        run += v[k];
+      }
+      __syncthreads();
+      return all;
+    };
+    if (ties) {
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         const uint32_t t = __ballot_sync(0xffffffffu, key[i] == th);
-        if (lane == 0) rounds[0][i * kSelectWarps + warp] = __popc(t);
+        if (lane == 0) cells[i * kSelectWarps + warp] = __popc(t);
       }
       __syncthreads();
-      int all;
-      constexpr int kCells = I * kSelectWarps, kCellPer = (kCells + kSelectThreads - 1) / kSelectThreads;
-      int v = 0;
-#pragma unroll
-      for (int k = 0; k < kCellPer; ++k)
-        if (tid * kCellPer + k < kCells) v += rounds[0][tid * kCellPer + k];
-      int run = block_scan(v, slots, phase, &all) + tie_base;
-#pragma unroll
-      for (int k = 0; k < kCellPer; ++k)
-        if (tid * kCellPer + k < kCells) {
-          const int x = rounds[0][tid * kCellPer + k];
-          rounds[0][tid * kCellPer + k] = run;
-          run += x;
-        }
-      __syncthreads();
+      const int all = scan_cells(tie_base);
       tie_base += all;
 #pragma unroll
       for (int i = 0; i < I; ++i) {
         const uint32_t t = __ballot_sync(0xffffffffu, key[i] == th);
-        const int rank = rounds[0][i * kSelectWarps + warp] + __popc(t & ((1u << lane) - 1u));
-        if (key[i] > th || (key[i] == th && rank < tie_room)) take |= 1u << i;
+        const int rank = cells[i * kSelectWarps + warp] + __popc(t & ((1u << lane) - 1u));
+        if (key[i] > th || (key[i] == th && rank < left)) take |= 1u << i;
       }
+      __syncthreads();
     } else if (need > 0) {
+      const uint32_t above = listed ? all_of_bin : th - 1u;  // (th > 0: a key is never 0)
 #pragma unroll
       for (int i = 0; i < I; ++i)
-        if (key[i] >= th) take |= 1u << i;
+        if (((in_list >> i) & 1u) ? chosen[key[i]] != 0 : key[i] > above) take |= 1u << i;
     }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int j = at + i * kSelectThreads + tid;
-      if (at + i * kSelectThreads >= n) {
-        if (lane == 0) rounds[1][i * kSelectWarps + warp] = 0;
-        continue;
+      uint32_t t = 0;
+      if (at + i * kSelectThreads < n) {
+        if (j < lo || (j >= hi && j < n)) take |= 1u << i;
+        t = __ballot_sync(0xffffffffu, (take >> i) & 1u);
       }
-      if (j < first || (j >= n - recent && j < n)) take |= 1u << i;
-      const uint32_t t = __ballot_sync(0xffffffffu, (take >> i) & 1u);
-      if (lane == 0) rounds[1][i * kSelectWarps + warp] = __popc(t);
+      if (lane == 0) cells[i * kSelectWarps + warp] = __popc(t);
     }
     __syncthreads();
-    int all;
-    constexpr int kCells = I * kSelectWarps, kCellPer = (kCells + kSelectThreads - 1) / kSelectThreads;
-    int v = 0;
-#pragma unroll
-    for (int k = 0; k < kCellPer; ++k)
-      if (tid * kCellPer + k < kCells) v += rounds[1][tid * kCellPer + k];
-    int run = block_scan(v, slots, phase, &all) + base;
-#pragma unroll
-    for (int k = 0; k < kCellPer; ++k)
-      if (tid * kCellPer + k < kCells) {
-        const int x = rounds[1][tid * kCellPer + k];
-        rounds[1][tid * kCellPer + k] = run;
-        run += x;
-      }
-    __syncthreads();
+    const int all = scan_cells(base);
     base += all;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       if (at + i * kSelectThreads >= n) continue;
       const uint32_t t = __ballot_sync(0xffffffffu, (take >> i) & 1u);
       if ((take >> i) & 1u)
-        o[rounds[1][i * kSelectWarps + warp] + __popc(t & ((1u << lane) - 1u))] =
+        o[cells[i * kSelectWarps + warp] + __popc(t & ((1u << lane) - 1u))] =
             at + i * kSelectThreads + tid;
     }
     if (LOOP) __syncthreads();  // the cells may be written again

@@ -38,6 +38,25 @@ __device__ __forceinline__ uint32_t finite_abs_max(uint32_t w) {
   return max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u);
 }
 
+// 8 codes moved to another scale: code <- e4m3(code * ratio).
+__device__ __forceinline__ uint2 rescale8(uint2 w, float ratio) {
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2(((k & 2) ? w.y : w.x) >> ((k & 1) * 16)));
+    o[k] = f32x2_to_e4m3x2(f.x * ratio, f.y * ratio);
+  }
+  return make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+}
+// 8 bf16 to codes: e4m3(x * inv).
+__device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
+  const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = f32x2_to_e4m3x2(bf16lo(w4[k]) * inv, bf16hi(w4[k]) * inv);
+  return make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+}
+
 template <int P>  // passes of 16 rows: block = 16 * P
 __global__ void __launch_bounds__(256) kv8_append_kernel(
     const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
@@ -133,28 +152,14 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
       const float ratio = s_old[op] * inv;
       for (int r = row0 + (tid >> 4); r < pos; r += 16) {
         uint2* at = reinterpret_cast<uint2*>(cache + (size_t)r * kD8 + c * 8);
-        uint2 w = *at;
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f =
-              f16x2_to_f32x2(e4m3x2_to_f16x2(((k & 2) ? w.y : w.x) >> ((k & 1) * 16)));
-          o[k] = f32x2_to_e4m3x2(f.x * ratio, f.y * ratio);
-        }
-        *at = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+        *at = rescale8(*at, ratio);
       }
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int t = t0 + i * 16;
       if (t >= 0 && t < S) {
-        const uint32_t w4[4] = {x[op][i].x, x[op][i].y, x[op][i].z, x[op][i].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          o[k] = f32x2_to_e4m3x2(bf16lo(w4[k]) * inv, bf16hi(w4[k]) * inv);
-        *reinterpret_cast<uint2*>(cache + (size_t)(t + pos) * kD8 + c * 8) =
-            make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+        *reinterpret_cast<uint2*>(cache + (size_t)(t + pos) * kD8 + c * 8) = encode8(x[op][i], inv);
       }
     }
   }
@@ -169,6 +174,69 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
   }
 }
 
+// One new token per sequence: a warp per (sequence, KV head), its lower half
+// the key and its upper half the value (16 bytes a lane), no block barrier.
+// The new rows go out before the position is read.  (64 sequences, 8 heads:
+// 5.2 us by the kernel above, APPEND_NOW us by this one.)
+constexpr int kTokenWarps = 4;
+__global__ void __launch_bounds__(kTokenWarps * 32) kv8_append_token_kernel(
+    const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
+    const int32_t* __restrict__ positions, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
+    float* v_scale, uint4* k_bounds, int segs, int Hkv, int L, int nb, int lb) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int seg = blockIdx.x * kTokenWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (seg >= segs) return;
+  const int c = lane & 15;
+  const bool op = lane >= 16;  // the value's half
+  const uint4 x = (op ? v_new : k_new)[(size_t)seg * 16 + c];
+  const int pos = positions[seg / Hkv];
+  if (!rows_in_cache(pos, 0, L)) return;  // reported by the decode call
+  const int j = pos >> lb, row0 = j << lb;
+  const bool had = row0 < pos;
+  float* scale = (op ? v_scale : k_scale) + (size_t)seg * nb + j;
+  const float s_old = had ? *scale : 0.f;
+  uint4* bound = k_bounds + ((size_t)seg * nb + j) * 32 + lane;  // lower half: maxima, upper: minima
+  uint4 was = make_uint4(0u, 0u, 0u, 0u);
+  if (k_bounds != nullptr && had) was = *bound;
+
+  uint32_t amax = max(max(finite_abs_max(x.x), finite_abs_max(x.y)),
+                      max(finite_abs_max(x.z), finite_abs_max(x.w)));
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  const float s_new = block_scale(__uint_as_float(amax << 16));
+  const float s = had ? fmaxf(s_old, s_new) : s_new;
+  __syncwarp();  // every lane's read of s_old comes before the write
+  if (c == 0) *scale = s;
+  const float inv = 1.f / s;
+  uint8_t* cache = (op ? v_cache : k_cache) + (size_t)seg * L * kD8 + c * 8;
+  if (had && s > s_old) {  // the block's scale grew: move the older rows
+    const float ratio = s_old * inv;
+#pragma unroll 4
+    for (int r = row0; r < pos; ++r) {
+      uint2* at = reinterpret_cast<uint2*>(cache + (size_t)r * kD8);
+      *at = rescale8(*at, ratio);
+    }
+  }
+  *reinterpret_cast<uint2*>(cache + (size_t)pos * kD8) = encode8(x, inv);
+  if (k_bounds != nullptr) {
+    uint4 k = x;  // the key's dims, for both halves
+    k.x = __shfl_sync(0xffffffffu, x.x, c);
+    k.y = __shfl_sync(0xffffffffu, x.y, c);
+    k.z = __shfl_sync(0xffffffffu, x.z, c);
+    k.w = __shfl_sync(0xffffffffu, x.w, c);
+    // a NaN leaves the bound as it is, and a first NaN the identity
+    const uint32_t id = op ? 0x7f807f80u : 0xff80ff80u;
+    if (!had) was = make_uint4(id, id, id, id);
+    uint4 m;
+    m.x = op ? bf16x2_min(k.x, was.x) : bf16x2_max(k.x, was.x);
+    m.y = op ? bf16x2_min(k.y, was.y) : bf16x2_max(k.y, was.y);
+    m.z = op ? bf16x2_min(k.z, was.z) : bf16x2_max(k.z, was.z);
+    m.w = op ? bf16x2_min(k.w, was.w) : bf16x2_max(k.w, was.w);
+    *bound = m;
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_kv8_append(const void* k_new, const void* v_new, const int32_t* positions,
@@ -176,6 +244,15 @@ cudaError_t launch_kv8_append(const void* k_new, const void* v_new, const int32_
                               void* k_bounds, int B, int S, int Hkv, int L, int block,
                               cudaStream_t stream) {
   const int nb = (L + block - 1) / block;
+  if (S == 1) {
+    const int segs = B * Hkv;
+    const int lb = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+    return launch_pdl(kv8_append_token_kernel, dim3((segs + kTokenWarps - 1) / kTokenWarps),
+                      dim3(kTokenWarps * 32), 0, stream, static_cast<const uint4*>(k_new),
+                      static_cast<const uint4*>(v_new), positions,
+                      static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale,
+                      v_scale, static_cast<uint4*>(k_bounds), segs, Hkv, L, nb, lb);
+  }
   const int touched = min(nb, (S + block - 2) / block + 1);
   auto kernel = block == 16   ? kv8_append_kernel<1>
                 : block == 32 ? kv8_append_kernel<2>
