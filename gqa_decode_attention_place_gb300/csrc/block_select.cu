@@ -15,10 +15,10 @@
 // found digit by digit from the top (12, 12 and 8 bits: a histogram in shared
 // memory and a scan over its bins each), with the keys in registers; most
 // often the bin of the first digit is small, and its few keys are ranked among
-// themselves.  Then one scan over (round, warp) counts places the chosen
-// indices in ascending order.  Bound by its instructions (512 rows of up to
+// themselves.  Each thread holds items in a row, so one scan over the threads'
+// counts places the chosen indices in ascending order.  Bound by its instructions (512 rows of up to
 // 8192 scores: 36 us with one bit a round, 20 us with three digits a row,
-// SELECT_NOW us this way).  The
+// 15.4 us this way).  The
 // first digit holds sign, exponent and three bits of the mantissa, so that
 // scores of one size still spread over many bins (the histogram's atomics
 // contend only where scores are alike).
@@ -29,7 +29,7 @@
 namespace gqa {
 namespace {
 
-constexpr int kScoreWarps = 8;
+constexpr int kScoreWarps = 4;  // (8: 26.6 us for 142 MB, 4: 23.7)
 constexpr int kScoreThreads = kScoreWarps * 32;
 constexpr int kScoreBlocksPerWarp = 16;
 constexpr int kScoreBlocksPerCta = kScoreWarps * kScoreBlocksPerWarp;
@@ -75,18 +75,19 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(
     ua[i] = j0 + c < n ? row[c * 32] : make_uint4(0u, 0u, 0u, 0u);
     ub[i] = j0 + c + 8 < n ? row[(c + 8) * 32] : make_uint4(0u, 0u, 0u, 0u);
   }
-  {  // element tid of the vector: dims of q+ summed over the heads, then of q-
-    const uint16_t* src = q + (size_t)seg * g * kDecodeD + (tid & (kDecodeD - 1));
+  // the vector: dims of q+ summed over the heads, then of q-
+  for (int e = tid; e < 2 * kDecodeD; e += kScoreThreads) {
+    const uint16_t* src = q + (size_t)seg * g * kDecodeD + (e & (kDecodeD - 1));
     float w = 0.f;
 #pragma unroll 4
     for (int h = 0; h < g; ++h) {
       const float x = __uint_as_float((uint32_t)src[h * kDecodeD] << 16);
-      w += tid < kDecodeD ? fmaxf(x, 0.f) : fminf(x, 0.f);
+      w += e < kDecodeD ? fmaxf(x, 0.f) : fminf(x, 0.f);
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       const uint32_t r = pack_bf16x2(w, 0.f);
-      parts[k][tid] = (uint16_t)r;
+      parts[k][e] = (uint16_t)r;
       w -= bf16lo(r);
     }
   }
@@ -113,14 +114,13 @@ constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 4096;
 constexpr int kListed = 256;  // a bin this small is ranked directly
+static_assert(kSelectThreads == 2 * kListed, "two threads to a listed key");
 
-// Order-preserving key of a score: larger score, larger key; -0 = +0; NaN is
-// taken as -inf.
+// Order-preserving key of a score: larger score, larger key, never 0; -0 is
+// +0, NaN is taken as -inf (fmaxf drops it).
 __device__ __forceinline__ uint32_t score_key(float x) {
-  if (x != x) x = -INFINITY;
-  x += 0.f;  // -0 -> +0
-  const uint32_t u = __float_as_uint(x);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t u = __float_as_uint(fmaxf(x, -INFINITY) + 0.f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 // Exclusive prefix sum of v over the block's threads; *all = the total.  One
@@ -141,25 +141,26 @@ __device__ __forceinline__ int block_scan(int v, uint32_t (*slots)[32], int& pha
   return (int)__reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + x - v;
 }
 
-// Items are dealt out to the threads in rounds (item r*kSelectThreads + tid in
-// round r), I rounds to a chunk.  LOOP: more than one chunk, whose scores are
-// read again in every pass; else the keys stay in registers.
+// Thread t holds I items in a row of each chunk of I * kSelectThreads; LOOP:
+// more than one chunk, whose scores are read again in every pass; else the
+// keys stay in registers.
 template <int I, bool LOOP>
-__global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
+__global__ void __launch_bounds__(kSelectThreads, 3) block_select_kernel(
     const float* __restrict__ scores, const int32_t* __restrict__ positions, int32_t* out,
     int Hkv, int L, int block, int nb, int count, int first, int recent) {
+  static_assert(I % 4 == 0, "scores come in fours");
   constexpr int kChunk = I * kSelectThreads;
-  constexpr int kCells = I * kSelectWarps;
   __shared__ __align__(16) int hist[kBins];
   __shared__ uint32_t slots[2][32];
-  __shared__ int cells[kCells];
   __shared__ int found[4];
   grid_dependency_wait();
   grid_dependents_launch();
   const int seg = blockIdx.x, b = seg / Hkv, tid = threadIdx.x;
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < kBins / 4; i += kSelectThreads)
-    reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+  auto clear = [&]() {
+    for (int i = tid; i < kBins / 4; i += kSelectThreads)
+      reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+  };
+  clear();
   const int pos = positions[b];
   const int n = rows_in_cache(pos, 0, L) ? pos / block + 1 : 0;
   int32_t* o = out + (size_t)seg * count;
@@ -168,15 +169,27 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
     return;
   }
   const float* sc = scores + (size_t)seg * nb;
-  const int need = count - first - recent;  // of the blocks first .. n-recent-1
+  const int need = count - first - recent;  // of the blocks lo .. hi-1
   const int lo = first, hi = n - recent;
+  // items are shifted so that their groups of four start on 16 bytes
+  const int shift4 = (int)((reinterpret_cast<uintptr_t>(sc) >> 2) & 3);
+  const int j0 = tid * I - shift4;  // this thread's first item of chunk 0
   uint32_t key[I];
   auto load = [&](int at) {  // the keys of the chunk at item `at`; 0 (below every key): no candidate
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const int j = at + i * kSelectThreads + tid;
-      key[i] = 0u;
-      if (at + i * kSelectThreads < n && j >= lo && j < hi) key[i] = score_key(sc[j]);
+    for (int g = 0; g < I; g += 4) {
+      const int j = at + j0 + g;
+      if (j >= lo && j + 4 <= hi) {
+        const float4 x = *reinterpret_cast<const float4*>(sc + j);
+        key[g] = score_key(x.x);
+        key[g + 1] = score_key(x.y);
+        key[g + 2] = score_key(x.z);
+        key[g + 3] = score_key(x.w);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          key[g + k] = j + k >= lo && j + k < hi ? score_key(sc[j + k]) : 0u;
+      }
     }
   };
   int phase = 0;
@@ -189,16 +202,13 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 20 : pass == 1 ? 8 : 0;
       const uint32_t digits = pass == 2 ? 0xffu : 0xfffu;
-      if (pass > 0)
-        for (int i = tid; i < kBins / 4; i += kSelectThreads)
-          reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+      if (pass > 0) clear();
       __syncthreads();
-      for (int at = 0; at < (LOOP ? n : 1); at += kChunk) {
+      for (int at = 0; at < (LOOP ? n + 3 : 1); at += kChunk) {
         if (LOOP) load(at);
 #pragma unroll
         for (int i = 0; i < I; ++i)
-          if (at + i * kSelectThreads < n && key[i] != 0u && (key[i] & mask) == th)
-            atomicAdd(&hist[(key[i] >> shift) & digits], 1);
+          if (key[i] != 0u && (key[i] & mask) == th) atomicAdd(&hist[(key[i] >> shift) & digits], 1);
       }
       __syncthreads();
       // the digit of the left-th largest: thread t holds 8 bins from the top
@@ -236,107 +246,79 @@ __global__ void __launch_bounds__(kSelectThreads) block_select_kernel(
       }
     }
   }
-  // The bin's keys and indices, in any order, then each one's rank among them
-  // (a larger key first, then a lower index): chosen if below `left`.  The
-  // list takes the histogram's place; a thread keeps its item's place in it
-  // where the key was.
-  uint2* list = reinterpret_cast<uint2*>(hist);  // [kListed]
-  int* chosen = hist + 2 * kListed;              // [kListed]
-  uint32_t in_list = 0;                          // bit i: the key of round i is a place
+  const uint32_t bin_top = th | ~mask;  // the bin's largest possible key
+  // The bin's keys and indices as one number (a larger key first, then a lower
+  // index), in any order, and each one's rank among them: chosen if below
+  // `left`.  The list takes the histogram's place; a thread keeps its item's
+  // place in it where the key was.
+  unsigned long long* list = reinterpret_cast<unsigned long long*>(hist);  // [kListed]
+  int* rank_of = hist + 2 * kListed;                                       // [kListed]
+  uint32_t in_list = 0;  // bit i: key[i] is a place
   if (listed) {
 #pragma unroll
     for (int i = 0; i < I; ++i)
-      if (i * kSelectThreads < n && key[i] != 0u && (key[i] & mask) == th) {
+      if (key[i] >= th && key[i] <= bin_top) {
         const int k = atomicAdd(&found[3], 1);
-        list[k] = make_uint2(key[i], (uint32_t)(i * kSelectThreads + tid));
+        list[k] = ((unsigned long long)key[i] << 32) | (uint32_t)~(j0 + i);
         key[i] = (uint32_t)k;
         in_list |= 1u << i;
       }
+    if (tid < kListed) rank_of[tid] = 0;
     __syncthreads();
     const int m = found[3];
-    if (tid < m) {
-      const uint2 me = list[tid];
+    // two threads to a key, or four if that covers the list
+    const int parts = m <= kSelectThreads / 4 ? 4 : 2;
+    const int k = tid & (kSelectThreads / parts - 1), part = tid / (kSelectThreads / parts);
+    if (k < m) {
+      const unsigned long long me = list[k];
       int rank = 0;
 #pragma unroll 4
-      for (int x = 0; x < m; ++x) {
-        const uint2 other = list[x];
-        rank += other.x > me.x || (other.x == me.x && other.y < me.y);
-      }
-      chosen[tid] = rank < left;
+      for (int x = part; x < m; x += parts) rank += list[x] > me;
+      atomicAdd(&rank_of[k], rank);
     }
     __syncthreads();
   }
-  // Place the chosen indices in ascending order: per round and warp a count,
-  // one scan over them, then each lane's rank within its warp.
+  // Place the chosen indices in ascending order: a count per thread, a scan.
   int base = 0, tie_base = 0;
-  const uint32_t all_of_bin = th | ~mask;  // the bin's largest possible key
-  for (int at = 0; at < n; at += kChunk) {
+  for (int at = 0; at < n + 3; at += kChunk) {
     if (LOOP && need > 0) load(at);
-    uint32_t take = 0;  // bit i: item of round i
-    // a partly chosen bin that went into no list holds one key alone (all three
-    // digits): its lowest indices, by a scan of their own
-    const bool ties = need > 0 && !whole && !listed;
-    auto scan_cells = [&](int from) -> int {  // exclusive, in place; the total
-      int v[(kCells + kSelectThreads - 1) / kSelectThreads], sum = 0, all;
-      constexpr int kPer = (kCells + kSelectThreads - 1) / kSelectThreads;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        v[k] = tid * kPer + k < kCells ? cells[tid * kPer + k] : 0;
-        sum += v[k];
-      }
-      int run = block_scan(sum, slots, phase, &all) + from;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        if (tid * kPer + k < kCells) cells[tid * kPer + k] = run;
-        run += v[k];
-      }
-      __syncthreads();
-      return all;
-    };
-    if (ties) {
-#pragma unroll
-      for (int i = 0; i < I; ++i) {
-        const uint32_t t = __ballot_sync(0xffffffffu, key[i] == th);
-        if (lane == 0) cells[i * kSelectWarps + warp] = __popc(t);
-      }
-      __syncthreads();
-      const int all = scan_cells(tie_base);
-      tie_base += all;
-#pragma unroll
-      for (int i = 0; i < I; ++i) {
-        const uint32_t t = __ballot_sync(0xffffffffu, key[i] == th);
-        const int rank = cells[i * kSelectWarps + warp] + __popc(t & ((1u << lane) - 1u));
-        if (key[i] > th || (key[i] == th && rank < left)) take |= 1u << i;
-      }
-      __syncthreads();
-    } else if (need > 0) {
-      const uint32_t above = listed ? all_of_bin : th - 1u;  // (th > 0: a key is never 0)
+    uint32_t take = 0;  // bit i: item i of this thread
+    if (need > 0) {
+      // keys that are chosen for sure: above the bin, or all of it too (th > 0)
+      const uint32_t above = whole ? th - 1u : bin_top;
 #pragma unroll
       for (int i = 0; i < I; ++i)
-        if (((in_list >> i) & 1u) ? chosen[key[i]] != 0 : key[i] > above) take |= 1u << i;
-    }
+        if (key[i] > above) take |= 1u << i;
+      if (listed) {
+        take &= ~in_list;
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-      const int j = at + i * kSelectThreads + tid;
-      uint32_t t = 0;
-      if (at + i * kSelectThreads < n) {
-        if (j < lo || (j >= hi && j < n)) take |= 1u << i;
-        t = __ballot_sync(0xffffffffu, (take >> i) & 1u);
+        for (int i = 0; i < I; ++i)
+          if ((in_list >> i) & 1u && rank_of[key[i]] < left) take |= 1u << i;
+      } else if (!whole) {
+        // the bin is one key alone (all three digits): its lowest indices
+        uint32_t ties = 0;
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+          if (key[i] == th) ties |= 1u << i;
+        int all;
+        int room = left - tie_base - block_scan(__popc(ties), slots, phase, &all);
+        tie_base += all;
+        for (; ties && room > 0; --room) {
+          take |= ties & (0u - ties);
+          ties &= ties - 1u;
+        }
       }
-      if (lane == 0) cells[i * kSelectWarps + warp] = __popc(t);
     }
-    __syncthreads();
-    const int all = scan_cells(base);
-    base += all;
+    const int j = at + j0;
+    if (j < lo || j + I > hi) {  // the first and the last blocks
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-      if (at + i * kSelectThreads >= n) continue;
-      const uint32_t t = __ballot_sync(0xffffffffu, (take >> i) & 1u);
-      if ((take >> i) & 1u)
-        o[cells[i * kSelectWarps + warp] + __popc(t & ((1u << lane) - 1u))] =
-            at + i * kSelectThreads + tid;
+      for (int i = 0; i < I; ++i)
+        if ((j + i >= 0 && j + i < lo) || (j + i >= hi && j + i < n)) take |= 1u << i;
     }
-    if (LOOP) __syncthreads();  // the cells may be written again
+    int all;
+    int32_t* to = o + base + block_scan(__popc(take), slots, phase, &all);
+    base += all;
+    for (; take; take &= take - 1u) *to++ = j + __ffs((int)take) - 1;
   }
 }
 
@@ -356,9 +338,10 @@ cudaError_t launch_block_select(const float* scores, const int32_t* positions, i
                                 int L, int block, int count, int first, int recent, int32_t* out,
                                 cudaStream_t stream) {
   const int nb = (L + block - 1) / block;
-  const int per = (nb + kSelectThreads - 1) / kSelectThreads;
-  auto kernel = per <= 1    ? block_select_kernel<1, false>
-                : per <= 4  ? block_select_kernel<4, false>
+  // rows that do not all start on 16 bytes shift their items by up to three
+  const int shifts = nb % 4 != 0 || (reinterpret_cast<uintptr_t>(scores) & 15u) != 0 ? 3 : 0;
+  const int per = (nb + shifts + kSelectThreads - 1) / kSelectThreads;
+  auto kernel = per <= 4    ? block_select_kernel<4, false>
                 : per <= 16 ? block_select_kernel<16, false>
                             : block_select_kernel<16, true>;
   return launch_pdl(kernel, dim3(B * Hkv), dim3(kSelectThreads), 0, stream, scores, positions,
