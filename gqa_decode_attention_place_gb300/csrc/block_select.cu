@@ -174,6 +174,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) block_select_kernel(
   // items are shifted so that their groups of four start on 16 bytes
   const int shift4 = (int)((reinterpret_cast<uintptr_t>(sc) >> 2) & 3);
   const int j0 = tid * I - shift4;  // this thread's first item of chunk 0
+  const int end = LOOP ? n + shift4 : 1;  // chunks: at 0, kChunk, .. below this
   uint32_t key[I];
   auto load = [&](int at) {  // the keys of the chunk at item `at`; 0 (below every key): no candidate
 #pragma unroll
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) block_select_kernel(
       const uint32_t digits = pass == 2 ? 0xffu : 0xfffu;
       if (pass > 0) clear();
       __syncthreads();
-      for (int at = 0; at < (LOOP ? n + 3 : 1); at += kChunk) {
+      for (int at = 0; at < end; at += kChunk) {
         if (LOOP) load(at);
 #pragma unroll
         for (int i = 0; i < I; ++i)
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) block_select_kernel(
   }
   // Place the chosen indices in ascending order: a count per thread, a scan.
   int base = 0, tie_base = 0;
-  for (int at = 0; at < n + 3; at += kChunk) {
+  for (int at = 0; at < end; at += kChunk) {
     if (LOOP && need > 0) load(at);
     uint32_t take = 0;  // bit i: item i of this thread
     if (need > 0) {

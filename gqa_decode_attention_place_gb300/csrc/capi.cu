@@ -244,7 +244,7 @@ int kv8_decode(const void* q, const int32_t* positions, const void* k_cache, con
 }
 
 bool list_ok(int count, int block) {
-  return count >= 1 && (long long)count * block < (1ll << 30);
+  return count >= 1 && (long long)count * block <= (1ll << 24);
 }
 
 // Workspace of the sparse step: the decode's, then the scores, then the list.

@@ -393,7 +393,8 @@ int attn_qk_norm_rope_append(const void* q, const void* k_new, const void* v_new
  *     its new rows:                   code <- e4m3(x / s)
  * rounded to nearest even, beyond +-448 saturating, NaN kept.  Only codes of
  * rows up to the last new one are written.  The bounds of a block become those
- * of its new rows and, if it held rows before, what they were (NaN ignored).
+ * of its new rows and, if it held rows before, what they were (NaN ignored;
+ * -inf and +inf for a channel with nothing else).
  *   k_bounds : or null.
  *   S        : >= 0 (0 does nothing).
  * A sequence whose rows are not all in [0, L) is skipped (the decode call
@@ -468,7 +469,7 @@ int attn_block_select(const float* scores, const int32_t* positions, int B, int 
  * order, -1 for none.  A block listed twice counts twice; one past the
  * position adds nothing; a list without any row gives zeros.  An index below
  * -1 or not below NB is skipped and sets ATTN_DEV_BAD_BLOCK.
- *   count : >= 1, count * block < 2^30.  The rest as attn_decode_step_kv8.
+ *   count : >= 1, count * block <= 2^24.  The rest as attn_decode_step_kv8.
  */
 int attn_decode_step_kv8_blocks(const void* q, const int32_t* positions, const void* k_cache,
                                 const void* v_cache, const float* k_scale, const float* v_scale,

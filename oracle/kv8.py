@@ -82,7 +82,8 @@ def kv8_append(codes, scale, new, positions, block, bounds=None):
                 scale[b, h, j] = s
                 codes[b, h, lo:hi] = e4m3_encode(x / s)
                 if bounds is not None:
-                    top, low = np.fmax.reduce(x, axis=0), np.fmin.reduce(x, axis=0)
+                    top = np.fmax.reduce(x, axis=0, initial=-np.inf)
+                    low = np.fmin.reduce(x, axis=0, initial=np.inf)
                     if had:
                         top = np.fmax(top, bounds[b, h, j, 0])
                         low = np.fmin(low, bounds[b, h, j, 1])

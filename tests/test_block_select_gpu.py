@@ -46,7 +46,11 @@ def test_scores(B, Hkv, g, L, positions, block):
 
 def _select(scores, positions, L, block, count, first, recent):
     pos = torch.tensor(positions, dtype=torch.int32, device="cuda")
-    got = ga.attn_block_select(scores, pos, L, block, count, first, recent).cpu().numpy()
+    B, Hkv = scores.shape[:2]
+    whole = torch.full((B * Hkv * count + 4096,), -77, dtype=torch.int32, device="cuda")
+    out = whole[2048:2048 + B * Hkv * count].view(B, Hkv, count)
+    got = ga.attn_block_select(scores, pos, L, block, count, first, recent, out=out).cpu().numpy()
+    assert (whole[:2048] == -77).all() and (whole[-2048:] == -77).all()  # nothing written outside
     s = scores.cpu().numpy()
     for b, p in enumerate(positions):
         for h in range(s.shape[1]):
@@ -66,6 +70,24 @@ def test_select(L, block, count, first, recent):
     gen = torch.Generator(device="cuda").manual_seed(61)
     scores = torch.randn((3, 2, nb), generator=gen, device="cuda")
     _select(scores, [L - 1, L // 2, L // 3], L, block, count, first, recent)
+
+
+@pytest.mark.parametrize("nb", [4, 2045, 2046, 2047, 2048, 2049, 8188, 8189, 8190, 8191, 8192, 8193,
+                                16384])
+def test_select_row_lengths_at_the_kernels_limits(nb):
+    """Rows that just fill, and just pass, what a block's threads hold, on and off 16 bytes; full
+    rows and the lengths next to them."""
+    gen = torch.Generator(device="cuda").manual_seed(63)
+    scores = torch.randn((4, 3, nb), generator=gen, device="cuda")
+    pos = [nb * 16 - 1, (nb - 1) * 16 - 1, (nb - 2) * 16 - 1, (nb - 3) * 16 - 1]
+    for count in (1, min(nb - 1, 65), min(nb - 1, 2000)):
+        _select(scores, pos, nb * 16, 16, count, 0, 0)
+        _select(scores, pos, nb * 16, 16, count, 1, count - 1)
+        if count > 2:
+            _select(scores, pos, nb * 16, 16, count, 1, 1)
+    # the same rows from a base that is not on 16 bytes
+    shifted = torch.empty(scores.numel() + 1, device="cuda")[1:].view_as(scores).copy_(scores)
+    _select(shifted, pos, nb * 16, 16, min(nb - 1, 65), 0, 1)
 
 
 def test_select_ties_signs_and_non_finite():

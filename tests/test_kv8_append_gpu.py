@@ -104,6 +104,25 @@ def test_non_finite_values():
     assert np.array_equal(f64(st["bounds"]), wk[2])
 
 
+@pytest.mark.parametrize("pos", [32, 40])
+def test_non_finite_single_tokens(pos):
+    """One token with NaN and infinities, at a block's first row and inside it: a channel that has
+    only been NaN keeps the empty bounds."""
+    st = _state(1, 1, 2, 64, 32, seed=9)
+    st["kn"][0, 0, 0, :3] = torch.tensor([float("nan"), float("inf"), float("-inf")])
+    st["vn"][0, 0, 1] = float("nan")
+    wk = kv8.kv8_append(u8(st["kc"]), f64(st["ks"]), f64(st["kn"]), [pos], 32, f64(st["bounds"]))
+    wv = kv8.kv8_append(u8(st["vc"]), f64(st["vs"]), f64(st["vn"]), [pos], 32)
+    at = torch.tensor([pos], dtype=torch.int32, device="cuda")
+    ga.attn_kv8_append(st["kn"], st["vn"], at, st["kc"], st["vc"], st["ks"], st["vs"], 32,
+                       k_bounds=st["bounds"])
+    torch.cuda.synchronize()
+    for got, (codes, scale, *_), sc in ((st["kc"], wk, st["ks"]), (st["vc"], wv, st["vs"])):
+        assert np.array_equal(f64(sc), scale)
+        assert np.array_equal(kv8.e4m3_decode(u8(got)), kv8.e4m3_decode(codes), equal_nan=True)
+    assert np.array_equal(f64(st["bounds"]), wk[2])
+
+
 def test_rows_outside_the_cache_are_skipped():
     st = _state(5, 3, 2, 50, 16, seed=7)
     before = {k: v.clone() for k, v in st.items()}
