@@ -54,7 +54,7 @@ cudaError_t launch_qk_norm_rope(const void* q, const void* k, const void* v, lon
 
 // 8-bit cache: append, block scores and selection, decode (block_index null:
 // all rows; else count listed blocks per (sequence, KV head)).
-constexpr int kKv8MaxGrid = 512;  // CTAs of the 8-bit decode (workspace partial slots)
+constexpr int kKv8MaxGrid = 192;  // CTAs of the 8-bit decode (workspace partial slots)
 cudaError_t launch_kv8_append(const void* k_new, const void* v_new, const int32_t* positions,
                               void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                               void* k_bounds, int B, int S, int Hkv, int L, int block,

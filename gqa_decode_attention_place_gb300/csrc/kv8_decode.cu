@@ -145,8 +145,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // what its end costs (about a tile's time), so that an even split of the
 // units is an even split of the work however short the segments are.
 struct Walk8 {
-  long long u;
+  long long u, end;  // the unit at hand; the end of the part of the range it lies in
   int b, kvh, k, nt, pos;
+};
+// A CTA's range of units [t0, t1).  If its last segment begins inside it and
+// goes on past t1, that part [tA, t1) is done first, then the rest; the CTA
+// that has the segment's next part starts with it too.  So a split segment's
+// parts are all done early, and their merge goes on behind the tiles that
+// follow.  (tA = t1: nothing goes first.)
+struct Range8 {
+  long long t0, tA, t1;
 };
 // To the first tile of the next segment (b = B past the last).
 __device__ __forceinline__ void walk8_segment(Walk8& w, const int* prefix, const int* spos,
@@ -179,10 +187,37 @@ __device__ __forceinline__ void walk8_init(Walk8& w, long long u, const int* pre
   w.pos = spos[lo];
   if (w.k == w.nt) walk8_segment(w, prefix, spos, B, Hkv);
 }
-__device__ __forceinline__ void walk8_next(Walk8& w, const int* prefix, const int* spos, int B,
-                                           int Hkv) {
+__device__ __forceinline__ void range8_init(Range8& r, const int* prefix, int B, int Hkv) {
+  int lo = 0, hi = B - 1;  // largest b with Hkv*prefix[b] <= t1 - 1
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((long long)Hkv * prefix[mid] <= r.t1 - 1) lo = mid; else hi = mid - 1;
+  }
+  const int n = prefix[lo + 1] - prefix[lo];
+  const int k = (int)((uint32_t)(r.t1 - 1 - (long long)Hkv * prefix[lo]) % (uint32_t)n);
+  const long long f0 = r.t1 - 1 - k;  // the segment's first unit; its tiles are f0 .. f0+n-2
+  // (from t0 + 1 on: the unit before f0 ends another segment and holds no tile)
+  r.tA = k + 1 < n - 1 && f0 > r.t0 + 1 ? f0 : r.t1;
+}
+// The range's first tile in this order.
+__device__ __forceinline__ void walk8_start(Walk8& w, const Range8& r, const int* prefix,
+                                            const int* spos, int B, int Hkv) {
+  walk8_init(w, r.tA < r.t1 ? r.tA : r.t0, prefix, spos, B, Hkv);
+  w.end = r.t1;
+}
+// Past the end of the part that went first: to the rest of the range.
+__device__ __forceinline__ void walk8_turn(Walk8& w, const Range8& r, const int* prefix,
+                                           const int* spos, int B, int Hkv) {
+  if (w.u >= w.end && w.end == r.t1 && r.tA < r.t1) {
+    walk8_init(w, r.t0, prefix, spos, B, Hkv);
+    w.end = r.tA;
+  }
+}
+__device__ __forceinline__ void walk8_next(Walk8& w, const Range8& r, const int* prefix,
+                                           const int* spos, int B, int Hkv) {
   ++w.u;
   if (++w.k == w.nt) walk8_segment(w, prefix, spos, B, Hkv);
+  walk8_turn(w, r, prefix, spos, B, Hkv);
 }
 
 // One consumer warp: 16 rows of each tile for one KV head's g <= 8*NT heads.
@@ -379,26 +414,64 @@ __device__ __forceinline__ void merge_warps8(const float* mo, const float* mml, 
   }
 }
 
-// A segment of which this CTA did a part: its tiles' units [f0, f1) in the flat order.
+// A segment split over CTAs c0 .. c0 + n - 1; f0: its first unit.
 struct Part8 {
-  long long f0, f1;
+  long long f0;
   size_t out_at;
-  int seg;
+  int c0, n;
 };
 
 // Merge the parts of a split segment, in CTA order, by the consumer warps.
-// All of the parts' (max, sum) come in one round trip, then the outputs, a
-// float4 per thread and part: heads x 32 columns, and where those leave
-// threads over (g < 8) the parts are dealt out among them as well.
+// Few parts: every thread loads all of its column's in one round trip.  More:
+// the parts' (max, sum) come first, then the outputs, a float4 per thread and
+// part, heads x 32 columns, and where those leave threads over (g < 8) the
+// parts are dealt out among them as well.
+constexpr int kFewParts = 4;
 __device__ __forceinline__ void merge_parts(const Kv8Params& p, const Part8& pt, long long T,
                                             int G, float* buf, ConsumerSync& csync, int warp,
                                             int lane) {
-  const int g = p.g, tid = warp * 32 + lane;
-  const int c0 = cta_of(pt.f0, T, G), n = cta_of(pt.f1 - 1, T, G) - c0 + 1;
+  const int g = p.g, tid = warp * 32 + lane, n = pt.n;
   // CTA c0's part is its second unless the segment opens its range, right
   // away or after the end unit of the one before
-  const int slot0 = 2 * c0 + (T * c0 / G >= pt.f0 - 1 ? 0 : 1);
-  auto slot = [&](int r) { return r == 0 ? slot0 : 2 * (c0 + r); };
+  const int slot0 = 2 * pt.c0 + (T * pt.c0 / G >= pt.f0 - 1 ? 0 : 1);
+  auto slot = [&](int r) { return r == 0 ? slot0 : 2 * (pt.c0 + r); };
+  const int cols = g * (kD / 4);
+  auto store = [&](int col, const float4& o, float inv) {
+    *reinterpret_cast<uint2*>(p.out + pt.out_at + (size_t)col * 4) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  };
+  if (n <= kFewParts) {
+    for (int col = tid; col < cols; col += kConsumers) {
+      const int h = col / (kD / 4);
+      float2 ml[kFewParts];
+      float4 x[kFewParts];
+      float M = kMInit;
+#pragma unroll
+      for (int r = 0; r < kFewParts; ++r) {
+        ml[r] = make_float2(kMInit, 0.f);
+        x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < n) {
+          ml[r] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((size_t)slot(r) * g + h) * 2));
+          x[r] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (size_t)slot(r) * g * kD) + col);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kFewParts; ++r) M = fmaxf(M, ml[r].x);
+      float ls = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < kFewParts; ++r) {
+        const float e = ex2(ml[r].x - M);
+        ls = fmaf(ml[r].y, e, ls);
+        o.x = fmaf(x[r].x, e, o.x);
+        o.y = fmaf(x[r].y, e, o.y);
+        o.z = fmaf(x[r].z, e, o.z);
+        o.w = fmaf(x[r].w, e, o.w);
+      }
+      store(col, o, ls == 0.f ? 0.f : 1.f / ls);
+    }
+    return;
+  }
   float* wt = buf;              // [n][g] maxima, then weights
   float* ls = buf + n * g;      // [n][g] sums
   for (int i = tid; i < n * g; i += kConsumers) {
@@ -425,7 +498,6 @@ __device__ __forceinline__ void merge_parts(const Kv8Params& p, const Part8& pt,
     if (lane == 0) ls[h] = sum == 0.f ? 0.f : 1.f / sum;  // row 0's own sum has been read
   }
   csync(lane);
-  const int cols = g * (kD / 4);
   const int deal = max(1, kConsumers / cols);  // threads that share a column
   float4* red = reinterpret_cast<float4*>(buf + ((2 * n * g + 3) & ~3));
   for (int base = 0; base < cols; base += kConsumers) {
@@ -458,14 +530,19 @@ __device__ __forceinline__ void merge_parts(const Kv8Params& p, const Part8& pt,
         }
       }
     }
-    if (on && (deal == 1 || who == 0)) {
-      const float inv = ls[col / (kD / 4)];
-      uint2 v = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-      *reinterpret_cast<uint2*>(p.out + pt.out_at + (size_t)col * 4) = v;
-    }
+    if (on && (deal == 1 || who == 0)) store(col, o, ls[col / (kD / 4)]);
   }
   csync(lane);  // buf may be written again
 }
+// What merge_parts keeps in the merge buffer: (max, sum) of every part, and the
+// dealt-out columns where heads leave threads over.
+constexpr bool merge_fits(int g) {
+  return 2 * kKv8MaxGrid * g + 3 + (g * (kD / 4) * 2 <= kConsumers ? kConsumers * 4 : 0) <=
+         merge_floats(g);
+}
+static_assert(merge_fits(1) && merge_fits(2) && merge_fits(3) && merge_fits(4) && merge_fits(5) &&
+                  merge_fits(8) && merge_fits(9) && merge_fits(16),
+              "the parts' statistics fit the merge buffer");
 
 template <int NT, bool LIST>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -548,7 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (T <= (long long)(kWholeTiles + 1) * nseg) gw = min(gw, nseg);
   const int G = (int)gw;
   if ((int)blockIdx.x >= G) return;
-  const long long t0 = T * blockIdx.x / G, t1 = T * (blockIdx.x + 1) / G;
+  Range8 rg;
+  rg.t0 = T * blockIdx.x / G;
+  rg.t1 = T * (blockIdx.x + 1) / G;
+  range8_init(rg, prefix, B, Hkv);
 
   if (warp >= kWarps) {
     // ----------------------------------------------------------- producers --
@@ -583,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return row <= w.pos ? row : kNoRow;
     };
     auto step = [&](Walk8& w, int n) {  // n tiles on, as far as the range goes
-      for (int k = 0; k < n && w.u < t1; ++k) walk8_next(w, prefix, spos, B, Hkv);
+      for (int k = 0; k < n && w.u < w.end; ++k) walk8_next(w, rg, prefix, spos, B, Hkv);
     };
     int s = 0;          // the ring's stage and pass of the tile at hand
     uint32_t pass = 0;
@@ -614,10 +694,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   p.q + ((size_t)b * p.Hq + (size_t)kvh * g) * kD, q_bytes, full);
     };
     Walk8 w;
-    walk8_init(w, t0, prefix, spos, B, Hkv);
-    bool first = true;
+    walk8_start(w, rg, prefix, spos, B, Hkv);
     if (copies && !LIST) {
-      for (; w.u < t1; walk8_next(w, prefix, spos, B, Hkv)) {
+      for (; w.u < w.end; walk8_next(w, rg, prefix, spos, B, Hkv)) {
         if (!wait_empty()) break;
         const int z = w.b * Hkv + w.kvh, row = w.k * kTile;
         // failure-path tests only: a tile never issued
@@ -625,26 +704,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0 && !skip && range_ok(row < L && z < B * Hkv, p.status)) {
           const uint32_t full = smem_u32(&bars[s]);
           const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes);
-          expect(full, kStageBytes, first || w.k == 0, w.b, w.kvh);
+          expect(full, kStageBytes, w.k == 0 || w.u == rg.t0, w.b, w.kvh);
           tma_load_3d(sK, &tm_k, 0, row, z, full);
           tma_load_3d(sK + kOpBytes, &tm_v, 0, row, z, full);
         }
         __syncwarp();
-        first = false;
         turn();
       }
     } else if (copies) {
       step(w, ti);  // this lane's tile of the batch at hand
-      int blk = w.u < t1 ? fetch(w) : -1;
+      int blk = w.u < w.end ? fetch(w) : -1;
       bool ok = true;
       while (ok) {
-        const bool on = w.u < t1;
+        const bool on = w.u < w.end;
         const int n_q = __popc(__ballot_sync(0xffffffffu, on)) >> 3;  // tiles of the batch
         if (n_q == 0) break;
         const int row = on ? row_of(w, blk) : kNoRow, b = w.b, kvh = w.kvh, k = w.k;
+        const bool starts = w.k == 0 || w.u == rg.t0;
         const int z = b * Hkv + kvh;
         step(w, 4);
-        blk = w.u < t1 ? fetch(w) : -1;
+        blk = w.u < w.end ? fetch(w) : -1;
         const bool skip = p.test_skip >= 0 && z == 0 && k == p.test_skip;
         const bool have = !skip && row != kNoRow && in_block == 0 &&
                           range_ok(row >= 0 && row < L && z < B * Hkv, p.status);
@@ -657,21 +736,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t full = smem_u32(&bars[s]);
           if (lane == 8 * q && !skip)
             expect(full, __popc((boxes >> (8 * q)) & 0xffu) * (uint32_t)entry_rows * 2u * kD,
-                   first || k == 0, b, kvh);
+                   starts, b, kvh);
           __syncwarp();
           if (ti == q && have) {
             const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes) + slice * 16 * kD;
             tma_load_3d(sK, &tm_k, 0, row, z, full);
             tma_load_3d(sK + kOpBytes, &tm_v, 0, row, z, full);
           }
-          first = false;
           turn();
         }
       }
     } else {
       step(w, ti);
       auto look_up = [&](int blk, int& row, float& ks, float& vs) {
-        row = w.u < t1 ? row_of(w, blk) : kNoRow;
+        row = w.u < w.end ? row_of(w, blk) : kNoRow;
         ks = vs = 1.f;
         if (row != kNoRow) {
           const size_t at = (size_t)(w.b * Hkv + w.kvh) * p.nb + (row >> p.lb);
@@ -681,10 +759,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int row;
       float ks, vs;
-      bool on = w.u < t1;
+      bool on = w.u < w.end;
       look_up(LIST && on ? fetch(w) : -1, row, ks, vs);
       step(w, 4);
-      int blk = LIST && w.u < t1 ? fetch(w) : -1;
+      int blk = LIST && w.u < w.end ? fetch(w) : -1;
       bool ok = true;
       while (ok) {
         const int n_q = __popc(__ballot_sync(0xffffffffu, on)) >> 3;
@@ -692,9 +770,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int row_next;
         float ks_next, vs_next;
         look_up(blk, row_next, ks_next, vs_next);
-        on = w.u < t1;
+        on = w.u < w.end;
         step(w, 4);
-        blk = LIST && w.u < t1 ? fetch(w) : -1;
+        blk = LIST && w.u < w.end ? fetch(w) : -1;
         const SliceMeta mt = slice_meta(row, ks, vs);
         for (int q = 0; q < n_q; ++q) {
           if (!wait_empty()) {
@@ -718,17 +796,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     cs.c = lane >> 2;
     cs.t = lane & 3;
     Walk8 w;
-    walk8_init(w, t0, prefix, spos, B, Hkv);
-    // A piece that is only part of its segment leaves its partial in global
-    // memory; who merges the segment is settled at the end, so that the
-    // round trips through L2 never hold up the tiles.  A CTA has at most two
-    // such pieces, its first and its last.
-    Part8 parts[2];
-    int n_parts = 0;
+    walk8_start(w, rg, prefix, spos, B, Hkv);
     int s = 0;
     uint32_t ph = 0;
-    for (bool first = true; w.u < t1; first = false) {
-      const int len = (int)min((long long)(w.nt - w.k), t1 - w.u);
+    while (w.u < w.end) {
+      const int len = (int)min((long long)(w.nt - w.k), w.end - w.u);
       cs.reset();
       bool ok = true;
       for (int i = 0; i < len; ++i) {
@@ -754,7 +826,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*abort_flag) break;
       // ---- this CTA's part: the warps' partials, in warp order -----------
       const bool whole = w.k == 0 && len == w.nt;
-      const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+      // a part that does not open the range is its last segment's
+      const int slot = 2 * blockIdx.x + (w.end == rg.t1 && rg.tA < rg.t1 ? 1 : 0);
       const size_t out_at = ((size_t)w.b * p.Hq + (size_t)w.kvh * g) * kD;
       for (int i = tid; i < g * (kD / 4); i += kConsumers) {
         const int h = i / (kD / 4), d = (i % (kD / 4)) * 4;
@@ -772,35 +845,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_float2(M, ls);
         }
       }
+      csync(lane);  // the merge buffers may be written again; a partial is in place
       if (!whole) {
-        Part8& pt = parts[n_parts++];
+        // the segment's last CTA to arrive merges the parts
+        Part8 pt;
         pt.f0 = w.u - w.k;
-        pt.f1 = pt.f0 + w.nt;
-        pt.seg = w.b * Hkv + w.kvh;
         pt.out_at = out_at;
-      }
-      csync(lane);  // the merge buffers may be written again
-      if (len < w.nt - w.k) break;  // the range ends inside the segment
-      walk8_segment(w, prefix, spos, B, Hkv);
-    }
-    if (n_parts > 0 && !*abort_flag) {
-      // ---- each split segment: its last CTA to arrive merges the parts ------
-      __threadfence();
-      csync(lane);
-      if (tid == 0) {
-        for (int i = 0; i < n_parts; ++i) {
-          const uint32_t n =
-              (uint32_t)(cta_of(parts[i].f1 - 1, T, G) - cta_of(parts[i].f0, T, G) + 1);
-          const bool last = atomicAdd(&p.counters[parts[i].seg], 1u) + 1 == n;
-          if (last) p.counters[parts[i].seg] = 0;
-          misc[2 + i] = last;
+        pt.c0 = cta_of(pt.f0, T, G);
+        pt.n = cta_of(pt.f0 + w.nt - 1, T, G) - pt.c0 + 1;
+        if (tid == 0) {
+          uint32_t* counter = &p.counters[w.b * Hkv + w.kvh];
+          __threadfence();  // (the other threads' stores came before the barrier)
+          const bool last = atomicAdd(counter, 1u) + 1 == (uint32_t)pt.n;
+          if (last) *counter = 0;
+          __threadfence();
+          misc[2] = last;
         }
-        __threadfence();
+        csync(lane);
+        if (misc[2] && !*abort_flag) merge_parts(p, pt, T, G, merge_o, csync, warp, lane);
       }
-      csync(lane);
-      for (int i = 0; i < n_parts && !*abort_flag; ++i)
-        if (misc[2 + i])  // every tile has been consumed: the ring is free
-          merge_parts(p, parts[i], T, G, reinterpret_cast<float*>(stages), csync, warp, lane);
+      if (*abort_flag) break;
+      if (len < w.nt - w.k) {  // the part of the range ends inside the segment
+        w.u = w.end;
+      } else {
+        walk8_segment(w, prefix, spos, B, Hkv);
+      }
+      walk8_turn(w, rg, prefix, spos, B, Hkv);
     }
   }
   if (*abort_flag) {  // copies in flight land before the shared memory goes

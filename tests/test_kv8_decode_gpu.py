@@ -257,6 +257,29 @@ def test_every_way_of_splitting(cluster, g):
     _check(listed, st, L, block, pos, index=index.tolist(), seqs=good, what=f"cluster {cluster}")
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_ragged_batches_split_anywhere(seed):
+    """Batches of all kinds of lengths through the flat list, so that its cuts fall at, next to
+    and inside segments, with bad positions in between; the same bits on a second run."""
+    rng = np.random.default_rng(1000 + seed)
+    B, Hkv, g = int(rng.integers(1, 90)), int(rng.integers(1, 6)), int(rng.integers(1, 5))
+    L = int(rng.integers(100, 3000)) if B < 40 else int(rng.integers(100, 1000))
+    pos = [int(p) for p in rng.integers(0, L, B)]
+    if B > 4:
+        for b in rng.integers(0, B, 2):
+            pos[b] = L + 5
+    st = _case(B, Hkv, g, L, 64, pos, seed=52)
+    good = [b for b in range(B) if pos[b] < L]
+    ga.attn_test_force_schedule(0)
+    try:
+        out, again = _run(st, 64), _run(st, 64)
+        torch.cuda.synchronize()
+    finally:
+        ga.attn_test_force_schedule(-1)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+    _check(out, st, L, 64, pos, seqs=good)
+
+
 @pytest.mark.parametrize("cluster", [0, 8])
 @pytest.mark.parametrize("listed", [False, True])
 def test_a_wait_that_runs_out_is_reported(cluster, listed):
