@@ -282,8 +282,15 @@ struct Consumer8 {
     }
   }
   // 16 rows at Ks, Vs (the slice's first row in the tile), of which the
-  // first `rows` count (rows >= 1); the others may hold anything.
+  // first `rows` count (rows >= 1); the others may hold anything.  FULL: all
+  // of them count, and nothing is masked.
   __device__ __forceinline__ void slice(const uint8_t* Ks, const uint8_t* Vs, int rows,
+                                        const SliceMeta& meta) {
+    if (rows >= 16) slice_of<true>(Ks, Vs, 16, meta);
+    else slice_of<false>(Ks, Vs, rows, meta);
+  }
+  template <bool FULL>
+  __device__ __forceinline__ void slice_of(const uint8_t* Ks, const uint8_t* Vs, int rows,
                                         const SliceMeta& meta) {
     uint4 ka[2], kb[2];
 #pragma unroll
@@ -310,7 +317,8 @@ struct Consumer8 {
     for (int k = 0; k < 4; ++k) {
       const int r = 2 * t + (k & 1) + 8 * (k >> 1);
       v[k] = lds128(Vs + sw128(r, c));
-      if (r >= rows) v[k] = make_uint4(0u, 0u, 0u, 0u);  // may be NaN: 0 * NaN would spread
+      // rows that do not count may be NaN: 0 * NaN would spread
+      if (!FULL && r >= rows) v[k] = make_uint4(0u, 0u, 0u, 0u);
     }
     uint32_t pb[NT][2];
 #pragma unroll
@@ -319,7 +327,8 @@ struct Consumer8 {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float sc = s[n][0][k] + s[n][1][k];
-        x[k] = (c + 8 * (k >> 1)) < rows ? fmaf(sc, qk[n][k & 1] * meta.ks, meta.lv) : -INFINITY;
+        x[k] = FULL || (c + 8 * (k >> 1)) < rows ? fmaf(sc, qk[n][k & 1] * meta.ks, meta.lv)
+                                                 : -INFINITY;
       }
       const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
       if (__any_sync(0xffffffffu, mx0 > m[n][0] + kTau || mx1 > m[n][1] + kTau)) {
