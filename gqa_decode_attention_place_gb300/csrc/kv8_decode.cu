@@ -22,10 +22,11 @@
 //    MMAs (m16n8k16, fp16 in, fp32 out) with rows or dims as M and the heads
 //    as N, so a KV head's g heads share one conversion of its codes.  q is
 //    scaled per head by a power of two into fp16 (its 8 bits fit).
-//  * The order of the dims in q.k and of the dims in the output blocks is
-//    free, so every lane reads 16-byte pieces without bank conflicts and no
-//    code is moved between lanes: K pieces feed the A operand as they are, V
-//    pieces of two rows are interleaved byte-wise (prmt) before conversion.
+//  * The order of the dims in q.k and of the rows in both products is free, so
+//    K's 16-byte pieces feed the A operand as they are, and V comes through
+//    transposing 8-bit matrix loads; no bank conflicts, no code moved between
+//    lanes.  The conversions are what the warps spend most of their issue
+//    slots on (96 of about 250 instructions a slice).
 //  * A flat list of all tiles is split evenly over the grid (one CTA per SM);
 //    a segment split over CTAs is merged by the CTA that arrives last, in
 //    CTA order, so results do not depend on timing.  For few segments a
@@ -104,7 +105,7 @@ struct Kv8Params {
 // Shared memory: the ring, per stage the q rows of a piece that starts there
 // and the slices' scales, the warps' partials, barriers, and per sequence the
 // tiles before it and its position.
-constexpr int kMergeRow = kD + 4;
+constexpr int kMergeRow = kD + 8;
 __host__ __device__ constexpr int merge_heads(int g) { return (g + 1) & ~1; }
 __host__ __device__ constexpr int merge_row(int warp, int h, int g) {
   return ((warp * 2 + (h & 1)) * (merge_heads(g) >> 1) + (h >> 1)) * kMergeRow;
@@ -220,13 +221,26 @@ __device__ __forceinline__ void walk8_next(Walk8& w, const Range8& r, const int*
   walk8_turn(w, r, prefix, spos, B, Hkv);
 }
 
-// One consumer warp: 16 rows of each tile for one KV head's g <= 8*NT heads.
+// 16 rows x 16 codes of two 16-code columns, transposed (lane l gives the
+// address of row l % 16 of column block l / 16): r[2j] holds, for code c of
+// block j (lane 4c + t), rows 4t .. 4t+3, and r[2j+1] the same for code c + 8.
+__device__ __forceinline__ void ldmatrix_codes(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// One consumer warp: 16 rows of a tile for one KV head's g <= 8*NT heads.
 // Lane 4c + t.
-//  * S = K q^T: MMA row c is slice row c (c+8 the upper half), columns the
-//    heads.  MMA step w takes dims 32t + 4w .. +3 of every lane t, so a
-//    lane's 32 bytes of a row are its operand and q is held to match.
-//  * P^T by 8x8 transposes; O^T += V^T P^T: MMA m-block i holds dims 16c+2i
-//    (row c) and 16c+2i+1 (row c+8); keys 2t, 2t+1, 2t+8, 2t+9 per lane.
+//  * S = K q^T: MMA row c is slice row key(c) = 4*(c/2) + c%2, row c+8 is
+//    key(c) + 2, columns the heads.  MMA step w takes dims 32t + 4w .. +3 of
+//    every lane t, so a lane's 32 bytes of a row are its operand and q is held
+//    to match.
+//  * P^T by 8x8 transposes: lane t gets rows 4t, 4t+1 and 4t+2, 4t+3.
+//  * O^T += V^T P^T: the transposing matrix loads put those four rows' codes of
+//    one dim in one register; MMA block i holds dims 16i + c (row c) and
+//    16i + 8 + c (row c+8).
 template <int NT>
 struct Consumer8 {
   uint32_t qb[NT][8][2];
@@ -292,11 +306,12 @@ struct Consumer8 {
   template <bool FULL>
   __device__ __forceinline__ void slice_of(const uint8_t* Ks, const uint8_t* Vs, int rows,
                                         const SliceMeta& meta) {
+    const int key = 4 * (c >> 1) + (c & 1);
     uint4 ka[2], kb[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      ka[i] = lds128(Ks + sw128(c, 2 * t + i));
-      kb[i] = lds128(Ks + sw128(c + 8, 2 * t + i));
+      ka[i] = lds128(Ks + sw128(key, 2 * t + i));
+      kb[i] = lds128(Ks + sw128(key + 2, 2 * t + i));
     }
     float s[NT][2][4];
 #pragma unroll
@@ -312,14 +327,6 @@ struct Consumer8 {
       for (int n = 0; n < NT; ++n)
         mma_f16(s[n][w & 1], a0, a1, a2, a3, qb[n][w][0], qb[n][w][1]);
     }
-    uint4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = 2 * t + (k & 1) + 8 * (k >> 1);
-      v[k] = lds128(Vs + sw128(r, c));
-      // rows that do not count may be NaN: 0 * NaN would spread
-      if (!FULL && r >= rows) v[k] = make_uint4(0u, 0u, 0u, 0u);
-    }
     uint32_t pb[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -327,7 +334,7 @@ struct Consumer8 {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float sc = s[n][0][k] + s[n][1][k];
-        x[k] = FULL || (c + 8 * (k >> 1)) < rows ? fmaf(sc, qk[n][k & 1] * meta.ks, meta.lv)
+        x[k] = FULL || key + (k & 2) < rows ? fmaf(sc, qk[n][k & 1] * meta.ks, meta.lv)
                                                  : -INFINITY;
       }
       const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
@@ -358,23 +365,31 @@ struct Consumer8 {
       pb[n][0] = movm_trans(pack_f16x2(pr[0], pr[1]));
       pb[n][1] = movm_trans(pack_f16x2(pr[2], pr[3]));
     }
+    // rows that do not count may be NaN: 0 * NaN would spread
+    const int seen = rows - 4 * t;  // of this lane's four rows
+    const uint32_t keep = FULL || seen >= 4 ? 0xffffffffu
+                          : seen <= 0       ? 0u
+                                            : (1u << (8 * seen)) - 1u;
+    const int lane = 4 * c + t;
+    const uint32_t v_row = smem_u32(Vs) + (lane & 15) * 128;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int i = 0; i < 8; i += 2) {
+      uint32_t v[4];
+      ldmatrix_codes(v, v_row + (((i + (lane >> 4)) ^ (lane & 7)) << 4));
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const uint32_t sel = hf ? 0x7362u : 0x5140u;
-        const uint32_t e0 = prmt(word(v[0], w), word(v[1], w), sel);
-        const uint32_t e1 = prmt(word(v[2], w), word(v[3], w), sel);
-        const uint32_t a0 = e4m3x2_to_f16x2(e0), a1 = e4m3x2_to_f16x2(e0 >> 16);
-        const uint32_t a2 = e4m3x2_to_f16x2(e1), a3 = e4m3x2_to_f16x2(e1 >> 16);
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t lo = FULL ? v[2 * j] : v[2 * j] & keep;
+        const uint32_t hi = FULL ? v[2 * j + 1] : v[2 * j + 1] & keep;
+        const uint32_t a0 = e4m3x2_to_f16x2(lo), a2 = e4m3x2_to_f16x2(lo >> 16);
+        const uint32_t a1 = e4m3x2_to_f16x2(hi), a3 = e4m3x2_to_f16x2(hi >> 16);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * w + hf], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+        for (int n = 0; n < NT; ++n) mma_f16(o[n][i + j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
       }
     }
   }
   // This warp's (m, l, o) -> ml [warp][g][2], mo (merge_row): rows of even and
-  // of odd heads apart and 132 floats long, so that the 8 lanes of a store
-  // phase (two c, four t) fall on 32 different banks.
+  // of odd heads apart and 136 floats long, so that a store's lanes (8 c, 4 t)
+  // fall on 32 different banks.
   __device__ __forceinline__ void stash(float* mo, float* ml, int warp, int g) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -385,11 +400,12 @@ struct Consumer8 {
         for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         const int h = 8 * n + 2 * t + e;
         if (h < g) {
-          float4* dst = reinterpret_cast<float4*>(mo + merge_row(warp, h, g) + 16 * c);
+          float* dst = mo + merge_row(warp, h, g) + c;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_float4(o[n][2 * i][e], o[n][2 * i][2 + e], o[n][2 * i + 1][e],
-                                 o[n][2 * i + 1][2 + e]);
+          for (int i = 0; i < 8; ++i) {
+            dst[16 * i] = o[n][i][e];
+            dst[16 * i + 8] = o[n][i][2 + e];
+          }
           if (c == 0)
             *reinterpret_cast<float2*>(ml + (warp * g + h) * 2) = make_float2(m[n][e], sum);
         }
