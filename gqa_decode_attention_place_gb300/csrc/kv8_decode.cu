@@ -55,7 +55,7 @@ constexpr int kWarps = kSlices;             // consumer warps
 constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 64;   // and the two producer warps
 constexpr int kMaxStages = 6;
-constexpr int kMiscInts = 32;
+constexpr int kMiscInts = 40;  // [0] abort, [2] last, [8..16) scan, [24..34) a walk
 constexpr int kNoRow = 0x40000000;          // row of a slice that holds nothing
 constexpr float kMInit = -1e30f;            // running maximum before any row
 constexpr float kTau = 8.f;                 // the running maximum may lag by 2^kTau
@@ -142,9 +142,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // A tile's place in the flat (sequence, KV head, tile) order.  The order is
-// counted in units: a segment of nt tiles takes nt + 1, its tiles and one for
-// what its end costs (about a tile's time), so that an even split of the
-// units is an even split of the work however short the segments are.
+// counted in units: a segment of nt tiles takes nt + E, its tiles and E for
+// what its end costs (measured: 1.2 tiles' time at g = 2, 1.5 at g = 8, 2.1 at
+// g = 16), so that an even split of the units is an even split of the work
+// however short the segments are.
+template <int NT> constexpr int kEndUnits = NT;
 struct Walk8 {
   long long u, end;  // the unit at hand; the end of the part of the range it lies in
   int b, kvh, k, nt, pos;
@@ -158,19 +160,21 @@ struct Range8 {
   long long t0, tA, t1;
 };
 // To the first tile of the next segment (b = B past the last).
+template <int E>
 __device__ __forceinline__ void walk8_segment(Walk8& w, const int* prefix, const int* spos,
                                               int B, int Hkv) {
-  w.u += w.nt - w.k + 1;
+  w.u += w.nt - w.k + E;
   w.k = 0;
   if (++w.kvh < Hkv) return;
   w.kvh = 0;
   do { ++w.b; } while (w.b < B && prefix[w.b + 1] == prefix[w.b]);
   if (w.b < B) {
-    w.nt = prefix[w.b + 1] - prefix[w.b] - 1;
+    w.nt = prefix[w.b + 1] - prefix[w.b] - E;
     w.pos = spos[w.b];
   }
 }
 // The first tile at or after unit u.
+template <int E>
 __device__ __forceinline__ void walk8_init(Walk8& w, long long u, const int* prefix,
                                            const int* spos, int B, int Hkv) {
   int lo = 0, hi = B - 1;  // largest b with Hkv*prefix[b] <= u
@@ -182,12 +186,13 @@ __device__ __forceinline__ void walk8_init(Walk8& w, long long u, const int* pre
   const uint32_t off = (uint32_t)(u - (long long)Hkv * prefix[lo]);
   w.u = u;
   w.b = lo;
-  w.nt = n - 1;
+  w.nt = n - E;
   w.kvh = (int)(off / (uint32_t)n);
   w.k = (int)(off % (uint32_t)n);
   w.pos = spos[lo];
-  if (w.k == w.nt) walk8_segment(w, prefix, spos, B, Hkv);
+  if (w.k >= w.nt) walk8_segment<E>(w, prefix, spos, B, Hkv);
 }
+template <int E>
 __device__ __forceinline__ void range8_init(Range8& r, const int* prefix, int B, int Hkv) {
   int lo = 0, hi = B - 1;  // largest b with Hkv*prefix[b] <= t1 - 1
   while (lo < hi) {
@@ -196,29 +201,53 @@ __device__ __forceinline__ void range8_init(Range8& r, const int* prefix, int B,
   }
   const int n = prefix[lo + 1] - prefix[lo];
   const int k = (int)((uint32_t)(r.t1 - 1 - (long long)Hkv * prefix[lo]) % (uint32_t)n);
-  const long long f0 = r.t1 - 1 - k;  // the segment's first unit; its tiles are f0 .. f0+n-2
-  // (from t0 + 1 on: the unit before f0 ends another segment and holds no tile)
-  r.tA = k + 1 < n - 1 && f0 > r.t0 + 1 ? f0 : r.t1;
+  const long long f0 = r.t1 - 1 - k;  // the segment's first unit; its tiles are f0 .. f0+n-E-1
+  // (from t0 + E on: the units before f0 end another segment and hold no tile)
+  r.tA = k + 1 < n - E && f0 > r.t0 + E ? f0 : r.t1;
 }
 // The range's first tile in this order.
+template <int E>
 __device__ __forceinline__ void walk8_start(Walk8& w, const Range8& r, const int* prefix,
                                             const int* spos, int B, int Hkv) {
-  walk8_init(w, r.tA < r.t1 ? r.tA : r.t0, prefix, spos, B, Hkv);
+  walk8_init<E>(w, r.tA < r.t1 ? r.tA : r.t0, prefix, spos, B, Hkv);
   w.end = r.t1;
 }
 // Past the end of the part that went first: to the rest of the range.
+template <int E>
 __device__ __forceinline__ void walk8_turn(Walk8& w, const Range8& r, const int* prefix,
                                            const int* spos, int B, int Hkv) {
   if (w.u >= w.end && w.end == r.t1 && r.tA < r.t1) {
-    walk8_init(w, r.t0, prefix, spos, B, Hkv);
+    walk8_init<E>(w, r.t0, prefix, spos, B, Hkv);
     w.end = r.tA;
   }
 }
+template <int E>
 __device__ __forceinline__ void walk8_next(Walk8& w, const Range8& r, const int* prefix,
                                            const int* spos, int B, int Hkv) {
   ++w.u;
-  if (++w.k == w.nt) walk8_segment(w, prefix, spos, B, Hkv);
-  walk8_turn(w, r, prefix, spos, B, Hkv);
+  if (++w.k == w.nt) walk8_segment<E>(w, prefix, spos, B, Hkv);
+  walk8_turn<E>(w, r, prefix, spos, B, Hkv);
+}
+
+__device__ __forceinline__ void put_walk8(volatile Walk8* to, const Walk8& w) {
+  to->u = w.u;
+  to->end = w.end;
+  to->b = w.b;
+  to->kvh = w.kvh;
+  to->k = w.k;
+  to->nt = w.nt;
+  to->pos = w.pos;
+}
+__device__ __forceinline__ Walk8 get_walk8(const volatile Walk8* from) {
+  Walk8 w;
+  w.u = from->u;
+  w.end = from->end;
+  w.b = from->b;
+  w.kvh = from->kvh;
+  w.k = from->k;
+  w.nt = from->nt;
+  w.pos = from->pos;
+  return w;
 }
 
 // 16 rows x 16 codes of two 16-code columns, transposed (lane l gives the
@@ -452,13 +481,14 @@ struct Part8 {
 // part, heads x 32 columns, and where those leave threads over (g < 8) the
 // parts are dealt out among them as well.
 constexpr int kFewParts = 4;
+template <int E>
 __device__ __forceinline__ void merge_parts(const Kv8Params& p, const Part8& pt, long long T,
                                             int G, float* buf, ConsumerSync& csync, int warp,
                                             int lane) {
   const int g = p.g, tid = warp * 32 + lane, n = pt.n;
   // CTA c0's part is its second unless the segment opens its range, right
-  // away or after the end unit of the one before
-  const int slot0 = 2 * pt.c0 + (T * pt.c0 / G >= pt.f0 - 1 ? 0 : 1);
+  // away or after the end units of the one before
+  const int slot0 = 2 * pt.c0 + (T * pt.c0 / G >= pt.f0 - E ? 0 : 1);
   auto slot = [&](int r) { return r == 0 ? slot0 : 2 * (pt.c0 + r); };
   const int cols = g * (kD / 4);
   auto store = [&](int col, const float4& o, float inv) {
@@ -573,6 +603,7 @@ template <int NT, bool LIST>
 __global__ void __launch_bounds__(kThreads, 1)
     kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Kv8Params p) {
+  constexpr int E = kEndUnits<NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int NS = p.stages;
   uint8_t* stages = smem;
@@ -611,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos = p.positions[b];
       spos[b] = pos;
       if (rows_in_cache(pos, 0, L)) {
-        v = (LIST ? list_tiles : pos / kTile + 1) + 1;
+        v = (LIST ? list_tiles : pos / kTile + 1) + E;
       } else if (b % (int)gridDim.x == (int)blockIdx.x) {
         // out-of-range position: flag it and make the sequence's output NaN
         set_status(p.status, ATTN_DEV_BAD_POSITION);
@@ -647,13 +678,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // are short (a split costs a round trip through L2).
   const long long nseg = (long long)B * Hkv;
   long long gw = min((long long)gridDim.x, T);
-  if (T <= (long long)(kWholeTiles + 1) * nseg) gw = min(gw, nseg);
+  if (T <= (long long)(kWholeTiles + E) * nseg) gw = min(gw, nseg);
   const int G = (int)gw;
   if ((int)blockIdx.x >= G) return;
   Range8 rg;
   rg.t0 = T * blockIdx.x / G;
   rg.t1 = T * (blockIdx.x + 1) / G;
-  range8_init(rg, prefix, B, Hkv);
+  range8_init<E>(rg, prefix, B, Hkv);
 
   if (warp >= kWarps) {
     // ----------------------------------------------------------- producers --
@@ -688,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return row <= w.pos ? row : kNoRow;
     };
     auto step = [&](Walk8& w, int n) {  // n tiles on, as far as the range goes
-      for (int k = 0; k < n && w.u < w.end; ++k) walk8_next(w, rg, prefix, spos, B, Hkv);
+      for (int k = 0; k < n && w.u < w.end; ++k) walk8_next<E>(w, rg, prefix, spos, B, Hkv);
     };
     int s = 0;          // the ring's stage and pass of the tile at hand
     uint32_t pass = 0;
@@ -719,9 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   p.q + ((size_t)b * p.Hq + (size_t)kvh * g) * kD, q_bytes, full);
     };
     Walk8 w;
-    walk8_start(w, rg, prefix, spos, B, Hkv);
+    walk8_start<E>(w, rg, prefix, spos, B, Hkv);
     if (copies && !LIST) {
-      for (; w.u < w.end; walk8_next(w, rg, prefix, spos, B, Hkv)) {
+      for (; w.u < w.end; walk8_next<E>(w, rg, prefix, spos, B, Hkv)) {
         if (!wait_empty()) break;
         const int z = w.b * Hkv + w.kvh, row = w.k * kTile;
         // failure-path tests only: a tile never issued
@@ -820,12 +851,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     Consumer8<NT> cs;
     cs.c = lane >> 2;
     cs.t = lane & 3;
+    // Two blocks of heads leave no registers for the walk during the tiles: it
+    // lies in shared memory then, and thread 0 moves it on while the others
+    // merge.  (g = 16: 64 -> 58 us for 268 MB; at g = 2 it cost 2%.)
+    constexpr bool kSharedWalk = NT > 1;
+    volatile Walk8* walk = reinterpret_cast<Walk8*>(misc + 24);
     Walk8 w;
-    walk8_start(w, rg, prefix, spos, B, Hkv);
+    if (!kSharedWalk || tid == 0) walk8_start<E>(w, rg, prefix, spos, B, Hkv);
+    if (kSharedWalk) {
+      if (tid == 0) put_walk8(walk, w);
+      csync(lane);
+    }
     int s = 0;
     uint32_t ph = 0;
-    while (w.u < w.end) {
+    while (true) {
+      if (kSharedWalk) w = get_walk8(walk);
+      if (w.u >= w.end) break;
       const int len = (int)min((long long)(w.nt - w.k), w.end - w.u);
+      const int pos = w.pos;
       cs.reset();
       bool ok = true;
       for (int i = 0; i < len; ++i) {
@@ -835,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (i == 0) cs.load_q(qbuf + s * g * kD * 2, g, p.qscale);
         const SliceMeta mt = meta[s * kSlices + warp];
-        const int rows = min(16, w.pos + 1 - mt.row0);
+        const int rows = min(16, pos + 1 - mt.row0);
         const uint8_t* Ks = stages + (size_t)s * kStageBytes + warp * 16 * kD;
         if (rows > 0) cs.slice(Ks, Ks + kOpBytes, rows, mt);
         __syncwarp();
@@ -847,8 +890,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       cs.stash(merge_o, merge_ml, warp, g);
+      if (kSharedWalk) w = get_walk8(walk);
       csync(lane);
       if (*abort_flag) break;
+      Walk8 next = w;
+      if (!kSharedWalk || tid == 0) {
+        if (len < w.nt - w.k) {  // the part of the range ends inside the segment
+          next.u = w.end;
+        } else {
+          walk8_segment<E>(next, prefix, spos, B, Hkv);
+        }
+        walk8_turn<E>(next, rg, prefix, spos, B, Hkv);
+        if (kSharedWalk) put_walk8(walk, next);  // (every warp has read the walk)
+      }
       // ---- this CTA's part: the warps' partials, in warp order -----------
       const bool whole = w.k == 0 && len == w.nt;
       // a part that does not open the range is its last segment's
@@ -887,15 +941,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           misc[2] = last;
         }
         csync(lane);
-        if (misc[2] && !*abort_flag) merge_parts(p, pt, T, G, merge_o, csync, warp, lane);
+        if (misc[2] && !*abort_flag) merge_parts<E>(p, pt, T, G, merge_o, csync, warp, lane);
       }
       if (*abort_flag) break;
-      if (len < w.nt - w.k) {  // the part of the range ends inside the segment
-        w.u = w.end;
-      } else {
-        walk8_segment(w, prefix, spos, B, Hkv);
-      }
-      walk8_turn(w, rg, prefix, spos, B, Hkv);
+      w = next;
     }
   }
   if (*abort_flag) {  // copies in flight land before the shared memory goes
