@@ -38,6 +38,14 @@ __device__ __forceinline__ uint32_t finite_abs_max(uint32_t w) {
   return max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u);
 }
 
+// Largest magnitudes of two pairs of bf16, half by half (as bits: NaN and
+// infinities come out largest).
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t w) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w & 0x7fff7fffu));
+  return d;
+}
+
 // 8 codes moved to another scale: code <- e4m3(code * ratio).
 __device__ __forceinline__ uint2 rescale8(uint2 w, float ratio) {
   uint32_t o[4];
@@ -96,15 +104,18 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
   uint32_t* bound = k_bounds + (seg * nb + j) * 128 + tid;
   const bool bounds = k_bounds != nullptr && tid < 128;
   const uint32_t was = bounds && had ? *bound : 0u;
+  // The block's maxima, two halves of a word at a time.  That takes
+  // infinities and NaN for the largest: where one turns up, the block looks
+  // again, at finite values only.
 #pragma unroll
   for (int op = 0; op < 2; ++op) {
-    uint32_t amax = 0;
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < P; ++i)
-      amax = max(max(max(amax, finite_abs_max(x[op][i].x)), max(finite_abs_max(x[op][i].y),
-                 finite_abs_max(x[op][i].z))), finite_abs_max(x[op][i].w));
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    if (lane == 0) s_max[op][warp] = amax;
+      m = abs_max2(abs_max2(abs_max2(abs_max2(m, x[op][i].x), x[op][i].y), x[op][i].z),
+                   x[op][i].w);
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+    if (lane == 0) s_max[op][warp] = m;
   }
   if (k_bounds != nullptr) {
     uint32_t hi[4], lo[4];
@@ -141,6 +152,20 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
     uint32_t amax = 0;
 #pragma unroll
     for (int w = 0; w < 8; ++w) amax = max(amax, s_max[op][w]);
+    if (amax >= 0x7f80u) {  // the same for the whole block
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        m = max(max(max(m, finite_abs_max(x[op][i].x)), max(finite_abs_max(x[op][i].y),
+                finite_abs_max(x[op][i].z))), finite_abs_max(x[op][i].w));
+      m = __reduce_max_sync(0xffffffffu, m);
+      __syncthreads();  // every thread has read the maxima
+      if (lane == 0) s_max[op][warp] = m;
+      __syncthreads();
+      amax = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) amax = max(amax, s_max[op][w]);
+    }
     const float s_new = block_scale(__uint_as_float(amax << 16));
     const float s = had ? fmaxf(s_old[op], s_new) : s_new;
     // every thread's read of s_old came before the barrier
