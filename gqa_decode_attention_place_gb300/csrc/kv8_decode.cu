@@ -12,11 +12,13 @@
 // blocks' scales are.
 //
 // Bound by memory: a row costs 256 bytes for K and V, half of the bf16
-// cache's.  How:
+// cache's.  4.3 GB (B=256, g=8) take 594 us, 7.2 TB/s; 268 MB (B=32) 48 us at
+// g <= 8 and 58 us at g = 16.  How:
 //  * 128-row tiles (32 KB for K and V) stream through a shared-memory ring by
 //    tiled TMA copies (128-byte swizzle: a row of codes is exactly one
-//    swizzle span) issued by a producer warp that also fetches each 16-row
+//    swizzle span) issued by one producer warp; another fetches each 16-row
 //    slice's scales, four tiles at a time, and leaves them beside the tile.
+//    The query rows come with a segment's first tile.
 //  * 8 consumer warps take 16 rows each.  e4m3 -> fp16 is exact and one
 //    conversion instruction per two values; both products run on warp-level
 //    MMAs (m16n8k16, fp16 in, fp32 out) with rows or dims as M and the heads
