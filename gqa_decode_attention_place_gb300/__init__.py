@@ -129,8 +129,8 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.attn_qk_norm_rope_append.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, f32, vp, vp, vp,
                                              vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
     lib.attn_qk_norm_rope_append.restype = i32
-    lib.attn_kv8_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
-                                    vp]
+    lib.attn_kv8_append.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                    i32, i32, vp]
     lib.attn_kv8_append.restype = i32
     lib.attn_kv8_workspace_size.argtypes = [i32, i32, i32, i32, i32]
     lib.attn_kv8_workspace_size.restype = sz

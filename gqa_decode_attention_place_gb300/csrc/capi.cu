@@ -285,9 +285,10 @@ int attn_qk_norm_rope_append(const void* q, const void* k_new, const void* v_new
                       k_cache, v_cache, stream);
 }
 
-int attn_kv8_append(const void* k_new, const void* v_new, const int32_t* positions,
-                    void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* k_bounds,
-                    int B, int S, int Hkv, int L, int D, int block, cudaStream_t stream) {
+int attn_kv8_append(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                    const int32_t* positions, void* k_cache, void* v_cache, float* k_scale,
+                    float* v_scale, void* k_bounds, int B, int S, int Hkv, int L, int D,
+                    int block, cudaStream_t stream) {
   if (S < 0) return ATTN_ERR_INVALID_ARG;
   if (const int st = kv8_sizes(B, Hkv, Hkv, L, D, block)) return st;
   if (S == 0) return ATTN_OK;
@@ -296,9 +297,12 @@ int attn_kv8_append(const void* k_new, const void* v_new, const int32_t* positio
   if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
       !aligned16(k_bounds) || !aligned4(positions) || !aligned4(k_scale) || !aligned4(v_scale))
     return ATTN_ERR_INVALID_ARG;
+  if (k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D || k_stride % 8 || v_stride % 8)
+    return ATTN_ERR_INVALID_ARG;
   if (S > L) return ATTN_OK;  // no sequence's rows fit: all are skipped
-  return cuda_status(gqa::launch_kv8_append(k_new, v_new, positions, k_cache, v_cache, k_scale,
-                                            v_scale, k_bounds, B, S, Hkv, L, block, stream));
+  return cuda_status(gqa::launch_kv8_append(k_new, v_new, k_stride, v_stride, positions, k_cache,
+                                            v_cache, k_scale, v_scale, k_bounds, B, S, Hkv, L,
+                                            block, stream));
 }
 
 size_t attn_kv8_workspace_size(int B, int Hq, int Hkv, int L, int D) {

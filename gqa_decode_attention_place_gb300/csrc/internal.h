@@ -55,7 +55,8 @@ cudaError_t launch_qk_norm_rope(const void* q, const void* k, const void* v, lon
 // 8-bit cache: append, block scores and selection, decode (block_index null:
 // all rows; else count listed blocks per (sequence, KV head)).
 constexpr int kKv8MaxGrid = 192;  // CTAs of the 8-bit decode (workspace partial slots)
-cudaError_t launch_kv8_append(const void* k_new, const void* v_new, const int32_t* positions,
+cudaError_t launch_kv8_append(const void* k_new, const void* v_new, long long k_stride,
+                              long long v_stride, const int32_t* positions,
                               void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                               void* k_bounds, int B, int S, int Hkv, int L, int block,
                               cudaStream_t stream);

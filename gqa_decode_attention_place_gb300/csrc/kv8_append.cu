@@ -69,9 +69,10 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
 
 template <int P>  // passes of 16 rows: block = 16 * P
 __global__ void __launch_bounds__(256) kv8_append_kernel(
-    const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
-    const int32_t* __restrict__ positions, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
-    float* v_scale, uint32_t* k_bounds, int B, int S, int Hkv, int L, int nb) {
+    const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, long long k_stride,
+    long long v_stride, const int32_t* __restrict__ positions, uint8_t* k_cache,
+    uint8_t* v_cache, float* k_scale, float* v_scale, uint32_t* k_bounds, int B, int S, int Hkv,
+    int L, int nb) {
   constexpr int T = 16 * P;
   __shared__ uint32_t s_max[2][8];
   __shared__ uint32_t s_hi[8][64], s_lo[8][64];
@@ -95,7 +96,9 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
     for (int i = 0; i < P; ++i) {
       const int t = t0 + i * 16;
       x[op][i] = make_uint4(0u, 0u, 0u, 0u);
-      if (t >= 0 && t < S) x[op][i] = (op ? v_new : k_new)[(((size_t)b * S + t) * Hkv + h) * 16 + c];
+      if (t >= 0 && t < S)
+        x[op][i] = (op ? v_new : k_new)[((long long)b * S + t) * (op ? v_stride : k_stride) +
+                                        h * 16 + c];
     }
   float s_old[2] = {0.f, 0.f};
   if (had) {
@@ -203,21 +206,22 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
 
 // One new token per sequence: a warp per (sequence, KV head), its lower half
 // the key and its upper half the value (16 bytes a lane), no block barrier.
-// The new rows go out before the position is read.  (64 sequences, 8 heads:
+// The new rows are fetched before the position is read.  (64 sequences, 8 heads:
 // 5.2 us by the kernel above, 1.7 us by this one.)
 constexpr int kTokenWarps = 4;
 __global__ void __launch_bounds__(kTokenWarps * 32) kv8_append_token_kernel(
-    const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
-    const int32_t* __restrict__ positions, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
-    float* v_scale, uint4* k_bounds, int segs, int Hkv, int L, int nb, int lb) {
+    const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, long long k_stride,
+    long long v_stride, const int32_t* __restrict__ positions, uint8_t* k_cache,
+    uint8_t* v_cache, float* k_scale, float* v_scale, uint4* k_bounds, int segs, int Hkv, int L, int nb, int lb) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int seg = blockIdx.x * kTokenWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (seg >= segs) return;
   const int c = lane & 15;
   const bool op = lane >= 16;  // the value's half
-  const uint4 x = (op ? v_new : k_new)[(size_t)seg * 16 + c];
-  const int pos = positions[seg / Hkv];
+  const int b = seg / Hkv, h = seg - b * Hkv;
+  const uint4 x = (op ? v_new : k_new)[b * (op ? v_stride : k_stride) + h * 16 + c];
+  const int pos = positions[b];
   if (!rows_in_cache(pos, 0, L)) return;  // reported by the decode call
   const int j = pos >> lb, row0 = j << lb;
   const bool had = row0 < pos;
@@ -266,7 +270,8 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv8_append_token_kernel(
 
 }  // namespace
 
-cudaError_t launch_kv8_append(const void* k_new, const void* v_new, const int32_t* positions,
+cudaError_t launch_kv8_append(const void* k_new, const void* v_new, long long k_stride,
+                              long long v_stride, const int32_t* positions,
                               void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                               void* k_bounds, int B, int S, int Hkv, int L, int block,
                               cudaStream_t stream) {
@@ -276,7 +281,7 @@ cudaError_t launch_kv8_append(const void* k_new, const void* v_new, const int32_
     const int lb = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
     return launch_pdl(kv8_append_token_kernel, dim3((segs + kTokenWarps - 1) / kTokenWarps),
                       dim3(kTokenWarps * 32), 0, stream, static_cast<const uint4*>(k_new),
-                      static_cast<const uint4*>(v_new), positions,
+                      static_cast<const uint4*>(v_new), k_stride / 8, v_stride / 8, positions,
                       static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale,
                       v_scale, static_cast<uint4*>(k_bounds), segs, Hkv, L, nb, lb);
   }
@@ -286,8 +291,8 @@ cudaError_t launch_kv8_append(const void* k_new, const void* v_new, const int32_
                 : block == 64 ? kv8_append_kernel<4>
                               : kv8_append_kernel<8>;
   return launch_pdl(kernel, dim3(touched, Hkv, B), dim3(256), 0, stream,
-                    static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), positions,
-                    static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale,
+                    static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new),
+                    k_stride / 8, v_stride / 8, positions, static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale,
                     v_scale, static_cast<uint32_t*>(k_bounds), B, S, Hkv, L, nb);
 }
 

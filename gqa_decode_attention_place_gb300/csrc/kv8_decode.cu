@@ -59,7 +59,7 @@ constexpr int kThreads = kConsumers + 64;   // and the two producer warps
 constexpr int kMaxStages = 6;
 constexpr int kMiscInts = 40;  // [0] abort, [2] last, [8..16) scan, [24..34) a walk
 constexpr int kNoRow = 0x40000000;          // row of a slice that holds nothing
-constexpr float kMInit = -1e30f;            // running maximum before any row
+constexpr float kMInit = -3e38f;            // running maximum before any row
 constexpr float kTau = 8.f;                 // the running maximum may lag by 2^kTau
 constexpr float kShift = 6.f;               // probabilities sit at 2^kShift .. 2^(kShift+kTau)
 constexpr int kMaxSmem = 227 * 1024;

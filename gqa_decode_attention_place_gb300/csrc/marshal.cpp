@@ -256,11 +256,12 @@ PyObject* kv8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t four[4] = {B, S, Hkv, D}, three[3] = {B, Hkv, D};
     const at::IntArrayRef rows =
         k.dim() == 4 ? at::IntArrayRef(four, 4) : at::IntArrayRef(three, 3);
-    auto fn = reinterpret_cast<int (*)(const void*, const void*, const void*, void*, void*, void*,
-                                       void*, void*, int, int, int, int, int, int, void*)>(
-        handle(a[0]));
-    void* kn = c.dense(a[2], "k_new", kBF16, rows);
-    void* vn = c.dense(a[3], "v_new", kBF16, rows);
+    auto fn = reinterpret_cast<int (*)(const void*, const void*, int64_t, int64_t, const void*,
+                                       void*, void*, void*, void*, void*, int, int, int, int, int,
+                                       int, void*)>(handle(a[0]));
+    int64_t kst, vst;
+    void* kn = c.rows(a[2], "k_new", rows, &kst);
+    void* vn = c.rows(a[3], "v_new", rows, &vst);
     void* pos = c.dense(a[4], "positions", kI32, {B});
     void* kc = c.dense(a[5], "k_cache", kE4M3, {B, Hkv, L, D});
     void* vc = c.dense(a[6], "v_cache", kE4M3, {B, Hkv, L, D});
@@ -270,7 +271,7 @@ PyObject* kv8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* stream = handle(a[1]);
     const c10::DeviceGuard guard(c.device);
     const NoGil nogil;
-    return fn(kn, vn, pos, kc, vc, ks, vs, bounds, narrow(B), narrow(S), narrow(Hkv), narrow(L),
+    return fn(kn, vn, kst, vst, pos, kc, vc, ks, vs, bounds, narrow(B), narrow(S), narrow(Hkv), narrow(L),
               narrow(D), (int)block, stream);
   });
 }

@@ -101,9 +101,10 @@ def attn_qk_norm_rope_append(q, k_new, v_new, q_weight, k_weight, eps: float, po
 
 def attn_kv8_append(k_new, v_new, positions, k_cache, v_cache, k_scale, v_scale, block: int,
                     k_bounds=None, stream=None) -> None:
-    """Rows k_new/v_new [B,S,Hkv,D] (or [B,Hkv,D]) into rows positions[b] + t
-    of the 8-bit caches [B,Hkv,L,D], in place, with the blocks' scales
-    [B,Hkv,NB] and, if given, the keys' bounds [B,Hkv,NB,2,D]."""
+    """Rows k_new/v_new [B,S,Hkv,D] (or [B,Hkv,D]; views with a token stride
+    will do) into rows positions[b] + t of the 8-bit caches [B,Hkv,L,D], in
+    place, with the blocks' scales [B,Hkv,NB] and, if given, the keys' bounds
+    [B,Hkv,NB,2,D]."""
     m = _native or _load()
     code = m.kv8_append(_address["attn_kv8_append"], _stream(stream, k_cache), k_new, v_new,
                         positions, k_cache, v_cache, k_scale, v_scale, block, k_bounds)

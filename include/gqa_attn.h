@@ -383,7 +383,9 @@ int attn_qk_norm_rope_append(const void* q, const void* k_new, const void* v_new
  * before rounding to 8 bits.
  *
  * attn_kv8_append -- S new rows per sequence, k_new and v_new [B, S, Hkv, D]
- * bf16, to rows positions[b] .. positions[b] + S - 1.  For every block of a
+ * bf16, to rows positions[b] .. positions[b] + S - 1.  Token b*S + t lies at
+ * k_new + (b*S + t) * k_stride (v_stride) elements, its heads dense; strides are
+ * multiples of 8 and at least Hkv * D.  For every block of a
  * KV head that gets new rows, and for K and V apart:
  *     s_new = 2^e, e the least integer with max |x| <= 448 * 2^e over the
  *             block's new rows x (finite values only)
@@ -400,9 +402,10 @@ int attn_qk_norm_rope_append(const void* q, const void* k_new, const void* v_new
  * A sequence whose rows are not all in [0, L) is skipped (the decode call
  * reports it).  Supported: B <= 8192, Hkv <= 1024, L <= 2^24.
  */
-int attn_kv8_append(const void* k_new, const void* v_new, const int32_t* positions,
-                    void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* k_bounds,
-                    int B, int S, int Hkv, int L, int D, int block, cudaStream_t stream);
+int attn_kv8_append(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                    const int32_t* positions, void* k_cache, void* v_cache, float* k_scale,
+                    float* v_scale, void* k_bounds, int B, int S, int Hkv, int L, int D,
+                    int block, cudaStream_t stream);
 
 /*
  * attn_kv8_workspace_size -- bytes of device workspace the 8-bit decode calls
@@ -440,7 +443,7 @@ int attn_decode_step_kv8(const void* q, const int32_t* positions, const void* k_
  *     scores[b,hk,j] = sum_h sum_d max(q[b,h,d] * max_jd, q[b,h,d] * min_jd)
  * over the heads h of KV head hk, from k_bounds; -inf for blocks past
  * positions[b] / block (and for all blocks of a position outside [0, L)).
- * Their bounds are not read.  fp32 sums.
+ * Their bounds are not read.  fp32 sums.  (A bound for positive score scales.)
  *
  *   scores : [B, Hkv, NB] fp32.
  *   Sizes as attn_decode_step_kv8.  The bounds are taken as finite.

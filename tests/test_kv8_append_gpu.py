@@ -83,6 +83,25 @@ def test_without_bounds_and_3d_rows():
     assert torch.equal(st["kc"].view(torch.uint8), four["kc"].view(torch.uint8))
 
 
+@pytest.mark.parametrize("S", [1, 45])
+def test_rows_as_views_of_a_fused_buffer(S):
+    """Keys and values at a token stride of their projections' buffer; the same with and without
+    the token axis for one token."""
+    B, Hq, Hkv, L, block = 3, 4, 2, 90, 32
+    st = _state(B, S, Hkv, L, block, seed=10)
+    qkv = torch.randn((B, S, Hq + 2 * Hkv, D), device="cuda").bfloat16()
+    st["kn"], st["vn"] = qkv[:, :, Hq:Hq + Hkv], qkv[:, :, Hq + Hkv:]
+    if S == 1:
+        alone = {k: v.clone() for k, v in st.items() if k not in ("kn", "vn")}
+        pos = torch.tensor([0, 31, 45], dtype=torch.int32, device="cuda")
+        ga.attn_kv8_append(st["kn"][:, 0], st["vn"][:, 0], pos, alone["kc"], alone["vc"],
+                           alone["ks"], alone["vs"], block, k_bounds=alone["bounds"])
+    _check(st, [0, 31, 45], block)
+    if S == 1:
+        for k in alone:
+            assert torch.equal(alone[k].view(torch.uint8), st[k].view(torch.uint8))
+
+
 def test_non_finite_values():
     """NaN is kept as a NaN code, infinities saturate, and neither sets the scale; a block of
     nothing finite takes the smallest scale; NaN leaves the bounds alone."""

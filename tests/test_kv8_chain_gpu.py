@@ -43,7 +43,7 @@ class Stream:
                                     self.w[0], self.w[1], 1e-6, pos, self.cos, self.sin)
         zero = torch.zeros(B, dtype=torch.int32, device="cuda")
         ga.attn_kv8_append(k.view(B, S, self.Hkv, D),
-                           qkv[:, :, self.Hq + self.Hkv:].contiguous(), zero, self.kc, self.vc,
+                           qkv[:, :, self.Hq + self.Hkv:], zero, self.kc, self.vc,
                            self.ks, self.vs, self.block, k_bounds=self.bounds)
 
     def step(self, qkv, v, pos, stream=None):

@@ -71,6 +71,17 @@ def test_large_batch_of_short_sequences():
     _check(_run(st, 16), st, 130, 16, pos, seqs=range(0, B, 13))
 
 
+def test_largest_batch():
+    """8192 sequences at 16 heads to a KV head: the fewest pipeline stages beside their scan."""
+    B = 8192
+    pos = [(b * 7) % 40 for b in range(B)]
+    st = _case(B, 2, 16, 40, 16, pos, seed=53)
+    _check(_run(st, 16), st, 40, 16, pos, seqs=range(0, B, 331))
+    index = torch.tensor([2, 0], dtype=torch.int32, device="cuda").expand(B, 2, 2).contiguous()
+    _check(_run_blocks(st, 16, index), st, 40, 16, pos, index=index.tolist(),
+           seqs=range(0, B, 331))
+
+
 @pytest.mark.parametrize("lo,hi", [(-60, -20), (-60, 61), (40, 61)])
 def test_block_scales_far_apart(lo, hi):
     """V scales over the whole range: a probability must keep its weight whatever its block's

@@ -45,18 +45,19 @@ def test_norm_rope_append(lib):
 
 
 def test_kv8_append(lib):
-    def call(kn=P, vn=P, pos=P, kc=P, vc=P, ks=P, vs=P, bounds=P, B=1, S=1, Hkv=8, L=64, D=128,
-             block=64):
-        return lib.attn_kv8_append(kn, vn, pos, kc, vc, ks, vs, bounds, B, S, Hkv, L, D, block,
-                                   None)
+    def call(kn=P, vn=P, kst=1024, vst=1024, pos=P, kc=P, vc=P, ks=P, vs=P, bounds=P, B=1, S=1,
+             Hkv=8, L=64, D=128, block=64):
+        return lib.attn_kv8_append(kn, vn, kst, vst, pos, kc, vc, ks, vs, bounds, B, S, Hkv, L, D,
+                                   block, None)
     for bad in (dict(kn=None), dict(vn=None), dict(pos=None), dict(kc=None), dict(vc=None),
                 dict(ks=None), dict(vs=None), dict(kn=P + 8), dict(bounds=P + 8), dict(ks=P + 2),
-                dict(B=0), dict(S=-1), dict(Hkv=0), dict(L=0), dict(D=0), dict(block=0)):
+                dict(B=0), dict(S=-1), dict(Hkv=0), dict(L=0), dict(D=0), dict(block=0),
+                dict(kst=1016), dict(vst=1023), dict(vst=0)):
         assert call(**bad) == INVALID, bad
     for bad in (dict(D=64), dict(block=8), dict(block=48), dict(block=256), dict(B=8193),
                 dict(Hkv=1025), dict(L=(1 << 24) + 1)):
         assert call(**bad) == UNSUPPORTED, bad
-    assert call(S=0) == 0
+    assert call(S=0) == 0 and call(S=65) == 0  # nothing to append; no row fits
 
 
 def test_kv8_decode(lib):
