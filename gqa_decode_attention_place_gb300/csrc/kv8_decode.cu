@@ -12,13 +12,14 @@
 // blocks' scales are.
 //
 // Bound by memory: a row costs 256 bytes for K and V, half of the bf16
-// cache's.  4.3 GB (B=256, g=8) take 594 us, 7.2 TB/s; 268 MB (B=32) 48 us at
-// g <= 8 and 58 us at g = 16.  How:
+// cache's.  4.3 GB (B=256, g=8) take 596 us, 7.2 TB/s; 268 MB (B=32) 47 us at
+// g = 2, 50 at g = 8 and 58 at g = 16.  How:
 //  * 128-row tiles (32 KB for K and V) stream through a shared-memory ring by
 //    tiled TMA copies (128-byte swizzle: a row of codes is exactly one
 //    swizzle span) issued by one producer warp; another fetches each 16-row
-//    slice's scales, four tiles at a time, and leaves them beside the tile.
-//    The query rows come with a segment's first tile.
+//    slice's scales, four tiles at a time, and leaves them beside the tile,
+//    with flags for where a segment starts and ends.  The query rows come with
+//    a segment's first tile.
 //  * 8 consumer warps take 16 rows each.  e4m3 -> fp16 is exact and one
 //    conversion instruction per two values; both products run on warp-level
 //    MMAs (m16n8k16, fp16 in, fp32 out) with rows or dims as M and the heads
@@ -29,10 +30,13 @@
 //    transposing 8-bit matrix loads; no bank conflicts, no code moved between
 //    lanes.  The conversions are what the warps spend most of their issue
 //    slots on (96 of about 250 instructions a slice).
-//  * A flat list of all tiles is split evenly over the grid (one CTA per SM);
-//    a segment split over CTAs is merged by the CTA that arrives last, in
-//    CTA order, so results do not depend on timing.  For few segments a
-//    thread-block cluster takes each (kv8_cluster.cuh).
+//  * A flat list of all tiles is split evenly over the grid (one CTA per SM).
+//    At a segment's end the consumers leave their partials in shared memory
+//    and go on; two further warps merge them (512 x 8 segments of one tile:
+//    55 -> 44 us).  A segment split over CTAs is merged by the CTA that
+//    arrives last, in CTA order, so results do not depend on timing; short
+//    ones are not split.  For few segments a thread-block cluster takes each
+//    (kv8_cluster.cuh).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -55,9 +59,12 @@ constexpr int kOpBytes = kTile * kD;        // 16 KB per operand
 constexpr int kStageBytes = 2 * kOpBytes;
 constexpr int kWarps = kSlices;             // consumer warps
 constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 64;   // and the two producer warps
+constexpr int kMergeThreads = 64;           // two warps that merge (flat list)
+constexpr int kThreads = kConsumers + 64 + kMergeThreads;  // and two producer warps
+constexpr int kClusterThreads = kConsumers + 64;
 constexpr int kMaxStages = 6;
-constexpr int kMiscInts = 40;  // [0] abort, [2] last, [8..16) scan, [24..34) a walk
+constexpr int kMiscInts = 40;  // [0] abort, [2] last, [3] segments left over, [8..16) scan,
+                               // [24..40) those segments
 constexpr int kNoRow = 0x40000000;          // row of a slice that holds nothing
 constexpr float kMInit = -3e38f;            // running maximum before any row
 constexpr float kTau = 8.f;                 // the running maximum may lag by 2^kTau
@@ -65,16 +72,21 @@ constexpr float kShift = 6.f;               // probabilities sit at 2^kShift .. 
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kWholeTiles = 4;              // segments this short are not split
 
+constexpr int kRowsMask = 0xff;
+constexpr int kStarts = 0x100;              // a piece starts with this tile
+constexpr int kEnds = 0x200;                // and ends with this one
+constexpr int kLast = 0x400;                // the CTA's last tile
+
 struct SliceMeta {
-  int row0;       // first row, or kNoRow
+  int rows;       // how many of the slice's rows count (0..16), and the tile's flags
   float ks;       // K scale
   float lv;       // log2 of the V scale
   float inv_vs;   // 1 / V scale
 };
 
-__device__ __forceinline__ SliceMeta slice_meta(int row, float ks, float vs) {
+__device__ __forceinline__ SliceMeta slice_meta(int rows, float ks, float vs) {
   SliceMeta mt;
-  mt.row0 = row;
+  mt.rows = rows;
   mt.ks = ks;
   // log2 of a power of two comes out exact
   const uint32_t bits = __float_as_uint(vs);
@@ -105,8 +117,8 @@ struct Kv8Params {
 };
 
 // Shared memory: the ring, per stage the q rows of a piece that starts there
-// and the slices' scales, the warps' partials, barriers, and per sequence the
-// tiles before it and its position.
+// and the slices' scales, the warps' partials (twice where they are small),
+// barriers, and per sequence the units before it and its position.
 constexpr int kMergeRow = kD + 8;
 __host__ __device__ constexpr int merge_heads(int g) { return (g + 1) & ~1; }
 __host__ __device__ constexpr int merge_row(int warp, int h, int g) {
@@ -115,9 +127,11 @@ __host__ __device__ constexpr int merge_row(int warp, int h, int g) {
 __host__ __device__ constexpr int merge_floats(int g) {
   return kWarps * (merge_heads(g) * kMergeRow + 2 * g);
 }
+__host__ __device__ constexpr int merge_buffers(int g) { return g <= 8 ? 2 : 1; }
 inline size_t smem_bytes(int stages, int B, int g) {
-  return (size_t)stages * (kStageBytes + g * kD * 2 + kSlices * sizeof(SliceMeta) + 16) + 16 +
-         (size_t)merge_floats(g) * 4 + kMiscInts * 4 + ((size_t)2 * B + 1) * 4;
+  return (size_t)stages * (kStageBytes + g * kD * 2 + kSlices * sizeof(SliceMeta) + 16) + 7 * 8 +
+         (size_t)merge_buffers(g) * merge_floats(g) * 4 + kMiscInts * 4 +
+         ((size_t)2 * B + 1) * 4;
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -145,10 +159,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 // A tile's place in the flat (sequence, KV head, tile) order.  The order is
 // counted in units: a segment of nt tiles takes nt + E, its tiles and E for
-// what its end costs (measured: 1.2 tiles' time at g = 2, 1.5 at g = 8, 2.1 at
-// g = 16), so that an even split of the units is an even split of the work
-// however short the segments are.
-template <int NT> constexpr int kEndUnits = NT;
+// what its end costs, so that an even split of the units is an even split of
+// the work however short the segments are (64 ragged segments of up to 64
+// tiles a head, g = 16: 150 -> 112 us when it came in).
+template <int NT> constexpr int kEndUnits = NT == 1 ? 1 : 3;
 struct Walk8 {
   long long u, end;  // the unit at hand; the end of the part of the range it lies in
   int b, kvh, k, nt, pos;
@@ -194,18 +208,38 @@ __device__ __forceinline__ void walk8_init(Walk8& w, long long u, const int* pre
   w.pos = spos[lo];
   if (w.k >= w.nt) walk8_segment<E>(w, prefix, spos, B, Hkv);
 }
+// CTA c's range.  An even share, but a boundary inside a segment of at most
+// kShortTiles tiles moves to that segment's nearer end: such a segment is not
+// worth a merge through L2 (340 of one or two tiles: 18.4 -> 11.8 us).  (A longer segment's parts stay where the even
+// shares put them: cta_of.)
+constexpr int kShortTiles = 4;
 template <int E>
-__device__ __forceinline__ void range8_init(Range8& r, const int* prefix, int B, int Hkv) {
-  int lo = 0, hi = B - 1;  // largest b with Hkv*prefix[b] <= t1 - 1
+__device__ __forceinline__ long long boundary8(long long u, long long T, const int* prefix, int B,
+                                               int Hkv, long long& f0, int& n) {
+  f0 = u;
+  n = 0;
+  if (u >= T) return T;
+  int lo = 0, hi = B - 1;  // largest b with Hkv*prefix[b] <= u
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if ((long long)Hkv * prefix[mid] <= r.t1 - 1) lo = mid; else hi = mid - 1;
+    if ((long long)Hkv * prefix[mid] <= u) lo = mid; else hi = mid - 1;
   }
-  const int n = prefix[lo + 1] - prefix[lo];
-  const int k = (int)((uint32_t)(r.t1 - 1 - (long long)Hkv * prefix[lo]) % (uint32_t)n);
-  const long long f0 = r.t1 - 1 - k;  // the segment's first unit; its tiles are f0 .. f0+n-E-1
-  // (from t0 + E on: the units before f0 end another segment and hold no tile)
-  r.tA = k + 1 < n - E && f0 > r.t0 + E ? f0 : r.t1;
+  n = prefix[lo + 1] - prefix[lo];
+  const int k = (int)((uint32_t)(u - (long long)Hkv * prefix[lo]) % (uint32_t)n);
+  f0 = u - k;  // the segment's first unit; its tiles are f0 .. f0+n-E-1
+  if (k > 0 && n - E <= kShortTiles) return 2 * k < n ? f0 : f0 + n;
+  return u;
+}
+template <int E>
+__device__ __forceinline__ void range8_init(Range8& r, long long T, int c, int G,
+                                            const int* prefix, int B, int Hkv) {
+  long long f0;
+  int n;
+  r.t0 = boundary8<E>(T * c / G, T, prefix, B, Hkv, f0, n);
+  r.t1 = boundary8<E>(T * (c + 1) / G, T, prefix, B, Hkv, f0, n);
+  // tiles of the segment both before t1 (from f0 on) and behind it; before f0,
+  // the units up to t0 + E may end another segment and hold no tile
+  r.tA = f0 < r.t1 && r.t1 < f0 + n - E && f0 > r.t0 + E ? f0 : r.t1;
 }
 // The range's first tile in this order.
 template <int E>
@@ -229,27 +263,6 @@ __device__ __forceinline__ void walk8_next(Walk8& w, const Range8& r, const int*
   ++w.u;
   if (++w.k == w.nt) walk8_segment<E>(w, prefix, spos, B, Hkv);
   walk8_turn<E>(w, r, prefix, spos, B, Hkv);
-}
-
-__device__ __forceinline__ void put_walk8(volatile Walk8* to, const Walk8& w) {
-  to->u = w.u;
-  to->end = w.end;
-  to->b = w.b;
-  to->kvh = w.kvh;
-  to->k = w.k;
-  to->nt = w.nt;
-  to->pos = w.pos;
-}
-__device__ __forceinline__ Walk8 get_walk8(const volatile Walk8* from) {
-  Walk8 w;
-  w.u = from->u;
-  w.end = from->end;
-  w.b = from->b;
-  w.kvh = from->kvh;
-  w.k = from->k;
-  w.nt = from->nt;
-  w.pos = from->pos;
-  return w;
 }
 
 // 16 rows x 16 codes of two 16-code columns, transposed (lane l gives the
@@ -470,71 +483,76 @@ __device__ __forceinline__ void merge_warps8(const float* mo, const float* mml, 
   }
 }
 
-// A segment split over CTAs c0 .. c0 + n - 1; f0: its first unit.
+// A segment split over CTAs c0 .. c0 + n - 1.
 struct Part8 {
-  long long f0;
   size_t out_at;
   int c0, n;
 };
+static_assert(2 * sizeof(Part8) <= 16 * 4, "two fit behind misc[24]");
 
-// Merge the parts of a split segment, in CTA order, by the consumer warps.
-// Few parts: every thread loads all of its column's in one round trip.  More:
-// the parts' (max, sum) come first, then the outputs, a float4 per thread and
-// part, heads x 32 columns, and where those leave threads over (g < 8) the
-// parts are dealt out among them as well.
+__device__ __forceinline__ void store_column(const Kv8Params& p, size_t out_at, int col,
+                                             const float4& o, float ls) {
+  const float inv = ls == 0.f ? 0.f : 1.f / ls;
+  *reinterpret_cast<uint2*>(p.out + out_at + (size_t)col * 4) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+}
+// Where part r of a segment lies: a CTA holds at most one segment's first part
+// and at most one later part.
+__device__ __forceinline__ int part_slot(const Part8& pt, int r) {
+  return 2 * (pt.c0 + r) + (r == 0);
+}
+
+// Merge the parts of a split segment, in CTA order.  Few parts, by the merge
+// warps: every thread loads all of its column's in one round trip.
 constexpr int kFewParts = 4;
-template <int E>
-__device__ __forceinline__ void merge_parts(const Kv8Params& p, const Part8& pt, long long T,
-                                            int G, float* buf, ConsumerSync& csync, int warp,
-                                            int lane) {
-  const int g = p.g, tid = warp * 32 + lane, n = pt.n;
-  // CTA c0's part is its second unless the segment opens its range, right
-  // away or after the end units of the one before
-  const int slot0 = 2 * pt.c0 + (T * pt.c0 / G >= pt.f0 - E ? 0 : 1);
-  auto slot = [&](int r) { return r == 0 ? slot0 : 2 * (pt.c0 + r); };
-  const int cols = g * (kD / 4);
-  auto store = [&](int col, const float4& o, float inv) {
-    *reinterpret_cast<uint2*>(p.out + pt.out_at + (size_t)col * 4) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  };
-  if (n <= kFewParts) {
-    for (int col = tid; col < cols; col += kConsumers) {
-      const int h = col / (kD / 4);
-      float2 ml[kFewParts];
-      float4 x[kFewParts];
-      float M = kMInit;
+__device__ __forceinline__ void merge_few(const Kv8Params& p, const Part8& pt, int tid) {
+  const int g = p.g;
+  for (int col = tid; col < g * (kD / 4); col += kMergeThreads) {
+    const int h = col / (kD / 4);
+    float2 ml[kFewParts];
+    float4 x[kFewParts];
+    float M = kMInit;
 #pragma unroll
-      for (int r = 0; r < kFewParts; ++r) {
-        ml[r] = make_float2(kMInit, 0.f);
-        x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < n) {
-          ml[r] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((size_t)slot(r) * g + h) * 2));
-          x[r] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (size_t)slot(r) * g * kD) + col);
-        }
+    for (int r = 0; r < kFewParts; ++r) {
+      ml[r] = make_float2(kMInit, 0.f);
+      x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < pt.n) {
+        const size_t at = (size_t)part_slot(pt, r) * g;
+        ml[r] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (at + h) * 2));
+        x[r] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kD) + col);
       }
-#pragma unroll
-      for (int r = 0; r < kFewParts; ++r) M = fmaxf(M, ml[r].x);
-      float ls = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int r = 0; r < kFewParts; ++r) {
-        const float e = ex2(ml[r].x - M);
-        ls = fmaf(ml[r].y, e, ls);
-        o.x = fmaf(x[r].x, e, o.x);
-        o.y = fmaf(x[r].y, e, o.y);
-        o.z = fmaf(x[r].z, e, o.z);
-        o.w = fmaf(x[r].w, e, o.w);
-      }
-      store(col, o, ls == 0.f ? 0.f : 1.f / ls);
     }
-    return;
+#pragma unroll
+    for (int r = 0; r < kFewParts; ++r) M = fmaxf(M, ml[r].x);
+    float ls = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kFewParts; ++r) {
+      const float e = ex2(ml[r].x - M);
+      ls = fmaf(ml[r].y, e, ls);
+      o.x = fmaf(x[r].x, e, o.x);
+      o.y = fmaf(x[r].y, e, o.y);
+      o.z = fmaf(x[r].z, e, o.z);
+      o.w = fmaf(x[r].w, e, o.w);
+    }
+    store_column(p, pt.out_at, col, o, ls);
   }
+}
+
+// More, by the consumer warps once the CTA's tiles are done, with `buf` (the
+// ring's memory) in shared memory: the parts' (max, sum) come first, then the
+// outputs, a float4 per thread and part, heads x 32 columns, and where those
+// leave threads over (g < 8) the parts are dealt out among them as well.
+__device__ __forceinline__ void merge_many(const Kv8Params& p, const Part8& pt, float* buf,
+                                           ConsumerSync& csync, int warp, int lane) {
+  const int g = p.g, tid = warp * 32 + lane, n = pt.n;
+  const int cols = g * (kD / 4);
   float* wt = buf;              // [n][g] maxima, then weights
-  float* ls = buf + n * g;      // [n][g] sums
+  float* ls = buf + n * g;      // [n][g] sums; row 0 then holds the totals
   for (int i = tid; i < n * g; i += kConsumers) {
     const int r = i / g, h = i - r * g;
-    const float2 ml =
-        __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((size_t)slot(r) * g + h) * 2));
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(
+        p.part_ml + ((size_t)part_slot(pt, r) * g + h) * 2));
     wt[i] = ml.x;
     ls[i] = ml.y;
   }
@@ -552,7 +570,7 @@ __device__ __forceinline__ void merge_parts(const Kv8Params& p, const Part8& pt,
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     __syncwarp();
-    if (lane == 0) ls[h] = sum == 0.f ? 0.f : 1.f / sum;  // row 0's own sum has been read
+    if (lane == 0) ls[h] = sum;  // row 0's own sum has been read
   }
   csync(lane);
   const int deal = max(1, kConsumers / cols);  // threads that share a column
@@ -565,8 +583,8 @@ __device__ __forceinline__ void merge_parts(const Kv8Params& p, const Part8& pt,
       const int h = col / (kD / 4);
 #pragma unroll 4
       for (int r = deal > 1 ? who : 0; r < n; r += deal) {
-        const float4 x =
-            __ldcg(reinterpret_cast<const float4*>(p.part_o + (size_t)slot(r) * g * kD) + col);
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(
+                                    p.part_o + (size_t)part_slot(pt, r) * g * kD) + col);
         const float e = wt[r * g + h];
         o.x = fmaf(x.x, e, o.x);
         o.y = fmaf(x.y, e, o.y);
@@ -587,19 +605,12 @@ __device__ __forceinline__ void merge_parts(const Kv8Params& p, const Part8& pt,
         }
       }
     }
-    if (on && (deal == 1 || who == 0)) store(col, o, ls[col / (kD / 4)]);
+    if (on && (deal == 1 || who == 0)) store_column(p, pt.out_at, col, o, ls[col / (kD / 4)]);
   }
   csync(lane);  // buf may be written again
 }
-// What merge_parts keeps in the merge buffer: (max, sum) of every part, and the
-// dealt-out columns where heads leave threads over.
-constexpr bool merge_fits(int g) {
-  return 2 * kKv8MaxGrid * g + 3 + (g * (kD / 4) * 2 <= kConsumers ? kConsumers * 4 : 0) <=
-         merge_floats(g);
-}
-static_assert(merge_fits(1) && merge_fits(2) && merge_fits(3) && merge_fits(4) && merge_fits(5) &&
-                  merge_fits(8) && merge_fits(9) && merge_fits(16),
-              "the parts' statistics fit the merge buffer");
+// The statistics of all parts and the dealt-out columns fit two stages.
+static_assert((2 * kKv8MaxGrid * 16 + 4 + 4 * kConsumers) * 4 <= 2 * kStageBytes, "merge_many");
 
 template <int NT, bool LIST>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -612,10 +623,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int B = p.B, Hkv = p.Hkv, L = p.L, g = p.g;
   uint8_t* qbuf = smem + (size_t)NS * kStageBytes;                             // [NS][g][kD] bf16
   SliceMeta* meta = reinterpret_cast<SliceMeta*>(qbuf + NS * g * kD * 2);      // [NS][kSlices]
-  float* merge_o = reinterpret_cast<float*>(meta + NS * kSlices);              // merge_row
-  float* merge_ml = merge_o + kWarps * merge_heads(g) * kMergeRow;             // [warps][g][2]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(merge_ml + kWarps * g * 2);         // full, empty, sync
-  int* misc = reinterpret_cast<int*>(bars + 2 * NS + 2);  // [0] abort, [2..4) last, [8..24) scan
+  // [merge_buffers] of merge_row rows, then (max, sum) [warps][g]
+  const int n_buf = merge_buffers(g), buf_floats = merge_floats(g);
+  float* merge = reinterpret_cast<float*>(meta + NS * kSlices);
+  const int ml_at = kWarps * merge_heads(g) * kMergeRow;
+  // full [NS], empty [NS], consumers' sync, merge full [2], empty [2], merged
+  uint64_t* bars = reinterpret_cast<uint64_t*>(merge + n_buf * buf_floats);
+  uint64_t* m_full = bars + 2 * NS + 1;
+  uint64_t* m_empty = m_full + 2;
+  uint64_t* merged = m_empty + 2;
+  uint64_t* m_sync = merged + 1;  // the merge warps' own barrier
+  int* misc = reinterpret_cast<int*>(m_sync + 1);
   int* prefix = misc + kMiscInts;                         // [B+1]
   int* spos = prefix + B + 1;                             // [B]
 
@@ -628,7 +646,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars[NS + s]), kWarps);
     }
     mbar_init(smem_u32(&bars[2 * NS]), kWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&m_full[i]), kWarps);               // every consumer warp has stashed
+      mbar_init(smem_u32(&m_empty[i]), kMergeThreads / 32);  // both merge warps have read
+    }
+    mbar_init(smem_u32(merged), 1);  // the merge warps are done
+    mbar_init(smem_u32(m_sync), kMergeThreads / 32);
     misc[0] = 0;
+    misc[3] = 0;
     fence_mbar_init();
   }
   grid_dependency_wait();
@@ -684,11 +709,74 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = (int)gw;
   if ((int)blockIdx.x >= G) return;
   Range8 rg;
-  rg.t0 = T * blockIdx.x / G;
-  rg.t1 = T * (blockIdx.x + 1) / G;
-  range8_init<E>(rg, prefix, B, Hkv);
+  range8_init<E>(rg, T, blockIdx.x, G, prefix, B, Hkv);
+  if (rg.t0 >= rg.t1) return;
+  Walk8 w;
+  walk8_start<E>(w, rg, prefix, spos, B, Hkv);
+  if (w.u >= w.end) return;  // end units alone
 
-  if (warp >= kWarps) {
+  if (warp >= kWarps + 2) {
+    // --------------------------------------------------------------- merge --
+    // The consumers leave each piece's partials in a buffer and go on; these
+    // two warps merge them and write the output, or, for a piece that is only
+    // part of its segment, the CTA's partial, and settle who merges the parts.
+    const int mtid = tid - kConsumers - 64;
+    ConsumerSync msync{smem_u32(m_sync), abort_flag, p.status, 0u};
+    for (int k = 0; w.u < w.end; ++k) {
+      const int len = (int)min((long long)(w.nt - w.k), w.end - w.u);
+      const bool whole = w.k == 0 && len == w.nt;
+      const int slot = 2 * blockIdx.x + (w.k == 0);  // part_slot
+      const size_t out_at = ((size_t)w.b * p.Hq + (size_t)w.kvh * g) * kD;
+      const int buf = n_buf == 2 ? k & 1 : 0;
+      const uint32_t use = (uint32_t)(n_buf == 2 ? k >> 1 : k);
+      if (!consumer_wait(smem_u32(&m_full[buf]), use & 1u, abort_flag, p.status, lane)) break;
+      const float* mo = merge + buf * buf_floats;
+#pragma unroll 2
+      for (int i = mtid; i < g * (kD / 4); i += kMergeThreads) {
+        float M, ls;
+        float4 os;
+        merge_warps8(mo, mo + ml_at, i, g, M, ls, os);
+        if (whole) {
+          store_column(p, out_at, i, os, ls);
+        } else {
+          reinterpret_cast<float4*>(p.part_o + (size_t)slot * g * kD)[i] = os;
+          if (i % (kD / 4) == 0)
+            *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * g + i / (kD / 4)) * 2) =
+                make_float2(M, ls);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&m_empty[buf]));
+      if (!whole) {
+        // the segment's last CTA to arrive merges the parts
+        const long long f0 = w.u - w.k;  // its first unit
+        Part8 pt;
+        pt.out_at = out_at;
+        pt.c0 = cta_of(f0, T, G);
+        pt.n = cta_of(f0 + w.nt - 1, T, G) - pt.c0 + 1;
+        msync(lane);
+        if (mtid == 0) {
+          uint32_t* counter = &p.counters[w.b * Hkv + w.kvh];
+          __threadfence();  // (the other threads' stores came before the barrier)
+          const bool last = atomicAdd(counter, 1u) + 1 == (uint32_t)pt.n;
+          if (last) *counter = 0;
+          __threadfence();
+          misc[2] = last;
+          if (last && pt.n > kFewParts)  // left to the consumers; at most two (first and last)
+            reinterpret_cast<Part8*>(misc + 24)[misc[3]++] = pt;
+        }
+        msync(lane);
+        if (misc[2] && pt.n <= kFewParts && !*abort_flag) merge_few(p, pt, mtid);
+      }
+      if (len < w.nt - w.k) {  // the part of the range ends inside the segment
+        w.u = w.end;
+      } else {
+        walk8_segment<E>(w, prefix, spos, B, Hkv);
+      }
+      walk8_turn<E>(w, rg, prefix, spos, B, Hkv);
+    }
+    if (mtid == 0) mbar_arrive(smem_u32(merged));
+  } else if (warp >= kWarps) {
     // ----------------------------------------------------------- producers --
     // Warp kWarps issues the copies, warp kWarps + 1 brings the scales; a tile is full
     // when both have arrived and the copies have landed.
@@ -721,6 +809,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       return row <= w.pos ? row : kNoRow;
     };
     auto step = [&](Walk8& w, int n) {  // n tiles on, as far as the range goes
+      if (w.k + n < w.nt && w.u + n < w.end) {
+        w.k += n;
+        w.u += n;
+        return;
+      }
       for (int k = 0; k < n && w.u < w.end; ++k) walk8_next<E>(w, rg, prefix, spos, B, Hkv);
     };
     int s = 0;          // the ring's stage and pass of the tile at hand
@@ -751,8 +844,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_load(smem_u32(qbuf + s * g * kD * 2),
                   p.q + ((size_t)b * p.Hq + (size_t)kvh * g) * kD, q_bytes, full);
     };
-    Walk8 w;
-    walk8_start<E>(w, rg, prefix, spos, B, Hkv);
     if (copies && !LIST) {
       for (; w.u < w.end; walk8_next<E>(w, rg, prefix, spos, B, Hkv)) {
         if (!wait_empty()) break;
@@ -769,184 +860,146 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         turn();
       }
-    } else if (copies) {
-      step(w, ti);  // this lane's tile of the batch at hand
-      int blk = w.u < w.end ? fetch(w) : -1;
-      bool ok = true;
-      while (ok) {
-        const bool on = w.u < w.end;
-        const int n_q = __popc(__ballot_sync(0xffffffffu, on)) >> 3;  // tiles of the batch
-        if (n_q == 0) break;
-        const int row = on ? row_of(w, blk) : kNoRow, b = w.b, kvh = w.kvh, k = w.k;
-        const bool starts = w.k == 0 || w.u == rg.t0;
-        const int z = b * Hkv + kvh;
-        step(w, 4);
-        blk = w.u < w.end ? fetch(w) : -1;
-        const bool skip = p.test_skip >= 0 && z == 0 && k == p.test_skip;
-        const bool have = !skip && row != kNoRow && in_block == 0 &&
-                          range_ok(row >= 0 && row < L && z < B * Hkv, p.status);
-        const uint32_t boxes = __ballot_sync(0xffffffffu, have);
-        for (int q = 0; q < n_q; ++q) {
-          if (!wait_empty()) {
-            ok = false;
-            break;
-          }
-          const uint32_t full = smem_u32(&bars[s]);
-          if (lane == 8 * q && !skip)
-            expect(full, __popc((boxes >> (8 * q)) & 0xffu) * (uint32_t)entry_rows * 2u * kD,
-                   starts, b, kvh);
-          __syncwarp();
-          if (ti == q && have) {
-            const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes) + slice * 16 * kD;
-            tma_load_3d(sK, &tm_k, 0, row, z, full);
-            tma_load_3d(sK + kOpBytes, &tm_v, 0, row, z, full);
-          }
-          turn();
-        }
-      }
     } else {
-      step(w, ti);
-      auto look_up = [&](int blk, int& row, float& ks, float& vs) {
-        row = w.u < w.end ? row_of(w, blk) : kNoRow;
-        ks = vs = 1.f;
-        if (row != kNoRow) {
-          const size_t at = (size_t)(w.b * Hkv + w.kvh) * p.nb + (row >> p.lb);
-          ks = p.k_scale[at];
-          vs = p.v_scale[at];
-        }
+      long long last_end = w.end;  // of the part of the range done last
+      if (rg.tA < rg.t1) {
+        Walk8 rest;
+        walk8_init<E>(rest, rg.t0, prefix, spos, B, Hkv);
+        if (rest.u < rg.tA) last_end = rg.tA;
+      }
+      // What a lane knows of its tile, and of the next batch's.
+      struct Mine {
+        int row, z, k, flags;
+        float ks, vs;
+        bool on;
       };
-      int row;
-      float ks, vs;
-      bool on = w.u < w.end;
-      look_up(LIST && on ? fetch(w) : -1, row, ks, vs);
+      auto look_up = [&](int blk) -> Mine {
+        Mine m;
+        m.on = w.u < w.end;
+        m.z = w.b * Hkv + w.kvh;
+        m.k = w.k;
+        m.row = m.on ? row_of(w, blk) : kNoRow;
+        m.ks = m.vs = 1.f;
+        m.flags = 0;
+        if (m.on) {
+          if (!copies && m.row != kNoRow) {
+            const size_t at = (size_t)m.z * p.nb + (m.row >> p.lb);
+            m.ks = p.k_scale[at];
+            m.vs = p.v_scale[at];
+            m.flags = min(16, w.pos + 1 - m.row);
+          }
+          if (w.k == 0 || w.u == rg.t0) m.flags |= kStarts;
+          if (w.k == w.nt - 1 || w.u + 1 == w.end) m.flags |= kEnds;
+          // the CTA's last tile: none in what is left of this part of the
+          // range (the next one would come after the end units), nor a part after it
+          if (w.u + 1 + (w.k == w.nt - 1 ? E : 0) >= w.end && w.end == last_end) m.flags |= kLast;
+        }
+        return m;
+      };
+      step(w, ti);  // this lane's tile of the first batch
+      Mine cur = look_up(LIST && w.u < w.end ? fetch(w) : -1);
       step(w, 4);
       int blk = LIST && w.u < w.end ? fetch(w) : -1;
-      bool ok = true;
+      bool ok = true, fresh = false;
       while (ok) {
-        const int n_q = __popc(__ballot_sync(0xffffffffu, on)) >> 3;
+        const int n_q = __popc(__ballot_sync(0xffffffffu, cur.on)) >> 3;  // tiles of the batch
         if (n_q == 0) break;
-        int row_next;
-        float ks_next, vs_next;
-        look_up(blk, row_next, ks_next, vs_next);
-        on = w.u < w.end;
+        const Mine nxt = look_up(blk);
         step(w, 4);
         blk = LIST && w.u < w.end ? fetch(w) : -1;
-        const SliceMeta mt = slice_meta(row, ks, vs);
+        SliceMeta mt;
+        if (!copies) mt = slice_meta(cur.flags, cur.ks, cur.vs);
+        const bool skip = p.test_skip >= 0 && cur.z == 0 && cur.k == p.test_skip;  // tests only
+        const bool have = cur.row != kNoRow && in_block == 0 && !skip &&
+                          range_ok(cur.row >= 0 && cur.row < L && cur.z < B * Hkv, p.status);
+        const uint32_t boxes = __ballot_sync(0xffffffffu, have);
+        const uint32_t any = __ballot_sync(0xffffffffu, cur.row != kNoRow);
+        const uint32_t first = __ballot_sync(0xffffffffu, (cur.flags & kStarts) != 0);
+        const uint32_t ends = __ballot_sync(0xffffffffu, (cur.flags & kEnds) != 0);
         for (int q = 0; q < n_q; ++q) {
+          // a listed tile without a row is passed over, but for a piece's last
+          fresh = fresh || ((first >> (8 * q)) & 1u);
+          if (LIST && !((any >> (8 * q)) & 0xffu) && !((ends >> (8 * q)) & 1u)) continue;
           if (!wait_empty()) {
             ok = false;
             break;
           }
-          if (ti == q) meta[s * kSlices + slice] = mt;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars[s]));
+          if (copies) {
+            const uint32_t full = smem_u32(&bars[s]);
+            if (lane == 8 * q && !skip) {
+              const int b = cur.z / Hkv;
+              expect(full, __popc((boxes >> (8 * q)) & 0xffu) * (uint32_t)entry_rows * 2u * kD,
+                     fresh, b, cur.z - b * Hkv);
+            }
+            __syncwarp();
+            if (ti == q && have) {
+              const uint32_t sK = smem_u32(stages + (size_t)s * kStageBytes) + slice * 16 * kD;
+              tma_load_3d(sK, &tm_k, 0, cur.row, cur.z, full);
+              tma_load_3d(sK + kOpBytes, &tm_v, 0, cur.row, cur.z, full);
+            }
+          } else {
+            if (ti == q) {
+              mt.rows = (mt.rows & ~kStarts) | (fresh ? kStarts : 0);
+              meta[s * kSlices + slice] = mt;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars[s]));
+          }
+          fresh = false;
           turn();
         }
-        row = row_next;
-        ks = ks_next;
-        vs = vs_next;
+        cur = nxt;
       }
     }
   } else {
     // ----------------------------------------------------------- consumers --
-    ConsumerSync csync{smem_u32(&bars[2 * NS]), abort_flag, p.status, 0u};
+    // The flags beside a tile say where pieces start and end, so these warps
+    // keep no place in the list.
     Consumer8<NT> cs;
     cs.c = lane >> 2;
     cs.t = lane & 3;
-    // Two blocks of heads leave no registers for the walk during the tiles: it
-    // lies in shared memory then, and thread 0 moves it on while the others
-    // merge.  (g = 16: 64 -> 58 us for 268 MB; at g = 2 it cost 2%.)
-    constexpr bool kSharedWalk = NT > 1;
-    volatile Walk8* walk = reinterpret_cast<Walk8*>(misc + 24);
-    Walk8 w;
-    if (!kSharedWalk || tid == 0) walk8_start<E>(w, rg, prefix, spos, B, Hkv);
-    if (kSharedWalk) {
-      if (tid == 0) put_walk8(walk, w);
-      csync(lane);
-    }
-    int s = 0;
+    int s = 0, piece = 0;
     uint32_t ph = 0;
-    while (true) {
-      if (kSharedWalk) w = get_walk8(walk);
-      if (w.u >= w.end) break;
-      const int len = (int)min((long long)(w.nt - w.k), w.end - w.u);
-      const int pos = w.pos;
-      cs.reset();
-      bool ok = true;
-      for (int i = 0; i < len; ++i) {
-        if (!consumer_wait(smem_u32(&bars[s]), ph, abort_flag, p.status, lane)) {
-          ok = false;
-          break;
-        }
-        if (i == 0) cs.load_q(qbuf + s * g * kD * 2, g, p.qscale);
-        const SliceMeta mt = meta[s * kSlices + warp];
-        const int rows = min(16, pos + 1 - mt.row0);
-        const uint8_t* Ks = stages + (size_t)s * kStageBytes + warp * 16 * kD;
-        if (rows > 0) cs.slice(Ks, Ks + kOpBytes, rows, mt);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars[NS + s]));
-        if (++s == NS) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
+    bool ok = true;
+    for (int flags = 0; !(flags & kLast);) {
+      ok = consumer_wait(smem_u32(&bars[s]), ph, abort_flag, p.status, lane);
       if (!ok) break;
-      cs.stash(merge_o, merge_ml, warp, g);
-      if (kSharedWalk) w = get_walk8(walk);
-      csync(lane);
-      if (*abort_flag) break;
-      Walk8 next = w;
-      if (!kSharedWalk || tid == 0) {
-        if (len < w.nt - w.k) {  // the part of the range ends inside the segment
-          next.u = w.end;
-        } else {
-          walk8_segment<E>(next, prefix, spos, B, Hkv);
-        }
-        walk8_turn<E>(next, rg, prefix, spos, B, Hkv);
-        if (kSharedWalk) put_walk8(walk, next);  // (every warp has read the walk)
+      const SliceMeta mt = meta[s * kSlices + warp];
+      flags = mt.rows;
+      if (flags & kStarts) {
+        cs.load_q(qbuf + s * g * kD * 2, g, p.qscale);
+        cs.reset();
       }
-      // ---- this CTA's part: the warps' partials, in warp order -----------
-      const bool whole = w.k == 0 && len == w.nt;
-      // a part that does not open the range is its last segment's
-      const int slot = 2 * blockIdx.x + (w.end == rg.t1 && rg.tA < rg.t1 ? 1 : 0);
-      const size_t out_at = ((size_t)w.b * p.Hq + (size_t)w.kvh * g) * kD;
-      for (int i = tid; i < g * (kD / 4); i += kConsumers) {
-        const int h = i / (kD / 4), d = (i % (kD / 4)) * 4;
-        float M, ls;
-        float4 os;
-        merge_warps8(merge_o, merge_ml, i, g, M, ls, os);
-        if (whole) {
-          const float inv = ls == 0.f ? 0.f : 1.f / ls;
-          *reinterpret_cast<uint2*>(p.out + out_at + (size_t)i * 4) = make_uint2(
-              pack_bf16x2(os.x * inv, os.y * inv), pack_bf16x2(os.z * inv, os.w * inv));
-        } else {
-          reinterpret_cast<float4*>(p.part_o + (size_t)slot * g * kD)[i] = os;
-          if (d == 0)
-            *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * g + h) * 2) =
-                make_float2(M, ls);
-        }
+      const uint8_t* Ks = stages + (size_t)s * kStageBytes + warp * 16 * kD;
+      const int rows = flags & kRowsMask;
+      if (rows > 0) cs.slice(Ks, Ks + kOpBytes, rows, mt);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars[NS + s]));
+      if (++s == NS) {
+        s = 0;
+        ph ^= 1u;
       }
-      csync(lane);  // the merge buffers may be written again; a partial is in place
-      if (!whole) {
-        // the segment's last CTA to arrive merges the parts
-        Part8 pt;
-        pt.f0 = w.u - w.k;
-        pt.out_at = out_at;
-        pt.c0 = cta_of(pt.f0, T, G);
-        pt.n = cta_of(pt.f0 + w.nt - 1, T, G) - pt.c0 + 1;
-        if (tid == 0) {
-          uint32_t* counter = &p.counters[w.b * Hkv + w.kvh];
-          __threadfence();  // (the other threads' stores came before the barrier)
-          const bool last = atomicAdd(counter, 1u) + 1 == (uint32_t)pt.n;
-          if (last) *counter = 0;
-          __threadfence();
-          misc[2] = last;
+      if (flags & kEnds) {  // this piece's partial for the merge warps
+        const int buf = n_buf == 2 ? piece & 1 : 0;
+        const uint32_t use = (uint32_t)(n_buf == 2 ? piece >> 1 : piece);
+        ++piece;
+        if (use > 0) {
+          ok = consumer_wait(smem_u32(&m_empty[buf]), (use & 1u) ^ 1u, abort_flag, p.status, lane);
+          if (!ok) break;
         }
-        csync(lane);
-        if (misc[2] && !*abort_flag) merge_parts<E>(p, pt, T, G, merge_o, csync, warp, lane);
+        float* mo = merge + buf * buf_floats;
+        cs.stash(mo, mo + ml_at, warp, g);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&m_full[buf]));
       }
-      if (*abort_flag) break;
-      w = next;
+    }
+    // segments of many parts that this CTA was the last to reach
+    if (ok && consumer_wait(smem_u32(merged), 0u, abort_flag, p.status, lane)) {
+      ConsumerSync csync{smem_u32(&bars[2 * NS]), abort_flag, p.status, 0u};
+      const int left = *(volatile int*)(misc + 3);
+      for (int i = 0; i < left && !*abort_flag; ++i)
+        merge_many(p, reinterpret_cast<const Part8*>(misc + 24)[i],
+                   reinterpret_cast<float*>(stages), csync, warp, lane);
     }
   }
   if (*abort_flag) {  // copies in flight land before the shared memory goes
@@ -996,7 +1049,7 @@ cudaError_t find_device(Device8& d, int dev) {
   for (int c = 1; c <= kMaxCluster; ++c) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(c * 64);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kClusterThreads);
     cfg.dynamicSmemBytes = kMaxSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1034,13 +1087,17 @@ cudaError_t device8(const Device8** out) {
   return cudaSuccess;
 }
 
-// CTAs per segment in cluster mode, or 0 for the split over a flat list.  A
-// cluster for every segment, all resident at once and of at least 8 CTAs
-// where there are tiles for them; with several sequences, whose lengths may
-// differ, only while the longest possible one leaves a CTA no more than
-// kClusterTiles tiles: beyond that an even split is worth more than the
-// latency saved.
-constexpr int kClusterTiles = 8;
+// CTAs per segment in cluster mode, or 0 for the split over a flat list: the
+// most that let every segment have its cluster resident at once, or 1.  With
+// one sequence, whose heads are all as long, always where that is at least 8
+// (or as many as there are tiles).  Otherwise while the longest possible
+// segment leaves a CTA no more than kClusterTiles tiles and the clusters fit
+// the device kClusterWaves times: a wave of clusters costs about 4 us and 0.55
+// for each tile of its longest segment, the flat list 10 us and 0.69 for each
+// tile of an even share (108 segments of 10 tiles: 18 us by the list, 10 in
+// clusters of one; 332 of one tile at g = 16: 13.7 and 15.5).
+constexpr int kClusterTiles = 24;
+constexpr int kClusterWaves = 2;
 int cluster_size8(const Kv8Params& p, const Device8& d) {
   if (g_decode_test_cluster >= 0)  // schedule tests only
     return min(g_decode_test_cluster, kMaxCluster);
@@ -1048,12 +1105,10 @@ int cluster_size8(const Kv8Params& p, const Device8& d) {
   const long long rows = p.index ? (long long)p.count << p.lb : (long long)p.L;
   const int tiles = (int)((rows + kTile - 1) / kTile);
   const int want = min(kMaxCluster, tiles);
-  for (int c = want; c >= min(8, want); --c)
-    if (nseg <= d.clusters[c]) {
-      if (p.B > 1 && (tiles + c - 1) / c > kClusterTiles) return 0;
-      return c;
-    }
-  return 0;
+  int c = want;
+  while (c > 1 && nseg > d.clusters[c]) --c;
+  if (p.B == 1 && c >= min(8, want)) return c;
+  return (tiles + c - 1) / c <= kClusterTiles && nseg <= (long long)kClusterWaves * d.sms ? c : 0;
 }
 
 // A cache [segs, L, 128] of codes as a 3-D tensor map, box 128 codes x rows x
@@ -1084,7 +1139,7 @@ cudaError_t launch8(Kv8Params& p, const CUtensorMap& mk, const CUtensorMap& mv,
     while (p.stages > 2 && cluster_smem_bytes(p.stages, p.g, C) > (size_t)kMaxSmem) --p.stages;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * C));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kClusterThreads);
     cfg.dynamicSmemBytes = cluster_smem_bytes(p.stages, p.g, C);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

@@ -291,6 +291,35 @@ def test_ragged_batches_split_anywhere(seed):
     _check(out, st, L, 64, pos, seqs=good)
 
 
+@pytest.mark.parametrize("g", [2, 16])
+@pytest.mark.parametrize("longest", [130, 700, 5000])
+def test_short_segments_beside_long_ones(longest, g):
+    """Hundreds of segments of one to five tiles, which are kept whole, with a long one here and
+    there that is split; the same for lists of which whole tiles hold no row."""
+    B, Hkv, block = 150, 3, 16
+    rng = np.random.default_rng(longest + g)
+    pos = [int(p) for p in rng.integers(0, min(longest, 640), B)]
+    for b in (0, 70, 149):
+        pos[b] = longest - 1
+    pos[5] = -3
+    st = _case(B, Hkv, g, longest, block, pos, seed=53)
+    index = torch.from_numpy(rng.integers(0, -(-longest // block), (B, Hkv, 37))).int()
+    index[::2, :, 8:24] = -1  # two whole tiles
+    index[::3, :, 30:] = -1
+    index[9] = -1
+    ga.attn_test_force_schedule(0)
+    try:
+        dense, listed = _run(st, block), _run_blocks(st, block, index.cuda())
+        torch.cuda.synchronize()
+    finally:
+        ga.attn_test_force_schedule(-1)
+    assert torch.isnan(dense[5]).all() and torch.isnan(listed[5]).all()
+    assert (listed[9] == 0).all()
+    seqs = [0, 1, 2, 3, 9, 70, 71, 100, 148, 149]
+    _check(dense, st, longest, block, pos, seqs=seqs, what="dense")
+    _check(listed, st, longest, block, pos, index=index.tolist(), seqs=seqs, what="listed")
+
+
 @pytest.mark.parametrize("cluster", [0, 8])
 @pytest.mark.parametrize("listed", [False, True])
 def test_a_wait_that_runs_out_is_reported(cluster, listed):
