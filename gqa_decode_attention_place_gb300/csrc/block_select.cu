@@ -16,12 +16,12 @@
 // memory and a scan over its bins each), with the keys in registers; most
 // often the bin of the first digit is small, and its few keys are ranked among
 // themselves.  Each thread holds items in a row, so one scan over the threads'
-// counts places the chosen indices in ascending order.  Bound by its instructions (512 rows of up to
-// 8192 scores: 36 us with one bit a round, 20 us with three digits a row,
-// 15.4 us this way).  The
-// first digit holds sign, exponent and three bits of the mantissa, so that
-// scores of one size still spread over many bins (the histogram's atomics
-// contend only where scores are alike).
+// counts places the chosen indices in ascending order.  Bound by its
+// instructions (512 rows of up to 8192 scores: 36 us with one bit a round, 20
+// with three digits a row, 15 this way).  The first digit holds
+// sign, exponent and three bits of the mantissa, so that scores of one size
+// still spread over many bins (the histogram's atomics contend only where
+// scores are alike).
 #include "common.cuh"
 #include "decode_params.h"
 #include "internal.h"

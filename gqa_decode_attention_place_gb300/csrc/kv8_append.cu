@@ -212,7 +212,8 @@ constexpr int kTokenWarps = 4;
 __global__ void __launch_bounds__(kTokenWarps * 32) kv8_append_token_kernel(
     const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, long long k_stride,
     long long v_stride, const int32_t* __restrict__ positions, uint8_t* k_cache,
-    uint8_t* v_cache, float* k_scale, float* v_scale, uint4* k_bounds, int segs, int Hkv, int L, int nb, int lb) {
+    uint8_t* v_cache, float* k_scale, float* v_scale, uint4* k_bounds, int segs, int Hkv, int L,
+    int nb, int lb) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int seg = blockIdx.x * kTokenWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -227,7 +228,8 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv8_append_token_kernel(
   const bool had = row0 < pos;
   float* scale = (op ? v_scale : k_scale) + (size_t)seg * nb + j;
   const float s_old = had ? *scale : 0.f;
-  uint4* bound = k_bounds + ((size_t)seg * nb + j) * 32 + lane;  // lower half: maxima, upper: minima
+  // lower half: the maxima, upper half: the minima
+  uint4* bound = k_bounds + ((size_t)seg * nb + j) * 32 + lane;
   uint4 was = make_uint4(0u, 0u, 0u, 0u);
   if (k_bounds != nullptr && had) was = *bound;
 
@@ -292,8 +294,9 @@ cudaError_t launch_kv8_append(const void* k_new, const void* v_new, long long k_
                               : kv8_append_kernel<8>;
   return launch_pdl(kernel, dim3(touched, Hkv, B), dim3(256), 0, stream,
                     static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new),
-                    k_stride / 8, v_stride / 8, positions, static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale,
-                    v_scale, static_cast<uint32_t*>(k_bounds), B, S, Hkv, L, nb);
+                    k_stride / 8, v_stride / 8, positions, static_cast<uint8_t*>(k_cache),
+                    static_cast<uint8_t*>(v_cache), k_scale, v_scale,
+                    static_cast<uint32_t*>(k_bounds), B, S, Hkv, L, nb);
 }
 
 }  // namespace gqa

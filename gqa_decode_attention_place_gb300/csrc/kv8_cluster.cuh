@@ -151,7 +151,9 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
         ++pass;
       }
     };
-    auto skipped = [&](int i) { return p.test_skip >= 0 && seg == 0 && rank + i * C == p.test_skip; };
+    auto skipped = [&](int i) {  // failure-path tests only
+      return p.test_skip >= 0 && seg == 0 && rank + i * C == p.test_skip;
+    };
     if (copies && !LIST) {
       for (int i = 0; i < mine; ++i) {
         if (!wait_empty()) break;

@@ -210,8 +210,8 @@ __device__ __forceinline__ void walk8_init(Walk8& w, long long u, const int* pre
 }
 // CTA c's range.  An even share, but a boundary inside a segment of at most
 // kShortTiles tiles moves to that segment's nearer end: such a segment is not
-// worth a merge through L2 (340 of one or two tiles: 18.4 -> 11.8 us).  (A longer segment's parts stay where the even
-// shares put them: cta_of.)
+// worth a merge through L2 (340 of one or two tiles: 18.4 -> 11.8 us).  (A
+// longer segment's parts stay where the even shares put them: cta_of.)
 constexpr int kShortTiles = 4;
 template <int E>
 __device__ __forceinline__ long long boundary8(long long u, long long T, const int* prefix, int B,

@@ -22,10 +22,16 @@ namespace {
 
 struct Raised {};  // a Python exception is set
 
-struct NoGil {  // other Python threads may run during the C call
+// The C call, on the tensors' device, while other Python threads may run.  (Its
+// arguments are made before: what they raise needs the interpreter's lock.)
+template <typename F, typename... A>
+int call(c10::Device device, F fn, A... args) {
+  const c10::DeviceGuard guard(device);
   PyThreadState* state = PyEval_SaveThread();
-  ~NoGil() { PyEval_RestoreThread(state); }
-};
+  const int code = fn(args...);
+  PyEval_RestoreThread(state);
+  return code;
+}
 
 [[noreturn]] void fail(PyObject* type, const std::string& what) {
   PyErr_SetString(type, what.c_str());
@@ -197,10 +203,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* ko = c.dense(a[11], "k_out", kBF16, {N, Hkv, D});
     const float eps = real(a[6]);
     void* stream = handle(a[1]);
-    const c10::DeviceGuard guard(c.device);
-    const NoGil nogil;
-    return fn(qp, kp, qs, ks, wq, wk, eps, pos, cos, sin, narrow(N), narrow(Hq), narrow(Hkv),
-              narrow(D), narrow(L), qo, ko, stream);
+    return call(c.device, fn, qp, kp, qs, ks, wq, wk, eps, pos, cos, sin, narrow(N), narrow(Hq),
+                narrow(Hkv), narrow(D), narrow(L), qo, ko, stream);
   });
 }
 
@@ -238,10 +242,8 @@ PyObject* qk_norm_rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* qo = c.dense(a[13], "q_out", kBF16, q.sizes());
     const float eps = real(a[7]);
     void* stream = handle(a[1]);
-    const c10::DeviceGuard guard(c.device);
-    const NoGil nogil;
-    return fn(qp, kp, vp, qs, ks, vs, wq, wk, eps, pos, cos, sin, kc, vc, narrow(B), narrow(S),
-              narrow(Hq), narrow(Hkv), narrow(D), narrow(L), qo, stream);
+    return call(c.device, fn, qp, kp, vp, qs, ks, vs, wq, wk, eps, pos, cos, sin, kc, vc, narrow(B),
+                narrow(S), narrow(Hq), narrow(Hkv), narrow(D), narrow(L), qo, stream);
   });
 }
 
@@ -269,10 +271,8 @@ PyObject* kv8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* vs = c.dense(a[8], "v_scale", kF32, {B, Hkv, nb});
     void* bounds = c.optional(a[10], "k_bounds", kBF16, {B, Hkv, nb, 2, D});
     void* stream = handle(a[1]);
-    const c10::DeviceGuard guard(c.device);
-    const NoGil nogil;
-    return fn(kn, vn, kst, vst, pos, kc, vc, ks, vs, bounds, narrow(B), narrow(S), narrow(Hkv), narrow(L),
-              narrow(D), (int)block, stream);
+    return call(c.device, fn, kn, vn, kst, vst, pos, kc, vc, ks, vs, bounds, narrow(B), narrow(S),
+                narrow(Hkv), narrow(L), narrow(D), (int)block, stream);
   });
 }
 
@@ -315,10 +315,9 @@ PyObject* decode_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                        float, void*, void*, size_t, void*)>(handle(a[0]));
     const float scale = real(a[9]);
     void* stream = handle(a[1]);
-    const c10::DeviceGuard guard(d.c.device);
-    const NoGil nogil;
-    return fn(d.q, d.pos, d.kc, d.vc, d.ks, d.vs, narrow(d.B), narrow(d.Hq), narrow(d.Hkv),
-              narrow(d.L), narrow(d.D), d.block, scale, d.out, d.ws, d.ws_bytes, stream);
+    return call(d.c.device, fn, d.q, d.pos, d.kc, d.vc, d.ks, d.vs, narrow(d.B), narrow(d.Hq),
+                narrow(d.Hkv), narrow(d.L), narrow(d.D), d.block, scale, d.out, d.ws, d.ws_bytes,
+                stream);
   });
 }
 
@@ -335,11 +334,9 @@ PyObject* decode_kv8_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
         handle(a[0]));
     const float scale = real(a[10]);
     void* stream = handle(a[1]);
-    const c10::DeviceGuard guard(d.c.device);
-    const NoGil nogil;
-    return fn(d.q, d.pos, d.kc, d.vc, d.ks, d.vs, index, narrow(count), narrow(d.B), narrow(d.Hq),
-              narrow(d.Hkv), narrow(d.L), narrow(d.D), d.block, scale, d.out, d.ws, d.ws_bytes,
-              stream);
+    return call(d.c.device, fn, d.q, d.pos, d.kc, d.vc, d.ks, d.vs, index, narrow(count),
+                narrow(d.B), narrow(d.Hq), narrow(d.Hkv), narrow(d.L), narrow(d.D), d.block, scale,
+                d.out, d.ws, d.ws_bytes, stream);
   });
 }
 
@@ -356,11 +353,9 @@ PyObject* decode_kv8_sparse(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int count = (int)whole(a[10]), first = (int)whole(a[11]), recent = (int)whole(a[12]);
     const float scale = real(a[13]);
     void* stream = handle(a[1]);
-    const c10::DeviceGuard guard(d.c.device);
-    const NoGil nogil;
-    return fn(d.q, d.pos, d.kc, d.vc, d.ks, d.vs, bounds, count, first, recent, narrow(d.B),
-              narrow(d.Hq), narrow(d.Hkv), narrow(d.L), narrow(d.D), d.block, scale, d.out, d.ws,
-              d.ws_bytes, stream);
+    return call(d.c.device, fn, d.q, d.pos, d.kc, d.vc, d.ks, d.vs, bounds, count, first, recent,
+                narrow(d.B), narrow(d.Hq), narrow(d.Hkv), narrow(d.L), narrow(d.D), d.block, scale,
+                d.out, d.ws, d.ws_bytes, stream);
   });
 }
 
@@ -379,10 +374,8 @@ PyObject* block_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* bp = c.dense(a[4], "k_bounds", kBF16, {B, Hkv, nb, 2, D});
     void* out = c.dense(a[7], "out", kF32, {B, Hkv, nb});
     void* stream = handle(a[1]);
-    const c10::DeviceGuard guard(c.device);
-    const NoGil nogil;
-    return fn(qp, pos, bp, narrow(B), narrow(Hq), narrow(Hkv), (int)L, narrow(D), (int)block, out,
-              stream);
+    return call(c.device, fn, qp, pos, bp, narrow(B), narrow(Hq), narrow(Hkv), (int)L, narrow(D),
+                (int)block, out, stream);
   });
 }
 
@@ -400,10 +393,8 @@ PyObject* block_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* pos = c.dense(a[3], "positions", kI32, {B});
     void* out = c.dense(a[9], "out", kI32, {B, Hkv, count});
     void* stream = handle(a[1]);
-    const c10::DeviceGuard guard(c.device);
-    const NoGil nogil;
-    return fn(sp, pos, narrow(B), narrow(Hkv), (int)L, (int)block, (int)count, first, recent, out,
-              stream);
+    return call(c.device, fn, sp, pos, narrow(B), narrow(Hkv), (int)L, (int)block, (int)count,
+                first, recent, out, stream);
   });
 }
 

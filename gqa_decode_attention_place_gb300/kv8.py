@@ -9,8 +9,10 @@ native (csrc/marshal.cpp).  Codes are ``torch.float8_e4m3fn`` tensors.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.util
+import threading
 
 import torch
 
@@ -19,20 +21,23 @@ from . import AttnError, _DEBUG_WORKSPACES, _build, _raise, attn_debug_build, lo
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _native = None
 _address: dict = {}
+_loading = threading.Lock()
 
 
 def _load():
     """The native checks and the addresses of the C entry points (built in-tree first if needed)."""
     global _native
-    lib = load_library()
-    path = _build.build_marshal()
-    spec = importlib.util.spec_from_file_location("_gqa_marshal", path)
-    _native = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(_native)
-    for name in ("attn_qk_norm_rope", "attn_qk_norm_rope_append", "attn_kv8_append",
-                 "attn_decode_step_kv8", "attn_decode_step_kv8_blocks",
-                 "attn_decode_step_kv8_sparse", "attn_block_scores", "attn_block_select"):
-        _address[name] = ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+    with _loading:
+        if _native is None:
+            lib = load_library()
+            spec = importlib.util.spec_from_file_location("_gqa_marshal", _build.build_marshal())
+            native = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(native)
+            for name in ("attn_qk_norm_rope", "attn_qk_norm_rope_append", "attn_kv8_append",
+                         "attn_decode_step_kv8", "attn_decode_step_kv8_blocks",
+                         "attn_decode_step_kv8_sparse", "attn_block_scores", "attn_block_select"):
+                _address[name] = ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+            _native = native  # last: other threads go on from here
     return _native
 
 
@@ -45,6 +50,23 @@ def _stream(stream, t) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _made_on(stream, device):
+    """Where a call makes its output or workspace itself: memory of the stream the call runs on,
+    so that it is filled and handed back in that stream's order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _made_on(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _on(t, name, dtype=_BF16):
@@ -72,9 +94,9 @@ def attn_qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions, cos_table
     Returns (q_out, k_out), dense bf16."""
     m = _native or _load()
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=_BF16, device=_on(q, "q"))
+        q_out = _empty(q.shape, _BF16, _on(q, "q"), stream)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=_BF16, device=_on(k, "k"))
+        k_out = _empty(k.shape, _BF16, _on(k, "k"), stream)
     code = m.qk_norm_rope(_address["attn_qk_norm_rope"], _stream(stream, q), q, k, q_weight,
                           k_weight, eps, positions, cos_table, sin_table, q_out, k_out)
     if code:
@@ -90,7 +112,7 @@ def attn_qk_norm_rope_append(q, k_new, v_new, q_weight, k_weight, eps: float, po
     positions[b] + t of the bf16 caches [B,Hkv,L,D].  Returns q_out."""
     m = _native or _load()
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=_BF16, device=_on(q, "q"))
+        q_out = _empty(q.shape, _BF16, _on(q, "q"), stream)
     code = m.qk_norm_rope_append(_address["attn_qk_norm_rope_append"], _stream(stream, q), q,
                                  k_new, v_new, q_weight, k_weight, eps, positions, k_cache,
                                  v_cache, cos_table, sin_table, q_out)
@@ -148,11 +170,12 @@ def attn_decode_step_kv8(q, positions, k_cache, v_cache, k_scale, v_scale, block
     scales [B,Hkv,ceil(L/block)])."""
     m = _native or _load()
     if out is None:
-        out = torch.empty(q.shape, dtype=_BF16, device=_on(q, "q"))
+        out = _empty(q.shape, _BF16, _on(q, "q"), stream)
     if workspace is None:
         B, Hq, D = _dims(q, "q", 3)
         _, Hkv, L, _ = _dims(k_cache, "k_cache", 4)
-        workspace = kv8_workspace(B, Hq, Hkv, L, D, q.device)
+        with _made_on(stream, q.device):
+            workspace = kv8_workspace(B, Hq, Hkv, L, D, q.device)
     code = m.decode_kv8(_address["attn_decode_step_kv8"], _stream(stream, q), q, positions,
                         k_cache, v_cache, k_scale, v_scale, block, scale, out, workspace)
     if code:
@@ -168,7 +191,7 @@ def attn_block_scores(q, positions, k_bounds, L: int, block: int, out=None,
     m = _native or _load()
     if out is None:
         device = _on(q, "q")
-        out = torch.empty(_dims(k_bounds, "k_bounds", 5)[:3], dtype=_F32, device=device)
+        out = _empty(_dims(k_bounds, "k_bounds", 5)[:3], _F32, device, stream)
     code = m.block_scores(_address["attn_block_scores"], _stream(stream, q), q, positions,
                           k_bounds, L, block, out)
     if code:
@@ -186,7 +209,7 @@ def attn_block_select(scores, positions, L: int, block: int, count: int, first: 
         device = _on(scores, "scores", _F32)
         if count < 1:
             raise AttnError(1, "attn_block_select")
-        out = torch.empty((*_dims(scores, "scores", 3)[:2], count), dtype=_I32, device=device)
+        out = _empty((*_dims(scores, "scores", 3)[:2], count), _I32, device, stream)
     code = m.block_select(_address["attn_block_select"], _stream(stream, scores), scores,
                           positions, L, block, count, first, recent, out)
     if code:
@@ -201,11 +224,12 @@ def attn_decode_step_kv8_blocks(q, positions, k_cache, v_cache, k_scale, v_scale
     [B,Hkv,count] int32 (-1: none), up to each position."""
     m = _native or _load()
     if out is None:
-        out = torch.empty(q.shape, dtype=_BF16, device=_on(q, "q"))
+        out = _empty(q.shape, _BF16, _on(q, "q"), stream)
     if workspace is None:
         B, Hq, D = _dims(q, "q", 3)
         _, Hkv, L, _ = _dims(k_cache, "k_cache", 4)
-        workspace = kv8_workspace(B, Hq, Hkv, L, D, q.device)
+        with _made_on(stream, q.device):
+            workspace = kv8_workspace(B, Hq, Hkv, L, D, q.device)
     code = m.decode_kv8_blocks(_address["attn_decode_step_kv8_blocks"], _stream(stream, q), q,
                                positions, k_cache, v_cache, k_scale, v_scale, block, block_index,
                                scale, out, workspace)
@@ -222,11 +246,12 @@ def attn_decode_step_kv8_sparse(q, positions, k_cache, v_cache, k_scale, v_scale
     one call: a decode step that attends `count` blocks per KV head."""
     m = _native or _load()
     if out is None:
-        out = torch.empty(q.shape, dtype=_BF16, device=_on(q, "q"))
+        out = _empty(q.shape, _BF16, _on(q, "q"), stream)
     if workspace is None:
         B, Hq, D = _dims(q, "q", 3)
         _, Hkv, L, _ = _dims(k_cache, "k_cache", 4)
-        workspace = kv8_sparse_workspace(B, Hq, Hkv, L, D, block, count, q.device)
+        with _made_on(stream, q.device):
+            workspace = kv8_sparse_workspace(B, Hq, Hkv, L, D, block, count, q.device)
     code = m.decode_kv8_sparse(_address["attn_decode_step_kv8_sparse"], _stream(stream, q), q,
                                positions, k_cache, v_cache, k_scale, v_scale, block, k_bounds,
                                count, first, recent, scale, out, workspace)

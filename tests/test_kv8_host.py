@@ -141,3 +141,26 @@ def test_binding_checks_tensors():
         ga.attn_decode_step_kv8(x.float(), i, c, c, x, x, 16, 1.0)
     with pytest.raises(TypeError):
         ga.attn_block_select(x, i, 16, 16, 1)
+
+
+def test_first_calls_from_several_threads():
+    """The native checks are loaded once, and no thread goes on before all of it is there."""
+    import threading
+
+    from gqa_decode_attention_place_gb300 import kv8
+
+    kv8._native = None
+    kv8._address.clear()
+    seen, start = [], threading.Barrier(8)
+
+    def first():
+        start.wait()
+        seen.append((kv8._native or kv8._load(), len(kv8._address)))
+
+    threads = [threading.Thread(target=first) for _ in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(seen) == 8 and len({id(m) for m, _ in seen}) == 1
+    assert all(n == 8 for _, n in seen)
