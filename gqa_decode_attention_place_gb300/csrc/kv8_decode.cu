@@ -12,8 +12,8 @@
 // blocks' scales are.
 //
 // Bound by memory: a row costs 256 bytes for K and V, half of the bf16
-// cache's.  4.3 GB (B=256, g=8) take 596 us, 7.2 TB/s; 268 MB (B=32) 47 us at
-// g = 2, 50 at g = 8 and 58 at g = 16.  How:
+// cache's.  4.3 GB (B=256, g=8) take 591 us, 7.3 TB/s; 268 MB (B=32) 46 us at
+// g <= 8 and 54 at g = 16.  How:
 //  * 128-row tiles (32 KB for K and V) stream through a shared-memory ring by
 //    tiled TMA copies (128-byte swizzle: a row of codes is exactly one
 //    swizzle span) issued by one producer warp; another fetches each 16-row
@@ -35,7 +35,9 @@
 //    and go on; two further warps merge them (512 x 8 segments of one tile:
 //    55 -> 44 us).  A segment split over CTAs is merged by the CTA that
 //    arrives last, in CTA order, so results do not depend on timing; short
-//    ones are not split.  For few segments a thread-block cluster takes each
+//    ones are not split.  The last segment is the consumers' own to merge, and
+//    its other part is fetched while they finish it (g = 8: 50 -> 46 us, g = 16:
+//    58 -> 54).  For few segments a thread-block cluster takes each
 //    (kv8_cluster.cuh).
 #include <cooperative_groups.h>
 
@@ -63,8 +65,8 @@ constexpr int kMergeThreads = 64;           // two warps that merge (flat list)
 constexpr int kThreads = kConsumers + 64 + kMergeThreads;  // and two producer warps
 constexpr int kClusterThreads = kConsumers + 64;
 constexpr int kMaxStages = 6;
-constexpr int kMiscInts = 40;  // [0] abort, [2] last, [3] segments left over, [8..16) scan,
-                               // [24..40) those segments
+constexpr int kMiscInts = 48;  // [0] abort, [2] last, [3] segments left over, [8..16) scan,
+                               // [24..32) those segments, [32..48) the last piece
 constexpr int kNoRow = 0x40000000;          // row of a slice that holds nothing
 constexpr float kMInit = -3e38f;            // running maximum before any row
 constexpr float kTau = 8.f;                 // the running maximum may lag by 2^kTau
@@ -128,9 +130,11 @@ __host__ __device__ constexpr int merge_floats(int g) {
   return kWarps * (merge_heads(g) * kMergeRow + 2 * g);
 }
 __host__ __device__ constexpr int merge_buffers(int g) { return g <= 8 ? 2 : 1; }
+// The other part of the last piece's segment: its outputs, then (max, sum).
+__host__ __device__ constexpr int other_floats(int g) { return g * (kD + 2) + (g & 1) * 2; }
 inline size_t smem_bytes(int stages, int B, int g) {
   return (size_t)stages * (kStageBytes + g * kD * 2 + kSlices * sizeof(SliceMeta) + 16) + 7 * 8 +
-         (size_t)merge_buffers(g) * merge_floats(g) * 4 + kMiscInts * 4 +
+         ((size_t)merge_buffers(g) * merge_floats(g) + other_floats(g)) * 4 + kMiscInts * 4 +
          ((size_t)2 * B + 1) * 4;
 }
 
@@ -488,7 +492,15 @@ struct Part8 {
   size_t out_at;
   int c0, n;
 };
-static_assert(2 * sizeof(Part8) <= 16 * 4, "two fit behind misc[24]");
+static_assert(2 * sizeof(Part8) <= 8 * 4, "two fit behind misc[24]");
+// The CTA's last piece: whole, or part `own` of a segment; have: the segment's
+// only other part has arrived and lies in shared memory.
+struct Last8 {
+  Part8 pt;
+  uint32_t* counter;
+  int whole, own, have;
+};
+static_assert(sizeof(Last8) <= 16 * 4, "behind misc[32]");
 
 __device__ __forceinline__ void store_column(const Kv8Params& p, size_t out_at, int col,
                                              const float4& o, float ls) {
@@ -502,16 +514,38 @@ __device__ __forceinline__ int part_slot(const Part8& pt, int r) {
   return 2 * (pt.c0 + r) + (r == 0);
 }
 
-// Merge the parts of a split segment, in CTA order.  Few parts, by the merge
-// warps: every thread loads all of its column's in one round trip.
+// A column's output from few parts, in CTA order (absent ones: kMInit, zeros).
 constexpr int kFewParts = 4;
-__device__ __forceinline__ void merge_few(const Kv8Params& p, const Part8& pt, int tid) {
+__device__ __forceinline__ void join_parts(const Kv8Params& p, size_t out_at, int col,
+                                           const float2 (&ml)[kFewParts],
+                                           const float4 (&x)[kFewParts]) {
+  float M = kMInit;
+#pragma unroll
+  for (int r = 0; r < kFewParts; ++r) M = fmaxf(M, ml[r].x);
+  float ls = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int r = 0; r < kFewParts; ++r) {
+    const float e = ex2(ml[r].x - M);
+    ls = fmaf(ml[r].y, e, ls);
+    o.x = fmaf(x[r].x, e, o.x);
+    o.y = fmaf(x[r].y, e, o.y);
+    o.z = fmaf(x[r].z, e, o.z);
+    o.w = fmaf(x[r].w, e, o.w);
+  }
+  store_column(p, out_at, col, o, ls);
+}
+
+// Merge the parts of a split segment.  Few parts: every one of `threads` loads
+// all of its column's in one round trip.
+__device__ __forceinline__ void merge_few(const Kv8Params& p, const Part8& pt, int tid,
+                                          int threads) {
   const int g = p.g;
-  for (int col = tid; col < g * (kD / 4); col += kMergeThreads) {
+#pragma unroll 2
+  for (int col = tid; col < g * (kD / 4); col += threads) {
     const int h = col / (kD / 4);
     float2 ml[kFewParts];
     float4 x[kFewParts];
-    float M = kMInit;
 #pragma unroll
     for (int r = 0; r < kFewParts; ++r) {
       ml[r] = make_float2(kMInit, 0.f);
@@ -522,20 +556,7 @@ __device__ __forceinline__ void merge_few(const Kv8Params& p, const Part8& pt, i
         x[r] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kD) + col);
       }
     }
-#pragma unroll
-    for (int r = 0; r < kFewParts; ++r) M = fmaxf(M, ml[r].x);
-    float ls = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int r = 0; r < kFewParts; ++r) {
-      const float e = ex2(ml[r].x - M);
-      ls = fmaf(ml[r].y, e, ls);
-      o.x = fmaf(x[r].x, e, o.x);
-      o.y = fmaf(x[r].y, e, o.y);
-      o.z = fmaf(x[r].z, e, o.z);
-      o.w = fmaf(x[r].w, e, o.w);
-    }
-    store_column(p, pt.out_at, col, o, ls);
+    join_parts(p, pt.out_at, col, ml, x);
   }
 }
 
@@ -549,6 +570,7 @@ __device__ __forceinline__ void merge_many(const Kv8Params& p, const Part8& pt, 
   const int cols = g * (kD / 4);
   float* wt = buf;              // [n][g] maxima, then weights
   float* ls = buf + n * g;      // [n][g] sums; row 0 then holds the totals
+#pragma unroll 4
   for (int i = tid; i < n * g; i += kConsumers) {
     const int r = i / g, h = i - r * g;
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(
@@ -581,7 +603,7 @@ __device__ __forceinline__ void merge_many(const Kv8Params& p, const Part8& pt, 
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (on) {
       const int h = col / (kD / 4);
-#pragma unroll 4
+#pragma unroll 16
       for (int r = deal > 1 ? who : 0; r < n; r += deal) {
         const float4 x = __ldcg(reinterpret_cast<const float4*>(
                                     p.part_o + (size_t)part_slot(pt, r) * g * kD) + col);
@@ -609,6 +631,23 @@ __device__ __forceinline__ void merge_many(const Kv8Params& p, const Part8& pt, 
   }
   csync(lane);  // buf may be written again
 }
+// This CTA's part of a segment, column by column.
+__device__ __forceinline__ void store_part(const Kv8Params& p, int slot, int col, float M,
+                                           float ls, const float4& o) {
+  reinterpret_cast<float4*>(p.part_o + (size_t)slot * p.g * kD)[col] = o;
+  if (col % (kD / 4) == 0)
+    *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * p.g + col / (kD / 4)) * 2) =
+        make_float2(M, ls);
+}
+// One thread, when all of the CTA's part is written: whether it is the last of
+// n to arrive.
+__device__ __forceinline__ bool arrive_last(uint32_t* counter, int n) {
+  __threadfence();  // (the other threads' stores came before a barrier)
+  const bool last = atomicAdd(counter, 1u) + 1 == (uint32_t)n;
+  if (last) *counter = 0;
+  __threadfence();
+  return last;
+}
 // The statistics of all parts and the dealt-out columns fit two stages.
 static_assert((2 * kKv8MaxGrid * 16 + 4 + 4 * kConsumers) * 4 <= 2 * kStageBytes, "merge_many");
 
@@ -628,7 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* merge = reinterpret_cast<float*>(meta + NS * kSlices);
   const int ml_at = kWarps * merge_heads(g) * kMergeRow;
   // full [NS], empty [NS], consumers' sync, merge full [2], empty [2], merged
-  uint64_t* bars = reinterpret_cast<uint64_t*>(merge + n_buf * buf_floats);
+  float* other = merge + n_buf * buf_floats;  // [g][kD], then (max, sum) [g]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(other + other_floats(g));
   uint64_t* m_full = bars + 2 * NS + 1;
   uint64_t* m_empty = m_full + 2;
   uint64_t* merged = m_empty + 2;
@@ -650,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&m_full[i]), kWarps);               // every consumer warp has stashed
       mbar_init(smem_u32(&m_empty[i]), kMergeThreads / 32);  // both merge warps have read
     }
-    mbar_init(smem_u32(merged), 1);  // the merge warps are done
+    mbar_init(smem_u32(merged), 1);  // the merge warps have come to the last piece
     mbar_init(smem_u32(m_sync), kMergeThreads / 32);
     misc[0] = 0;
     misc[3] = 0;
@@ -720,13 +760,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The consumers leave each piece's partials in a buffer and go on; these
     // two warps merge them and write the output, or, for a piece that is only
     // part of its segment, the CTA's partial, and settle who merges the parts.
+    // The last piece is for the consumers, which have nothing else to do then;
+    // if it is one of two parts and the other has arrived, that one is fetched
+    // while they are still at work.
     const int mtid = tid - kConsumers - 64;
     ConsumerSync msync{smem_u32(m_sync), abort_flag, p.status, 0u};
     for (int k = 0; w.u < w.end; ++k) {
       const int len = (int)min((long long)(w.nt - w.k), w.end - w.u);
       const bool whole = w.k == 0 && len == w.nt;
       const int slot = 2 * blockIdx.x + (w.k == 0);  // part_slot
-      const size_t out_at = ((size_t)w.b * p.Hq + (size_t)w.kvh * g) * kD;
+      const long long f0 = w.u - w.k;                // the segment's first unit
+      Part8 pt;
+      pt.out_at = ((size_t)w.b * p.Hq + (size_t)w.kvh * g) * kD;
+      pt.c0 = whole ? 0 : cta_of(f0, T, G);
+      pt.n = whole ? 1 : cta_of(f0 + w.nt - 1, T, G) - pt.c0 + 1;
+      uint32_t* counter = &p.counters[w.b * Hkv + w.kvh];
+      if (len < w.nt - w.k) {  // the part of the range ends inside the segment
+        w.u = w.end;
+      } else {
+        walk8_segment<E>(w, prefix, spos, B, Hkv);
+      }
+      walk8_turn<E>(w, rg, prefix, spos, B, Hkv);
+      if (w.u >= w.end) {  // the last piece
+        const int own = (int)blockIdx.x - pt.c0;
+        if (mtid == 0) {
+          bool have = false;
+          if (!whole && pt.n == 2) {
+            have = *(volatile uint32_t*)counter == 1u;
+            __threadfence();
+          }
+          Last8* last = reinterpret_cast<Last8*>(misc + 32);
+          last->pt = pt;
+          last->counter = counter;
+          last->whole = whole;
+          last->own = own;
+          last->have = have;
+          misc[2] = have;
+        }
+        msync(lane);
+        if (misc[2]) {
+          const size_t at = (size_t)part_slot(pt, 1 - own) * g;
+          const float4* o = reinterpret_cast<const float4*>(p.part_o + at * kD);
+#pragma unroll 8
+          for (int i = mtid; i < g * (kD / 4); i += kMergeThreads)
+            reinterpret_cast<float4*>(other)[i] = __ldcg(o + i);
+          if (mtid < g)
+            reinterpret_cast<float2*>(other + g * kD)[mtid] =
+                __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2) + mtid);
+        }
+        msync(lane);
+        break;
+      }
       const int buf = n_buf == 2 ? k & 1 : 0;
       const uint32_t use = (uint32_t)(n_buf == 2 ? k >> 1 : k);
       if (!consumer_wait(smem_u32(&m_full[buf]), use & 1u, abort_flag, p.status, lane)) break;
@@ -736,44 +820,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         float M, ls;
         float4 os;
         merge_warps8(mo, mo + ml_at, i, g, M, ls, os);
-        if (whole) {
-          store_column(p, out_at, i, os, ls);
-        } else {
-          reinterpret_cast<float4*>(p.part_o + (size_t)slot * g * kD)[i] = os;
-          if (i % (kD / 4) == 0)
-            *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * g + i / (kD / 4)) * 2) =
-                make_float2(M, ls);
-        }
+        if (whole) store_column(p, pt.out_at, i, os, ls);
+        else store_part(p, slot, i, M, ls, os);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&m_empty[buf]));
       if (!whole) {
         // the segment's last CTA to arrive merges the parts
-        const long long f0 = w.u - w.k;  // its first unit
-        Part8 pt;
-        pt.out_at = out_at;
-        pt.c0 = cta_of(f0, T, G);
-        pt.n = cta_of(f0 + w.nt - 1, T, G) - pt.c0 + 1;
         msync(lane);
         if (mtid == 0) {
-          uint32_t* counter = &p.counters[w.b * Hkv + w.kvh];
-          __threadfence();  // (the other threads' stores came before the barrier)
-          const bool last = atomicAdd(counter, 1u) + 1 == (uint32_t)pt.n;
-          if (last) *counter = 0;
-          __threadfence();
+          const bool last = arrive_last(counter, pt.n);
           misc[2] = last;
-          if (last && pt.n > kFewParts)  // left to the consumers; at most two (first and last)
+          if (last && pt.n > kFewParts)  // left to the consumers
             reinterpret_cast<Part8*>(misc + 24)[misc[3]++] = pt;
         }
         msync(lane);
-        if (misc[2] && pt.n <= kFewParts && !*abort_flag) merge_few(p, pt, mtid);
+        if (misc[2] && pt.n <= kFewParts && !*abort_flag) merge_few(p, pt, mtid, kMergeThreads);
       }
-      if (len < w.nt - w.k) {  // the part of the range ends inside the segment
-        w.u = w.end;
-      } else {
-        walk8_segment<E>(w, prefix, spos, B, Hkv);
-      }
-      walk8_turn<E>(w, rg, prefix, spos, B, Hkv);
     }
     if (mtid == 0) mbar_arrive(smem_u32(merged));
   } else if (warp >= kWarps) {
@@ -961,6 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0, piece = 0;
     uint32_t ph = 0;
     bool ok = true;
+    float* mo = merge;  // the last piece's buffer
     for (int flags = 0; !(flags & kLast);) {
       ok = consumer_wait(smem_u32(&bars[s]), ph, abort_flag, p.status, lane);
       if (!ok) break;
@@ -987,15 +1051,56 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = consumer_wait(smem_u32(&m_empty[buf]), (use & 1u) ^ 1u, abort_flag, p.status, lane);
           if (!ok) break;
         }
-        float* mo = merge + buf * buf_floats;
+        mo = merge + buf * buf_floats;
         cs.stash(mo, mo + ml_at, warp, g);
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&m_full[buf]));
+        if (lane == 0 && !(flags & kLast)) mbar_arrive(smem_u32(&m_full[buf]));
       }
     }
-    // segments of many parts that this CTA was the last to reach
-    if (ok && consumer_wait(smem_u32(merged), 0u, abort_flag, p.status, lane)) {
+    // the last piece, and segments of many parts that this CTA was the last to reach
+    if (ok && consumer_wait(smem_u32(merged), 0u, abort_flag, p.status, lane) && !*abort_flag) {
       ConsumerSync csync{smem_u32(&bars[2 * NS]), abort_flag, p.status, 0u};
+      csync(lane);  // every warp has stashed
+      const Last8 last = *reinterpret_cast<const Last8*>(misc + 32);
+      const int slot = 2 * blockIdx.x + (last.own == 0);
+      for (int i = tid; i < g * (kD / 4); i += kConsumers) {
+        float2 ml[kFewParts];
+        float4 x[kFewParts];
+#pragma unroll
+        for (int r = 0; r < kFewParts; ++r) {
+          ml[r] = make_float2(kMInit, 0.f);
+          x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float2 me;
+        float4 mine;
+        merge_warps8(mo, mo + ml_at, i, g, me.x, me.y, mine);
+        if (last.whole) {
+          store_column(p, last.pt.out_at, i, mine, me.y);
+        } else if (last.have) {
+          const float4 their = reinterpret_cast<const float4*>(other)[i];
+          const float2 tml = reinterpret_cast<const float2*>(other + g * kD)[i / (kD / 4)];
+          ml[0] = last.own == 0 ? me : tml;
+          x[0] = last.own == 0 ? mine : their;
+          ml[1] = last.own == 0 ? tml : me;
+          x[1] = last.own == 0 ? their : mine;
+          join_parts(p, last.pt.out_at, i, ml, x);
+        } else {
+          store_part(p, slot, i, me.x, me.y, mine);
+        }
+      }
+      if (!last.whole && last.have) {
+        if (tid == 0) *last.counter = 0;
+      } else if (!last.whole) {
+        csync(lane);
+        if (tid == 0) misc[2] = arrive_last(last.counter, last.pt.n);
+        csync(lane);
+        if (misc[2] && !*abort_flag) {
+          if (last.pt.n <= kFewParts)
+            merge_few(p, last.pt, tid, kConsumers);
+          else
+            merge_many(p, last.pt, reinterpret_cast<float*>(stages), csync, warp, lane);
+        }
+      }
       const int left = *(volatile int*)(misc + 3);
       for (int i = 0; i < left && !*abort_flag; ++i)
         merge_many(p, reinterpret_cast<const Part8*>(misc + 24)[i],
@@ -1087,28 +1192,35 @@ cudaError_t device8(const Device8** out) {
   return cudaSuccess;
 }
 
-// CTAs per segment in cluster mode, or 0 for the split over a flat list: the
-// most that let every segment have its cluster resident at once, or 1.  With
-// one sequence, whose heads are all as long, always where that is at least 8
-// (or as many as there are tiles).  Otherwise while the longest possible
-// segment leaves a CTA no more than kClusterTiles tiles and the clusters fit
-// the device kClusterWaves times: a wave of clusters costs about 4 us and 0.55
-// for each tile of its longest segment, the flat list 10 us and 0.69 for each
-// tile of an even share (108 segments of 10 tiles: 18 us by the list, 10 in
-// clusters of one; 332 of one tile at g = 16: 13.7 and 15.5).
-constexpr int kClusterTiles = 24;
-constexpr int kClusterWaves = 2;
+// CTAs per segment in cluster mode, or 0 for the split over a flat list.  The
+// cluster would be the largest that lets every segment have its own resident at
+// once, or one CTA; it is taken where it should be faster (us, measured):
+//   clusters   a wave: 4.1, and 0.55 for each tile of a CTA (g > 8: 4.6, 0.67)
+//   flat list  10, and 0.69 for each tile of a CTA's even share (g > 8: 13),
+//              and 0.007 for each head and part of a segment's merge
+// The host knows the cache's length only: a position is taken to lie half-way
+// on average, and the longest of several, which a cluster waits for, at the
+// end; a list is taken as full.  (One segment of 131072 rows, g = 2: 37 us in a
+// cluster, 17 by the list; of 16384 rows: 8 and 12; 108 segments of up to 10
+// tiles: 10 and 17.)
 int cluster_size8(const Kv8Params& p, const Device8& d) {
   if (g_decode_test_cluster >= 0)  // schedule tests only
     return min(g_decode_test_cluster, kMaxCluster);
   const long long nseg = (long long)p.B * p.Hkv;
   const long long rows = p.index ? (long long)p.count << p.lb : (long long)p.L;
   const int tiles = (int)((rows + kTile - 1) / kTile);
-  const int want = min(kMaxCluster, tiles);
-  int c = want;
+  int c = min(kMaxCluster, tiles);
   while (c > 1 && nseg > d.clusters[c]) --c;
-  if (p.B == 1 && c >= min(8, want)) return c;
-  return (tiles + c - 1) / c <= kClusterTiles && nseg <= (long long)kClusterWaves * d.sms ? c : 0;
+  const float mean = p.index ? (float)tiles : 0.5f * (float)tiles;
+  const float longest = p.B == 1 ? mean : (float)tiles;
+  const float waves = c > 1 ? 1.f : (float)((nseg + d.sms - 1) / d.sms);
+  const bool wide = p.g > 8;
+  const float clusters =
+      waves * ((wide ? 4.6f : 4.1f) + (wide ? 0.67f : 0.55f) * ceilf(longest / (float)c));
+  const float sms = (float)d.sms, parts = sms / (float)nseg;
+  const float flat = (wide ? 13.f : 10.f) + 0.69f * (float)nseg * mean / sms +
+                     (parts > 1.f ? 0.007f * (float)p.g * parts : 0.f);
+  return clusters <= flat ? c : 0;
 }
 
 // A cache [segs, L, 128] of codes as a 3-D tensor map, box 128 codes x rows x
