@@ -409,7 +409,7 @@ struct Consumer8 {
       for (int k = 0; k < 4; ++k) pr[k] = ex2(x[k] - (m[n][k & 1] - kShift));
       l[n][0] = fmaf(pr[0] + pr[2], meta.inv_vs, l[n][0]);
       l[n][1] = fmaf(pr[1] + pr[3], meta.inv_vs, l[n][1]);
-      // one rounding to fp16 (2^-12 relative), far below the bf16 output's 2^-9
+      // one rounding to fp16 (2^-11 relative), an eighth of the bf16 output's
       pb[n][0] = movm_trans(pack_f16x2(pr[0], pr[1]));
       pb[n][1] = movm_trans(pack_f16x2(pr[2], pr[3]));
     }
