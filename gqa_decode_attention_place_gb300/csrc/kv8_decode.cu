@@ -12,7 +12,7 @@
 // blocks' scales are.
 //
 // Bound by memory: a row costs 256 bytes for K and V, half of the bf16
-// cache's.  4.3 GB (B=256, g=8) take 591 us, 7.3 TB/s; 268 MB (B=32) 46 us at
+// cache's.  4.3 GB (B=256, g=8) take 591 to 603 us, 7.2 TB/s; 268 MB (B=32) 46 us at
 // g <= 8 and 54 at g = 16.  How:
 //  * 128-row tiles (32 KB for K and V) stream through a shared-memory ring by
 //    tiled TMA copies (128-byte swizzle: a row of codes is exactly one
