@@ -11,17 +11,18 @@
 // Selection.  Of the blocks 0..last a position has (last = pos / block): all
 // of them if there are no more than `count`; else the first `first`, the
 // `recent` last ones, and of the others the best-scored, ties to the lowest
-// index.  Scores become order-preserving integer keys; the need-th largest is
-// found digit by digit from the top (12, 12 and 8 bits: a histogram in shared
-// memory and a scan over its bins each), with the keys in registers; most
-// often the bin of the first digit is small, and its few keys are ranked among
-// themselves.  Each thread holds items in a row, so one scan over the threads'
-// counts places the chosen indices in ascending order.  Bound by its
-// instructions (512 rows of up to 8192 scores: 36 us with one bit a round, 20
-// with three digits a row, 15 this way).  The first digit holds
-// sign, exponent and three bits of the mantissa, so that scores of one size
-// still spread over many bins (the histogram's atomics contend only where
-// scores are alike).
+// index.  A row that fits the block's registers (8192 scores) has its range cut
+// into 4095 equal parts: a histogram in shared memory over them and a scan give
+// the part that the need-th largest lies in, and its few scores are ranked
+// among themselves.  Longer rows, and rows of another shape (infinities,
+// outliers, hundreds alike), go by order-preserving integer keys, digit by digit
+// from the top (12, 12 and 8 bits, a histogram and a scan each, scores read
+// again in every pass where they do not fit).  The first digit holds sign,
+// exponent and three bits of the mantissa.  Each thread holds items in a row, so
+// one scan over the threads' counts places the chosen indices in ascending
+// order.  Bound by its instructions (512 rows of up to 8192 scores: 36 us with
+// one bit a round, 20 with three digits, 15 with one digit and up to 256 keys
+// ranked, 11.2 with equal parts and four blocks to an SM).
 #include "common.cuh"
 #include "decode_params.h"
 #include "internal.h"
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 4096;
-constexpr int kListed = 256;  // a bin this small is ranked directly
+constexpr int kListed = 256;  // a bin of keys this small is ranked directly
+constexpr int kFew = 64;      // a part of the scores' range this small is
 static_assert(kSelectThreads == 2 * kListed, "two threads to a listed key");
 
 // Order-preserving key of a score: larger score, larger key, never 0; -0 is
@@ -121,6 +123,10 @@ static_assert(kSelectThreads == 2 * kListed, "two threads to a listed key");
 __device__ __forceinline__ uint32_t score_key(float x) {
   const uint32_t u = __float_as_uint(fmaxf(x, -INFINITY) + 0.f);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
 }
 
 // Exclusive prefix sum of v over the block's threads; *all = the total.  One
@@ -145,7 +151,7 @@ __device__ __forceinline__ int block_scan(int v, uint32_t (*slots)[32], int& pha
 // more than one chunk, whose scores are read again in every pass; else the
 // keys stay in registers.
 template <int I, bool LOOP>
-__global__ void __launch_bounds__(kSelectThreads, 3) block_select_kernel(
+__global__ void __launch_bounds__(kSelectThreads, I == 16 && !LOOP ? 4 : 3) block_select_kernel(
     const float* __restrict__ scores, const int32_t* __restrict__ positions, int32_t* out,
     int Hkv, int L, int block, int nb, int count, int first, int recent) {
   static_assert(I % 4 == 0, "scores come in fours");
@@ -198,7 +204,122 @@ __global__ void __launch_bounds__(kSelectThreads, 3) block_select_kernel(
   int left = need;            // and `left` of those in that bin: the largest, the lowest indices
   bool whole = true;          // ... which are all of them
   bool listed = false;        // ... which are ranked in a list
-  if (need > 0) {
+  // In the histogram, the bin of the left-th largest: thread t holds 8 bins
+  // from the top.
+  auto find = [&]() {
+    __syncthreads();
+    constexpr int kPer = kBins / kSelectThreads;
+    static_assert(kPer == 8, "two int4 per thread");
+    int c[kPer], sum = 0, all;
+    const int top = kBins - 1 - tid * kPer;
+    *reinterpret_cast<int4*>(c) = *reinterpret_cast<const int4*>(&hist[top - 7]);
+    *reinterpret_cast<int4*>(c + 4) = *reinterpret_cast<const int4*>(&hist[top - 3]);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += c[i];
+    int before = block_scan(sum, slots, phase, &all);
+    if (before < left && before + sum >= left) {  // one thread
+#pragma unroll
+      for (int i = kPer - 1; i >= 0; --i) {
+        if (before < left && before + c[i] >= left) {
+          found[0] = top - 7 + i;
+          found[1] = left - before;
+          found[2] = c[i];
+          found[3] = 0;  // the list's length
+        }
+        before += c[i];
+      }
+    }
+    __syncthreads();
+    whole = found[2] == found[1];
+  };
+  unsigned long long* list = reinterpret_cast<unsigned long long*>(hist);  // [kListed]
+  // A score and its index as one number: a larger score first, then a lower index.
+  auto entry = [&](uint32_t k, int j) { return ((unsigned long long)k << 32) | (uint32_t)~j; };
+  bool done = need == 0;
+  uint32_t sure = 0;  // bit i: item i is chosen (done)
+  if (!LOOP && !done) {
+    // One row in registers: its range in 4095 equal parts (part 0: no
+    // candidate), which rise with the score; scores of any common shape spread
+    // over them so well that the last part to be chosen from holds only few.
+    float x[I];
+    float low = INFINITY, high = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < I; g += 4) {
+      const int j = j0 + g;
+      if (j >= lo && j + 4 <= hi) {
+        const float4 f = *reinterpret_cast<const float4*>(sc + j);
+        x[g] = fmaxf(f.x, -INFINITY);  // NaN is taken as -inf
+        x[g + 1] = fmaxf(f.y, -INFINITY);
+        x[g + 2] = fmaxf(f.z, -INFINITY);
+        x[g + 3] = fmaxf(f.w, -INFINITY);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          x[g + k] = j + k >= lo && j + k < hi ? fmaxf(sc[j + k], -INFINITY)
+                                               : __uint_as_float(0x7fffffffu);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // (a NaN is passed over)
+        low = fminf(low, x[g + k]);
+        high = fmaxf(high, x[g + k]);
+      }
+    }
+    uint32_t k_low = __reduce_min_sync(0xffffffffu, score_key(low));
+    uint32_t k_high = __reduce_max_sync(0xffffffffu, score_key(high));
+    const int lane = tid & 31;
+    if (lane == 0) {
+      slots[0][tid >> 5] = k_low;
+      slots[1][tid >> 5] = k_high;
+    }
+    __syncthreads();  // and the histogram is clear
+    k_low = __reduce_min_sync(0xffffffffu, slots[0][lane & (kSelectWarps - 1)]);
+    k_high = __reduce_max_sync(0xffffffffu, slots[1][lane & (kSelectWarps - 1)]);
+    low = key_score(k_low);
+    const float span = key_score(k_high) - low;
+    if (span > 1e-30f && span < 1e30f) {  // (neither infinities nor scores all alike)
+      const float per_unit = (float)(kBins - 2) / span;
+      uint32_t part[I / 2];
+#pragma unroll
+      for (int i = 0; i < I; ++i) {
+        const uint32_t d =
+            x[i] == x[i] ? (uint32_t)min((int)((x[i] - low) * per_unit), kBins - 2) + 1u : 0u;
+        if (d != 0u) atomicAdd(&hist[d], 1);
+        if (i & 1) part[i >> 1] |= d << 16;
+        else part[i >> 1] = d;
+      }
+      find();
+      if (whole || found[2] <= kFew) {
+        done = true;
+        const uint32_t d = (uint32_t)found[0], from = whole ? d : d + 1;
+        uint32_t mine = 0;  // the items in part d
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+          const uint32_t e = i & 1 ? part[i >> 1] >> 16 : part[i >> 1] & 0xffffu;
+          if (e >= from) sure |= 1u << i;
+          if (e == d) mine |= 1u << i;
+        }
+        if (!whole) {
+          left = found[1];
+          for (uint32_t r = mine; r; r &= r - 1u) {
+            const int j = j0 + __ffs((int)r) - 1;
+            list[atomicAdd(&found[3], 1)] = entry(score_key(sc[j]), j);
+          }
+          __syncthreads();
+          const int m = found[3];
+          for (uint32_t r = mine; r; r &= r - 1u) {
+            const int i = __ffs((int)r) - 1;
+            const unsigned long long me = entry(score_key(sc[j0 + i]), j0 + i);
+            int above = 0;
+            for (int k = 0; k < m; ++k) above += list[k] > me;
+            if (above < left) sure |= 1u << i;
+          }
+        }
+      } else {
+        clear();
+      }
+    }
+  }
+  if (!done) {
     if (!LOOP) load(0);
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 20 : pass == 1 ? 8 : 0;
@@ -211,56 +332,26 @@ __global__ void __launch_bounds__(kSelectThreads, 3) block_select_kernel(
         for (int i = 0; i < I; ++i)
           if (key[i] != 0u && (key[i] & mask) == th) atomicAdd(&hist[(key[i] >> shift) & digits], 1);
       }
-      __syncthreads();
-      // the digit of the left-th largest: thread t holds 8 bins from the top
-      constexpr int kPer = kBins / kSelectThreads;
-      static_assert(kPer == 8, "two int4 per thread");
-      int c[kPer], sum = 0, all;
-      const int top = kBins - 1 - tid * kPer;
-      *reinterpret_cast<int4*>(c) = *reinterpret_cast<const int4*>(&hist[top - 7]);
-      *reinterpret_cast<int4*>(c + 4) = *reinterpret_cast<const int4*>(&hist[top - 3]);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) sum += c[i];
-      int before = block_scan(sum, slots, phase, &all);
-      if (before < left && before + sum >= left) {  // one thread
-#pragma unroll
-        for (int i = kPer - 1; i >= 0; --i) {
-          if (before < left && before + c[i] >= left) {
-            found[0] = top - 7 + i;
-            found[1] = left - before;
-            found[2] = c[i];
-            found[3] = 0;  // the list's length
-          }
-          before += c[i];
-        }
-      }
-      __syncthreads();
+      find();
       th |= (uint32_t)found[0] << shift;
       mask |= digits << shift;
       left = found[1];
-      const int in_bin = found[2];
-      whole = in_bin == left;
-      if (whole) break;
-      if (!LOOP && in_bin <= kListed) {  // few: rank them among themselves
-        listed = true;
-        break;
-      }
+      listed = !LOOP && !whole && found[2] <= kListed;  // few: rank them among themselves
+      if (whole || listed) break;
     }
   }
   const uint32_t bin_top = th | ~mask;  // the bin's largest possible key
-  // The bin's keys and indices as one number (a larger key first, then a lower
-  // index), in any order, and each one's rank among them: chosen if below
-  // `left`.  The list takes the histogram's place; a thread keeps its item's
-  // place in it where the key was.
-  unsigned long long* list = reinterpret_cast<unsigned long long*>(hist);  // [kListed]
-  int* rank_of = hist + 2 * kListed;                                       // [kListed]
+  // The bin's entries, in any order, and each one's rank among them: chosen if
+  // below `left`.  The list takes the histogram's place; a thread keeps its
+  // item's place in it where the key was.
+  int* rank_of = hist + 2 * kListed;  // [kListed]
   uint32_t in_list = 0;  // bit i: key[i] is a place
   if (listed) {
 #pragma unroll
     for (int i = 0; i < I; ++i)
       if (key[i] >= th && key[i] <= bin_top) {
         const int k = atomicAdd(&found[3], 1);
-        list[k] = ((unsigned long long)key[i] << 32) | (uint32_t)~(j0 + i);
+        list[k] = entry(key[i], j0 + i);
         key[i] = (uint32_t)k;
         in_list |= 1u << i;
       }
@@ -282,9 +373,9 @@ __global__ void __launch_bounds__(kSelectThreads, 3) block_select_kernel(
   // Place the chosen indices in ascending order: a count per thread, a scan.
   int base = 0, tie_base = 0;
   for (int at = 0; at < end; at += kChunk) {
-    if (LOOP && need > 0) load(at);
-    uint32_t take = 0;  // bit i: item i of this thread
-    if (need > 0) {
+    if (LOOP && !done) load(at);
+    uint32_t take = sure;  // bit i: item i of this thread
+    if (!done) {
       // keys that are chosen for sure: above the bin, or all of it too (th > 0)
       const uint32_t above = whole ? th - 1u : bin_top;
 #pragma unroll

@@ -113,3 +113,26 @@ def test_scores_past_the_position_are_ignored():
     s = torch.zeros((1, 1, 400), device="cuda")
     s[..., 200:] = math.inf
     _select(s, [200 * 16 - 1], 6400, 16, 10, 1, 1)
+
+
+@pytest.mark.parametrize("nb", [300, 2048, 8189, 8192])
+@pytest.mark.parametrize("shape", ["close", "outlier", "tiny", "huge", "two", "wide", "coarse",
+                                   "stairs", "one_low"])
+def test_select_distributions(shape, nb):
+    """Scores that spread evenly over their range, and ones of which most lie in a small part."""
+    gen = torch.Generator(device="cuda").manual_seed(64)
+    r = torch.randn((3, 2, nb), generator=gen, device="cuda")
+    s = {
+        "close": 1000 + r,
+        "outlier": torch.where(r == r.amax(-1, keepdim=True), torch.full_like(r, 1e20), r),
+        "tiny": r * 1e-33,
+        "huge": r * 1e37,
+        "two": torch.where(r > 0, r * 1e-3 + 5, r * 1e-3 - 5),
+        "wide": torch.exp(r * 12),
+        "coarse": (r * 20).bfloat16().float(),
+        "stairs": torch.floor(r * 3),
+        "one_low": torch.where(r == r.amin(-1, keepdim=True), torch.full_like(r, -math.inf), r),
+    }[shape]
+    pos = [nb * 16 - 1, nb * 16 - 17, nb * 8]
+    for count, first, recent in ((1, 0, 0), (40, 1, 2), (nb // 2, 0, 1), (nb - 3, 1, 1)):
+        _select(s, pos, nb * 16, 16, count, first, recent)
