@@ -22,7 +22,7 @@
 // one scan over the threads' counts places the chosen indices in ascending
 // order.  Bound by its instructions (512 rows of up to 8192 scores: 36 us with
 // one bit a round, 20 with three digits, 15 with one digit and up to 256 keys
-// ranked, 11.2 with equal parts and four blocks to an SM).
+// ranked, 10.7 with equal parts and four blocks to an SM).
 #include "common.cuh"
 #include "decode_params.h"
 #include "internal.h"
@@ -243,8 +243,10 @@ __global__ void __launch_bounds__(kSelectThreads, I == 16 && !LOOP ? 4 : 3) bloc
     // over them so well that the last part to be chosen from holds only few.
     float x[I];
     float low = INFINITY, high = -INFINITY;
+    const bool some = j0 < hi && j0 + I > lo;  // (few threads of a short row have candidates)
 #pragma unroll
     for (int g = 0; g < I; g += 4) {
+      if (!some) break;
       const int j = j0 + g;
       if (j >= lo && j + 4 <= hi) {
         const float4 f = *reinterpret_cast<const float4*>(sc + j);
@@ -281,6 +283,7 @@ __global__ void __launch_bounds__(kSelectThreads, I == 16 && !LOOP ? 4 : 3) bloc
       uint32_t part[I / 2];
 #pragma unroll
       for (int i = 0; i < I; ++i) {
+        if (!some) break;
         const uint32_t d =
             x[i] == x[i] ? (uint32_t)min((int)((x[i] - low) * per_unit), kBins - 2) + 1u : 0u;
         if (d != 0u) atomicAdd(&hist[d], 1);
@@ -294,6 +297,7 @@ __global__ void __launch_bounds__(kSelectThreads, I == 16 && !LOOP ? 4 : 3) bloc
         uint32_t mine = 0;  // the items in part d
 #pragma unroll
         for (int i = 0; i < I; ++i) {
+          if (!some) break;
           const uint32_t e = i & 1 ? part[i >> 1] >> 16 : part[i >> 1] & 0xffffu;
           if (e >= from) sure |= 1u << i;
           if (e == d) mine |= 1u << i;
