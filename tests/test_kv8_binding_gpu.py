@@ -58,3 +58,90 @@ def test_sizes_past_32_bits_are_refused():
     for _ in range(3):
         with pytest.raises(ValueError, match="out of range"):
             ga.attn_decode_step_kv8(q, at, cache, cache, scale, scale, 16, SCALE, workspace=ws)
+
+
+def test_calls_from_several_threads():
+    """Four threads, each with its own stream, workspace and output; the same bits as alone."""
+    import threading
+
+    L, block, B = 2000, 32, 5
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    kc, vc = (codes_cache(B, 2, L, gen) for _ in "kv")
+    ks, vs = (scales(B, 2, L, block, gen) for _ in "kv")
+    bounds = torch.randn((B, 2, -(-L // block), 2, D), generator=gen, device="cuda")
+    bounds = bounds.sort(dim=3, descending=True).values.bfloat16()
+    q = [torch.randn((B, 16, D), generator=gen, device="cuda").bfloat16() for _ in range(4)]
+    at = torch.tensor([0, 1999, 300, 1024, 77], dtype=torch.int32, device="cuda")
+
+    def step(x, **kw):
+        return (ga.attn_decode_step_kv8(x, at, kc, vc, ks, vs, block, SCALE, **kw),
+                ga.attn_decode_step_kv8_sparse(x, at, kc, vc, ks, vs, bounds, block, 9, SCALE,
+                                               **kw))
+
+    want = [step(x) for x in q]
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(4)
+
+    def many(i):
+        s = torch.cuda.Stream()
+        start.wait()
+        for _ in range(50):
+            got = step(q[i], stream=s)
+            s.synchronize()
+            if not all(torch.equal(a.view(torch.int16), b.view(torch.int16))
+                       for a, b in zip(got, want[i])):
+                wrong.append(i)
+                return
+
+    threads = [threading.Thread(target=many, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+CAPTURE_FIRST = """
+import torch, gqa_decode_attention_place_gb300 as ga
+B, Hkv, L, block = 3, 2, 700, 16
+g = torch.Generator(device="cuda").manual_seed(9)
+codes = lambda: (torch.randn((B, Hkv, L, 128), generator=g, device="cuda") * 50).to(torch.float8_e4m3fn)
+kc, vc = codes(), codes()
+nb = -(-L // block)
+ks, vs = (torch.full((B, Hkv, nb), 2.0 ** -7, device="cuda") for _ in "kv")
+bounds = torch.zeros((B, Hkv, nb, 2, 128), dtype=torch.bfloat16, device="cuda")
+q = torch.randn((B, 8, 128), generator=g, device="cuda").bfloat16()
+k = torch.randn((B, Hkv, 128), generator=g, device="cuda").bfloat16()
+at = torch.tensor([5, 699, 350], dtype=torch.int32, device="cuda")
+ws = ga.kv8_sparse_workspace(B, 8, Hkv, L, 128, block, 6)
+out, qn, kn = torch.empty_like(q), torch.empty_like(q), torch.empty_like(k)
+def step():
+    ga.attn_qk_norm_rope(q, k, None, None, 1e-6, at, q_out=qn, k_out=kn)
+    ga.attn_kv8_append(kn, kn, at, kc, vc, ks, vs, block, k_bounds=bounds)
+    ga.attn_decode_step_kv8_sparse(qn, at, kc, vc, ks, vs, bounds, block, 6, 0.1, out=out, workspace=ws)
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+first = out.clone()
+out.zero_()
+step()
+torch.cuda.synchronize()
+assert torch.equal(first.view(torch.int16), out.view(torch.int16)) and torch.isfinite(first).all()
+print("same")
+"""
+
+
+def test_a_process_whose_first_calls_are_captured():
+    """Nothing has to run before a capture: what the calls find out about the device at their first
+    use needs no stream."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURE_FIRST], capture_output=True, text=True,
+                       cwd=root, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr
