@@ -65,8 +65,9 @@ constexpr int kMergeThreads = 64;           // two warps that merge (flat list)
 constexpr int kThreads = kConsumers + 64 + kMergeThreads;  // and two producer warps
 constexpr int kClusterThreads = kConsumers + 64;
 constexpr int kMaxStages = 6;
-constexpr int kMiscInts = 48;  // [0] abort, [2] last, [3] segments left over, [8..16) scan,
-                               // [24..32) those segments, [32..48) the last piece
+constexpr int kMiscInts = 48;  // [0] abort, [1] the last piece's other part is there, [2] last to
+                               // arrive, [3] segments left over, [8..16) scan, [24..32) those
+                               // segments, [32..48) the last piece
 constexpr int kNoRow = 0x40000000;          // row of a slice that holds nothing
 constexpr float kMInit = -3e38f;            // running maximum before any row
 constexpr float kTau = 8.f;                 // the running maximum may lag by 2^kTau
@@ -795,10 +796,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           last->whole = whole;
           last->own = own;
           last->have = have;
-          misc[2] = have;
+          misc[1] = have;  // (misc[2] may still be being read for the piece before)
         }
         msync(lane);
-        if (misc[2]) {
+        if (misc[1]) {
           const size_t at = (size_t)part_slot(pt, 1 - own) * g;
           const float4* o = reinterpret_cast<const float4*>(p.part_o + at * kD);
 #pragma unroll 8
