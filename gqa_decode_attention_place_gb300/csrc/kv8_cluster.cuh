@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
     for (int r = 0; r < C; ++r) {
       const Landing& x = land[r * cols + j];
       const float e = ex2(x.m - M);
-      l = fmaf(x.l, e, l);
+      l += moved(x.l, x.m - M);
       o.x = fmaf(x.o.x, e, o.x);
       o.y = fmaf(x.o.y, e, o.y);
       o.z = fmaf(x.o.z, e, o.z);

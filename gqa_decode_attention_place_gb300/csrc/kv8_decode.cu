@@ -3,13 +3,16 @@
 // rows up to each position or over the rows of listed blocks only.
 //
 // For sequence b, query head h and KV head h/g, over the attended rows j:
-//   s_j   = scale * ks_j * (q . k8_j)          ks_j, vs_j: the scales of j's block
-//   out   = sum_j 2^(x_j - M) v8_j / sum_j 2^(x_j - M) / vs_j,
-//   x_j   = log2(e) s_j + log2(vs_j),  M = max x_j
-// which is softmax(s) (vs v8) with the value scale moved into the exponent:
-// every probability then enters its product on the scale of what it
-// contributes, so one fp16 rounding of 2^(x_j - M) is enough whatever the
-// blocks' scales are.
+//   s_j   = log2(e) scale * ks_j * (q . k8_j)    ks_j, vs_j: the scales of j's block
+//   w_j   = 2^(s_j - M),  M = max_j (s_j + log2 vs_j)
+//   out   = sum_j (w_j vs_j) v8_j / sum_j w_j
+// which is softmax(s) (vs v8) relative to the row that contributes most, not
+// the one that weighs most: w_j vs_j <= 1 enters the product on the scale of
+// what it contributes, so one fp16 rounding is enough whatever the blocks'
+// scales are.  The sum of the w_j stays in fp32 and in range: with scales of
+// 2^-60 to 2^60 its largest lies between 2^-60 and 2^60 of M, and a factor
+// between two maxima, as far as 2^-120 and more, comes in two halves (moved):
+// in one it would be zero below 2^-126, and weight lost with it.
 //
 // Bound by memory: a row costs 256 bytes for K and V, half of the bf16
 // cache's.  4.3 GB (B=256, g=8) take 591 to 603 us, 7.2 TB/s; 268 MB (B=32) 46 us at
@@ -83,20 +86,27 @@ constexpr int kLast = 0x400;                // the CTA's last tile
 struct SliceMeta {
   int rows;       // how many of the slice's rows count (0..16), and the tile's flags
   float ks;       // K scale
-  float lv;       // log2 of the V scale
-  float inv_vs;   // 1 / V scale
+  float vs;       // V scale
+  float lv;       // its log2
 };
 
 __device__ __forceinline__ SliceMeta slice_meta(int rows, float ks, float vs) {
   SliceMeta mt;
   mt.rows = rows;
   mt.ks = ks;
+  mt.vs = vs;
   // log2 of a power of two comes out exact
   const uint32_t bits = __float_as_uint(vs);
   mt.lv = (float)((int)(bits >> 23) - 127) +
           log2f(__uint_as_float((bits & 0x7fffffu) | 0x3f800000u));
-  mt.inv_vs = 1.f / vs;
   return mt;
+}
+
+// A sum of weights relative to one maximum, relative to another that lies
+// 2^-d away.
+__device__ __forceinline__ float moved(float sum, float d) {
+  const float half = ex2(0.5f * d);
+  return sum * half * half;
 }
 
 struct Kv8Params {
@@ -396,8 +406,8 @@ struct Consumer8 {
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], off));
           const float to = mx[e] > m[n][e] + kTau ? mx[e] : m[n][e];
           const float alpha = ex2(m[n][e] - to);
+          l[n][e] = moved(l[n][e], m[n][e] - to);
           m[n][e] = to;
-          l[n][e] *= alpha;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             o[n][i][e] *= alpha;
@@ -405,11 +415,15 @@ struct Consumer8 {
           }
         }
       }
+      // the weights, up to 2^(kShift + kTau) / vs, and what they count in the product
+      const float ref[2] = {m[n][0] - kShift + meta.lv, m[n][1] - kShift + meta.lv};
       float pr[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) pr[k] = ex2(x[k] - (m[n][k & 1] - kShift));
-      l[n][0] = fmaf(pr[0] + pr[2], meta.inv_vs, l[n][0]);
-      l[n][1] = fmaf(pr[1] + pr[3], meta.inv_vs, l[n][1]);
+      for (int k = 0; k < 4; ++k) pr[k] = ex2(x[k] - ref[k & 1]);
+      l[n][0] += pr[0] + pr[2];
+      l[n][1] += pr[1] + pr[3];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pr[k] *= meta.vs;
       // one rounding to fp16 (2^-11 relative), an eighth of the bf16 output's
       pb[n][0] = movm_trans(pack_f16x2(pr[0], pr[1]));
       pb[n][1] = movm_trans(pack_f16x2(pr[2], pr[3]));
@@ -480,7 +494,7 @@ __device__ __forceinline__ void merge_warps8(const float* mo, const float* mml, 
   for (int ww = 0; ww < kWarps; ++ww) {
     const float e = ex2(ml[ww].x - M);
     const float4 x = *reinterpret_cast<const float4*>(mo + merge_row(ww, h, g) + d);
-    ls = fmaf(ml[ww].y, e, ls);
+    ls += moved(ml[ww].y, ml[ww].x - M);
     os.x = fmaf(x.x, e, os.x);
     os.y = fmaf(x.y, e, os.y);
     os.z = fmaf(x.z, e, os.z);
@@ -528,7 +542,7 @@ __device__ __forceinline__ void join_parts(const Kv8Params& p, size_t out_at, in
 #pragma unroll
   for (int r = 0; r < kFewParts; ++r) {
     const float e = ex2(ml[r].x - M);
-    ls = fmaf(ml[r].y, e, ls);
+    ls += moved(ml[r].y, ml[r].x - M);
     o.x = fmaf(x[r].x, e, o.x);
     o.y = fmaf(x[r].y, e, o.y);
     o.z = fmaf(x[r].z, e, o.z);
@@ -586,9 +600,9 @@ __device__ __forceinline__ void merge_many(const Kv8Params& p, const Part8& pt, 
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     for (int r = lane; r < n; r += 32) {
-      const float e = ex2(wt[r * g + h] - M);
-      wt[r * g + h] = e;
-      sum = fmaf(ls[r * g + h], e, sum);
+      const float d = wt[r * g + h] - M;
+      wt[r * g + h] = ex2(d);
+      sum += moved(ls[r * g + h], d);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
