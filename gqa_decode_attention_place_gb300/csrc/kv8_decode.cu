@@ -8,8 +8,8 @@
 //   out   = sum_j (w_j vs_j) v8_j / sum_j w_j
 // which is softmax(s) (vs v8) relative to the row that contributes most, not
 // the one that weighs most: w_j vs_j <= 1 enters the product on the scale of
-// what it contributes, so one fp16 rounding is enough whatever the blocks'
-// scales are.  The sum of the w_j stays in fp32 and in range: with scales of
+// what it contributes, so fp16 parts carry it whatever the blocks' scales are.
+// The sum of the w_j stays in fp32 and in range: with scales of
 // 2^-60 to 2^60 its largest lies between 2^-60 and 2^60 of M, and a factor
 // between two maxima, as far as 2^-120 and more, comes in two halves (moved):
 // in one it would be zero below 2^-126, and weight lost with it.
@@ -302,6 +302,7 @@ __device__ __forceinline__ void ldmatrix_codes(uint32_t (&r)[4], uint32_t addr) 
 //    16i + 8 + c (row c+8).
 template <int NT>
 struct Consumer8 {
+  static constexpr bool kTwoParts = NT == 1;  // of a probability
   uint32_t qb[NT][8][2];
   float o[NT][8][4];
   float m[NT][2], l[NT][2], qk[NT][2];
@@ -386,7 +387,7 @@ struct Consumer8 {
       for (int n = 0; n < NT; ++n)
         mma_f16(s[n][w & 1], a0, a1, a2, a3, qb[n][w][0], qb[n][w][1]);
     }
-    uint32_t pb[NT][2];
+    uint32_t pb[NT][2], rest[2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float x[4];
@@ -424,9 +425,20 @@ struct Consumer8 {
       l[n][1] += pr[1] + pr[3];
 #pragma unroll
       for (int k = 0; k < 4; ++k) pr[k] *= meta.vs;
-      // one rounding to fp16 (2^-11 relative), an eighth of the bf16 output's
-      pb[n][0] = movm_trans(pack_f16x2(pr[0], pr[1]));
-      pb[n][1] = movm_trans(pack_f16x2(pr[2], pr[3]));
+      // Rounded to fp16; up to 8 heads what that leaves (22 bits together)
+      // enters as well, for nothing where memory bounds the call (268 MB at
+      // g = 8: 46.7 us without, 47.0 with; a CTA's tile 0.03 us more).  At more
+      // heads the warps' own work does (g = 16: 53.5 and 59.2 us), and the one
+      // rounding of 2^-12, an eighth of the bf16 output's, stays.
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t hi = pack_f16x2(pr[2 * k], pr[2 * k + 1]);
+        pb[n][k] = movm_trans(hi);
+        if (kTwoParts) {
+          const float2 f = f16x2_to_f32x2(hi);
+          rest[k] = movm_trans(pack_f16x2(pr[2 * k] - f.x, pr[2 * k + 1] - f.y));
+        }
+      }
     }
     // rows that do not count may be NaN: 0 * NaN would spread
     const int seen = rows - 4 * t;  // of this lane's four rows
@@ -446,7 +458,10 @@ struct Consumer8 {
         const uint32_t a0 = e4m3x2_to_f16x2(lo), a2 = e4m3x2_to_f16x2(lo >> 16);
         const uint32_t a1 = e4m3x2_to_f16x2(hi), a3 = e4m3x2_to_f16x2(hi >> 16);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_f16(o[n][i + j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+        for (int n = 0; n < NT; ++n) {
+          mma_f16(o[n][i + j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+          if (kTwoParts) mma_f16(o[n][i + j], a0, a1, a2, a3, rest[0], rest[1]);
+        }
       }
     }
   }

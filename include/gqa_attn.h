@@ -423,8 +423,9 @@ size_t attn_kv8_workspace_size(int B, int Hq, int Hkv, int L, int D);
  *     out[b,h,:] = softmax_j(scale * q[b,h,:] . ks_j k_j) (vs_j v_j)
  * with the codes k_j, v_j and scales ks_j, vs_j of row j and KV head h / g.
  * Codes enter both products exactly (as fp16), q exactly to 2^-22 of its
- * head's largest element, the probabilities rounded once to fp16; sums in
- * fp32.  Codes and scales of rows above positions[b] are not used and may hold
+ * head's largest element, the probabilities (relative to the row that
+ * contributes most) as two fp16 parts for g <= 8 (22 bits) and rounded once to
+ * fp16 for g > 8; sums in fp32.  Codes and scales of rows above positions[b] are not used and may hold
  * anything.
  *
  *   Supported: D == 128; any g = Hq / Hkv from 1 to 16; B <= 8192;
