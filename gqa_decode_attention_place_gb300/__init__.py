@@ -28,7 +28,7 @@ __all__ = [
     "attn_read_prefill_status", "attn_last_cuda_error", "decode_workspace", "attn_decode_step_noalloc",
     "attn_decode_step_append", "attn_decode_step_rope_append", "attn_decode_stream_step",
     "attn_decode_step_window", "attn_decode_multi", "attn_test_skip_tile",
-    "attn_debug_build", "attn_read_prefill_skips", "debug_collect_range_bits",
+    "attn_debug_build", "attn_read_prefill_skips", "attn_read_range_skips", "debug_collect_range_bits",
     "attn_test_force_schedule",
     "attn_qk_norm_rope", "attn_qk_norm_rope_append", "attn_kv8_append", "attn_kv8_workspace_size",
     "kv8_workspace", "attn_decode_step_kv8", "attn_block_scores", "attn_block_select",
@@ -122,6 +122,8 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.attn_debug_build.restype = i32
     lib.attn_read_prefill_skips.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
     lib.attn_read_prefill_skips.restype = i32
+    lib.attn_read_range_skips.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
+    lib.attn_read_range_skips.restype = i32
     i64 = ctypes.c_int64
     lib.attn_qk_norm_rope.argtypes = [vp, vp, i64, i64, vp, vp, f32, vp, vp, vp, i32, i32, i32,
                                       i32, i32, vp, vp, vp]
@@ -223,9 +225,10 @@ def decode_workspace(B: int, Hq: int, Hkv: int, L: int, D: int, device=None) -> 
 def debug_collect_range_bits() -> int:
     """Range-checked builds: synchronise, then return ATTN_DEV_RANGE if any
     decode launch since the last call skipped an access (read from every
-    workspace decode_workspace() handed out, and from the status reads callers
-    made themselves) or if a prefill launch did; clears all of it.  Always 0
-    in release builds."""
+    workspace decode_workspace(), kv8_workspace() and kv8_sparse_workspace()
+    handed out, and from the status reads callers made themselves) or if a
+    prefill launch or a call without a workspace did; clears all of it.
+    Always 0 in release builds."""
     global _DEBUG_RANGE_SEEN
     if not attn_debug_build():
         return 0
@@ -234,7 +237,7 @@ def debug_collect_range_bits() -> int:
         bits |= attn_read_device_status(ws)
     _DEBUG_WORKSPACES.clear()
     _DEBUG_RANGE_SEEN = 0
-    if attn_read_prefill_skips():
+    if attn_read_prefill_skips() or attn_read_range_skips():
         bits |= ATTN_DEV_RANGE
     return bits & ATTN_DEV_RANGE
 
@@ -500,6 +503,16 @@ def attn_read_prefill_skips(stream=None) -> int:
     code = load_library().attn_read_prefill_skips(ctypes.byref(n), _stream(stream))
     if code not in (0, 5):
         raise AttnError(code, "attn_read_prefill_skips")
+    return int(n.value)
+
+
+def attn_read_range_skips(stream=None) -> int:
+    """The same count for the calls without a workspace: the norm with
+    rotation, the 8-bit append, the block scores and the selection."""
+    n = ctypes.c_uint32(0)
+    code = load_library().attn_read_range_skips(ctypes.byref(n), _stream(stream))
+    if code not in (0, 5):
+        raise AttnError(code, "attn_read_range_skips")
     return int(n.value)
 
 

@@ -30,6 +30,8 @@
 namespace gqa {
 namespace {
 
+__device__ unsigned int g_block_skips;  // debug builds: accesses a range check skipped
+
 constexpr int kScoreWarps = 4;  // (8: 26.6 us for 142 MB, 4: 23.7)
 constexpr int kScoreThreads = kScoreWarps * 32;
 constexpr int kScoreBlocksPerWarp = 16;
@@ -64,6 +66,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(
   const int j0 = blockIdx.y * kScoreBlocksPerCta + warp * kScoreBlocksPerWarp;
   const int cta0 = blockIdx.y * kScoreBlocksPerCta;
   float* out = scores + (size_t)seg * nb;
+  if (!range_ok_count(n <= nb, &g_block_skips)) return;  // so j < n is inside bounds and scores
   if (cta0 >= n) {  // nothing here up to the position
     for (int j = cta0 + tid; j < min(nb, cta0 + kScoreBlocksPerCta); j += kScoreThreads)
       out[j] = -INFINITY;
@@ -170,6 +173,7 @@ __global__ void __launch_bounds__(kSelectThreads, I == 16 && !LOOP ? 4 : 3) bloc
   const int pos = positions[b];
   const int n = rows_in_cache(pos, 0, L) ? pos / block + 1 : 0;
   int32_t* o = out + (size_t)seg * count;
+  if (!range_ok_count(n <= nb, &g_block_skips)) return;  // so the items below hi are in the row
   if (n <= count) {
     for (int i = tid; i < count; i += kSelectThreads) o[i] = i < n ? i : -1;
     return;
@@ -305,11 +309,12 @@ __global__ void __launch_bounds__(kSelectThreads, I == 16 && !LOOP ? 4 : 3) bloc
         if (!whole) {
           left = found[1];
           for (uint32_t r = mine; r; r &= r - 1u) {
-            const int j = j0 + __ffs((int)r) - 1;
-            list[atomicAdd(&found[3], 1)] = entry(score_key(sc[j]), j);
+            const int j = j0 + __ffs((int)r) - 1, k = atomicAdd(&found[3], 1);
+            if (range_ok_count(k < kListed && j >= lo && j < hi, &g_block_skips))
+              list[k] = entry(score_key(sc[j]), j);
           }
           __syncthreads();
-          const int m = found[3];
+          const int m = kDebugChecks ? min(found[3], kListed) : found[3];
           for (uint32_t r = mine; r; r &= r - 1u) {
             const int i = __ffs((int)r) - 1;
             const unsigned long long me = entry(score_key(sc[j0 + i]), j0 + i);
@@ -355,13 +360,14 @@ __global__ void __launch_bounds__(kSelectThreads, I == 16 && !LOOP ? 4 : 3) bloc
     for (int i = 0; i < I; ++i)
       if (key[i] >= th && key[i] <= bin_top) {
         const int k = atomicAdd(&found[3], 1);
+        if (!range_ok_count(k < kListed, &g_block_skips)) continue;
         list[k] = entry(key[i], j0 + i);
         key[i] = (uint32_t)k;
         in_list |= 1u << i;
       }
     if (tid < kListed) rank_of[tid] = 0;
     __syncthreads();
-    const int m = found[3];
+    const int m = kDebugChecks ? min(found[3], kListed) : found[3];
     // two threads to a key, or four if that covers the list
     const int parts = m <= kSelectThreads / 4 ? 4 : 2;
     const int k = tid & (kSelectThreads / parts - 1), part = tid / (kSelectThreads / parts);
@@ -414,11 +420,14 @@ __global__ void __launch_bounds__(kSelectThreads, I == 16 && !LOOP ? 4 : 3) bloc
     int all;
     int32_t* to = o + base + block_scan(__popc(take), slots, phase, &all);
     base += all;
-    for (; take; take &= take - 1u) *to++ = j + __ffs((int)take) - 1;
+    for (; take; take &= take - 1u, ++to)
+      if (range_ok_count(to - o < count, &g_block_skips)) *to = j + __ffs((int)take) - 1;
   }
 }
 
 }  // namespace
+
+cudaError_t block_read_skips(uint32_t* count) { return read_and_clear(g_block_skips, count); }
 
 cudaError_t launch_block_scores(const void* q, const int32_t* positions, const void* k_bounds,
                                 int B, int Hq, int Hkv, int L, int block, float* scores,

@@ -415,6 +415,18 @@ int attn_read_prefill_skips(uint32_t* skips, cudaStream_t stream) {
   return n ? ATTN_ERR_DEVICE : ATTN_OK;
 }
 
+int attn_read_range_skips(uint32_t* skips, cudaStream_t stream) {
+  uint32_t n[3] = {0, 0, 0};
+  cudaError_t e = cudaStreamSynchronize(stream);
+  if (e == cudaSuccess) e = gqa::qk_norm_read_skips(&n[0]);
+  if (e == cudaSuccess) e = gqa::kv8_append_read_skips(&n[1]);
+  if (e == cudaSuccess) e = gqa::block_read_skips(&n[2]);
+  if (e != cudaSuccess) return cuda_status(e);
+  const uint32_t all = n[0] + n[1] + n[2];
+  if (skips) *skips = all;
+  return all ? ATTN_ERR_DEVICE : ATTN_OK;
+}
+
 int attn_debug_build(void) {
 #ifdef GQA_DEBUG
   return 1;

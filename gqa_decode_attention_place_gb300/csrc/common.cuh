@@ -175,6 +175,19 @@ __device__ __forceinline__ bool range_ok_count(bool ok, unsigned int* counter) {
   return false;
 }
 
+// Host: a device counter's value, which is cleared.
+template <typename T>
+cudaError_t read_and_clear(T& symbol, uint32_t* count) {
+  unsigned v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, symbol, sizeof(v));
+  if (e == cudaSuccess && v != 0) {
+    const unsigned zero = 0;
+    e = cudaMemcpyToSymbol(symbol, &zero, sizeof(zero));
+  }
+  *count = v;
+  return e;
+}
+
 // Launch `kernel` on `stream` with programmatic stream serialisation, so it
 // may begin while the previous kernel on the stream drains (the kernel calls
 // grid_dependency_wait() before touching anything that kernel wrote).

@@ -66,6 +66,10 @@ cudaError_t launch_block_scores(const void* q, const int32_t* positions, const v
 cudaError_t launch_block_select(const float* scores, const int32_t* positions, int B, int Hkv,
                                 int L, int block, int count, int first, int recent, int32_t* out,
                                 cudaStream_t stream);
+// Debug builds: accesses a range check skipped since the last call; 0 in others.
+cudaError_t qk_norm_read_skips(uint32_t* count);
+cudaError_t kv8_append_read_skips(uint32_t* count);
+cudaError_t block_read_skips(uint32_t* count);
 DecodeWorkspace kv8_workspace_layout(int B, int Hq, int Hkv);
 cudaError_t launch_kv8_decode(const void* q, const int32_t* positions, const void* k_cache,
                               const void* v_cache, const float* k_scale, const float* v_scale,

@@ -23,6 +23,7 @@ namespace gqa {
 namespace {
 
 constexpr int kD8 = 128;
+__device__ unsigned int g_append_skips;  // debug builds: accesses a range check skipped
 
 __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
   if (!rows_in_cache(pos, S - 1, L)) return;  // reported by the decode call
   const int j = pos / T + blockIdx.x;
   if (j > (pos + S - 1) / T) return;
+  if (!range_ok_count(j >= 0 && j < nb && b < B && h < Hkv, &g_append_skips)) return;
   const int tid = threadIdx.x, c = tid & 15, warp = tid >> 5, lane = tid & 31;
   const size_t seg = (size_t)b * Hkv + h;
   const int row0 = j * T;
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
     if (had && s > s_old[op]) {  // the block's scale grew: move the older rows
       const float ratio = s_old[op] * inv;
       for (int r = row0 + (tid >> 4); r < pos; r += 16) {
+        if (!range_ok_count(r >= 0 && r < L, &g_append_skips)) continue;
         uint2* at = reinterpret_cast<uint2*>(cache + (size_t)r * kD8 + c * 8);
         *at = rescale8(*at, ratio);
       }
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int t = t0 + i * 16;
-      if (t >= 0 && t < S) {
+      if (t >= 0 && t < S && range_ok_count(t + pos >= 0 && t + pos < L, &g_append_skips)) {
         *reinterpret_cast<uint2*>(cache + (size_t)(t + pos) * kD8 + c * 8) = encode8(x[op][i], inv);
       }
     }
@@ -225,6 +228,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv8_append_token_kernel(
   const int pos = positions[b];
   if (!rows_in_cache(pos, 0, L)) return;  // reported by the decode call
   const int j = pos >> lb, row0 = j << lb;
+  if (!range_ok_count(j >= 0 && j < nb && pos < L, &g_append_skips)) return;
   const bool had = row0 < pos;
   float* scale = (op ? v_scale : k_scale) + (size_t)seg * nb + j;
   const float s_old = had ? *scale : 0.f;
@@ -271,6 +275,8 @@ __global__ void __launch_bounds__(kTokenWarps * 32) kv8_append_token_kernel(
 }
 
 }  // namespace
+
+cudaError_t kv8_append_read_skips(uint32_t* count) { return read_and_clear(g_append_skips, count); }
 
 cudaError_t launch_kv8_append(const void* k_new, const void* v_new, long long k_stride,
                               long long v_stride, const int32_t* positions,

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
       auto look_up = [&](int i, int blk, int& row, float& ks, float& vs) {
         row = row_of(i, blk);
         ks = vs = 1.f;
-        if (row != kNoRow) {
+        if (row != kNoRow && range_ok((row >> p.lb) < p.nb, p.status)) {
           const size_t at = (size_t)seg * p.nb + (row >> p.lb);
           ks = p.k_scale[at];
           vs = p.v_scale[at];
@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
       Landing x;
       merge_warps8(merge_o, merge_ml, i, g, x.m, x.l, x.o);
       const int owner = i / cols;
+      if (!range_ok(owner < C && rank < C, p.status)) continue;
       Landing* to = cluster.map_shared_rank(land, owner) + rank * cols + (i - owner * cols);
       to->o = x.o;
       *reinterpret_cast<float2*>(&to->m) = make_float2(x.m, x.l);
@@ -293,9 +294,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
       o.z = fmaf(x.o.z, e, o.z);
       o.w = fmaf(x.o.w, e, o.w);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(p.out + out_at + (size_t)i * 4) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    store_column(p, out_at, i, o, l);
   }
   if (*abort_flag) {  // copies in flight land before the shared memory goes
     const uint64_t t_start = globaltimer_ns();

@@ -535,6 +535,8 @@ static_assert(sizeof(Last8) <= 16 * 4, "behind misc[32]");
 __device__ __forceinline__ void store_column(const Kv8Params& p, size_t out_at, int col,
                                              const float4& o, float ls) {
   const float inv = ls == 0.f ? 0.f : 1.f / ls;
+  if (!range_ok(col >= 0 && out_at + (size_t)col * 4 + 4 <= (size_t)p.B * p.Hq * kD, p.status))
+    return;
   *reinterpret_cast<uint2*>(p.out + out_at + (size_t)col * 4) =
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
 }
@@ -542,6 +544,9 @@ __device__ __forceinline__ void store_column(const Kv8Params& p, size_t out_at, 
 // and at most one later part.
 __device__ __forceinline__ int part_slot(const Part8& pt, int r) {
   return 2 * (pt.c0 + r) + (r == 0);
+}
+__device__ __forceinline__ bool slot_ok(const Kv8Params& p, int slot) {
+  return range_ok(slot >= 0 && slot < 2 * kKv8MaxGrid, p.status);
 }
 
 // A column's output from few parts, in CTA order (absent ones: kMInit, zeros).
@@ -580,7 +585,7 @@ __device__ __forceinline__ void merge_few(const Kv8Params& p, const Part8& pt, i
     for (int r = 0; r < kFewParts; ++r) {
       ml[r] = make_float2(kMInit, 0.f);
       x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < pt.n) {
+      if (r < pt.n && slot_ok(p, part_slot(pt, r))) {
         const size_t at = (size_t)part_slot(pt, r) * g;
         ml[r] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (at + h) * 2));
         x[r] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kD) + col);
@@ -596,7 +601,9 @@ __device__ __forceinline__ void merge_few(const Kv8Params& p, const Part8& pt, i
 // leave threads over (g < 8) the parts are dealt out among them as well.
 __device__ __forceinline__ void merge_many(const Kv8Params& p, const Part8& pt, float* buf,
                                            ConsumerSync& csync, int warp, int lane) {
-  const int g = p.g, tid = warp * 32 + lane, n = pt.n;
+  const int g = p.g, tid = warp * 32 + lane;
+  // (the slots rise with the part: the last one bounds them all, and `buf`)
+  const int n = slot_ok(p, pt.c0) && slot_ok(p, 2 * (pt.c0 + pt.n - 1) + 1) ? pt.n : 0;
   const int cols = g * (kD / 4);
   float* wt = buf;              // [n][g] maxima, then weights
   float* ls = buf + n * g;      // [n][g] sums; row 0 then holds the totals
@@ -664,6 +671,7 @@ __device__ __forceinline__ void merge_many(const Kv8Params& p, const Part8& pt, 
 // This CTA's part of a segment, column by column.
 __device__ __forceinline__ void store_part(const Kv8Params& p, int slot, int col, float M,
                                            float ls, const float4& o) {
+  if (!slot_ok(p, slot)) return;
   reinterpret_cast<float4*>(p.part_o + (size_t)slot * p.g * kD)[col] = o;
   if (col % (kD / 4) == 0)
     *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * p.g + col / (kD / 4)) * 2) =
@@ -828,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           misc[1] = have;  // (misc[2] may still be being read for the piece before)
         }
         msync(lane);
-        if (misc[1]) {
+        if (misc[1] && slot_ok(p, part_slot(pt, 1 - own))) {
           const size_t at = (size_t)part_slot(pt, 1 - own) * g;
           const float4* o = reinterpret_cast<const float4*>(p.part_o + at * kD);
 #pragma unroll 8
@@ -861,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mtid == 0) {
           const bool last = arrive_last(counter, pt.n);
           misc[2] = last;
-          if (last && pt.n > kFewParts)  // left to the consumers
+          if (last && pt.n > kFewParts && range_ok(misc[3] < 2, p.status))  // left to the consumers
             reinterpret_cast<Part8*>(misc + 24)[misc[3]++] = pt;
         }
         msync(lane);
@@ -975,7 +983,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         m.ks = m.vs = 1.f;
         m.flags = 0;
         if (m.on) {
-          if (!copies && m.row != kNoRow) {
+          if (!copies && m.row != kNoRow &&
+              range_ok((m.row >> p.lb) < p.nb && m.z < B * Hkv, p.status)) {
             const size_t at = (size_t)m.z * p.nb + (m.row >> p.lb);
             m.ks = p.k_scale[at];
             m.vs = p.v_scale[at];

@@ -25,6 +25,8 @@
 namespace gqa {
 namespace {
 
+__device__ unsigned int g_norm_skips;  // debug builds: accesses a range check skipped
+
 struct NormRopeParams {
   const uint16_t *q, *k, *v;
   long long q_stride, k_stride, v_stride;  // elements from token to token
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
           unpack8(*reinterpret_cast<const uint4*>(w + d0), wa);
           unpack8(*reinterpret_cast<const uint4*>(w + d0 + half), wb);
         }
-        if (p.cos && ok) {
+        if (p.cos && ok && range_ok_count(pos >= 0 && pos < p.L, &g_norm_skips)) {
           const size_t row = (size_t)pos * D + d0;
           load8f(p.cos + row, ca);
           load8f(p.cos + row + half, cb);
@@ -194,6 +196,10 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
       ua = make_uint4(oa[0], oa[1], oa[2], oa[3]);
       ub = make_uint4(ob[0], ob[1], ob[2], ob[3]);
     }
+    if (!range_ok_count(n >= 0 && n < p.N && h >= 0 && h < (is_q ? p.Hq : p.Hkv) &&
+                            (!ok || (pos >= 0 && pos < p.L)),
+                        &g_norm_skips))
+      continue;
     uint16_t* dst;
     if (is_q) {
       dst = p.q_out + ((size_t)n * p.Hq + h) * D;
@@ -210,6 +216,8 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
 }
 
 }  // namespace
+
+cudaError_t qk_norm_read_skips(uint32_t* count) { return read_and_clear(g_norm_skips, count); }
 
 cudaError_t launch_qk_norm_rope(const void* q, const void* k, const void* v, long long q_stride,
                                 long long k_stride, long long v_stride, const void* q_weight,

@@ -575,8 +575,10 @@ int attn_test_force_schedule(int cluster);
  * attn_debug_build -- 1 if this library was compiled with the device range
  * checks (-DGQA_DEBUG), else 0.  In such a build every decode kernel checks
  * the index-derived addresses named under ATTN_DEV_RANGE before it uses them,
- * and both prefill kernels check their bulk-copy tile coordinates and output
- * rows; a failed check skips the access and records it (no trap, no assert).
+ * both prefill kernels check their bulk-copy tile coordinates and output
+ * rows, and the calls without a workspace (norm with rotation, 8-bit append,
+ * block scores and selection) check the blocks, rows and list places that they
+ * write; a failed check skips the access and records it (no trap, no assert).
  * Release builds contain no checks.
  */
 int attn_debug_build(void);
@@ -589,6 +591,13 @@ int attn_debug_build(void);
  * builds.  `skips` may be NULL.
  */
 int attn_read_prefill_skips(uint32_t* skips, cudaStream_t stream);
+
+/*
+ * attn_read_range_skips -- the same count for attn_qk_norm_rope,
+ * attn_qk_norm_rope_append, attn_kv8_append, attn_block_scores and
+ * attn_block_select, which have no status word.
+ */
+int attn_read_range_skips(uint32_t* skips, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
