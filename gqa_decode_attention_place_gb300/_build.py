@@ -11,9 +11,9 @@ with ``-DGQA_DEBUG``: the kernels then check their index-derived addresses
 output rows) before each access and record a failed check instead of making
 it.  Setting ``GQA_ATTN_DEBUG=1`` makes the package load that library.
 
-``build_marshal()`` makes ``lib/_gqa_marshal.so`` from ``csrc/marshal.cpp`` with
-the host compiler against the installed PyTorch's headers: the Python
-binding's argument checks.
+``build_marshal()`` makes ``lib/_gqa_marshal.<versions>.so`` from
+``csrc/marshal.cpp`` with the host compiler against the installed PyTorch's
+headers: the Python binding's argument checks.
 """
 
 from __future__ import annotations
@@ -117,19 +117,28 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
 
 
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
-MARSHAL_PATH = os.path.join(LIBDIR, "_gqa_marshal.so")
+
+
+def marshal_path() -> str:
+    """The module's file.  It is compiled against PyTorch's C++ headers and Python's, so its name
+    holds their versions: another PyTorch or Python in the same tree makes its own."""
+    import torch
+    tag = (f"torch{torch.__version__}.{sysconfig.get_config_var('SOABI')}"
+           f".abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+    return os.path.join(LIBDIR, f"_gqa_marshal.{tag}.so")
 
 
 def build_marshal(force: bool = False) -> str:
     """Compile the binding's native argument checks; return the module's path."""
+    path = marshal_path()
     deps = (MARSHAL_SRC, os.path.abspath(__file__))
-    if not force and os.path.exists(MARSHAL_PATH) and \
-            all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL_PATH) for p in deps):
-        return MARSHAL_PATH
+    if not force and os.path.exists(path) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps):
+        return path
     import torch
     base = os.path.dirname(torch.__file__)
     os.makedirs(LIBDIR, exist_ok=True)
-    tmp = f"{MARSHAL_PATH}.{os.getpid()}.tmp"
+    tmp = f"{path}.{os.getpid()}.tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", os.path.join(base, "include"),
@@ -141,8 +150,8 @@ def build_marshal(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"{os.path.basename(MARSHAL_SRC)} failed to compile:\n"
                            f"{r.stdout}{r.stderr}")
-    os.replace(tmp, MARSHAL_PATH)
-    return MARSHAL_PATH
+    os.replace(tmp, path)
+    return path
 
 
 if __name__ == "__main__":
