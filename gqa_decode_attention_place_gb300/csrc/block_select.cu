@@ -1,8 +1,9 @@
 // block_select.cu -- which blocks of a cache a decode step attends.
 //
 // Scores.  Block j of a KV head has, per channel d, the largest and smallest
-// key value max_jd and min_jd, so no key of the block scores above
-// sum_d max(q_d max_jd, q_d min_jd) with query q.  Summed over the g query
+// key value max_jd and min_jd, so no key of the block, as it was appended,
+// scores above sum_d max(q_d max_jd, q_d min_jd) with query q (its code may, by
+// the code's rounding: the scores rank blocks).  Summed over the g query
 // heads of the KV head (q+ = max(q, 0), q- = min(q, 0)):
 //   s_j = sum_d (sum_h q+_hd) max_jd + (sum_h q-_hd) min_jd,
 // one vector of 256 against the block's 512 bytes of bounds.  Bound by

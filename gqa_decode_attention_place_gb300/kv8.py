@@ -185,8 +185,9 @@ def attn_decode_step_kv8(q, positions, k_cache, v_cache, k_scale, v_scale, block
 
 def attn_block_scores(q, positions, k_bounds, L: int, block: int, out=None,
                       stream=None) -> torch.Tensor:
-    """scores [B,Hkv,NB]: what the g query heads of a KV head can score in
-    each block at most, summed over the heads; -inf past the position's block.
+    """scores [B,Hkv,NB]: what the g query heads of a KV head can score at
+    most with each block's keys as they were appended (before their rounding to
+    8 bits), summed over the heads; -inf past the position's block.
     L is the cache's length, k_bounds [B,Hkv,NB,2,D]."""
     m = _native or _load()
     if out is None:

@@ -439,12 +439,16 @@ int attn_decode_step_kv8(const void* q, const int32_t* positions, const void* k_
                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
- * attn_block_scores -- an upper bound of what a query can score in each block,
- * summed over the g query heads of a KV head:
+ * attn_block_scores -- an upper bound of what a query can score with a block's
+ * keys as they were appended, summed over the g query heads of a KV head:
  *     scores[b,hk,j] = sum_h sum_d max(q[b,h,d] * max_jd, q[b,h,d] * min_jd)
  * over the heads h of KV head hk, from k_bounds; -inf for blocks past
  * positions[b] / block (and for all blocks of a position outside [0, L)).
  * Their bounds are not read.  fp32 sums.  (A bound for positive score scales.)
+ * The decode attends the keys' codes, which may lie beyond the bounds by their
+ * rounding, half an e4m3 step (up to 2^-4 of a value), so a code's score may
+ * exceed the block's by that much: the scores rank blocks, they do not prove
+ * that a block left out holds no larger score.
  *
  *   scores : [B, Hkv, NB] fp32.
  *   Sizes as attn_decode_step_kv8.  The bounds are taken as finite.
