@@ -6,7 +6,9 @@
 //   s_new = 2^e, e the least integer with max|x| <= 448 * 2^e  (block_scale)
 //   s     = max(s_old, s_new) if the block already held rows, else s_new
 //   old rows (if s > s_old): code <- e4m3(code * s_old / s)
-//   new rows:                code <- e4m3(x / s)
+//   new rows:                code <- e4m3(x / s)     (x * (1/s): exact, s = 2^e; a
+//                            block that came with another scale keeps that,
+//                            1/s then rounded to fp32)
 //   bounds: per channel, max and min of the new rows and, if the block
 //           already held rows, of what was there.
 //

@@ -393,7 +393,9 @@ int attn_qk_norm_rope_append(const void* q, const void* k_new, const void* v_new
  *             first row), else max(s_old, s_new)
  *     its earlier rows, if s > s_old: code <- e4m3(code * s_old / s)
  *     its new rows:                   code <- e4m3(x / s)
- * rounded to nearest even, beyond +-448 saturating, NaN kept.  Only codes of
+ * rounded to nearest even, beyond +-448 saturating, NaN kept.  x / s is
+ * x * (1 / s) in fp32: exact for the powers of two that the append writes; in a
+ * block that holds rows at another scale, 1 / s is rounded first.  Only codes of
  * rows up to the last new one are written.  The bounds of a block become those
  * of its new rows and, if it held rows before, what they were (NaN ignored;
  * -inf and +inf for a channel with nothing else).
