@@ -19,6 +19,8 @@
 // with loads into registers too few bytes were under way (8191 tokens of
 // 32 + 8 heads of 128: 35.4 us, 30.0 us this way; copying as many bytes takes
 // 26).
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -215,6 +217,21 @@ __global__ void __launch_bounds__(kNormWarps * 32) qk_norm_rope_kernel(const Nor
   }
 }
 
+// The current device's SMs, asked for once.
+cudaError_t sm_count(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+  if (e != cudaSuccess) return e;
+  *sms = known[dev].load(std::memory_order_relaxed);
+  if (*sms == 0) {
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) known[dev].store(*sms, std::memory_order_relaxed);
+  }
+  return e;
+}
+
 }  // namespace
 
 cudaError_t qk_norm_read_skips(uint32_t* count) { return read_and_clear(g_norm_skips, count); }
@@ -253,9 +270,13 @@ cudaError_t launch_qk_norm_rope(const void* q, const void* k, const void* v, lon
   const int rpw = 32 / lpr;
   const int all = (Hq + Hkv * (k_out ? 1 : 2) + rpw - 1) / rpw;  // steps of one warp for a token
   // Few tokens: a warp for every step, for latency.  Many: a warp keeps its
-  // token's rotation row over several steps, as long as the device stays full
-  // of warps.
-  const long long full = 152ll * 24;
+  // token's rotation row over several steps, as long as 24 warps are left for
+  // every SM.  (20 are resident at 96 registers.  Of 16, 20, 24, 28 and 32 none
+  // is best for every count: 32 + 8 heads of 128, 650 tokens 6.1 us with 20
+  // and 7.1 with 24, 1100 tokens 8.3 and 7.7, 1600 tokens 11.2 and 9.8.)
+  int sms = 0;
+  if (const cudaError_t e = sm_count(&sms)) return e;
+  const long long full = 24ll * sms;
   int steps = 1;
   while (steps < all && (long long)p.N * ((all + 2 * steps - 1) / (2 * steps)) >= full) steps *= 2;
   steps = min(steps, all);
