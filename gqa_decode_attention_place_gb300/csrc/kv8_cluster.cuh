@@ -11,7 +11,8 @@
 // one cluster barrier each rank merges its columns from its own memory, in
 // rank order, and writes them.  Against the split over a flat list this saves
 // the merge's three round trips through L2 and the scan: B=1, 8 KV heads,
-// 8001 rows, g=2: 10.5 -> 6.6 us.  (When it is taken: cluster_size8.)
+// 8001 rows, g=2: 10.5 -> 6.6 us (7.0 with probabilities in two parts).  (When
+// it is taken: cluster_size8.)
 #pragma once
 
 namespace gqa {

@@ -15,8 +15,8 @@
 // in one it would be zero below 2^-126, and weight lost with it.
 //
 // Bound by memory: a row costs 256 bytes for K and V, half of the bf16
-// cache's.  4.3 GB (B=256, g=8) take 591 to 603 us, 7.2 TB/s; 268 MB (B=32) 46 us at
-// g <= 8 and 54 at g = 16.  How:
+// cache's.  4.3 GB (B=256, g=8) take 599 to 608 us, 7.2 TB/s; 268 MB (B=32) 45 to
+// 47 us at g <= 8 and 54 at g = 16.  How:
 //  * 128-row tiles (32 KB for K and V) stream through a shared-memory ring by
 //    tiled TMA copies (128-byte swizzle: a row of codes is exactly one
 //    swizzle span) issued by one producer warp; another fetches each 16-row
@@ -32,7 +32,7 @@
 //    K's 16-byte pieces feed the A operand as they are, and V comes through
 //    transposing 8-bit matrix loads; no bank conflicts, no code moved between
 //    lanes.  The conversions are what the warps spend most of their issue
-//    slots on (96 of about 250 instructions a slice).
+//    slots on (96 of about 270 instructions a slice).
 //  * A flat list of all tiles is split evenly over the grid (one CTA per SM).
 //    At a segment's end the consumers leave their partials in shared memory
 //    and go on; two further warps merge them (512 x 8 segments of one tile:
@@ -1239,7 +1239,9 @@ cudaError_t device8(const Device8** out) {
 //              and 0.007 for each head and part of a segment's merge
 // The host knows the cache's length only: a position is taken to lie half-way
 // on average, and the longest of several, which a cluster waits for, at the
-// end; a list is taken as full.  (One segment of 131072 rows, g = 2: 37 us in a
+// end; a list is taken as full.  So a young sequence pays for a long cache: at
+// row 1000 of one stream (8 KV heads, g = 2) a step takes 4.4 us in caches up to
+// about 166000 rows and 9.8 us in longer ones.  (One segment of 131072 rows, g = 2: 37 us in a
 // cluster, 17 by the list; of 16384 rows: 8 and 12; 108 segments of up to 10
 // tiles: 10 and 17.)
 int cluster_size8(const Kv8Params& p, const Device8& d) {
