@@ -223,7 +223,7 @@ def prepare(case, seed):
         s["k_pages"], s["v_pages"] = _pools(len(refs), c, g)
         s["taken"] = torch.empty(B, dtype=torch.int32, device="cuda")
         per = -(-(c["S"] - 1) // page) + 1
-        s["workspace"] = torch.zeros(8192 + 16 * B + 4 * B * per, dtype=torch.uint8,
+        s["workspace"] = torch.zeros(8192 + 24 * B + 8 * B * per, dtype=torch.uint8,
                                      device="cuda")
         return s
     S, Hkv, D = c["S"], c["Hkv"], c["D"]
