@@ -34,6 +34,9 @@ __all__ = [
     "kv8_workspace", "attn_decode_step_kv8", "attn_block_scores", "attn_block_select",
     "attn_decode_step_kv8_blocks", "attn_decode_step_kv8_sparse",
     "attn_kv8_sparse_workspace_size", "kv8_sparse_workspace",
+    "attn_paged_append", "attn_decode_step_paged", "attn_paged_workspace_size", "paged_workspace",
+    "attn_pages_reserve", "attn_pages_fork", "attn_pages_compact", "attn_pages_workspace_size",
+    "pages_workspace",
 ]
 
 ATTN_OK = 0
@@ -41,6 +44,8 @@ ATTN_DEV_BAD_POSITION = 0x1
 ATTN_DEV_TIMEOUT = 0x2
 ATTN_DEV_RANGE = 0x4
 ATTN_DEV_BAD_BLOCK = 0x8
+ATTN_DEV_BAD_PAGE = 0x10
+ATTN_DEV_BAD_PARENT = 0x20
 
 _LIB: Optional[ctypes.CDLL] = None
 # Range-checked builds only: every workspace handed out by decode_workspace()
@@ -151,6 +156,24 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.attn_block_scores.restype = i32
     lib.attn_block_select.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]
     lib.attn_block_select.restype = i32
+    lib.attn_paged_append.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp, i64, i64, i64, i32,
+                                      i32, i32, i32, i32, i32, i32, vp]
+    lib.attn_paged_append.restype = i32
+    lib.attn_paged_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.attn_paged_workspace_size.restype = sz
+    lib.attn_decode_step_paged.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32,
+                                           i32, i32, i32, i32, i32, f32, vp, vp, sz, vp]
+    lib.attn_decode_step_paged.restype = i32
+    lib.attn_pages_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.attn_pages_workspace_size.restype = sz
+    lib.attn_pages_reserve.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, i32,
+                                       i32, i32, i32, vp, vp, sz, vp]
+    lib.attn_pages_reserve.restype = i32
+    lib.attn_pages_fork.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, sz, vp]
+    lib.attn_pages_fork.restype = i32
+    lib.attn_pages_compact.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, i32, i32, i32,
+                                       vp, vp, sz, vp]
+    lib.attn_pages_compact.restype = i32
     _LIB = lib
     return lib
 
@@ -508,7 +531,8 @@ def attn_read_prefill_skips(stream=None) -> int:
 
 def attn_read_range_skips(stream=None) -> int:
     """The same count for the calls without a workspace: the norm with
-    rotation, the 8-bit append, the block scores and the selection."""
+    rotation, the 8-bit and the paged append, the block scores and the
+    selection."""
     n = ctypes.c_uint32(0)
     code = load_library().attn_read_range_skips(ctypes.byref(n), _stream(stream))
     if code not in (0, 5):
@@ -533,3 +557,7 @@ from .kv8 import (  # noqa: E402
     attn_decode_step_kv8_sparse, attn_kv8_append, attn_kv8_sparse_workspace_size,
     attn_kv8_workspace_size, attn_qk_norm_rope, attn_qk_norm_rope_append, kv8_sparse_workspace,
     kv8_workspace)
+from .paged import (  # noqa: E402
+    attn_decode_step_paged, attn_paged_append, attn_paged_workspace_size, attn_pages_compact,
+    attn_pages_fork, attn_pages_reserve, attn_pages_workspace_size, pages_workspace,
+    paged_workspace)

@@ -5,6 +5,7 @@
 #include "gqa_attn.h"
 #include "decode_params.h"
 #include "internal.h"
+#include "paged.h"
 
 namespace gqa {
 bool decode_supported(int B, int Hq, int Hkv, int L, int D);
@@ -385,6 +386,169 @@ int attn_decode_step_kv8_sparse(const void* q, const int32_t* positions, const v
   return st;
 }
 
+namespace {
+
+// A pool of pages, its sizes and strides.
+int paged_pool(const void* k, const void* v, int64_t page_stride, int64_t head_stride,
+               int64_t row_stride, int Hkv, int D, int P, int page, int M, gqa::PagedPool* pool) {
+  if (!k || !v || !aligned16(k) || !aligned16(v) || Hkv <= 0 || D <= 0 || P <= 0 || page <= 0 ||
+      M < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if ((page != 16 && page != 32 && page != 64 && page != 128) || (D != 64 && D != 128) ||
+      Hkv > 1024 || P > (1 << 26) || (int64_t)M * page > (1 << 30))
+    return ATTN_ERR_UNSUPPORTED;
+  // a stride that nothing steps by is any valid one
+  if (Hkv == 1) head_stride = row_stride;
+  if (P == 1) page_stride = row_stride;
+  struct {
+    int64_t stride, size;
+  } dims[3] = {{row_stride, page}, {head_stride, Hkv}, {page_stride, P}};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (dims[j].stride > dims[j + 1].stride) {
+        const auto x = dims[j];
+        dims[j] = dims[j + 1];
+        dims[j + 1] = x;
+      }
+  int64_t reach = D;  // elements that the dims so far cover
+  for (const auto& d : dims) {
+    if (d.stride < D || d.stride % 8 || d.stride >= (1ll << 38)) return ATTN_ERR_INVALID_ARG;
+    if (d.size > 1) {
+      if (d.stride < reach) return ATTN_ERR_INVALID_ARG;  // rows would overlap
+      reach += (d.size - 1) * d.stride;
+    }
+  }
+  *pool = gqa::PagedPool{static_cast<uint8_t*>(const_cast<void*>(k)),
+                         static_cast<uint8_t*>(const_cast<void*>(v)),
+                         page_stride, head_stride, row_stride, P, Hkv, page, D};
+  return ATTN_OK;
+}
+bool pages_sizes(int B, int S, int page) {
+  return B > 0 && B <= 65536 && S > 0 && page > 0 &&
+         (int64_t)B * ((S - 1 + (int64_t)page - 1) / page + 1) <= (1 << 28);
+}
+
+}  // namespace
+
+int attn_paged_append(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                      const int32_t* positions, const int32_t* lengths,
+                      const int32_t* page_table, void* k_pages, void* v_pages,
+                      int64_t page_stride, int64_t head_stride, int64_t row_stride, int B, int S,
+                      int Hkv, int D, int P, int page, int M, cudaStream_t stream) {
+  gqa::PagedPool pool;
+  if (B <= 0 || S < 0 || M <= 0 || !positions || !page_table || !aligned4(positions) ||
+      !aligned4(lengths) || !aligned4(page_table))
+    return ATTN_ERR_INVALID_ARG;
+  if (const int st = paged_pool(k_pages, v_pages, page_stride, head_stride, row_stride, Hkv, D, P,
+                                page, M, &pool))
+    return st;
+  if (S == 0) return ATTN_OK;
+  if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) ||
+      k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D || k_stride % 8 || v_stride % 8)
+    return ATTN_ERR_INVALID_ARG;
+  return cuda_status(gqa::launch_paged_append(k_new, v_new, k_stride, v_stride, positions, lengths,
+                                              page_table, pool, B, S, M, stream));
+}
+
+namespace {
+int paged_decode_sizes(int B, int S, int Hq, int Hkv, int D) {
+  if (B <= 0 || S <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || Hkv > 1024 || B > gqa::kPagedMaxB ||
+      (int64_t)S * (Hq / Hkv) > gqa::kPagedMaxRows || (int64_t)B * Hkv >= (1ll << 31) / 16)
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+}  // namespace
+
+size_t attn_paged_workspace_size(int B, int S, int Hq, int Hkv, int D) {
+  if (paged_decode_sizes(B, S, Hq, Hkv, D) != ATTN_OK) return 0;
+  return gqa::paged_workspace_layout(B, S, Hq, Hkv, D).total;
+}
+
+int attn_decode_step_paged(const void* q, const int32_t* positions, const int32_t* lengths,
+                           const int32_t* page_table, const void* k_pages, const void* v_pages,
+                           int64_t page_stride, int64_t head_stride, int64_t row_stride, int B,
+                           int S, int Hq, int Hkv, int D, int P, int page, int M, float scale,
+                           void* out, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream) {
+  gqa::PagedPool pool;
+  if (!q || !positions || !page_table || !out || M <= 0 || !aligned16(q) || !aligned16(out) ||
+      !aligned4(positions) || !aligned4(lengths) || !aligned4(page_table))
+    return ATTN_ERR_INVALID_ARG;
+  if (const int st = paged_decode_sizes(B, S, Hq, Hkv, D)) return st;
+  if (const int st = paged_pool(k_pages, v_pages, page_stride, head_stride, row_stride, Hkv, D, P,
+                                page, M, &pool))
+    return st;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < gqa::paged_workspace_layout(B, S, Hq, Hkv, D).total)
+    return ATTN_ERR_WORKSPACE;
+  return cuda_status(gqa::launch_paged_decode(q, positions, lengths, page_table, pool, B, S, Hq, M,
+                                              scale, out, workspace, stream));
+}
+
+size_t attn_pages_workspace_size(int B, int S, int P, int page) {
+  if (!pages_sizes(B, S, page) || P <= 0 || P > (1 << 26) ||
+      (page != 16 && page != 32 && page != 64 && page != 128))
+    return 0;
+  const size_t a = gqa::pages_reserve_layout(B, S, page).total;
+  const size_t b = gqa::pages_compact_layout(P).total;
+  return a > b ? a : b;
+}
+
+int attn_pages_reserve(int32_t* page_table, int32_t* page_refs, const int32_t* positions,
+                       const int32_t* lengths, void* k_pages, void* v_pages, int64_t page_stride,
+                       int64_t head_stride, int64_t row_stride, int B, int S, int Hkv, int D,
+                       int P, int page, int M, int32_t* taken, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream) {
+  gqa::PagedPool pool;
+  if (!page_table || !page_refs || !positions || !taken || B <= 0 || S <= 0 || M <= 0 ||
+      !aligned4(page_table) || !aligned4(page_refs) || !aligned4(positions) ||
+      !aligned4(lengths) || !aligned4(taken))
+    return ATTN_ERR_INVALID_ARG;
+  if (const int st = paged_pool(k_pages, v_pages, page_stride, head_stride, row_stride, Hkv, D, P,
+                                page, M, &pool))
+    return st;
+  if (!pages_sizes(B, S, page)) return ATTN_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < gqa::pages_reserve_layout(B, S, page).total)
+    return ATTN_ERR_WORKSPACE;
+  return cuda_status(gqa::launch_pages_reserve(page_table, page_refs, positions, lengths, pool, B,
+                                               S, M, taken, workspace, stream));
+}
+
+int attn_pages_fork(int32_t* page_table, int32_t* page_refs, const int32_t* parents,
+                    const int32_t* lengths, int B, int M, int P, int page, void* workspace,
+                    size_t workspace_bytes, cudaStream_t stream) {
+  if (!page_table || !page_refs || B <= 0 || M <= 0 || P <= 0 || page <= 0 ||
+      !aligned4(page_table) || !aligned4(page_refs) || !aligned4(parents) || !aligned4(lengths))
+    return ATTN_ERR_INVALID_ARG;
+  if ((page != 16 && page != 32 && page != 64 && page != 128) || P > (1 << 26) ||
+      (int64_t)M * page > (1 << 30) || B > (parents ? gqa::kPagedMaxB : 65536))
+    return ATTN_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < 256) return ATTN_ERR_WORKSPACE;
+  return cuda_status(gqa::launch_pages_fork(page_table, page_refs, parents, lengths, B, M, P, page,
+                                            workspace, stream));
+}
+
+int attn_pages_compact(int32_t* page_table, int32_t* page_refs, void* k_pages, void* v_pages,
+                       int64_t page_stride, int64_t head_stride, int64_t row_stride, int B,
+                       int M, int Hkv, int D, int P, int page, int32_t* page_map, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream) {
+  gqa::PagedPool pool;
+  if (!page_refs || !page_map || B < 0 || M < 0 || ((int64_t)B * M > 0 && !page_table) ||
+      !aligned4(page_table) || !aligned4(page_refs) || !aligned4(page_map))
+    return ATTN_ERR_INVALID_ARG;
+  if (const int st = paged_pool(k_pages, v_pages, page_stride, head_stride, row_stride, Hkv, D, P,
+                                page, M, &pool))
+    return st;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < gqa::pages_compact_layout(P).total)
+    return ATTN_ERR_WORKSPACE;
+  return cuda_status(gqa::launch_pages_compact(page_table, page_refs, pool, B, M, page_map,
+                                               workspace, stream));
+}
+
 int attn_prefill_causal(const void* q, const void* k, const void* v, int S, int start_pos,
                         int Hq, int Hkv, int d, float scale, void* out, cudaStream_t stream) {
   if (S < 0 || start_pos < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0)
@@ -416,13 +580,14 @@ int attn_read_prefill_skips(uint32_t* skips, cudaStream_t stream) {
 }
 
 int attn_read_range_skips(uint32_t* skips, cudaStream_t stream) {
-  uint32_t n[3] = {0, 0, 0};
+  uint32_t n[4] = {0, 0, 0, 0};
   cudaError_t e = cudaStreamSynchronize(stream);
   if (e == cudaSuccess) e = gqa::qk_norm_read_skips(&n[0]);
   if (e == cudaSuccess) e = gqa::kv8_append_read_skips(&n[1]);
   if (e == cudaSuccess) e = gqa::block_read_skips(&n[2]);
+  if (e == cudaSuccess) e = gqa::paged_append_read_skips(&n[3]);
   if (e != cudaSuccess) return cuda_status(e);
-  const uint32_t all = n[0] + n[1] + n[2];
+  const uint32_t all = n[0] + n[1] + n[2] + n[3];
   if (skips) *skips = all;
   return all ? ATTN_ERR_DEVICE : ATTN_OK;
 }

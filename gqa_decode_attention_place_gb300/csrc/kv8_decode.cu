@@ -50,6 +50,7 @@
 #include "fp8.cuh"
 #include "internal.h"
 #include "decode_params.h"
+#include "flat_list.cuh"
 #include "tcgen05.cuh"
 #include "warp_ops.cuh"
 
@@ -172,113 +173,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// A tile's place in the flat (sequence, KV head, tile) order.  The order is
-// counted in units: a segment of nt tiles takes nt + E, its tiles and E for
-// what its end costs, so that an even split of the units is an even split of
-// the work however short the segments are (64 ragged segments of up to 64
-// tiles a head, g = 16: 150 -> 112 us when it came in).
+// What a segment's end costs, in tiles' time (flat_list.cuh).
 template <int NT> constexpr int kEndUnits = NT == 1 ? 1 : 3;
-struct Walk8 {
-  long long u, end;  // the unit at hand; the end of the part of the range it lies in
-  int b, kvh, k, nt, pos;
-};
-// A CTA's range of units [t0, t1).  If its last segment begins inside it and
-// goes on past t1, that part [tA, t1) is done first, then the rest; the CTA
-// that has the segment's next part starts with it too.  So a split segment's
-// parts are all done early, and their merge goes on behind the tiles that
-// follow.  (tA = t1: nothing goes first.)
-struct Range8 {
-  long long t0, tA, t1;
-};
-// To the first tile of the next segment (b = B past the last).
-template <int E>
-__device__ __forceinline__ void walk8_segment(Walk8& w, const int* prefix, const int* spos,
-                                              int B, int Hkv) {
-  w.u += w.nt - w.k + E;
-  w.k = 0;
-  if (++w.kvh < Hkv) return;
-  w.kvh = 0;
-  do { ++w.b; } while (w.b < B && prefix[w.b + 1] == prefix[w.b]);
-  if (w.b < B) {
-    w.nt = prefix[w.b + 1] - prefix[w.b] - E;
-    w.pos = spos[w.b];
-  }
-}
-// The first tile at or after unit u.
-template <int E>
-__device__ __forceinline__ void walk8_init(Walk8& w, long long u, const int* prefix,
-                                           const int* spos, int B, int Hkv) {
-  int lo = 0, hi = B - 1;  // largest b with Hkv*prefix[b] <= u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((long long)Hkv * prefix[mid] <= u) lo = mid; else hi = mid - 1;
-  }
-  const int n = prefix[lo + 1] - prefix[lo];
-  const uint32_t off = (uint32_t)(u - (long long)Hkv * prefix[lo]);
-  w.u = u;
-  w.b = lo;
-  w.nt = n - E;
-  w.kvh = (int)(off / (uint32_t)n);
-  w.k = (int)(off % (uint32_t)n);
-  w.pos = spos[lo];
-  if (w.k >= w.nt) walk8_segment<E>(w, prefix, spos, B, Hkv);
-}
-// CTA c's range.  An even share, but a boundary inside a segment of at most
-// kShortTiles tiles moves to that segment's nearer end: such a segment is not
-// worth a merge through L2 (340 of one or two tiles: 18.4 -> 11.8 us).  (A
-// longer segment's parts stay where the even shares put them: cta_of.)
-constexpr int kShortTiles = 4;
-template <int E>
-__device__ __forceinline__ long long boundary8(long long u, long long T, const int* prefix, int B,
-                                               int Hkv, long long& f0, int& n) {
-  f0 = u;
-  n = 0;
-  if (u >= T) return T;
-  int lo = 0, hi = B - 1;  // largest b with Hkv*prefix[b] <= u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((long long)Hkv * prefix[mid] <= u) lo = mid; else hi = mid - 1;
-  }
-  n = prefix[lo + 1] - prefix[lo];
-  const int k = (int)((uint32_t)(u - (long long)Hkv * prefix[lo]) % (uint32_t)n);
-  f0 = u - k;  // the segment's first unit; its tiles are f0 .. f0+n-E-1
-  if (k > 0 && n - E <= kShortTiles) return 2 * k < n ? f0 : f0 + n;
-  return u;
-}
-template <int E>
-__device__ __forceinline__ void range8_init(Range8& r, long long T, int c, int G,
-                                            const int* prefix, int B, int Hkv) {
-  long long f0;
-  int n;
-  r.t0 = boundary8<E>(T * c / G, T, prefix, B, Hkv, f0, n);
-  r.t1 = boundary8<E>(T * (c + 1) / G, T, prefix, B, Hkv, f0, n);
-  // tiles of the segment both before t1 (from f0 on) and behind it; before f0,
-  // the units up to t0 + E may end another segment and hold no tile
-  r.tA = f0 < r.t1 && r.t1 < f0 + n - E && f0 > r.t0 + E ? f0 : r.t1;
-}
-// The range's first tile in this order.
-template <int E>
-__device__ __forceinline__ void walk8_start(Walk8& w, const Range8& r, const int* prefix,
-                                            const int* spos, int B, int Hkv) {
-  walk8_init<E>(w, r.tA < r.t1 ? r.tA : r.t0, prefix, spos, B, Hkv);
-  w.end = r.t1;
-}
-// Past the end of the part that went first: to the rest of the range.
-template <int E>
-__device__ __forceinline__ void walk8_turn(Walk8& w, const Range8& r, const int* prefix,
-                                           const int* spos, int B, int Hkv) {
-  if (w.u >= w.end && w.end == r.t1 && r.tA < r.t1) {
-    walk8_init<E>(w, r.t0, prefix, spos, B, Hkv);
-    w.end = r.tA;
-  }
-}
-template <int E>
-__device__ __forceinline__ void walk8_next(Walk8& w, const Range8& r, const int* prefix,
-                                           const int* spos, int B, int Hkv) {
-  ++w.u;
-  if (++w.k == w.nt) walk8_segment<E>(w, prefix, spos, B, Hkv);
-  walk8_turn<E>(w, r, prefix, spos, B, Hkv);
-}
 
 // 16 rows x 16 codes of two 16-code columns, transposed (lane l gives the
 // address of row l % 16 of column block l / 16): r[2j] holds, for code c of
@@ -786,11 +682,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (T <= (long long)(kWholeTiles + E) * nseg) gw = min(gw, nseg);
   const int G = (int)gw;
   if ((int)blockIdx.x >= G) return;
-  Range8 rg;
-  range8_init<E>(rg, T, blockIdx.x, G, prefix, B, Hkv);
+  FlatRange rg;
+  flat_range<E>(rg, T, blockIdx.x, G, prefix, B, Hkv);
   if (rg.t0 >= rg.t1) return;
-  Walk8 w;
-  walk8_start<E>(w, rg, prefix, spos, B, Hkv);
+  FlatWalk w;
+  flat_start<E>(w, rg, prefix, spos, B, Hkv);
   if (w.u >= w.end) return;  // end units alone
 
   if (warp >= kWarps + 2) {
@@ -816,9 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (len < w.nt - w.k) {  // the part of the range ends inside the segment
         w.u = w.end;
       } else {
-        walk8_segment<E>(w, prefix, spos, B, Hkv);
+        flat_segment<E>(w, prefix, spos, B, Hkv);
       }
-      walk8_turn<E>(w, rg, prefix, spos, B, Hkv);
+      flat_turn<E>(w, rg, prefix, spos, B, Hkv);
       if (w.u >= w.end) {  // the last piece
         const int own = (int)blockIdx.x - pt.c0;
         if (mtid == 0) {
@@ -892,11 +788,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int entry = (slice * 16) >> p.lb;            // of this slice, within a tile
     const int per_tile = kTile >> p.lb;
     // the block a listed tile's slice lies in (-1: none)
-    auto fetch = [&](const Walk8& w) -> int {
+    auto fetch = [&](const FlatWalk& w) -> int {
       const int e = w.k * per_tile + entry;
       return e < p.count ? p.index[(size_t)(w.b * Hkv + w.kvh) * p.count + e] : -1;
     };
-    auto row_of = [&](const Walk8& w, int blk) -> int {
+    auto row_of = [&](const FlatWalk& w, int blk) -> int {
       int row;
       if (LIST) {
         if (blk < -1 || blk >= p.nb) {
@@ -909,13 +805,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return row <= w.pos ? row : kNoRow;
     };
-    auto step = [&](Walk8& w, int n) {  // n tiles on, as far as the range goes
+    auto step = [&](FlatWalk& w, int n) {  // n tiles on, as far as the range goes
       if (w.k + n < w.nt && w.u + n < w.end) {
         w.k += n;
         w.u += n;
         return;
       }
-      for (int k = 0; k < n && w.u < w.end; ++k) walk8_next<E>(w, rg, prefix, spos, B, Hkv);
+      for (int k = 0; k < n && w.u < w.end; ++k) flat_next<E>(w, rg, prefix, spos, B, Hkv);
     };
     int s = 0;          // the ring's stage and pass of the tile at hand
     uint32_t pass = 0;
@@ -946,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   p.q + ((size_t)b * p.Hq + (size_t)kvh * g) * kD, q_bytes, full);
     };
     if (copies && !LIST) {
-      for (; w.u < w.end; walk8_next<E>(w, rg, prefix, spos, B, Hkv)) {
+      for (; w.u < w.end; flat_next<E>(w, rg, prefix, spos, B, Hkv)) {
         if (!wait_empty()) break;
         const int z = w.b * Hkv + w.kvh, row = w.k * kTile;
         // failure-path tests only: a tile never issued
@@ -964,8 +860,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       long long last_end = w.end;  // of the part of the range done last
       if (rg.tA < rg.t1) {
-        Walk8 rest;
-        walk8_init<E>(rest, rg.t0, prefix, spos, B, Hkv);
+        FlatWalk rest;
+        flat_init<E>(rest, rg.t0, prefix, spos, B, Hkv);
         if (rest.u < rg.tA) last_end = rg.tA;
       }
       // What a lane knows of its tile, and of the next batch's.

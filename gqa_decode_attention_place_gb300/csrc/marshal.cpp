@@ -1,5 +1,5 @@
 // marshal.cpp -- argument checks of the Python binding for the query/key norm,
-// the 8-bit cache and the block-sparse decode, natively: a call checks every
+// the 8-bit cache, the block-sparse decode and the paged cache, natively: a call checks every
 // tensor (type, device, dtype, shape, density) and hands pointers and sizes to
 // the C entry point whose address it is given, on the tensors' own device.
 // (With the checks in Python a call took 10 to 20 us of the host's time, with
@@ -398,14 +398,173 @@ PyObject* block_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A pool: k_pages and v_pages [P, Hkv, page, D] with the same strides, D dense.
+struct Pool {
+  int64_t P, Hkv, page, D, page_stride, head_stride, row_stride;
+  void *k, *v;
+  Pool(const Call& c, PyObject* ko, PyObject* vo) {
+    const at::Tensor& t = lead(ko, "k_pages", kBF16, 4);
+    const at::Tensor& u = lead(vo, "v_pages", kBF16, 4);
+    P = t.size(0);
+    Hkv = t.size(1);
+    page = t.size(2);
+    D = t.size(3);
+    c.placed(t, "k_pages", t.sizes());
+    c.placed(u, "v_pages", t.sizes());
+    const auto st = t.strides(), su = u.strides();
+    bool ok = D <= 1 || (st[3] == 1 && su[3] == 1);
+    for (int i = 0; i < 3; ++i) ok = ok && (t.size(i) <= 1 || st[i] == su[i]);
+    if (!ok)
+      fail(PyExc_ValueError, std::string(c.where) +
+                                 ": the rows of k_pages and v_pages must be dense and their "
+                                 "strides alike, got " + text(st) + " and " + text(su));
+    page_stride = P > 1 ? st[0] : Hkv * page * D;
+    head_stride = Hkv > 1 ? st[1] : page * D;
+    row_stride = page > 1 ? st[2] : D;
+    k = t.data_ptr();
+    v = u.data_ptr();
+  }
+};
+
+// fn, stream, k_new, v_new, positions, lengths, page_table, k_pages, v_pages
+PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> int {
+    const at::Tensor& k = lead(a[2], "k_new", kBF16, 3, 4);
+    const Call c{"attn_paged_append", k.device()};
+    const Pool pool(c, a[7], a[8]);
+    const int64_t B = k.size(0), S = k.dim() == 4 ? k.size(1) : 1;
+    const int64_t M = lead(a[6], "page_table", kI32, 2).size(1);
+    const int64_t four[4] = {B, S, pool.Hkv, pool.D}, three[3] = {B, pool.Hkv, pool.D};
+    const at::IntArrayRef rows =
+        k.dim() == 4 ? at::IntArrayRef(four, 4) : at::IntArrayRef(three, 3);
+    auto fn = reinterpret_cast<int (*)(const void*, const void*, int64_t, int64_t, const void*,
+                                       const void*, const void*, void*, void*, int64_t, int64_t,
+                                       int64_t, int, int, int, int, int, int, int, void*)>(
+        handle(a[0]));
+    int64_t kst, vst;
+    void* kn = c.rows(a[2], "k_new", rows, &kst);
+    void* vn = c.rows(a[3], "v_new", rows, &vst);
+    void* pos = c.dense(a[4], "positions", kI32, {B});
+    void* len = c.optional(a[5], "lengths", kI32, {B});
+    void* table = c.dense(a[6], "page_table", kI32, {B, M});
+    void* stream = handle(a[1]);
+    return call(c.device, fn, kn, vn, kst, vst, pos, len, table, pool.k, pool.v, pool.page_stride,
+                pool.head_stride, pool.row_stride, narrow(B), narrow(S), narrow(pool.Hkv),
+                narrow(pool.D), narrow(pool.P), narrow(pool.page), narrow(M), stream);
+  });
+}
+
+// fn, stream, q, positions, lengths, page_table, k_pages, v_pages, scale, out, workspace
+PyObject* decode_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> int {
+    const at::Tensor& q = lead(a[2], "q", kBF16, 3, 4);
+    const Call c{"attn_decode_step_paged", q.device()};
+    const Pool pool(c, a[6], a[7]);
+    const int dims = (int)q.dim();
+    const int64_t B = q.size(0), S = dims == 4 ? q.size(1) : 1, Hq = q.size(dims - 2);
+    const int64_t M = lead(a[5], "page_table", kI32, 2).size(1);
+    const int64_t four[4] = {B, S, Hq, pool.D}, three[3] = {B, Hq, pool.D};
+    const at::IntArrayRef rows = dims == 4 ? at::IntArrayRef(four, 4) : at::IntArrayRef(three, 3);
+    auto fn = reinterpret_cast<int (*)(const void*, const void*, const void*, const void*,
+                                       const void*, const void*, int64_t, int64_t, int64_t, int,
+                                       int, int, int, int, int, int, int, float, void*, void*,
+                                       size_t, void*)>(handle(a[0]));
+    void* qp = c.dense(a[2], "q", kBF16, rows);
+    void* pos = c.dense(a[3], "positions", kI32, {B});
+    void* len = c.optional(a[4], "lengths", kI32, {B});
+    void* table = c.dense(a[5], "page_table", kI32, {B, M});
+    void* out = c.dense(a[9], "out", kBF16, rows);
+    size_t ws_bytes;
+    void* ws = c.workspace(a[10], &ws_bytes);
+    const float scale = real(a[8]);
+    void* stream = handle(a[1]);
+    return call(c.device, fn, qp, pos, len, table, pool.k, pool.v, pool.page_stride,
+                pool.head_stride, pool.row_stride, narrow(B), narrow(S), narrow(Hq),
+                narrow(pool.Hkv), narrow(pool.D), narrow(pool.P), narrow(pool.page), narrow(M),
+                scale, out, ws, ws_bytes, stream);
+  });
+}
+
+// fn, stream, page_table, page_refs, positions, lengths, k_pages, v_pages, tokens, taken, workspace
+PyObject* pages_reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> int {
+    const at::Tensor& t = lead(a[2], "page_table", kI32, 2);
+    const Call c{"attn_pages_reserve", t.device()};
+    const Pool pool(c, a[6], a[7]);
+    const int64_t B = t.size(0), M = t.size(1), S = whole(a[8]);
+    auto fn = reinterpret_cast<int (*)(void*, void*, const void*, const void*, void*, void*,
+                                       int64_t, int64_t, int64_t, int, int, int, int, int, int,
+                                       int, void*, void*, size_t, void*)>(handle(a[0]));
+    void* table = c.dense(a[2], "page_table", kI32, {B, M});
+    void* refs = c.dense(a[3], "page_refs", kI32, {pool.P});
+    void* pos = c.dense(a[4], "positions", kI32, {B});
+    void* len = c.optional(a[5], "lengths", kI32, {B});
+    void* taken = c.dense(a[9], "taken", kI32, {B});
+    size_t ws_bytes;
+    void* ws = c.workspace(a[10], &ws_bytes);
+    void* stream = handle(a[1]);
+    return call(c.device, fn, table, refs, pos, len, pool.k, pool.v, pool.page_stride,
+                pool.head_stride, pool.row_stride, narrow(B), (int)S, narrow(pool.Hkv),
+                narrow(pool.D), narrow(pool.P), narrow(pool.page), narrow(M), taken, ws, ws_bytes,
+                stream);
+  });
+}
+
+// fn, stream, page_table, page_refs, page, parents, lengths, workspace
+PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> int {
+    const at::Tensor& t = lead(a[2], "page_table", kI32, 2);
+    const Call c{"attn_pages_fork", t.device()};
+    const int64_t B = t.size(0), M = t.size(1);
+    const int64_t P = lead(a[3], "page_refs", kI32, 1).size(0);
+    auto fn = reinterpret_cast<int (*)(void*, void*, const void*, const void*, int, int, int, int,
+                                       void*, size_t, void*)>(handle(a[0]));
+    void* table = c.dense(a[2], "page_table", kI32, {B, M});
+    void* refs = c.dense(a[3], "page_refs", kI32, {P});
+    const int page = (int)whole(a[4]);
+    void* parents = c.optional(a[5], "parents", kI32, {B});
+    void* len = c.optional(a[6], "lengths", kI32, {B});
+    size_t ws_bytes;
+    void* ws = c.workspace(a[7], &ws_bytes);
+    void* stream = handle(a[1]);
+    return call(c.device, fn, table, refs, parents, len, narrow(B), narrow(M), narrow(P), page, ws,
+                ws_bytes, stream);
+  });
+}
+
+// fn, stream, page_table, page_refs, k_pages, v_pages, page_map, workspace
+PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> int {
+    const at::Tensor& t = lead(a[2], "page_table", kI32, 2);
+    const Call c{"attn_pages_compact", t.device()};
+    const Pool pool(c, a[4], a[5]);
+    const int64_t B = t.size(0), M = t.size(1);
+    auto fn = reinterpret_cast<int (*)(void*, void*, void*, void*, int64_t, int64_t, int64_t, int,
+                                       int, int, int, int, int, void*, void*, size_t, void*)>(
+        handle(a[0]));
+    void* table = c.dense(a[2], "page_table", kI32, {B, M});
+    void* refs = c.dense(a[3], "page_refs", kI32, {pool.P});
+    void* map = c.dense(a[6], "page_map", kI32, {pool.P});
+    size_t ws_bytes;
+    void* ws = c.workspace(a[7], &ws_bytes);
+    void* stream = handle(a[1]);
+    return call(c.device, fn, table, refs, pool.k, pool.v, pool.page_stride, pool.head_stride,
+                pool.row_stride, narrow(B), narrow(M), narrow(pool.Hkv), narrow(pool.D),
+                narrow(pool.P), narrow(pool.page), map, ws, ws_bytes, stream);
+  });
+}
+
 #define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, ""}
 PyMethodDef kMethods[] = {ENTRY(qk_norm_rope),      ENTRY(qk_norm_rope_append),
                           ENTRY(kv8_append),        ENTRY(decode_kv8),
                           ENTRY(decode_kv8_blocks), ENTRY(decode_kv8_sparse),
                           ENTRY(block_scores),      ENTRY(block_select),
+                          ENTRY(paged_append),      ENTRY(decode_paged),
+                          ENTRY(pages_reserve),     ENTRY(pages_fork),
+                          ENTRY(pages_compact),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_gqa_marshal",
-                       "Argument checks of the 8-bit cache's binding.", -1, kMethods,
+                       "Argument checks of the 8-bit and the paged cache's binding.", -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

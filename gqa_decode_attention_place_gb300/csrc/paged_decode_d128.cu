@@ -1,0 +1,11 @@
+// paged_decode_d128.cu -- the paged decode at head dim 128.
+#include "paged_decode.cuh"
+
+namespace gqa {
+
+cudaError_t launch_paged_decode_128(PagedParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
+                                   cudaStream_t stream) {
+  return launch_paged_rows<128>(p, mk, mv, stream);
+}
+
+}  // namespace gqa

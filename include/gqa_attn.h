@@ -65,6 +65,10 @@ extern "C" {
                                         and was skipped; the launch's outputs are undefined */
 #define ATTN_DEV_BAD_BLOCK     0x8u  /* a listed block below -1 or past the cache's last one
                                         (attn_decode_step_kv8_blocks); it was skipped */
+#define ATTN_DEV_BAD_PAGE      0x10u /* attn_decode_step_paged: a page table entry that holds
+                                        attended rows names no page; its rows were skipped */
+#define ATTN_DEV_BAD_PARENT    0x20u /* attn_pages_fork: a parent outside -1 .. B - 1; the row
+                                        kept its entries */
 
 /*
  * attn_kv_append -- the in-place cache write of the decode page, section 4.1
@@ -502,6 +506,142 @@ int attn_decode_step_kv8_sparse(const void* q, const int32_t* positions, const v
                                 void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * The paged cache.  Keys and values lie in a pool of P pages, k_pages and
+ * v_pages [P, Hkv, page, D] bf16, laid out alike: element (p, h, r, d) at
+ * p * page_stride + h * head_stride + r * row_stride + d elements from either
+ * base.  Strides are multiples of 8, row_stride >= D, and rows do not overlap
+ * (any order of the three; a stride whose size is 1 counts for nothing).
+ *   page       : 16, 32, 64 or 128 rows.   D: 64 or 128.
+ *   page_table : [B, M] int32: row j of sequence b is row j % page of page
+ *                page_table[b][j / page], -1 for none.  A sequence can hold
+ *                M * page rows (at most 2^30).
+ *   page_refs  : [P] int32: how many table entries name a page; 0: it is free.
+ *                Sequences may share pages (forked ones do); rows are written
+ *                only into pages of one's own, which attn_pages_reserve sees to.
+ *   positions  : [B] int32: the row of each sequence's first new token.
+ *   lengths    : [B] int32, 0 .. S new tokens of each sequence in a padded
+ *                batch, or null for S each.
+ * All of these are device memory.  A step is: attn_pages_reserve,
+ * attn_paged_append, attn_decode_step_paged; attn_pages_fork passes pages on,
+ * cuts sequences and frees them; attn_pages_compact moves what is in use to the
+ * front of the pool.
+ *
+ * attn_paged_append -- rows k_new, v_new [B, S, Hkv, D] (token b*S + t at
+ * (b*S + t) * k_stride or v_stride elements, its heads dense) to rows
+ * positions[b] + t for t < lengths[b], bit-exact.  Nothing else is written.
+ * A sequence whose rows are not all in [0, M * page), or whose lengths[b] is not
+ * in 0 .. S, is skipped, and so are rows without a page (the decode call reports
+ * both).  S = 0 does nothing.
+ *   Limits: Hkv <= 1024, P <= 2^26.
+ */
+int attn_paged_append(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                      const int32_t* positions, const int32_t* lengths,
+                      const int32_t* page_table, void* k_pages, void* v_pages,
+                      int64_t page_stride, int64_t head_stride, int64_t row_stride, int B, int S,
+                      int Hkv, int D, int P, int page, int M, cudaStream_t stream);
+
+/*
+ * attn_paged_workspace_size -- bytes of device workspace attn_decode_step_paged
+ * needs; 0 if the sizes are invalid or unsupported.  The rules of
+ * attn_decode_workspace_size hold: zero-filled before first use, before use
+ * with other sizes and after ATTN_DEV_TIMEOUT; no overlapping calls on one
+ * workspace (two captured graphs that may run at once need one each).  Its
+ * first word is the device status word of attn_read_device_status.
+ */
+size_t attn_paged_workspace_size(int B, int S, int Hq, int Hkv, int D);
+
+/*
+ * attn_decode_step_paged -- attn_decode_step (S = 1) and attn_decode_multi over
+ * the paged cache: token t of sequence b attends rows 0 .. positions[b] + t,
+ *     out[b,t,h] = softmax_j(scale * q[b,t,h] . K_j) V_j
+ * with K_j and V_j of KV head h / g.  The rows must be there already
+ * (attn_paged_append).  Rows that a token does not see may hold anything, NaN
+ * included; entries behind the last attended row are not read.
+ *
+ *   q, out : [B, S, Hq, D] bf16.  Tokens t >= lengths[b] get zeros.
+ *   Both products in bf16 with fp32 sums, as in attn_decode_step; the
+ *   probabilities enter as two bf16 parts for S * g <= 16 and are rounded to
+ *   bf16 once beyond.
+ *   Supported: any g = Hq / Hkv with S * g <= 32; B <= 4096; Hkv <= 1024;
+ *   B * Hkv < 2^31 / 16.
+ *
+ * A sequence whose rows positions[b] .. positions[b] + lengths[b] - 1 are not
+ * all in [0, M * page), or whose lengths[b] is not in 0 .. S, gets NaN output
+ * rows and ATTN_DEV_BAD_POSITION; with lengths[b] = 0 its position and pages
+ * are not looked at.  An entry outside [0, P) that should hold attended rows
+ * sets ATTN_DEV_BAD_PAGE and its rows are left out (zeros if none is left).
+ */
+int attn_decode_step_paged(const void* q, const int32_t* positions, const int32_t* lengths,
+                           const int32_t* page_table, const void* k_pages, const void* v_pages,
+                           int64_t page_stride, int64_t head_stride, int64_t row_stride, int B,
+                           int S, int Hq, int Hkv, int D, int P, int page, int M, float scale,
+                           void* out, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+/*
+ * attn_pages_workspace_size -- bytes of device workspace that the three calls
+ * below need for these sizes (S: the most new tokens of a reserve); 0 if they
+ * are invalid.  Its first word is the device status word, to be zero before the
+ * first use.  Calls that share a workspace must not overlap in time.
+ */
+size_t attn_pages_workspace_size(int B, int S, int P, int page);
+
+/*
+ * attn_pages_reserve -- pages for the new rows positions[b] .. positions[b] +
+ * lengths[b] - 1.  Of the entries that hold them, one without a page (outside
+ * [0, P)) takes a free page, and one whose page is shared (page_refs > 1) takes
+ * a free page for itself: the rows before positions[b] that the shared page holds
+ * are copied, and the shared page counts one entry less.  So every sequence that
+ * shares a page leaves it, and a page that all of them left is free afterwards.
+ * The free pages (those whose count was 0 before the call) are taken from the
+ * lowest on, in the order of the sequences and their rows.
+ *
+ *   taken : [B] int32: how many pages the sequence took; -1 if the pages that
+ *           it and the sequences before it need are more than there are, or its
+ *           rows do not fit (ATTN_DEV_BAD_POSITION): nothing of it is changed.
+ *   S     : >= 1.  Other limits: B <= 65536, B * ceil(S / page + 1) <= 2^28.
+ * Two launches.
+ */
+int attn_pages_reserve(int32_t* page_table, int32_t* page_refs, const int32_t* positions,
+                       const int32_t* lengths, void* k_pages, void* v_pages, int64_t page_stride,
+                       int64_t head_stride, int64_t row_stride, int B, int S, int Hkv, int D,
+                       int P, int page, int M, int32_t* taken, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * attn_pages_fork -- every sequence b becomes a copy of what sequence parents[b]
+ * was before the call, cut to the pages of its first lengths[b] rows:
+ *     table'[b][j] = table[parents[b]][j]  if j * page < lengths[b], else -1
+ * with parents[b] = b for a sequence that stays and -1 for one that ends, and
+ * page_refs follows the entries that change.  No row is copied: the sequences
+ * share their pages (attn_pages_reserve parts them where rows are written).
+ * Forks, reordered beams, dropped tokens and freed sequences are all this.
+ *
+ *   parents : [B] int32, or null: every sequence stays.
+ *   lengths : [B] int32, or null: no sequence is cut; below 0 counts as 0.
+ *   A parent outside -1 .. B - 1 leaves that sequence's pages in place (to be cut
+ *   by lengths) and sets ATTN_DEV_BAD_PARENT.  Entries outside [0, P) count for
+ *   no page.  Limits: B <= 4096 with parents, else 65536.
+ */
+int attn_pages_fork(int32_t* page_table, int32_t* page_refs, const int32_t* parents,
+                    const int32_t* lengths, int B, int M, int P, int page, void* workspace,
+                    size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * attn_pages_compact -- moves the n pages in use (page_refs > 0) to pages
+ * 0 .. n - 1: the k-th of those at n or above goes to the k-th free page below
+ * n, with its rows, its count and every table entry that names it.
+ *
+ *   page_map : [P] int32, written: where each page went (p for one that stayed),
+ *              -1 for a free one: for page numbers kept elsewhere.
+ *   Table entries outside [0, P) stay.  B * M may be 0.  Two launches.
+ */
+int attn_pages_compact(int32_t* page_table, int32_t* page_refs, void* k_pages, void* v_pages,
+                       int64_t page_stride, int64_t head_stride, int64_t row_stride, int B,
+                       int M, int Hkv, int D, int P, int page, int32_t* page_map, void* workspace,
+                       size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * attn_prefill_causal -- causal prefill over a cached prefix (prefill page,
  * section "F.scaled_dot_product_attention"; decode page section 5: batch
  * prefill is causal).  New token i (absolute position start_pos + i) attends
@@ -600,8 +740,8 @@ int attn_read_prefill_skips(uint32_t* skips, cudaStream_t stream);
 
 /*
  * attn_read_range_skips -- the same count for attn_qk_norm_rope,
- * attn_qk_norm_rope_append, attn_kv8_append, attn_block_scores and
- * attn_block_select, which have no status word.
+ * attn_qk_norm_rope_append, attn_kv8_append, attn_block_scores,
+ * attn_block_select and attn_paged_append, which have no status word.
  */
 int attn_read_range_skips(uint32_t* skips, cudaStream_t stream);
 
