@@ -81,13 +81,17 @@ __device__ __forceinline__ long long flat_boundary(long long u, long long T, con
   if (k > 0 && n - E <= kShortTiles) return 2 * k < n ? f0 : f0 + n;
   return u;
 }
+// T * c / G, in 32 bits where that will do (c <= G <= 2^8 or so).
+__device__ __forceinline__ long long flat_share(long long T, int c, int G) {
+  return T < (1ll << 22) ? (long long)((uint32_t)T * (uint32_t)c / (uint32_t)G) : T * c / G;
+}
 template <int E>
 __device__ __forceinline__ void flat_range(FlatRange& r, long long T, int c, int G,
                                             const int* prefix, int B, int Hkv) {
   long long f0;
   int n;
-  r.t0 = flat_boundary<E>(T * c / G, T, prefix, B, Hkv, f0, n);
-  r.t1 = flat_boundary<E>(T * (c + 1) / G, T, prefix, B, Hkv, f0, n);
+  r.t0 = flat_boundary<E>(flat_share(T, c, G), T, prefix, B, Hkv, f0, n);
+  r.t1 = flat_boundary<E>(flat_share(T, c + 1, G), T, prefix, B, Hkv, f0, n);
   // tiles of the segment both before t1 (from f0 on) and behind it; before f0,
   // the units up to t0 + E may end another segment and hold no tile
   r.tA = f0 < r.t1 && r.t1 < f0 + n - E && f0 > r.t0 + E ? f0 : r.t1;

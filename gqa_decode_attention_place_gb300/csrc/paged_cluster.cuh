@@ -5,23 +5,27 @@
 // Rank r takes tiles r, r + C, r + 2C, ...  Its first tile is then tile r
 // whatever the position, so the tile's table entries are fetched beside the
 // position, and its copies go out one round trip after the launch's start.  No
-// scan, no global scratch, no atomics: each CTA's maxima and sums go to all
-// ranks, its outputs to the rank that owns their columns, and after one cluster
-// barrier each rank merges its columns, in rank order, and writes them.
+// scan, no global scratch, no atomics: each CTA's merged column goes straight
+// into the shared memory of the rank that owns it, and after one cluster barrier
+// each rank merges its columns, in rank order, and writes them.
 #pragma once
 
 namespace gqa {
 namespace {
 
-// Floats of the outputs that a rank owns.
-__host__ __device__ constexpr int owned(int R, int D, int C) {
-  return (R * (D / 4) + C - 1) / C * 4;
+struct Landing {  // one column of 4 dims of a query row, from one rank
+  float4 o;
+  float m, l;
+  float pad[2];
+};
+__host__ __device__ constexpr int landing_cols(int R, int D, int C) {
+  return (R * (D / 4) + C - 1) / C;
 }
 template <int D, int NT>
 size_t cluster_smem_bytes(int stages, int R, int C) {
   using Sh = Shape<D, NT>;
-  return (size_t)stages * (Sh::kStage + sizeof(TileMeta) + 16) + Sh::kQ + Sh::kFixed + 8 + 64 +
-         (size_t)C * (owned(R, D, C) * 4 + R * 8) + 16;
+  return (size_t)stages * (Sh::kStage + sizeof(TileMeta) + 16) + Sh::kQ + Sh::kMl + 8 + 64 +
+         (size_t)C * landing_cols(R, D, C) * sizeof(Landing) + 16;
 }
 
 template <int D, int NT>
@@ -32,17 +36,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int NS = p.stages, R = p.R, own = owned(R, D, C);
+  const int NS = p.stages, R = p.R, cols = landing_cols(R, D, C);
   uint8_t* stages = smem;
   uint8_t* qbuf = stages + (size_t)NS * Sh::kStage;               // [NT * 8] query rows
   TileMeta* meta = reinterpret_cast<TileMeta*>(qbuf + Sh::kQ);
-  uint8_t* weights = reinterpret_cast<uint8_t*>(meta + NS);
-  float* osum = reinterpret_cast<float*>(weights + 2 * Sh::kP);
-  float* wmax = osum + Sh::kO / 4;
-  float* lsum = wmax + 2 * NT * 64;
-  float* land = lsum + NT * 64;                                   // [C][own]
-  float2* land_ml = reinterpret_cast<float2*>(land + C * own);    // [C][R]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(land_ml + C * R);  // full [NS], empty [NS], sync
+  Landing* land = reinterpret_cast<Landing*>(meta + NS);          // [C][cols]
+  float2* ml = reinterpret_cast<float2*>(land + C * cols);        // [query rows][warps]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ml + Sh::kMl / 8);  // full [NS], empty [NS], sync
   int* misc = reinterpret_cast<int*>(bars + 2 * NS + 1);          // [0] abort
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_u32(&bars[s]), 1);
+      mbar_init(smem_u32(&bars[s]), 2);  // keys, values
       mbar_init(smem_u32(&bars[NS + s]), kWarps);
     }
     mbar_init(smem_u32(&bars[2 * NS]), kWarps);
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long e = ((long long)(rank + (long long)i * C) * kTile + slice * 16) >> p.lp;
     return e < p.M ? p.table[(size_t)b * p.M + e] : -1;
   };
-  int page = warp == kWarps ? entry(ti) : -1;
+  int page = warp >= kWarps ? entry(ti) : -1;
   int pos, n;
   const int kind = sequence(p, b, pos, n);
   if (kind != 2) {  // the same for the whole cluster, and for the sequence's other heads
@@ -85,10 +85,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nt = (pos + n - 1) / kTile + 1;
   const int mine = rank < nt ? (nt - rank + C - 1) / C : 0;  // tiles rank + i*C
 
-  ConsumerSync csync{smem_u32(&bars[2 * NS]), abort_flag, p.status, 0u};
-  PagedConsumer<D, NT> cs;
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ producer --
+  if (warp >= kWarps) {
+    // ----------------------------------------------------------- producers --
+    const bool keys = warp == kWarps;
     const int page_rows = 1 << p.lp, in_page = (slice * 16) & (page_rows - 1);
     auto in_use = [&](int i, int page) -> int {
       if (i >= mine || (rank + i * C) * kTile + slice * 16 > pos + n - 1) return -1;
@@ -119,20 +118,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool first = base + q == 0;
         const bool skip = p.test_skip >= 0 && seg == 0 && k == p.test_skip;  // tests only
         if (lane == 0) {
-          meta[s] = TileMeta{(int)((there >> (8 * q)) & 0xffu) | (first ? kStarts : 0), k * kTile,
-                             pos, n, b, kvh, 0, 1};
+          if (keys)
+            meta[s] = TileMeta{(int)((there >> (8 * q)) & 0xffu), k * kTile, pos, n, b, kvh, 0, 1};
           if (!skip)
             mbar_arrive_expect_tx(full, __popc((boxes >> (8 * q)) & 0xffu) *
-                                                ((uint32_t)page_rows * D * 4u) +
-                                            (first ? (uint32_t)R * D * 2u : 0u));
+                                                ((uint32_t)page_rows * D * 2u) +
+                                            (keys && first ? (uint32_t)R * D * 2u : 0u));
         }
         __syncwarp();
         if (ti == q && lead && !skip) {
           const uint32_t dst = smem_u32(stages + (size_t)s * Sh::kStage) + slice * 16 * D * 2;
-          tma_load_5d(dst, &tm_k, 0, 0, 0, kvh, cur, full);
-          tma_load_5d(dst + Sh::kOp, &tm_v, 0, 0, 0, kvh, cur, full);
+          tma_load_5d(dst + (keys ? 0 : Sh::kOp), keys ? &tm_k : &tm_v, 0, 0, 0, kvh, cur, full);
         }
-        if (first && !skip && lane < R)
+        if (first && !skip && keys && lane < R)
           bulk_load(smem_u32(qbuf) + lane * Sh::kQStride,
                     p.q + query_row(p, b, kvh, lane) * D, D * 2, full);
         if (++s == NS) {
@@ -144,25 +142,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ----------------------------------------------------------- consumers --
-    cs.c = lane >> 2;
-    cs.t = lane & 3;
-    cs.warp = warp;
-    cs.lane = lane;
-    cs.parity = 0;
-    cs.p_smem = smem_u32(weights);
-    cs.wmax = wmax;
-    cs.lsum = lsum;
-    cs.osum = osum;
-    cs.sync = &csync;
-    const TileMeta none{0, 0, pos, n, b, kvh, 0, 1};
-    cs.start(p, none);
+    ConsumerSync csync{smem_u32(&bars[2 * NS]), abort_flag, p.status, 0u};
+    PagedConsumer<D, NT> cs;
+    cs.init(warp, lane);
+    cs.start(p, pos, n);
     int s = 0;
     uint32_t ph = 0;
     for (int i = 0; i < mine; ++i) {
       if (!consumer_wait(smem_u32(&bars[s]), ph, abort_flag, p.status, lane)) break;
-      const TileMeta mt = meta[s];
       if (i == 0) cs.load_q(qbuf);
-      cs.tile(stages + (size_t)s * Sh::kStage, p, mt);
+      cs.tile(stages + (size_t)s * Sh::kStage, p, meta[s]);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars[NS + s]));
       if (++s == NS) {
@@ -170,47 +159,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         ph ^= 1u;
       }
     }
-    cs.finish();
-  }
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  if (warp < kWarps) {
-    cs.each_output([&](int, int r, int d, float2 y) {
-      if (r >= R) return;
-      const int at = r * D + d, owner = at / own;
+    // every other CTA of the cluster has started; each column goes to its owner
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    cs.merge(p, stages, ml, csync, [&](int r, int d, float m, float l, const float4& o) {
+      const int at = r * (D / 4) + d / 4, owner = at / cols;
       if (!range_ok(owner < C && rank < C, p.status)) return;
-      *reinterpret_cast<float2*>(cluster.map_shared_rank(land, owner) + rank * own +
-                                 (at - owner * own)) = y;
+      Landing* to = cluster.map_shared_rank(land, owner) + rank * cols + (at - owner * cols);
+      to->o = o;
+      *reinterpret_cast<float2*>(&to->m) = make_float2(m, l);
     });
-    // maxima and sums: warp w tells ranks w, w + 8; lane (c, t = i) row 8i + c
-    for (int to = warp; to < C; to += kWarps) {
-      float2* ml = cluster.map_shared_rank(land_ml, to) + rank * R;
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-        if (cs.t == i && 8 * i + cs.c < R) ml[8 * i + cs.c] = make_float2(cs.ref[i], cs.l[i]);
-    }
   }
+  if (warp >= kWarps) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   cluster.sync();
-  for (int j = tid * 4; j < own; j += kThreads * 4) {
-    const int at = rank * own + j;
-    if (at >= R * D) break;
-    const int r = at / D;
+  for (int j = tid; j < cols; j += kThreads) {
+    const int at = rank * cols + j;
+    if (at >= R * (D / 4)) break;
     float M = kMInit;
 #pragma unroll 4
-    for (int k = 0; k < C; ++k) M = fmaxf(M, land_ml[k * R + r].x);
+    for (int k = 0; k < C; ++k) M = fmaxf(M, land[k * cols + j].m);
     float l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = 0; k < C; ++k) {
-      const float2 ml = land_ml[k * R + r];
-      const float4 x = *reinterpret_cast<const float4*>(land + k * own + j);
-      const float e = ex2(ml.x - M);
-      l = fmaf(ml.y, e, l);
-      o.x = fmaf(x.x, e, o.x);
-      o.y = fmaf(x.y, e, o.y);
-      o.z = fmaf(x.z, e, o.z);
-      o.w = fmaf(x.w, e, o.w);
+      const Landing& x = land[k * cols + j];
+      const float e = ex2(x.m - M);
+      l = fmaf(x.l, e, l);
+      o.x = fmaf(x.o.x, e, o.x);
+      o.y = fmaf(x.o.y, e, o.y);
+      o.z = fmaf(x.o.z, e, o.z);
+      o.w = fmaf(x.o.w, e, o.w);
     }
-    store4<D>(p, b, kvh, r, at - r * D, o, l, r / p.g >= n);
+    const int r = at / (D / 4);
+    store4<D>(p, b, kvh, r, (at - r * (D / 4)) * 4, o, l, r / p.g >= n);
   }
   if (*abort_flag) {  // copies in flight land before the shared memory goes
     const uint64_t t_start = globaltimer_ns();

@@ -6,7 +6,7 @@
 //   out = softmax_j(scale q . K_j) V_j      over rows j = 0 .. positions[b] + t,
 // row j in row j % page of page table[b][j / page].  The R = S g <= 32 query
 // rows of a KV head share one pass over its keys and values: with x_j the score
-// in base 2, M a reference at most 2^64 below the largest x_j so far and
+// in base 2, M a reference at most kTau below the largest x_j so far and
 // w_j = 2^(x_j - M),
 //   out = sum_j w_j V_j / sum_j w_j.
 //
@@ -14,22 +14,22 @@
 //  * 128-row tiles stream through a shared-memory ring by tiled TMA copies with
 //    the 128-byte swizzle, one copy per page and operand: the pool is a 5-D
 //    tensor (dims, rows, dim halves, heads, pages), so any strides will do and
-//    a page's rows land where a contiguous tile's would.  One producer warp
-//    looks up table entries four tiles ahead (a lane per 16 rows) and issues.
-//  * 8 consumer warps.  Scores: each takes 16 rows, S = q K^T with the query
-//    rows as M (m16n8k16, bf16 in, fp32 out).  The weights go to shared memory
-//    as bf16, and for the second product each warp takes 16 dims of all 128
-//    rows (for D = 64: of 64), so a warp holds R x 16 outputs instead of R x D,
-//    a segment's end needs no merge among warps, and R can be 32.
-//  * One barrier a tile: the weights are relative to a reference that earlier
-//    tiles settled, and each tile's maximum, published with them, moves it for
-//    the next.  Only where a tile's maximum lies 2^64 above the reference (and
-//    in a piece's first tile) are the weights made again.
+//    a page's rows land where a contiguous tile's would.  Two producer warps,
+//    one for keys and one for values, look up table entries four tiles ahead (a
+//    lane per 16 rows) and issue.
+//  * 8 consumer warps take 16 rows of a tile each, with a maximum and a sum of
+//    their own, and never wait for one another inside a piece.  Both products
+//    run on warp-level MMAs (m16n8k16, bf16 in, fp32 out) with the query rows
+//    as M: the scores' accumulators are then, lane by lane, the A operand of
+//    the second product, so the weights stay in registers, and V comes through
+//    transposing matrix loads.
 //  * Up to 8 rows the weights enter as two bf16 parts for nothing: rows 8..15
 //    of the MMA's M are free and take the rest (16 bits).  Up to 16 rows they
 //    take a second MMA.  Beyond, the weights are rounded to bf16 once (2^-9,
 //    of errors that average over the keys; the output's own rounding is the
 //    same size).
+//  * At a piece's end the warps' partials meet in the memory of its last tile,
+//    eight query rows at a time, before that goes back to the ring.
 //  * Work is split as in the 8-bit decode (flat_list.cuh): a flat list of all
 //    tiles over a persistent grid, or for few segments a thread-block cluster
 //    per segment, merged through distributed shared memory.
@@ -56,16 +56,18 @@ constexpr int kTile = 128;
 constexpr int kSlices = kTile / 16;
 constexpr int kWarps = 8;                   // consumer warps
 constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 32;   // and the producer
+constexpr int kThreads = kConsumers + 64;   // and the producers: of keys, of values
 constexpr int kMaxStages = 6;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kE = 1;                       // units of a segment's end (flat_list.cuh)
 constexpr int kWholeTiles = 4;              // segments this short are not split
+// Whole segments, one CTA each (below): a lone CTA's tile takes kWholeNum / kWholeDen of
+// its share of a busy GPU, and a merge as long as kMergeCost / kWholeDen tiles.
+constexpr int kWholeNum = 5, kWholeDen = 9;
+template <int D> constexpr int kMergeCost = D == 128 ? 37 : 74;
 constexpr int kMaxCluster = 16;
 constexpr float kMInit = -3e38f;            // the reference before any row
-constexpr float kTau = 8.f;                 // it moves when a maximum lies 2^kTau above
-constexpr float kFar = 64.f;                // and before the weights, not after, beyond 2^kFar
-constexpr int kPStride = kTile * 2 + 16;    // bytes between rows of weights: no bank conflicts
+constexpr float kTau = 8.f;                 // it moves when a score lies more than this above
 
 constexpr int kSlicesMask = 0xff;  // TileMeta::flags: slices that hold rows
 constexpr int kStarts = 0x100;     // a piece starts with this tile
@@ -87,12 +89,12 @@ struct Shape {
   static constexpr int kStage = 2 * kOp;
   static constexpr int kQStride = D * 2 + 16;     // bytes between query rows: no bank conflicts
   static constexpr int kQ = NT * 8 * kQStride;
-  static constexpr int kPRows = NT == 1 ? 16 : 32;  // rows of weights, both parts
-  static constexpr int kP = kPRows * kPStride;
-  static constexpr int kHalves = 128 / D;         // warps that share 16 dims, half of the rows each
-  static constexpr int kO = kHalves > 1 ? NT * 8 * (D + 8) * 4 : 0;
-  static constexpr int kFixed = 2 * kP + kO + 3 * NT * 8 * 8 * 4 + 128;
+  static constexpr int kORow = D + 8;             // floats between rows of partials: likewise
+  static constexpr int kMl = kWarps * (NT == 1 ? 8 : 16) * 8;  // bytes of the warps' (reference, sum)
 };
+static_assert(kWarps * 8 * Shape<128, 1>::kORow * 4 <= Shape<128, 1>::kStage &&
+                  kWarps * 8 * Shape<64, 1>::kORow * 4 <= Shape<64, 1>::kStage,
+              "eight rows of every warp's partials fit a tile's memory");
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
                                             int c2, int c3, int c4, uint32_t bar) {
@@ -137,351 +139,310 @@ __device__ __forceinline__ size_t query_row(const PagedParams& p, int b, int kvh
   return ((size_t)b * p.S + t) * p.Hq + (size_t)kvh * p.g + (r - t * p.g);
 }
 
-// A consumer warp.  Lane 4c + t.  Query rows are r = 8 i + c for group i < NT;
-// MMA m-block m holds groups 2m and 2m + 1 as its rows c and c + 8 (NT = 1:
-// rows 8..15 are zero queries, and in the second product the weights' rest).
+// A consumer warp.  Lane 4c + t.  It serves G 8-row groups of query rows, rows c
+// and c + 8 of the MMA's M (G = 1: rows 8..15 are zero queries, and in the second
+// product the weights' rest).  Of a tile it takes 16 rows; with more than 16
+// query rows (NT = 4) half of the warps take 32 each for query rows 0..15, and the
+// other half the same for 16..31.  (Warps with all 32 query rows would hold 128
+// registers of outputs, and spill.)
 template <int D, int NT>
 struct PagedConsumer {
   using Sh = Shape<D, NT>;
-  static constexpr int MT = NT == 4 ? 2 : 1;  // m-blocks
-  static constexpr int KS = D / 16;           // MMA steps of a score
-  uint32_t qa[MT][KS][NT == 1 ? 2 : 4];
-  float o[MT][2][4];     // dims 8j + 2t, +1 of this warp's 16 for rows c, c + 8 of m-block m
-  float ref[NT], l[NT];  // l: this lane's rows only
-  int lim[NT];           // last cache row that the query row sees, -1: none
+  static constexpr int G = NT == 1 ? 1 : 2;       // 8-row groups of a warp
+  static constexpr int kTeams = NT == 4 ? 2 : 1;
+  static constexpr int kTeam = kWarps / kTeams;   // warps that share query rows
+  static constexpr int KS = D / 16;               // MMA steps of a score
+  uint32_t qa[KS][2 * G];
+  float o[D / 8][4];    // dims 8j + 2t, +1 for rows c, c + 8
+  float ref[G], l[G];   // of this warp's rows; l: of this lane's
+  int lim[G];           // last cache row that the query row sees, -1: none
   int c, t, warp, lane;
-  int parity;            // of the weights' double buffer
+  int team, row_base;   // its place; its first query row
 
-  uint32_t p_smem;       // weights [2][kPRows][kPStride]
-  float* wmax;           // [2][NT * 8][8] maxima of a tile by row and warp
-  float* lsum;           // [NT * 8][8]
-  float* osum;           // D = 64: the second half's outputs [NT * 8][D + 8]
-  ConsumerSync* sync;
-
+  __device__ __forceinline__ void init(int warp_, int lane_) {
+    warp = warp_;
+    lane = lane_;
+    c = lane >> 2;
+    t = lane & 3;
+    team = warp / kTeam;
+    row_base = 16 * team;
+  }
   __device__ __forceinline__ void load_q(const uint8_t* qs) {
     const uint32_t base = smem_u32(qs);
     const int i = lane >> 3, r = lane & 7;
-    if (NT == 1) {
+    if (G == 1) {
 #pragma unroll
       for (int k = 0; k < KS; k += 2) {
         uint32_t x[4];  // rows 0..7, four 8-dim chunks
         ldmatrix4(x, base + r * Sh::kQStride + (2 * k + i) * 16);
-        qa[0][k][0] = x[0];
-        qa[0][k][1] = x[1];
-        qa[0][k + 1][0] = x[2];
-        qa[0][k + 1][1] = x[3];
+        qa[k][0] = x[0];
+        qa[k][1] = x[1];
+        qa[k + 1][0] = x[2];
+        qa[k + 1][1] = x[3];
       }
     } else {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int k = 0; k < KS; ++k) {
+        uint32_t x[4];
+        ldmatrix4(x, base + (row_base + r + 8 * (i & 1)) * Sh::kQStride + (2 * k + (i >> 1)) * 16);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t x[4];
-          ldmatrix4(x, base + (16 * m + r + 8 * (i & 1)) * Sh::kQStride + (2 * k + (i >> 1)) * 16);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) qa[m][k][NT == 1 ? 0 : e] = x[e];
-        }
+        for (int e = 0; e < 4; ++e) qa[k][G == 1 ? 0 : e] = x[e];
+      }
     }
   }
-  __device__ __forceinline__ void start(const PagedParams& p, const TileMeta& mt) {
+  __device__ __forceinline__ void start(const PagedParams& p, int pos, int n) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int r = 8 * i + c, tok = r / p.g;
+    for (int i = 0; i < G; ++i) {
+      const int r = row_base + 8 * i + c, tok = r / p.g;
       ref[i] = kMInit;
       l[i] = 0.f;
-      lim[i] = r < p.R && tok < mt.n ? mt.pos + tok : -1;
+      lim[i] = r < p.R && tok < n ? pos + tok : -1;
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[m][j][e] = 0.f;
-  }
-  // Group i's rows of an accumulator: elements 2 (i % 2), +1 of m-block i / 2.
-  __device__ __forceinline__ void rescale(int i, float alpha) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (NT == 1) {
-          o[0][j][e] *= alpha;
-          o[0][j][2 + e] *= alpha;
-        } else {
-          o[i >> 1][j][2 * (i & 1) + e] *= alpha;
-        }
-      }
-    l[i] *= alpha;
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
   }
   // Byte offset in a tile of row 16 * slice (its first 64 dims).
   __device__ __forceinline__ static int slice_at(int slice, int lp) {
     const int row = slice * 16, pg = row >> lp;
     return ((pg << lp) * D * 2) + (row & ((1 << lp) - 1)) * 128;
   }
-  // Four weights of row group i (keys 2t, 2t+1, 8+2t, 9+2t of this warp's 16)
-  // and their sum.
-  __device__ __forceinline__ float weights(int i, const float (&x)[4]) {
-    float w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = ex2(x[e] - ref[i]);
-    const uint32_t at = p_smem + parity * Sh::kP + (8 * i + c) * kPStride + (16 * warp + 2 * t) * 2;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t hi = pack_bf16x2(w[2 * j], w[2 * j + 1]);
-      asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 16 * j), "r"(hi) : "memory");
-      if (NT <= 2) {
-        const uint32_t rest = pack_bf16x2(w[2 * j] - bf16lo(hi), w[2 * j + 1] - bf16hi(hi));
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 8 * NT * kPStride + 16 * j), "r"(rest)
-                     : "memory");
-      }
-    }
-    return (w[0] + w[1]) + (w[2] + w[3]);
-  }
 
-  // One tile.  ks: its keys; the values lie behind them.
+  // This warp's rows of a tile.  ks: its keys; the values lie behind them.
   __device__ __forceinline__ void tile(const uint8_t* ks, const PagedParams& p,
                                        const TileMeta& mt) {
-    const bool starts = (mt.flags & kStarts) != 0;
-    // every row of the tile is there and seen by every query row in use
-    const bool full = mt.row0 + kTile - 1 <= mt.pos && (mt.flags & kSlicesMask) == kSlicesMask;
-    const int lp = p.lp;
-    float s[MT][2][4];
+    const int first = warp & (kTeam - 1);
+    constexpr int kAll = kTeams == 1 ? 1 : 1 | (1 << kTeam);
+    if (kTeams > 1 && mt.row0 + 16 * (first + kTeam) + 15 <= mt.pos &&
+        ((mt.flags >> first) & kAll) == kAll) {
+      slices<kTeams, true>(ks, first, p, mt);
+      return;
+    }
+#pragma unroll 1
+    for (int sl = first; sl < kSlices; sl += kTeam) {
+      if (!((mt.flags >> sl) & 1)) continue;  // no rows there
+      // full: every row is seen by every query row in use
+      if (mt.row0 + 16 * sl + 15 <= mt.pos) slices<1, true>(ks, sl, p, mt);
+      else slices<1, false>(ks, sl, p, mt);
+    }
+  }
+  // 16 rows of slice sl, and with N = 2 of slice sl + kTeam, whose chains of
+  // products and exponentials overlap.
+  template <int N, bool FULL>
+  __device__ __forceinline__ void slices(const uint8_t* ks, int sl, const PagedParams& p,
+                                         const TileMeta& mt) {
+    const int half = 128 << p.lp;  // from a page's first 64 dims to the others
+    const int i8 = lane >> 3, r8 = lane & 7;
+    uint32_t at[N];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < N; ++n) at[n] = smem_u32(ks) + slice_at(sl + n * kTeam, p.lp);
+    const int row0 = mt.row0 + 16 * sl;  // the first cache row (N = 1)
+    float s[N][2][2][4];  // of each slice rows 0..7 and 8..15, in two chains each
+#pragma unroll
+    for (int n = 0; n < N; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[m][j][e] = 0.f;
-    {
-      const int i = lane >> 3, r = lane & 7;
-      const uint32_t at = smem_u32(ks) + slice_at(warp, lp) + (8 * (i >> 1) + r) * 128;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
+          for (int e = 0; e < 4; ++e) s[n][j][h][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      uint32_t a[4];
+      if (G == 1) {
+        a[0] = qa[k][0];
+        a[2] = qa[k][1];
+        a[1] = a[3] = 0u;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = qa[k][G == 1 ? 0 : e];
+      }
+      const int ch = 2 * k + (i8 & 1);
+      const int to = (8 * (i8 >> 1) + r8) * 128 + (2 * k >= 8 ? half : 0) + (((ch & 7) ^ r8) << 4);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
         uint32_t b[4];
-        const int ch = 2 * k + (i & 1);
-        ldmatrix4(b, at + (ch >> 3 ? 128 << lp : 0) + (((ch & 7) ^ r) << 4));
+        ldmatrix4(b, at[n] + to);
+        mma_bf16(s[n][0][N == 1 ? k & 1 : 0], a, b[0], b[1]);
+        mma_bf16(s[n][1][N == 1 ? k & 1 : 0], a, b[2], b[3]);
+      }
+    }
+    // weights as the second product's A operand: rows 2t, 2t+1 and 8 on of a slice
+    uint32_t w[N][4], rest[N][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          uint32_t a[4];
-          if (NT == 1) {
-            a[0] = qa[m][k][0];
-            a[2] = qa[m][k][1];
-            a[1] = a[3] = 0u;
-          } else {
+    for (int i = 0; i < G; ++i) {
+      float x[N][4], mine = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = qa[m][k][NT == 1 ? 0 : e];
+      for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v = s[n][e >> 1][0][2 * i + (e & 1)];
+          if (N == 1) v += s[n][e >> 1][1][2 * i + (e & 1)];
+          const int row = row0 + 8 * (e >> 1) + 2 * t + (e & 1);
+          x[n][e] = FULL || row <= lim[i] ? v * p.qscale : -INFINITY;
+        }
+        mine = fmax3(mine, x[n][0], fmax3(x[n][1], x[n][2], x[n][3]));
+      }
+      if (__any_sync(0xffffffffu, mine > ref[i] + kTau)) {
+        float mx = mine;
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float to = mx > ref[i] + kTau ? mx : ref[i];
+        const float alpha = ex2(ref[i] - to);
+        ref[i] = to;
+        l[i] *= alpha;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            o[j][2 * i + e] *= alpha;
+            if (G == 1) o[j][2 + e] *= alpha;
           }
-          mma_bf16(s[m][0], a, b[0], b[1]);
-          mma_bf16(s[m][1], a, b[2], b[3]);
-        }
       }
-    }
-    float x[NT][4], sum[NT];
-    const int buf = parity * NT * 64;
-    const bool mine = (mt.flags >> warp) & 1;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+      for (int n = 0; n < N; ++n) {
+        float y[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float sc = s[i >> 1][e >> 1][2 * (i & 1) + (e & 1)] * p.qscale;
-        const int row = mt.row0 + 16 * warp + 8 * (e >> 1) + 2 * t + (e & 1);
-        x[i][e] = full || (mine && row <= lim[i]) ? sc : -INFINITY;
-      }
-      float mx = fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (t == 0) wmax[buf + (8 * i + c) * 8 + warp] = mx;
-      sum[i] = starts ? 0.f : weights(i, x[i]);
-    }
-    (*sync)(lane);
-    float top[NT];
-    bool far = starts, grow = false;
+        for (int e = 0; e < 4; ++e) y[e] = ex2(x[n][e] - ref[i]);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const float4 u = *reinterpret_cast<const float4*>(wmax + buf + (8 * i + c) * 8);
-      const float4 v = *reinterpret_cast<const float4*>(wmax + buf + (8 * i + c) * 8 + 4);
-      top[i] = fmaxf(fmax3(u.x, u.y, u.z), fmax3(u.w, v.x, fmax3(v.y, v.z, v.w)));
-      far = far || top[i] > ref[i] + kFar;
-      grow = grow || top[i] > ref[i] + kTau;
-    }
-    // every warp sees the same maxima, so all of them decide alike
-    far = __any_sync(0xffffffffu, far);
-    if (far) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        if (top[i] > ref[i] + kTau) {
-          rescale(i, ex2(ref[i] - top[i]));
-          ref[i] = top[i];
-        }
-        sum[i] = weights(i, x[i]);
-      }
-      grow = false;
-      (*sync)(lane);
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i) l[i] += sum[i];
-    if (full) values<true>(ks + Sh::kOp, p, mt);
-    else values<false>(ks + Sh::kOp, p, mt);
-    if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-        if (top[i] > ref[i] + kTau) {
-          rescale(i, ex2(ref[i] - top[i]));
-          ref[i] = top[i];
-        }
-    }
-    parity ^= 1;
-  }
-
-  // The A operand of the second product for m-block m, part `rest`, slice s.
-  __device__ __forceinline__ void load_p(uint32_t (&a)[4], int m, int rest, int s) const {
-    const int i = lane >> 3, r = lane & 7;
-    ldmatrix4(a, p_smem + parity * Sh::kP + (16 * m + 8 * NT * rest + r + 8 * (i & 1)) * kPStride +
-                     (16 * s + 8 * (i >> 1)) * 2);
-  }
-  // o += P V for this warp's 16 dims.
-  template <bool FULL>
-  __device__ __forceinline__ void values(const uint8_t* vs, const PagedParams& p,
-                                         const TileMeta& mt) {
-    constexpr int kGroups = D / 16;                // warps side by side
-    constexpr int kSteps = kSlices / Sh::kHalves;  // slices of a warp
-    const int dims = warp % kGroups, s0 = (warp / kGroups) * kSteps;
-    const int i = lane >> 3, r = lane & 7;
-    const int ch = 2 * dims + (i >> 1);
-    const uint32_t at = smem_u32(vs) + (ch >> 3 ? 128 << p.lp : 0) + (8 * (i & 1) + r) * 128 +
-                        (((ch & 7) ^ r) << 4);
-    const int seen = mt.pos + mt.n - mt.row0;  // rows of the tile that a token may see
-#pragma unroll(FULL ? kSteps : 1)
-    for (int k = 0; k < kSteps; ++k) {
-      const int s = s0 + k;
-      if (!FULL && !((mt.flags >> s) & 1)) continue;  // nothing was loaded there
-      uint32_t b[4];
-      ldmatrix4_trans(b, at + slice_at(s, p.lp));
-      if (!FULL) {
-        // rows past the last token may be NaN: 0 * NaN would spread
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] &= keep(seen - (16 * s + 8 * (e & 1) + 2 * t));
-        // and so may a drafted token's be, which earlier tokens do not see
-        if (mt.n > 1 && 16 * s + 15 > mt.pos - mt.row0) {
-          bool odd = false;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            odd = odd || (b[e] & 0x7f80u) == 0x7f80u || (b[e] & 0x7f800000u) == 0x7f800000u;
-          if (__any_sync(0xffffffffu, odd)) {
-            values_by_token(b, s, p, mt);
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t hi = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+          w[n][2 * j + i] = hi;
+          if (NT == 4) {  // the sum is of the weights as they enter
+            y[2 * j] = bf16lo(hi);
+            y[2 * j + 1] = bf16hi(hi);
             continue;
           }
+          const uint32_t lo = pack_bf16x2(y[2 * j] - bf16lo(hi), y[2 * j + 1] - bf16hi(hi));
+          if (G == 1) w[n][2 * j + 1] = lo;
+          else rest[n][2 * j + i] = lo;
         }
+        l[i] += (y[0] + y[1]) + (y[2] + y[3]);
       }
+    }
+    const int seen = mt.pos + mt.n - row0;  // rows that some token may see
+    const bool drafts = !FULL && mt.n > 1;
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        uint32_t a[4];
-        load_p(a, m, 0, s);
-        mma_bf16(o[m][0], a, b[0], b[1]);
-        mma_bf16(o[m][1], a, b[2], b[3]);
-        if (NT == 2) {
-          load_p(a, m, 1, s);
-          mma_bf16(o[m][0], a, b[0], b[1]);
-          mma_bf16(o[m][1], a, b[2], b[3]);
+    for (int d = 0; d < D / 16; ++d) {
+      const int ch = 2 * d + (i8 >> 1);
+      const int to = Sh::kOp + (8 * (i8 & 1) + r8) * 128 + (2 * d >= 8 ? half : 0) +
+                     (((ch & 7) ^ r8) << 4);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        uint32_t b[4];  // 16 dims: rows 0..7 and 8..15 of the first 8, then of the others
+        ldmatrix4_trans(b, at[n] + to);
+        if (!FULL) {
+          // rows past the last token may be NaN: 0 * NaN would spread
+#pragma unroll
+          for (int e = 0; e < 4; ++e) b[e] &= keep(seen - 8 * (e & 1) - 2 * t);
+          // and so may a drafted token's be, which earlier tokens do not see
+          if (drafts) {
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              odd = odd || (b[e] & 0x7f80u) == 0x7f80u || (b[e] & 0x7f800000u) == 0x7f800000u;
+            if (__any_sync(0xffffffffu, odd)) {
+              by_token(o[2 * d], o[2 * d + 1], w[n], b, row0, p, mt);
+              if (kTwoParts) by_token(o[2 * d], o[2 * d + 1], rest[n], b, row0, p, mt);
+              continue;
+            }
+          }
+        }
+        mma_bf16(o[2 * d], w[n], b[0], b[1]);
+        mma_bf16(o[2 * d + 1], w[n], b[2], b[3]);
+        if (kTwoParts) {
+          mma_bf16(o[2 * d], rest[n], b[0], b[1]);
+          mma_bf16(o[2 * d + 1], rest[n], b[2], b[3]);
         }
       }
     }
   }
+  static constexpr bool kTwoParts = NT == 2;  // a second MMA for the weights' rest
   // Mask of a register with two rows of which the first n (or all) count.
   __device__ __forceinline__ static uint32_t keep(int n) {
     return n >= 2 ? 0xffffffffu : n == 1 ? 0x0000ffffu : 0u;
   }
-  // The same for one slice with infinities or NaN among the values: token by
-  // token, each with the rows that it sees, into its own rows of o only.
-  __device__ __forceinline__ void values_by_token(const uint32_t (&b)[4], int s, const PagedParams& p,
-                                               const TileMeta& mt) {
+  // The same products for values b with infinities or NaN among them: token by
+  // token, each with the rows that it sees, into its own rows of o0 and o1 only.
+  __device__ __forceinline__ void by_token(float (&o0)[4], float (&o1)[4], const uint32_t (&w)[4],
+                                           const uint32_t (&b)[4], int row0, const PagedParams& p,
+                                           const TileMeta& mt) const {
+#pragma unroll 1
     for (int tok = 0; tok < mt.n; ++tok) {
       uint32_t seen[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        seen[e] = b[e] & keep(mt.pos + tok + 1 - mt.row0 - (16 * s + 8 * (e & 1) + 2 * t));
+        seen[e] = b[e] & keep(mt.pos + tok + 1 - row0 - 8 * (e & 1) - 2 * t);
+      float y0[4] = {0.f, 0.f, 0.f, 0.f}, y1[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_bf16(y0, w, seen[0], seen[1]);
+      mma_bf16(y1, w, seen[2], seen[3]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float y[2][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[j][e] = 0.f;
-#pragma unroll
-        for (int rest = 0; rest < (NT == 2 ? 2 : 1); ++rest) {
-          uint32_t a[4];
-          load_p(a, m, rest, s);
-          mma_bf16(y[0], a, seen[0], seen[1]);
-          mma_bf16(y[1], a, seen[2], seen[3]);
+      for (int e = 0; e < 4; ++e)
+        if ((G == 1 ? c : row_base + 8 * (e >> 1) + c) / p.g == tok) {
+          o0[e] += y0[e];
+          o1[e] += y1[e];
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = NT == 1 ? c : 16 * m + 8 * (e >> 1) + c;
-            if (r / p.g == tok) o[m][j][e] += y[j][e];
-          }
-      }
     }
   }
 
-  // The piece's sums over all lanes and warps; for D = 64 also the outputs of
-  // both halves, in the first four warps.
-  __device__ __forceinline__ void finish() {
+  // The piece's end, by all consumer warps: their partials meet in `buf` (a
+  // tile's memory that all of them are done with after the first barrier), and
+  // f(row, dim, reference, sum, four outputs) gets each column of a query row,
+  // merged in warp order.
+  template <typename F>
+  __device__ __forceinline__ void merge(const PagedParams& p, uint8_t* buf, float2* ml,
+                                        ConsumerSync& csync, F f) {
+    float* part = reinterpret_cast<float*>(buf);
+    const int tid = warp * 32 + lane, w0 = warp & (kTeam - 1);
+    csync(lane);
+    // with two teams, both teams' groups in a round: [team][warp][8 rows]
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < G; ++i) {
+      if (8 * i >= p.R) break;
+      if (i > 0) csync(lane);  // the rows before have been read
       float sum = l[i];
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (t == 0) lsum[(8 * i + c) * 8 + warp] = sum;
-    }
-    if (NT == 1) {  // the weights' two parts
+      if (t == 0) ml[(row_base + 8 * i + c) * kTeam + w0] = make_float2(ref[i], sum);
+      float* to = part + (warp * 8 + c) * Sh::kORow + 2 * t;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) o[0][j][e] += o[0][j][2 + e];
-    }
-    if (Sh::kHalves > 1 && warp >= kWarps / 2) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<float2*>(osum + (8 * i + c) * (D + 8) + 16 * (warp - kWarps / 2) +
-                                     8 * j + 2 * t) =
-              make_float2(o[i >> 1][j][2 * (i & 1)], o[i >> 1][j][2 * (i & 1) + 1]);
-    }
-    (*sync)(lane);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const float4 u = *reinterpret_cast<const float4*>(lsum + (8 * i + c) * 8);
-      const float4 v = *reinterpret_cast<const float4*>(lsum + (8 * i + c) * 8 + 4);
-      l[i] = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
-    }
-    if (Sh::kHalves > 1 && warp < kWarps / 2) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 y = *reinterpret_cast<const float2*>(osum + (8 * i + c) * (D + 8) +
-                                                            16 * warp + 8 * j + 2 * t);
-          o[i >> 1][j][2 * (i & 1)] += y.x;
-          o[i >> 1][j][2 * (i & 1) + 1] += y.y;
+      for (int j = 0; j < D / 8; ++j) {
+        float2 y = make_float2(o[j][2 * i], o[j][2 * i + 1]);
+        if (G == 1) {  // the weights' two parts
+          y.x += o[j][2];
+          y.y += o[j][3];
         }
+        *reinterpret_cast<float2*>(to + 8 * j) = y;
+      }
+      csync(lane);
+#pragma unroll
+      for (int col = tid; col < kTeams * 8 * (D / 4); col += kConsumers) {
+        const int row = col / (D / 4) & 7, tm = col / (8 * (D / 4)), d = col % (D / 4) * 4;
+        const int r = 16 * tm + 8 * i + row;
+        if (r >= p.R) continue;
+        float2 x[kTeam];
+        float M = kMInit, L = 0.f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kTeam; ++k) {
+          x[k] = ml[r * kTeam + k];
+          M = fmaxf(M, x[k].x);
+        }
+#pragma unroll
+        for (int k = 0; k < kTeam; ++k) {
+          const float e = ex2(x[k].x - M);
+          const float4 v = *reinterpret_cast<const float4*>(
+              part + ((tm * kTeam + k) * 8 + row) * Sh::kORow + d);
+          L = fmaf(x[k].y, e, L);
+          y.x = fmaf(v.x, e, y.x);
+          y.y = fmaf(v.y, e, y.y);
+          y.z = fmaf(v.z, e, y.z);
+          y.w = fmaf(v.w, e, y.w);
+        }
+        f(r, d, M, L, y);
+      }
     }
-  }
-  __device__ __forceinline__ bool holds_output() const {
-    return Sh::kHalves == 1 || warp < kWarps / 2;
-  }
-  // f(row, first of two dims, values) for this lane's outputs.
-  template <typename F>
-  __device__ __forceinline__ void each_output(F f) const {
-    if (!holds_output()) return;
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        f(i, 8 * i + c, 16 * warp + 8 * j + 2 * t,
-          make_float2(o[i >> 1][j][2 * (i & 1)], o[i >> 1][j][2 * (i & 1) + 1]));
   }
 };
 
@@ -566,7 +527,8 @@ __device__ __forceinline__ void merge_parts(const PagedParams& p, const TileMeta
   }
 }
 
-// A table entry that is in use; -1 where it names no page.
+constexpr int kNoRows = -0x7fffffff - 1;  // a table entry that holds no attended rows
+// A table entry that does; -1 where it names no page.
 __device__ __forceinline__ int page_ok(const PagedParams& p, int page) {
   if (page >= 0 && page < p.P) return page;
   set_status(p.status, ATTN_DEV_BAD_PAGE);
@@ -583,12 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* stages = smem;
   uint8_t* qbuf = stages + (size_t)NS * Sh::kStage;            // [NS][NT * 8] query rows
   TileMeta* meta = reinterpret_cast<TileMeta*>(qbuf + NS * Sh::kQ);
-  uint8_t* weights = reinterpret_cast<uint8_t*>(meta + NS);
-  float* osum = reinterpret_cast<float*>(weights + 2 * Sh::kP);
-  float* wmax = osum + Sh::kO / 4;
-  float* lsum = wmax + 2 * NT * 64;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(lsum + NT * 64);  // full [NS], empty [NS], sync
-  int* misc = reinterpret_cast<int*>(bars + 2 * NS + 1);  // [0] abort, [1] last to arrive, [8..16) scan
+  float2* ml = reinterpret_cast<float2*>(meta + NS);             // [query rows][warps]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ml + Sh::kMl / 8);  // full [NS], empty [NS], sync
+  int* misc = reinterpret_cast<int*>(bars + 2 * NS + 1);  // [0] abort, [1] last to arrive,
+                                                          // [2] longest segment, [8..16) scan
   int* prefix = misc + 16;                                // [B + 1]
   int* spos = prefix + B + 1;                             // [B]
   uint8_t* snew = reinterpret_cast<uint8_t*>(spos + B);   // [B]
@@ -598,15 +558,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_u32(&bars[s]), 1);
+      mbar_init(smem_u32(&bars[s]), 2);  // keys, values
       mbar_init(smem_u32(&bars[NS + s]), kWarps);
     }
     mbar_init(smem_u32(&bars[2 * NS]), kWarps);
-    misc[0] = 0;
+    misc[0] = misc[2] = 0;
     fence_mbar_init();
   }
   for (int i = tid; i < NS * Sh::kQ / 16; i += kThreads)  // rows past R stay zero
     reinterpret_cast<uint4*>(qbuf)[i] = make_uint4(0u, 0u, 0u, 0u);
+  // (they come before the query copies that land over them)
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();
   grid_dependency_wait();
   grid_dependents_launch();
 
@@ -622,6 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       snew[b] = (uint8_t)n;
       if (kind == 2) v = (pos + n - 1) / kTile + 1 + kE;
     }
+    const int most = __reduce_max_sync(0xffffffffu, v);
+    if (lane == 0 && warp < kWarps) atomicMax(misc + 2, most);
     int x = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -642,8 +607,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   if (tid == 0) prefix[B] = carry;
-  // (the zeros written above come before the query copies that land over them)
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
 
   for (int b = blockIdx.x; b < B; b += gridDim.x)
@@ -653,27 +616,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long nseg = (long long)B * Hkv;
   long long gw = min((long long)gridDim.x, T);
   if (T <= (long long)(kWholeTiles + kE) * nseg) gw = min(gw, nseg);
-  const int G = (int)gw;
+  // A CTA for each segment where the longest alone takes no longer than an even
+  // share of the tiles and the merge of a split segment would.
+  const bool whole = nseg <= (long long)gridDim.x &&
+                     (long long)misc[2] * kWholeNum * gw <= T * kWholeDen + kMergeCost<D> * gw;
+  const int G = whole ? (int)nseg : (int)gw;
   if ((int)blockIdx.x >= G) return;
   FlatRange rg;
-  flat_range<kE>(rg, T, blockIdx.x, G, prefix, B, Hkv);
+  if (whole) {
+    const int b = (int)blockIdx.x / Hkv, n = prefix[b + 1] - prefix[b];
+    rg.t0 = (long long)Hkv * prefix[b] + (long long)((int)blockIdx.x - b * Hkv) * n;
+    rg.t1 = rg.tA = rg.t0 + n;
+  } else {
+    flat_range<kE>(rg, T, blockIdx.x, G, prefix, B, Hkv);
+  }
   if (rg.t0 >= rg.t1) return;
   FlatWalk w;
   flat_start<kE>(w, rg, prefix, spos, B, Hkv);
   if (w.u >= w.end) return;  // end units alone
 
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ producer --
+  if (warp >= kWarps) {
+    // ----------------------------------------------------------- producers --
     // Tiles go in batches of four, lane 8*ti + slice looks after slice
     // `slice` of the batch's tile ti; a batch's table entries are loaded while
     // the one before it is issued.
+    const bool keys = warp == kWarps;  // this warp also describes the tile and brings the queries
     const int ti = lane >> 3, slice = lane & 7;
     const int page_rows = 1 << p.lp, in_page = (slice * 16) & (page_rows - 1);
-    auto fetch = [&](const FlatWalk& w) -> int {  // -1: no rows there
+    // The slice's table entry, kNoRows where it holds none; looked at a batch later.
+    auto fetch = [&](const FlatWalk& w) -> int {
       const int row = w.k * kTile + slice * 16;
-      if (w.u >= w.end || row > w.pos + snew[w.b] - 1) return -1;
-      if (!range_ok((row >> p.lp) < p.M, p.status)) return -1;
-      return page_ok(p, p.table[(size_t)w.b * p.M + (row >> p.lp)]);
+      if (w.u >= w.end || row > w.pos + snew[w.b] - 1) return kNoRows;
+      if (!range_ok((row >> p.lp) < p.M, p.status)) return kNoRows;
+      return p.table[(size_t)w.b * p.M + (row >> p.lp)];
     };
     auto step = [&](FlatWalk& w, int n) {  // n tiles on, as far as the range goes
       if (w.k + n < w.nt && w.u + n < w.end) {
@@ -714,15 +689,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t pass = 0;
     step(w, ti);
     FlatWalk cur = w;
-    int page = fetch(w);
+    int entry = fetch(w);
     bool ok = true;
     while (ok) {
       const bool on = cur.u < cur.end;
       const int n_q = __popc(__ballot_sync(0xffffffffu, on)) >> 3;  // tiles of the batch
       if (n_q == 0) break;
       step(w, 4);
-      const int next_page = fetch(w);
-      TileMeta mt;
+      const int next = fetch(w);
+      const int page = entry == kNoRows ? -1 : page_ok(p, entry);
+      TileMeta mt = {};
       if (on && slice == 0) describe(cur, mt);
       const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
       const bool lead = page >= 0 && in_page == 0;
@@ -740,31 +716,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t full = smem_u32(&bars[s]);
-        uint32_t first = 0;
-        int b = 0, kvh = 0;
+        const bool first = __shfl_sync(0xffffffffu, (mt.flags & kStarts) != 0, 8 * q);
         if (lane == 8 * q) {
           mt.flags |= (there >> (8 * q)) & 0xffu;
-          meta[s] = mt;
-          first = (mt.flags & kStarts) != 0;
-          b = mt.b;
-          kvh = mt.kvh;
+          if (keys) meta[s] = mt;
           if (!skip)
             mbar_arrive_expect_tx(full, __popc((boxes >> (8 * q)) & 0xffu) *
-                                                ((uint32_t)page_rows * D * 4u) +
-                                            (first ? (uint32_t)p.R * D * 2u : 0u));
+                                                ((uint32_t)page_rows * D * 2u) +
+                                            (keys && first ? (uint32_t)p.R * D * 2u : 0u));
         }
         __syncwarp();
-        first = __shfl_sync(0xffffffffu, first, 8 * q);
         const bool hold = __shfl_sync(0xffffffffu, skip, 8 * q);
         if (ti == q && lead && !hold) {
-          const uint32_t dst =
-              smem_u32(stages + (size_t)s * Sh::kStage) + slice * 16 * D * 2;
-          tma_load_5d(dst, &tm_k, 0, 0, 0, cur.kvh, page, full);
-          tma_load_5d(dst + Sh::kOp, &tm_v, 0, 0, 0, cur.kvh, page, full);
+          const uint32_t dst = smem_u32(stages + (size_t)s * Sh::kStage) + slice * 16 * D * 2;
+          tma_load_5d(dst + (keys ? 0 : Sh::kOp), keys ? &tm_k : &tm_v, 0, 0, 0, cur.kvh, page,
+                      full);
         }
-        if (first && !hold) {  // the piece's query rows, one by each lane
-          b = __shfl_sync(0xffffffffu, b, 8 * q);
-          kvh = __shfl_sync(0xffffffffu, kvh, 8 * q);
+        if (first && !hold && keys) {  // the piece's query rows, one by each lane
+          const int b = __shfl_sync(0xffffffffu, mt.b, 8 * q);
+          const int kvh = __shfl_sync(0xffffffffu, mt.kvh, 8 * q);
           if (lane < p.R)
             bulk_load(smem_u32(qbuf + s * Sh::kQ) + lane * Sh::kQStride,
                       p.q + query_row(p, b, kvh, lane) * D, D * 2, full);
@@ -775,74 +745,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       cur = w;
-      page = next_page;
+      entry = next;
     }
   } else {
     // ----------------------------------------------------------- consumers --
     ConsumerSync csync{smem_u32(&bars[2 * NS]), abort_flag, p.status, 0u};
     PagedConsumer<D, NT> cs;
-    cs.c = lane >> 2;
-    cs.t = lane & 3;
-    cs.warp = warp;
-    cs.lane = lane;
-    cs.parity = 0;
-    cs.p_smem = smem_u32(weights);
-    cs.wmax = wmax;
-    cs.lsum = lsum;
-    cs.osum = osum;
-    cs.sync = &csync;
+    cs.init(warp, lane);
     int s = 0;
     uint32_t ph = 0;
     for (;;) {
       if (!consumer_wait(smem_u32(&bars[s]), ph, abort_flag, p.status, lane)) break;
       const TileMeta mt = meta[s];
+      uint8_t* tile = stages + (size_t)s * Sh::kStage;
       if (mt.flags & kStarts) {
         cs.load_q(qbuf + s * Sh::kQ);
-        cs.start(p, mt);
+        cs.start(p, mt.pos, mt.n);
       }
-      cs.tile(stages + (size_t)s * Sh::kStage, p, mt);
+      cs.tile(tile, p, mt);
+      if (mt.flags & kEnds) {
+        if (mt.parts == 1) {
+          cs.merge(p, tile, ml, csync, [&](int r, int d, float, float l, const float4& o) {
+            store4<D>(p, mt.b, mt.kvh, r, d, o, l, r / p.g >= mt.n);
+          });
+        } else {
+          const int slot = part_slot(mt.c0, (int)blockIdx.x - mt.c0);
+          cs.merge(p, tile, ml, csync, [&](int r, int d, float m, float l, const float4& o) {
+            if (!slot_ok(p, slot)) return;
+            *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * p.R + r) * D + d) = o;
+            if (d == 0)
+              *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * p.R + r) * 2) =
+                  make_float2(m, l);
+          });
+        }
+        // (this memory was written here; copies land in it next)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars[NS + s]));
       if (++s == NS) {
         s = 0;
         ph ^= 1u;
       }
-      if (mt.flags & kEnds) {
-        cs.finish();
-        if (*abort_flag) break;
-        if (mt.parts == 1) {
-          cs.each_output([&](int i, int r, int d, float2 y) {
-            if (r >= p.R) return;
-            const bool idle = r / p.g >= mt.n;
-            const float inv = idle || cs.l[i] == 0.f ? 0.f : 1.f / cs.l[i];
-            const size_t at = query_row(p, mt.b, mt.kvh, r) * D + d;
-            if (range_ok(at + 2 <= (size_t)p.B * p.S * p.Hq * D, p.status))
-              *reinterpret_cast<uint32_t*>(p.out + at) =
-                  idle ? 0u : pack_bf16x2(y.x * inv, y.y * inv);
-          });
-        } else {
-          const int slot = part_slot(mt.c0, (int)blockIdx.x - mt.c0);
-          if (slot_ok(p, slot)) {
-            cs.each_output([&](int i, int r, int d, float2 y) {
-              if (r >= p.R) return;
-              *reinterpret_cast<float2*>(p.part_o + ((size_t)slot * p.R + r) * D + d) = y;
-              if (d == 0)
-                *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * p.R + r) * 2) =
-                    make_float2(cs.ref[i], cs.l[i]);
-            });
-          }
-          csync(lane);
-          if (tid == 0) {
-            uint32_t* counter = p.counters + mt.b * Hkv + mt.kvh;
-            __threadfence();  // (the other threads' stores came before the barrier)
-            const bool last = atomicAdd(counter, 1u) + 1 == (uint32_t)mt.parts;
-            if (last) *counter = 0;
-            __threadfence();
-            misc[1] = last;
-          }
-          csync(lane);
-          if (misc[1] && !*abort_flag) merge_parts<D>(p, mt, tid);
+      if ((mt.flags & kEnds) && mt.parts > 1) {
+        csync(lane);
+        if (tid == 0) {
+          uint32_t* counter = p.counters + mt.b * Hkv + mt.kvh;
+          __threadfence();  // (the other threads' stores came before the barrier)
+          const bool last = !*abort_flag && atomicAdd(counter, 1u) + 1 == (uint32_t)mt.parts;
+          if (last) *counter = 0;
+          __threadfence();
+          misc[1] = last;
         }
+        csync(lane);
+        if (misc[1] && !*abort_flag) merge_parts<D>(p, mt, tid);
       }
       if (mt.flags & kLast) break;
     }
@@ -867,7 +823,7 @@ namespace {
 template <int D, int NT>
 size_t flat_smem_bytes(int stages, int B) {
   using Sh = Shape<D, NT>;
-  return (size_t)stages * (Sh::kStage + Sh::kQ + sizeof(TileMeta) + 16) + Sh::kFixed + 8 + 64 +
+  return (size_t)stages * (Sh::kStage + Sh::kQ + sizeof(TileMeta) + 16) + Sh::kMl + 8 + 64 +
          (size_t)9 * B + 16;
 }
 
@@ -942,9 +898,15 @@ cudaError_t paged_device(const PagedDevice** out) {
 
 // CTAs per segment in cluster mode, or 0 for the split over a flat list.  The
 // cluster would be the largest that lets every segment have its own resident at
-// once; it is taken where its estimate is lower (us).  The host knows only what
-// the table can hold: a position is taken to lie half-way on average, and the
-// longest of several, which a cluster waits for, at the end.
+// once, or one CTA; it is taken where it should be faster.  The host knows only
+// what the table can hold: positions are taken as spread evenly over that.  In
+// us, measured (D = 128; a tile at D = 64 takes half):
+//   all SMs    1.45 for each tile of an SM's even share
+//   clusters   4.3, then the even share and 15% of it, or 0.62 for each tile of the
+//              longest segment's CTAs where that is more; 2 for each further wave
+//   flat list  12 (scan, lookups, the merge of split segments) and the even share
+// (2 sequences up to 8192 rows, 8 heads: 17 in clusters, 21 by the list; 10 up to
+// 16000: 74 and 50.)
 template <int D>
 int cluster_size(const PagedParams& p, const PagedDevice& d) {
   if (g_decode_test_cluster >= 0)  // schedule tests only
@@ -953,13 +915,13 @@ int cluster_size(const PagedParams& p, const PagedDevice& d) {
   const int tiles = (p.cap + kTile - 1) / kTile;
   int c = min(kMaxCluster, tiles);
   while (c > 1 && nseg > d.clusters[c]) --c;
-  const float mean = 0.5f * (float)tiles;
-  const float longest = p.B == 1 ? mean : (float)tiles;
+  const float longest = (float)tiles * (float)p.B / (float)(p.B + 1);
   const float waves = c > 1 ? 1.f : (float)((nseg + d.sms - 1) / d.sms);
-  const float per_tile = D == 128 ? 1.4f : 0.8f;
-  const float clusters = waves * (4.f + per_tile * ceilf(longest / (float)c));
-  const float flat = 9.f + per_tile * (float)nseg * mean / (float)d.sms;
-  return clusters <= flat ? c : 0;
+  const float per_tile = D == 128 ? 1.45f : 0.75f;
+  const float share = per_tile * 0.5f * (float)tiles * (float)nseg / (float)d.sms;
+  const float clusters = 4.3f + 2.f * (waves - 1.f) +
+                         fmaxf(1.15f * share, 0.43f * per_tile * ceilf(longest / (float)c));
+  return clusters <= 12.f + share ? c : 0;
 }
 
 template <int D, int NT>

@@ -9,9 +9,9 @@
 // alone.  Counts change by integer atomics, whose order does not matter.
 //
 // Latency bounds the bookkeeping (a few hundred KB at most): reserve and
-// compact scan the counts with one cluster of 8 CTAs, whose sums meet through
-// distributed shared memory, and the pages' rows are copied by a second launch
-// over the whole GPU that starts with the list ready.
+// compact scan the counts with one CTA, or for large pools with a cluster whose
+// sums meet through distributed shared memory, and the pages' rows are copied by
+// a second launch over the whole GPU that starts with the list ready.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -23,54 +23,115 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kCtas = 8;         // CTAs of the scanning cluster
 constexpr int kScanThreads = 1024;
 constexpr int kScanWarps = kScanThreads / 32;
+constexpr int kManyCtas = 8;     // of the cluster that scans a large pool
+// One CTA scans a pool this small: what the cluster's barriers cost is more than
+// what its seven other CTAs save (20000 pages, 256 sequences: 9.3 -> 5.9 us).
+constexpr int kOneCtaPages = 16384;
+constexpr int kOneCtaItems = 1024;
 
 int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
 __device__ __forceinline__ uint32_t lanes_below(int lane) { return (1u << lane) - 1u; }
 
-// A warp's contiguous part of [0, n), split over the cluster's warps.
+// A warp's contiguous part of [0, n), split over the warps of C CTAs.
 struct Span {
   int lo, hi;
 };
+template <int C>
 __device__ __forceinline__ Span span_of(int n, int rank, int warp) {
-  const long long w = (long long)rank * kScanWarps + warp, all = kCtas * kScanWarps;
+  const long long w = (long long)rank * kScanWarps + warp, all = C * kScanWarps;
   return Span{(int)((long long)n * w / all), (int)((long long)n * (w + 1) / all)};
 }
 
-// Exclusive sum over the cluster's warps, in order, of one count each; *total
-// over all.  `mine` is [kScanWarps] of shared memory, `ctas` [kCtas] that every
-// CTA of the cluster writes its own sum into.  begun: the cluster barrier that the
-// kernel arrived at when it started is still to be waited for.
-__device__ __forceinline__ int cluster_prefix(cg::cluster_group& cluster, bool begun, int count,
-                                              int* mine, int* ctas, int* total) {
-  const int rank = (int)cluster.block_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) mine[warp] = count;
-  __syncthreads();
-  int x = mine[lane];
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, off);
-    if (lane >= off) x += y;
-  }
-  const int before = __shfl_sync(0xffffffffu, x, warp) - count;
-  const int sum = __shfl_sync(0xffffffffu, x, 31);
-  // every CTA has started before another writes into its shared memory
-  if (begun) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  if (warp == 0 && lane < kCtas) cluster.map_shared_rank(ctas, lane)[rank] = sum;
-  cluster.sync();
-  int all = 0, ahead = 0;
-#pragma unroll
-  for (int r = 0; r < kCtas; ++r) {
-    const int c = ctas[r];
-    all += c;
-    ahead += r < rank ? c : 0;
-  }
-  *total = all;
-  return ahead + before;
+// All threads of the C CTAs: what any of them wrote before, all see after.
+template <int C>
+__device__ __forceinline__ void sync_all() {
+  if (C == 1) __syncthreads();
+  else cg::this_cluster().sync();
 }
+
+// Exclusive sums over all warps, in order, of N counts each; total[] over all.
+// C > 1: the kernel arrived at the cluster's barrier when it started.
+template <int C, int N>
+struct Prefix {
+  int warps[N][kScanWarps], ctas[N][C];
+  __device__ __forceinline__ void operator()(const int (&count)[N], int (&before)[N],
+                                             int (&total)[N]) {
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane == 0) warps[i][warp] = count[i];
+    __syncthreads();
+    // every CTA has started before another writes into its shared memory
+    if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      int x = warps[i][lane];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += y;
+      }
+      before[i] = __shfl_sync(0xffffffffu, x, warp) - count[i];
+      total[i] = __shfl_sync(0xffffffffu, x, 31);
+      if (C > 1 && warp == i && lane < C) cluster.map_shared_rank(ctas[i], lane)[rank] = total[i];
+    }
+    if (C == 1) return;
+    cluster.sync();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      total[i] = 0;
+#pragma unroll
+      for (int r = 0; r < C; ++r) {
+        const int c = ctas[i][r];
+        total[i] += c;
+        before[i] += r < rank ? c : 0;
+      }
+    }
+  }
+};
+
+// The counts of a warp's span of pages as bits, one word of 32 pages at a time;
+// the first kWords stay in registers for a second look.
+struct PageBits {
+  static constexpr int kWords = 16;
+  uint32_t kept[kWords];
+  const int32_t* refs;
+  Span s;
+  int lane;
+  __device__ __forceinline__ uint32_t look(int k) const {  // pages in use, of word k
+    const int i = s.lo + 32 * k + lane;
+    return __ballot_sync(0xffffffffu, i < s.hi && refs[i] > 0);
+  }
+  __device__ __forceinline__ int words() const { return (s.hi - s.lo + 31) >> 5; }
+  __device__ __forceinline__ uint32_t valid(int k) const {
+    const int n = s.hi - s.lo - 32 * k;
+    return n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+  }
+  // f(k, bits) for every word; `again`: a second time.
+  template <bool AGAIN, typename F>
+  __device__ __forceinline__ void each(F f) {
+    const int n = words();
+    if (!AGAIN) {
+      int32_t x[kWords];
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        const int i = s.lo + 32 * k + lane;
+        x[k] = k < n && i < s.hi ? refs[i] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) kept[k] = __ballot_sync(0xffffffffu, x[k] > 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kWords; ++k)
+      if (k < n) f(k, kept[k]);
+#pragma unroll 4
+    for (int k = kWords; k < n; ++k) f(k, look(k));
+  }
+};
 
 // ---------------------------------------------------------------- reserve --
 
@@ -90,100 +151,114 @@ struct ReserveParams {
 };
 constexpr int kNothing = -2;  // an item that needs no page
 
-// The item's entry if it needs a page: -1 (it has none) or the page that others
-// share; kNothing if it needs none.
-__device__ __forceinline__ int item_info(const ReserveParams& p, int b, int jj) {
-  const int n = p.lengths ? p.lengths[b] : p.S, pos = p.positions[b];
-  if (n <= 0 || n > p.S || n > p.cap || !rows_in_cache(pos, n - 1, p.cap)) return kNothing;
-  const int j = (pos >> p.lp) + jj;
-  if (j > (pos + n - 1) >> p.lp) return kNothing;
-  const int page = p.table[(size_t)b * p.M + j];
-  if (page < 0 || page >= p.P) return -1;
-  return p.refs[page] > 1 ? page : kNothing;
+// An item is one of the `per` pages that a sequence's new rows can touch.
+struct Item {
+  int was;  // its entry if it needs a page: -1 (it has none) or the page that others share
+  int pos;
+  __device__ __forceinline__ Item(const ReserveParams& p, int b, int jj) {
+    const int n = p.lengths ? p.lengths[b] : p.S;
+    pos = p.positions[b];
+    was = kNothing;
+    if (n <= 0 || n > p.S || n > p.cap || !rows_in_cache(pos, n - 1, p.cap)) return;
+    const int j = (pos >> p.lp) + jj;
+    if (j > (pos + n - 1) >> p.lp) return;
+    const int page = p.table[(size_t)b * p.M + j];
+    if (page < 0 || page >= p.P) was = -1;
+    else if (p.refs[page] > 1) was = page;
+  }
+};
+
+// The item's page changes hands.
+__device__ __forceinline__ void give(const ReserveParams& p, int b, int jj, int was, int pos,
+                                     int page) {
+  p.table[(size_t)b * p.M + (pos >> p.lp) + jj] = page;
+  p.refs[page] = 1;
+  if (was < 0) return;
+  atomicSub(&p.refs[was], 1);
+  const int rows = pos & ((1 << p.lp) - 1);
+  if (jj == 0 && rows > 0) p.copies[atomicAdd(p.n_copies, 1)] = make_int4(was, page, rows, 0);
 }
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kScanThreads, 1)
-    pages_reserve_kernel(const ReserveParams p) {
-  __shared__ int warps[2][kScanWarps], ctas[2][kCtas];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), tid = threadIdx.x;
+// C CTAs, a cluster.  Three steps, a barrier between them: count the free pages
+// and the needed ones; list the free pages that are wanted and how far the
+// sequences reach; give the pages out.
+template <int C>
+__global__ void __launch_bounds__(kScanThreads, 1) pages_reserve_kernel(const ReserveParams p) {
+  __shared__ Prefix<C, 2> prefix;
+  const int rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank(), tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   grid_dependency_wait();
   grid_dependents_launch();
-  const int items = p.B * p.per;
-  const Span fs = span_of(p.P, rank, warp), is = span_of(items, rank, warp);
+  const Span is = span_of<C>(p.B * p.per, rank, warp);
   if (rank == 0 && tid == 0) *p.n_copies = 0;
 
-  // how many pages are free, and how many are needed
-  int n_free = 0, n_need = 0;
-  for (int i0 = is.lo; i0 < is.hi; i0 += 32) {
+  // the first 32 items of a warp stay in registers, the others in `info`
+  PageBits bits{{}, p.refs, span_of<C>(p.P, rank, warp), lane};
+  int first = kNothing, pos0 = 0, count[2] = {0, 0};
+  if (is.lo + lane < is.hi) {
+    const int b = (is.lo + lane) / p.per;
+    const Item x(p, b, is.lo + lane - b * p.per);
+    first = x.was;
+    pos0 = x.pos;
+  }
+  bits.each<false>([&](int k, uint32_t used) { count[0] += __popc(~used & bits.valid(k)); });
+  count[1] = __popc(__ballot_sync(0xffffffffu, first != kNothing));
+  for (int i0 = is.lo + 32; i0 < is.hi; i0 += 32) {
     const int i = i0 + lane;
-    int x = kNothing;
+    int was = kNothing;
     if (i < is.hi) {
       const int b = i / p.per;
-      x = item_info(p, b, i - b * p.per);
-      p.info[i] = x;
+      was = Item(p, b, i - b * p.per).was;
+      p.info[i] = was;
     }
-    n_need += __popc(__ballot_sync(0xffffffffu, x != kNothing));
+    count[1] += __popc(__ballot_sync(0xffffffffu, was != kNothing));
   }
-#pragma unroll 4
-  for (int i0 = fs.lo; i0 < fs.hi; i0 += 32) {
-    const int i = i0 + lane;
-    n_free += __popc(__ballot_sync(0xffffffffu, i < fs.hi && p.refs[i] <= 0));
-  }
-  int free_all, need_all;
-  int at_free = cluster_prefix(cluster, true, n_free, warps[0], ctas[0], &free_all);
-  int at_need = cluster_prefix(cluster, false, n_need, warps[1], ctas[1], &need_all);
+  int before[2], total[2];
+  prefix(count, before, total);
+  const int n_free = total[0], n_need = total[1];
 
-  // the free pages that are wanted, and how far the sequences reach
-#pragma unroll 4
-  for (int i0 = fs.lo; i0 < fs.hi && at_free < need_all; i0 += 32) {
-    const int i = i0 + lane;
-    const bool is_free = i < fs.hi && p.refs[i] <= 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, is_free);
-    const int k = at_free + __popc(m & lanes_below(lane));
-    if (is_free && k < need_all) p.list[k] = i;
-    at_free += __popc(m);
-  }
-  {
-    int at = at_need;
-    for (int i0 = is.lo; i0 < is.hi; i0 += 32) {
-      const int i = i0 + lane;
-      const bool need = i < is.hi && p.info[i] != kNothing;
-      const uint32_t m = __ballot_sync(0xffffffffu, need);
-      const int k = at + __popc(m & lanes_below(lane));
-      if (i < is.hi) {
-        const int b = i / p.per, jj = i - b * p.per;
-        if (jj == 0) p.reach[b].x = k;
-        if (jj == p.per - 1) p.reach[b].y = k + need;
-      }
-      at += __popc(m);
-    }
-  }
-  cluster.sync();
-
-  // the pages change hands
+  int at = before[0];
+  bits.each<true>([&](int k, uint32_t used) {
+    const uint32_t m = ~used & bits.valid(k);
+    const int to = at + __popc(m & lanes_below(lane));
+    if ((m >> lane & 1) && to < n_need) p.list[to] = bits.s.lo + 32 * k + lane;
+    at += __popc(m);
+  });
+  at = before[1];
+  int k0 = 0;  // of the first item
   for (int i0 = is.lo; i0 < is.hi; i0 += 32) {
+    const int i = i0 + lane;
+    const bool need = (i0 == is.lo ? first : i < is.hi ? p.info[i] : kNothing) != kNothing;
+    const uint32_t m = __ballot_sync(0xffffffffu, need);
+    const int k = at + __popc(m & lanes_below(lane));
+    if (i0 == is.lo) k0 = k;
+    if (i < is.hi) {
+      const int b = i / p.per, jj = i - b * p.per;
+      if (jj == 0) p.reach[b].x = k;
+      if (jj == p.per - 1) p.reach[b].y = k + need;
+    }
+    at += __popc(m);
+  }
+  sync_all<C>();
+
+  // a sequence gets its pages if there are enough for it and those before it
+  if (first != kNothing) {
+    const int b = (is.lo + lane) / p.per, jj = is.lo + lane - b * p.per;
+    if ((p.per == 1 ? k0 + 1 : p.reach[b].y) <= n_free) give(p, b, jj, first, pos0, p.list[k0]);
+  }
+  at = before[1] + __popc(__ballot_sync(0xffffffffu, first != kNothing));
+  for (int i0 = is.lo + 32; i0 < is.hi; i0 += 32) {
     const int i = i0 + lane;
     const int was = i < is.hi ? p.info[i] : kNothing;
     const uint32_t m = __ballot_sync(0xffffffffu, was != kNothing);
-    const int k = at_need + __popc(m & lanes_below(lane));
-    at_need += __popc(m);
+    const int k = at + __popc(m & lanes_below(lane));
+    at += __popc(m);
     if (was == kNothing) continue;
     const int b = i / p.per, jj = i - b * p.per;
-    if (p.reach[b].y > free_all) continue;  // the pool is too small for this sequence
-    const int page = p.list[k], pos = p.positions[b];
-    p.table[(size_t)b * p.M + (pos >> p.lp) + jj] = page;
-    p.refs[page] = 1;
-    if (was >= 0) {
-      atomicSub(&p.refs[was], 1);
-      const int rows = pos & ((1 << p.lp) - 1);
-      if (jj == 0 && rows > 0)
-        p.copies[atomicAdd(p.n_copies, 1)] = make_int4(was, page, rows, 0);
-    }
+    if (p.reach[b].y <= n_free) give(p, b, jj, was, p.positions[b], p.list[k]);
   }
-  for (int b = rank * kScanThreads + tid; b < p.B; b += kCtas * kScanThreads) {
+  for (int b = rank * kScanThreads + tid; b < p.B; b += C * kScanThreads) {
     const int n = p.lengths ? p.lengths[b] : p.S, pos = p.positions[b];
     int t = 0;
     if (n != 0) {
@@ -192,7 +267,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kScanThreads, 1)
         t = -1;
       } else {
         const int2 r = p.reach[b];
-        t = r.y == r.x ? 0 : r.y <= free_all ? r.y - r.x : -1;
+        t = r.y == r.x ? 0 : r.y <= n_free ? r.y - r.x : -1;
       }
     }
     p.taken[b] = t;
@@ -201,84 +276,103 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kScanThreads, 1)
 
 // ------------------------------------------------------------------ copies --
 
-// `rows` rows of one operand and head of page `from` to page `to`, by a warp.
+// Rows r0 .. r1 - 1 (16 at most) of one operand and head of page `from` to page
+// `to`, by a warp: all of a lane's loads (four or eight) are under way at once.
 __device__ __forceinline__ void copy_rows(uint8_t* base, const PagedPool& pool, int h, int from,
-                                          int to, int rows, int lane) {
+                                          int to, int r0, int r1, int lane) {
   const int lv = pool.D == 128 ? 4 : 3;
-  const int vecs = rows << lv;
+  const int vecs = (r1 - r0) << lv;
   const long long rs = pool.row_stride >> 3;
-  const uint4* src = reinterpret_cast<const uint4*>(base) +
-                     ((from * pool.page_stride + h * pool.head_stride) >> 3);
-  uint4* dst = reinterpret_cast<uint4*>(base) +
-               ((to * pool.page_stride + h * pool.head_stride) >> 3);
-  for (int j0 = lane; j0 < vecs; j0 += 256) {
-    uint4 x[8];
+  const long long in = (h * pool.head_stride >> 3) + r0 * rs;
+  const uint4* src = reinterpret_cast<const uint4*>(base) + (from * pool.page_stride >> 3) + in;
+  uint4* dst = reinterpret_cast<uint4*>(base) + (to * pool.page_stride >> 3) + in;
+  uint4 x[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int j = j0 + 32 * u;
-      if (j < vecs) x[u] = src[(j >> lv) * rs + (j & ((1 << lv) - 1))];
-    }
+  for (int u = 0; u < 8; ++u) {
+    const int j = lane + 32 * u;
+    if (j < vecs) x[u] = src[(j >> lv) * rs + (j & ((1 << lv) - 1))];
+  }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int j = j0 + 32 * u;
-      if (j < vecs) dst[(j >> lv) * rs + (j & ((1 << lv) - 1))] = x[u];
-    }
+  for (int u = 0; u < 8; ++u) {
+    const int j = lane + 32 * u;
+    if (j < vecs) dst[(j >> lv) * rs + (j & ((1 << lv) - 1))] = x[u];
   }
 }
 
 constexpr int kCopyThreads = 256;
-// A warp for each (copy, operand, head).
+// A warp for each (copy, operand, head, 16 rows).  (A warp for all rows of a
+// head: 64 copies of up to 127 rows, 8 heads: 10.5 us instead of 4.4.)
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_rows_kernel(
     PagedPool pool, const int* __restrict__ n_copies, const int4* __restrict__ copies) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const long long units = (long long)*n_copies * 2 * pool.Hkv;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, parts = pool.page >> 4, per = 2 * pool.Hkv * parts;
+  const long long units = (long long)*n_copies * per;
   for (long long u = ((long long)blockIdx.x * kCopyThreads + threadIdx.x) >> 5; u < units;
        u += (long long)gridDim.x * (kCopyThreads / 32)) {
-    const int c = (int)(u / (2 * pool.Hkv)), oh = (int)(u - (long long)c * 2 * pool.Hkv);
+    const int c = (int)(u / per);
+    int rest = (int)(u - (long long)c * per);
+    const int r0 = rest % parts * 16;
+    rest /= parts;
     const int4 x = copies[c];
-    copy_rows(oh & 1 ? pool.v : pool.k, pool, oh >> 1, x.x, x.y, x.z, lane);
+    if (r0 < x.z)
+      copy_rows(rest & 1 ? pool.v : pool.k, pool, rest >> 1, x.x, x.y, r0, min(r0 + 16, x.z),
+                lane);
   }
 }
 
 // -------------------------------------------------------------------- fork --
 
 // Row b becomes what row parents[b] was, cut to the pages of its first
-// lengths[b] rows.  A CTA takes `cols` columns of all rows, so that it has read
-// what it will write over: a column's entries depend on that column alone.
+// lengths[b] rows.  A CTA takes 8 or 32 columns of all rows, so that it has read
+// what it will write over: a column's entries depend on that column alone.  A
+// thread's first kForkRows rows stay in registers: all its loads are one round trip.
 constexpr int kForkThreads = 1024;
+constexpr int kForkRows = 4;
 __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(
     int32_t* __restrict__ table, int32_t* __restrict__ refs, const int32_t* __restrict__ parents,
     const int32_t* __restrict__ lengths, int B, int M, int P, int lp, int lc, uint32_t* status) {
-  extern __shared__ int32_t old[];  // [B][cols]
+  extern __shared__ int32_t old[];  // [B][columns]
   grid_dependency_wait();
   grid_dependents_launch();
-  const int cols = 1 << lc, j0 = blockIdx.x << lc;
-  const int col = threadIdx.x & (cols - 1), j = j0 + col;
+  const int col = threadIdx.x & ((1 << lc) - 1), j = (blockIdx.x << lc) + col;
   const int b0 = threadIdx.x >> lc, step = kForkThreads >> lc;
+  int was[kForkRows], from[kForkRows], kept[kForkRows];
+#pragma unroll
+  for (int k = 0; k < kForkRows; ++k) {
+    const int b = b0 + k * step;
+    was[k] = b < B && j < M ? table[(size_t)b * M + j] : -1;
+    from[k] = b < B ? parents[b] : -1;
+    kept[k] = lengths && b < B ? lengths[b] : 0x7fffffff;
+  }
+#pragma unroll
+  for (int k = 0; k < kForkRows; ++k)
+    if (b0 + k * step < B) old[((b0 + k * step) << lc) + col] = was[k];
 #pragma unroll 4
-  for (int b = b0; b < B; b += step)
+  for (int b = b0 + kForkRows * step; b < B; b += step)
     old[(b << lc) + col] = j < M ? table[(size_t)b * M + j] : -1;
   __syncthreads();
   if (j >= M) return;
-  for (int b = b0; b < B; b += step) {
-    int from = parents[b];
+  auto pass_on = [&](int b, int was, int from, int kept) {
     if (from < -1 || from >= B) {  // no such row: this one stays
       set_status(status, ATTN_DEV_BAD_PARENT);
       from = b;
     }
-    const int was = old[(b << lc) + col];
     int now = from < 0 ? -1 : old[(from << lc) + col];
-    if (lengths && (long long)j << lp >= lengths[b]) now = -1;
-    if (now == was) continue;
+    if ((long long)j << lp >= kept) now = -1;
+    if (now == was) return;
     table[(size_t)b * M + j] = now;
     if (now >= 0 && now < P) atomicAdd(&refs[now], 1);
     if (was >= 0 && was < P) atomicSub(&refs[was], 1);
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kForkRows; ++k)
+    if (b0 + k * step < B) pass_on(b0 + k * step, was[k], from[k], kept[k]);
+  for (int b = b0 + kForkRows * step; b < B; b += step)
+    pass_on(b, old[(b << lc) + col], parents[b], lengths ? lengths[b] : 0x7fffffff);
 }
 // Without parents: only entries past the kept rows are looked at.  A warp for
-// each row and 1024 columns.
+// 256 columns of a row, all of a lane's eight loads under way at once.
 __global__ void __launch_bounds__(256) pages_cut_kernel(int32_t* __restrict__ table,
                                                         int32_t* __restrict__ refs,
                                                         const int32_t* __restrict__ lengths, int B,
@@ -288,13 +382,19 @@ __global__ void __launch_bounds__(256) pages_cut_kernel(int32_t* __restrict__ ta
   const int lane = threadIdx.x & 31, b = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (b >= B) return;
   const int first = (int)(((long long)max(lengths[b], 0) + (1 << lp) - 1) >> lp);
-  const int j0 = blockIdx.x * 1024, j1 = min(j0 + 1024, M);
-#pragma unroll 8
-  for (int j = max(first, j0) + lane; j < j1; j += 32) {
-    const int was = table[(size_t)b * M + j];
-    if (was == -1) continue;
-    table[(size_t)b * M + j] = -1;
-    if (was >= 0 && was < P) atomicSub(&refs[was], 1);
+  const int j0 = blockIdx.x * 256 + lane;
+  int32_t* row = table + (size_t)b * M;
+  int was[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int j = j0 + 32 * k;
+    was[k] = j >= first && j < M ? row[j] : -1;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (was[k] == -1) continue;
+    row[j0 + 32 * k] = -1;
+    if (was[k] >= 0 && was[k] < P) atomicSub(&refs[was[k]], 1);
   }
 }
 
@@ -311,73 +411,92 @@ struct CompactParams {
 };
 
 // n pages are in use: the k-th of those at n or above goes to the k-th free
-// page below n.
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kScanThreads, 1)
-    pages_plan_kernel(const CompactParams p) {
-  __shared__ int warps[kScanWarps], ctas[kCtas];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), tid = threadIdx.x;
+// page below n.  C CTAs, a cluster.
+template <int C>
+__global__ void __launch_bounds__(kScanThreads, 1) pages_plan_kernel(const CompactParams p) {
+  __shared__ Prefix<C, 1> prefix;
+  const int rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank(), tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   grid_dependency_wait();
   grid_dependents_launch();
-  const Span s = span_of(p.P, rank, warp);
-  int count = 0;
-#pragma unroll 4
-  for (int i0 = s.lo; i0 < s.hi; i0 += 32) {
-    const int i = i0 + lane;
-    count += __popc(__ballot_sync(0xffffffffu, i < s.hi && p.refs[i] > 0));
-  }
-  int n;
-  int at = cluster_prefix(cluster, true, count, warps, ctas, &n);
-  for (int i0 = s.lo; i0 < s.hi; i0 += 32) {
-    const int i = i0 + lane;
-    const bool in = i < s.hi, used = in && p.refs[i] > 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, used);
-    const int before = at + __popc(m & lanes_below(lane));  // used pages before i
-    at += __popc(m);
-    if (!in) continue;
-    if (i == n) *p.n_moves = n - before;  // as many high pages as low holes
-    if (used) {
+  PageBits bits{{}, p.refs, span_of<C>(p.P, rank, warp), lane};
+  int count[1] = {0}, at[1], total[1];
+  bits.each<false>([&](int, uint32_t used) { count[0] += __popc(used); });
+  prefix(count, at, total);
+  const int n = total[0];
+  bits.each<true>([&](int k, uint32_t m) {
+    const int i = bits.s.lo + 32 * k + lane;
+    const int before = at[0] + __popc(m & lanes_below(lane));  // used pages before i
+    at[0] += __popc(m);
+    if (i >= bits.s.hi) return;
+    if (i == n) {
+      p.n_moves[0] = n - before;  // as many high pages as low holes
+      p.n_moves[1] = n;
+    }
+    if (m >> lane & 1) {
       if (i >= n) p.from[before] = i;
       else p.map[i] = i;
     } else {
       if (i < n) p.to[i - before] = i;
       p.map[i] = -1;
     }
-  }
-  if (n == p.P && rank == 0 && tid == 0) *p.n_moves = 0;  // no page is free
-  cluster.sync();
+  });
+  if (n == p.P && rank == 0 && tid == 0) p.n_moves[0] = 0;  // no page is free
+  sync_all<C>();
   const int moves = *(volatile int*)p.n_moves;
-  for (int k = rank * kScanThreads + tid; k < moves; k += kCtas * kScanThreads) {
+  for (int k = rank * kScanThreads + tid; k < moves; k += C * kScanThreads) {
     const int src = p.from[n - moves + k], dst = p.to[k];
     p.map[src] = dst;
     p.refs[dst] = p.refs[src];
     p.refs[src] = 0;
-    if (k == 0) p.n_moves[1] = n;
   }
 }
 
-// The moved pages' rows, a warp for each (move, operand, head), and the table.
+// The moved pages' rows, a warp for each (move, operand, head, 16 rows), and the table.
 __global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(CompactParams p, PagedPool pool) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int moves = p.n_moves[0], n = p.n_moves[1];
-  const int lane = threadIdx.x & 31;
+  if (moves == 0) return;  // (nothing in the table changes either)
+  const int lane = threadIdx.x & 31, parts = pool.page >> 4, per = 2 * pool.Hkv * parts;
   const long long thread = (long long)blockIdx.x * kCopyThreads + threadIdx.x;
   const long long threads = (long long)gridDim.x * kCopyThreads;
-  const long long units = (long long)moves * 2 * pool.Hkv;
-  for (long long u = thread >> 5; u < units; u += threads >> 5) {
-    const int c = (int)(u / (2 * pool.Hkv)), oh = (int)(u - (long long)c * 2 * pool.Hkv);
-    copy_rows(oh & 1 ? pool.v : pool.k, pool, oh >> 1, p.from[n - moves + c], p.to[c], pool.page,
-              lane);
-  }
   for (long long i = thread; i < (long long)p.B * p.M; i += threads) {
     const int e = p.table[i];
-    if (e < 0 || e >= p.P) continue;
-    const int now = p.map[e];
-    if (now != e) p.table[i] = now;
+    if (e < n || e >= p.P) continue;  // pages below n stay
+    p.table[i] = p.map[e];
   }
+  const long long units = (long long)moves * per;
+  for (long long u = thread >> 5; u < units; u += threads >> 5) {
+    const int c = (int)(u / per);
+    int rest = (int)(u - (long long)c * per);
+    const int r0 = rest % parts * 16;
+    rest /= parts;
+    copy_rows(rest & 1 ? pool.v : pool.k, pool, rest >> 1, p.from[n - moves + c], p.to[c], r0,
+              r0 + 16, lane);
+  }
+}
+
+// A scanning kernel on one CTA or a cluster of kManyCtas.
+template <typename P>
+cudaError_t launch_scan(void (*one)(P), void (*many)(P), bool small, cudaStream_t stream,
+                        const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(small ? 1 : kManyCtas);
+  cfg.blockDim = dim3(kScanThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kManyCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = small ? 1 : 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, small ? one : many, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t sm_count(int* sms) {
@@ -432,10 +551,11 @@ cudaError_t launch_pages_reserve(int32_t* table, int32_t* refs, const int32_t* p
   p.list = p.info + (size_t)B * p.per;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
+  const bool small = pool.P <= kOneCtaPages && (long long)B * p.per <= kOneCtaItems;
   if (e == cudaSuccess)
-    e = launch_pdl(pages_reserve_kernel, dim3(kCtas), dim3(kScanThreads), 0, stream, p);
+    e = launch_scan(pages_reserve_kernel<1>, pages_reserve_kernel<kManyCtas>, small, stream, p);
   if (e != cudaSuccess) return e;
-  const long long warps = (long long)B * 2 * pool.Hkv;
+  const long long warps = (long long)B * 2 * pool.Hkv * (pool.page >> 4);
   const long long blocks = (warps * 32 + kCopyThreads - 1) / kCopyThreads;
   return launch_pdl(pages_copy_rows_kernel, dim3((unsigned)min(blocks, (long long)sms * 8)),
                     dim3(kCopyThreads), 0, stream, pool, (const int*)p.n_copies,
@@ -447,15 +567,19 @@ cudaError_t launch_pages_fork(int32_t* table, int32_t* refs, const int32_t* pare
                               void* workspace, cudaStream_t stream) {
   if (!parents) {
     if (!lengths) return cudaSuccess;
-    return launch_pdl(pages_cut_kernel, dim3((M + 1023) / 1024, (B + 7) / 8), dim3(256), 0, stream,
+    return launch_pdl(pages_cut_kernel, dim3((M + 255) / 256, (B + 7) / 8), dim3(256), 0, stream,
                       table, refs, lengths, B, M, P, log2_of(page));
   }
-  // 128-byte pieces of rows; 32-byte ones where that many rows would not fit
-  const int lc = B <= 1024 ? 5 : 3;
-  const size_t smem = ((size_t)B << lc) * 4;
-  cudaError_t e = cudaFuncSetAttribute(pages_fork_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+  // 128-byte pieces of rows; 32-byte ones where that many rows would not fit, or
+  // where that makes CTAs for SMs that would have none
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             128 * 1024);
   if (e != cudaSuccess) return e;
+  const int lc = B > 1024 || M <= 8 * sms ? 3 : 5;
+  const size_t smem = ((size_t)B << lc) * 4;
   return launch_pdl(pages_fork_kernel, dim3((M + (1 << lc) - 1) >> lc), dim3(kForkThreads), smem,
                     stream, table, refs, parents, lengths, B, M, P, log2_of(page), lc,
                     reinterpret_cast<uint32_t*>(workspace));
@@ -478,7 +602,8 @@ cudaError_t launch_pages_compact(int32_t* table, int32_t* refs, const PagedPool&
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e == cudaSuccess)
-    e = launch_pdl(pages_plan_kernel, dim3(kCtas), dim3(kScanThreads), 0, stream, p);
+    e = launch_scan(pages_plan_kernel<1>, pages_plan_kernel<kManyCtas>, pool.P <= kOneCtaPages,
+                    stream, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(pages_move_kernel, dim3(sms * 8), dim3(kCopyThreads), 0, stream, p, pool);
 }
