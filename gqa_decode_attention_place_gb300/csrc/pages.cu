@@ -14,6 +14,8 @@
 // a second launch over the whole GPU that starts with the list ready.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
@@ -26,10 +28,11 @@ namespace cg = cooperative_groups;
 constexpr int kScanThreads = 1024;
 constexpr int kScanWarps = kScanThreads / 32;
 constexpr int kManyCtas = 8;     // of the cluster that scans a large pool
-// One CTA scans a pool this small: what the cluster's barriers cost is more than
-// what its seven other CTAs save (20000 pages, 256 sequences: 9.3 -> 5.9 us).
-constexpr int kOneCtaPages = 16384;
-constexpr int kOneCtaItems = 1024;
+constexpr int kCopyThreads = 256;
+// Up to these sizes a call is one launch: every CTA scans the counts for itself.
+constexpr int kSoloPages = 16384;     // reserve
+constexpr int kSoloItems = 1024;
+constexpr int kSoloMoves = 8192;      // pages of a pool to compact
 
 int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
@@ -102,36 +105,73 @@ struct PageBits {
   const int32_t* refs;
   Span s;
   int lane;
+  // The first words' loads, to be under way beside others; their values become
+  // bits in settle().
+  __device__ __forceinline__ PageBits(const int32_t* refs_, Span s_, int lane_)
+      : refs(refs_), s(s_), lane(lane_) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      const int i = s.lo + 32 * k + lane;
+      kept[k] = i < s.hi ? (uint32_t)refs[i] : 0u;
+    }
+  }
+  __device__ __forceinline__ void settle() {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) kept[k] = __ballot_sync(0xffffffffu, (int)kept[k] > 0);
+  }
   __device__ __forceinline__ uint32_t look(int k) const {  // pages in use, of word k
     const int i = s.lo + 32 * k + lane;
     return __ballot_sync(0xffffffffu, i < s.hi && refs[i] > 0);
   }
-  __device__ __forceinline__ int words() const { return (s.hi - s.lo + 31) >> 5; }
   __device__ __forceinline__ uint32_t valid(int k) const {
     const int n = s.hi - s.lo - 32 * k;
     return n >= 32 ? 0xffffffffu : (1u << n) - 1u;
   }
-  // f(k, bits) for every word; `again`: a second time.
-  template <bool AGAIN, typename F>
-  __device__ __forceinline__ void each(F f) {
-    const int n = words();
-    if (!AGAIN) {
-      int32_t x[kWords];
-#pragma unroll
-      for (int k = 0; k < kWords; ++k) {
-        const int i = s.lo + 32 * k + lane;
-        x[k] = k < n && i < s.hi ? refs[i] : 0;
-      }
-#pragma unroll
-      for (int k = 0; k < kWords; ++k) kept[k] = __ballot_sync(0xffffffffu, x[k] > 0);
-    }
+  // f(k, bits) for every word, until it says false.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    const int n = (s.hi - s.lo + 31) >> 5;
+    bool on = true;
 #pragma unroll
     for (int k = 0; k < kWords; ++k)
-      if (k < n) f(k, kept[k]);
+      if (on && k < n) on = f(k, kept[k]);
 #pragma unroll 4
-    for (int k = kWords; k < n; ++k) f(k, look(k));
+    for (int k = kWords; k < n && on; ++k) on = f(k, look(k));
   }
 };
+
+// Rows r0 .. r1 - 1 (16 at most) of one operand and head of page `from` to page
+// `to`, by a warp: all of a lane's loads (four or eight) are under way at once.
+__device__ __forceinline__ void copy_rows(uint8_t* base, const PagedPool& pool, int h, int from,
+                                          int to, int r0, int r1, int lane) {
+  const int lv = pool.D == 128 ? 4 : 3;
+  const int vecs = (r1 - r0) << lv;
+  const long long rs = pool.row_stride >> 3;
+  const long long in = (h * pool.head_stride >> 3) + r0 * rs;
+  const uint4* src = reinterpret_cast<const uint4*>(base) + (from * pool.page_stride >> 3) + in;
+  uint4* dst = reinterpret_cast<uint4*>(base) + (to * pool.page_stride >> 3) + in;
+  uint4 x[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int j = lane + 32 * u;
+    if (j < vecs) x[u] = src[(j >> lv) * rs + (j & ((1 << lv) - 1))];
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int j = lane + 32 * u;
+    if (j < vecs) dst[(j >> lv) * rs + (j & ((1 << lv) - 1))] = x[u];
+  }
+}
+
+// Thread 0 of a CTA that has read all it will: whether it is the last of the
+// grid's, and may write what others read.
+__device__ __forceinline__ bool last_to_read(uint32_t* ticket) {
+  __threadfence();  // (the other threads' reads came before a barrier)
+  const bool last = atomicAdd(ticket, 1u) + 1 == gridDim.x;
+  if (last) *ticket = 0;
+  __threadfence();
+  return last;
+}
 
 // ---------------------------------------------------------------- reserve --
 
@@ -142,6 +182,7 @@ struct ReserveParams {
   const int32_t* lengths;
   int32_t* taken;
   uint32_t* status;
+  uint32_t* ticket;
   int* n_copies;
   int4* copies;    // (from, to, rows) in any order
   int2* reach;     // [B] needed pages before and up to a sequence
@@ -173,13 +214,94 @@ __device__ __forceinline__ void give(const ReserveParams& p, int b, int jj, int 
                                      int page) {
   p.table[(size_t)b * p.M + (pos >> p.lp) + jj] = page;
   p.refs[page] = 1;
-  if (was < 0) return;
-  atomicSub(&p.refs[was], 1);
-  const int rows = pos & ((1 << p.lp) - 1);
-  if (jj == 0 && rows > 0) p.copies[atomicAdd(p.n_copies, 1)] = make_int4(was, page, rows, 0);
+  if (was >= 0) atomicSub(&p.refs[was], 1);
+}
+// Rows to copy from the page `was` that item jj leaves: those before the new ones.
+__device__ __forceinline__ int copied(const ReserveParams& p, int jj, int was, int pos) {
+  return jj == 0 && was >= 0 ? pos & ((1 << p.lp) - 1) : 0;
+}
+// What a sequence took, of its needed pages' reach; sets the status of one that does not fit.
+__device__ __forceinline__ int taken_by(const ReserveParams& p, int n, int pos, int2 reach,
+                                        int n_free) {
+  if (n == 0) return 0;
+  if (n < 0 || n > p.S || n > p.cap || !rows_in_cache(pos, n - 1, p.cap)) {
+    set_status(p.status, ATTN_DEV_BAD_POSITION);
+    return -1;
+  }
+  return reach.y == reach.x ? 0 : reach.y <= n_free ? reach.y - reach.x : -1;
 }
 
-// C CTAs, a cluster.  Three steps, a barrier between them: count the free pages
+// A small pool: every CTA works out who gets what from the state as it was, an
+// item a thread, and copies its part of the rows; the last one to have read the
+// state changes it.  No CTA waits for another.  (One CTA's scan, then a launch of
+// copies: 8.4 us on the device for 256 sequences' step instead of 5.3, and 2 more
+// of the host's time.)
+__global__ void __launch_bounds__(kScanThreads, 1)
+    pages_reserve_solo_kernel(const ReserveParams p, const PagedPool pool) {
+  __shared__ Prefix<1, 2> prefix;
+  __shared__ int list[kSoloItems];
+  __shared__ int2 reach[kSoloItems];
+  __shared__ int4 copies[kSoloItems];  // by sequence: (from, to, rows)
+  __shared__ bool last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int items = p.B * p.per, b = tid / p.per, jj = tid - b * p.per;
+  int was = kNothing, pos = 0, n_b = 0, pos_b = 0;
+  PageBits bits(p.refs, span_of<1>(p.P, 0, warp), lane);
+  if (tid < p.B) {
+    n_b = p.lengths ? p.lengths[tid] : p.S;
+    pos_b = p.positions[tid];
+  }
+  if (tid < items) {
+    const Item x(p, b, jj);
+    was = x.was;
+    pos = x.pos;
+  }
+  bits.settle();
+  int count[2] = {0, 0}, before[2], total[2];
+  bits.each([&](int k, uint32_t used) {
+    count[0] += __popc(~used & bits.valid(k));
+    return true;
+  });
+  const uint32_t need = __ballot_sync(0xffffffffu, was != kNothing);
+  count[1] = __popc(need);
+  prefix(count, before, total);
+  if (tid == 0) last = last_to_read(p.ticket);  // (this CTA has read all of the state)
+  bits.each([&](int k, uint32_t used) {
+    if (before[0] >= total[1]) return false;  // no more are wanted
+    const uint32_t m = ~used & bits.valid(k);
+    const int to = before[0] + __popc(m & lanes_below(lane));
+    if ((m >> lane & 1) && to < total[1]) list[to] = bits.s.lo + 32 * k + lane;
+    before[0] += __popc(m);
+    return true;
+  });
+  const int k = before[1] + __popc(need & lanes_below(lane));
+  if (tid < items) {
+    if (jj == 0) reach[b].x = k;
+    if (jj == p.per - 1) reach[b].y = k + (was != kNothing);
+  }
+  __syncthreads();
+  // a sequence gets its pages if there are enough for it and those before it
+  const bool given = was != kNothing && reach[b].y <= total[0];
+  const int page = given ? list[k] : -1;
+  const int rows = given ? copied(p, jj, was, pos) : 0;
+  if (tid < items && jj == 0) copies[b] = make_int4(was, page, rows, 0);
+  const bool some = __syncthreads_or(rows > 0);
+  const int parts = pool.page >> 4, per = 2 * pool.Hkv * parts;
+  for (int u = blockIdx.x * kScanWarps + warp; some && u < p.B * per;
+       u += gridDim.x * kScanWarps) {
+    const int c = u / per, rest = u - c * per, r0 = rest % parts * 16, oh = rest / parts;
+    const int4 x = copies[c];
+    if (r0 < x.z)
+      copy_rows(oh & 1 ? pool.v : pool.k, pool, oh >> 1, x.x, x.y, r0, min(r0 + 16, x.z), lane);
+  }
+  if (!last) return;
+  if (given) give(p, b, jj, was, pos, page);
+  if (tid < p.B) p.taken[tid] = taken_by(p, n_b, pos_b, reach[tid], total[0]);
+}
+
+// A larger one: C CTAs, a cluster.  Three steps, a barrier between them: count the free pages
 // and the needed ones; list the free pages that are wanted and how far the
 // sequences reach; give the pages out.
 template <int C>
@@ -194,7 +316,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_reserve_kernel(const Re
   if (rank == 0 && tid == 0) *p.n_copies = 0;
 
   // the first 32 items of a warp stay in registers, the others in `info`
-  PageBits bits{{}, p.refs, span_of<C>(p.P, rank, warp), lane};
+  PageBits bits(p.refs, span_of<C>(p.P, rank, warp), lane);
   int first = kNothing, pos0 = 0, count[2] = {0, 0};
   if (is.lo + lane < is.hi) {
     const int b = (is.lo + lane) / p.per;
@@ -202,7 +324,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_reserve_kernel(const Re
     first = x.was;
     pos0 = x.pos;
   }
-  bits.each<false>([&](int k, uint32_t used) { count[0] += __popc(~used & bits.valid(k)); });
+  bits.settle();
+  bits.each([&](int k, uint32_t used) {
+    count[0] += __popc(~used & bits.valid(k));
+    return true;
+  });
   count[1] = __popc(__ballot_sync(0xffffffffu, first != kNothing));
   for (int i0 = is.lo + 32; i0 < is.hi; i0 += 32) {
     const int i = i0 + lane;
@@ -219,11 +345,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_reserve_kernel(const Re
   const int n_free = total[0], n_need = total[1];
 
   int at = before[0];
-  bits.each<true>([&](int k, uint32_t used) {
+  bits.each([&](int k, uint32_t used) {
+    if (at >= n_need) return false;  // no more are wanted
     const uint32_t m = ~used & bits.valid(k);
     const int to = at + __popc(m & lanes_below(lane));
     if ((m >> lane & 1) && to < n_need) p.list[to] = bits.s.lo + 32 * k + lane;
     at += __popc(m);
+    return true;
   });
   at = before[1];
   int k0 = 0;  // of the first item
@@ -242,10 +370,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_reserve_kernel(const Re
   }
   sync_all<C>();
 
-  // a sequence gets its pages if there are enough for it and those before it
+  auto hand_over = [&](int b, int jj, int was, int pos, int page) {
+    give(p, b, jj, was, pos, page);
+    const int rows = copied(p, jj, was, pos);
+    if (rows > 0) p.copies[atomicAdd(p.n_copies, 1)] = make_int4(was, page, rows, 0);
+  };
   if (first != kNothing) {
     const int b = (is.lo + lane) / p.per, jj = is.lo + lane - b * p.per;
-    if ((p.per == 1 ? k0 + 1 : p.reach[b].y) <= n_free) give(p, b, jj, first, pos0, p.list[k0]);
+    if (p.reach[b].y <= n_free) hand_over(b, jj, first, pos0, p.list[k0]);
   }
   at = before[1] + __popc(__ballot_sync(0xffffffffu, first != kNothing));
   for (int i0 = is.lo + 32; i0 < is.hi; i0 += 32) {
@@ -256,50 +388,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_reserve_kernel(const Re
     at += __popc(m);
     if (was == kNothing) continue;
     const int b = i / p.per, jj = i - b * p.per;
-    if (p.reach[b].y <= n_free) give(p, b, jj, was, p.positions[b], p.list[k]);
+    if (p.reach[b].y <= n_free) hand_over(b, jj, was, p.positions[b], p.list[k]);
   }
-  for (int b = rank * kScanThreads + tid; b < p.B; b += C * kScanThreads) {
-    const int n = p.lengths ? p.lengths[b] : p.S, pos = p.positions[b];
-    int t = 0;
-    if (n != 0) {
-      if (n < 0 || n > p.S || n > p.cap || !rows_in_cache(pos, n - 1, p.cap)) {
-        set_status(p.status, ATTN_DEV_BAD_POSITION);
-        t = -1;
-      } else {
-        const int2 r = p.reach[b];
-        t = r.y == r.x ? 0 : r.y <= n_free ? r.y - r.x : -1;
-      }
-    }
-    p.taken[b] = t;
-  }
+  for (int b = rank * kScanThreads + tid; b < p.B; b += C * kScanThreads)
+    p.taken[b] = taken_by(p, p.lengths ? p.lengths[b] : p.S, p.positions[b], p.reach[b], n_free);
 }
 
 // ------------------------------------------------------------------ copies --
 
-// Rows r0 .. r1 - 1 (16 at most) of one operand and head of page `from` to page
-// `to`, by a warp: all of a lane's loads (four or eight) are under way at once.
-__device__ __forceinline__ void copy_rows(uint8_t* base, const PagedPool& pool, int h, int from,
-                                          int to, int r0, int r1, int lane) {
-  const int lv = pool.D == 128 ? 4 : 3;
-  const int vecs = (r1 - r0) << lv;
-  const long long rs = pool.row_stride >> 3;
-  const long long in = (h * pool.head_stride >> 3) + r0 * rs;
-  const uint4* src = reinterpret_cast<const uint4*>(base) + (from * pool.page_stride >> 3) + in;
-  uint4* dst = reinterpret_cast<uint4*>(base) + (to * pool.page_stride >> 3) + in;
-  uint4 x[8];
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int j = lane + 32 * u;
-    if (j < vecs) x[u] = src[(j >> lv) * rs + (j & ((1 << lv) - 1))];
-  }
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int j = lane + 32 * u;
-    if (j < vecs) dst[(j >> lv) * rs + (j & ((1 << lv) - 1))] = x[u];
-  }
-}
-
-constexpr int kCopyThreads = 256;
 // A warp for each (copy, operand, head, 16 rows).  (A warp for all rows of a
 // head: 64 copies of up to 127 rows, 8 heads: 10.5 us instead of 4.4.)
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_rows_kernel(
@@ -404,11 +500,73 @@ struct CompactParams {
   int32_t* table;
   int32_t* refs;
   int32_t* map;
+  uint32_t* ticket;
   int* n_moves;
   int32_t* from;  // [P] used pages by how many come before them
   int32_t* to;    // [P] free pages by how many come before them
   int B, M, P;
 };
+
+// A small pool in one launch: every CTA works the moves out for itself, and does
+// its part of the rows and of the table; the last one to have read the counts
+// changes them.
+__global__ void __launch_bounds__(kScanThreads, 1)
+    pages_compact_solo_kernel(const CompactParams p, const PagedPool pool) {
+  __shared__ Prefix<1, 1> prefix;
+  // from: the high pages from the last on; to: the free pages below n
+  __shared__ uint16_t from[kSoloMoves / 2], to[kSoloMoves / 2], where[kSoloMoves];
+  __shared__ int holes;  // free pages below n
+  __shared__ bool last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  PageBits bits(p.refs, span_of<1>(p.P, 0, warp), lane);
+  int count[1] = {0}, at[1], total[1];
+  bits.settle();
+  bits.each([&](int, uint32_t used) {
+    count[0] += __popc(used);
+    return true;
+  });
+  if (tid == 0) holes = 0;
+  prefix(count, at, total);
+  const int n = total[0];
+  if (tid == 0) last = last_to_read(p.ticket);  // (this CTA has read all of the counts)
+  bits.each([&](int k, uint32_t m) {
+    const int i = bits.s.lo + 32 * k + lane;
+    const int before = at[0] + __popc(m & lanes_below(lane));  // used pages before i
+    at[0] += __popc(m);
+    if (i >= bits.s.hi) return true;
+    if (i == n) holes = n - before;
+    const bool used = m >> lane & 1;
+    if (used && i >= n) from[n - 1 - before] = (uint16_t)i;
+    if (!used && i < n) to[i - before] = (uint16_t)i;
+    where[i] = used ? (uint16_t)i : 0xffff;
+    return true;
+  });
+  __syncthreads();
+  const int moves = holes;
+  for (int k = tid; k < moves; k += kScanThreads) where[from[moves - 1 - k]] = to[k];
+  __syncthreads();
+  const int thread = blockIdx.x * kScanThreads + tid, threads = gridDim.x * kScanThreads;
+  for (int i = thread; i < p.P; i += threads) p.map[i] = where[i] == 0xffff ? -1 : where[i];
+  if (moves == 0) return;
+  for (long long i = thread; i < (long long)p.B * p.M; i += threads) {
+    const int e = p.table[i];
+    if (e >= n && e < p.P) p.table[i] = where[e] == 0xffff ? -1 : where[e];
+  }
+  const int parts = pool.page >> 4, per = 2 * pool.Hkv * parts;
+  for (int u = thread >> 5; u < moves * per; u += threads >> 5) {
+    const int c = u / per, rest = u - c * per, r0 = rest % parts * 16, oh = rest / parts;
+    copy_rows(oh & 1 ? pool.v : pool.k, pool, oh >> 1, from[moves - 1 - c], to[c], r0, r0 + 16,
+              lane);
+  }
+  if (!last) return;
+  for (int k = tid; k < moves; k += kScanThreads) {
+    const int src = from[moves - 1 - k], dst = to[k];
+    p.refs[dst] = p.refs[src];
+    p.refs[src] = 0;
+  }
+}
 
 // n pages are in use: the k-th of those at n or above goes to the k-th free
 // page below n.  C CTAs, a cluster.
@@ -420,16 +578,20 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_plan_kernel(const Compa
   if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   grid_dependency_wait();
   grid_dependents_launch();
-  PageBits bits{{}, p.refs, span_of<C>(p.P, rank, warp), lane};
+  PageBits bits(p.refs, span_of<C>(p.P, rank, warp), lane);
   int count[1] = {0}, at[1], total[1];
-  bits.each<false>([&](int, uint32_t used) { count[0] += __popc(used); });
+  bits.settle();
+  bits.each([&](int, uint32_t used) {
+    count[0] += __popc(used);
+    return true;
+  });
   prefix(count, at, total);
   const int n = total[0];
-  bits.each<true>([&](int k, uint32_t m) {
+  bits.each([&](int k, uint32_t m) {
     const int i = bits.s.lo + 32 * k + lane;
     const int before = at[0] + __popc(m & lanes_below(lane));  // used pages before i
     at[0] += __popc(m);
-    if (i >= bits.s.hi) return;
+    if (i >= bits.s.hi) return true;
     if (i == n) {
       p.n_moves[0] = n - before;  // as many high pages as low holes
       p.n_moves[1] = n;
@@ -441,6 +603,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_plan_kernel(const Compa
       if (i < n) p.to[i - before] = i;
       p.map[i] = -1;
     }
+    return true;
   });
   if (n == p.P && rank == 0 && tid == 0) p.n_moves[0] = 0;  // no page is free
   sync_all<C>();
@@ -478,12 +641,11 @@ __global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(CompactParams 
   }
 }
 
-// A scanning kernel on one CTA or a cluster of kManyCtas.
+// A scanning kernel on a cluster of kManyCtas.
 template <typename P>
-cudaError_t launch_scan(void (*one)(P), void (*many)(P), bool small, cudaStream_t stream,
-                        const P& p) {
+cudaError_t launch_scan(void (*kernel)(P), cudaStream_t stream, const P& p) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(small ? 1 : kManyCtas);
+  cfg.gridDim = dim3(kManyCtas);
   cfg.blockDim = dim3(kScanThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -494,15 +656,29 @@ cudaError_t launch_scan(void (*one)(P), void (*many)(P), bool small, cudaStream_
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = small ? 1 : 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, small ? one : many, p);
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// The current device's SMs; found once per device, with what its kernels need.
 cudaError_t sm_count(int* sms) {
+  static std::atomic<int> known[64];
   int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
-  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if ((*sms = known[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             128 * 1024);
+  if (e == cudaSuccess) known[dev].store(*sms, std::memory_order_release);
+  return e;
+}
+// CTAs for `warps` warps' work, one to an SM.
+dim3 solo_grid(long long warps, int sms) {
+  return dim3((unsigned)max(1ll, min((warps + kScanWarps - 1) / kScanWarps, (long long)sms)));
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -537,6 +713,7 @@ cudaError_t launch_pages_reserve(int32_t* table, int32_t* refs, const int32_t* p
   p.lengths = lengths;
   p.taken = taken;
   p.status = reinterpret_cast<uint32_t*>(base);
+  p.ticket = reinterpret_cast<uint32_t*>(base + 64);
   p.n_copies = reinterpret_cast<int*>(base + 128);
   p.copies = reinterpret_cast<int4*>(base + ws.copies_off);
   p.reach = reinterpret_cast<int2*>(base + ws.copies_off + (size_t)B * 16);
@@ -551,11 +728,13 @@ cudaError_t launch_pages_reserve(int32_t* table, int32_t* refs, const int32_t* p
   p.list = p.info + (size_t)B * p.per;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
-  const bool small = pool.P <= kOneCtaPages && (long long)B * p.per <= kOneCtaItems;
-  if (e == cudaSuccess)
-    e = launch_scan(pages_reserve_kernel<1>, pages_reserve_kernel<kManyCtas>, small, stream, p);
   if (e != cudaSuccess) return e;
-  const long long warps = (long long)B * 2 * pool.Hkv * (pool.page >> 4);
+  const long long warps = (long long)B * 2 * pool.Hkv * (pool.page >> 4);  // of copies, at most
+  if (pool.P <= kSoloPages && (long long)B * p.per <= kSoloItems)
+    return launch_pdl(pages_reserve_solo_kernel, solo_grid(warps, sms), dim3(kScanThreads), 0,
+                      stream, p, pool);
+  e = launch_scan(pages_reserve_kernel<kManyCtas>, stream, p);
+  if (e != cudaSuccess) return e;
   const long long blocks = (warps * 32 + kCopyThreads - 1) / kCopyThreads;
   return launch_pdl(pages_copy_rows_kernel, dim3((unsigned)min(blocks, (long long)sms * 8)),
                     dim3(kCopyThreads), 0, stream, pool, (const int*)p.n_copies,
@@ -573,10 +752,7 @@ cudaError_t launch_pages_fork(int32_t* table, int32_t* refs, const int32_t* pare
   // 128-byte pieces of rows; 32-byte ones where that many rows would not fit, or
   // where that makes CTAs for SMs that would have none
   int sms = 0;
-  cudaError_t e = sm_count(&sms);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(pages_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             128 * 1024);
+  const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   const int lc = B > 1024 || M <= 8 * sms ? 3 : 5;
   const size_t smem = ((size_t)B << lc) * 4;
@@ -593,6 +769,7 @@ cudaError_t launch_pages_compact(int32_t* table, int32_t* refs, const PagedPool&
   p.table = table;
   p.refs = refs;
   p.map = page_map;
+  p.ticket = reinterpret_cast<uint32_t*>(base + 64);
   p.n_moves = reinterpret_cast<int*>(base + 128);
   p.from = reinterpret_cast<int32_t*>(base + ws.list_off);
   p.to = p.from + pool.P;
@@ -601,9 +778,15 @@ cudaError_t launch_pages_compact(int32_t* table, int32_t* refs, const PagedPool&
   p.P = pool.P;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
-  if (e == cudaSuccess)
-    e = launch_scan(pages_plan_kernel<1>, pages_plan_kernel<kManyCtas>, pool.P <= kOneCtaPages,
-                    stream, p);
+  if (e != cudaSuccess) return e;
+  if (pool.P <= kSoloMoves) {
+    // as many moves as can be, or the table's entries by 32
+    const long long moves = (long long)(pool.P / 2) * 2 * pool.Hkv * (pool.page >> 4);
+    return launch_pdl(pages_compact_solo_kernel,
+                      solo_grid(max(moves, ((long long)B * M + 31) / 32), sms), dim3(kScanThreads),
+                      0, stream, p, pool);
+  }
+  e = launch_scan(pages_plan_kernel<kManyCtas>, stream, p);
   if (e != cudaSuccess) return e;
   return launch_pdl(pages_move_kernel, dim3(sms * 8), dim3(kCopyThreads), 0, stream, p, pool);
 }

@@ -581,8 +581,8 @@ int attn_decode_step_paged(const void* q, const int32_t* positions, const int32_
 /*
  * attn_pages_workspace_size -- bytes of device workspace that the three calls
  * below need for these sizes (S: the most new tokens of a reserve); 0 if they
- * are invalid.  Its first word is the device status word, to be zero before the
- * first use.  Calls that share a workspace must not overlap in time.
+ * are invalid.  It must be zero-filled before its first use; its first word is
+ * the device status word.  Calls that share a workspace must not overlap in time.
  */
 size_t attn_pages_workspace_size(int B, int S, int P, int page);
 
@@ -600,7 +600,7 @@ size_t attn_pages_workspace_size(int B, int S, int P, int page);
  *           it and the sequences before it need are more than there are, or its
  *           rows do not fit (ATTN_DEV_BAD_POSITION): nothing of it is changed.
  *   S     : >= 1.  Other limits: B <= 65536, B * ceil(S / page + 1) <= 2^28.
- * Two launches.
+ * One launch for up to 16384 pages and 1024 pages that the rows can touch, else two.
  */
 int attn_pages_reserve(int32_t* page_table, int32_t* page_refs, const int32_t* positions,
                        const int32_t* lengths, void* k_pages, void* v_pages, int64_t page_stride,
@@ -634,7 +634,8 @@ int attn_pages_fork(int32_t* page_table, int32_t* page_refs, const int32_t* pare
  *
  *   page_map : [P] int32, written: where each page went (p for one that stayed),
  *              -1 for a free one: for page numbers kept elsewhere.
- *   Table entries outside [0, P) stay.  B * M may be 0.  Two launches.
+ *   Table entries outside [0, P) stay.  B * M may be 0.  One launch for up to 8192
+ *   pages, else two.
  */
 int attn_pages_compact(int32_t* page_table, int32_t* page_refs, void* k_pages, void* v_pages,
                        int64_t page_stride, int64_t head_stride, int64_t row_stride, int B,
