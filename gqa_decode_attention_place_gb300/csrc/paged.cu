@@ -6,6 +6,8 @@
 #include "paged.h"
 #include "tcgen05.cuh"
 
+#include <cmath>
+
 namespace gqa {
 
 __device__ unsigned int g_paged_append_skips;  // debug builds
@@ -90,9 +92,9 @@ PagedWorkspace paged_workspace_layout(int B, int S, int Hq, int Hkv, int D) {
 }
 
 // A pool as a 5-D tensor map (64 dims, rows, halves of a row, heads, pages); a
-// box is a page's rows of one head, [half][row][64 dims] in shared memory with
-// the 128-byte swizzle.
-static bool pool_map(CUtensorMap* m, const void* ptr, const PagedPool& pool) {
+// box is `rows` of a page's rows of one head, [half][row][64 dims] in shared
+// memory with the 128-byte swizzle.
+static bool pool_map(CUtensorMap* m, const void* ptr, const PagedPool& pool, int rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t half = 64 * 2;
@@ -100,12 +102,16 @@ static bool pool_map(CUtensorMap* m, const void* ptr, const PagedPool& pool) {
                         (cuuint64_t)pool.Hkv, (cuuint64_t)pool.P};
   cuuint64_t strides[4] = {(cuuint64_t)pool.row_stride * 2, half,
                            (cuuint64_t)pool.head_stride * 2, (cuuint64_t)pool.page_stride * 2};
-  cuuint32_t box[5] = {64, (cuuint32_t)pool.page, (cuuint32_t)(pool.D / 64), 1, 1};
+  cuuint32_t box[5] = {64, (cuuint32_t)rows, (cuuint32_t)(pool.D / 64), 1, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
+}
+
+bool paged_maps(const PagedPool& pool, int rows, CUtensorMap* mk, CUtensorMap* mv) {
+  return pool_map(mk, pool.k, pool, rows) && pool_map(mv, pool.v, pool, rows);
 }
 
 cudaError_t launch_paged_decode(const void* q, const int32_t* positions, const int32_t* lengths,
@@ -136,11 +142,11 @@ cudaError_t launch_paged_decode(const void* q, const int32_t* positions, const i
   p.cap = M * pool.page;
   p.stages = 0;
   p.test_skip = g_decode_test_skip;
-  p.qscale = scale * 1.4426950408889634f;
-  CUtensorMap mk, mv;
-  if (!pool_map(&mk, pool.k, pool) || !pool_map(&mv, pool.v, pool)) return cudaErrorInvalidValue;
-  return pool.D == 64 ? launch_paged_decode_64(p, mk, mv, stream)
-                      : launch_paged_decode_128(p, mk, mv, stream);
+  // (a scale of zero: tiny, so that masked scores stay -inf times it)
+  p.qscale = fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-37f);
+  p.flip = scale < 0.f ? 0x80008000u : 0u;
+  return pool.D == 64 ? launch_paged_decode_64(p, pool, stream)
+                      : launch_paged_decode_128(p, pool, stream);
 }
 
 cudaError_t paged_append_read_skips(uint32_t* count) {

@@ -36,16 +36,18 @@ struct PagedParams {
   int B, S, Hq, Hkv, g, P, M;
   int R;                   // S * g
   int lp;                  // log2 of the page's rows
+  int lb;                  // log2 of a copy's rows: the page's, or the tile's where that is less
   int cap;                 // rows that a sequence's pages can hold
   int stages;
   int test_skip;
-  float qscale;            // scale * log2(e)
+  float qscale;            // |scale| * log2(e), above zero
+  uint32_t flip;           // sign bits of two bf16 if scale is negative, else 0
 };
 
-cudaError_t launch_paged_decode_64(PagedParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
-                                   cudaStream_t stream);
-cudaError_t launch_paged_decode_128(PagedParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
-                                    cudaStream_t stream);
+// Makes the pool's tensor maps for copies of `rows` rows.
+bool paged_maps(const PagedPool& pool, int rows, CUtensorMap* mk, CUtensorMap* mv);
+cudaError_t launch_paged_decode_64(PagedParams& p, const PagedPool& pool, cudaStream_t stream);
+cudaError_t launch_paged_decode_128(PagedParams& p, const PagedPool& pool, cudaStream_t stream);
 
 struct PagedWorkspace {
   size_t counters_off, ml_off, o_off, total;  // the status word comes first

@@ -67,7 +67,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependents_launch();
 
   // the producer's first table entries, beside the position
-  const int ti = lane >> 3, slice = lane & 7;
+  constexpr int kTile = Sh::kTile, kSlices = Sh::kSlices, kBatch = Sh::kBatch;
+  constexpr uint32_t kAll = (1u << kSlices) - 1u;
+  const int ti = lane / kSlices, slice = lane % kSlices;
   auto entry = [&](int i) -> int {  // of slice `slice` of my tile i, whatever is in use
     const long long e = ((long long)(rank + (long long)i * C) * kTile + slice * 16) >> p.lp;
     return e < p.M ? p.table[(size_t)b * p.M + e] : -1;
@@ -88,7 +90,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kWarps) {
     // ----------------------------------------------------------- producers --
     const bool keys = warp == kWarps;
-    const int page_rows = 1 << p.lp, in_page = (slice * 16) & (page_rows - 1);
+    const int box_rows = 1 << p.lb, in_box = (slice * 16) & (box_rows - 1);
+    const int page_mask = (1 << p.lp) - 1;
     auto in_use = [&](int i, int page) -> int {
       if (i >= mine || (rank + i * C) * kTile + slice * 16 > pos + n - 1) return -1;
       return page_ok(p, page);
@@ -96,14 +99,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0;
     uint32_t pass = 0;
     bool ok = true;
-    for (int base = 0; ok && base < mine; base += 4) {
+    for (int base = 0; ok && base < mine; base += kBatch) {
       const int i = base + ti;
       const int cur = in_use(i, page);
-      if (i + 4 < mine) page = entry(i + 4);
+      if (i + kBatch < mine) page = entry(i + kBatch);
       const uint32_t there = __ballot_sync(0xffffffffu, cur >= 0);
-      const bool lead = cur >= 0 && in_page == 0;
+      const bool lead = cur >= 0 && in_box == 0;
       const uint32_t boxes = __ballot_sync(0xffffffffu, lead);
-      for (int q = 0; q < 4 && base + q < mine; ++q) {
+      for (int q = 0; q < kBatch && base + q < mine; ++q) {
         if (pass > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[NS + s]),
                                                            (pass & 1u) ^ 1u, abort_flag))) {
           if (lane == 0) {
@@ -119,16 +122,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool skip = p.test_skip >= 0 && seg == 0 && k == p.test_skip;  // tests only
         if (lane == 0) {
           if (keys)
-            meta[s] = TileMeta{(int)((there >> (8 * q)) & 0xffu), k * kTile, pos, n, b, kvh, 0, 1};
+            meta[s] = TileMeta{(int)((there >> (kSlices * q)) & kAll), k * kTile, pos, n, b, kvh, 0, 1};
           if (!skip)
-            mbar_arrive_expect_tx(full, __popc((boxes >> (8 * q)) & 0xffu) *
-                                                ((uint32_t)page_rows * D * 2u) +
+            mbar_arrive_expect_tx(full, __popc((boxes >> (kSlices * q)) & kAll) *
+                                                ((uint32_t)box_rows * D * 2u) +
                                             (keys && first ? (uint32_t)R * D * 2u : 0u));
         }
         __syncwarp();
         if (ti == q && lead && !skip) {
           const uint32_t dst = smem_u32(stages + (size_t)s * Sh::kStage) + slice * 16 * D * 2;
-          tma_load_5d(dst + (keys ? 0 : Sh::kOp), keys ? &tm_k : &tm_v, 0, 0, 0, kvh, cur, full);
+          tma_load_5d(dst + (keys ? 0 : Sh::kOp), keys ? &tm_k : &tm_v, 0,
+                      (k * kTile + slice * 16) & page_mask, 0, kvh, cur, full);
         }
         if (first && !skip && keys && lane < R)
           bulk_load(smem_u32(qbuf) + lane * Sh::kQStride,
@@ -150,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ph = 0;
     for (int i = 0; i < mine; ++i) {
       if (!consumer_wait(smem_u32(&bars[s]), ph, abort_flag, p.status, lane)) break;
-      if (i == 0) cs.load_q(qbuf);
+      if (i == 0) cs.load_q(qbuf, p.flip);
       cs.tile(stages + (size_t)s * Sh::kStage, p, meta[s]);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars[NS + s]));

@@ -52,24 +52,22 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kTile = 128;
-constexpr int kSlices = kTile / 16;
 constexpr int kWarps = 8;                   // consumer warps
 constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 64;   // and the producers: of keys, of values
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 12;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kE = 1;                       // units of a segment's end (flat_list.cuh)
 constexpr int kWholeTiles = 4;              // segments this short are not split
 // Whole segments, one CTA each (below): a lone CTA's tile takes kWholeNum / kWholeDen of
 // its share of a busy GPU, and a merge as long as kMergeCost / kWholeDen tiles.
 constexpr int kWholeNum = 5, kWholeDen = 9;
-template <int D> constexpr int kMergeCost = D == 128 ? 37 : 74;
+template <int D, int TILE> constexpr int kMergeCost = 37 * (128 / D) * (128 / TILE);
 constexpr int kMaxCluster = 16;
 constexpr float kMInit = -3e38f;            // the reference before any row
 constexpr float kTau = 8.f;                 // it moves when a score lies more than this above
 
-constexpr int kSlicesMask = 0xff;  // TileMeta::flags: slices that hold rows
+// TileMeta::flags: bits 0 .. 7, slices (16 rows) that hold rows, and
 constexpr int kStarts = 0x100;     // a piece starts with this tile
 constexpr int kEnds = 0x200;       // and ends with this one
 constexpr int kLast = 0x400;       // the CTA's last tile
@@ -85,16 +83,16 @@ struct TileMeta {
 // NT: 8-row groups of query rows (1, 2 or 4).
 template <int D, int NT>
 struct Shape {
+  static constexpr int kTile = 128;
+  static constexpr int kSlices = kTile / 16;
+  static constexpr int kBatch = 32 / kSlices;     // tiles that a producer looks up at a time
   static constexpr int kOp = kTile * D * 2;       // bytes of a tile's keys
   static constexpr int kStage = 2 * kOp;
   static constexpr int kQStride = D * 2 + 16;     // bytes between query rows: no bank conflicts
   static constexpr int kQ = NT * 8 * kQStride;
-  static constexpr int kORow = D + 8;             // floats between rows of partials: likewise
   static constexpr int kMl = kWarps * (NT == 1 ? 8 : 16) * 8;  // bytes of the warps' (reference, sum)
+  static_assert(kWarps * 8 * D * 4 <= kStage, "eight rows of every warp's partials fit a tile");
 };
-static_assert(kWarps * 8 * Shape<128, 1>::kORow * 4 <= Shape<128, 1>::kStage &&
-                  kWarps * 8 * Shape<64, 1>::kORow * 4 <= Shape<64, 1>::kStage,
-              "eight rows of every warp's partials fit a tile's memory");
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
                                             int c2, int c3, int c4, uint32_t bar) {
@@ -154,7 +152,8 @@ struct PagedConsumer {
   static constexpr int KS = D / 16;               // MMA steps of a score
   uint32_t qa[KS][2 * G];
   float o[D / 8][4];    // dims 8j + 2t, +1 for rows c, c + 8
-  float ref[G], l[G];   // of this warp's rows; l: of this lane's
+  float ref[G];         // the references
+  float sums[4];        // of the weights as they entered: rows c, c + 8 (in [0] and [2])
   int lim[G];           // last cache row that the query row sees, -1: none
   int c, t, warp, lane;
   int team, row_base;   // its place; its first query row
@@ -167,7 +166,8 @@ struct PagedConsumer {
     team = warp / kTeam;
     row_base = 16 * team;
   }
-  __device__ __forceinline__ void load_q(const uint8_t* qs) {
+  // The queries, negated for a negative score scale.
+  __device__ __forceinline__ void load_q(const uint8_t* qs, uint32_t flip) {
     const uint32_t base = smem_u32(qs);
     const int i = lane >> 3, r = lane & 7;
     if (G == 1) {
@@ -189,38 +189,46 @@ struct PagedConsumer {
         for (int e = 0; e < 4; ++e) qa[k][G == 1 ? 0 : e] = x[e];
       }
     }
+    if (flip) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 2 * G; ++e) qa[k][e] ^= flip;
+    }
   }
   __device__ __forceinline__ void start(const PagedParams& p, int pos, int n) {
 #pragma unroll
     for (int i = 0; i < G; ++i) {
       const int r = row_base + 8 * i + c, tok = r / p.g;
       ref[i] = kMInit;
-      l[i] = 0.f;
       lim[i] = r < p.R && tok < n ? pos + tok : -1;
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sums[e] = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
   }
   // Byte offset in a tile of row 16 * slice (its first 64 dims).
-  __device__ __forceinline__ static int slice_at(int slice, int lp) {
-    const int row = slice * 16, pg = row >> lp;
-    return ((pg << lp) * D * 2) + (row & ((1 << lp) - 1)) * 128;
+  __device__ __forceinline__ static int slice_at(int slice, int lb) {
+    const int row = slice * 16, box = row >> lb;
+    return ((box << lb) * D * 2) + (row & ((1 << lb) - 1)) * 128;
   }
 
   // This warp's rows of a tile.  ks: its keys; the values lie behind them.
   __device__ __forceinline__ void tile(const uint8_t* ks, const PagedParams& p,
                                        const TileMeta& mt) {
     const int first = warp & (kTeam - 1);
-    constexpr int kAll = kTeams == 1 ? 1 : 1 | (1 << kTeam);
-    if (kTeams > 1 && mt.row0 + 16 * (first + kTeam) + 15 <= mt.pos &&
+    constexpr bool kTwo = Sh::kSlices == 2 * kTeam;
+    constexpr int kAll = kTwo ? 1 | (1 << kTeam) : 1;
+    if (kTwo && mt.row0 + 16 * (first + kTeam) + 15 <= mt.pos &&
         ((mt.flags >> first) & kAll) == kAll) {
-      slices<kTeams, true>(ks, first, p, mt);
+      slices<kTwo ? 2 : 1, true>(ks, first, p, mt);
       return;
     }
 #pragma unroll 1
-    for (int sl = first; sl < kSlices; sl += kTeam) {
+    for (int sl = first; sl < Sh::kSlices; sl += kTeam) {
       if (!((mt.flags >> sl) & 1)) continue;  // no rows there
       // full: every row is seen by every query row in use
       if (mt.row0 + 16 * sl + 15 <= mt.pos) slices<1, true>(ks, sl, p, mt);
@@ -232,11 +240,11 @@ struct PagedConsumer {
   template <int N, bool FULL>
   __device__ __forceinline__ void slices(const uint8_t* ks, int sl, const PagedParams& p,
                                          const TileMeta& mt) {
-    const int half = 128 << p.lp;  // from a page's first 64 dims to the others
+    const int half = 128 << p.lb;  // from a box's first 64 dims to the others
     const int i8 = lane >> 3, r8 = lane & 7;
     uint32_t at[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) at[n] = smem_u32(ks) + slice_at(sl + n * kTeam, p.lp);
+    for (int n = 0; n < N; ++n) at[n] = smem_u32(ks) + slice_at(sl + n * kTeam, p.lb);
     const int row0 = mt.row0 + 16 * sl;  // the first cache row (N = 1)
     float s[N][2][2][4];  // of each slice rows 0..7 and 8..15, in two chains each
 #pragma unroll
@@ -268,11 +276,25 @@ struct PagedConsumer {
         mma_bf16(s[n][1][N == 1 ? k & 1 : 0], a, b[2], b[3]);
       }
     }
+    // the first values, on their way while the weights are made
+    constexpr int kAhead = FULL ? (N == 2 || (G == 2 && D == 128) ? 2 : 4) : 0;
+    auto load_v = [&](uint32_t (&b)[4], int d, int n) {
+      const int ch = 2 * d + (i8 >> 1);
+      ldmatrix4_trans(b, at[n] + Sh::kOp + (8 * (i8 & 1) + r8) * 128 + (2 * d >= 8 ? half : 0) +
+                             (((ch & 7) ^ r8) << 4));
+    };
+    uint32_t ahead[kAhead > 0 ? kAhead : 1][N][4];
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d)
+#pragma unroll
+      for (int n = 0; n < N; ++n) load_v(ahead[d][n], d, n);
     // weights as the second product's A operand: rows 2t, 2t+1 and 8 on of a slice
     uint32_t w[N][4], rest[N][4];
+    float x[N][G][4], mine[G];
+    bool grow = false;
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      float x[N][4], mine = -INFINITY;
+      mine[i] = -INFINITY;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
 #pragma unroll
@@ -280,18 +302,24 @@ struct PagedConsumer {
           float v = s[n][e >> 1][0][2 * i + (e & 1)];
           if (N == 1) v += s[n][e >> 1][1][2 * i + (e & 1)];
           const int row = row0 + 8 * (e >> 1) + 2 * t + (e & 1);
-          x[n][e] = FULL || row <= lim[i] ? v * p.qscale : -INFINITY;
+          x[n][i][e] = FULL || row <= lim[i] ? v : -INFINITY;
         }
-        mine = fmax3(mine, x[n][0], fmax3(x[n][1], x[n][2], x[n][3]));
+        mine[i] = fmax3(mine[i], x[n][i][0], fmax3(x[n][i][1], x[n][i][2], x[n][i][3]));
       }
-      if (__any_sync(0xffffffffu, mine > ref[i] + kTau)) {
-        float mx = mine;
+      mine[i] *= p.qscale;
+      grow = grow || mine[i] > ref[i] + kTau;
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        float mx = mine[i];
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const float to = mx > ref[i] + kTau ? mx : ref[i];
         const float alpha = ex2(ref[i] - to);
         ref[i] = to;
-        l[i] *= alpha;
+        sums[2 * i] *= alpha;
+        if (G == 1) sums[2] *= alpha;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j)
 #pragma unroll
@@ -300,38 +328,43 @@ struct PagedConsumer {
             if (G == 1) o[j][2 + e] *= alpha;
           }
       }
+    }
+#pragma unroll
+    for (int i = 0; i < G; ++i)
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = ex2(x[n][e] - ref[i]);
+        for (int e = 0; e < 4; ++e) y[e] = ex2(fmaf(x[n][i][e], p.qscale, -ref[i]));
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t hi = pack_bf16x2(y[2 * j], y[2 * j + 1]);
           w[n][2 * j + i] = hi;
-          if (NT == 4) {  // the sum is of the weights as they enter
-            y[2 * j] = bf16lo(hi);
-            y[2 * j + 1] = bf16hi(hi);
-            continue;
-          }
+          if (NT == 4) continue;
           const uint32_t lo = pack_bf16x2(y[2 * j] - bf16lo(hi), y[2 * j + 1] - bf16hi(hi));
           if (G == 1) w[n][2 * j + 1] = lo;
           else rest[n][2 * j + i] = lo;
         }
-        l[i] += (y[0] + y[1]) + (y[2] + y[3]);
       }
+    // their sums, as a product with ones
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      mma_bf16(sums, w[n], 0x3f803f80u, 0x3f803f80u);
+      if (kTwoParts) mma_bf16(sums, rest[n], 0x3f803f80u, 0x3f803f80u);
     }
     const int seen = mt.pos + mt.n - row0;  // rows that some token may see
     const bool drafts = !FULL && mt.n > 1;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
-      const int ch = 2 * d + (i8 >> 1);
-      const int to = Sh::kOp + (8 * (i8 & 1) + r8) * 128 + (2 * d >= 8 ? half : 0) +
-                     (((ch & 7) ^ r8) << 4);
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         uint32_t b[4];  // 16 dims: rows 0..7 and 8..15 of the first 8, then of the others
-        ldmatrix4_trans(b, at[n] + to);
+        if (d < kAhead) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) b[e] = ahead[d < kAhead ? d : 0][n][e];
+        } else {
+          load_v(b, d, n);
+        }
         if (!FULL) {
           // rows past the last token may be NaN: 0 * NaN would spread
 #pragma unroll
@@ -401,11 +434,10 @@ struct PagedConsumer {
     for (int i = 0; i < G; ++i) {
       if (8 * i >= p.R) break;
       if (i > 0) csync(lane);  // the rows before have been read
-      float sum = l[i];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (t == 0) ml[(row_base + 8 * i + c) * kTeam + w0] = make_float2(ref[i], sum);
-      float* to = part + (warp * 8 + c) * Sh::kORow + 2 * t;
+      if (t == 0)
+        ml[(row_base + 8 * i + c) * kTeam + w0] =
+            make_float2(ref[i], G == 1 ? sums[0] + sums[2] : sums[2 * i]);
+      float* to = part + (warp * 8 + c) * D;  // dim d at d ^ swizzle(row): no bank conflicts
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
         float2 y = make_float2(o[j][2 * i], o[j][2 * i + 1]);
@@ -413,7 +445,7 @@ struct PagedConsumer {
           y.x += o[j][2];
           y.y += o[j][3];
         }
-        *reinterpret_cast<float2*>(to + 8 * j) = y;
+        *reinterpret_cast<float2*>(to + ((8 * j + 2 * t) ^ ((c & 3) << 3))) = y;
       }
       csync(lane);
 #pragma unroll
@@ -433,7 +465,7 @@ struct PagedConsumer {
         for (int k = 0; k < kTeam; ++k) {
           const float e = ex2(x[k].x - M);
           const float4 v = *reinterpret_cast<const float4*>(
-              part + ((tm * kTeam + k) * 8 + row) * Sh::kORow + d);
+              part + ((tm * kTeam + k) * 8 + row) * D + (d ^ ((row & 3) << 3)));
           L = fmaf(x[k].y, e, L);
           y.x = fmaf(v.x, e, y.x);
           y.y = fmaf(v.y, e, y.y);
@@ -583,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kind = sequence(p, b, pos, n);
       spos[b] = pos;
       snew[b] = (uint8_t)n;
-      if (kind == 2) v = (pos + n - 1) / kTile + 1 + kE;
+      if (kind == 2) v = (pos + n - 1) / Sh::kTile + 1 + kE;
     }
     const int most = __reduce_max_sync(0xffffffffu, v);
     if (lane == 0 && warp < kWarps) atomicMax(misc + 2, most);
@@ -619,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A CTA for each segment where the longest alone takes no longer than an even
   // share of the tiles and the merge of a split segment would.
   const bool whole = nseg <= (long long)gridDim.x &&
-                     (long long)misc[2] * kWholeNum * gw <= T * kWholeDen + kMergeCost<D> * gw;
+                     (long long)misc[2] * kWholeNum * gw <= T * kWholeDen + kMergeCost<D, Sh::kTile> * gw;
   const int G = whole ? (int)nseg : (int)gw;
   if ((int)blockIdx.x >= G) return;
   FlatRange rg;
@@ -637,15 +669,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kWarps) {
     // ----------------------------------------------------------- producers --
-    // Tiles go in batches of four, lane 8*ti + slice looks after slice
+    // Tiles go in batches of kBatch, lane kSlices * ti + slice looks after slice
     // `slice` of the batch's tile ti; a batch's table entries are loaded while
     // the one before it is issued.
+    constexpr int kSlices = Sh::kSlices, kBatch = Sh::kBatch;
     const bool keys = warp == kWarps;  // this warp also describes the tile and brings the queries
-    const int ti = lane >> 3, slice = lane & 7;
-    const int page_rows = 1 << p.lp, in_page = (slice * 16) & (page_rows - 1);
+    const int ti = lane / kSlices, slice = lane % kSlices;
+    const int box_rows = 1 << p.lb, in_box = (slice * 16) & (box_rows - 1);
+    const int page_mask = (1 << p.lp) - 1;
     // The slice's table entry, kNoRows where it holds none; looked at a batch later.
     auto fetch = [&](const FlatWalk& w) -> int {
-      const int row = w.k * kTile + slice * 16;
+      const int row = w.k * Sh::kTile + slice * 16;
       if (w.u >= w.end || row > w.pos + snew[w.b] - 1) return kNoRows;
       if (!range_ok((row >> p.lp) < p.M, p.status)) return kNoRows;
       return p.table[(size_t)w.b * p.M + (row >> p.lp)];
@@ -673,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the CTA's last tile: none in what is left of this part of the range (the
       // next one would come after the end units), nor a part after it
       if (w.u + 1 + (w.k == w.nt - 1 ? kE : 0) >= w.end && w.end == last_end) m.flags |= kLast;
-      m.row0 = w.k * kTile;
+      m.row0 = w.k * Sh::kTile;
       m.pos = w.pos;
       m.n = snew[w.b];
       m.b = w.b;
@@ -693,15 +727,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok) {
       const bool on = cur.u < cur.end;
-      const int n_q = __popc(__ballot_sync(0xffffffffu, on)) >> 3;  // tiles of the batch
+      const int n_q = __popc(__ballot_sync(0xffffffffu, on)) / kSlices;  // tiles of the batch
       if (n_q == 0) break;
-      step(w, 4);
+      step(w, kBatch);
       const int next = fetch(w);
       const int page = entry == kNoRows ? -1 : page_ok(p, entry);
       TileMeta mt = {};
       if (on && slice == 0) describe(cur, mt);
       const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-      const bool lead = page >= 0 && in_page == 0;
+      const bool lead = page >= 0 && in_box == 0;
       const uint32_t boxes = __ballot_sync(0xffffffffu, lead);
       const bool skip = on && p.test_skip >= 0 && cur.b == 0 && cur.kvh == 0 &&
                         cur.k == p.test_skip;  // failure-path tests only
@@ -716,25 +750,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t full = smem_u32(&bars[s]);
-        const bool first = __shfl_sync(0xffffffffu, (mt.flags & kStarts) != 0, 8 * q);
-        if (lane == 8 * q) {
-          mt.flags |= (there >> (8 * q)) & 0xffu;
+        const bool first = __shfl_sync(0xffffffffu, (mt.flags & kStarts) != 0, kSlices * q);
+        if (lane == kSlices * q) {
+          mt.flags |= (there >> (kSlices * q)) & ((1u << kSlices) - 1u);
           if (keys) meta[s] = mt;
           if (!skip)
-            mbar_arrive_expect_tx(full, __popc((boxes >> (8 * q)) & 0xffu) *
-                                                ((uint32_t)page_rows * D * 2u) +
+            mbar_arrive_expect_tx(full, __popc((boxes >> (kSlices * q)) & ((1u << kSlices) - 1u)) *
+                                                ((uint32_t)box_rows * D * 2u) +
                                             (keys && first ? (uint32_t)p.R * D * 2u : 0u));
         }
         __syncwarp();
-        const bool hold = __shfl_sync(0xffffffffu, skip, 8 * q);
+        const bool hold = __shfl_sync(0xffffffffu, skip, kSlices * q);
         if (ti == q && lead && !hold) {
           const uint32_t dst = smem_u32(stages + (size_t)s * Sh::kStage) + slice * 16 * D * 2;
-          tma_load_5d(dst + (keys ? 0 : Sh::kOp), keys ? &tm_k : &tm_v, 0, 0, 0, cur.kvh, page,
-                      full);
+          tma_load_5d(dst + (keys ? 0 : Sh::kOp), keys ? &tm_k : &tm_v, 0,
+                      (cur.k * Sh::kTile + slice * 16) & page_mask, 0, cur.kvh, page, full);
         }
         if (first && !hold && keys) {  // the piece's query rows, one by each lane
-          const int b = __shfl_sync(0xffffffffu, mt.b, 8 * q);
-          const int kvh = __shfl_sync(0xffffffffu, mt.kvh, 8 * q);
+          const int b = __shfl_sync(0xffffffffu, mt.b, kSlices * q);
+          const int kvh = __shfl_sync(0xffffffffu, mt.kvh, kSlices * q);
           if (lane < p.R)
             bulk_load(smem_u32(qbuf + s * Sh::kQ) + lane * Sh::kQStride,
                       p.q + query_row(p, b, kvh, lane) * D, D * 2, full);
@@ -759,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const TileMeta mt = meta[s];
       uint8_t* tile = stages + (size_t)s * Sh::kStage;
       if (mt.flags & kStarts) {
-        cs.load_q(qbuf + s * Sh::kQ);
+        cs.load_q(qbuf + s * Sh::kQ, p.flip);
         cs.start(p, mt.pos, mt.n);
       }
       cs.tile(tile, p, mt);
@@ -907,8 +941,9 @@ cudaError_t paged_device(const PagedDevice** out) {
 //   flat list  12 (scan, lookups, the merge of split segments) and the even share
 // (2 sequences up to 8192 rows, 8 heads: 17 in clusters, 21 by the list; 10 up to
 // 16000: 74 and 50.)
-template <int D>
+template <int D, int NT>
 int cluster_size(const PagedParams& p, const PagedDevice& d) {
+  constexpr int kTile = Shape<D, NT>::kTile;
   if (g_decode_test_cluster >= 0)  // schedule tests only
     return min(g_decode_test_cluster, kMaxCluster);
   const long long nseg = (long long)p.B * p.Hkv;
@@ -917,7 +952,7 @@ int cluster_size(const PagedParams& p, const PagedDevice& d) {
   while (c > 1 && nseg > d.clusters[c]) --c;
   const float longest = (float)tiles * (float)p.B / (float)(p.B + 1);
   const float waves = c > 1 ? 1.f : (float)((nseg + d.sms - 1) / d.sms);
-  const float per_tile = D == 128 ? 1.45f : 0.75f;
+  const float per_tile = (D == 128 ? 1.45f : 0.75f) * (float)(kTile / 128.0);
   const float share = per_tile * 0.5f * (float)tiles * (float)nseg / (float)d.sms;
   const float clusters = 4.3f + 2.f * (waves - 1.f) +
                          fmaxf(1.15f * share, 0.43f * per_tile * ceilf(longest / (float)c));
@@ -925,13 +960,16 @@ int cluster_size(const PagedParams& p, const PagedDevice& d) {
 }
 
 template <int D, int NT>
-cudaError_t launch_paged(PagedParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
-                         cudaStream_t stream) {
+cudaError_t launch_paged(PagedParams& p, const PagedPool& pool, cudaStream_t stream) {
   const PagedDevice* d = nullptr;
   cudaError_t e = paged_device<D>(&d);
   if (e != cudaSuccess) return e;
+  const int rows = min(pool.page, Shape<D, NT>::kTile);
+  p.lb = rows == 16 ? 4 : rows == 32 ? 5 : rows == 64 ? 6 : 7;
+  CUtensorMap mk, mv;
+  if (!paged_maps(pool, rows, &mk, &mv)) return cudaErrorInvalidValue;
   p.stages = kMaxStages;
-  const int C = cluster_size<D>(p, *d);
+  const int C = cluster_size<D, NT>(p, *d);
   if (C > 0) {
     if (d->clusters[C] == 0) return cudaErrorNotSupported;
     while (p.stages > 2 && cluster_smem_bytes<D, NT>(p.stages, p.R, C) > (size_t)kMaxSmem)
@@ -959,11 +997,10 @@ cudaError_t launch_paged(PagedParams& p, const CUtensorMap& mk, const CUtensorMa
 }
 
 template <int D>
-cudaError_t launch_paged_rows(PagedParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
-                              cudaStream_t stream) {
-  return p.R <= 8    ? launch_paged<D, 1>(p, mk, mv, stream)
-         : p.R <= 16 ? launch_paged<D, 2>(p, mk, mv, stream)
-                     : launch_paged<D, 4>(p, mk, mv, stream);
+cudaError_t launch_paged_rows(PagedParams& p, const PagedPool& pool, cudaStream_t stream) {
+  return p.R <= 8    ? launch_paged<D, 1>(p, pool, stream)
+         : p.R <= 16 ? launch_paged<D, 2>(p, pool, stream)
+                     : launch_paged<D, 4>(p, pool, stream);
 }
 
 }  // namespace

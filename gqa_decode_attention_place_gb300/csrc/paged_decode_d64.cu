@@ -3,9 +3,8 @@
 
 namespace gqa {
 
-cudaError_t launch_paged_decode_64(PagedParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
-                                   cudaStream_t stream) {
-  return launch_paged_rows<64>(p, mk, mv, stream);
+cudaError_t launch_paged_decode_64(PagedParams& p, const PagedPool& pool, cudaStream_t stream) {
+  return launch_paged_rows<64>(p, pool, stream);
 }
 
 }  // namespace gqa

@@ -196,3 +196,14 @@ def test_append_skips_what_does_not_fit():
     paged.append(want_k, want_v, f64(kn[:, :1]), f64(vn[:, :1]), [16 * i for i in range(5)], None,
                  i64(table))
     assert (f64(k) == want_k).all() and (f64(v) == want_v).all()
+
+
+@pytest.mark.parametrize("S,g", [(1, 2), (1, 16), (2, 16)])
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 2.0])
+def test_score_scales(S, g, scale):
+    """A negative scale, zero (the mean of the rows), and one that leaves a single row."""
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    pos = [0, 129, 400]
+    q, table, k, v = make(3, S, 2 * g, 2, 128, 16, pos, gen)
+    out = ga.attn_decode_step_paged(q, i32(pos), table, k, v, scale)
+    check_decode(out, q, k, v, pos, None, table, scale)
