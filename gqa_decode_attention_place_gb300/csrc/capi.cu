@@ -442,6 +442,7 @@ int attn_paged_append(const void* k_new, const void* v_new, int64_t k_stride, in
   if (const int st = paged_pool(k_pages, v_pages, page_stride, head_stride, row_stride, Hkv, D, P,
                                 page, M, &pool))
     return st;
+  if (k_pages == v_pages) return ATTN_ERR_INVALID_ARG;
   if (S == 0) return ATTN_OK;
   if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new) ||
       k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D || k_stride % 8 || v_stride % 8)
@@ -480,6 +481,7 @@ int attn_decode_step_paged(const void* q, const int32_t* positions, const int32_
   if (const int st = paged_pool(k_pages, v_pages, page_stride, head_stride, row_stride, Hkv, D, P,
                                 page, M, &pool))
     return st;
+  if ((int64_t)B * ((int64_t)M * page / 128 + 2) >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < gqa::paged_workspace_layout(B, S, Hq, Hkv, D).total)
     return ATTN_ERR_WORKSPACE;
@@ -509,6 +511,7 @@ int attn_pages_reserve(int32_t* page_table, int32_t* page_refs, const int32_t* p
   if (const int st = paged_pool(k_pages, v_pages, page_stride, head_stride, row_stride, Hkv, D, P,
                                 page, M, &pool))
     return st;
+  if (k_pages == v_pages) return ATTN_ERR_INVALID_ARG;
   if (!pages_sizes(B, S, page)) return ATTN_ERR_UNSUPPORTED;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < gqa::pages_reserve_layout(B, S, page).total)
@@ -542,6 +545,7 @@ int attn_pages_compact(int32_t* page_table, int32_t* page_refs, void* k_pages, v
   if (const int st = paged_pool(k_pages, v_pages, page_stride, head_stride, row_stride, Hkv, D, P,
                                 page, M, &pool))
     return st;
+  if (k_pages == v_pages) return ATTN_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < gqa::pages_compact_layout(P).total)
     return ATTN_ERR_WORKSPACE;

@@ -143,7 +143,11 @@ struct PageBits {
 // Rows r0 .. r1 - 1 (16 at most) of one operand and head of page `from` to page
 // `to`, by a warp: all of a lane's loads (four or eight) are under way at once.
 __device__ __forceinline__ void copy_rows(uint8_t* base, const PagedPool& pool, int h, int from,
-                                          int to, int r0, int r1, int lane) {
+                                          int to, int r0, int r1, int lane, uint32_t* status) {
+  if (!range_ok(from >= 0 && from < pool.P && to >= 0 && to < pool.P && h < pool.Hkv && r0 < r1 &&
+                    r1 <= pool.page && r1 - r0 <= 16,
+                status))
+    return;
   const int lv = pool.D == 128 ? 4 : 3;
   const int vecs = (r1 - r0) << lv;
   const long long rs = pool.row_stride >> 3;
@@ -212,6 +216,7 @@ struct Item {
 // The item's page changes hands.
 __device__ __forceinline__ void give(const ReserveParams& p, int b, int jj, int was, int pos,
                                      int page) {
+  if (!range_ok(page >= 0 && page < p.P && b < p.B && (pos >> p.lp) + jj < p.M, p.status)) return;
   p.table[(size_t)b * p.M + (pos >> p.lp) + jj] = page;
   p.refs[page] = 1;
   if (was >= 0) atomicSub(&p.refs[was], 1);
@@ -272,7 +277,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     if (before[0] >= total[1]) return false;  // no more are wanted
     const uint32_t m = ~used & bits.valid(k);
     const int to = before[0] + __popc(m & lanes_below(lane));
-    if ((m >> lane & 1) && to < total[1]) list[to] = bits.s.lo + 32 * k + lane;
+    if ((m >> lane & 1) && to < total[1] && range_ok(to < kSoloItems, p.status))
+      list[to] = bits.s.lo + 32 * k + lane;
     before[0] += __popc(m);
     return true;
   });
@@ -294,7 +300,8 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     const int c = u / per, rest = u - c * per, r0 = rest % parts * 16, oh = rest / parts;
     const int4 x = copies[c];
     if (r0 < x.z)
-      copy_rows(oh & 1 ? pool.v : pool.k, pool, oh >> 1, x.x, x.y, r0, min(r0 + 16, x.z), lane);
+      copy_rows(oh & 1 ? pool.v : pool.k, pool, oh >> 1, x.x, x.y, r0, min(r0 + 16, x.z), lane,
+                p.status);
   }
   if (!last) return;
   if (given) give(p, b, jj, was, pos, page);
@@ -349,7 +356,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_reserve_kernel(const Re
     if (at >= n_need) return false;  // no more are wanted
     const uint32_t m = ~used & bits.valid(k);
     const int to = at + __popc(m & lanes_below(lane));
-    if ((m >> lane & 1) && to < n_need) p.list[to] = bits.s.lo + 32 * k + lane;
+    if ((m >> lane & 1) && to < n_need && range_ok(to < p.B * p.per, p.status))
+      p.list[to] = bits.s.lo + 32 * k + lane;
     at += __popc(m);
     return true;
   });
@@ -373,7 +381,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_reserve_kernel(const Re
   auto hand_over = [&](int b, int jj, int was, int pos, int page) {
     give(p, b, jj, was, pos, page);
     const int rows = copied(p, jj, was, pos);
-    if (rows > 0) p.copies[atomicAdd(p.n_copies, 1)] = make_int4(was, page, rows, 0);
+    if (rows == 0) return;
+    const int at = atomicAdd(p.n_copies, 1);
+    if (range_ok(at < p.B, p.status)) p.copies[at] = make_int4(was, page, rows, 0);
   };
   if (first != kNothing) {
     const int b = (is.lo + lane) / p.per, jj = is.lo + lane - b * p.per;
@@ -399,7 +409,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_reserve_kernel(const Re
 // A warp for each (copy, operand, head, 16 rows).  (A warp for all rows of a
 // head: 64 copies of up to 127 rows, 8 heads: 10.5 us instead of 4.4.)
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_rows_kernel(
-    PagedPool pool, const int* __restrict__ n_copies, const int4* __restrict__ copies) {
+    PagedPool pool, const int* __restrict__ n_copies, const int4* __restrict__ copies,
+    uint32_t* status) {
   grid_dependency_wait();
   grid_dependents_launch();
   const int lane = threadIdx.x & 31, parts = pool.page >> 4, per = 2 * pool.Hkv * parts;
@@ -413,7 +424,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_rows_kernel(
     const int4 x = copies[c];
     if (r0 < x.z)
       copy_rows(rest & 1 ? pool.v : pool.k, pool, rest >> 1, x.x, x.y, r0, min(r0 + 16, x.z),
-                lane);
+                lane, status);
   }
 }
 
@@ -500,6 +511,7 @@ struct CompactParams {
   int32_t* table;
   int32_t* refs;
   int32_t* map;
+  uint32_t* status;
   uint32_t* ticket;
   int* n_moves;
   int32_t* from;  // [P] used pages by how many come before them
@@ -538,8 +550,10 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     if (i >= bits.s.hi) return true;
     if (i == n) holes = n - before;
     const bool used = m >> lane & 1;
-    if (used && i >= n) from[n - 1 - before] = (uint16_t)i;
-    if (!used && i < n) to[i - before] = (uint16_t)i;
+    if (used && i >= n && range_ok(n - 1 - before < kSoloMoves / 2, p.status))
+      from[n - 1 - before] = (uint16_t)i;
+    if (!used && i < n && range_ok(i - before < kSoloMoves / 2, p.status))
+      to[i - before] = (uint16_t)i;
     where[i] = used ? (uint16_t)i : 0xffff;
     return true;
   });
@@ -558,7 +572,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   for (int u = thread >> 5; u < moves * per; u += threads >> 5) {
     const int c = u / per, rest = u - c * per, r0 = rest % parts * 16, oh = rest / parts;
     copy_rows(oh & 1 ? pool.v : pool.k, pool, oh >> 1, from[moves - 1 - c], to[c], r0, r0 + 16,
-              lane);
+              lane, p.status);
   }
   if (!last) return;
   for (int k = tid; k < moves; k += kScanThreads) {
@@ -597,10 +611,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_plan_kernel(const Compa
       p.n_moves[1] = n;
     }
     if (m >> lane & 1) {
+      if (!range_ok(before >= 0 && before < p.P, p.status)) return true;
       if (i >= n) p.from[before] = i;
       else p.map[i] = i;
     } else {
-      if (i < n) p.to[i - before] = i;
+      if (i < n && range_ok(i - before >= 0 && i - before < p.P, p.status)) p.to[i - before] = i;
       p.map[i] = -1;
     }
     return true;
@@ -637,7 +652,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(CompactParams 
     const int r0 = rest % parts * 16;
     rest /= parts;
     copy_rows(rest & 1 ? pool.v : pool.k, pool, rest >> 1, p.from[n - moves + c], p.to[c], r0,
-              r0 + 16, lane);
+              r0 + 16, lane, p.status);
   }
 }
 
@@ -738,7 +753,7 @@ cudaError_t launch_pages_reserve(int32_t* table, int32_t* refs, const int32_t* p
   const long long blocks = (warps * 32 + kCopyThreads - 1) / kCopyThreads;
   return launch_pdl(pages_copy_rows_kernel, dim3((unsigned)min(blocks, (long long)sms * 8)),
                     dim3(kCopyThreads), 0, stream, pool, (const int*)p.n_copies,
-                    (const int4*)p.copies);
+                    (const int4*)p.copies, p.status);
 }
 
 cudaError_t launch_pages_fork(int32_t* table, int32_t* refs, const int32_t* parents,
@@ -769,6 +784,7 @@ cudaError_t launch_pages_compact(int32_t* table, int32_t* refs, const PagedPool&
   p.table = table;
   p.refs = refs;
   p.map = page_map;
+  p.status = reinterpret_cast<uint32_t*>(base);
   p.ticket = reinterpret_cast<uint32_t*>(base + 64);
   p.n_moves = reinterpret_cast<int*>(base + 128);
   p.from = reinterpret_cast<int32_t*>(base + ws.list_off);

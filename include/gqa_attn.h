@@ -510,7 +510,8 @@ int attn_decode_step_kv8_sparse(const void* q, const int32_t* positions, const v
  * v_pages [P, Hkv, page, D] bf16, laid out alike: element (p, h, r, d) at
  * p * page_stride + h * head_stride + r * row_stride + d elements from either
  * base.  Strides are multiples of 8, row_stride >= D, and rows do not overlap
- * (any order of the three; a stride whose size is 1 counts for nothing).
+ * (any order of the three; a stride whose size is 1 counts for nothing).  The
+ * calls that write into the pool want two different bases.
  *   page       : 16, 32, 64 or 128 rows.   D: 64 or 128.
  *   page_table : [B, M] int32: row j of sequence b is row j % page of page
  *                page_table[b][j / page], -1 for none.  A sequence can hold
@@ -563,7 +564,7 @@ size_t attn_paged_workspace_size(int B, int S, int Hq, int Hkv, int D);
  *   probabilities enter as two bf16 parts for S * g <= 16 and are rounded to
  *   bf16 once beyond.
  *   Supported: any g = Hq / Hkv with S * g <= 32; B <= 4096; Hkv <= 1024;
- *   B * Hkv < 2^31 / 16.
+ *   B * Hkv < 2^31 / 16; B * (M * page / 128 + 2) < 2^31.
  *
  * A sequence whose rows positions[b] .. positions[b] + lengths[b] - 1 are not
  * all in [0, M * page), or whose lengths[b] is not in 0 .. S, gets NaN output
