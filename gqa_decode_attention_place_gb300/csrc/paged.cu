@@ -138,6 +138,7 @@ cudaError_t launch_paged_decode(const void* q, const int32_t* positions, const i
   p.P = pool.P;
   p.M = M;
   p.R = S * p.g;
+  p.g_inverse = (65536 + p.g - 1) / p.g;
   p.lp = log2_of(pool.page);
   p.cap = M * pool.page;
   p.stages = 0;

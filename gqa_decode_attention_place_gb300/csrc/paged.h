@@ -35,6 +35,7 @@ struct PagedParams {
   float* part_o;           // [slots][R][D]
   int B, S, Hq, Hkv, g, P, M;
   int R;                   // S * g
+  int g_inverse;           // 2^16 / g, rounded up
   int lp;                  // log2 of the page's rows
   int lb;                  // log2 of a copy's rows: the page's, or the tile's where that is less
   int cap;                 // rows that a sequence's pages can hold

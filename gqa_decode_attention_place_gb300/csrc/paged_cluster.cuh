@@ -150,9 +150,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     PagedConsumer<D, NT> cs;
     cs.init(warp, lane);
     cs.start(p, pos, n);
-    int s = 0;
+    int s = 0, last = 0;  // last: the stage of the last tile
     uint32_t ph = 0;
     for (int i = 0; i < mine; ++i) {
+      last = s;
       if (!consumer_wait(smem_u32(&bars[s]), ph, abort_flag, p.status, lane)) break;
       if (i == 0) cs.load_q(qbuf, p.flip);
       cs.tile(stages + (size_t)s * Sh::kStage, p, meta[s]);
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every other CTA of the cluster has started; each column goes to its owner
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    cs.merge(p, stages, ml, csync, [&](int r, int d, float m, float l, const float4& o) {
+    cs.merge(p, stages + (size_t)last * Sh::kStage, ml, csync, [&](int r, int d, float m, float l, const float4& o) {
       const int at = r * (D / 4) + d / 4, owner = at / cols;
       if (!range_ok(owner < C && rank < C, p.status)) return;
       Landing* to = cluster.map_shared_rank(land, owner) + rank * cols + (at - owner * cols);
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       o.w = fmaf(x.o.w, e, o.w);
     }
     const int r = at / (D / 4);
-    store4<D>(p, b, kvh, r, (at - r * (D / 4)) * 4, o, l, r / p.g >= n);
+    store4<D>(p, b, kvh, r, (at - r * (D / 4)) * 4, o, l, token_of(p, r) >= n);
   }
   if (*abort_flag) {  // copies in flight land before the shared memory goes
     const uint64_t t_start = globaltimer_ns();

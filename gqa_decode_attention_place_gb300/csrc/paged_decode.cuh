@@ -29,7 +29,7 @@
 //    of errors that average over the keys; the output's own rounding is the
 //    same size).
 //  * At a piece's end the warps' partials meet in the memory of its last tile,
-//    eight query rows at a time, before that goes back to the ring.
+//    each in the slice that its warp alone has read, so one barrier is enough.
 //  * Work is split as in the 8-bit decode (flat_list.cuh): a flat list of all
 //    tiles over a persistent grid, or for few segments a thread-block cluster
 //    per segment, merged through distributed shared memory.
@@ -90,8 +90,7 @@ struct Shape {
   static constexpr int kStage = 2 * kOp;
   static constexpr int kQStride = D * 2 + 16;     // bytes between query rows: no bank conflicts
   static constexpr int kQ = NT * 8 * kQStride;
-  static constexpr int kMl = kWarps * (NT == 1 ? 8 : 16) * 8;  // bytes of the warps' (reference, sum)
-  static_assert(kWarps * 8 * D * 4 <= kStage, "eight rows of every warp's partials fit a tile");
+  static constexpr int kMl = 2 * kWarps * (NT == 1 ? 8 : 16) * 8;  // bytes of (reference, sum)
 };
 
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
@@ -131,9 +130,13 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                : "memory");
 }
 
+// The token of query row r: r / g, exact for r < 32 and g <= 32.
+__device__ __forceinline__ int token_of(const PagedParams& p, int r) {
+  return (r * p.g_inverse) >> 16;
+}
 // Row of q and out that query row r of (b, kvh) is: rows are ordered token, head.
 __device__ __forceinline__ size_t query_row(const PagedParams& p, int b, int kvh, int r) {
-  const int t = r / p.g;
+  const int t = token_of(p, r);
   return ((size_t)b * p.S + t) * p.Hq + (size_t)kvh * p.g + (r - t * p.g);
 }
 
@@ -157,6 +160,7 @@ struct PagedConsumer {
   int lim[G];           // last cache row that the query row sees, -1: none
   int c, t, warp, lane;
   int team, row_base;   // its place; its first query row
+  int turn;             // pieces merged
 
   __device__ __forceinline__ void init(int warp_, int lane_) {
     warp = warp_;
@@ -165,6 +169,7 @@ struct PagedConsumer {
     t = lane & 3;
     team = warp / kTeam;
     row_base = 16 * team;
+    turn = 0;
   }
   // The queries, negated for a negative score scale.
   __device__ __forceinline__ void load_q(const uint8_t* qs, uint32_t flip) {
@@ -199,7 +204,7 @@ struct PagedConsumer {
   __device__ __forceinline__ void start(const PagedParams& p, int pos, int n) {
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      const int r = row_base + 8 * i + c, tok = r / p.g;
+      const int r = row_base + 8 * i + c, tok = token_of(p, r);
       ref[i] = kMInit;
       lim[i] = r < p.R && tok < n ? pos + tok : -1;
     }
@@ -412,32 +417,40 @@ struct PagedConsumer {
       mma_bf16(y1, w, seen[2], seen[3]);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if ((G == 1 ? c : row_base + 8 * (e >> 1) + c) / p.g == tok) {
+        if (token_of(p, G == 1 ? c : row_base + 8 * (e >> 1) + c) == tok) {
           o0[e] += y0[e];
           o1[e] += y1[e];
         }
     }
   }
 
-  // The piece's end, by all consumer warps: their partials meet in `buf` (a
-  // tile's memory that all of them are done with after the first barrier), and
-  // f(row, dim, reference, sum, four outputs) gets each column of a query row,
-  // merged in warp order.
+  // Float index, from a tile's first byte, of dim d of a warp's partial of row c of
+  // group i: in the keys (i = 0) or values of the warp's own slice, whose 16 rows
+  // of 64 dims are eight of fp32; the dims of rows c turned so that a store's or a
+  // load's lanes fall on different banks.
+  __device__ __forceinline__ static int partial_at(int w, int i, int row, int d, int lb) {
+    return (slice_at(w, lb) + i * Sh::kOp + (d >= 64 ? 128 << lb : 0)) / 4 + row * 64 +
+           ((d & 63) ^ ((row & 3) << 3));
+  }
+  // The piece's end, by all consumer warps: their partials meet in the memory of
+  // its last tile, each warp's in the slice that it alone has read (with two teams
+  // two warps have: they wait for one another first), and f(row, dim, reference,
+  // sum, four outputs) gets each column of a query row, merged in warp order.
+  // ml: [2][query rows][warps], by turns, so that a warp that is still reading one
+  // piece's is not written over by the next.
   template <typename F>
-  __device__ __forceinline__ void merge(const PagedParams& p, uint8_t* buf, float2* ml,
+  __device__ __forceinline__ void merge(const PagedParams& p, uint8_t* tile, float2* ml,
                                         ConsumerSync& csync, F f) {
-    float* part = reinterpret_cast<float*>(buf);
+    float* part = reinterpret_cast<float*>(tile);
     const int tid = warp * 32 + lane, w0 = warp & (kTeam - 1);
-    csync(lane);
-    // with two teams, both teams' groups in a round: [team][warp][8 rows]
+    if (kTeams > 1) csync(lane);
+    ml += (turn & 1) * (Sh::kMl / 16);
+    ++turn;
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      if (8 * i >= p.R) break;
-      if (i > 0) csync(lane);  // the rows before have been read
       if (t == 0)
         ml[(row_base + 8 * i + c) * kTeam + w0] =
             make_float2(ref[i], G == 1 ? sums[0] + sums[2] : sums[2 * i]);
-      float* to = part + (warp * 8 + c) * D;  // dim d at d ^ swizzle(row): no bank conflicts
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
         float2 y = make_float2(o[j][2 * i], o[j][2 * i + 1]);
@@ -445,35 +458,35 @@ struct PagedConsumer {
           y.x += o[j][2];
           y.y += o[j][3];
         }
-        *reinterpret_cast<float2*>(to + ((8 * j + 2 * t) ^ ((c & 3) << 3))) = y;
+        *reinterpret_cast<float2*>(part + partial_at(warp, i, c, 8 * j + 2 * t, p.lb)) = y;
       }
-      csync(lane);
+    }
+    csync(lane);
 #pragma unroll
-      for (int col = tid; col < kTeams * 8 * (D / 4); col += kConsumers) {
-        const int row = col / (D / 4) & 7, tm = col / (8 * (D / 4)), d = col % (D / 4) * 4;
-        const int r = 16 * tm + 8 * i + row;
-        if (r >= p.R) continue;
-        float2 x[kTeam];
-        float M = kMInit, L = 0.f;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int col = tid; col < NT * 8 * (D / 4); col += kConsumers) {
+      const int r = col / (D / 4), d = col % (D / 4) * 4;
+      if (r >= p.R) break;
+      const int tm = r / 16 * (kTeams - 1), i = r / 8 % G, row = r % 8;
+      float2 x[kTeam];
+      float M = kMInit, L = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < kTeam; ++k) {
-          x[k] = ml[r * kTeam + k];
-          M = fmaxf(M, x[k].x);
-        }
-#pragma unroll
-        for (int k = 0; k < kTeam; ++k) {
-          const float e = ex2(x[k].x - M);
-          const float4 v = *reinterpret_cast<const float4*>(
-              part + ((tm * kTeam + k) * 8 + row) * D + (d ^ ((row & 3) << 3)));
-          L = fmaf(x[k].y, e, L);
-          y.x = fmaf(v.x, e, y.x);
-          y.y = fmaf(v.y, e, y.y);
-          y.z = fmaf(v.z, e, y.z);
-          y.w = fmaf(v.w, e, y.w);
-        }
-        f(r, d, M, L, y);
+      for (int k = 0; k < kTeam; ++k) {
+        x[k] = ml[r * kTeam + k];
+        M = fmaxf(M, x[k].x);
       }
+#pragma unroll
+      for (int k = 0; k < kTeam; ++k) {
+        const float e = ex2(x[k].x - M);
+        const float4 v = *reinterpret_cast<const float4*>(
+            part + partial_at(tm * kTeam + k, i, row, d, p.lb));
+        L = fmaf(x[k].y, e, L);
+        y.x = fmaf(v.x, e, y.x);
+        y.y = fmaf(v.y, e, y.y);
+        y.z = fmaf(v.z, e, y.z);
+        y.w = fmaf(v.w, e, y.w);
+      }
+      f(r, d, M, L, y);
     }
   }
 };
@@ -555,7 +568,7 @@ __device__ __forceinline__ void merge_parts(const PagedParams& p, const TileMeta
         o.w = fmaf(x[k].w, e, o.w);
       }
     }
-    store4<D>(p, mt.b, mt.kvh, r, d, o, l, r / p.g >= mt.n);
+    store4<D>(p, mt.b, mt.kvh, r, d, o, l, token_of(p, r) >= mt.n);
   }
 }
 
@@ -800,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (mt.flags & kEnds) {
         if (mt.parts == 1) {
           cs.merge(p, tile, ml, csync, [&](int r, int d, float, float l, const float4& o) {
-            store4<D>(p, mt.b, mt.kvh, r, d, o, l, r / p.g >= mt.n);
+            store4<D>(p, mt.b, mt.kvh, r, d, o, l, token_of(p, r) >= mt.n);
           });
         } else {
           const int slot = part_slot(mt.c0, (int)blockIdx.x - mt.c0);
