@@ -29,7 +29,7 @@ size_t cluster_smem_bytes(int stages, int R, int C) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kClusterThreads, 1)
     paged_cluster_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
   using Sh = Shape<D, NT>;
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     misc[0] = 0;
     fence_mbar_init();
   }
-  for (int i = tid; i < Sh::kQ / 16; i += kThreads)  // rows past R stay zero
+  for (int i = tid; i < Sh::kQ / 16; i += kClusterThreads)  // rows past R stay zero
     reinterpret_cast<uint4*>(qbuf)[i] = make_uint4(0u, 0u, 0u, 0u);
   // (they come before the query copies that land over them)
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -166,7 +166,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every other CTA of the cluster has started; each column goes to its owner
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    cs.merge(p, stages + (size_t)last * Sh::kStage, ml, csync, [&](int r, int d, float m, float l, const float4& o) {
+    uint8_t* tile = stages + (size_t)last * Sh::kStage;
+    cs.stash(p, tile, ml, csync);
+    csync(lane);
+    cs.merge(p, tile, ml, tid, kConsumers, [&](int r, int d, float m, float l, const float4& o) {
       const int at = r * (D / 4) + d / 4, owner = at / cols;
       if (!range_ok(owner < C && rank < C, p.status)) return;
       Landing* to = cluster.map_shared_rank(land, owner) + rank * cols + (at - owner * cols);
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp >= kWarps) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   cluster.sync();
-  for (int j = tid; j < cols; j += kThreads) {
+  for (int j = tid; j < cols; j += kClusterThreads) {
     const int at = rank * cols + j;
     if (at >= R * (D / 4)) break;
     float M = kMInit;

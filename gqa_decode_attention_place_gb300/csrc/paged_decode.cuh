@@ -54,7 +54,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 8;                   // consumer warps
 constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 64;   // and the producers: of keys, of values
+constexpr int kMergeThreads = 64;           // two warps that merge (flat list)
+constexpr int kClusterThreads = kConsumers + 64;  // and the producers: of keys, of values
+constexpr int kThreads = kClusterThreads + kMergeThreads;
 constexpr int kMaxStages = 12;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kE = 1;                       // units of a segment's end (flat_list.cuh)
@@ -160,7 +162,6 @@ struct PagedConsumer {
   int lim[G];           // last cache row that the query row sees, -1: none
   int c, t, warp, lane;
   int team, row_base;   // its place; its first query row
-  int turn;             // pieces merged
 
   __device__ __forceinline__ void init(int warp_, int lane_) {
     warp = warp_;
@@ -169,7 +170,6 @@ struct PagedConsumer {
     t = lane & 3;
     team = warp / kTeam;
     row_base = 16 * team;
-    turn = 0;
   }
   // The queries, negated for a negative score scale.
   __device__ __forceinline__ void load_q(const uint8_t* qs, uint32_t flip) {
@@ -432,24 +432,17 @@ struct PagedConsumer {
     return (slice_at(w, lb) + i * Sh::kOp + (d >= 64 ? 128 << lb : 0)) / 4 + row * 64 +
            ((d & 63) ^ ((row & 3) << 3));
   }
-  // The piece's end, by all consumer warps: their partials meet in the memory of
-  // its last tile, each warp's in the slice that it alone has read (with two teams
-  // two warps have: they wait for one another first), and f(row, dim, reference,
-  // sum, four outputs) gets each column of a query row, merged in warp order.
-  // ml: [2][query rows][warps], by turns, so that a warp that is still reading one
-  // piece's is not written over by the next.
-  template <typename F>
-  __device__ __forceinline__ void merge(const PagedParams& p, uint8_t* tile, float2* ml,
-                                        ConsumerSync& csync, F f) {
+  // A piece's end: the warps' partials meet in the memory of its last tile, each in
+  // the slice that its warp alone has read (with two teams two warps have: they
+  // wait for one another first), their (reference, sum) in ml, [query rows][warps].
+  __device__ __forceinline__ void stash(const PagedParams& p, uint8_t* tile, float2* ml,
+                                        ConsumerSync& csync) const {
     float* part = reinterpret_cast<float*>(tile);
-    const int tid = warp * 32 + lane, w0 = warp & (kTeam - 1);
     if (kTeams > 1) csync(lane);
-    ml += (turn & 1) * (Sh::kMl / 16);
-    ++turn;
 #pragma unroll
     for (int i = 0; i < G; ++i) {
       if (t == 0)
-        ml[(row_base + 8 * i + c) * kTeam + w0] =
+        ml[(row_base + 8 * i + c) * kTeam + (warp & (kTeam - 1))] =
             make_float2(ref[i], G == 1 ? sums[0] + sums[2] : sums[2 * i]);
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
@@ -461,32 +454,46 @@ struct PagedConsumer {
         *reinterpret_cast<float2*>(part + partial_at(warp, i, c, 8 * j + 2 * t, p.lb)) = y;
       }
     }
-    csync(lane);
-#pragma unroll
-    for (int col = tid; col < NT * 8 * (D / 4); col += kConsumers) {
-      const int r = col / (D / 4), d = col % (D / 4) * 4;
-      if (r >= p.R) break;
+  }
+  // f(row, dim, reference, sum, four outputs) for each column of a query row,
+  // merged in warp order, by `threads` threads, a power of two: as many to a row as
+  // there are for R rows, so that a thread makes its row's weights once.
+  template <typename F>
+  __device__ __forceinline__ static void merge(const PagedParams& p, const uint8_t* tile,
+                                               const float2* ml, int tid, int threads, F f) {
+    const float* part = reinterpret_cast<const float*>(tile);
+    int lt = D == 128 ? 5 : 4;  // log2 of the threads to a row
+    while (p.R << lt > threads && lt > 1) --lt;
+    for (int r = tid >> lt; r < p.R; r += threads >> lt) {
       const int tm = r / 16 * (kTeams - 1), i = r / 8 % G, row = r % 8;
-      float2 x[kTeam];
-      float M = kMInit, L = 0.f;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      float e[kTeam], M = kMInit, L = 0.f;
+      {
+        float2 x[kTeam];
 #pragma unroll
-      for (int k = 0; k < kTeam; ++k) {
-        x[k] = ml[r * kTeam + k];
-        M = fmaxf(M, x[k].x);
-      }
+        for (int k = 0; k < kTeam; ++k) {
+          x[k] = ml[r * kTeam + k];
+          M = fmaxf(M, x[k].x);
+        }
 #pragma unroll
-      for (int k = 0; k < kTeam; ++k) {
-        const float e = ex2(x[k].x - M);
-        const float4 v = *reinterpret_cast<const float4*>(
-            part + partial_at(tm * kTeam + k, i, row, d, p.lb));
-        L = fmaf(x[k].y, e, L);
-        y.x = fmaf(v.x, e, y.x);
-        y.y = fmaf(v.y, e, y.y);
-        y.z = fmaf(v.z, e, y.z);
-        y.w = fmaf(v.w, e, y.w);
+        for (int k = 0; k < kTeam; ++k) {
+          e[k] = ex2(x[k].x - M);
+          L = fmaf(x[k].y, e[k], L);
+        }
       }
-      f(r, d, M, L, y);
+#pragma unroll 2
+      for (int d = (tid & ((1 << lt) - 1)) * 4; d < D; d += 4 << lt) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kTeam; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(
+              part + partial_at(tm * kTeam + k, i, row, d, p.lb));
+          y.x = fmaf(v.x, e[k], y.x);
+          y.y = fmaf(v.y, e[k], y.y);
+          y.z = fmaf(v.z, e[k], y.z);
+          y.w = fmaf(v.w, e[k], y.w);
+        }
+        f(r, d, M, L, y);
+      }
     }
   }
 };
@@ -519,7 +526,7 @@ __device__ __forceinline__ void fill_rows(const PagedParams& p, int b, int tid) 
   if (bad && tid == 0) set_status(p.status, ATTN_DEV_BAD_POSITION);
   const uint32_t v = bad ? 0x7fff7fffu : 0u;
   uint4* row = reinterpret_cast<uint4*>(p.out + (size_t)b * p.S * p.Hq * D);
-  for (int i = tid; i < p.S * p.Hq * D / 8; i += kThreads) row[i] = make_uint4(v, v, v, v);
+  for (int i = tid; i < p.S * p.Hq * D / 8; i += kClusterThreads) row[i] = make_uint4(v, v, v, v);
 }
 
 // Where part r of a segment lies: a CTA holds at most one segment's first part
@@ -531,10 +538,11 @@ __device__ __forceinline__ bool slot_ok(const PagedParams& p, int slot) {
 
 // Merge the parts of a split segment, in CTA order, eight in one round trip.
 template <int D>
-__device__ __forceinline__ void merge_parts(const PagedParams& p, const TileMeta& mt, int tid) {
+__device__ __forceinline__ void merge_parts(const PagedParams& p, const TileMeta& mt, int tid,
+                                            int threads) {
   const int R = p.R;
   const int parts = slot_ok(p, part_slot(mt.c0, mt.parts - 1)) ? mt.parts : 0;
-  for (int col = tid; col < R * (D / 4); col += kConsumers) {
+  for (int col = tid; col < R * (D / 4); col += threads) {
     const int r = col / (D / 4), d = (col % (D / 4)) * 4;
     float M = kMInit, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -580,6 +588,45 @@ __device__ __forceinline__ int page_ok(const PagedParams& p, int page) {
   return -1;
 }
 
+// A piece's output: whole, or this CTA's part of a segment.
+template <int D, int NT>
+__device__ __forceinline__ void put_piece(const PagedParams& p, const TileMeta& mt,
+                                          const uint8_t* tile, const float2* ml, int tid,
+                                          int threads) {
+  if (mt.parts == 1) {
+    PagedConsumer<D, NT>::merge(p, tile, ml, tid, threads,
+                                [&](int r, int d, float, float l, const float4& o) {
+      store4<D>(p, mt.b, mt.kvh, r, d, o, l, token_of(p, r) >= mt.n);
+    });
+    return;
+  }
+  const int slot = part_slot(mt.c0, (int)blockIdx.x - mt.c0);
+  PagedConsumer<D, NT>::merge(p, tile, ml, tid, threads,
+                              [&](int r, int d, float m, float l, const float4& o) {
+    if (!slot_ok(p, slot)) return;
+    *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * p.R + r) * D + d) = o;
+    if (d == 0)
+      *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * p.R + r) * 2) = make_float2(m, l);
+  });
+}
+// The CTA's part is written (by threads that `sync` joins): the last CTA of the
+// segment's to come here merges the parts.
+template <int D>
+__device__ __forceinline__ void join_parts(const PagedParams& p, const TileMeta& mt, int tid,
+                                           int threads, ConsumerSync& sync, int* flag, int lane) {
+  sync(lane);
+  if (tid == 0) {
+    uint32_t* counter = p.counters + mt.b * p.Hkv + mt.kvh;
+    __threadfence();  // (the other threads' stores came before the barrier)
+    const bool last = !*sync.abort_flag && atomicAdd(counter, 1u) + 1 == (uint32_t)mt.parts;
+    if (last) *counter = 0;
+    __threadfence();
+    *flag = last;
+  }
+  sync(lane);
+  if (*(volatile int*)flag && !*sync.abort_flag) merge_parts<D>(p, mt, tid, threads);
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -591,9 +638,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* qbuf = stages + (size_t)NS * Sh::kStage;            // [NS][NT * 8] query rows
   TileMeta* meta = reinterpret_cast<TileMeta*>(qbuf + NS * Sh::kQ);
   float2* ml = reinterpret_cast<float2*>(meta + NS);             // [query rows][warps]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ml + Sh::kMl / 8);  // full [NS], empty [NS], sync
-  int* misc = reinterpret_cast<int*>(bars + 2 * NS + 1);  // [0] abort, [1] last to arrive,
-                                                          // [2] longest segment, [8..16) scan
+  // full [NS], empty [NS], the consumers' and the merge warps' sync, merge full [2], empty [2]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ml + Sh::kMl / 8);
+  uint64_t* m_full = bars + 2 * NS + 2;
+  uint64_t* m_empty = m_full + 2;
+  // [0] abort, [1] last to arrive (consumers), [2] longest segment, [3] last to arrive (merge
+  // warps), [4..6) stage of the piece's last tile, [8..16) scan
+  int* misc = reinterpret_cast<int*>(m_empty + 2);
   int* prefix = misc + 16;                                // [B + 1]
   int* spos = prefix + B + 1;                             // [B]
   uint8_t* snew = reinterpret_cast<uint8_t*>(spos + B);   // [B]
@@ -607,6 +658,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars[NS + s]), kWarps);
     }
     mbar_init(smem_u32(&bars[2 * NS]), kWarps);
+    mbar_init(smem_u32(&bars[2 * NS + 1]), kMergeThreads / 32);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&m_full[i]), kWarps);
+      mbar_init(smem_u32(&m_empty[i]), kMergeThreads / 32);
+    }
     misc[0] = misc[2] = 0;
     fence_mbar_init();
   }
@@ -655,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   for (int b = blockIdx.x; b < B; b += gridDim.x)
-    if (prefix[b + 1] == prefix[b]) fill_rows<D>(p, b, tid);  // it takes no part
+    if (tid < kClusterThreads && prefix[b + 1] == prefix[b]) fill_rows<D>(p, b, tid);  // no part
 
   const long long T = (long long)Hkv * carry;  // all units
   const long long nseg = (long long)B * Hkv;
@@ -680,7 +736,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   flat_start<kE>(w, rg, prefix, spos, B, Hkv);
   if (w.u >= w.end) return;  // end units alone
 
-  if (warp >= kWarps) {
+  if (warp >= kWarps + 2) {
+    // --------------------------------------------------------------- merge --
+    // The consumers leave a piece's partials in its last tile and go on; these
+    // two warps write its output, or its part of a segment's, give the tile back to
+    // the ring, and settle who merges the parts.  (512 sequences of up to 128 rows:
+    // 54 -> MM us.)  The last piece is the consumers', who have nothing else to do.
+    const int mtid = tid - kClusterThreads;
+    ConsumerSync msync{smem_u32(&bars[2 * NS + 1]), abort_flag, p.status, 0u};
+    for (int turn = 0;; ++turn) {
+      const int buf = turn & 1;
+      if (!consumer_wait(smem_u32(&m_full[buf]), (turn >> 1) & 1u, abort_flag, p.status, lane))
+        break;
+      const int s = *(volatile int*)(misc + 4 + buf);
+      if (s < 0) break;
+      const TileMeta mt = meta[s];
+      put_piece<D, NT>(p, mt, stages + (size_t)s * Sh::kStage, ml + buf * (Sh::kMl / 16), mtid,
+                       kMergeThreads);
+      __syncwarp();
+      if (lane < kWarps * 32 / kMergeThreads) mbar_arrive(smem_u32(&bars[NS + s]));  // for all
+      if (lane == 0) mbar_arrive(smem_u32(&m_empty[buf]));
+      if (mt.parts > 1)
+        join_parts<D>(p, mt, mtid, kMergeThreads, msync, misc + 3, lane);
+    }
+  } else if (warp >= kWarps) {
     // ----------------------------------------------------------- producers --
     // Tiles go in batches of kBatch, lane kSlices * ti + slice looks after slice
     // `slice` of the batch's tile ti; a batch's table entries are loaded while
@@ -746,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int next = fetch(w);
       const int page = entry == kNoRows ? -1 : page_ok(p, entry);
       TileMeta mt = {};
-      if (on && slice == 0) describe(cur, mt);
+      if (keys && on && slice == 0) describe(cur, mt);
       const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
       const bool lead = page >= 0 && in_box == 0;
       const uint32_t boxes = __ballot_sync(0xffffffffu, lead);
@@ -799,55 +878,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     ConsumerSync csync{smem_u32(&bars[2 * NS]), abort_flag, p.status, 0u};
     PagedConsumer<D, NT> cs;
     cs.init(warp, lane);
-    int s = 0;
+    int s = 0, turn = 0;
     uint32_t ph = 0;
     for (;;) {
       if (!consumer_wait(smem_u32(&bars[s]), ph, abort_flag, p.status, lane)) break;
-      const TileMeta mt = meta[s];
+      const int flags = meta[s].flags;
       uint8_t* tile = stages + (size_t)s * Sh::kStage;
-      if (mt.flags & kStarts) {
+      if (flags & kStarts) {
         cs.load_q(qbuf + s * Sh::kQ, p.flip);
-        cs.start(p, mt.pos, mt.n);
+        cs.start(p, meta[s].pos, meta[s].n);
       }
-      cs.tile(tile, p, mt);
-      if (mt.flags & kEnds) {
-        if (mt.parts == 1) {
-          cs.merge(p, tile, ml, csync, [&](int r, int d, float, float l, const float4& o) {
-            store4<D>(p, mt.b, mt.kvh, r, d, o, l, token_of(p, r) >= mt.n);
-          });
-        } else {
-          const int slot = part_slot(mt.c0, (int)blockIdx.x - mt.c0);
-          cs.merge(p, tile, ml, csync, [&](int r, int d, float m, float l, const float4& o) {
-            if (!slot_ok(p, slot)) return;
-            *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * p.R + r) * D + d) = o;
-            if (d == 0)
-              *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * p.R + r) * 2) =
-                  make_float2(m, l);
-          });
-        }
+      cs.tile(tile, p, meta[s]);
+      if (flags & kEnds) {
+        const int buf = turn & 1;
+        float2* to = ml + buf * (Sh::kMl / 16);
+        if (turn > 1 && !consumer_wait(smem_u32(&m_empty[buf]), ((turn >> 1) & 1u) ^ 1u,
+                                       abort_flag, p.status, lane))
+          break;
+        ++turn;
+        if (tid == 0) misc[4 + buf] = flags & kLast ? -1 : s;
+        cs.stash(p, tile, to, csync);
         // (this memory was written here; copies land in it next)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&m_full[buf]));
+        if (flags & kLast) {
+          csync(lane);
+          if (*abort_flag) break;
+          const TileMeta mt = meta[s];
+          put_piece<D, NT>(p, mt, tile, to, tid, kConsumers);
+          if (mt.parts > 1) join_parts<D>(p, mt, tid, kConsumers, csync, misc + 1, lane);
+          break;
+        }
+      } else {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars[NS + s]));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars[NS + s]));
       if (++s == NS) {
         s = 0;
         ph ^= 1u;
       }
-      if ((mt.flags & kEnds) && mt.parts > 1) {
-        csync(lane);
-        if (tid == 0) {
-          uint32_t* counter = p.counters + mt.b * Hkv + mt.kvh;
-          __threadfence();  // (the other threads' stores came before the barrier)
-          const bool last = !*abort_flag && atomicAdd(counter, 1u) + 1 == (uint32_t)mt.parts;
-          if (last) *counter = 0;
-          __threadfence();
-          misc[1] = last;
-        }
-        csync(lane);
-        if (misc[1] && !*abort_flag) merge_parts<D>(p, mt, tid);
-      }
-      if (mt.flags & kLast) break;
     }
   }
   if (*abort_flag) {  // copies in flight land before the shared memory goes
@@ -870,7 +940,7 @@ namespace {
 template <int D, int NT>
 size_t flat_smem_bytes(int stages, int B) {
   using Sh = Shape<D, NT>;
-  return (size_t)stages * (Sh::kStage + Sh::kQ + sizeof(TileMeta) + 16) + Sh::kMl + 8 + 64 +
+  return (size_t)stages * (Sh::kStage + Sh::kQ + sizeof(TileMeta) + 16) + Sh::kMl + 48 + 64 +
          (size_t)9 * B + 16;
 }
 
@@ -904,7 +974,7 @@ cudaError_t find_device(PagedDevice& d, int dev) {
   for (int c = 1; c <= kMaxCluster; ++c) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(c * 64);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kClusterThreads);
     cfg.dynamicSmemBytes = kMaxSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -989,7 +1059,7 @@ cudaError_t launch_paged(PagedParams& p, const PagedPool& pool, cudaStream_t str
       --p.stages;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * C));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kClusterThreads);
     cfg.dynamicSmemBytes = cluster_smem_bytes<D, NT>(p.stages, p.R, C);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
