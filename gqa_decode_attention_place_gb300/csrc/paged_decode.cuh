@@ -765,7 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // `slice` of the batch's tile ti; a batch's table entries are loaded while
     // the one before it is issued.
     constexpr int kSlices = Sh::kSlices, kBatch = Sh::kBatch;
-    const bool keys = warp == kWarps;  // this warp also describes the tile and brings the queries
+    const bool keys = warp == kWarps;  // this warp also describes the tile, the other brings the
+                                       // queries
     const int ti = lane / kSlices, slice = lane % kSlices;
     const int box_rows = 1 << p.lb, in_box = (slice * 16) & (box_rows - 1);
     const int page_mask = (1 << p.lp) - 1;
@@ -776,13 +777,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!range_ok((row >> p.lp) < p.M, p.status)) return kNoRows;
       return p.table[(size_t)w.b * p.M + (row >> p.lp)];
     };
-    auto step = [&](FlatWalk& w, int n) {  // n tiles on, as far as the range goes
-      if (w.k + n < w.nt && w.u + n < w.end) {
-        w.k += n;
-        w.u += n;
-        return;
+    // This lane's tile of the batch that starts at w, which goes on to the next one
+    // (the whole warp walks alike: lanes that walked for themselves took turns).
+    auto take = [&](FlatWalk& w) -> FlatWalk {
+      FlatWalk mine = w;
+      if (w.k + kBatch < w.nt && w.u + kBatch < w.end) {
+        mine.k += ti;
+        mine.u += ti;
+        w.k += kBatch;
+        w.u += kBatch;
+        return mine;
       }
-      for (int k = 0; k < n && w.u < w.end; ++k) flat_next<kE>(w, rg, prefix, spos, B, Hkv);
+#pragma unroll 1
+      for (int k = 0; k < kBatch; ++k) {
+        if (k == ti) mine = w;
+        if (w.u < w.end) flat_next<kE>(w, rg, prefix, spos, B, Hkv);
+      }
+      return mine;
     };
     long long last_end = w.end;  // of the part of the range done last
     if (rg.tA < rg.t1) {
@@ -813,16 +824,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int s = 0;
     uint32_t pass = 0;
-    step(w, ti);
-    FlatWalk cur = w;
-    int entry = fetch(w);
+    FlatWalk cur = take(w);
+    int entry = fetch(cur);
     bool ok = true;
     while (ok) {
       const bool on = cur.u < cur.end;
       const int n_q = __popc(__ballot_sync(0xffffffffu, on)) / kSlices;  // tiles of the batch
       if (n_q == 0) break;
-      step(w, kBatch);
-      const int next = fetch(w);
+      const FlatWalk ahead = take(w);
+      const int next = fetch(ahead);
       const int page = entry == kNoRows ? -1 : page_ok(p, entry);
       TileMeta mt = {};
       if (keys && on && slice == 0) describe(cur, mt);
@@ -842,14 +852,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t full = smem_u32(&bars[s]);
-        const bool first = __shfl_sync(0xffffffffu, (mt.flags & kStarts) != 0, kSlices * q);
+        const bool first = __shfl_sync(0xffffffffu, cur.k == 0 || cur.u == rg.t0, kSlices * q);
         if (lane == kSlices * q) {
           mt.flags |= (there >> (kSlices * q)) & ((1u << kSlices) - 1u);
           if (keys) meta[s] = mt;
           if (!skip)
             mbar_arrive_expect_tx(full, __popc((boxes >> (kSlices * q)) & ((1u << kSlices) - 1u)) *
                                                 ((uint32_t)box_rows * D * 2u) +
-                                            (keys && first ? (uint32_t)p.R * D * 2u : 0u));
+                                            (!keys && first ? (uint32_t)p.R * D * 2u : 0u));
         }
         __syncwarp();
         const bool hold = __shfl_sync(0xffffffffu, skip, kSlices * q);
@@ -858,9 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_5d(dst + (keys ? 0 : Sh::kOp), keys ? &tm_k : &tm_v, 0,
                       (cur.k * Sh::kTile + slice * 16) & page_mask, 0, cur.kvh, page, full);
         }
-        if (first && !hold && keys) {  // the piece's query rows, one by each lane
-          const int b = __shfl_sync(0xffffffffu, mt.b, kSlices * q);
-          const int kvh = __shfl_sync(0xffffffffu, mt.kvh, kSlices * q);
+        if (first && !hold && !keys) {  // the piece's query rows, one by each lane
+          const int b = __shfl_sync(0xffffffffu, cur.b, kSlices * q);
+          const int kvh = __shfl_sync(0xffffffffu, cur.kvh, kSlices * q);
           if (lane < p.R)
             bulk_load(smem_u32(qbuf + s * Sh::kQ) + lane * Sh::kQStride,
                       p.q + query_row(p, b, kvh, lane) * D, D * 2, full);
@@ -870,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++pass;
         }
       }
-      cur = w;
+      cur = ahead;
       entry = next;
     }
   } else {
