@@ -59,7 +59,9 @@ constexpr int kClusterThreads = kConsumers + 64;  // and the producers: of keys,
 constexpr int kThreads = kClusterThreads + kMergeThreads;
 constexpr int kMaxStages = 12;
 constexpr int kMaxSmem = 227 * 1024;
-constexpr int kE = 1;                       // units of a segment's end (flat_list.cuh)
+// What a segment's end costs, in tiles' time (flat_list.cuh; with 1 for all, 32 ragged
+// sequences of up to 16384 rows and 32 query rows: 185 us instead of 173).
+template <int NT> constexpr int kEndUnits = NT == 4 ? 4 : NT == 2 ? 3 : 1;
 constexpr int kWholeTiles = 4;              // segments this short are not split
 // Whole segments, one CTA each (below): a lone CTA's tile takes kWholeNum / kWholeDen of
 // its share of a busy GPU, and a merge as long as kMergeCost / kWholeDen tiles.
@@ -281,18 +283,11 @@ struct PagedConsumer {
         mma_bf16(s[n][1][N == 1 ? k & 1 : 0], a, b[2], b[3]);
       }
     }
-    // the first values, on their way while the weights are made
-    constexpr int kAhead = FULL ? (N == 2 || (G == 2 && D == 128) ? 2 : 4) : 0;
     auto load_v = [&](uint32_t (&b)[4], int d, int n) {
       const int ch = 2 * d + (i8 >> 1);
       ldmatrix4_trans(b, at[n] + Sh::kOp + (8 * (i8 & 1) + r8) * 128 + (2 * d >= 8 ? half : 0) +
                              (((ch & 7) ^ r8) << 4));
     };
-    uint32_t ahead[kAhead > 0 ? kAhead : 1][N][4];
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d)
-#pragma unroll
-      for (int n = 0; n < N; ++n) load_v(ahead[d][n], d, n);
     // weights as the second product's A operand: rows 2t, 2t+1 and 8 on of a slice
     uint32_t w[N][4], rest[N][4];
     float x[N][G][4], mine[G];
@@ -364,12 +359,7 @@ struct PagedConsumer {
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         uint32_t b[4];  // 16 dims: rows 0..7 and 8..15 of the first 8, then of the others
-        if (d < kAhead) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) b[e] = ahead[d < kAhead ? d : 0][n][e];
-        } else {
-          load_v(b, d, n);
-        }
+        load_v(b, d, n);
         if (!FULL) {
           // rows past the last token may be NaN: 0 * NaN would spread
 #pragma unroll
@@ -536,47 +526,73 @@ __device__ __forceinline__ bool slot_ok(const PagedParams& p, int slot) {
   return range_ok(slot >= 0 && slot < 2 * kPagedMaxGrid, p.status);
 }
 
-// Merge the parts of a split segment, in CTA order, eight in one round trip.
+// One column (four dims) of a split segment from N of its parts on, k0 .. k0 + N - 1,
+// all loaded in one round trip, onto what the parts before gave.
+struct Column {
+  float M, l;
+  float4 o;
+};
+template <int D, int N>
+__device__ __forceinline__ void join_column(const PagedParams& p, const TileMeta& mt, int parts,
+                                            int k0, int r, int d, Column& c) {
+  float2 ml[N];
+  float4 x[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    ml[k] = make_float2(kMInit, 0.f);
+    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k0 + k < parts) {
+      const size_t slot = part_slot(mt.c0, k0 + k);
+      ml[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (slot * p.R + r) * 2));
+      x[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot * p.R + r) * D + d));
+    }
+  }
+  float top = c.M;
+#pragma unroll
+  for (int k = 0; k < N; ++k) top = fmaxf(top, ml[k].x);
+  const float a = ex2(c.M - top);
+  c.M = top;
+  c.l *= a;
+  c.o = make_float4(c.o.x * a, c.o.y * a, c.o.z * a, c.o.w * a);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float e = ex2(ml[k].x - top);
+    c.l = fmaf(ml[k].y, e, c.l);
+    c.o.x = fmaf(x[k].x, e, c.o.x);
+    c.o.y = fmaf(x[k].y, e, c.o.y);
+    c.o.z = fmaf(x[k].z, e, c.o.z);
+    c.o.w = fmaf(x[k].w, e, c.o.w);
+  }
+}
+// Merge the parts of a split segment, in CTA order.
 template <int D>
 __device__ __forceinline__ void merge_parts(const PagedParams& p, const TileMeta& mt, int tid,
                                             int threads) {
-  const int R = p.R;
   const int parts = slot_ok(p, part_slot(mt.c0, mt.parts - 1)) ? mt.parts : 0;
-  for (int col = tid; col < R * (D / 4); col += threads) {
-    const int r = col / (D / 4), d = (col % (D / 4)) * 4;
-    float M = kMInit, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < parts; k0 += 8) {
-      float2 ml[8];
-      float4 x[8];
+  const int cols = p.R * (D / 4);
+  if (parts <= 2) {  // most segments: four columns in one round trip
+    for (int c0 = tid; c0 < cols; c0 += 4 * threads) {
+      Column c[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        ml[k] = make_float2(kMInit, 0.f);
-        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k0 + k < parts) {
-          const size_t slot = part_slot(mt.c0, k0 + k);
-          ml[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (slot * R + r) * 2));
-          x[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (slot * R + r) * D + d));
-        }
+      for (int u = 0; u < 4; ++u) {
+        const int col = c0 + u * threads, r = col / (D / 4), d = col % (D / 4) * 4;
+        c[u] = Column{kMInit, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (col < cols) join_column<D, 2>(p, mt, parts, 0, r, d, c[u]);
       }
-      float top = M;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].x);
-      const float a = ex2(M - top);
-      M = top;
-      l *= a;
-      o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float e = ex2(ml[k].x - M);
-        l = fmaf(ml[k].y, e, l);
-        o.x = fmaf(x[k].x, e, o.x);
-        o.y = fmaf(x[k].y, e, o.y);
-        o.z = fmaf(x[k].z, e, o.z);
-        o.w = fmaf(x[k].w, e, o.w);
+      for (int u = 0; u < 4; ++u) {
+        const int col = c0 + u * threads, r = col / (D / 4), d = col % (D / 4) * 4;
+        if (col < cols)
+          store4<D>(p, mt.b, mt.kvh, r, d, c[u].o, c[u].l, token_of(p, r) >= mt.n);
       }
     }
-    store4<D>(p, mt.b, mt.kvh, r, d, o, l, token_of(p, r) >= mt.n);
+    return;
+  }
+  for (int col = tid; col < cols; col += threads) {
+    const int r = col / (D / 4), d = col % (D / 4) * 4;
+    Column c{kMInit, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int k0 = 0; k0 < parts; k0 += 8) join_column<D, 8>(p, mt, parts, k0, r, d, c);
+    store4<D>(p, mt.b, mt.kvh, r, d, c.o, c.l, token_of(p, r) >= mt.n);
   }
 }
 
@@ -632,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
   using Sh = Shape<D, NT>;
+  constexpr int kE = kEndUnits<NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int NS = p.stages, B = p.B, Hkv = p.Hkv;
   uint8_t* stages = smem;
