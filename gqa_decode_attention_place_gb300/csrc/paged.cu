@@ -146,8 +146,11 @@ cudaError_t launch_paged_decode(const void* q, const int32_t* positions, const i
   // (a scale of zero: tiny, so that masked scores stay -inf times it)
   p.qscale = fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-37f);
   p.flip = scale < 0.f ? 0x80008000u : 0u;
-  return pool.D == 64 ? launch_paged_decode_64(p, pool, stream)
-                      : launch_paged_decode_128(p, pool, stream);
+  if (pool.D == 64)
+    return S == 1 ? launch_paged_decode_64(p, pool, stream)
+                  : launch_paged_decode_64_drafts(p, pool, stream);
+  return S == 1 ? launch_paged_decode_128(p, pool, stream)
+                : launch_paged_decode_128_drafts(p, pool, stream);
 }
 
 cudaError_t paged_append_read_skips(uint32_t* count) {

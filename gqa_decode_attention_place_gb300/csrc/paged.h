@@ -47,8 +47,13 @@ struct PagedParams {
 
 // Makes the pool's tensor maps for copies of `rows` rows.
 bool paged_maps(const PagedPool& pool, int rows, CUtensorMap* mk, CUtensorMap* mv);
+// For head dims 64 and 128, one new token or several (paged_decode_d*.cu).
 cudaError_t launch_paged_decode_64(PagedParams& p, const PagedPool& pool, cudaStream_t stream);
+cudaError_t launch_paged_decode_64_drafts(PagedParams& p, const PagedPool& pool,
+                                          cudaStream_t stream);
 cudaError_t launch_paged_decode_128(PagedParams& p, const PagedPool& pool, cudaStream_t stream);
+cudaError_t launch_paged_decode_128_drafts(PagedParams& p, const PagedPool& pool,
+                                           cudaStream_t stream);
 
 struct PagedWorkspace {
   size_t counters_off, ml_off, o_off, total;  // the status word comes first

@@ -28,7 +28,7 @@ size_t cluster_smem_bytes(int stages, int R, int C) {
          (size_t)C * landing_cols(R, D, C) * sizeof(Landing) + 16;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool DRAFTS>
 __global__ void __launch_bounds__(kClusterThreads, 1)
     paged_cluster_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
   } else {
     // ----------------------------------------------------------- consumers --
     ConsumerSync csync{smem_u32(&bars[2 * NS]), abort_flag, p.status, 0u};
-    PagedConsumer<D, NT> cs;
+    PagedConsumer<D, NT, DRAFTS> cs;
     cs.init(warp, lane);
     cs.start(p, pos, n);
     int s = 0, last = 0;  // last: the stage of the last tile

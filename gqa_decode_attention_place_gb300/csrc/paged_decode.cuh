@@ -1,6 +1,7 @@
 // paged_decode.cuh -- split-KV decode attention over a paged bf16 cache, S new
-// tokens per sequence: the kernels and their launch, included by one
-// translation unit per head dim (paged_decode_d64.cu, paged_decode_d128.cu).
+// tokens per sequence: the kernels and their launch, included by one translation
+// unit per head dim, and for one token or several (DRAFTS: what several need makes
+// a kernel's code longer, which one stream's step pays for: 9.1 and 9.5 us).
 //
 // For sequence b, new token t, query head h and KV head h/g:
 //   out = softmax_j(scale q . K_j) V_j      over rows j = 0 .. positions[b] + t,
@@ -150,7 +151,7 @@ __device__ __forceinline__ size_t query_row(const PagedParams& p, int b, int kvh
 // query rows (NT = 4) half of the warps take 32 each for query rows 0..15, and the
 // other half the same for 16..31.  (Warps with all 32 query rows would hold 128
 // registers of outputs, and spill.)
-template <int D, int NT>
+template <int D, int NT, bool DRAFTS>
 struct PagedConsumer {
   using Sh = Shape<D, NT>;
   static constexpr int G = NT == 1 ? 1 : 2;       // 8-row groups of a warp
@@ -206,7 +207,7 @@ struct PagedConsumer {
   __device__ __forceinline__ void start(const PagedParams& p, int pos, int n) {
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      const int r = row_base + 8 * i + c, tok = token_of(p, r);
+      const int r = row_base + 8 * i + c, tok = DRAFTS ? token_of(p, r) : 0;
       ref[i] = kMInit;
       lim[i] = r < p.R && tok < n ? pos + tok : -1;
     }
@@ -229,16 +230,17 @@ struct PagedConsumer {
     const int first = warp & (kTeam - 1);
     constexpr bool kTwo = Sh::kSlices == 2 * kTeam;
     constexpr int kAll = kTwo ? 1 | (1 << kTeam) : 1;
-    if (kTwo && mt.row0 + 16 * (first + kTeam) + 15 <= mt.pos &&
-        ((mt.flags >> first) & kAll) == kAll) {
+    // full: every row is there and seen by every query row in use
+    if (((mt.flags >> first) & kAll) == kAll &&
+        mt.row0 + 16 * (first + (kTwo ? kTeam : 0)) + 15 <= mt.pos) {
       slices<kTwo ? 2 : 1, true>(ks, first, p, mt);
       return;
     }
 #pragma unroll 1
     for (int sl = first; sl < Sh::kSlices; sl += kTeam) {
       if (!((mt.flags >> sl) & 1)) continue;  // no rows there
-      // full: every row is seen by every query row in use
-      if (mt.row0 + 16 * sl + 15 <= mt.pos) slices<1, true>(ks, sl, p, mt);
+      // (one slice that is full, where two are taken, does without the masks)
+      if (kTwo && mt.row0 + 16 * sl + 15 <= mt.pos) slices<1, true>(ks, sl, p, mt);
       else slices<1, false>(ks, sl, p, mt);
     }
   }
@@ -353,7 +355,7 @@ struct PagedConsumer {
       if (kTwoParts) mma_bf16(sums, rest[n], 0x3f803f80u, 0x3f803f80u);
     }
     const int seen = mt.pos + mt.n - row0;  // rows that some token may see
-    const bool drafts = !FULL && mt.n > 1;
+    const bool drafts = DRAFTS && !FULL && mt.n > 1;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
 #pragma unroll
@@ -605,19 +607,19 @@ __device__ __forceinline__ int page_ok(const PagedParams& p, int page) {
 }
 
 // A piece's output: whole, or this CTA's part of a segment.
-template <int D, int NT>
+template <int D, int NT, bool DRAFTS>
 __device__ __forceinline__ void put_piece(const PagedParams& p, const TileMeta& mt,
                                           const uint8_t* tile, const float2* ml, int tid,
                                           int threads) {
   if (mt.parts == 1) {
-    PagedConsumer<D, NT>::merge(p, tile, ml, tid, threads,
+    PagedConsumer<D, NT, DRAFTS>::merge(p, tile, ml, tid, threads,
                                 [&](int r, int d, float, float l, const float4& o) {
       store4<D>(p, mt.b, mt.kvh, r, d, o, l, token_of(p, r) >= mt.n);
     });
     return;
   }
   const int slot = part_slot(mt.c0, (int)blockIdx.x - mt.c0);
-  PagedConsumer<D, NT>::merge(p, tile, ml, tid, threads,
+  PagedConsumer<D, NT, DRAFTS>::merge(p, tile, ml, tid, threads,
                               [&](int r, int d, float m, float l, const float4& o) {
     if (!slot_ok(p, slot)) return;
     *reinterpret_cast<float4*>(p.part_o + ((size_t)slot * p.R + r) * D + d) = o;
@@ -643,7 +645,7 @@ __device__ __forceinline__ void join_parts(const PagedParams& p, const TileMeta&
   if (*(volatile int*)flag && !*sync.abort_flag) merge_parts<D>(p, mt, tid, threads);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool DRAFTS>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
@@ -768,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s = *(volatile int*)(misc + 4 + buf);
       if (s < 0) break;
       const TileMeta mt = meta[s];
-      put_piece<D, NT>(p, mt, stages + (size_t)s * Sh::kStage, ml + buf * (Sh::kMl / 16), mtid,
+      put_piece<D, NT, DRAFTS>(p, mt, stages + (size_t)s * Sh::kStage, ml + buf * (Sh::kMl / 16), mtid,
                        kMergeThreads);
       __syncwarp();
       if (lane < kWarps * 32 / kMergeThreads) mbar_arrive(smem_u32(&bars[NS + s]));  // for all
@@ -903,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ----------------------------------------------------------- consumers --
     ConsumerSync csync{smem_u32(&bars[2 * NS]), abort_flag, p.status, 0u};
-    PagedConsumer<D, NT> cs;
+    PagedConsumer<D, NT, DRAFTS> cs;
     cs.init(warp, lane);
     int s = 0, turn = 0;
     uint32_t ph = 0;
@@ -933,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           csync(lane);
           if (*abort_flag) break;
           const TileMeta mt = meta[s];
-          put_piece<D, NT>(p, mt, tile, to, tid, kConsumers);
+          put_piece<D, NT, DRAFTS>(p, mt, tile, to, tid, kConsumers);
           if (mt.parts > 1) join_parts<D>(p, mt, tid, kConsumers, csync, misc + 1, lane);
           break;
         }
@@ -978,25 +980,25 @@ struct PagedDevice {
   int clusters[kMaxCluster + 1];
 };
 
-template <int D, int NT>
+template <int D, int NT, bool DRAFTS>
 cudaError_t set_attributes() {
   cudaError_t e = cudaFuncSetAttribute(
-      paged_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+      paged_decode_kernel<D, NT, DRAFTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(paged_cluster_kernel<D, NT>,
+    e = cudaFuncSetAttribute(paged_cluster_kernel<D, NT, DRAFTS>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(paged_cluster_kernel<D, NT>,
+    e = cudaFuncSetAttribute(paged_cluster_kernel<D, NT, DRAFTS>,
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e;
 }
 
-template <int D>
+template <int D, bool DRAFTS>
 cudaError_t find_device(PagedDevice& d, int dev) {
   cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = set_attributes<D, 1>();
-  if (e == cudaSuccess) e = set_attributes<D, 2>();
-  if (e == cudaSuccess) e = set_attributes<D, 4>();
+  if (e == cudaSuccess) e = set_attributes<D, 1, DRAFTS>();
+  if (e == cudaSuccess) e = set_attributes<D, 2, DRAFTS>();
+  if (e == cudaSuccess) e = set_attributes<D, 4, DRAFTS>();
   if (e != cudaSuccess) return e;
   for (int c = 1; c <= kMaxCluster; ++c) {
     cudaLaunchConfig_t cfg = {};
@@ -1010,7 +1012,7 @@ cudaError_t find_device(PagedDevice& d, int dev) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&d.clusters[c], paged_cluster_kernel<D, 1>, &cfg) !=
+    if (cudaOccupancyMaxActiveClusters(&d.clusters[c], paged_cluster_kernel<D, 1, DRAFTS>, &cfg) !=
         cudaSuccess) {
       cudaGetLastError();
       d.clusters[c] = 0;
@@ -1019,7 +1021,7 @@ cudaError_t find_device(PagedDevice& d, int dev) {
   return cudaSuccess;
 }
 
-template <int D>
+template <int D, bool DRAFTS>
 cudaError_t paged_device(const PagedDevice** out) {
   static PagedDevice known[64];
   static std::atomic<bool> ready[64];
@@ -1031,7 +1033,7 @@ cudaError_t paged_device(const PagedDevice** out) {
   if (!ready[dev].load(std::memory_order_acquire)) {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev].load(std::memory_order_relaxed)) {
-      e = find_device<D>(known[dev], dev);
+      e = find_device<D, DRAFTS>(known[dev], dev);
       if (e != cudaSuccess) return e;
       ready[dev].store(true, std::memory_order_release);
     }
@@ -1069,10 +1071,10 @@ int cluster_size(const PagedParams& p, const PagedDevice& d) {
   return clusters <= 12.f + share ? c : 0;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool DRAFTS>
 cudaError_t launch_paged(PagedParams& p, const PagedPool& pool, cudaStream_t stream) {
   const PagedDevice* d = nullptr;
-  cudaError_t e = paged_device<D>(&d);
+  cudaError_t e = paged_device<D, DRAFTS>(&d);
   if (e != cudaSuccess) return e;
   const int rows = min(pool.page, Shape<D, NT>::kTile);
   p.lb = rows == 16 ? 4 : rows == 32 ? 5 : rows == 64 ? 6 : 7;
@@ -1098,19 +1100,19 @@ cudaError_t launch_paged(PagedParams& p, const PagedPool& pool, cudaStream_t str
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, paged_cluster_kernel<D, NT>, mk, mv, p);
+    e = cudaLaunchKernelEx(&cfg, paged_cluster_kernel<D, NT, DRAFTS>, mk, mv, p);
     return e != cudaSuccess ? e : cudaGetLastError();
   }
   while (p.stages > 2 && flat_smem_bytes<D, NT>(p.stages, p.B) > (size_t)kMaxSmem) --p.stages;
-  return launch_pdl(paged_decode_kernel<D, NT>, dim3(min(kPagedMaxGrid, d->sms)), dim3(kThreads),
+  return launch_pdl(paged_decode_kernel<D, NT, DRAFTS>, dim3(min(kPagedMaxGrid, d->sms)), dim3(kThreads),
                     flat_smem_bytes<D, NT>(p.stages, p.B), stream, mk, mv, p);
 }
 
-template <int D>
+template <int D, bool DRAFTS>
 cudaError_t launch_paged_rows(PagedParams& p, const PagedPool& pool, cudaStream_t stream) {
-  return p.R <= 8    ? launch_paged<D, 1>(p, pool, stream)
-         : p.R <= 16 ? launch_paged<D, 2>(p, pool, stream)
-                     : launch_paged<D, 4>(p, pool, stream);
+  return p.R <= 8    ? launch_paged<D, 1, DRAFTS>(p, pool, stream)
+         : p.R <= 16 ? launch_paged<D, 2, DRAFTS>(p, pool, stream)
+                     : launch_paged<D, 4, DRAFTS>(p, pool, stream);
 }
 
 }  // namespace
