@@ -150,22 +150,31 @@ __device__ __forceinline__ void copy_rows(uint8_t* base, const PagedPool& pool, 
     return;
   const int lv = pool.D == 128 ? 4 : 3;
   const int vecs = (r1 - r0) << lv;
-  const long long rs = pool.row_stride >> 3;
-  const long long in = (h * pool.head_stride >> 3) + r0 * rs;
+  const long long rs = pool.row_stride >> 3, step = rs << (5 - lv);  // of 32 vectors
+  const long long in = (h * pool.head_stride >> 3) + (r0 + (lane >> lv)) * rs +
+                       (lane & ((1 << lv) - 1));
   const uint4* src = reinterpret_cast<const uint4*>(base) + (from * pool.page_stride >> 3) + in;
   uint4* dst = reinterpret_cast<uint4*>(base) + (to * pool.page_stride >> 3) + in;
   uint4 x[8];
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int j = lane + 32 * u;
-    if (j < vecs) x[u] = src[(j >> lv) * rs + (j & ((1 << lv) - 1))];
-  }
+  for (int u = 0; u < 8; ++u)
+    if (lane + 32 * u < vecs) x[u] = src[u * step];
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int j = lane + 32 * u;
-    if (j < vecs) dst[(j >> lv) * rs + (j & ((1 << lv) - 1))] = x[u];
-  }
+  for (int u = 0; u < 8; ++u)
+    if (lane + 32 * u < vecs) dst[u * step] = x[u];
 }
+
+// Unit u of copied pages: page `c`, operand and head `oh`, first row.
+struct Unit {
+  int c, oh, r0;
+  // lp: log2 of the page's rows; heads: operands and heads of a page
+  __device__ __forceinline__ Unit(uint32_t u, int lp, int heads) {
+    const uint32_t x = u >> (lp - 4);
+    c = (int)(x / (uint32_t)heads);
+    oh = (int)(x - (uint32_t)c * heads);
+    r0 = (int)(u & ((1u << (lp - 4)) - 1u)) * 16;
+  }
+};
 
 // Thread 0 of a CTA that has read all it will: whether it is the last of the
 // grid's, and may write what others read.
@@ -294,14 +303,15 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   const int rows = given ? copied(p, jj, was, pos) : 0;
   if (tid < items && jj == 0) copies[b] = make_int4(was, page, rows, 0);
   const bool some = __syncthreads_or(rows > 0);
-  const int parts = pool.page >> 4, per = 2 * pool.Hkv * parts;
-  for (int u = blockIdx.x * kScanWarps + warp; some && u < p.B * per;
+  const int heads = 2 * pool.Hkv;
+  const uint32_t units = (uint32_t)(p.B * heads) << (p.lp - 4);
+  for (uint32_t u = blockIdx.x * kScanWarps + warp; some && u < units;
        u += gridDim.x * kScanWarps) {
-    const int c = u / per, rest = u - c * per, r0 = rest % parts * 16, oh = rest / parts;
-    const int4 x = copies[c];
-    if (r0 < x.z)
-      copy_rows(oh & 1 ? pool.v : pool.k, pool, oh >> 1, x.x, x.y, r0, min(r0 + 16, x.z), lane,
-                p.status);
+    const Unit v(u, p.lp, heads);
+    const int4 x = copies[v.c];
+    if (v.r0 < x.z)
+      copy_rows(v.oh & 1 ? pool.v : pool.k, pool, v.oh >> 1, x.x, x.y, v.r0,
+                min(v.r0 + 16, x.z), lane, p.status);
   }
   if (!last) return;
   if (given) give(p, b, jj, was, pos, page);
@@ -516,7 +526,7 @@ struct CompactParams {
   int* n_moves;
   int32_t* from;  // [P] used pages by how many come before them
   int32_t* to;    // [P] free pages by how many come before them
-  int B, M, P;
+  int B, M, P, lp;
 };
 
 // A small pool in one launch: every CTA works the moves out for itself, and does
@@ -568,11 +578,12 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     const int e = p.table[i];
     if (e >= n && e < p.P) p.table[i] = where[e] == 0xffff ? -1 : where[e];
   }
-  const int parts = pool.page >> 4, per = 2 * pool.Hkv * parts;
-  for (int u = thread >> 5; u < moves * per; u += threads >> 5) {
-    const int c = u / per, rest = u - c * per, r0 = rest % parts * 16, oh = rest / parts;
-    copy_rows(oh & 1 ? pool.v : pool.k, pool, oh >> 1, from[moves - 1 - c], to[c], r0, r0 + 16,
-              lane, p.status);
+  const int heads = 2 * pool.Hkv;
+  const uint32_t units = (uint32_t)(moves * heads) << (p.lp - 4);
+  for (uint32_t u = thread >> 5; u < units; u += threads >> 5) {
+    const Unit v(u, p.lp, heads);
+    copy_rows(v.oh & 1 ? pool.v : pool.k, pool, v.oh >> 1, from[moves - 1 - v.c], to[v.c], v.r0,
+              v.r0 + 16, lane, p.status);
   }
   if (!last) return;
   for (int k = tid; k < moves; k += kScanThreads) {
@@ -792,6 +803,7 @@ cudaError_t launch_pages_compact(int32_t* table, int32_t* refs, const PagedPool&
   p.B = B;
   p.M = M;
   p.P = pool.P;
+  p.lp = log2_of(pool.page);
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
