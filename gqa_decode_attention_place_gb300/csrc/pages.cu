@@ -32,7 +32,10 @@ constexpr int kCopyThreads = 256;
 // Up to these sizes a call is one launch: every CTA scans the counts for itself.
 constexpr int kSoloPages = 16384;     // reserve
 constexpr int kSoloItems = 1024;
-constexpr int kSoloMoves = 8192;      // pages of a pool to compact
+constexpr int kSoloPool = 8192;       // compact
+// and so many 16-row copies (4096 pages of 64 KB: 30 us in one launch, 32 in two; 2048
+// of 512 KB: 92 and 85)
+constexpr int kSoloUnits = 49152;
 
 int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     pages_compact_solo_kernel(const CompactParams p, const PagedPool pool) {
   __shared__ Prefix<1, 1> prefix;
   // from: the high pages from the last on; to: the free pages below n
-  __shared__ uint16_t from[kSoloMoves / 2], to[kSoloMoves / 2], where[kSoloMoves];
+  __shared__ uint16_t from[kSoloPool / 2], to[kSoloPool / 2], where[kSoloPool];
   __shared__ int holes;  // free pages below n
   __shared__ bool last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -560,9 +563,9 @@ __global__ void __launch_bounds__(kScanThreads, 1)
     if (i >= bits.s.hi) return true;
     if (i == n) holes = n - before;
     const bool used = m >> lane & 1;
-    if (used && i >= n && range_ok(n - 1 - before < kSoloMoves / 2, p.status))
+    if (used && i >= n && range_ok(n - 1 - before < kSoloPool / 2, p.status))
       from[n - 1 - before] = (uint16_t)i;
-    if (!used && i < n && range_ok(i - before < kSoloMoves / 2, p.status))
+    if (!used && i < n && range_ok(i - before < kSoloPool / 2, p.status))
       to[i - before] = (uint16_t)i;
     where[i] = used ? (uint16_t)i : 0xffff;
     return true;
@@ -807,16 +810,21 @@ cudaError_t launch_pages_compact(int32_t* table, int32_t* refs, const PagedPool&
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  if (pool.P <= kSoloMoves) {
-    // as many moves as can be, or the table's entries by 32
-    const long long moves = (long long)(pool.P / 2) * 2 * pool.Hkv * (pool.page >> 4);
+  // 16-row copies, as many as there can be, and CTAs' worth of table entries
+  const long long units = (long long)(pool.P / 2) * 2 * pool.Hkv * (pool.page >> 4);
+  if (pool.P <= kSoloPool && units <= kSoloUnits)
     return launch_pdl(pages_compact_solo_kernel,
-                      solo_grid(max(moves, ((long long)B * M + 31) / 32), sms), dim3(kScanThreads),
+                      solo_grid(max(units, ((long long)B * M + 31) / 32), sms), dim3(kScanThreads),
                       0, stream, p, pool);
-  }
   e = launch_scan(pages_plan_kernel<kManyCtas>, stream, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(pages_move_kernel, dim3(sms * 8), dim3(kCopyThreads), 0, stream, p, pool);
+  // About one unit a warp: CTAs that come and go keep reads and writes of DRAM better
+  // apart than a few that stay (8192 pages of 64 KB: 168 us by 64 to an SM, 177 by 8
+  // and 206 by 2).
+  const long long ctas = max(((long long)B * M + kCopyThreads - 1) / kCopyThreads,
+                             units / (kCopyThreads / 32));
+  return launch_pdl(pages_move_kernel, dim3((unsigned)max(1ll, min(ctas, (long long)sms * 64))),
+                    dim3(kCopyThreads), 0, stream, p, pool);
 }
 
 }  // namespace gqa

@@ -635,8 +635,8 @@ int attn_pages_fork(int32_t* page_table, int32_t* page_refs, const int32_t* pare
  *
  *   page_map : [P] int32, written: where each page went (p for one that stayed),
  *              -1 for a free one: for page numbers kept elsewhere.
- *   Table entries outside [0, P) stay.  B * M may be 0.  One launch for up to 8192
- *   pages, else two.
+ *   Table entries outside [0, P) stay.  B * M may be 0.  One launch for a small pool
+ *   (up to 8192 pages, about 200 MB), else two.
  */
 int attn_pages_compact(int32_t* page_table, int32_t* page_refs, void* k_pages, void* v_pages,
                        int64_t page_stride, int64_t head_stride, int64_t row_stride, int B,
