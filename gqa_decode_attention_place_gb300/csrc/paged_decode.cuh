@@ -24,11 +24,13 @@
 //    as M: the scores' accumulators are then, lane by lane, the A operand of
 //    the second product, so the weights stay in registers, and V comes through
 //    transposing matrix loads.
-//  * Up to 8 rows the weights enter as two bf16 parts for nothing: rows 8..15
-//    of the MMA's M are free and take the rest (16 bits).  Up to 16 rows they
-//    take a second MMA.  Beyond, the weights are rounded to bf16 once (2^-9,
-//    of errors that average over the keys; the output's own rounding is the
-//    same size).
+//  * The weights enter as two bf16 parts (16 bits): up to 8 query rows for nothing,
+//    as rows 8..15 of the MMA's M are free and take the rest; beyond, by a second
+//    MMA (32 rows, 1.07 GB: 169 -> 175 us, and nothing for a ragged batch).  Only
+//    at D = 64 with more than 16 rows they are rounded to bf16 once (2^-9, of errors
+//    that average over the keys; the output's own rounding is the same size):
+//    there a tile's transfer is half as long and the MMAs are what it waits for
+//    (91 us, 107 with two parts).  The sums are of the weights as they entered.
 //  * At a piece's end the warps' partials meet in the memory of its last tile,
 //    each in the slice that its warp alone has read, so one barrier is enough.
 //  * Work is split as in the 8-bit decode (flat_list.cuh): a flat list of all
@@ -342,7 +344,7 @@ struct PagedConsumer {
         for (int j = 0; j < 2; ++j) {
           const uint32_t hi = pack_bf16x2(y[2 * j], y[2 * j + 1]);
           w[n][2 * j + i] = hi;
-          if (NT == 4) continue;
+          if (G == 2 && !kTwoParts) continue;
           const uint32_t lo = pack_bf16x2(y[2 * j] - bf16lo(hi), y[2 * j + 1] - bf16hi(hi));
           if (G == 1) w[n][2 * j + 1] = lo;
           else rest[n][2 * j + i] = lo;
@@ -388,7 +390,8 @@ struct PagedConsumer {
       }
     }
   }
-  static constexpr bool kTwoParts = NT == 2;  // a second MMA for the weights' rest
+  // a second MMA for the weights' rest
+  static constexpr bool kTwoParts = NT == 2 || (NT == 4 && D == 128);
   // Mask of a register with two rows of which the first n (or all) count.
   __device__ __forceinline__ static uint32_t keep(int n) {
     return n >= 2 ? 0xffffffffu : n == 1 ? 0x0000ffffu : 0u;

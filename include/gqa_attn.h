@@ -561,8 +561,8 @@ size_t attn_paged_workspace_size(int B, int S, int Hq, int Hkv, int D);
  *
  *   q, out : [B, S, Hq, D] bf16.  Tokens t >= lengths[b] get zeros.
  *   Both products in bf16 with fp32 sums, as in attn_decode_step; the
- *   probabilities enter as two bf16 parts for S * g <= 16 and are rounded to
- *   bf16 once beyond.
+ *   probabilities enter as two bf16 parts (16 bits), at D = 64 and S * g > 16
+ *   rounded to bf16 once.
  *   Supported: any g = Hq / Hkv with S * g <= 32; B <= 4096; Hkv <= 1024;
  *   B * Hkv < 2^31 / 16; B * (M * page / 128 + 2) < 2^31.
  *
