@@ -481,7 +481,8 @@ int attn_decode_step_paged(const void* q, const int32_t* positions, const int32_
   if (const int st = paged_pool(k_pages, v_pages, page_stride, head_stride, row_stride, Hkv, D, P,
                                 page, M, &pool))
     return st;
-  if ((int64_t)B * ((int64_t)M * page / 128 + 2) >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
+  if ((int64_t)(B > Hkv ? B : Hkv) * ((int64_t)M * page / 128 + 8) >= (1ll << 31))
+    return ATTN_ERR_UNSUPPORTED;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < gqa::paged_workspace_layout(B, S, Hq, Hkv, D).total)
     return ATTN_ERR_WORKSPACE;

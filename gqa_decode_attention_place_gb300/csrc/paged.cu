@@ -72,7 +72,7 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, long long 
                                 const int32_t* lengths, const int32_t* table,
                                 const PagedPool& pool, int B, int S, int M, cudaStream_t stream) {
   const long long tokens = (long long)B * S;
-  const int per = (int)((tokens + (1ll << 24) - 1) >> 24);  // more than 2^26 tokens: several a warp
+  const int per = (int)((tokens + (1ll << 24) - 1) >> 24);  // more than 2^24 tokens: several a warp
   const long long warps = (tokens + per - 1) / per;
   return launch_pdl(paged_append_kernel, dim3((unsigned)((warps + kAppendWarps - 1) / kAppendWarps)),
                     dim3(kAppendWarps * 32), 0, stream, static_cast<const uint4*>(k_new),

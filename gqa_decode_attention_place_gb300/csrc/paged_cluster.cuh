@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
     misc[0] = 0;
     fence_mbar_init();
   }
+  prefetch_maps(tm_k, tm_v, warp, lane);
   for (int i = tid; i < Sh::kQ / 16; i += kClusterThreads)  // rows past R stay zero
     reinterpret_cast<uint4*>(qbuf)[i] = make_uint4(0u, 0u, 0u, 0u);
   // (they come before the query copies that land over them)

@@ -564,7 +564,7 @@ size_t attn_paged_workspace_size(int B, int S, int Hq, int Hkv, int D);
  *   probabilities enter as two bf16 parts (16 bits), at D = 64 and S * g > 16
  *   rounded to bf16 once.
  *   Supported: any g = Hq / Hkv with S * g <= 32; B <= 4096; Hkv <= 1024;
- *   B * Hkv < 2^31 / 16; B * (M * page / 128 + 2) < 2^31.
+ *   B * Hkv < 2^31 / 16; max(B, Hkv) * (M * page / 128 + 8) < 2^31.
  *
  * A sequence whose rows positions[b] .. positions[b] + lengths[b] - 1 are not
  * all in [0, M * page), or whose lengths[b] is not in 0 .. S, gets NaN output

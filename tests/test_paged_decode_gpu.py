@@ -207,3 +207,43 @@ def test_score_scales(S, g, scale):
     q, table, k, v = make(3, S, 2 * g, 2, 128, 16, pos, gen)
     out = ga.attn_decode_step_paged(q, i32(pos), table, k, v, scale)
     check_decode(out, q, k, v, pos, None, table, scale)
+
+
+@pytest.mark.parametrize("schedule", [0, 2])
+@pytest.mark.parametrize("S,g,D", [(3, 2, 128), (3, 5, 128), (3, 8, 64), (3, 8, 128)])
+def test_odd_keys_reach_who_sees_them(S, g, D, schedule):
+    """NaN, +inf and -inf scores: in a drafted token's row, and in one that all see."""
+    gen = torch.Generator(device="cuda").manual_seed(16)
+    pos = [126, 40, 500, 300]
+    q, table, k, v = make(4, S, g, 1, D, 16, pos, gen)
+    want, _, _, _ = paged.decode(f64(q), f64(k), f64(v), pos, None, i64(table), 0.09)
+    k[int(table[0, 127 // 16]), :, 127 % 16] = float("nan")       # the second token's own row
+    k[int(table[1, 3 // 16]), :, 3] = float("nan")                # an old row
+    k[int(table[2, 502 // 16]), :, 502 % 16] = q[2, 0, 0, 0].sign() * float("inf")  # the third's
+    row = k[int(table[3, 7 // 16]), :, 7]
+    row.zero_()
+    row[..., 5] = float("inf")  # a score of +inf or -inf, by the sign of a query's dim 5
+    ga.attn_test_force_schedule(schedule)
+    try:
+        out = f64(ga.attn_decode_step_paged(q, i32(pos), table, k, v, 0.09))
+    finally:
+        ga.attn_test_force_schedule(-1)
+    assert np.abs(out[0, 0] - want[0, 0]).max() < 0.05 and np.isnan(out[0, 1:]).all()
+    assert np.isnan(out[1]).all()
+    assert np.abs(out[2, :2] - want[2, :2]).max() < 0.05 and np.isnan(out[2, 2]).all()
+    # +inf: no weight is finite; -inf: the row has none
+    up = f64(q)[3, :, :, 5] > 0
+    assert np.isnan(out[3][up]).all()
+    without = table.clone()
+    kz, vz = f64(k), f64(v)
+    kz[int(without[3, 0]), :, 7] = 0.0
+    rest = np.delete(np.arange(303), 7)
+    pg = i64(table)[3, rest // 16]
+    for t in range(S):
+        seen = rest <= 300 + t
+        K, V = kz[pg[seen], 0, rest[seen] % 16], vz[pg[seen], 0, rest[seen] % 16]
+        x = 0.09 * (f64(q)[3, t] @ K.T)
+        w = np.exp(x - x.max(axis=1, keepdims=True))
+        exact = (w @ V) / w.sum(axis=1, keepdims=True)
+        down = f64(q)[3, t, :, 5] < 0
+        assert np.abs(out[3, t][down] - exact[down]).max(initial=0) < 0.05
