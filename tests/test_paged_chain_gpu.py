@@ -329,3 +329,59 @@ def test_the_binding_refuses_what_does_not_fit():
     with pytest.raises(ValueError):
         ga.attn_pages_fork(table, refs, 16, parents=pos[:2])
     decode()
+
+
+CAPTURE_FIRST = """
+import torch, gqa_decode_attention_place_gb300 as ga
+g = torch.Generator(device="cuda").manual_seed(9)
+for B, S, P in ((3, 2, 200), (1100, 1, 20000)):  # calls of one launch, and of two
+    k, v = (torch.randn((P, 2, 16, 64), generator=g, device="cuda").bfloat16() for _ in "kv")
+    new = torch.randn((B, S, 12, 64), generator=g, device="cuda").bfloat16()
+    q, pos = new[:, :, :8].contiguous(), torch.full((B,), 15, dtype=torch.int32, device="cuda")
+    first = torch.full((B * 8 + P,), -1, dtype=torch.int32, device="cuda")
+    first[B * 8:] = 0
+    first[:B * 8:8] = torch.arange(B, device="cuda") // 2 + P // 2
+    first[B * 8:] += torch.bincount(first[:B * 8:8], minlength=P).int()
+    live = first.clone()
+    table, refs = live[:B * 8].view(B, 8), live[B * 8:]
+    parents = torch.arange(B, device="cuda").flip(0).int()
+    ws, pws = ga.paged_workspace(B, S, 8, 2, 64), ga.pages_workspace(B, S, P, 16)
+    out, taken = torch.empty_like(q), torch.empty_like(pos)
+    page_map = torch.empty(P, dtype=torch.int32, device="cuda")
+    kept = k.clone(), v.clone()
+    def step():
+        k.copy_(kept[0])
+        v.copy_(kept[1])
+        live.copy_(first)
+        ga.attn_pages_reserve(table, refs, pos, k, v, S, taken=taken, workspace=pws)
+        ga.attn_paged_append(new[:, :, 8:10], new[:, :, 10:], pos, table, k, v)
+        ga.attn_pages_fork(table, refs, 16, parents=parents, workspace=pws)
+        ga.attn_pages_fork(table, refs, 16, lengths=pos + S, workspace=pws)
+        ga.attn_pages_compact(table, refs, k, v, page_map=page_map, workspace=pws)
+        ga.attn_decode_step_paged(q, pos, table, k, v, 0.1, out=out, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [x.clone() for x in (out.view(torch.int16), live, taken, page_map)]
+    out.zero_()
+    step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, (out.view(torch.int16), live, taken, page_map)))
+    assert torch.isfinite(out).all() and (taken > 0).all() and ga.attn_read_device_status(pws) == 0
+print("same")
+"""
+
+
+def test_a_process_whose_first_calls_are_captured():
+    """Nothing has to run before a capture, and a replay does what the calls do."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURE_FIRST], capture_output=True, text=True,
+                       cwd=root, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr

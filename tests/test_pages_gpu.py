@@ -47,7 +47,8 @@ def same_counts(table, refs):
     (1, 1, 1, 1, 16, 1, 64, "heads"), (9, 1, 6, 40, 16, 2, 128, "rows"),
     (40, 3, 9, 300, 32, 1, 64, "pair"), (6, 100, 20, 110, 16, 2, 64, "heads"),
     (300, 1, 5, 900, 16, 1, 64, "woven"), (3, 700, 60, 5000, 16, 1, 64, "heads"),
-    (70, 5, 4, 120, 128, 1, 64, "heads"), (1100, 1, 3, 2500, 16, 1, 64, "heads")])
+    (70, 5, 4, 120, 128, 1, 64, "heads"), (1100, 1, 3, 2500, 16, 1, 64, "heads"),
+    (300, 700, 60, 13000, 16, 1, 64, "heads"), (2, 1, 3, 20000, 16, 1, 64, "pair")])
 def test_reserve(B, S, M, P, page, Hkv, D, layout):
     for seed in range(3):
         r = random.Random(seed + 100)
