@@ -130,6 +130,11 @@ cudaError_t launch_paged_decode(const void* q, const int32_t* positions, const i
   p.counters = reinterpret_cast<uint32_t*>(base + ws.counters_off);
   p.part_ml = reinterpret_cast<float*>(base + ws.ml_off);
   p.part_o = reinterpret_cast<float*>(base + ws.o_off);
+  p.k = reinterpret_cast<const uint16_t*>(pool.k);
+  p.v = reinterpret_cast<const uint16_t*>(pool.v);
+  p.page_stride = pool.page_stride;
+  p.head_stride = pool.head_stride;
+  p.row_stride = pool.row_stride;
   p.B = B;
   p.S = S;
   p.Hq = Hq;

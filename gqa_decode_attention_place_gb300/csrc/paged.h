@@ -33,6 +33,9 @@ struct PagedParams {
   uint32_t* counters;
   float* part_ml;          // [slots][R][2]
   float* part_o;           // [slots][R][D]
+  const uint16_t* k;       // the pool, for copies that need no tensor map
+  const uint16_t* v;
+  long long page_stride, head_stride, row_stride;
   int B, S, Hq, Hkv, g, P, M;
   int R;                   // S * g
   int g_inverse;           // 2^16 / g, rounded up

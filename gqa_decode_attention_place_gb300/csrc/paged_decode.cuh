@@ -238,33 +238,36 @@ struct PagedConsumer {
   __device__ __forceinline__ void tile(const uint8_t* ks, const PagedParams& p,
                                        const TileMeta& mt) {
     const int first = warp & (kTeam - 1);
+    const uint32_t base = smem_u32(ks);
+    const int half = 128 << p.lb;  // from a box's first 64 dims to the others
     constexpr bool kTwo = Sh::kSlices == 2 * kTeam;
     constexpr int kAll = kTwo ? 1 | (1 << kTeam) : 1;
     // full: every row is there and seen by every query row in use
     if (((mt.flags >> first) & kAll) == kAll &&
         mt.row0 + 16 * (first + (kTwo ? kTeam : 0)) + 15 <= mt.pos) {
-      slices<kTwo ? 2 : 1, true>(ks, first, p, mt);
+      slices<kTwo ? 2 : 1, true>(base + slice_at(first, p.lb),
+                                 base + slice_at(first + (kTwo ? kTeam : 0), p.lb), half, Sh::kOp,
+                                 mt.row0 + 16 * first, p, mt);
       return;
     }
 #pragma unroll 1
     for (int sl = first; sl < Sh::kSlices; sl += kTeam) {
       if (!((mt.flags >> sl) & 1)) continue;  // no rows there
       // (one slice that is full, where two are taken, does without the masks)
-      if (kTwo && mt.row0 + 16 * sl + 15 <= mt.pos) slices<1, true>(ks, sl, p, mt);
-      else slices<1, false>(ks, sl, p, mt);
+      const uint32_t at = base + slice_at(sl, p.lb);
+      const int row = mt.row0 + 16 * sl;
+      if (kTwo && row + 15 <= mt.pos) slices<1, true>(at, at, half, Sh::kOp, row, p, mt);
+      else slices<1, false>(at, at, half, Sh::kOp, row, p, mt);
     }
   }
-  // 16 rows of slice sl, and with N = 2 of slice sl + kTeam, whose chains of
-  // products and exponentials overlap.
+  // 16 cache rows from row0 on, whose keys lie at at0 (dims from 64 on `half` bytes
+  // further, values v_off), and with N = 2 another 16 at at1, which are full too: the
+  // two slices' chains of products and exponentials overlap.
   template <int N, bool FULL>
-  __device__ __forceinline__ void slices(const uint8_t* ks, int sl, const PagedParams& p,
-                                         const TileMeta& mt) {
-    const int half = 128 << p.lb;  // from a box's first 64 dims to the others
+  __device__ __forceinline__ void slices(uint32_t at0, uint32_t at1, int half, int v_off, int row0,
+                                         const PagedParams& p, const TileMeta& mt) {
     const int i8 = lane >> 3, r8 = lane & 7;
-    uint32_t at[N];
-#pragma unroll
-    for (int n = 0; n < N; ++n) at[n] = smem_u32(ks) + slice_at(sl + n * kTeam, p.lb);
-    const int row0 = mt.row0 + 16 * sl;  // the first cache row (N = 1)
+    const uint32_t at[2] = {at0, at1};
     float s[N][2][2][4];  // of each slice rows 0..7 and 8..15, in two chains each
 #pragma unroll
     for (int n = 0; n < N; ++n)
@@ -297,7 +300,7 @@ struct PagedConsumer {
     }
     auto load_v = [&](uint32_t (&b)[4], int d, int n) {
       const int ch = 2 * d + (i8 >> 1);
-      ldmatrix4_trans(b, at[n] + Sh::kOp + (8 * (i8 & 1) + r8) * 128 + (2 * d >= 8 ? half : 0) +
+      ldmatrix4_trans(b, at[n] + v_off + (8 * (i8 & 1) + r8) * 128 + (2 * d >= 8 ? half : 0) +
                              (((ch & 7) ^ r8) << 4));
     };
     // weights as the second product's A operand: rows 2t, 2t+1 and 8 on of a slice
@@ -656,6 +659,128 @@ __device__ __forceinline__ void join_parts(const PagedParams& p, const TileMeta&
   if (*(volatile int*)flag && !*sync.abort_flag) merge_parts<D>(p, mt, tid, threads);
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Many short sequences: a warp takes a whole segment (with more than 16 query rows,
+// half of its query rows), 16 cache rows at a time, by copies of its own into
+// `room` bytes of shared memory of its own.  A CTA that takes a segment at a time has
+// three under way and pays for each one's copy, merge and hand-over in turn; here
+// there are eight, and nothing to merge.  (8 heads, 4 query rows: 128 sequences of 8
+// rows 13.7 -> 4.8 us, of 64 15.4 -> 8.6, of 128 19.4 -> 14.6; 512 of 8 rows 36 -> 13,
+// of 128 53 either way; of 256 rows tiles are faster, 88 and 93.)
+template <int D, int NT, bool DRAFTS>
+__device__ __forceinline__ void short_segments(const PagedParams& p, const int* prefix,
+                                               const int* spos, const uint8_t* snew, uint8_t* own,
+                                               int room, int warp, int lane) {
+  using Sh = Shape<D, NT>;
+  using Consumer = PagedConsumer<D, NT, DRAFTS>;
+  constexpr int kG = Consumer::G, kTeams = Consumer::kTeams, kRows = 8 * kG;
+  constexpr int kBuf = 16 * D * 4, kQBytes = kRows * Sh::kQStride;
+  const int bufs = min(4, (room - kQBytes) / kBuf);
+  uint8_t* qs = own + bufs * kBuf;
+  Consumer cs;
+  cs.init(0, lane);
+  const long long units = (long long)p.B * p.Hkv * kTeams;
+  for (long long u = (long long)blockIdx.x * kWarps + warp; u < units;
+       u += (long long)gridDim.x * kWarps) {
+    const int team = (int)(u % kTeams), seg = (int)(u / kTeams);
+    const int b = seg / p.Hkv, kvh = seg - b * p.Hkv;
+    if (prefix[b + 1] == prefix[b]) continue;
+    TileMeta mt = {};
+    mt.pos = spos[b];
+    mt.n = snew[b];
+    const int rows = mt.pos + mt.n, slices = (rows + 15) >> 4;
+    const int mask = (1 << p.lp) - 1;
+    // table entries, a lane for each of the first 32 slices
+    auto entry = [&](int i) -> int {
+      const int j = (16 * i) >> p.lp;
+      return i < slices && range_ok(j < p.M, p.status) ? p.table[(size_t)b * p.M + j] : 0;
+    };
+    int entries = entry(lane), from = 0;
+    cs.row_base = 16 * team;
+    // the query rows, zeros behind the last
+#pragma unroll
+    for (int i = lane; i < kRows * (D / 8); i += 32) {
+      const int r = i / (D / 8), ch = i % (D / 8), row = 16 * team + r;
+      const uint4 x = row < p.R ? *reinterpret_cast<const uint4*>(
+                                      p.q + query_row(p, b, kvh, row) * D + ch * 8)
+                                : make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(qs + r * Sh::kQStride + ch * 16) = x;
+    }
+    // 16 rows of keys and values, as a box of a tile would lie
+    uint32_t there = 0;  // of the buffers: which hold rows
+    auto load = [&](int i) {
+      if (i < slices) {
+        if (i - from >= 32) {
+          from = i;
+          entries = entry(i + lane);
+        }
+        const int pg = page_ok(p, __shfl_sync(0xffffffffu, entries, i - from));
+        const int buf = i % bufs;
+        there = pg >= 0 ? there | 1u << buf : there & ~(1u << buf);
+        if (pg >= 0) {
+          const long long at = pg * p.page_stride + kvh * p.head_stride +
+                               (long long)((16 * i) & mask) * p.row_stride;
+          const uint32_t dst = smem_u32(own + buf * kBuf);
+#pragma unroll
+          for (int k = 0; k < 16 * (D / 8) / 32; ++k) {
+            const int j = lane + 32 * k, r = j / (D / 8), ch = j % (D / 8);
+            if (16 * i + r < rows) {
+              const long long e = at + r * p.row_stride + ch * 8;
+              const uint32_t to = dst + (ch >> 3) * 2048 + sw128(r, ch & 7);
+              cp_async16(to, p.k + e);
+              cp_async16(to + 16 * D * 2, p.v + e);
+            }
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < bufs - 1; ++i) load(i);
+    __syncwarp();
+    cs.load_q(qs - 16 * team * Sh::kQStride, p.flip);
+    cs.start(p, mt.pos, mt.n);
+    for (int i = 0; i < slices; ++i) {
+      load(i + bufs - 1);
+      // all but the newest bufs - 1 have landed
+      if (bufs == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+      else if (bufs == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else if (bufs == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncwarp();
+      const int buf = i % bufs;
+      if (there >> buf & 1) {
+        const uint32_t at = smem_u32(own + buf * kBuf);
+        if (16 * i + 15 <= mt.pos)
+          cs.template slices<1, true>(at, at, 2048, 16 * D * 2, 16 * i, p, mt);
+        else
+          cs.template slices<1, false>(at, at, 2048, 16 * D * 2, 16 * i, p, mt);
+      }
+      __syncwarp();  // the buffer may be written again
+    }
+#pragma unroll
+    for (int i = 0; i < kG; ++i) {
+      const int r = 16 * team + 8 * i + cs.c;
+      const float l = kG == 1 ? cs.sums[0] + cs.sums[2] : cs.sums[2 * i];
+      const bool idle = token_of(p, r) >= mt.n;
+      const float inv = idle || l == 0.f ? 0.f : 1.f / l;
+      if (r >= p.R) continue;
+      uint16_t* out = p.out + query_row(p, b, kvh, r) * D + 2 * cs.t;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        float2 y = make_float2(cs.o[j][2 * i], cs.o[j][2 * i + 1]);
+        if (kG == 1) {
+          y.x += cs.o[j][2];
+          y.y += cs.o[j][3];
+        }
+        *reinterpret_cast<uint32_t*>(out + 8 * j) =
+            idle ? 0u : pack_bf16x2(y.x * inv, y.y * inv);
+      }
+    }
+  }
+}
+
 template <int D, int NT, bool DRAFTS>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -748,6 +873,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long nseg = (long long)B * Hkv;
   long long gw = min((long long)gridDim.x, T);
   if (T <= (long long)(kWholeTiles + kE) * nseg) gw = min(gw, nseg);
+  if (misc[2] <= 1 + kE && nseg > (long long)gridDim.x) {  // no segment is longer than a tile
+    if (warp < kWarps) {
+      const int room = NS * Sh::kStage / kWarps;
+      short_segments<D, NT, DRAFTS>(p, prefix, spos, snew, stages + warp * room, room, warp, lane);
+    }
+    return;
+  }
   // A CTA for each segment where the longest alone takes no longer than an even
   // share of the tiles and the merge of a split segment would.
   const bool whole =
@@ -1063,8 +1195,10 @@ cudaError_t paged_device(const PagedDevice** out) {
 // us, measured (D = 128; a tile at D = 64 takes half):
 //   all SMs    1.45 for each tile of an SM's even share
 //   clusters   4.3, then the even share and 15% of it, or 0.62 for each tile of the
-//              longest segment's CTAs where that is more; 2 for each further wave
+//              longest segment's CTAs where that is more
 //   flat list  12 (scan, lookups, the merge of split segments) and the even share
+// With more segments than SMs it is the flat list, which sees on the device how
+// long they are.
 // (2 sequences up to 8192 rows, 8 heads: 17 in clusters, 21 by the list; 10 up to
 // 16000: 74 and 50.)
 template <int D, int NT>
@@ -1073,15 +1207,15 @@ int cluster_size(const PagedParams& p, const PagedDevice& d) {
   if (g_decode_test_cluster >= 0)  // schedule tests only
     return min(g_decode_test_cluster, kMaxCluster);
   const long long nseg = (long long)p.B * p.Hkv;
+  if (nseg > d.sms) return 0;
   const int tiles = (p.cap + kTile - 1) / kTile;
   int c = min(kMaxCluster, tiles);
   while (c > 1 && nseg > d.clusters[c]) --c;
   const float longest = (float)tiles * (float)p.B / (float)(p.B + 1);
-  const float waves = c > 1 ? 1.f : (float)((nseg + d.sms - 1) / d.sms);
   const float per_tile = (D == 128 ? 1.45f : 0.75f) * (float)(kTile / 128.0);
   const float share = per_tile * 0.5f * (float)tiles * (float)nseg / (float)d.sms;
-  const float clusters = 4.3f + 2.f * (waves - 1.f) +
-                         fmaxf(1.15f * share, 0.43f * per_tile * ceilf(longest / (float)c));
+  const float clusters =
+      4.3f + fmaxf(1.15f * share, 0.43f * per_tile * ceilf(longest / (float)c));
   return clusters <= 12.f + share ? c : 0;
 }
 

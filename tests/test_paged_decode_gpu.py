@@ -247,3 +247,64 @@ def test_odd_keys_reach_who_sees_them(S, g, D, schedule):
         exact = (w @ V) / w.sum(axis=1, keepdims=True)
         down = f64(q)[3, t, :, 5] < 0
         assert np.abs(out[3, t][down] - exact[down]).max(initial=0) < 0.05
+
+
+@pytest.mark.parametrize("S,g,D,page,layout", [
+    (1, 1, 128, 16, "heads"), (1, 4, 128, 128, "rows"), (1, 4, 64, 32, "pair"),
+    (1, 16, 128, 32, "woven"), (3, 4, 64, 16, "heads"), (2, 16, 128, 64, "rows"),
+    (4, 8, 64, 128, "heads"), (5, 1, 128, 64, "pair"), (17, 1, 128, 16, "rows")])
+@pytest.mark.parametrize("longest", [1, 17, 128])
+def test_many_short_sequences(S, g, D, page, layout, longest):
+    """More segments than CTAs, none longer than a tile: padded, idle and bad ones among them."""
+    B, Hkv = 400, 3
+    r = np.random.default_rng(17)
+    lengths = r.integers(0, S + 1, B).tolist()
+    pos = [int(r.integers(0, max(1, longest + 1 - n))) for n in lengths]
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    q, table, k, v = make(B, S, Hkv * g, Hkv, D, page, pos, gen, lengths, layout)
+    b = lengths.index(S)
+    pos[b] = 10 ** 6
+    ws = ga.paged_workspace(B, S, Hkv * g, Hkv, D)
+    ga.attn_test_force_schedule(0)
+    try:
+        out = ga.attn_decode_step_paged(q, i32(pos), table, k, v, 0.1, lengths=i32(lengths),
+                                        workspace=ws)
+        first = ga.attn_decode_step_paged(q[:, :1].contiguous(), i32(pos), table, k, v, 0.1,
+                                          lengths=i32([min(n, 1) for n in lengths]))
+    finally:
+        ga.attn_test_force_schedule(-1)
+    assert ga.attn_read_device_status(ws) == ga.ATTN_DEV_BAD_POSITION
+    check_decode(out, q, k, v, pos, lengths, table, 0.1)
+    check_decode(first, q[:, :1], k, v, pos, [min(n, 1) for n in lengths], table, 0.1)
+
+
+def test_many_short_sequences_with_bad_pages_and_odd_values():
+    B, S, g, D, page = 500, 3, 4, 128, 16
+    r = np.random.default_rng(18)
+    pos = r.integers(0, 126, B).tolist()
+    gen = torch.Generator(device="cuda").manual_seed(18)
+    q, table, k, v = make(B, S, g, 1, D, page, pos, gen)
+    for b in range(0, B, 7):
+        table[b, int(r.integers(0, (pos[b] + S - 1) // page + 1))] = int(r.choice([-1, 10 ** 6]))
+    ws = ga.paged_workspace(B, S, g, 1, D)
+    for schedule in (0, 1):
+        ga.attn_test_force_schedule(schedule)
+        try:
+            out = ga.attn_decode_step_paged(q, i32(pos), table, k, v, 0.1, workspace=ws)
+        finally:
+            ga.attn_test_force_schedule(-1)
+        assert ga.attn_read_device_status(ws) == ga.ATTN_DEV_BAD_PAGE
+        check_decode(out, q, k, v, pos, None, table, 0.1)
+    # a last token's values that are not finite stay with it
+    good = (table[:, :15] >= -1).all(1).tolist()
+    for b in range(1, B, 7):
+        row = pos[b] + S - 1
+        v[int(table[b, row // page]), :, row % page, ::2] = float("nan")
+    ga.attn_test_force_schedule(0)
+    try:
+        out = f64(ga.attn_decode_step_paged(q, i32(pos), table, k, v, 0.1))
+    finally:
+        ga.attn_test_force_schedule(-1)
+    for b in range(1, B, 7):
+        assert good[b] and not np.isnan(out[b, :S - 1]).any()
+        assert np.isnan(out[b, S - 1, :, ::2]).all() and not np.isnan(out[b, S - 1, :, 1::2]).any()
