@@ -781,6 +781,17 @@ __device__ __forceinline__ void short_segments(const PagedParams& p, const int* 
   }
 }
 
+// As a call: with several tokens and 128 dims, inlined, it cost the tiles' loop registers
+// (32 sequences up to 16000 rows, 32 query rows a head: 173.5 -> 176.5 us, 16: 147 ->
+// 148.5).  The call reads its parameters by loads (243 sequences of 43 rows: 19 us
+// inlined, 27 so), so the other forms, which inlining does not cost anything, do without.
+template <int D, int NT, bool DRAFTS>
+__device__ __noinline__ void short_segments_call(const PagedParams& p, const int* prefix,
+                                                 const int* spos, const uint8_t* snew,
+                                                 uint8_t* own, int room, int warp, int lane) {
+  short_segments<D, NT, DRAFTS>(p, prefix, spos, snew, own, room, warp, lane);
+}
+
 template <int D, int NT, bool DRAFTS>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -876,7 +887,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (misc[2] <= 1 + kE && nseg > (long long)gridDim.x) {  // no segment is longer than a tile
     if (warp < kWarps) {
       const int room = NS * Sh::kStage / kWarps;
-      short_segments<D, NT, DRAFTS>(p, prefix, spos, snew, stages + warp * room, room, warp, lane);
+      uint8_t* own = stages + warp * room;
+      if constexpr (D == 128 && DRAFTS)
+        short_segments_call<D, NT, DRAFTS>(p, prefix, spos, snew, own, room, warp, lane);
+      else
+        short_segments<D, NT, DRAFTS>(p, prefix, spos, snew, own, room, warp, lane);
     }
     return;
   }
