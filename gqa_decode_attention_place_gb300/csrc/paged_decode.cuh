@@ -662,13 +662,14 @@ __device__ __forceinline__ void join_parts(const PagedParams& p, const TileMeta&
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// Many short sequences: a warp takes a whole segment (with more than 16 query rows,
+// Many short segments: a warp takes a whole segment (with more than 16 query rows,
 // half of its query rows), 16 cache rows at a time, by copies of its own into
 // `room` bytes of shared memory of its own.  A CTA that takes a segment at a time has
 // three under way and pays for each one's copy, merge and hand-over in turn; here
-// there are eight, and nothing to merge.  (8 heads, 4 query rows: 128 sequences of 8
-// rows 13.7 -> 4.8 us, of 64 15.4 -> 8.6, of 128 19.4 -> 14.6; 512 of 8 rows 36 -> 13,
-// of 128 53 either way; of 256 rows tiles are faster, 88 and 93.)
+// there are eight, and nothing to merge.  (4 query rows: 160 segments of up to 32 rows
+// 7.8 -> 4.9 us, of 128 8.2 and 9.6; 912 of 32 rows 12.8 -> 5.4, of 128 15.2 -> 11.3, of
+// 256 20.5 -> 19.1.)  Neighbouring units go to different CTAs: 192 segments of 160 rows in
+// 24 full CTAs took 12.7 us, a warp in each CTA 11.1.
 template <int D, int NT, bool DRAFTS>
 __device__ __forceinline__ void short_segments(const PagedParams& p, const int* prefix,
                                                const int* spos, const uint8_t* snew, uint8_t* own,
@@ -682,7 +683,7 @@ __device__ __forceinline__ void short_segments(const PagedParams& p, const int* 
   Consumer cs;
   cs.init(0, lane);
   const long long units = (long long)p.B * p.Hkv * kTeams;
-  for (long long u = (long long)blockIdx.x * kWarps + warp; u < units;
+  for (long long u = blockIdx.x + (long long)gridDim.x * warp; u < units;
        u += (long long)gridDim.x * kWarps) {
     const int team = (int)(u % kTeams), seg = (int)(u / kTeams);
     const int b = seg / p.Hkv, kvh = seg - b * p.Hkv;
@@ -884,7 +885,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long nseg = (long long)B * Hkv;
   long long gw = min((long long)gridDim.x, T);
   if (T <= (long long)(kWholeTiles + kE) * nseg) gw = min(gw, nseg);
-  if (misc[2] <= 1 + kE && nseg > (long long)gridDim.x) {  // no segment is longer than a tile
+  // Short segments: a tile at most, or two where there are many (192 rows: of 608
+  // segments 14.7 -> 13.2 us, of 912 18.4 -> 15.5, of 320 10.3 and 12.7; 32 query rows at
+  // 128 dims, 912 of them: 38 and 45; the call's form is slower than the inlined).
+  constexpr int kWarpTiles = D == 128 && (NT == 4 || DRAFTS) ? 1 : 2;
+  if (nseg > (long long)gridDim.x &&
+      misc[2] <= kE + (nseg >= 4LL * (long long)gridDim.x ? kWarpTiles : 1)) {
     if (warp < kWarps) {
       const int room = NS * Sh::kStage / kWarps;
       uint8_t* own = stages + warp * room;

@@ -253,9 +253,9 @@ def test_odd_keys_reach_who_sees_them(S, g, D, schedule):
     (1, 1, 128, 16, "heads"), (1, 4, 128, 128, "rows"), (1, 4, 64, 32, "pair"),
     (1, 16, 128, 32, "woven"), (3, 4, 64, 16, "heads"), (2, 16, 128, 64, "rows"),
     (4, 8, 64, 128, "heads"), (5, 1, 128, 64, "pair"), (17, 1, 128, 16, "rows")])
-@pytest.mark.parametrize("longest", [1, 17, 128])
+@pytest.mark.parametrize("longest", [1, 17, 128, 250])
 def test_many_short_sequences(S, g, D, page, layout, longest):
-    """More segments than CTAs, none longer than a tile: padded, idle and bad ones among them."""
+    """More segments than CTAs, none longer than two tiles: padded, idle and bad ones among them."""
     B, Hkv = 400, 3
     r = np.random.default_rng(17)
     lengths = r.integers(0, S + 1, B).tolist()
