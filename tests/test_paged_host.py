@@ -171,7 +171,9 @@ PLACES = [  # file, the function's first words, range checks in its body at leas
     ("paged.cu", "paged_append_kernel(\n", 1),
     ("paged_decode.cuh", "void store4(", 1),
     ("paged_decode.cuh", "void merge_parts(", 1),
-    ("paged_decode.cuh", "paged_decode_kernel(const", 2),   # a table entry, a part's slot
+    ("paged_decode.cuh", "void put_piece(", 1),              # a part's slot
+    ("paged_decode.cuh", "void short_segments(", 1),         # a table entry
+    ("paged_decode.cuh", "paged_decode_kernel(const", 1),    # likewise
     ("paged_cluster.cuh", "paged_cluster_kernel(const", 1),  # landing places
     ("pages.cu", "void copy_rows(", 1),
     ("pages.cu", "void give(", 1),
