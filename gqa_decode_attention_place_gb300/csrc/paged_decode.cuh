@@ -670,6 +670,17 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 // 7.8 -> 4.9 us, of 128 8.2 and 9.6; 912 of 32 rows 12.8 -> 5.4, of 128 15.2 -> 11.3, of
 // 256 20.5 -> 19.1.)  Neighbouring units go to different CTAs: 192 segments of 160 rows in
 // 24 full CTAs took 12.7 us, a warp in each CTA 11.1.
+//
+// With several tokens and 128 dims it is a call: inlined, it cost the tiles' loop registers
+// (32 sequences up to 16000 rows, 32 query rows a head: 173.5 -> 176.5 us, 16: 147 ->
+// 148.5).  The call costs short segments 2 us, the other forms do without.  It takes its
+// parameters from shared memory (by reference each use was a load, 5% slower), and all
+// warps (8 where it is inlined: with 12, which leave less room for each, 16 query rows
+// were 20% slower; with 32 and a call 912 segments of 128 rows went from 36.4 to 22.6 us).
+template <int D, bool DRAFTS>
+constexpr bool kShortCall = D == 128 && DRAFTS;
+template <int D, bool DRAFTS>
+constexpr int kShortWarps = kShortCall<D, DRAFTS> ? kThreads / 32 : kWarps;
 template <int D, int NT, bool DRAFTS>
 __device__ __forceinline__ void short_segments(const PagedParams& p, const int* prefix,
                                                const int* spos, const uint8_t* snew, uint8_t* own,
@@ -677,14 +688,17 @@ __device__ __forceinline__ void short_segments(const PagedParams& p, const int* 
   using Sh = Shape<D, NT>;
   using Consumer = PagedConsumer<D, NT, DRAFTS>;
   constexpr int kG = Consumer::G, kTeams = Consumer::kTeams, kRows = 8 * kG;
+  // (with all warps the query rows go through the buffer that is filled last)
+  constexpr bool kAll = kShortCall<D, DRAFTS>;
   constexpr int kBuf = 16 * D * 4, kQBytes = kRows * Sh::kQStride;
-  const int bufs = min(4, (room - kQBytes) / kBuf);
-  uint8_t* qs = own + bufs * kBuf;
+  static_assert(kQBytes <= kBuf, "the query rows' place");
+  const int bufs = min(4, (room - (kAll ? 0 : kQBytes)) / kBuf);
+  uint8_t* qs = own + (bufs - kAll) * kBuf;
   Consumer cs;
   cs.init(0, lane);
   const long long units = (long long)p.B * p.Hkv * kTeams;
   for (long long u = blockIdx.x + (long long)gridDim.x * warp; u < units;
-       u += (long long)gridDim.x * kWarps) {
+       u += (long long)gridDim.x * kShortWarps<D, DRAFTS>) {
     const int team = (int)(u % kTeams), seg = (int)(u / kTeams);
     const int b = seg / p.Hkv, kvh = seg - b * p.Hkv;
     if (prefix[b + 1] == prefix[b]) continue;
@@ -741,6 +755,7 @@ __device__ __forceinline__ void short_segments(const PagedParams& p, const int* 
     for (int i = 0; i < bufs - 1; ++i) load(i);
     __syncwarp();
     cs.load_q(qs - 16 * team * Sh::kQStride, p.flip);
+    if (kAll) __syncwarp();
     cs.start(p, mt.pos, mt.n);
     for (int i = 0; i < slices; ++i) {
       load(i + bufs - 1);
@@ -782,10 +797,6 @@ __device__ __forceinline__ void short_segments(const PagedParams& p, const int* 
   }
 }
 
-// As a call: with several tokens and 128 dims, inlined, it cost the tiles' loop registers
-// (32 sequences up to 16000 rows, 32 query rows a head: 173.5 -> 176.5 us, 16: 147 ->
-// 148.5).  The call reads its parameters by loads (243 sequences of 43 rows: 19 us
-// inlined, 27 so), so the other forms, which inlining does not cost anything, do without.
 template <int D, int NT, bool DRAFTS>
 __device__ __noinline__ void short_segments_call(const PagedParams& p, const int* prefix,
                                                  const int* spos, const uint8_t* snew,
@@ -809,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(ml + Sh::kMl / 8);
   uint64_t* m_full = bars + 2 * NS + 2;
   uint64_t* m_empty = m_full + 2;
-  // [0] abort, [1] last to arrive (consumers), [2] longest segment, [3] last to arrive (merge
+  // [0] abort, [1] last to arrive (consumers), [2] longest segment's rows, [3] last to arrive (merge
   // warps), [4..6) stage of the piece's last tile, [8..16) scan
   int* misc = reinterpret_cast<int*>(m_empty + 2);
   int* prefix = misc + 16;                                // [B + 1]
@@ -846,15 +857,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   int carry = 0;
   for (int base = 0; base < B; base += kConsumers) {
     const int b = base + tid;
-    int v = 0;
+    int v = 0, rows = 0;
     if (tid < kConsumers && b < B) {
       int pos, n;
       const int kind = sequence(p, b, pos, n);
       spos[b] = pos;
       snew[b] = (uint8_t)n;
-      if (kind == 2) v = (pos + n - 1) / Sh::kTile + 1 + kE;
+      if (kind == 2) {
+        rows = pos + n;
+        v = (rows - 1) / Sh::kTile + 1 + kE;
+      }
     }
-    const int most = __reduce_max_sync(0xffffffffu, v);
+    const int most = __reduce_max_sync(0xffffffffu, rows);
     if (lane == 0 && warp < kWarps) atomicMax(misc + 2, most);
     int x = v;
 #pragma unroll
@@ -885,17 +899,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long nseg = (long long)B * Hkv;
   long long gw = min((long long)gridDim.x, T);
   if (T <= (long long)(kWholeTiles + kE) * nseg) gw = min(gw, nseg);
-  // Short segments: a tile at most, or two where there are many (192 rows: of 608
-  // segments 14.7 -> 13.2 us, of 912 18.4 -> 15.5, of 320 10.3 and 12.7; 32 query rows at
-  // 128 dims, 912 of them: 38 and 45; the call's form is slower than the inlined).
-  constexpr int kWarpTiles = D == 128 && (NT == 4 || DRAFTS) ? 1 : 2;
-  if (nseg > (long long)gridDim.x &&
-      misc[2] <= kE + (nseg >= 4LL * (long long)gridDim.x ? kWarpTiles : 1)) {
-    if (warp < kWarps) {
-      const int room = NS * Sh::kStage / kWarps;
+  // Short segments: the more a CTA has, the longer they may be (of 2, 3 and 4 a CTA with 4
+  // query rows, tiles and warps take alike at 96, 128 and 256 rows, at 64, 96 and 128 with
+  // several tokens and 128 dims; 32 query rows there, 912 of 192 rows: 38 and 45 us).
+  constexpr int kWarpRows = D == 128 && (NT == 4 || DRAFTS) ? 128 : 256;
+  const int per_cta = (int)((nseg + gridDim.x - 1) / gridDim.x);
+  if (per_cta > 1 &&
+      misc[2] <= min(kWarpRows, kShortCall<D, DRAFTS> ? 32 * per_cta : 64 * per_cta - 32)) {
+    constexpr int kShort = kShortWarps<D, DRAFTS>;
+    PagedParams* shared = reinterpret_cast<PagedParams*>(qbuf);
+    static_assert(sizeof(PagedParams) <= 2 * Sh::kQ);
+    if (kShortCall<D, DRAFTS>) {
+      if (tid == 0) *shared = p;  // over the query rows, which no copy fills here
+      __syncthreads();
+    }
+    if (warp < kShort) {
+      const int room = (NS * Sh::kStage / kShort) & ~1023;
       uint8_t* own = stages + warp * room;
-      if constexpr (D == 128 && DRAFTS)
-        short_segments_call<D, NT, DRAFTS>(p, prefix, spos, snew, own, room, warp, lane);
+      if constexpr (kShortCall<D, DRAFTS>)
+        short_segments_call<D, NT, DRAFTS>(*shared, prefix, spos, snew, own, room, warp, lane);
       else
         short_segments<D, NT, DRAFTS>(p, prefix, spos, snew, own, room, warp, lane);
     }
@@ -903,9 +925,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // A CTA for each segment where the longest alone takes no longer than an even
   // share of the tiles and the merge of a split segment would.
+  const int longest = ((misc[2] + Sh::kTile - 1) / Sh::kTile) + kE;
   const bool whole =
       nseg <= (long long)gridDim.x &&
-      (long long)misc[2] * kWholeNum * gw <= T * kWholeDen + kMergeCost<D, Sh::kTile> * gw;
+      longest * kWholeNum * gw <= T * kWholeDen + kMergeCost<D, Sh::kTile> * gw;
   const int G = whole ? (int)nseg : (int)gw;
   if ((int)blockIdx.x >= G) return;
   FlatRange rg;

@@ -278,6 +278,19 @@ def test_many_short_sequences(S, g, D, page, layout, longest):
     check_decode(first, q[:, :1], k, v, pos, [min(n, 1) for n in lengths], table, 0.1)
 
 
+@pytest.mark.parametrize("S,g,D", [(1, 4, 128), (1, 16, 128), (1, 32, 128), (3, 2, 128),
+                                   (8, 4, 128), (1, 4, 64), (5, 6, 64)])
+def test_most_sequences_of_a_launch_short(S, g, D):
+    """4096 sequences leave the rows in flight less room than fewer do."""
+    B, page = 4096, 16
+    r = np.random.default_rng(19)
+    pos = r.integers(0, 130 - S, B).tolist()
+    gen = torch.Generator(device="cuda").manual_seed(19)
+    q, table, k, v = make(B, S, g, 1, D, page, pos, gen)
+    out = ga.attn_decode_step_paged(q, i32(pos), table, k, v, 0.1)
+    check_decode(out, q, k, v, pos, None, table, 0.1)
+
+
 def test_many_short_sequences_with_bad_pages_and_odd_values():
     B, S, g, D, page = 500, 3, 4, 128, 16
     r = np.random.default_rng(18)
