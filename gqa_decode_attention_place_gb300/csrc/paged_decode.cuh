@@ -31,6 +31,7 @@
 //    that average over the keys; the output's own rounding is the same size):
 //    there a tile's transfer is half as long and the MMAs are what it waits for
 //    (91 us, 107 with two parts).  The sums are of the weights as they entered.
+//    Whatever the parts, an infinite value stays one (split_above_zero, both_parts).
 //  * At a piece's end the warps' partials meet in the memory of its last tile,
 //    each in the slice that its warp alone has read, so one barrier is enough.
 //  * Work is split as in the 8-bit decode (flat_list.cuh): a flat list of all
@@ -353,12 +354,14 @@ struct PagedConsumer {
         for (int e = 0; e < 4; ++e) y[e] = ex2(fmaf(x[n][i][e], p.qscale, -ref[i]));
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+          if (kTwoParts) {
+            split_above_zero(y[2 * j], y[2 * j + 1], w[n][2 * j + i], rest[n][2 * j + i]);
+            continue;
+          }
           const uint32_t hi = pack_bf16x2(y[2 * j], y[2 * j + 1]);
           w[n][2 * j + i] = hi;
-          if (G == 2 && !kTwoParts) continue;
-          const uint32_t lo = pack_bf16x2(y[2 * j] - bf16lo(hi), y[2 * j + 1] - bf16hi(hi));
-          if (G == 1) w[n][2 * j + 1] = lo;
-          else rest[n][2 * j + i] = lo;
+          if (G == 1)
+            w[n][2 * j + 1] = pack_bf16x2(y[2 * j] - bf16lo(hi), y[2 * j + 1] - bf16hi(hi));
         }
       }
     // their sums, as a product with ones
@@ -403,6 +406,22 @@ struct PagedConsumer {
   }
   // a second MMA for the weights' rest
   static constexpr bool kTwoParts = NT == 2 || (NT == 4 && D == 128);
+  // Two weights in two parts that go into the same sums.  An infinite value must get the
+  // same infinity from both, so the rest has to be above zero: the first part is cut
+  // off, not rounded, from a weight whose last bit is set.  (The rest is rounded to 2^-16
+  // of the weight.  It is zero for weights below 2^-110, and of a weight of zero.)
+  __device__ __forceinline__ static void split_above_zero(float a, float b, uint32_t& hi,
+                                                          uint32_t& rest) {
+    const uint32_t x = __float_as_uint(a) | 1u, y = __float_as_uint(b) | 1u;
+    hi = prmt(x, y, 0x7632u);
+    rest = pack_bf16x2(__uint_as_float(x) - __uint_as_float(x & 0xffff0000u),
+                       __uint_as_float(y) - __uint_as_float(y & 0xffff0000u));
+  }
+  // Up to 8 query rows the parts have sums of their own: where the first's is infinite,
+  // the rest's (of any sign, or NaN) does not count.
+  __device__ __forceinline__ static float both_parts(float hi, float rest) {
+    return fabsf(hi) == INFINITY ? hi : hi + rest;
+  }
   // Mask of a register with two rows of which the first n (or all) count.
   __device__ __forceinline__ static uint32_t keep(int n) {
     return n >= 2 ? 0xffffffffu : n == 1 ? 0x0000ffffu : 0u;
@@ -453,10 +472,7 @@ struct PagedConsumer {
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
         float2 y = make_float2(o[j][2 * i], o[j][2 * i + 1]);
-        if (G == 1) {  // the weights' two parts
-          y.x += o[j][2];
-          y.y += o[j][3];
-        }
+        if (G == 1) y = make_float2(both_parts(y.x, o[j][2]), both_parts(y.y, o[j][3]));
         *reinterpret_cast<float2*>(part + partial_at(warp, i, c, 8 * j + 2 * t, p.lb)) = y;
       }
     }
@@ -786,10 +802,8 @@ __device__ __forceinline__ void short_segments(const PagedParams& p, const int* 
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
         float2 y = make_float2(cs.o[j][2 * i], cs.o[j][2 * i + 1]);
-        if (kG == 1) {
-          y.x += cs.o[j][2];
-          y.y += cs.o[j][3];
-        }
+        if (kG == 1)
+          y = make_float2(cs.both_parts(y.x, cs.o[j][2]), cs.both_parts(y.y, cs.o[j][3]));
         *reinterpret_cast<uint32_t*>(out + 8 * j) =
             idle ? 0u : pack_bf16x2(y.x * inv, y.y * inv);
       }

@@ -557,7 +557,10 @@ size_t attn_paged_workspace_size(int B, int S, int Hq, int Hkv, int D);
  *     out[b,t,h] = softmax_j(scale * q[b,t,h] . K_j) V_j
  * with K_j and V_j of KV head h / g.  The rows must be there already
  * (attn_paged_append).  Rows that a token does not see may hold anything, NaN
- * included; entries behind the last attended row are not read.
+ * included; entries behind the last attended row are not read.  An infinite value
+ * in a row that it sees makes its output infinite in that dim, if the row's weight
+ * is at least 2^-100 of the largest; with less it may be NaN, and infinities of
+ * both signs give NaN.
  *
  *   q, out : [B, S, Hq, D] bf16.  Tokens t >= lengths[b] get zeros.
  *   Both products in bf16 with fp32 sums, as in attn_decode_step; the
