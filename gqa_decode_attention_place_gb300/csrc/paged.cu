@@ -148,8 +148,9 @@ cudaError_t launch_paged_decode(const void* q, const int32_t* positions, const i
   p.cap = M * pool.page;
   p.stages = 0;
   p.test_skip = g_decode_test_skip;
-  // (a scale of zero: tiny, so that masked scores stay -inf times it)
-  p.qscale = fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-37f);
+  // (a scale of zero: tiny, so that masked scores stay -inf times it; NaN stays NaN, where
+  // fmaxf would take the other operand)
+  p.qscale = std::isnan(scale) ? scale : fmaxf(fabsf(scale) * 1.4426950408889634f, 1e-37f);
   p.flip = scale < 0.f ? 0x80008000u : 0u;
   if (pool.D == 64)
     return S == 1 ? launch_paged_decode_64(p, pool, stream)

@@ -1,6 +1,6 @@
-"""attn_decode_step_paged where values are not finite: the output is what the
-formula gives, in the cluster, flat-list and warp-a-segment forms and for every
-group of query rows."""
+"""attn_decode_step_paged where values or the score scale are not finite: the
+output is what the formula gives, in the cluster, flat-list and warp-a-segment
+forms and for every group of query rows."""
 
 import numpy as np
 import pytest
@@ -103,3 +103,14 @@ def test_infinite_values_of_little_weight(S, g, D, schedule):
         put(v, table, b, low, slice(0, None, 3), INF)
     out = run(schedule, q, i32([600, 600]), table, k, v, 1.0)
     check(out, q, k, v, [600, 600], None, table, 1.0)
+
+
+@pytest.mark.parametrize("schedule", [0, 2])
+@pytest.mark.parametrize("S,g", [(1, 2), (1, 16), (4, 8)])
+def test_a_scale_that_is_nan(S, g, schedule):
+    """NaN in every row of a token that is there, zeros in the others, as ever."""
+    lengths = [S, 0, 1]
+    q, table, k, v = cache(3, S, g, 1, 128, 16, [100, 0, 300], 4, lengths)
+    out = run(schedule, q, i32([100, 0, 300]), table, k, v, float("nan"), lengths=i32(lengths))
+    for b, n in enumerate(lengths):
+        assert np.isnan(out[b, :n]).all() and (out[b, n:] == 0).all()
