@@ -425,7 +425,7 @@ int paged_pool(const void* k, const void* v, int64_t page_stride, int64_t head_s
 }
 bool pages_sizes(int B, int S, int page) {
   return B > 0 && B <= 65536 && S > 0 && page > 0 &&
-         (int64_t)B * ((S - 1 + (int64_t)page - 1) / page + 1) <= (1 << 28);
+         B * gqa::pages_touched(S, page) <= (1 << 28);
 }
 
 }  // namespace

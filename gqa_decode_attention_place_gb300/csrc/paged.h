@@ -72,6 +72,8 @@ cudaError_t launch_paged_append(const void* k_new, const void* v_new, long long 
                                 const PagedPool& pool, int B, int S, int M, cudaStream_t stream);
 
 // Pages: given out, shared and freed, moved (pages.cu).
+// The pages that S >= 1 rows in a row can touch; S may be any int.
+constexpr long long pages_touched(int S, int page) { return (S - 1ll + page - 1) / page + 1; }
 struct PagesWorkspace {
   size_t copies_off, list_off, total;  // the status word comes first
 };

@@ -716,7 +716,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // [B] copies, [B] reaches, then info and list [B * per] each.
 PagesWorkspace pages_reserve_layout(int B, int S, int page) {
-  const size_t per = (size_t)(S - 1 + page - 1) / page + 1;
+  const size_t per = (size_t)pages_touched(S, page);
   PagesWorkspace w;
   w.copies_off = 256;
   w.list_off = align256(w.copies_off + (size_t)B * 24);
@@ -752,7 +752,7 @@ cudaError_t launch_pages_reserve(int32_t* table, int32_t* refs, const int32_t* p
   p.P = pool.P;
   p.lp = log2_of(pool.page);
   p.cap = M * pool.page;
-  p.per = (S - 1 + pool.page - 1) / pool.page + 1;
+  p.per = (int)pages_touched(S, pool.page);
   p.info = reinterpret_cast<int32_t*>(base + ws.list_off);
   p.list = p.info + (size_t)B * p.per;
   int sms = 0;

@@ -603,7 +603,7 @@ size_t attn_pages_workspace_size(int B, int S, int P, int page);
  *   taken : [B] int32: how many pages the sequence took; -1 if the pages that
  *           it and the sequences before it need are more than there are, or its
  *           rows do not fit (ATTN_DEV_BAD_POSITION): nothing of it is changed.
- *   S     : >= 1.  Other limits: B <= 65536, B * ceil(S / page + 1) <= 2^28.
+ *   S     : >= 1.  Other limits: B <= 65536, B * (ceil((S - 1) / page) + 1) <= 2^28.
  * One launch for up to 16384 pages and 1024 pages that the rows can touch, else two.
  */
 int attn_pages_reserve(int32_t* page_table, int32_t* page_refs, const int32_t* positions,
