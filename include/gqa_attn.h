@@ -560,7 +560,8 @@ size_t attn_paged_workspace_size(int B, int S, int Hq, int Hkv, int D);
  * included; entries behind the last attended row are not read.  An infinite value
  * in a row that it sees makes its output infinite in that dim, if the row's weight
  * is at least 2^-100 of the largest; with less it may be NaN, and infinities of
- * both signs give NaN.
+ * both signs give NaN.  So do scores of +inf or NaN, in all dims.  A token all of
+ * whose scores are -inf gets zeros, like one that no row is left for.
  *
  *   q, out : [B, S, Hq, D] bf16.  Tokens t >= lengths[b] get zeros.
  *   Both products in bf16 with fp32 sums, as in attn_decode_step; the

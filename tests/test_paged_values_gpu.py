@@ -106,6 +106,21 @@ def test_infinite_values_of_little_weight(S, g, D, schedule):
 
 
 @pytest.mark.parametrize("schedule", [0, 2])
+@pytest.mark.parametrize("S,g,D", [(1, 2, 128), (1, 16, 128), (1, 32, 64), (4, 8, 128)])
+def test_scores_that_are_all_minus_infinity(S, g, D, schedule):
+    """Zeros for a token that sees no other row; one finite row is all that another sees."""
+    positions = [0, 40, 300]
+    q, table, k, v = cache(3, S, g, 1, D, 16, positions, 5)
+    q[..., 0] = 1.0
+    k[..., 0] = torch.where(k[..., 0].isnan(), k[..., 0], -INF)
+    last = positions[2] + S - 1  # seen by the last token alone
+    k[int(table[2, last // 16]), 0, last % 16] = 0.5
+    out = run(schedule, q, i32(positions), table, k, v, 0.1)
+    assert (out[:2] == 0).all() and (out[2, :S - 1] == 0).all()
+    assert (out[2, S - 1] == f64(v[int(table[2, last // 16]), 0, last % 16])).all()
+
+
+@pytest.mark.parametrize("schedule", [0, 2])
 @pytest.mark.parametrize("S,g", [(1, 2), (1, 16), (4, 8)])
 def test_a_scale_that_is_nan(S, g, schedule):
     """NaN in every row of a token that is there, zeros in the others, as ever."""
