@@ -723,12 +723,10 @@ __device__ __forceinline__ void short_segments(const PagedParams& p, const int* 
     mt.n = snew[b];
     const int rows = mt.pos + mt.n, slices = (rows + 15) >> 4;
     const int mask = (1 << p.lp) - 1;
-    // table entries, a lane for each of the first 32 slices
-    auto entry = [&](int i) -> int {
-      const int j = (16 * i) >> p.lp;
-      return i < slices && range_ok(j < p.M, p.status) ? p.table[(size_t)b * p.M + j] : 0;
-    };
-    int entries = entry(lane), from = 0;
+    // table entries, a lane for each slice
+    const int j = (16 * lane) >> p.lp;
+    const int entries =
+        lane < slices && range_ok(j < p.M, p.status) ? p.table[(size_t)b * p.M + j] : 0;
     cs.row_base = 16 * team;
     // the query rows, zeros behind the last
 #pragma unroll
@@ -743,11 +741,7 @@ __device__ __forceinline__ void short_segments(const PagedParams& p, const int* 
     uint32_t there = 0;  // of the buffers: which hold rows
     auto load = [&](int i) {
       if (i < slices) {
-        if (i - from >= 32) {
-          from = i;
-          entries = entry(i + lane);
-        }
-        const int pg = page_ok(p, __shfl_sync(0xffffffffu, entries, i - from));
+        const int pg = page_ok(p, __shfl_sync(0xffffffffu, entries, i));
         const int buf = i % bufs;
         there = pg >= 0 ? there | 1u << buf : there & ~(1u << buf);
         if (pg >= 0) {
@@ -917,6 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // query rows, tiles and warps take alike at 96, 128 and 256 rows, at 64, 96 and 128 with
   // several tokens and 128 dims; 32 query rows there, 912 of 192 rows: 38 and 45 us).
   constexpr int kWarpRows = D == 128 && (NT == 4 || DRAFTS) ? 128 : 256;
+  static_assert(kWarpRows <= 16 * 32, "a lane for each slice's table entry");
   const int per_cta = (int)((nseg + gridDim.x - 1) / gridDim.x);
   if (per_cta > 1 &&
       misc[2] <= min(kWarpRows, kShortCall<D, DRAFTS> ? 32 * per_cta : 64 * per_cta - 32)) {
