@@ -65,8 +65,6 @@ __global__ void __launch_bounds__(kAppendWarps * 32) paged_append_kernel(
   }
 }
 
-static int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
-
 cudaError_t launch_paged_append(const void* k_new, const void* v_new, long long k_stride,
                                 long long v_stride, const int32_t* positions,
                                 const int32_t* lengths, const int32_t* table,
@@ -92,9 +90,9 @@ PagedWorkspace paged_workspace_layout(int B, int S, int Hq, int Hkv, int D) {
 }
 
 // A pool as a 5-D tensor map (64 dims, rows, halves of a row, heads, pages); a
-// box is `rows` of a page's rows of one head, [half][row][64 dims] in shared
-// memory with the 128-byte swizzle.
-static bool pool_map(CUtensorMap* m, const void* ptr, const PagedPool& pool, int rows) {
+// box is a page's rows of one head, [half][row][64 dims] in shared memory with the
+// 128-byte swizzle.
+static bool pool_map(CUtensorMap* m, const void* ptr, const PagedPool& pool) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t half = 64 * 2;
@@ -102,7 +100,7 @@ static bool pool_map(CUtensorMap* m, const void* ptr, const PagedPool& pool, int
                         (cuuint64_t)pool.Hkv, (cuuint64_t)pool.P};
   cuuint64_t strides[4] = {(cuuint64_t)pool.row_stride * 2, half,
                            (cuuint64_t)pool.head_stride * 2, (cuuint64_t)pool.page_stride * 2};
-  cuuint32_t box[5] = {64, (cuuint32_t)rows, (cuuint32_t)(pool.D / 64), 1, 1};
+  cuuint32_t box[5] = {64, (cuuint32_t)pool.page, (cuuint32_t)(pool.D / 64), 1, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -110,8 +108,8 @@ static bool pool_map(CUtensorMap* m, const void* ptr, const PagedPool& pool, int
          CUDA_SUCCESS;
 }
 
-bool paged_maps(const PagedPool& pool, int rows, CUtensorMap* mk, CUtensorMap* mv) {
-  return pool_map(mk, pool.k, pool, rows) && pool_map(mv, pool.v, pool, rows);
+bool paged_maps(const PagedPool& pool, CUtensorMap* mk, CUtensorMap* mv) {
+  return pool_map(mk, pool.k, pool) && pool_map(mv, pool.v, pool);
 }
 
 cudaError_t launch_paged_decode(const void* q, const int32_t* positions, const int32_t* lengths,

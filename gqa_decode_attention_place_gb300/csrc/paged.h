@@ -40,7 +40,6 @@ struct PagedParams {
   int R;                   // S * g
   int g_inverse;           // 2^16 / g, rounded up
   int lp;                  // log2 of the page's rows
-  int lb;                  // log2 of a copy's rows: the page's, or the tile's where that is less
   int cap;                 // rows that a sequence's pages can hold
   int stages;
   int test_skip;
@@ -48,8 +47,10 @@ struct PagedParams {
   uint32_t flip;           // sign bits of two bf16 if scale is negative, else 0
 };
 
-// Makes the pool's tensor maps for copies of `rows` rows.
-bool paged_maps(const PagedPool& pool, int rows, CUtensorMap* mk, CUtensorMap* mv);
+// Makes the pool's tensor maps, for copies of a head's rows of a page.
+bool paged_maps(const PagedPool& pool, CUtensorMap* mk, CUtensorMap* mv);
+// (a page has 16, 32, 64 or 128 rows)
+inline int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 // For head dims 64 and 128, one new token or several (paged_decode_d*.cu).
 cudaError_t launch_paged_decode_64(PagedParams& p, const PagedPool& pool, cudaStream_t stream);
 cudaError_t launch_paged_decode_64_drafts(PagedParams& p, const PagedPool& pool,

@@ -91,8 +91,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
   if (warp >= kWarps) {
     // ----------------------------------------------------------- producers --
     const bool keys = warp == kWarps;
-    const int box_rows = 1 << p.lb, in_box = (slice * 16) & (box_rows - 1);
-    const int page_mask = (1 << p.lp) - 1;
+    const int page_rows = 1 << p.lp, in_page = (slice * 16) & (page_rows - 1);
     auto in_use = [&](int i, int page) -> int {
       if (i >= mine || (rank + i * C) * kTile + slice * 16 > pos + n - 1) return -1;
       return page_ok(p, page);
@@ -105,8 +104,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
       const int cur = in_use(i, page);
       if (i + kBatch < mine) page = entry(i + kBatch);
       const uint32_t there = __ballot_sync(0xffffffffu, cur >= 0);
-      const bool lead = cur >= 0 && in_box == 0;
-      const uint32_t boxes = __ballot_sync(0xffffffffu, lead);
+      const bool lead = cur >= 0 && in_page == 0;
+      const uint32_t copies = __ballot_sync(0xffffffffu, lead);
       for (int q = 0; q < kBatch && base + q < mine; ++q) {
         if (pass > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[NS + s]),
                                                            (pass & 1u) ^ 1u, abort_flag))) {
@@ -125,15 +124,15 @@ __global__ void __launch_bounds__(kClusterThreads, 1)
           if (keys)
             meta[s] = TileMeta{(int)((there >> (kSlices * q)) & kAll), k * kTile, pos, n, b, kvh, 0, 1};
           if (!skip)
-            mbar_arrive_expect_tx(full, __popc((boxes >> (kSlices * q)) & kAll) *
-                                                ((uint32_t)box_rows * D * 2u) +
+            mbar_arrive_expect_tx(full, __popc((copies >> (kSlices * q)) & kAll) *
+                                                ((uint32_t)page_rows * D * 2u) +
                                             (keys && first ? (uint32_t)R * D * 2u : 0u));
         }
         __syncwarp();
         if (ti == q && lead && !skip) {
           const uint32_t dst = smem_u32(stages + (size_t)s * Sh::kStage) + slice * 16 * D * 2;
-          tma_load_5d(dst + (keys ? 0 : Sh::kOp), keys ? &tm_k : &tm_v, 0,
-                      (k * kTile + slice * 16) & page_mask, 0, kvh, cur, full);
+          tma_load_5d(dst + (keys ? 0 : Sh::kOp), keys ? &tm_k : &tm_v, 0, 0, 0, kvh, cur,
+                      full);
         }
         if (first && !skip && keys && lane < R)
           bulk_load(smem_u32(qbuf) + lane * Sh::kQStride,

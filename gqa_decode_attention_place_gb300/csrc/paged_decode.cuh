@@ -70,7 +70,7 @@ constexpr int kWholeTiles = 4;              // segments this short are not split
 // Whole segments, one CTA each (below): a lone CTA's tile takes kWholeNum / kWholeDen of
 // its share of a busy GPU, and a merge as long as kMergeCost / kWholeDen tiles.
 constexpr int kWholeNum = 5, kWholeDen = 9;
-template <int D, int TILE> constexpr int kMergeCost = 37 * (128 / D) * (128 / TILE);
+template <int D> constexpr int kMergeCost = 37 * (128 / D);
 constexpr int kMaxCluster = 16;
 constexpr float kMInit = -3e38f;            // the reference before any row
 constexpr float kTau = 8.f;                 // it moves when a score lies more than this above
@@ -91,7 +91,7 @@ struct TileMeta {
 // NT: 8-row groups of query rows (1, 2 or 4).
 template <int D, int NT>
 struct Shape {
-  static constexpr int kTile = 128;
+  static constexpr int kTile = 128;               // rows: whole pages, which have 128 at most
   static constexpr int kSlices = kTile / 16;
   static constexpr int kBatch = 32 / kSlices;     // tiles that a producer looks up at a time
   static constexpr int kOp = kTile * D * 2;       // bytes of a tile's keys
@@ -230,9 +230,9 @@ struct PagedConsumer {
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
   }
   // Byte offset in a tile of row 16 * slice (its first 64 dims).
-  __device__ __forceinline__ static int slice_at(int slice, int lb) {
-    const int row = slice * 16, box = row >> lb;
-    return ((box << lb) * D * 2) + (row & ((1 << lb) - 1)) * 128;
+  __device__ __forceinline__ static int slice_at(int slice, int lp) {
+    const int row = slice * 16, page = row >> lp;
+    return ((page << lp) * D * 2) + (row & ((1 << lp) - 1)) * 128;
   }
 
   // This warp's rows of a tile.  ks: its keys; the values lie behind them.
@@ -240,14 +240,14 @@ struct PagedConsumer {
                                        const TileMeta& mt) {
     const int first = warp & (kTeam - 1);
     const uint32_t base = smem_u32(ks);
-    const int half = 128 << p.lb;  // from a box's first 64 dims to the others
+    const int half = 128 << p.lp;  // from a page's first 64 dims to the others
     constexpr bool kTwo = Sh::kSlices == 2 * kTeam;
     constexpr int kAll = kTwo ? 1 | (1 << kTeam) : 1;
     // full: every row is there and seen by every query row in use
     if (((mt.flags >> first) & kAll) == kAll &&
         mt.row0 + 16 * (first + (kTwo ? kTeam : 0)) + 15 <= mt.pos) {
-      slices<kTwo ? 2 : 1, true>(base + slice_at(first, p.lb),
-                                 base + slice_at(first + (kTwo ? kTeam : 0), p.lb), half, Sh::kOp,
+      slices<kTwo ? 2 : 1, true>(base + slice_at(first, p.lp),
+                                 base + slice_at(first + (kTwo ? kTeam : 0), p.lp), half, Sh::kOp,
                                  mt.row0 + 16 * first, p, mt);
       return;
     }
@@ -255,7 +255,7 @@ struct PagedConsumer {
     for (int sl = first; sl < Sh::kSlices; sl += kTeam) {
       if (!((mt.flags >> sl) & 1)) continue;  // no rows there
       // (one slice that is full, where two are taken, does without the masks)
-      const uint32_t at = base + slice_at(sl, p.lb);
+      const uint32_t at = base + slice_at(sl, p.lp);
       const int row = mt.row0 + 16 * sl;
       if (kTwo && row + 15 <= mt.pos) slices<1, true>(at, at, half, Sh::kOp, row, p, mt);
       else slices<1, false>(at, at, half, Sh::kOp, row, p, mt);
@@ -453,8 +453,8 @@ struct PagedConsumer {
   // group i: in the keys (i = 0) or values of the warp's own slice, whose 16 rows
   // of 64 dims are eight of fp32; the dims of rows c turned so that a store's or a
   // load's lanes fall on different banks.
-  __device__ __forceinline__ static int partial_at(int w, int i, int row, int d, int lb) {
-    return (slice_at(w, lb) + i * Sh::kOp + (d >= 64 ? 128 << lb : 0)) / 4 + row * 64 +
+  __device__ __forceinline__ static int partial_at(int w, int i, int row, int d, int lp) {
+    return (slice_at(w, lp) + i * Sh::kOp + (d >= 64 ? 128 << lp : 0)) / 4 + row * 64 +
            ((d & 63) ^ ((row & 3) << 3));
   }
   // A piece's end: the warps' partials meet in the memory of its last tile, each in
@@ -473,7 +473,7 @@ struct PagedConsumer {
       for (int j = 0; j < D / 8; ++j) {
         float2 y = make_float2(o[j][2 * i], o[j][2 * i + 1]);
         if (G == 1) y = make_float2(both_parts(y.x, o[j][2]), both_parts(y.y, o[j][3]));
-        *reinterpret_cast<float2*>(part + partial_at(warp, i, c, 8 * j + 2 * t, p.lb)) = y;
+        *reinterpret_cast<float2*>(part + partial_at(warp, i, c, 8 * j + 2 * t, p.lp)) = y;
       }
     }
   }
@@ -508,7 +508,7 @@ struct PagedConsumer {
 #pragma unroll
         for (int k = 0; k < kTeam; ++k) {
           const float4 v = *reinterpret_cast<const float4*>(
-              part + partial_at(tm * kTeam + k, i, row, d, p.lb));
+              part + partial_at(tm * kTeam + k, i, row, d, p.lp));
           y.x = fmaf(v.x, e[k], y.x);
           y.y = fmaf(v.y, e[k], y.y);
           y.z = fmaf(v.z, e[k], y.z);
@@ -737,7 +737,7 @@ __device__ __forceinline__ void short_segments(const PagedParams& p, const int* 
                                 : make_uint4(0u, 0u, 0u, 0u);
       *reinterpret_cast<uint4*>(qs + r * Sh::kQStride + ch * 16) = x;
     }
-    // 16 rows of keys and values, as a box of a tile would lie
+    // 16 rows of keys and values, as a page of 16 lies in a tile
     uint32_t there = 0;  // of the buffers: which hold rows
     auto load = [&](int i) {
       if (i < slices) {
@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int longest = ((misc[2] + Sh::kTile - 1) / Sh::kTile) + kE;
   const bool whole =
       nseg <= (long long)gridDim.x &&
-      longest * kWholeNum * gw <= T * kWholeDen + kMergeCost<D, Sh::kTile> * gw;
+      longest * kWholeNum * gw <= T * kWholeDen + kMergeCost<D> * gw;
   const int G = whole ? (int)nseg : (int)gw;
   if ((int)blockIdx.x >= G) return;
   FlatRange rg;
@@ -986,8 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool keys = warp == kWarps;  // this warp also describes the tile, the other brings the
                                        // queries
     const int ti = lane / kSlices, slice = lane % kSlices;
-    const int box_rows = 1 << p.lb, in_box = (slice * 16) & (box_rows - 1);
-    const int page_mask = (1 << p.lp) - 1;
+    const int page_rows = 1 << p.lp, in_page = (slice * 16) & (page_rows - 1);
     // The slice's table entry, kNoRows where it holds none; looked at a batch later.
     auto fetch = [&](const FlatWalk& w) -> int {
       const int row = w.k * Sh::kTile + slice * 16;
@@ -1055,8 +1054,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       TileMeta mt = {};
       if (keys && on && slice == 0) describe(cur, mt);
       const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-      const bool lead = page >= 0 && in_box == 0;
-      const uint32_t boxes = __ballot_sync(0xffffffffu, lead);
+      const bool lead = page >= 0 && in_page == 0;
+      const uint32_t copies = __ballot_sync(0xffffffffu, lead);
       const bool skip = on && p.test_skip >= 0 && cur.b == 0 && cur.kvh == 0 &&
                         cur.k == p.test_skip;  // failure-path tests only
       for (int q = 0; q < n_q; ++q) {
@@ -1075,16 +1074,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           mt.flags |= (there >> (kSlices * q)) & ((1u << kSlices) - 1u);
           if (keys) meta[s] = mt;
           if (!skip)
-            mbar_arrive_expect_tx(full, __popc((boxes >> (kSlices * q)) & ((1u << kSlices) - 1u)) *
-                                                ((uint32_t)box_rows * D * 2u) +
+            mbar_arrive_expect_tx(full, __popc((copies >> (kSlices * q)) & ((1u << kSlices) - 1u)) *
+                                                ((uint32_t)page_rows * D * 2u) +
                                             (!keys && first ? (uint32_t)p.R * D * 2u : 0u));
         }
         __syncwarp();
         const bool hold = __shfl_sync(0xffffffffu, skip, kSlices * q);
         if (ti == q && lead && !hold) {
           const uint32_t dst = smem_u32(stages + (size_t)s * Sh::kStage) + slice * 16 * D * 2;
-          tma_load_5d(dst + (keys ? 0 : Sh::kOp), keys ? &tm_k : &tm_v, 0,
-                      (cur.k * Sh::kTile + slice * 16) & page_mask, 0, cur.kvh, page, full);
+          tma_load_5d(dst + (keys ? 0 : Sh::kOp), keys ? &tm_k : &tm_v, 0, 0, 0, cur.kvh, page,
+                      full);
         }
         if (first && !hold && !keys) {  // the piece's query rows, one by each lane
           const int b = __shfl_sync(0xffffffffu, cur.b, kSlices * q);
@@ -1265,7 +1264,7 @@ int cluster_size(const PagedParams& p, const PagedDevice& d) {
   int c = min(kMaxCluster, tiles);
   while (c > 1 && nseg > d.clusters[c]) --c;
   const float longest = (float)tiles * (float)p.B / (float)(p.B + 1);
-  const float per_tile = (D == 128 ? 1.45f : 0.75f) * (float)(kTile / 128.0);
+  const float per_tile = D == 128 ? 1.45f : 0.75f;
   const float share = per_tile * 0.5f * (float)tiles * (float)nseg / (float)d.sms;
   const float clusters =
       4.3f + fmaxf(1.15f * share, 0.43f * per_tile * ceilf(longest / (float)c));
@@ -1277,10 +1276,8 @@ cudaError_t launch_paged(PagedParams& p, const PagedPool& pool, cudaStream_t str
   const PagedDevice* d = nullptr;
   cudaError_t e = paged_device<D, DRAFTS>(&d);
   if (e != cudaSuccess) return e;
-  const int rows = min(pool.page, Shape<D, NT>::kTile);
-  p.lb = rows == 16 ? 4 : rows == 32 ? 5 : rows == 64 ? 6 : 7;
   CUtensorMap mk, mv;
-  if (!paged_maps(pool, rows, &mk, &mv)) return cudaErrorInvalidValue;
+  if (!paged_maps(pool, &mk, &mv)) return cudaErrorInvalidValue;
   p.stages = kMaxStages;
   const int C = cluster_size<D, NT>(p, *d);
   if (C > 0) {

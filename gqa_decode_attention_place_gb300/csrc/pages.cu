@@ -37,8 +37,6 @@ constexpr int kSoloPool = 8192;       // compact
 // of 512 KB: 92 and 85)
 constexpr int kSoloUnits = 49152;
 
-int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
-
 __device__ __forceinline__ uint32_t lanes_below(int lane) { return (1u << lane) - 1u; }
 
 // A warp's contiguous part of [0, n), split over the warps of C CTAs.
