@@ -8,10 +8,11 @@
 // are taken, in the order of the sequences, so results depend on the state
 // alone.  Counts change by integer atomics, whose order does not matter.
 //
-// Latency bounds the bookkeeping (a few hundred KB at most): reserve and
-// compact scan the counts with one CTA, or for large pools with a cluster whose
-// sums meet through distributed shared memory, and the pages' rows are copied by
-// a second launch over the whole GPU that starts with the list ready.
+// Latency bounds the bookkeeping (a few hundred KB at most).  Reserve and compact
+// are one launch for a small pool: every CTA scans all counts for itself and copies
+// its part of the rows.  For a larger one a cluster scans them, its CTAs' sums meet
+// through distributed shared memory, and a second launch over the whole GPU copies
+// rows with the list ready.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -47,13 +48,6 @@ template <int C>
 __device__ __forceinline__ Span span_of(int n, int rank, int warp) {
   const long long w = (long long)rank * kScanWarps + warp, all = C * kScanWarps;
   return Span{(int)((long long)n * w / all), (int)((long long)n * (w + 1) / all)};
-}
-
-// All threads of the C CTAs: what any of them wrote before, all see after.
-template <int C>
-__device__ __forceinline__ void sync_all() {
-  if (C == 1) __syncthreads();
-  else cg::this_cluster().sync();
 }
 
 // Exclusive sums over all warps, in order, of N counts each; total[] over all.
@@ -319,15 +313,15 @@ __global__ void __launch_bounds__(kScanThreads, 1)
   if (tid < p.B) p.taken[tid] = taken_by(p, n_b, pos_b, reach[tid], total[0]);
 }
 
-// A larger one: C CTAs, a cluster.  Three steps, a barrier between them: count the free pages
+// A larger one: a cluster.  Three steps, a barrier between them: count the free pages
 // and the needed ones; list the free pages that are wanted and how far the
 // sequences reach; give the pages out.
-template <int C>
 __global__ void __launch_bounds__(kScanThreads, 1) pages_reserve_kernel(const ReserveParams p) {
+  constexpr int C = kManyCtas;
   __shared__ Prefix<C, 2> prefix;
-  const int rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank(), tid = threadIdx.x;
+  const int rank = (int)cg::this_cluster().block_rank(), tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
-  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   grid_dependency_wait();
   grid_dependents_launch();
   const Span is = span_of<C>(p.B * p.per, rank, warp);
@@ -387,7 +381,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_reserve_kernel(const Re
     }
     at += __popc(m);
   }
-  sync_all<C>();
+  cg::this_cluster().sync();
 
   auto hand_over = [&](int b, int jj, int was, int pos, int page) {
     give(p, b, jj, was, pos, page);
@@ -595,13 +589,13 @@ __global__ void __launch_bounds__(kScanThreads, 1)
 }
 
 // n pages are in use: the k-th of those at n or above goes to the k-th free
-// page below n.  C CTAs, a cluster.
-template <int C>
+// page below n.  A cluster.
 __global__ void __launch_bounds__(kScanThreads, 1) pages_plan_kernel(const CompactParams p) {
+  constexpr int C = kManyCtas;
   __shared__ Prefix<C, 1> prefix;
-  const int rank = C == 1 ? 0 : (int)cg::this_cluster().block_rank(), tid = threadIdx.x;
+  const int rank = (int)cg::this_cluster().block_rank(), tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
-  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   grid_dependency_wait();
   grid_dependents_launch();
   PageBits bits(p.refs, span_of<C>(p.P, rank, warp), lane);
@@ -633,7 +627,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) pages_plan_kernel(const Compa
     return true;
   });
   if (n == p.P && rank == 0 && tid == 0) p.n_moves[0] = 0;  // no page is free
-  sync_all<C>();
+  cg::this_cluster().sync();
   const int moves = *(volatile int*)p.n_moves;
   for (int k = rank * kScanThreads + tid; k < moves; k += C * kScanThreads) {
     const int src = p.from[n - moves + k], dst = p.to[k];
@@ -760,7 +754,7 @@ cudaError_t launch_pages_reserve(int32_t* table, int32_t* refs, const int32_t* p
   if (pool.P <= kSoloPages && (long long)B * p.per <= kSoloItems)
     return launch_pdl(pages_reserve_solo_kernel, solo_grid(warps, sms), dim3(kScanThreads), 0,
                       stream, p, pool);
-  e = launch_scan(pages_reserve_kernel<kManyCtas>, stream, p);
+  e = launch_scan(pages_reserve_kernel, stream, p);
   if (e != cudaSuccess) return e;
   const long long blocks = (warps * 32 + kCopyThreads - 1) / kCopyThreads;
   return launch_pdl(pages_copy_rows_kernel, dim3((unsigned)min(blocks, (long long)sms * 8)),
@@ -814,7 +808,7 @@ cudaError_t launch_pages_compact(int32_t* table, int32_t* refs, const PagedPool&
     return launch_pdl(pages_compact_solo_kernel,
                       solo_grid(max(units, ((long long)B * M + 31) / 32), sms), dim3(kScanThreads),
                       0, stream, p, pool);
-  e = launch_scan(pages_plan_kernel<kManyCtas>, stream, p);
+  e = launch_scan(pages_plan_kernel, stream, p);
   if (e != cudaSuccess) return e;
   // About one unit a warp: CTAs that come and go keep reads and writes of DRAM better
   // apart than a few that stay (8192 pages of 64 KB: 168 us by 64 to an SM, 177 by 8
