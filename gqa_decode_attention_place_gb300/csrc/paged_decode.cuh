@@ -740,7 +740,9 @@ __device__ __forceinline__ void short_segments(const PagedParams& p, const int* 
     // 16 rows of keys and values, as a page of 16 lies in a tile
     uint32_t there = 0;  // of the buffers: which hold rows
     auto load = [&](int i) {
-      if (i < slices) {
+      // (i is a lane.  Without the second limit the kernel for 16 query rows spilled 32 bytes
+      // instead of 20: 512 sequences, 8 heads, of up to 32 rows 29.4 us, with it 23.3.)
+      if (i < min(slices, 32)) {
         const int pg = page_ok(p, __shfl_sync(0xffffffffu, entries, i));
         const int buf = i % bufs;
         there = pg >= 0 ? there | 1u << buf : there & ~(1u << buf);
@@ -907,9 +909,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long nseg = (long long)B * Hkv;
   long long gw = min((long long)gridDim.x, T);
   if (T <= (long long)(kWholeTiles + kE) * nseg) gw = min(gw, nseg);
-  // Short segments: the more a CTA has, the longer they may be (of 2, 3 and 4 a CTA with 4
-  // query rows, tiles and warps take alike at 96, 128 and 256 rows, at 64, 96 and 128 with
-  // several tokens and 128 dims; 32 query rows there, 912 of 192 rows: 38 and 45 us).
+  // Short segments: the more a CTA has, the longer they may be: 96, 160, 224 and 256 rows
+  // for 2, 3, 4 and more of them (128 at most with 32 query rows at 128 dims), where the call
+  // below is taken 64, 96 and 128.  Tiles and warps, in us, ragged segments up to so many rows:
+  //   4 query rows          304 segments:  96 8.5 and 8.2, 128 8.7 and 9.9; 456: 160 12.2 and
+  //                         11.6, 192 12.6 and 13.2; 608: 224 16.1 and 15.6, 256 16.8 and 17.3;
+  //                         760: 256 19.3 and 19.3, 320 21.6 and 22.5
+  //   16 of several tokens  304: 32 11.0 and 9.9, 64 11.3 and 11.9; 456: 96 13.8 and 14.6; 608: 96
+  //                         16.2 and 14.8, 128 16.9 and 17.9; 912: 128 23.3 and 20.3
+  // Segments per CTA are rounded up; just above a whole number the warps' limit is too long
+  // (312 of up to 160 rows: 9.9 and 11.5).
   constexpr int kWarpRows = D == 128 && (NT == 4 || DRAFTS) ? 128 : 256;
   static_assert(kWarpRows <= 16 * 32, "a lane for each slice's table entry");
   const int per_cta = (int)((nseg + gridDim.x - 1) / gridDim.x);
