@@ -27,7 +27,7 @@
 //  * The weights enter as two bf16 parts (16 bits): up to 8 query rows for nothing,
 //    as rows 8..15 of the MMA's M are free and take the rest; beyond, by a second
 //    MMA (32 rows, 1.07 GB: 169 -> 175 us, and nothing for a ragged batch).  Only
-//    at D = 64 with more than 16 rows they are rounded to bf16 once (2^-9, of errors
+//    at D = 64 with more than 16 rows they are rounded to bf16 once (2^-8, of errors
 //    that average over the keys; the output's own rounding is the same size):
 //    there a tile's transfer is half as long and the MMAs are what it waits for
 //    (91 us, 107 with two parts).  The sums are of the weights as they entered.

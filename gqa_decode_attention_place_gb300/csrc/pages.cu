@@ -243,7 +243,7 @@ __device__ __forceinline__ int taken_by(const ReserveParams& p, int n, int pos, 
 // A small pool: every CTA works out who gets what from the state as it was, an
 // item a thread, and copies its part of the rows; the last one to have read the
 // state changes it.  No CTA waits for another.  (One CTA's scan, then a launch of
-// copies: 8.4 us on the device for 256 sequences' step instead of 5.3, and 2 more
+// copies: 8.4 us on the device for 256 sequences' step instead of 6.3, and 2 more
 // of the host's time.)
 __global__ void __launch_bounds__(kScanThreads, 1)
     pages_reserve_solo_kernel(const ReserveParams p, const PagedPool pool) {

@@ -119,7 +119,8 @@ size_t attn_decode_workspace_size(int B, int Hq, int Hkv, int L, int D);
  *               rounded to nearest even.  Both contractions of a tile run
  *               on tensor cores with bf16 operands and fp32 accumulation:
  *               per warp (mma.sync) for g <= 8, with the probabilities
- *               entering P.V as two bf16 parts (about 16 bits); on the
+ *               entering P.V as two bf16 parts (about 16 bits; an infinite
+ *               value in an attended row may give NaN there); on the
  *               tcgen05 tensor cores for g = 16 (and for the rotary entry
  *               points at g = 8), with the probabilities rounded to bf16
  *               before P.V.
@@ -557,7 +558,7 @@ size_t attn_paged_workspace_size(int B, int S, int Hq, int Hkv, int D);
  *     out[b,t,h] = softmax_j(scale * q[b,t,h] . K_j) V_j
  * with K_j and V_j of KV head h / g.  The rows must be there already
  * (attn_paged_append).  Rows that a token does not see may hold anything, NaN
- * included; entries behind the last attended row are not read.  An infinite value
+ * included, and entries behind the last attended row any number.  An infinite value
  * in a row that it sees makes its output infinite in that dim, if the row's weight
  * is at least 2^-100 of the largest; with less it may be NaN, and infinities of
  * both signs give NaN.  So do scores of +inf or NaN, in all dims.  A token all of
@@ -573,7 +574,7 @@ size_t attn_paged_workspace_size(int B, int S, int Hq, int Hkv, int D);
  * A sequence whose rows positions[b] .. positions[b] + lengths[b] - 1 are not
  * all in [0, M * page), or whose lengths[b] is not in 0 .. S, gets NaN output
  * rows and ATTN_DEV_BAD_POSITION; with lengths[b] = 0 its position and pages
- * are not looked at.  An entry outside [0, P) that should hold attended rows
+ * may be anything.  An entry outside [0, P) that should hold attended rows
  * sets ATTN_DEV_BAD_PAGE and its rows are left out (zeros if none is left).
  */
 int attn_decode_step_paged(const void* q, const int32_t* positions, const int32_t* lengths,
@@ -597,7 +598,8 @@ size_t attn_pages_workspace_size(int B, int S, int P, int page);
  * [0, P)) takes a free page, and one whose page is shared (page_refs > 1) takes
  * a free page for itself: the rows before positions[b] that the shared page holds
  * are copied, and the shared page counts one entry less.  So every sequence that
- * shares a page leaves it, and a page that all of them left is free afterwards.
+ * shares a page and writes into it leaves it, the last one too: two that share one
+ * take two, and a page that all of them left is free afterwards (not before).
  * The free pages (those whose count was 0 before the call) are taken from the
  * lowest on, in the order of the sequences and their rows.
  *
@@ -640,7 +642,7 @@ int attn_pages_fork(int32_t* page_table, int32_t* page_refs, const int32_t* pare
  *   page_map : [P] int32, written: where each page went (p for one that stayed),
  *              -1 for a free one: for page numbers kept elsewhere.
  *   Table entries outside [0, P) stay.  B * M may be 0.  One launch for a small pool
- *   (up to 8192 pages, about 200 MB), else two.
+ *   (P up to 8192 and P * Hkv * page up to 786432 rows), else two.
  */
 int attn_pages_compact(int32_t* page_table, int32_t* page_refs, void* k_pages, void* v_pages,
                        int64_t page_stride, int64_t head_stride, int64_t row_stride, int B,
